@@ -33,6 +33,7 @@ __all__ = [
     "fa_bwd_noalloc", "fa_noalloc_check_device_status", "fa_fwd_kv", "fa_bwd_kv_workspace_size", "fa_bwd_kv_preprocess", "fa_bwd_kv",
     "fa_status_string", "forward", "backward", "attention", "FA_OK", "FA_ERR_INVALID_ARG",
     "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT", "FA_BF16", "FA_FP32",
+    "PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -45,6 +46,8 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _sz = ctypes.c_size_t
 _f = ctypes.c_float
+_d = ctypes.c_double
+_ll = ctypes.c_longlong
 
 _SIGS = {
     "fa_status_string": (ctypes.c_char_p, [_i]),
@@ -69,6 +72,21 @@ _SIGS = {
                                   _i, _vp, _vp, _i, _vp]),
     "fa_bwd_kv": (_i, [_vp] * 9 + [_i, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
                                    _vp, _i, _vp]),
+    "fa_rotary_table": (_i, [_vp, _i, _ll, _d, _vp, _vp]),
+    "fa_rotary": (_i, [_vp, _vp, _i, _ll, _ll] * 2 + [_i, _i, _i, _i, _vp, _i, _vp, _i, _i, _i,
+                                                     _vp, _i, _i, _vp]),
+    "fa_cache_scratch_size": (_sz, [_i, _i, _i]),
+    "fa_cache_reserve": (_i, [_vp, _vp, _vp, _i, _i, _vp]),
+    "fa_cache_fork": (_i, [_vp, _vp, _vp, _i, _vp]),
+    "fa_cache_free": (_i, [_vp, _vp, _i, _vp]),
+    "fa_cache_accept": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "fa_cache_check": (_i, [_vp, _vp, _vp]),
+    "fa_cache_append": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _ll, _ll, _vp, _ll, _ll,
+                             _vp, _ll, _ll, _i, _vp, _i, _vp, _i, _i, _vp]),
+    "fa_tree_workspace_size": (_sz, [_i, _i, _i, _i]),
+    "fa_tree_mask": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "fa_tree_fwd": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _f,
+                         _i, _vp, _sz, _vp]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -396,7 +414,31 @@ class _Attention(torch.autograd.Function):
 
 
 def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,
-              deterministic=False, cu_seqlens_k=None, max_seqlen_k=None):
-    """Differentiable attention (autograd wrapper around forward/backward)."""
+              deterministic=False, cu_seqlens_k=None, max_seqlen_k=None, rotary=None,
+              positions=None, positions_k=None, interleaved=False):
+    """Differentiable attention (autograd wrapper around forward/backward).
+
+    With rotary (a rotary_table) q and k are first turned to their positions: by default
+    each sequence counts from 0; positions gives them, for q and k alike unless positions_k
+    is given too.  Queries and keys of different lengths need both."""
+    if rotary is not None:
+        turn = serving.rotary
+        if positions_k is not None:
+            if positions is None:
+                raise ValueError("positions_k needs positions")
+            q, _ = turn(q, None, rotary, positions=positions, interleaved=interleaved)
+            _, k = turn(None, k, rotary, positions=positions_k, interleaved=interleaved)
+        elif cu_seqlens_k is not None or k.shape[0] != q.shape[0]:
+            raise ValueError("queries and keys of different lengths need positions and positions_k")
+        else:
+            q, k = turn(q, k, rotary, positions=positions, cu_seqlens=cu_seqlens, batch=batch,
+                        interleaved=interleaved)
+    elif positions is not None or positions_k is not None:
+        raise ValueError("positions need a rotary table")
     return _Attention.apply(q, k, v, causal, scale, cu_seqlens, max_seqlen, batch, deterministic,
                             cu_seqlens_k, max_seqlen_k)
+
+
+from . import serving  # noqa: E402  (uses the binding above)
+from .serving import (PagedCache, cache_append, rotary, rotary_table, tree_attention,  # noqa: E402
+                      tree_mask)

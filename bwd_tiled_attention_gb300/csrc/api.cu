@@ -81,6 +81,38 @@ bool make_map_f32(CUtensorMap* m, const void* base, int T, int H, int d) {
     return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+int fa::device_sms() { return sm_count(); }
+
+bool fa::make_tree_maps(TreeParams& p, const fa_cache& c, const void* q, int T, int Hq,
+                        long long token_stride, long long head_stride, int tile_tokens, int bn) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const int group = Hq / c.heads;
+    cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)group, (cuuint64_t)c.heads, (cuuint64_t)T};
+    cuuint64_t strides[3] = {(cuuint64_t)head_stride * 2, (cuuint64_t)head_stride * group * 2,
+                             (cuuint64_t)token_stride * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)group, 1, (cuuint32_t)tile_tokens};
+    if (enc(&p.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box,
+            es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return false;
+    cuuint64_t kd[3] = {(cuuint64_t)c.d, (cuuint64_t)c.page_size,
+                        (cuuint64_t)c.layers * c.pages * c.heads};
+    cuuint64_t ks[2] = {(cuuint64_t)c.d * 2, (cuuint64_t)c.page_size * c.d * 2};
+    cuuint32_t kb[3] = {64, (cuuint32_t)(c.page_size < bn ? c.page_size : bn), 1};
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? &p.tm_v : &p.tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, i ? c.v : c.k, kd, ks, kb,
+                es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    return true;
+}
+
+namespace {
+
 struct Shape {
     int B, Hq, Hkv, Nq, Tq, Nk, Tk, d;
     bool varlen;

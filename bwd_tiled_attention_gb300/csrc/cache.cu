@@ -1,0 +1,526 @@
+// cache.cu -- page operations of the paged key/value cache: making room for
+// tokens, forking a sequence, accepting a path of drafted tokens, freeing.
+//
+// All state lives on the device and every call is asynchronous, so a serving
+// step with its changing lengths can be captured into a graph.  A call is one
+// planning CTA, and a copying kernel where rows move (fork, accept).
+//
+// Planning is whole-number work on a few kilobytes: what bounds it is latency,
+// so one CTA does it with barriers instead of several launches.  It checks
+// everything first and then either carries the whole call out or only sets the
+// status word.  Free pages (refs == 0) are handed out lowest index first, in
+// the order of the call's entries: results do not depend on timing.
+//
+// Copying is bound by memory: one CTA a (sequence, layer, K or V), 16-byte
+// accesses, only the rows that a page holds.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "cache.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kPlan = 1024;  // threads of the planning CTA
+
+// Scratch words: [0] status, [1] go flag of the running call, then per slot an
+// entry (4 words) and a mark, the list of pages taken, and a copy of the table
+// entries behind an accepted base.
+struct Scratch {
+    int* status;
+    int* go;
+    int4* entry;
+    int* mark;
+    int* taken;
+    int* shadow;
+};
+inline long long scratch_ints(long long pages, long long slots, long long max_pages) {
+    return 8 + 4 * slots + slots + pages + slots * max_pages;
+}
+__device__ __forceinline__ Scratch scratch_of(const fa_cache& c) {
+    Scratch s;
+    s.status = c.scratch;
+    s.go = c.scratch + 1;
+    s.entry = reinterpret_cast<int4*>(c.scratch + 8);
+    s.mark = c.scratch + 8 + 4 * (long long)c.slots;
+    s.taken = s.mark + c.slots;
+    s.shadow = s.taken + c.pages;
+    return s;
+}
+
+// Sum over the CTA's threads before this one, and the total.
+__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    long long incl = x;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // (the last call's sums have been read)
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    long long before = 0;
+    total = 0;
+    for (int w = 0; w < kPlan / 32; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    return before + incl - x;
+}
+
+// entry[i].z = first place in `taken` of entry i, for needs entry[i].x; returns
+// the number of pages wanted in all.
+__device__ __forceinline__ long long place_needs(int4* entry, int n, long long* sums) {
+    long long all = 0;
+    for (int i0 = 0; i0 < n; i0 += kPlan) {
+        const int i = i0 + threadIdx.x;
+        long long total;
+        const long long at = all + block_scan(i < n ? entry[i].x : 0, sums, total);
+        if (i < n) entry[i].z = (int)min(at, 0x7FFFFFFFLL);
+        all += total;
+    }
+    __syncthreads();
+    return all;
+}
+
+// The `want` lowest free pages into taken[]; false when there are fewer.
+__device__ __forceinline__ bool take_pages(const fa_cache& c, int* taken, long long want,
+                                           long long* sums) {
+    long long have = 0;
+    for (long long p0 = 0; p0 < c.pages && have < want; p0 += kPlan * 4) {
+        const long long p = p0 + threadIdx.x * 4;
+        int is_free[4], mine = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            is_free[e] = p + e < c.pages && c.refs[p + e] == 0;
+            mine += is_free[e];
+        }
+        long long total, at = have + block_scan(mine, sums, total);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (is_free[e]) {
+                if (at < want) taken[at] = (int)(p + e);
+                ++at;
+            }
+        have += total;
+    }
+    __syncthreads();
+    return have >= want;
+}
+
+__device__ __forceinline__ bool slot_ok(const fa_cache& c, int slot) { return slot >= 0 && slot < c.slots; }
+
+// A slot's length, or -1 when it is not one.
+__device__ __forceinline__ int length_of(const fa_cache& c, int slot) {
+    const int n = c.lengths[slot];
+    return n < 0 || n > (long long)c.max_pages * c.page_size ? -1 : n;
+}
+
+__global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const int* slots,
+                                                        const int* counts, int count, int n) {
+    pdl_begin();
+    __shared__ long long sums[kPlan / 32];
+    __shared__ int error;
+    const Scratch s = scratch_of(c);
+    if (threadIdx.x == 0) error = 0;
+    for (int i = threadIdx.x; i < n; i += kPlan)
+        if (slot_ok(c, slots[i])) s.mark[slots[i]] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int slot = slots[i], m = counts ? counts[i] : count;
+        int4 e = make_int4(0, 0, 0, 0);  // pages wanted, pages held, place in the list
+        int bad = 0;
+        if (!slot_ok(c, slot) || atomicCAS(&s.mark[slot], -1, i) != -1) bad = kCacheBadSlot;
+        else {
+            const int len = length_of(c, slot);
+            if (len < 0 || m < 0 || (long long)len + m > (long long)c.max_pages * c.page_size)
+                bad = kCacheBadLength;
+            else {
+                e.y = (len + c.page_size - 1) / c.page_size;
+                e.x = (int)(((long long)len + m + c.page_size - 1) / c.page_size) - e.y;
+                if (m > 0 && len % c.page_size) {  // tokens will go to the last page
+                    const int page = c.table[(long long)slot * c.max_pages + e.y - 1];
+                    if (page < 0 || page >= c.pages) bad = kCacheBadSlot;
+                    else if (c.refs[page] != 1) bad = kCacheShared;
+                }
+            }
+        }
+        if (bad) atomicOr(&error, bad);
+        s.entry[i] = e;
+    }
+    __syncthreads();
+    const long long want = place_needs(s.entry, n, sums);
+    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, sums)))
+        if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
+    __syncthreads();
+    if (error) {
+        if (threadIdx.x == 0) atomicOr(s.status, error);
+        return;
+    }
+    for (int r = threadIdx.x; r < want; r += kPlan) {
+        int lo = 0, hi = n - 1;  // the last entry whose place is <= r
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s.entry[mid].z <= r) lo = mid; else hi = mid - 1;
+        }
+        const int4 e = s.entry[lo];
+        const int page = s.taken[r];
+        c.table[(long long)slots[lo] * c.max_pages + e.y + (r - e.z)] = page;
+        c.refs[page] = 1;
+    }
+    for (int i = threadIdx.x; i < n; i += kPlan) c.lengths[slots[i]] += counts ? counts[i] : count;
+}
+
+__global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, const int* parents,
+                                                          const int* children, int n) {
+    pdl_begin();
+    __shared__ long long sums[kPlan / 32];
+    __shared__ int error;
+    const Scratch s = scratch_of(c);
+    if (threadIdx.x == 0) error = 0;
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        if (slot_ok(c, children[i])) s.mark[children[i]] = -1;
+        if (slot_ok(c, parents[i])) s.mark[parents[i]] = -1;
+    }
+    __syncthreads();
+    // a warp an entry
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
+        const int from = parents[i], to = children[i], lane = threadIdx.x & 31;
+        int4 e = make_int4(0, 0, 0, 0);  // pages wanted (0 or 1), whole pages, place, rows copied
+        int bad = 0;
+        if (!slot_ok(c, from) || !slot_ok(c, to)) bad = kCacheBadSlot;
+        else {
+            const int len = length_of(c, from);
+            if (len < 0 || c.lengths[to] != 0) bad = kCacheBadLength;
+            else {
+                e.y = len / c.page_size;
+                e.w = len % c.page_size;
+                e.x = e.w > 0;
+                for (int k = lane; k < e.y + e.x; k += 32) {
+                    const int p = c.table[(long long)from * c.max_pages + k];
+                    if (p < 0 || p >= c.pages) bad = kCacheBadSlot;
+                }
+            }
+            if (lane == 0 && atomicCAS(&s.mark[to], -1, i) != -1) bad = kCacheBadSlot;
+        }
+        if (bad) atomicOr(&error, bad);
+        if (lane == 0) s.entry[i] = e;
+    }
+    __syncthreads();
+    // a slot cannot be read and made in one call
+    for (int i = threadIdx.x; i < n; i += kPlan)
+        if (slot_ok(c, parents[i]) && s.mark[parents[i]] != -1) atomicOr(&error, kCacheBadSlot);
+    __syncthreads();
+    const long long want = place_needs(s.entry, n, sums);
+    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, sums)))
+        if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *s.go = error == 0;
+        if (error) atomicOr(s.status, error);
+    }
+    if (error) return;
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
+        const int4 e = s.entry[i];
+        const int* from = c.table + (long long)parents[i] * c.max_pages;
+        int* to = c.table + (long long)children[i] * c.max_pages;
+        __syncwarp();
+        for (int k = threadIdx.x & 31; k < e.y; k += 32) {
+            to[k] = from[k];
+            atomicAdd(&c.refs[from[k]], 1);
+        }
+        if ((threadIdx.x & 31) == 0) {
+            int src = 0, dst = 0;
+            if (e.x) {
+                src = from[e.y];
+                dst = s.taken[e.z];
+                to[e.y] = dst;
+                c.refs[dst] = 1;
+            }
+            c.lengths[children[i]] = c.lengths[parents[i]];
+            s.entry[i] = make_int4(src, dst, e.w, 0);
+        }
+    }
+}
+
+// Copies the first rows of a page to another page: entry (source page,
+// destination page, rows).
+__global__ void __launch_bounds__(256) fork_copy_kernel(const fa_cache c) {
+    pdl_begin();
+    const Scratch s = scratch_of(c);
+    if (!*s.go) return;
+    const int4 e = s.entry[blockIdx.x];
+    if (e.z == 0) return;
+    const int layer = blockIdx.y >> 1;
+    uint4* base = static_cast<uint4*>(blockIdx.y & 1 ? c.v : c.k);
+    const int row16 = c.d / 8;                       // 16-byte units of a row
+    const int head16 = c.page_size * row16, run = e.z * row16;
+    const uint4* src = base + ((long long)layer * c.pages + e.x) * c.heads * head16;
+    uint4* dst = base + ((long long)layer * c.pages + e.y) * c.heads * head16;
+    const int all = c.heads * run;
+    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * 256) {
+        uint4 x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 256;
+            if (i < all) x[u] = src[(long long)(i / run) * head16 + i % run];
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 256;
+            if (i < all) dst[(long long)(i / run) * head16 + i % run] = x[u];
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlan) free_kernel(const fa_cache c, const int* slots, int n) {
+    pdl_begin();
+    __shared__ int error;
+    const Scratch s = scratch_of(c);
+    if (threadIdx.x == 0) error = 0;
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp an entry
+        const int slot = slots[i], lane = threadIdx.x & 31;
+        int bad = 0;
+        if (!slot_ok(c, slot)) bad = kCacheBadSlot;
+        else {
+            const int len = length_of(c, slot);
+            if (len < 0) bad = kCacheBadLength;
+            else {
+                const int used = (len + c.page_size - 1) / c.page_size;
+                for (int k = lane; k < used; k += 32) {
+                    const int p = c.table[(long long)slot * c.max_pages + k];
+                    if (p < 0 || p >= c.pages) bad = kCacheBadSlot;
+                }
+            }
+        }
+        if (bad) atomicOr(&error, bad);
+    }
+    __syncthreads();
+    if (error) {
+        if (threadIdx.x == 0) atomicOr(s.status, error);
+        return;
+    }
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
+        const int slot = slots[i], lane = threadIdx.x & 31;
+        int len = 0;
+        // whoever takes the length frees the pages: a slot named twice is freed once
+        if (lane == 0) len = atomicExch(&c.lengths[slot], 0);
+        len = __shfl_sync(0xffffffffu, len, 0);
+        const int used = (len + c.page_size - 1) / c.page_size;
+        for (int k = lane; k < used; k += 32) {
+            int* at = c.table + (long long)slot * c.max_pages + k;
+            atomicSub(&c.refs[*at], 1);
+            *at = -1;
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, const int* slots,
+                                                            const int* base, const int* path,
+                                                            int width, const int* accepted, int n) {
+    pdl_begin();
+    __shared__ int error;
+    const Scratch s = scratch_of(c);
+    if (threadIdx.x == 0) error = 0;
+    for (int i = threadIdx.x; i < n; i += kPlan)
+        if (slot_ok(c, slots[i])) s.mark[slots[i]] = -1;
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp an entry
+        const int slot = slots[i], lane = threadIdx.x & 31;
+        int bad = 0, len = -1, used = 0, fresh = 0;
+        if (slot_ok(c, slot)) {
+            if (lane == 0) fresh = atomicCAS(&s.mark[slot], -1, i) == -1;
+            fresh = __shfl_sync(0xffffffffu, fresh, 0);
+            len = length_of(c, slot);
+        }
+        const int b = base[i], m = accepted[i];
+        if (!fresh) bad = kCacheBadSlot;
+        else if (len < 0 || b < 0 || b > len || m < 0 || m > width || m > len - b) bad = kCacheBadLength;
+        else {
+            used = (len + c.page_size - 1) / c.page_size;
+            const int* row = c.table + (long long)slot * c.max_pages;
+            const int kept = (b + m + c.page_size - 1) / c.page_size;
+            for (int k = b / c.page_size + lane; k < used; k += 32) {
+                const int p = row[k];
+                if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
+                else if (k < kept && c.refs[p] != 1) bad |= kCacheShared;
+                s.shadow[(long long)slot * c.max_pages + k] = p;
+            }
+            const int* at = path + (long long)i * width;
+            for (int j = lane; j < m; j += 32) {  // strictly ascending, within the draft
+                const int t = at[j];
+                if (t < 0 || t >= len - b || (j > 0 && at[j - 1] >= t)) bad |= kCacheBadLength;
+            }
+        }
+        if (bad) atomicOr(&error, bad);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        *s.go = error == 0;
+        if (error) atomicOr(s.status, error);
+    }
+    if (error) return;
+    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
+        const int slot = slots[i], lane = threadIdx.x & 31;
+        const int len = c.lengths[slot], now = base[i] + accepted[i];
+        __syncwarp();
+        const int used = (len + c.page_size - 1) / c.page_size;
+        for (int k = (now + c.page_size - 1) / c.page_size + lane; k < used; k += 32) {
+            int* at = c.table + (long long)slot * c.max_pages + k;
+            atomicSub(&c.refs[*at], 1);
+            *at = -1;
+        }
+        if (lane == 0) c.lengths[slot] = now;
+    }
+}
+
+// Moves token base + path[j] to base + j, for every head of one layer's K or
+// V.  path ascends strictly, so path[j] >= j: a thread owns its 16 bytes of a
+// row and walks j upward in runs, reading a run's rows before it writes them;
+// what it has written lies below every row still to be read.
+constexpr int kRun = 8;
+__global__ void __launch_bounds__(128) accept_move_kernel(const fa_cache c, const int* slots,
+                                                          const int* base, const int* path,
+                                                          int width, const int* accepted) {
+    pdl_begin();
+    const Scratch s = scratch_of(c);
+    if (!*s.go) return;
+    const int i = blockIdx.x, m = accepted[i], b = base[i];
+    const int* pages = s.shadow + (long long)slots[i] * c.max_pages;
+    const int* at = path + (long long)i * width;
+    const int layer = blockIdx.y >> 1;
+    uint4* data = static_cast<uint4*>(blockIdx.y & 1 ? c.v : c.k);
+    const int row16 = c.d / 8;
+    const long long plane = (long long)c.page_size * row16;
+    auto row_of = [&](int tok, int head) {
+        return data + (((long long)layer * c.pages + pages[tok / c.page_size]) * c.heads + head) * plane +
+               (long long)(tok % c.page_size) * row16;
+    };
+    for (int x = threadIdx.x; x < c.heads * row16; x += blockDim.x) {
+        const int head = x / row16, col = x - head * row16;
+        for (int j0 = 0; j0 < m; j0 += kRun) {
+            uint4 v[kRun];
+            int src[kRun];
+#pragma unroll
+            for (int u = 0; u < kRun; ++u) {
+                src[u] = j0 + u < m ? at[j0 + u] : j0 + u;
+                if (src[u] != j0 + u) v[u] = row_of(b + src[u], head)[col];
+            }
+#pragma unroll
+            for (int u = 0; u < kRun; ++u)
+                if (src[u] != j0 + u) row_of(b + j0 + u, head)[col] = v[u];
+        }
+    }
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+
+// A list of device integers.
+bool list_ok(const int* p) { return p && aligned(p, 4); }
+
+}  // namespace
+
+fa_status check_cache(const fa_cache* c) {
+    if (!c || !c->k || !c->v || !c->table || !c->lengths || !c->refs || !c->scratch)
+        return FA_ERR_INVALID_ARG;
+    if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->table, 4) || !aligned(c->lengths, 4) ||
+        !aligned(c->refs, 4) || !aligned(c->scratch, 16))
+        return FA_ERR_INVALID_ARG;
+    if (c->layers <= 0 || c->pages <= 0 || c->heads <= 0 || c->slots <= 0 || c->max_pages <= 0)
+        return FA_ERR_INVALID_ARG;
+    if (c->d != 64 && c->d != 96 && c->d != 128 && c->d != 192 && c->d != 256)
+        return FA_ERR_UNSUPPORTED;
+    if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
+        return FA_ERR_UNSUPPORTED;
+    if (c->heads > 65535 || c->layers > 32767 ||
+        (long long)c->layers * c->pages > 0x7FFFFFFFLL / c->heads ||
+        (long long)c->max_pages * c->page_size > 0x40000000LL)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_cache_scratch_size(int pages, int slots, int max_pages) {
+    if (pages <= 0 || slots <= 0 || max_pages <= 0) return 0;
+    return (size_t)scratch_ints(pages, slots, max_pages) * sizeof(int);
+}
+
+fa_status fa_cache_reserve(const fa_cache* cache, const int* slots, const int* counts, int count,
+                           int n, fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0 || n > cache->slots || (!counts && count < 0)) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(slots) || !aligned(counts, 4)) return FA_ERR_INVALID_ARG;
+    return launched(launch_pdl(reserve_kernel, dim3(1), dim3(kPlan), 0,
+                               reinterpret_cast<cudaStream_t>(stream), *cache, slots, counts, count, n));
+}
+
+fa_status fa_cache_fork(const fa_cache* cache, const int* parents, const int* children, int n,
+                        fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0 || n > cache->slots) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(parents) || !list_ok(children)) return FA_ERR_INVALID_ARG;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, parents,
+                                     children, n);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    return launched(launch_pdl(fork_copy_kernel, dim3(n, cache->layers * 2), dim3(256), 0, strm, *cache));
+}
+
+fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(slots)) return FA_ERR_INVALID_ARG;
+    return launched(launch_pdl(free_kernel, dim3(1), dim3(kPlan), 0,
+                               reinterpret_cast<cudaStream_t>(stream), *cache, slots, n));
+}
+
+fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* base, const int* path,
+                          int path_width, const int* accepted, int n, fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0 || n > cache->slots || path_width < 0) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(slots) || !list_ok(base) || !list_ok(accepted) || (path_width > 0 && !list_ok(path)))
+        return FA_ERR_INVALID_ARG;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_pdl(accept_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, slots,
+                                     base, path, path_width, accepted, n);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+    if (path_width == 0) return FA_OK;
+    return launched(launch_pdl(accept_move_kernel, dim3(n, cache->layers * 2), dim3(128), 0, strm,
+                               *cache, slots, base, path, path_width, accepted));
+}
+
+fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    int word = 0;
+    if (cudaMemcpyAsync(&word, cache->scratch, sizeof(int), cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
+        cudaStreamSynchronize(strm) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (word && cudaMemsetAsync(cache->scratch, 0, sizeof(int), strm) != cudaSuccess) return FA_ERR_CUDA;
+    if (bits) *bits = word;
+    if (word & kCacheTimeout) return FA_ERR_TIMEOUT;
+    return word ? FA_ERR_INVALID_ARG : FA_OK;
+}
+
+}  // extern "C"

@@ -6,6 +6,8 @@
 
 #include <cstddef>
 
+#include "../../include/fa.h"
+
 namespace fa {
 
 // Forward kernel arguments (device pointers, tensor maps built on the host).
@@ -77,5 +79,40 @@ cudaError_t launch_bwd_postprocess(const float* dq_acc, void* dq, const float* d
                                    const float* dv_acc, void* dk, void* dv, int Tq, int Tk,
                                    int Hq, int Hkv, int nruns, int d, float scale, int grad_fp32,
                                    int num_sms, cudaStream_t stream);
+
+// ---- paged cache (cache.cu, rotary.cu, tree.cu)
+
+// Validates a cache descriptor (host side).
+fa_status check_cache(const fa_cache* c);
+
+// SMs of the current device (cached), 0 on error.
+int device_sms();
+
+constexpr int kTreeMaxCtas = 160;  // CTAs that the attention over the cache runs at most
+
+struct TreeParams {
+    CUtensorMap tm_q;              // 4-D {d, group, Hkv, T}, box {64, group, 1, tile_tokens}
+    CUtensorMap tm_k, tm_v;        // 3-D {d, page_size, layers * pages * Hkv}, box of one page's keys
+    fa_cache cache;
+    const int* slots;
+    const int* cu;                 // null for a dense batch
+    const void* mask;              // int64 [T, words], or null: causal
+    void* o;                       // bf16 [T, Hq, d]
+    float* lse;                    // [Hq, T]
+    int4* meta;                    // per CTA: the item that its first piece ends
+    float* part_stats;             // [2 * CTAs, part_rows, 2]: m and l
+    float* part_o;                 // [2 * CTAs, part_rows, d], not normalised
+    int part_rows;
+    int layer, B, N, T, Hq, group;
+    int words;
+    int tile_tokens;               // tokens of one 128-row tile
+    int min_tiles;                 // least key tiles of a CTA
+    int zero_rest;                 // write zeros for tokens that no sequence owns
+    float scale_log2;
+};
+
+// The tensor maps of p (api.cu); bn: keys of a tile.
+bool make_tree_maps(TreeParams& p, const fa_cache& c, const void* q, int T, int Hq,
+                    long long token_stride, long long head_stride, int tile_tokens, int bn);
 
 }  // namespace fa

@@ -1,0 +1,422 @@
+// rotary.cu -- rotary positions, forward and backward, and the same pass
+// writing new keys and values into a paged cache.
+//
+// A head's first rot columns are rot / 2 pairs; pair i of a token at position
+// p turns by the angle p * freq_i: (a, b) -> (a cos - b sin, b cos + a sin).
+// A pair is columns (i, i + rot/2) (half layout) or (2i, 2i + 1)
+// (interleaved).  The rotation is linear, so its backward pass is the
+// transposed one: the same kernel with sin negated.  cos and sin come from a
+// table [length, rot/2, 2] in fp32 that the caller keeps; products and sums
+// are fp32, rounded once on the store.
+//
+// Bound: memory.  Each value is read and written once, and nothing is reused
+// but the token's table row.  So a thread takes one 16-byte unit of a head's
+// columns (half layout: the two units that hold its pairs) in kHeadsPerThread
+// heads of one token: the cos and sin it loads serve all of them, and all its
+// loads are in flight before the first use.  Head dimensions, strides or
+// alignments that do not allow 16-byte accesses run the same code one element
+// at a time (VW = 1).
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "cache.cuh"
+#include "common.cuh"
+#include "internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kRotThreads = 256;
+constexpr int kHeadsPerThread = 4;
+
+struct RotParams {
+    // segment 0: q, 1: k, 2: v (copied); heads 0 when absent
+    const void* in[3];
+    void* out[3];                // contiguous [T, heads, d]; 1 and 2 are unused for a paged call
+    long long ts[3], hs[3];      // input strides in elements
+    int heads[3], quads[3];      // quads: groups of kHeadsPerThread heads
+    int T, d, rot, units;        // units per head
+    int t_first;                 // first token of this launch
+    unsigned n_threads;
+    const float2* table;         // [table_len, rot / 2]
+    int table_len;
+    const void* positions;       // int32 or int64 [T], or null
+    int pos64;
+    const int* cu;               // packed batch, or null
+    int B, N;
+    int backward;
+    // paged call
+    fa_cache cache;
+    const int* slots;
+    int layer;
+};
+
+template <typename E>
+__device__ __forceinline__ float to_f(E x) { return (float)x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename E>
+__device__ __forceinline__ E from_f(float x) { return (E)x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+
+template <typename E, int VW>
+struct alignas(VW * sizeof(E)) Vec {
+    E e[VW];
+};
+
+// E: element type; VW: elements of one access; INTER: pairs (2i, 2i + 1);
+// PAGED: k and v go to the cache's pages.
+template <typename E, int VW, bool INTER, bool PAGED>
+__global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotParams p) {
+    pdl_begin();
+    const unsigned idx = blockIdx.x * kRotThreads + threadIdx.x;
+    if (idx >= p.n_threads) return;
+    using V = Vec<E, VW>;
+    const unsigned U = p.units;
+    const unsigned per_token = (unsigned)(p.quads[0] + p.quads[1] + p.quads[2]) * U;
+    const unsigned tok_i = idx / per_token, rem = idx - tok_i * per_token;
+    const int tok = p.t_first + (int)tok_i;
+    int quad = (int)(rem / U);
+    const int u = (int)(rem - (unsigned)quad * U);
+    int seg = 0;
+    if (quad >= p.quads[0]) {
+        quad -= p.quads[0];
+        seg = 1;
+        if (quad >= p.quads[1]) {
+            quad -= p.quads[1];
+            seg = 2;
+        }
+    }
+    const int h0 = quad * kHeadsPerThread;
+    const int nh = min(kHeadsPerThread, p.heads[seg] - h0);
+
+    // Columns of this unit: one access (c0) or, for the pairs of the half
+    // layout, two (c0 and c1).  first_pair < 0: nothing turns here.
+    const int half = p.rot >> 1;
+    int c0, c1 = -1, first_pair = -1;
+    if (INTER) {
+        // VW = 1 takes whole pairs all the same: unit u < half is pair u
+        if (VW == 1) {
+            if (u < half) { c0 = 2 * u; c1 = 2 * u + 1; first_pair = u; }
+            else c0 = p.rot + (u - half);
+        } else {
+            c0 = u * VW;
+            if (c0 < p.rot) first_pair = c0 >> 1;
+        }
+    } else {
+        const int pair_units = half / VW;
+        if (u < pair_units) { c0 = u * VW; c1 = c0 + half; first_pair = c0; }
+        else c0 = p.rot + (u - pair_units) * VW;
+    }
+
+    // All of the thread's data loads first; the position follows while they fly.
+    const E* src = static_cast<const E*>(p.in[seg]) + (long long)tok * p.ts[seg] +
+                   (long long)h0 * p.hs[seg];
+    V x0[kHeadsPerThread], x1[kHeadsPerThread];
+#pragma unroll
+    for (int h = 0; h < kHeadsPerThread; ++h) {
+        if (h < nh) {
+            x0[h] = *reinterpret_cast<const V*>(src + h * p.hs[seg] + c0);
+            if (c1 >= 0) x1[h] = *reinterpret_cast<const V*>(src + h * p.hs[seg] + c1);
+        }
+    }
+
+    // The token's sequence, place in the cache and position.
+    bool owned = true, writable = true;
+    long long pos = 0, place_off = 0;
+    if (PAGED) {
+        const int b = seq_of_token(p.cu, p.B, p.N, tok);
+        owned = b >= 0;
+        int place = -1;
+        if (owned) {
+            const SeqRange r = seq_range(p.cu, p.N, p.T, b);
+            const int slot = p.slots[b];
+            int bad = 0;
+            if (r.n < 0) bad = kCacheBadLength;
+            else if (slot < 0 || slot >= p.cache.slots) bad = kCacheBadSlot;
+            else {
+                const long long at = (long long)p.cache.lengths[slot] - r.n + (tok - r.t0);
+                const long long col = at >= 0 ? at / p.cache.page_size : -1;
+                if (col < 0 || col >= p.cache.max_pages) bad = kCacheBadLength;
+                else {
+                    place = (int)at;
+                    if (seg != 0) {  // (q stays out of the cache)
+                        const int page = p.cache.table[(long long)slot * p.cache.max_pages + col];
+                        if (page < 0 || page >= p.cache.pages) bad = kCacheBadSlot;
+                        else
+                            place_off = ((((long long)p.layer * p.cache.pages + page) *
+                                              p.cache.heads + h0) * p.cache.page_size +
+                                         place % p.cache.page_size) * p.d;
+                    }
+                }
+            }
+            if (bad) {
+                atomicOr(p.cache.scratch, bad);
+                writable = false;
+            }
+        }
+        pos = place;
+    } else if (!p.positions) {
+        const int b = seq_of_token(p.cu, p.B, p.N, tok);
+        owned = b >= 0;
+        if (owned) pos = tok - (p.cu ? p.cu[b] : b * p.N);
+    }
+    if (p.positions)
+        pos = p.pos64 ? static_cast<const long long*>(p.positions)[tok]
+                      : (long long)static_cast<const int*>(p.positions)[tok];
+
+    if (seg != 2 && first_pair >= 0) {
+        // A position outside the table reads nothing and makes the columns NaN.
+        const bool known = pos >= 0 && pos < p.table_len;
+        constexpr int NP = INTER && VW > 1 ? VW / 2 : VW;  // pairs of this unit
+        float cs[NP], sn[NP];
+        const float2* row = p.table + (known ? pos : 0) * half + first_pair;
+        if (NP == 1) {
+            const float2 t = *row;
+            cs[0] = t.x;
+            sn[0] = t.y;
+        } else {
+            // two pairs an access: the row begins at a multiple of 16 bytes (see vector_ok)
+#pragma unroll
+            for (int i = 0; i < NP / 2; ++i) {
+                const float4 t = reinterpret_cast<const float4*>(row)[i];
+                cs[2 * i] = t.x;
+                sn[2 * i] = t.y;
+                cs[2 * i + 1] = t.z;
+                sn[2 * i + 1] = t.w;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            if (!known) cs[i] = sn[i] = NAN;
+            if (p.backward) sn[i] = -sn[i];
+        }
+#pragma unroll
+        for (int h = 0; h < kHeadsPerThread; ++h) {
+            if (h >= nh) break;
+            if (INTER && VW > 1) {
+#pragma unroll
+                for (int i = 0; i < VW / 2; ++i) {
+                    const float a = to_f(x0[h].e[2 * i]), b = to_f(x0[h].e[2 * i + 1]);
+                    x0[h].e[2 * i] = from_f<E>(a * cs[i] - b * sn[i]);
+                    x0[h].e[2 * i + 1] = from_f<E>(b * cs[i] + a * sn[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VW; ++i) {
+                    const float a = to_f(x0[h].e[i]), b = to_f(x1[h].e[i]);
+                    x0[h].e[i] = from_f<E>(a * cs[i] - b * sn[i]);
+                    x1[h].e[i] = from_f<E>(b * cs[i] + a * sn[i]);
+                }
+            }
+        }
+    }
+    if (!owned) {  // a token behind the last sequence: zeros, and nothing in the cache
+        writable = false;
+#pragma unroll
+        for (int h = 0; h < kHeadsPerThread; ++h)
+#pragma unroll
+            for (int i = 0; i < VW; ++i) x0[h].e[i] = x1[h].e[i] = from_f<E>(0.f);
+    }
+
+    E* dst;
+    long long hs;
+    if (PAGED && seg != 0) {
+        if (!writable) return;
+        dst = static_cast<E*>(seg == 1 ? p.cache.k : p.cache.v) + place_off;
+        hs = (long long)p.cache.page_size * p.d;
+    } else {
+        dst = static_cast<E*>(p.out[seg]) + ((long long)tok * p.heads[seg] + h0) * p.d;
+        hs = p.d;
+    }
+#pragma unroll
+    for (int h = 0; h < kHeadsPerThread; ++h) {
+        if (h < nh) {
+            *reinterpret_cast<V*>(dst + h * hs + c0) = x0[h];
+            if (c1 >= 0) *reinterpret_cast<V*>(dst + h * hs + c1) = x1[h];
+        }
+    }
+}
+
+template <typename E, int VW, bool PAGED>
+cudaError_t launch_t(RotParams p, int interleaved, cudaStream_t stream) {
+    const int half = p.rot / 2;
+    p.units = VW == 1 ? half + (p.d - p.rot)
+                      : (interleaved ? p.d / VW : half / VW + (p.d - p.rot) / VW);
+    for (int s = 0; s < 3; ++s) p.quads[s] = cdiv(p.heads[s], kHeadsPerThread);
+    const long long per_token = (long long)(p.quads[0] + p.quads[1] + p.quads[2]) * p.units;
+    if (per_token == 0) return cudaSuccess;
+    // thread indexes are 32 bits: more tokens than that go in several launches
+    const long long most = 0x7FFFFF00LL / per_token;
+    for (long long t = 0; t < p.T; t += most) {
+        const long long n = p.T - t < most ? p.T - t : most;
+        p.t_first = (int)t;
+        p.n_threads = (unsigned)(n * per_token);
+        const dim3 grid((p.n_threads + kRotThreads - 1) / kRotThreads);
+        cudaError_t e = interleaved
+            ? launch_pdl(rotary_kernel<E, VW, true, PAGED>, grid, dim3(kRotThreads), 0, stream, p)
+            : launch_pdl(rotary_kernel<E, VW, false, PAGED>, grid, dim3(kRotThreads), 0, stream, p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// 16-byte accesses need every unit to begin on a 16-byte boundary, in memory
+// and in the rotated columns, and the units' pairs to begin on an even pair.
+template <typename E>
+bool vector_ok(const RotParams& p, int interleaved, bool paged) {
+    constexpr int VW = 16 / (int)sizeof(E);
+    if (p.d % VW || p.rot % VW || (!interleaved && (p.rot / 2) % VW)) return false;
+    uintptr_t bits = reinterpret_cast<uintptr_t>(p.table);
+    if (paged)
+        bits |= reinterpret_cast<uintptr_t>(p.cache.k) | reinterpret_cast<uintptr_t>(p.cache.v);
+    for (int s = 0; s < 3; ++s) {
+        if (!p.heads[s]) continue;
+        bits |= reinterpret_cast<uintptr_t>(p.in[s]) | (uintptr_t)(p.ts[s] * (long long)sizeof(E)) |
+                (uintptr_t)(p.hs[s] * (long long)sizeof(E));
+        if (!paged || s == 0) bits |= reinterpret_cast<uintptr_t>(p.out[s]);
+    }
+    return (bits & 15u) == 0;
+}
+
+template <typename E, bool PAGED>
+cudaError_t launch_any(const RotParams& p, int interleaved, cudaStream_t stream) {
+    return vector_ok<E>(p, interleaved, PAGED)
+               ? launch_t<E, 16 / (int)sizeof(E), PAGED>(p, interleaved, stream)
+               : launch_t<E, 1, PAGED>(p, interleaved, stream);
+}
+
+// Table row of one position: angle p * freq in 64 bits, so that far positions
+// keep their phase, rounded once to fp32.
+__global__ void rotary_table_kernel(const double* freq, int half, long long n, double scale,
+                                    float2* table) {
+    pdl_begin();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    const long long pos = i / half;
+    double s, c;
+    sincos((double)pos * freq[i - pos * half], &s, &c);
+    table[i] = make_float2((float)(c * scale), (float)(s * scale));
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// The arguments that both calls share.
+fa_status check_rotary(const RotParams& p, const float* table, int pos_bytes) {
+    if (p.T < 0 || p.d <= 0 || p.d > 65536 || p.rot < 0 || p.rot > p.d || (p.rot & 1))
+        return FA_ERR_INVALID_ARG;
+    for (int s = 0; s < 3; ++s)
+        if (p.heads[s] < 0 || p.heads[s] > 65535 || p.ts[s] < 0 || p.hs[s] < 0)
+            return FA_ERR_INVALID_ARG;
+    if (p.B < 0 || p.N < 0 || p.table_len < 0) return FA_ERR_INVALID_ARG;
+    if (pos_bytes != 0 && pos_bytes != 4 && pos_bytes != 8) return FA_ERR_INVALID_ARG;
+    if ((pos_bytes != 0) != (p.positions != nullptr)) return FA_ERR_INVALID_ARG;
+    if (!aligned(p.positions, pos_bytes ? pos_bytes : 1) || !aligned(p.cu, 4) || !aligned(table, 8))
+        return FA_ERR_INVALID_ARG;
+    if (!p.cu && (long long)p.B * p.N != p.T) return FA_ERR_INVALID_ARG;
+    // the most threads that one token takes must leave room for 32-bit indexes
+    if (((long long)p.heads[0] + p.heads[1] + p.heads[2] + 12) / kHeadsPerThread * p.d > 0x7FFFFF00LL)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+fa_status fa_rotary_table(const double* freq, int half, long long length, double scale,
+                          float* table, fa_stream_t stream) {
+    if (half <= 0 || half > 32768 || length < 0 || length > 0x7FFFFFFFLL || !std::isfinite(scale))
+        return FA_ERR_INVALID_ARG;
+    if (length == 0) return FA_OK;
+    if (!freq || !table || !aligned(freq, 8) || !aligned(table, 16)) return FA_ERR_INVALID_ARG;
+    const long long n = length * half;
+    if (n > 0x7FFFFFFFLL * 256) return FA_ERR_UNSUPPORTED;
+    const cudaError_t e =
+        launch_pdl(rotary_table_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0,
+                   reinterpret_cast<cudaStream_t>(stream), freq, half, n, scale,
+                   reinterpret_cast<float2*>(table));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_rotary(const void* q, void* q_out, int Hq, long long q_token_stride,
+                    long long q_head_stride, const void* k, void* k_out, int Hkv,
+                    long long k_token_stride, long long k_head_stride, fa_dtype dtype, int T,
+                    int d, int rot, const float* table, int table_len, const void* positions,
+                    int pos_bytes, int B, int N, const int* cu_seqlens, int interleaved,
+                    int backward, fa_stream_t stream) {
+    RotParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.in[0] = q; p.out[0] = q_out; p.heads[0] = Hq; p.ts[0] = q_token_stride; p.hs[0] = q_head_stride;
+    p.in[1] = k; p.out[1] = k_out; p.heads[1] = Hkv; p.ts[1] = k_token_stride; p.hs[1] = k_head_stride;
+    p.T = T; p.d = d; p.rot = rot;
+    p.table = reinterpret_cast<const float2*>(table);
+    p.table_len = table_len;
+    p.positions = positions;
+    p.pos64 = pos_bytes == 8;
+    p.cu = cu_seqlens;
+    p.B = B; p.N = N;
+    p.backward = backward ? 1 : 0;
+    if (dtype != FA_BF16 && dtype != FA_FP32) return FA_ERR_INVALID_ARG;
+    const fa_status st = check_rotary(p, table, pos_bytes);
+    if (st != FA_OK) return st;
+    if (T == 0 || Hq + Hkv == 0) return FA_OK;
+    if ((Hq > 0 && (!q || !q_out)) || (Hkv > 0 && (!k || !k_out)) || (rot > 0 && !table))
+        return FA_ERR_INVALID_ARG;
+    const unsigned e = dtype == FA_BF16 ? 2 : 4;
+    if (!aligned(q, e) || !aligned(q_out, e) || !aligned(k, e) || !aligned(k_out, e))
+        return FA_ERR_INVALID_ARG;
+    if (rot > 0 && table_len == 0) return FA_ERR_INVALID_ARG;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t err = dtype == FA_BF16 ? launch_any<__nv_bfloat16, false>(p, interleaved, strm)
+                                             : launch_any<float, false>(p, interleaved, strm);
+    return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                          const int* cu_seqlens, int T, const void* q, void* q_out, int Hq,
+                          long long q_token_stride, long long q_head_stride, const void* k,
+                          long long k_token_stride, long long k_head_stride, const void* v,
+                          long long v_token_stride, long long v_head_stride, int rot,
+                          const float* table, int table_len, const void* positions, int pos_bytes,
+                          int interleaved, fa_stream_t stream) {
+    const fa_status cs = check_cache(cache);
+    if (cs != FA_OK) return cs;
+    if (layer < 0 || layer >= cache->layers) return FA_ERR_INVALID_ARG;
+    RotParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.in[0] = q; p.out[0] = q_out; p.heads[0] = Hq; p.ts[0] = q_token_stride; p.hs[0] = q_head_stride;
+    p.in[1] = k; p.heads[1] = cache->heads; p.ts[1] = k_token_stride; p.hs[1] = k_head_stride;
+    p.in[2] = v; p.heads[2] = cache->heads; p.ts[2] = v_token_stride; p.hs[2] = v_head_stride;
+    p.T = T; p.d = cache->d; p.rot = rot;
+    p.table = reinterpret_cast<const float2*>(table);
+    p.table_len = table_len;
+    p.positions = positions;
+    p.pos64 = pos_bytes == 8;
+    p.cu = cu_seqlens;
+    p.B = B; p.N = N;
+    p.cache = *cache;
+    p.slots = slots;
+    p.layer = layer;
+    const fa_status st = check_rotary(p, table, pos_bytes);
+    if (st != FA_OK) return st;
+    if (T == 0) return FA_OK;
+    if (!slots || !k || !v || (Hq > 0 && (!q || !q_out)) || (rot > 0 && (!table || !table_len)))
+        return FA_ERR_INVALID_ARG;
+    if (!aligned(slots, 4) || !aligned(q, 2) || !aligned(q_out, 2) || !aligned(k, 2) || !aligned(v, 2))
+        return FA_ERR_INVALID_ARG;
+    const cudaError_t err = launch_any<__nv_bfloat16, true>(p, interleaved,
+                                                            reinterpret_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,1108 @@
+// tree.cu -- attention of new tokens over a paged key/value cache, for sm_103a:
+// single tokens, chunks of a prompt (causal) and trees of drafted tokens.
+//
+// A sequence holds len = ctx + n tokens in the cache, the last n of which are
+// the call's.  Row t sees every key of the context, and of its own n tokens
+// those with index <= t (no mask) or those whose bit is set in its mask row.
+//   m = max_j s_j,  l = sum_j 2^(s_j - m),  O = sum_j 2^(s_j - m) v_j / l,
+// with s = q.k * scale * log2 e over the visible keys j; LSE = (m + log2 l) ln 2.
+// The sums split: any two disjoint key ranges with their own (m, l, O~) join by
+// rescaling both to the larger m.  That identity carries the kernel twice: the
+// two softmax streams of a CTA take alternate key tiles, and the CTAs take
+// equal stretches of all tiles together, whatever item those belong to.
+//
+// Bound: reading the cache once.  The query rows are the group's heads times
+// the tokens (row = token * G + head), so a decoding step has few of them and
+// the tensor core runs mostly padded rows; a 128 x 128 x 128 tile pair costs
+// ~1040 tensor cycles against the ~2800 that its 64 KB take at this SM's share
+// of the memory bandwidth, so padding is free and the work per SM is all that
+// matters.  Hence:
+//   - linear split: all (sequence, kv head, row tile) items' key tiles stand in
+//     one line and CTA c takes [c * per, (c + 1) * per).  Every SM streams the
+//     same number of tiles for any mix of lengths; an item that spans CTAs
+//     leaves partials, joined by a second small kernel in a fixed order.
+//   - the K and V tiles of a CTA run through one ring of stages in the order
+//     the tensor core consumes them, filled by TMA boxes of one page each.
+//   - up to d = 128 two streams (softmax warpgroups, S/P and O in TMEM) work on
+//     alternate key tiles of one row tile; with more than 128 rows they take
+//     two row tiles and share each key tile (PAIR), since then the tensor core
+//     is the bound.  Above d = 128 TMEM holds one O: one stream with two S
+//     buffers, on tiles of 64 keys.
+//
+// Pages hold whatever was there before: keys past the length never reach a
+// sum (their scores are replaced, their V rows zeroed in shared memory), and
+// a drafted token's V that is not finite is kept from the rows that do not
+// see it: it is zeroed in shared memory and added to the rows that do see it
+// at the end.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "cache.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr float kRescale = 8.0f;  // log2 units: P <= 256 before the reference moves
+
+template <int D, bool PAIR>
+struct Cfg {
+    static constexpr int kBN = D > 128 ? 64 : 128;       // keys of a tile
+    static constexpr int kCols = D / 64;                 // 64-column boxes
+    static constexpr int kQTiles = PAIR ? 2 : 1;
+    static constexpr int kQBytes = 128 * D * 2;
+    static constexpr int kStageBytes = kBN * D * 2;      // one K or V tile
+    // what 227 KB leave beside Q, the alignment, and the barriers and statistics
+    static constexpr int kRoom = 232448 - 1024 - 5120 - kQTiles * kQBytes;
+    static constexpr int kMaxStages = kRoom / kStageBytes;
+    static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
+    static constexpr int kStreams = D > 128 ? 1 : 2;     // O accumulators
+    static_assert(kStages >= 4, "the ring holds two K and two V tiles");
+    static_assert(!PAIR || D <= 128, "two row tiles need two O accumulators");
+};
+
+// A stretch of one item's key tiles, worked on by one CTA.
+struct Piece {
+    int b, h;            // sequence (< 0: none left), kv head
+    int tok0, ntok;      // first token of the row tile(s) in the packed batch, tokens
+    int trow0;           // the first token's index in the sequence
+    int slot, ctx, len;
+    int k0, n;           // key tiles [k0, k0 + n)
+    int part;            // partial slot, or -1: the whole item
+};
+
+template <int D, bool PAIR>
+struct Smem {
+    using C = Cfg<D, PAIR>;
+    alignas(1024) uint8_t q[C::kQTiles][C::kQBytes];
+    alignas(1024) uint8_t kv[C::kStages][C::kStageBytes];
+    alignas(8) uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t q_full, q_empty, piece_full[2], piece_empty[2];
+    uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain;
+    Piece piece[2];
+    int start[4];        // this CTA's first item: sequence, kv head, row tile, key tile
+    long long sums[kThreads / 32];
+    uint32_t tmem_base;
+    int abort_flag, zero;
+    int poison;          // a drafted V that is not finite has been met (never cleared)
+    // row statistics that the two warpgroups exchange: [piece parity][stream][m, l]
+    float stats[2][2][2][128];
+};
+
+template <int D, bool PAIR>
+constexpr size_t smem_bytes() {
+    static_assert(sizeof(Smem<D, PAIR>) + 1024 <= 232448, "shared memory exceeds 227 KB");
+    return sizeof(Smem<D, PAIR>) + 1024;
+}
+
+struct SeqInfo {
+    int t0, n, slot, len, ctx, bad;
+};
+
+__device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int i) {
+    SeqInfo s;
+    const SeqRange r = seq_range(p.cu, p.N, p.T, i);
+    s.t0 = r.t0;
+    s.n = r.n;
+    s.slot = s.len = s.ctx = s.bad = 0;
+    if (r.n < 0) {  // boundaries out of order: no rows
+        s.n = 0;
+        s.bad = kCacheBadLength;
+        return s;
+    }
+    if (r.n == 0) return s;
+    s.slot = p.slots[i];
+    if (s.slot < 0 || s.slot >= p.cache.slots) {
+        s.slot = 0;
+        s.bad = kCacheBadSlot;
+        return s;
+    }
+    const int len = p.cache.lengths[s.slot];
+    if (len < s.n || s.n > p.N || len > (long long)p.cache.max_pages * p.cache.page_size) {
+        s.bad = kCacheBadLength;  // its rows see no key
+        return s;
+    }
+    s.len = len;
+    s.ctx = len - s.n;
+    return s;
+}
+
+// Key tiles that row tile q of a sequence visits (one even when it sees no
+// key, so that its rows are written).
+__device__ __forceinline__ int item_tiles(const TreeParams& p, const SeqInfo& s, int q, int tokens,
+                                          int bn) {
+    int keys = s.len;
+    if (!p.mask && s.len > 0) keys = min(s.len, s.ctx + min(s.n, (q + 1) * tokens));
+    return max(1, (keys + bn - 1) / bn);
+}
+
+__device__ __forceinline__ long long head_tiles(const TreeParams& p, const SeqInfo& s, int tokens,
+                                                int bn) {
+    const int nq = (s.n + tokens - 1) / tokens;
+    if (p.mask || s.len == 0) return (long long)nq * item_tiles(p, s, 0, tokens, bn);
+    long long sum = 0;
+    for (int q = 0; q < nq; ++q) sum += item_tiles(p, s, q, tokens, bn);
+    return sum;
+}
+
+__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* flag,
+                                             int* status) {
+    if (mbar_wait(bar, parity, flag)) return true;
+    *flag = 1;
+    atomicOr(status, kCacheTimeout);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
+                                          int* status) {
+    return __all_sync(0xffffffffu, wait_or_stop(bar, parity, flag, status));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                            int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ bool finite_bf16(uint32_t lo16) { return (lo16 & 0x7F80u) != 0x7F80u; }
+
+// Bits of the 32 keys from `j0` (an index among the sequence's own tokens;
+// negative: the context) that a row sees.
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t* words, int nwords, int j0) {
+    const int w = j0 >> 5;  // floor
+    const uint32_t lo = w < 0 ? 0xffffffffu : (w < nwords ? words[w] : 0u);
+    const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < nwords ? words[w + 1] : 0u);
+    return __funnelshift_r(lo, hi, j0 & 31);
+}
+
+// P = 2^(s c - m) of 32 columns as bf16 pairs (each rounded once: P enters the
+// tensor core in the type of V), and their fp32 sum before that rounding.
+__device__ __forceinline__ void exp_chunk(const float* s, float c, float neg, uint64_t (&acc)[2],
+                                          uint32_t (&pk)[16]) {
+    const uint64_t c2 = f2_pack(c, c), n2 = f2_pack(neg, neg);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint64_t x = f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), c2, n2);
+        float x0, x1;
+        f2_unpack(x, x0, x1);
+        x0 = ex2_approx(x0);
+        x1 = ex2_approx(x1);
+        acc[i & 1] = f2_add(acc[i & 1], f2_pack(x0, x1));
+        pk[i] = pack_bf16x2(x0, x1);
+    }
+}
+
+// FIFO place, within a piece of n tiles, of tile j's K and V.
+template <bool PAIR>
+__device__ __forceinline__ int fifo_k(int j) {
+    return PAIR ? 2 * j : (j == 0 ? 0 : 2 * j - 1);
+}
+template <bool PAIR>
+__device__ __forceinline__ int fifo_v(int j, int n) {
+    return PAIR ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
+}
+
+// D: tile columns; DR: head dimension in memory (96 runs on 128 columns whose
+// last 32 the TMA fills with zeros).
+template <int D, int DR, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
+    pdl_trigger();
+    using C = Cfg<D, PAIR>;
+    using SM = Smem<D, PAIR>;
+    constexpr int S = C::kStages, BN = C::kBN;
+    extern __shared__ uint8_t smem_raw[];
+    SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                    ~uintptr_t(1023));
+    const int warp = warp_id(), lane = lane_id();
+    volatile int* stop = &sm.abort_flag;
+    int* status = p.cache.scratch;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sm.q_full), 1);
+        mbar_init(smem_u32(&sm.q_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.piece_full[i]), 1);
+            mbar_init(smem_u32(&sm.piece_empty[i]), 1 + 8);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.p_hi[i]), 4);
+            mbar_init(smem_u32(&sm.o_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_free[i]), PAIR ? 4 : 8);
+        }
+        mbar_init(smem_u32(&sm.stat_full), 8);
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort_flag = sm.zero = sm.poison = 0;
+        sm.start[0] = -1;
+        fence_barrier_init();
+    }
+    if (warp == 2) {
+        tmem_alloc(smem_u32(&sm.tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const int tokens = p.tile_tokens * C::kQTiles;  // tokens of an item
+    pdl_wait();
+
+    // ---- the line of all key tiles, and where this CTA's stretch begins
+    long long per, begin, end;
+    {
+        const int chunk = (p.B + kThreads - 1) / kThreads;
+        const int i0 = threadIdx.x * chunk, i1 = min(p.B, i0 + chunk);
+        long long mine = 0;
+        int bad = 0;
+        for (int i = i0; i < i1; ++i) {
+            const SeqInfo s = seq_info(p, i);
+            bad |= s.bad;
+            mine += head_tiles(p, s, tokens, BN) * p.cache.heads;
+        }
+        if (bad && blockIdx.x == 0) atomicOr(status, bad);
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) sm.sums[warp] = incl;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sm.sums[w];
+            total += sm.sums[w];
+        }
+        per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
+        begin = min(total, per * blockIdx.x);
+        end = min(total, begin + per);
+        long long at = before + incl - mine;  // first tile of this thread's sequences
+        if (begin < end && begin >= at && begin < at + mine) {
+            for (int i = i0; i < i1; ++i) {
+                const SeqInfo s = seq_info(p, i);
+                const long long ht = head_tiles(p, s, tokens, BN), all = ht * p.cache.heads;
+                if (begin >= at + all) {
+                    at += all;
+                    continue;
+                }
+                const int h = (int)((begin - at) / ht);
+                int k = (int)((begin - at) - h * ht), q = 0;
+                for (;; ++q) {
+                    const int t = item_tiles(p, s, q, tokens, BN);
+                    if (k < t) break;
+                    k -= t;
+                }
+                sm.start[0] = i;
+                sm.start[1] = h;
+                sm.start[2] = q;
+                sm.start[3] = k;
+                break;
+            }
+        }
+        __syncthreads();
+    }
+    static_assert(128 * 72 + 256 * 216 == 384 * 168, "register split must match the launch");
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        setmaxnreg_dec<72>();
+        int it = 0, f = 0, nq = 0;  // pieces, stages and query loads so far
+        bool ok = true;
+        int own_first = -1, own_tok0 = 0, own_ntok = 0, own_h = 0;  // an item that ends here
+        int b = sm.start[0], h = sm.start[1], q = sm.start[2], k0 = sm.start[3];
+        long long left = end - begin;
+        SeqInfo s;
+        s.n = 0;
+        if (left > 0) s = seq_info(p, b);
+        const int ps = p.cache.page_size;
+        const int rows = min(ps, BN);          // keys of one box
+        const int boxes = BN / rows;
+        const int my_box = lane / C::kCols, my_col = lane % C::kCols;
+        const bool has_box = my_box < boxes;
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_empty[slot]), ((it >> 1) & 1) ^ 1, stop, status)))
+                break;
+            Piece x;
+            if (left <= 0) {
+                if (lane == 0) {
+                    sm.piece[slot].b = -1;
+                    mbar_arrive(smem_u32(&sm.piece_full[slot]));
+                }
+                break;
+            }
+            const int tiles = item_tiles(p, s, q, tokens, BN);
+            x.b = b;
+            x.h = h;
+            x.trow0 = q * tokens;
+            x.tok0 = s.t0 + x.trow0;
+            x.ntok = min(tokens, s.n - x.trow0);
+            x.slot = s.slot;
+            x.ctx = s.ctx;
+            x.len = s.len;
+            x.k0 = k0;
+            x.n = (int)min((long long)(tiles - k0), left);
+            const bool whole_end = k0 + x.n == tiles;
+            x.part = k0 == 0 ? (whole_end ? -1 : 2 * (int)blockIdx.x + 1) : 2 * (int)blockIdx.x;
+            if (k0 > 0 && whole_end) {  // this CTA's first piece ends an item begun elsewhere
+                own_first = (int)((begin - k0) / per);
+                own_tok0 = x.tok0;
+                own_ntok = x.ntok;
+                own_h = h;
+            }
+            if (lane == 0) {
+                sm.piece[slot] = x;
+                mbar_arrive(smem_u32(&sm.piece_full[slot]));
+            }
+            __syncwarp();
+
+            // -- loads of this piece
+            const int* table = p.cache.table + (long long)x.slot * p.cache.max_pages;
+            const int used = (x.len + ps - 1) / ps;
+            auto table_at = [&](int i) { return i < used ? table[i] : -1; };
+            // page ids of a window of 32 pages, and of the next one
+            int win = (int)((long long)x.k0 * BN / ps);
+            int ids = table_at(win + lane), nxt = table_at(win + 32 + lane);
+            int page_prev = -1;
+            // the page of this lane's box in tile j
+            auto page_of = [&](int j) {
+                const int first = (int)((long long)(x.k0 + j) * BN / ps);
+                if (first >= win + 32) {
+                    win += 32;
+                    ids = nxt;
+                    nxt = table_at(win + 32 + lane);
+                }
+                return __shfl_sync(0xffffffffu, ids, (first - win + my_box) & 31);
+            };
+            auto load_tile = [&](int j, int page, const CUtensorMap* map) {
+                const int st = f % S;
+                if (!(ok = warp_wait(smem_u32(&sm.empty[st]), ((f / S) & 1) ^ 1, stop, status)))
+                    return;
+                const int key0 = (x.k0 + j) * BN, key = key0 + my_box * rows;
+                const int have = max(0, min(boxes, (x.len - key0 + rows - 1) / rows));
+                const uint32_t bar = smem_u32(&sm.full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, have * rows * 128 * C::kCols);
+                __syncwarp();
+                if (has_box && my_box < have) {
+                    // a page id out of range reads the fill value (zeros) and is reported
+                    int plane = -1;
+                    if (page >= 0 && page < p.cache.pages)
+                        plane = (p.layer * p.cache.pages + page) * p.cache.heads + x.h;
+                    else
+                        atomicOr(status, kCacheBadSlot);
+                    tma_load_3d(smem_u32(sm.kv[st]) + my_col * (BN * 128) + my_box * rows * 128, map,
+                                bar, my_col * 64, key % ps, plane);
+                }
+                ++f;
+            };
+            auto load_q = [&] {
+                if (!(ok = warp_wait(smem_u32(&sm.q_empty), (it & 1) ^ 1, stop, status))) return;
+                if (lane == 0) {
+                    const uint32_t bar = smem_u32(&sm.q_full);
+                    const int nt = PAIR && x.ntok > p.tile_tokens ? 2 : 1;
+                    mbar_arrive_expect_tx(bar, nt * p.tile_tokens * p.group * 128 * C::kCols);
+                    for (int t = 0; t < nt; ++t)
+                        for (int c = 0; c < C::kCols; ++c)
+                            tma_load_4d(smem_u32(sm.q[t]) + c * 16384, &p.tm_q, bar, c * 64, 0, x.h,
+                                        x.tok0 + t * p.tile_tokens);
+                }
+                __syncwarp();
+                ++nq;
+            };
+            if constexpr (PAIR) {
+                for (int j = 0; j < x.n && ok; ++j) {
+                    const int pg = page_of(j);
+                    load_tile(j, pg, &p.tm_k);
+                    if (ok && j == 0) load_q();
+                    if (ok) load_tile(j, pg, &p.tm_v);
+                }
+            } else {
+                for (int j = 0; j <= x.n && ok; ++j) {
+                    int pg = -1;
+                    if (j < x.n) {
+                        pg = page_of(j);
+                        load_tile(j, pg, &p.tm_k);
+                        if (ok && j == 0) load_q();
+                    }
+                    if (ok && j >= 1) load_tile(j - 1, page_prev, &p.tm_v);
+                    page_prev = pg;
+                }
+            }
+            ++it;
+            // -- the next item
+            left -= x.n;
+            k0 = 0;
+            if (left > 0) {
+                ++q;
+                if (q * tokens >= s.n) {
+                    q = 0;
+                    if (++h == p.cache.heads) {
+                        h = 0;
+                        do {
+                            ++b;
+                            if (b >= p.B) {  // (cannot be: left counts real tiles)
+                                left = 0;
+                                break;
+                            }
+                            s = seq_info(p, b);
+                        } while (s.n == 0);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            p.meta[blockIdx.x] = make_int4(own_first, own_tok0, own_ntok, own_h);
+            // Never leave a TMA write in flight.
+            const volatile int* z = &sm.zero;
+            for (int i = 0; i < S && i < f; ++i) {
+                const int g = f - 1 - i;
+                mbar_wait(smem_u32(&sm.full[g % S]), (g / S) & 1, z);
+            }
+            if (nq > 0) mbar_wait(smem_u32(&sm.q_full), (nq - 1) & 1, z);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        setmaxnreg_dec<72>();
+        if (lane == 0) {
+            constexpr uint32_t idS = make_idesc_bf16(128, BN, false, false);
+            constexpr uint32_t idPV = make_idesc_bf16(128, D, false, true);
+            int it = 0, f = 0;
+            int cnt[2] = {0, 0};  // tiles through each S buffer
+            int done[2] = {0, 0}; // PAIR: pieces of each stream
+            bool ok = true;
+            auto wait = [&](uint64_t& bar, int n) {
+                return ok = ok && wait_or_stop(smem_u32(&bar), n & 1, stop, status);
+            };
+            auto issue_s = [&](int stage_no, int buf, int qt) {
+                const uint64_t da = make_sdesc_here(smem_u32(sm.q[qt]), 16, 1024);
+                const uint64_t db = make_sdesc_here(smem_u32(sm.kv[stage_no % S]), 16, 1024);
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < DR / 16; ++kk)
+                    mma_ss(tmem + buf * 128, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
+                           sdesc_add(db, (kk >> 2) * (BN * 128) + (kk & 3) * 32), idS, kk > 0);
+            };
+            auto issue_pv = [&](int stage_no, int buf, int o, int c, bool first) {
+                // keys [0, BN/2) of P, then the others once the softmax has them
+                const uint64_t db = make_sdesc_here(smem_u32(sm.kv[stage_no % S]), BN * 128, 1024);
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk) {
+                    if (kk == BN / 32) {
+                        if (!wait(sm.p_hi[buf], c)) return;
+                        tc_fence_after();
+                    }
+                    mma_ts(tmem + 256 + o * 128, tmem + buf * 128 + kk * 8, sdesc_add(db, kk * 2048),
+                           idPV, (first && kk == 0) ? 0u : 1u);
+                }
+            };
+            while (ok) {
+                const int slot = it & 1;
+                if (!wait(sm.piece_full[slot], it >> 1)) break;
+                const int pb = sm.piece[slot].b, n = sm.piece[slot].n, nt = sm.piece[slot].ntok;
+                mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+                if (pb < 0) break;
+                if (!wait(sm.q_full, it)) break;
+                if constexpr (PAIR) {
+                    const int ns = nt > p.tile_tokens ? 2 : 1;
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int fk = f + 2 * j, fv = fk + 1;
+                        if (!wait(sm.full[fk % S], fk / S)) break;
+                        for (int s = 0; s < ns && ok; ++s) {
+                            // S_s is free once the P written over it has been read
+                            if (cnt[s] > 0 && !wait(sm.o_done[s], cnt[s] - 1)) break;
+                            issue_s(fk, s, s);
+                            mma_commit(smem_u32(&sm.s_full[s]));
+                        }
+                        if (!ok) break;
+                        mma_commit(smem_u32(&sm.empty[fk % S]));
+                        if (j == n - 1) mma_commit(smem_u32(&sm.q_empty));
+                        for (int s = 0; s < ns && ok; ++s) {
+                            // (stream 0 mends V before its P is ready, so both may follow it)
+                            if (!wait(sm.p_full[s], cnt[s])) break;
+                            if (s == 0 && !wait(sm.full[fv % S], fv / S)) break;
+                            if (j == 0 && done[s] > 0 && !wait(sm.o_free[s], done[s] - 1)) break;
+                            issue_pv(fv, s, s, cnt[s], j == 0);
+                            if (!ok) break;
+                            mma_commit(smem_u32(&sm.o_done[s]));
+                            ++cnt[s];
+                        }
+                        if (!ok) break;
+                        mma_commit(smem_u32(&sm.empty[fv % S]));
+                    }
+                    for (int s = 0; s < ns; ++s) ++done[s];
+                } else {
+                    // S runs one tile ahead: S(0), S(1), PV(0), S(2), PV(1), ...
+                    auto do_s = [&](int j) {
+                        const int fk = f + fifo_k<false>(j), bf = j & 1;
+                        if (!wait(sm.full[fk % S], fk / S)) return;
+                        // the buffer's P of two tiles ago has been read
+                        const int c = cnt[bf] + (j >> 1);
+                        if (c > 0 && !wait(sm.o_done[bf], c - 1)) return;
+                        issue_s(fk, bf, 0);
+                        mma_commit(smem_u32(&sm.empty[fk % S]));
+                        mma_commit(smem_u32(&sm.s_full[bf]));
+                        if (j == n - 1) mma_commit(smem_u32(&sm.q_empty));
+                    };
+                    do_s(0);
+                    if (ok && n > 1) do_s(1);
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int fv = f + fifo_v<false>(j, n), bf = j & 1;
+                        const int c = cnt[bf] + (j >> 1);
+                        if (!wait(sm.p_full[bf], c)) break;
+                        if (!wait(sm.full[fv % S], fv / S)) break;
+                        if (j == 0 && it > 0 && !wait(sm.o_free[0], it - 1)) break;
+                        issue_pv(fv, bf, C::kStreams == 2 ? bf : 0, c,
+                                 C::kStreams == 2 ? j < 2 : j == 0);
+                        if (!ok) break;
+                        mma_commit(smem_u32(&sm.empty[fv % S]));
+                        mma_commit(smem_u32(&sm.o_done[bf]));
+                        if (j + 2 < n) do_s(j + 2);
+                    }
+                    cnt[0] += (n + 1) / 2;
+                    cnt[1] += n / 2;
+                }
+                if (!ok) break;
+                f += 2 * n;
+                ++it;
+            }
+            mma_commit(smem_u32(&sm.drain));
+            mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ softmax and epilogue
+        setmaxnreg_inc<216>();
+        const int w = (warp - 4) >> 2;          // stream
+        const int q4 = warp & 3;                // TMEM lane quarter
+        const int row = q4 * 32 + lane;
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        const int row_tok = row / p.group, row_head = row - row_tok * p.group;
+        const bool row_used = row_tok < p.tile_tokens;
+        int it = 0, f = 0, cnt[2] = {0, 0};
+        bool ok = true;
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_full[slot]), (it >> 1) & 1, stop, status))) break;
+            const Piece x = sm.piece[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+            if (x.b < 0) break;
+            const int tok_first = PAIR ? w * p.tile_tokens : 0;  // of this stream's rows
+            const int ntok = min(p.tile_tokens, x.ntok - tok_first);  // <= 0: no rows
+            const bool valid = row_used && row_tok < ntok;
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            const int trow = x.trow0 + tok_first + row_tok;  // index in the sequence
+            const size_t tok = (size_t)x.tok0 + tok_first + row_tok;
+            // no key from `limit` on is visible; without a mask all before it are
+            const int limit = p.mask ? x.len : min(x.len, x.ctx + trow + 1);
+            const uint32_t* words = p.mask
+                ? reinterpret_cast<const uint32_t*>(p.mask) + (valid ? tok : 0) * (2 * (size_t)p.words)
+                : nullptr;
+            const bool active = PAIR ? ntok > 0 : (C::kStreams == 2 || w == 0);
+            const int step = PAIR || C::kStreams == 1 ? 1 : 2;
+            float m_ref = -INFINITY, l = 0.f;
+            bool first = true;  // this stream has had no tile yet
+            if (active) {
+                for (int j = PAIR || C::kStreams == 1 ? 0 : w; j < x.n; j += step) {
+                    const int buf = PAIR ? w : j & 1;
+                    const int c = PAIR ? cnt[w] + j : cnt[buf] + (j >> 1);
+                    const int key0 = (x.k0 + j) * BN;
+                    if (!(ok = warp_wait(smem_u32(&sm.s_full[buf]), c & 1, stop, status))) break;
+                    tc_fence_after();
+                    const uint32_t s_at = tmem + lane_off + buf * 128;
+                    const bool ragged = key0 + BN > x.ctx;
+                    float s[BN];
+                    float alpha = 1.f;
+                    bool need = false;
+                    float neg = 0.f;
+                    if (warp_valid) {
+                        uint32_t r[BN / 32][32];
+#pragma unroll
+                        for (int i = 0; i < BN / 32; ++i) tmem_ld32(s_at + i * 32, r[i]);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < BN; ++i) s[i] = __uint_as_float(r[i / 32][i % 32]);
+                        if (ragged) {
+#pragma unroll
+                            for (int i = 0; i < BN / 32; ++i) {
+                                const int kb = key0 + i * 32;
+                                uint32_t bits = p.mask ? mask_bits(words, 2 * p.words, kb - x.ctx)
+                                                       : 0xffffffffu;
+                                const int room = limit - kb;
+                                if (room <= 0) bits = 0;
+                                else if (room < 32) bits &= (1u << room) - 1u;
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!((bits >> e) & 1u)) s[i * 32 + e] = -INFINITY;
+                            }
+                        }
+                        float m8[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            float m = fmax3(s[k], s[8 + k], s[16 + k]);
+#pragma unroll
+                            for (int i = 24; i + 8 < BN; i += 16) m = fmax3(m, s[i + k], s[i + 8 + k]);
+                            m8[k] = fmaxf(m, s[BN - 8 + k]);
+                        }
+                        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                               fmaxf(m8[6], m8[7])) * p.scale_log2;
+                        if (first) {
+                            m_ref = mx;
+                        } else if (mx > m_ref + kRescale) {
+                            need = true;
+                            alpha = ex2_approx(m_ref - mx);
+                            m_ref = mx;
+                            l *= alpha;
+                        }
+                        neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    }
+                    first = false;
+                    // O~ is stable when its last PV is done: with two streams S(j) was
+                    // issued after that; with one, PV(j - 1) may still run.
+                    if (__any_sync(0xffffffffu, need)) {
+                        const int o = PAIR ? w : (C::kStreams == 2 ? buf : 0);
+                        if (C::kStreams == 1) {
+                            const int pb = (j - 1) & 1;
+                            if (!(ok = warp_wait(smem_u32(&sm.o_done[pb]),
+                                                 (cnt[pb] + ((j - 1) >> 1)) & 1, stop, status)))
+                                break;
+                            tc_fence_after();
+                        }
+                        const uint32_t o_at = tmem + lane_off + 256 + o * 128;
+#pragma unroll 1
+                        for (int cc = 0; cc < DR / 32; ++cc) {
+                            uint32_t ov[32];
+                            tmem_ld32(o_at + cc * 32, ov);
+                            tmem_ld_wait();
+                            uint32_t lo[16], hi[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                lo[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+                                hi[i] = __float_as_uint(__uint_as_float(ov[16 + i]) * alpha);
+                            }
+                            tmem_st16(o_at + cc * 32, lo);
+                            tmem_st16(o_at + cc * 32 + 16, hi);
+                        }
+                    }
+                    // V rows past the length are whatever the page held, and a drafted V
+                    // may be anything: both are mended before P is handed over.
+                    if (ragged && (!PAIR || w == 0)) {
+                        const int fv = f + fifo_v<PAIR>(j, x.n);
+                        if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
+                            break;
+                        if (row < BN && key0 + row >= x.ctx) {
+                            const bool past = key0 + row >= x.len;
+#pragma unroll 1
+                            for (int cb = 0; cb < C::kCols; ++cb) {
+                                uint4* at = reinterpret_cast<uint4*>(sm.kv[fv % S] + cb * (BN * 128) +
+                                                                     row * 128);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int ch = (e + row) & 7;  // (spreads the banks)
+                                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                    if (!past) {
+                                        v = at[ch];
+                                        bool bad = false;
+                                        auto mend = [&](uint32_t& u) {
+                                            if (!finite_bf16(u)) { u &= 0xffff0000u; bad = true; }
+                                            if (!finite_bf16(u >> 16)) { u &= 0xffffu; bad = true; }
+                                        };
+                                        mend(v.x);
+                                        mend(v.y);
+                                        mend(v.z);
+                                        mend(v.w);
+                                        if (!bad) continue;
+                                        *reinterpret_cast<volatile int*>(&sm.poison) = 1;
+                                    }
+                                    at[ch] = v;
+                                }
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                    }
+                    uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (warp_valid) {
+#pragma unroll
+                            for (int cc = hf * (BN / 64); cc < (hf + 1) * (BN / 64); ++cc) {
+                                uint32_t pk[16];
+                                exp_chunk(s + cc * 32, p.scale_log2, neg, acc, pk);
+                                tmem_st16(s_at + cc * 16, pk);
+                            }
+                            tmem_st_wait();
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(hf == 0 ? &sm.p_full[buf] : &sm.p_hi[buf]));
+                    }
+                    if (warp_valid) {
+                        float a0, a1, b0, b1;
+                        f2_unpack(acc[0], a0, a1);
+                        f2_unpack(acc[1], b0, b1);
+                        l += (a0 + a1) + (b0 + b1);
+                    }
+                }
+            }
+            if (!ok) break;
+
+            // ---- epilogue
+            float w0 = 1.f, w1 = 0.f;      // weights of the two accumulators
+            const bool two = !PAIR && C::kStreams == 2 && x.n > 1;
+            if constexpr (!PAIR) {
+                // both warpgroups need both streams' statistics: each then stores
+                // every other 32 columns
+                auto& st = sm.stats[it & 1];
+                if (w < C::kStreams) {
+                    st[w][0][row] = m_ref;
+                    st[w][1][row] = l;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.stat_full));
+                if (!(ok = warp_wait(smem_u32(&sm.stat_full), it & 1, stop, status))) break;
+                m_ref = st[0][0][row];
+                l = st[0][1][row];
+                if (two) {
+                    const float m1 = st[1][0][row], l1 = st[1][1][row];
+                    const float m = fmaxf(m_ref, m1), base = m == -INFINITY ? 0.f : m;
+                    w0 = ex2_approx(m_ref - base);
+                    w1 = ex2_approx(m1 - base);
+                    l = l * w0 + l1 * w1;
+                    m_ref = m;
+                }
+                // the last PV of each buffer
+                const int n0 = (x.n + 1) / 2, n1 = x.n / 2;
+                if (!(ok = warp_wait(smem_u32(&sm.o_done[0]), (cnt[0] + n0 - 1) & 1, stop, status)))
+                    break;
+                if (x.n > 1 &&
+                    !(ok = warp_wait(smem_u32(&sm.o_done[1]), (cnt[1] + n1 - 1) & 1, stop, status)))
+                    break;
+                cnt[0] += n0;
+                cnt[1] += n1;
+            } else if (active) {
+                if (!(ok = warp_wait(smem_u32(&sm.o_done[w]), (cnt[w] + x.n - 1) & 1, stop, status)))
+                    break;
+                cnt[w] += x.n;
+            }
+            tc_fence_after();
+            if (active || !PAIR) {
+                const int poison = *reinterpret_cast<volatile int*>(&sm.poison);
+                const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+                const int head = x.h * p.group + row_head;
+                if (valid && (PAIR || w == 0)) {
+                    if (x.part < 0) {
+                        p.lse[(size_t)head * p.T + tok] = (m_ref + __log2f(l)) * 0.69314718055994531f;
+                    } else {
+                        float* st = p.part_stats + ((size_t)x.part * p.part_rows +
+                                                    (PAIR ? w * 128 : 0) + row) * 2;
+                        st[0] = m_ref;
+                        st[1] = l;
+                    }
+                }
+                if (warp_valid) {
+#pragma unroll 1
+                    for (int cc = PAIR ? 0 : w; cc < DR / 32; cc += PAIR ? 1 : 2) {
+                        float o[32];
+                        {
+                            uint32_t ov[32];
+                            tmem_ld32(tmem + lane_off + 256 + (PAIR ? w * 128 : 0) + cc * 32, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(ov[i]) * w0;
+                        }
+                        if (two) {
+                            uint32_t ov[32];
+                            tmem_ld32(tmem + lane_off + 384 + cc * 32, ov);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                o[i] = fmaf(__uint_as_float(ov[i]), w1, o[i]);
+                        }
+                        if (x.part < 0) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= inv;
+                        }
+                        if (poison && valid) {
+                            // a visible drafted V that is not finite: its weight is
+                            // positive, so it adds itself
+                            const int ps = p.cache.page_size;
+                            const int ka = max(x.ctx, x.k0 * BN);
+                            const int kz = min(limit, (x.k0 + x.n) * BN);
+                            for (int key = ka; key < kz; ++key) {
+                                if (p.mask && !(mask_bits(words, 2 * p.words, key - x.ctx) & 1u))
+                                    continue;
+                                const int page = p.cache.table[(long long)x.slot * p.cache.max_pages +
+                                                               key / ps];
+                                if (page < 0 || page >= p.cache.pages) continue;
+                                const uint16_t* v =
+                                    static_cast<const uint16_t*>(p.cache.v) +
+                                    ((((long long)p.layer * p.cache.pages + page) * p.cache.heads +
+                                      x.h) * ps + key % ps) * DR + cc * 32;
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) {
+                                    const uint32_t u = v[i];
+                                    if (!finite_bf16(u)) o[i] += __uint_as_float(u << 16);
+                                }
+                            }
+                        }
+                        if (valid && x.part < 0) {
+                            uint4* dst = reinterpret_cast<uint4*>(
+                                static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR + cc * 32);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                dst[i] = make_uint4(pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                                    pack_bf16x2(o[8 * i + 2], o[8 * i + 3]),
+                                                    pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                                    pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                        } else if (valid) {
+                            float4* dst = reinterpret_cast<float4*>(
+                                p.part_o + ((size_t)x.part * p.part_rows + (PAIR ? w * 128 : 0) + row) *
+                                               DR + cc * 32);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[PAIR ? w : 0]));
+            }
+            f += 2 * x.n;
+            ++it;
+        }
+    } else {
+        setmaxnreg_dec<72>();  // warps 2 and 3: TMEM allocation only
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the partials of every item that more than one CTA worked on: the CTA
+// whose first piece ends the item left (first CTA, token, tokens, head) in
+// meta; its partials stand in slot 2c + 1 of that first CTA and slot 2c of
+// the others, and are added in that order.  One warp a row.  Tokens that no
+// sequence owns are zeroed when asked to.
+template <int DR>
+__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
+    pdl_begin();
+    const int4 own = p.meta[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot_row = blockIdx.y * 8 + warp;
+    const int stream = slot_row >> 7, row = slot_row & 127;
+    const int row_tok = row / p.group;
+    const int t = stream * p.tile_tokens + row_tok;
+    if (own.x >= 0 && slot_row < p.part_rows && row_tok < p.tile_tokens && t < own.z) {
+        const int c0 = own.x, n = (int)blockIdx.x - c0 + 1;
+        auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + slot_row; };
+        float m = -INFINITY;
+        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_stats[slot(i) * 2]);
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float base = m == -INFINITY ? 0.f : m;
+        constexpr int V = DR / 32;  // columns of a lane: lane, lane + 32, ...
+        float acc[V], l = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const size_t s = slot(i);
+            const float w = ex2_approx(p.part_stats[s * 2] - base);
+            l += p.part_stats[s * 2 + 1] * w;
+#pragma unroll
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(p.part_o[s * DR + v * 32 + lane], w, acc[v]);
+        }
+        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+        const size_t tok = (size_t)own.y + t;
+        const int head = own.w * p.group + row - row_tok * p.group;
+        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v * 32 + lane] = __float2bfloat16_rn(acc[v] * inv);
+        if (lane == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
+    }
+    if (p.zero_rest && p.cu) {
+        const int used = min(max(p.cu[p.B], 0), p.T);
+        const long long step = (long long)gridDim.x * gridDim.y * 256;
+        const long long at = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+        const long long rows = (long long)(p.T - used) * p.Hq;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
+                                            (long long)used * p.Hq * DR);
+        for (long long i = at; i < rows * (DR / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (long long i = at; i < rows; i += step)
+            p.lse[(i / (p.T - used)) * p.T + used + i % (p.T - used)] = -INFINITY;
+    }
+}
+
+// Ancestor bits of drafted trees: token t of a sequence sees itself, its
+// parent, its parent's parent, ... up to a token whose parent is -1 (or is not
+// an earlier token of the sequence).  A thread a row.
+__global__ void tree_mask_kernel(const int* parents, const int* cu, int B, int N, int T, int words,
+                                 unsigned long long* mask) {
+    pdl_begin();
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t >= T) return;
+    unsigned long long* row = mask + (size_t)t * words;
+    for (int i = 0; i < words; ++i) row[i] = 0ull;
+    const int b = seq_of_token(cu, B, N, t);
+    if (b < 0) return;
+    const int t0 = cu ? max(cu[b], 0) : b * N;
+    int j = t - t0;
+    while (j >= 0) {
+        if (j < words * 64) row[j >> 6] |= 1ull << (j & 63);
+        const int up = parents[t0 + j];
+        if (up >= j) break;
+        j = up;
+    }
+}
+
+template <int D, int DR, bool PAIR>
+cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
+    auto kern = tree_kernel<D, DR, PAIR>;
+    constexpr size_t smem = smem_bytes<D, PAIR>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(tree_join_kernel<DR>, dim3(ctas, cdiv(p.part_rows, 8)), dim3(256), 0, stream, p);
+}
+
+// Row tiles: as many whole tokens (of group rows each) as 128 rows hold; more
+// rows than that take them in pairs where TMEM has two accumulators.
+struct Tiles {
+    int tokens, rows;
+    bool pair;
+};
+Tiles row_tiles(int group, int N, int d) {
+    Tiles t;
+    t.tokens = 128 / group < N ? 128 / group : N;
+    t.pair = d <= 128 && N > 128 / group;
+    t.rows = t.pair ? 256 : t.tokens * group;
+    return t;
+}
+
+struct TreeWs {
+    size_t stats, o, bytes;
+};
+TreeWs tree_ws(int rows, int d) {
+    TreeWs w;
+    w.stats = align_up(kTreeMaxCtas * sizeof(int4), kAlign);
+    w.o = align_up(w.stats + (size_t)kTreeMaxCtas * 2 * rows * 2 * sizeof(float), kAlign);
+    w.bytes = align_up(w.o + (size_t)kTreeMaxCtas * 2 * rows * d * sizeof(float), kAlign);
+    return w;
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_tree_workspace_size(int Hq, int Hkv, int N, int d) {
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || N <= 0 || d <= 0) return 0;
+    return tree_ws(row_tiles(Hq / Hkv, N, d).rows, d).bytes;
+}
+
+fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, int T, int words,
+                       void* mask, fa_stream_t stream) {
+    if (B < 0 || N < 0 || T < 0 || words <= 0 || (long long)words * 64 < N) return FA_ERR_INVALID_ARG;
+    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (T == 0) return FA_OK;
+    if (!parents || !mask || !aligned(parents, 4) || !aligned(cu_seqlens, 4) || !aligned(mask, 8))
+        return FA_ERR_INVALID_ARG;
+    const cudaError_t e = launch_pdl(tree_mask_kernel, dim3(cdiv(T, 128)), dim3(128), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), parents, cu_seqlens, B,
+                                     N, T, words, static_cast<unsigned long long*>(mask));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                      const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
+                      long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
+                      float scale, int zero_rest, void* workspace, size_t workspace_bytes,
+                      fa_stream_t stream) {
+    const fa_status cs = check_cache(cache);
+    if (cs != FA_OK) return cs;
+    const int d = cache->d, Hkv = cache->heads;
+    if (layer < 0 || layer >= cache->layers || B < 0 || N < 0 || T < 0 || Hq <= 0 || Hq % Hkv)
+        return FA_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || Hq > 65535 || (long long)T * Hq * d > (1LL << 40)) return FA_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_UNSUPPORTED;
+    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (mask && (mask_words <= 0 || (long long)mask_words * 64 < N)) return FA_ERR_INVALID_ARG;
+    if (T == 0) return FA_OK;
+    if ((B > 0 && !slots) || !q || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
+    if (N == 0) N = 1;  // (a packed batch of empty sequences)
+    if (!aligned(slots, 4) || !aligned(cu_seqlens, 4) || !aligned(q, 16) || !aligned(o, 16) ||
+        !aligned(lse, 4) || !aligned(mask, 8) || !aligned(workspace, 16))
+        return FA_ERR_INVALID_ARG;
+    if (T == 1) q_token_stride = (long long)Hq * d;  // (a stride that is never taken)
+    if (Hq == 1) q_head_stride = d;
+    if (q_token_stride <= 0 || q_head_stride <= 0 || q_token_stride % 8 || q_head_stride % 8 ||
+        q_token_stride >= (1LL << 38) || q_head_stride >= (1LL << 31))
+        return FA_ERR_INVALID_ARG;
+    TreeParams p;
+    std::memset(&p, 0, sizeof(p));
+    p.group = Hq / Hkv;
+    const Tiles tiles = row_tiles(p.group, N, d);
+    const TreeWs ws = tree_ws(tiles.rows, d);
+    if (workspace_bytes < ws.bytes) return FA_ERR_INVALID_ARG;
+    const int bn = d > 128 ? 64 : 128;
+    if (!make_tree_maps(p, *cache, q, T, Hq, q_token_stride, q_head_stride, tiles.tokens, bn))
+        return FA_ERR_CUDA;
+    p.cache = *cache;
+    p.slots = slots;
+    p.cu = cu_seqlens;
+    p.mask = mask;
+    p.words = mask_words;
+    p.o = o;
+    p.lse = lse;
+    char* base = static_cast<char*>(workspace);
+    p.meta = reinterpret_cast<int4*>(base);
+    p.part_stats = reinterpret_cast<float*>(base + ws.stats);
+    p.part_o = reinterpret_cast<float*>(base + ws.o);
+    p.part_rows = tiles.rows;
+    p.layer = layer;
+    p.B = B; p.N = N; p.T = T; p.Hq = Hq;
+    p.tile_tokens = tiles.tokens;
+    p.min_tiles = 1;
+    p.zero_rest = zero_rest ? 1 : 0;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int nsm = device_sms();
+    if (nsm <= 0) return FA_ERR_CUDA;
+    const int ctas = nsm < kTreeMaxCtas ? nsm : kTreeMaxCtas;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (d == 128)
+        e = tiles.pair ? launch_t<128, 128, true>(p, ctas, strm) : launch_t<128, 128, false>(p, ctas, strm);
+    else if (d == 96)
+        e = tiles.pair ? launch_t<128, 96, true>(p, ctas, strm) : launch_t<128, 96, false>(p, ctas, strm);
+    else if (d == 64)
+        e = tiles.pair ? launch_t<64, 64, true>(p, ctas, strm) : launch_t<64, 64, false>(p, ctas, strm);
+    else if (d == 192)
+        e = launch_t<192, 192, false>(p, ctas, strm);
+    else
+        e = launch_t<256, 256, false>(p, ctas, strm);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -275,6 +275,188 @@ fa_status fa_noalloc_check_device_status(fa_stream_t stream);
  */
 fa_status fa_check_device_status(const void* workspace, fa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions
+ * ------------------------------------------------------------------------
+ * A head's first `rot` columns are rot / 2 pairs; at position p pair i turns by
+ * p * freq[i]: (a, b) -> (a cos - b sin, b cos + a sin).  Pair i is columns
+ * (i, i + rot / 2), or with interleaved = 1 columns (2i, 2i + 1); columns from
+ * rot on are copied.  The angles come as a table [length, rot / 2, 2] of (cos,
+ * sin) in fp32 that the caller keeps; any scaling for long contexts is in its
+ * frequencies and factor.
+ */
+
+/*
+ * Fills table[p][i] = scale * (cos, sin)(p * freq[i]) for p in [0, length),
+ * angles in 64 bits.  freq: device double[half]; table: device, 16-byte
+ * aligned.  scale is usually 1 (some scalings for long contexts stretch q and
+ * k by a factor).
+ */
+fa_status fa_rotary_table(const double* freq, int half, long long length, double scale,
+                          float* table, fa_stream_t stream);
+
+/*
+ * q_out[t,h,:] and k_out[t,h,:] = q and k rotated to their tokens' positions.
+ *   q [T,Hq,d], k [T,Hkv,d]: device, dtype bf16 or fp32, last dimension
+ *   contiguous, token and head strides in elements (>= 0).  Hq or Hkv may be 0
+ *   (that tensor is left out).  q_out, k_out: contiguous, same dtype, not
+ *   overlapping the inputs.  Any d <= 65536, rot even, 0 <= rot <= d.
+ *   16-byte alignment of bases and strides and rot a multiple of 16 (of 8 when
+ *   interleaved or fp32) take the fast path; anything else is right but slower.
+ *   positions: device int32 (pos_bytes 4) or int64 (8) [T]; NULL (0) counts
+ *   from 0 in each sequence.  A position outside [0, table_len) makes the
+ *   token's rotated columns NaN and reads nothing.
+ *   Sequences: dense (cu_seqlens NULL, T = B * N) or packed (int32[B+1]);
+ *   without positions, tokens that no packed sequence owns are written as zeros.
+ *   backward = 1 turns the other way (the transpose): the gradient of the
+ *   inputs from that of the outputs.
+ */
+fa_status fa_rotary(const void* q, void* q_out, int Hq, long long q_token_stride,
+                    long long q_head_stride, const void* k, void* k_out, int Hkv,
+                    long long k_token_stride, long long k_head_stride, fa_dtype dtype, int T,
+                    int d, int rot, const float* table, int table_len, const void* positions,
+                    int pos_bytes, int B, int N, const int* cu_seqlens, int interleaved,
+                    int backward, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Paged key/value cache
+ * ------------------------------------------------------------------------
+ * Keys and values of all layers live in pages of page_size tokens; a sequence
+ * ("slot") holds lengths[slot] tokens, token p in row p % page_size of page
+ * table[slot][p / page_size].  Table entries past the pages in use are -1.
+ * refs[page] counts the sequences that hold the page, 0 = free.  A page that is
+ * only partly filled belongs to one sequence.  The caller owns every array;
+ * the calls below keep them consistent.
+ *
+ * All calls on one cache belong to one stream order (a graph replay included):
+ * they share the scratch words.  Lists of slots are device arrays.  What is
+ * wrong in them is found on the device: a call on pages then changes nothing
+ * at all, and the status word in scratch keeps the reason until fa_cache_check
+ * reads it:
+ *   1  a slot or page index out of range, or a slot named twice
+ *   2  a length, count or path that does not fit
+ *   4  not enough free pages
+ *   8  the call would write to a shared page
+ *   16 a bounded wait inside a kernel gave up
+ */
+typedef struct {
+    void* k;        /* device bf16 [layers, pages, heads, page_size, d], 16-byte aligned */
+    void* v;        /* the same */
+    int* table;     /* device int32 [slots, max_pages] */
+    int* lengths;   /* device int32 [slots] */
+    int* refs;      /* device int32 [pages] */
+    int* scratch;   /* device, fa_cache_scratch_size bytes, 16-byte aligned, zeroed once */
+    int layers, pages, heads, page_size, d, slots, max_pages;
+} fa_cache;         /* d: 64, 96, 128, 192 or 256; page_size: 16, 32, 64 or 128 */
+
+/* Bytes of fa_cache.scratch; 0 for invalid sizes. */
+size_t fa_cache_scratch_size(int pages, int slots, int max_pages);
+
+/*
+ * Makes room for counts[i] more tokens (or count each, counts NULL) at the end
+ * of slots[i], i < n: new pages where needed, lowest free index first in the
+ * order of the entries, and lengths raised.  Slots must differ.  The rows are
+ * not written (fa_cache_append does that).
+ */
+fa_status fa_cache_reserve(const fa_cache* cache, const int* slots, const int* counts, int count,
+                           int n, fa_stream_t stream);
+
+/*
+ * children[i] becomes a copy of parents[i]: whole pages are shared, the rows of
+ * a partly filled last page are copied, in all layers.  Children must be empty
+ * and differ; a parent may have several, but may not be a child of this call.
+ */
+fa_status fa_cache_fork(const fa_cache* cache, const int* parents, const int* children, int n,
+                        fa_stream_t stream);
+
+/*
+ * Empties slots: their pages lose a reference and are free at 0.  Freeing an
+ * empty slot, or naming one twice, does nothing more.
+ */
+fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_stream_t stream);
+
+/*
+ * Keeps some of the tokens behind position base[i] of slots[i] -- a verified
+ * path of a drafted tree -- and drops the others: token base[i] + path[i][j]
+ * moves to base[i] + j for j < accepted[i], in all layers, the length becomes
+ * base[i] + accepted[i], and pages past it are released.  path: device
+ * [n, path_width], strictly ascending in its first accepted[i] entries.
+ * accepted[i] = 0 drops the whole draft.  Pages that keep tokens behind
+ * base[i] must not be shared.
+ */
+fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* base, const int* path,
+                          int path_width, const int* accepted, int n, fa_stream_t stream);
+
+/*
+ * Synchronises the stream, reads the status word and clears it: FA_OK,
+ * FA_ERR_TIMEOUT (bit 16) or FA_ERR_INVALID_ARG; the bits go to *bits.
+ */
+fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream);
+
+/*
+ * Writes a call's new keys and values to one layer of the cache, and rotates
+ * them (and q) on the way.
+ *   The call's T tokens are those of B sequences (dense: N each; packed:
+ *   cu_seqlens), sequence i being slots[i].  They are the LAST tokens of the
+ *   slot: reserve them first.  Slots must differ.
+ *   k, v: bf16 [T, heads, d] with token and head strides, q [T,Hq,d] likewise
+ *   (Hq = 0: none), q_out contiguous.  rot, table, positions, interleaved as
+ *   in fa_rotary (rot = 0: nothing turns); without positions a token's position
+ *   is its place in the sequence.
+ *   A token whose place is not in the cache sets the status word and is not
+ *   written; one that no packed sequence owns has zeros in q_out.
+ */
+fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                          const int* cu_seqlens, int T, const void* q, void* q_out, int Hq,
+                          long long q_token_stride, long long q_head_stride, const void* k,
+                          long long k_token_stride, long long k_head_stride, const void* v,
+                          long long v_token_stride, long long v_head_stride, int rot,
+                          const float* table, int table_len, const void* positions, int pos_bytes,
+                          int interleaved, fa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Attention over the cache
+ * ------------------------------------------------------------------------
+ */
+
+/* Workspace of fa_tree_fwd in bytes (N: bound on a sequence's new tokens); 0 for invalid sizes. */
+size_t fa_tree_workspace_size(int Hq, int Hkv, int N, int d);
+
+/*
+ * Mask of drafted trees: bit j of mask[t] (int64 [T, words], 64 * words >= N)
+ * is set when token t of its sequence sees the sequence's token j of this call:
+ * itself and its ancestors.  parents[t]: index in the sequence of t's parent,
+ * -1 for none; parents come before their children, and an entry that does not
+ * ends the walk.  Tokens that no sequence owns get no bits.
+ */
+fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, int T, int words,
+                       void* mask, fa_stream_t stream);
+
+/*
+ * O = softmax(scale * Q K^T) V of new tokens over one layer of the cache.
+ *   The T tokens are the LAST tokens of slots[i], as in fa_cache_append, which
+ *   comes first.  Every row sees all earlier tokens of its sequence; of the
+ *   call's own tokens it sees those with set bits in its row of mask (int64
+ *   [T, mask_words], 64 * mask_words >= N), or with mask NULL itself and those
+ *   before it.  A row that sees nothing gets O = 0 and LSE = -inf.
+ *   q: bf16 [T,Hq,d], strides as in fa_rotary but positive multiples of 8
+ *   elements, 16-byte aligned; Hq / heads <= 128.  N bounds the new tokens of a
+ *   sequence.
+ *   o: bf16 [T,Hq,d] contiguous; lse: fp32 [Hq,T], natural log.
+ *   Rows of tokens that no packed sequence owns are left as they are, or with
+ *   zero_rest = 1 written as O = 0, LSE = -inf.  A sequence whose slot, length
+ *   or count does not fit sets the status word and its rows see nothing.
+ *   Results do not vary from run to run.  A slot may be read by several
+ *   sequences of a call.
+ *   Keys and values past a sequence's length never matter; those of drafted
+ *   tokens matter only to the rows that see them, whatever they hold.
+ */
+fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                      const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
+                      long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
+                      float scale, int zero_rest, void* workspace, size_t workspace_bytes,
+                      fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
