@@ -31,7 +31,7 @@
 namespace fa {
 namespace {
 
-constexpr int kRotThreads = 256;
+constexpr int kRotThreads = 64;
 constexpr int kHeadsPerThread = 4;
 
 struct RotParams {
@@ -42,7 +42,8 @@ struct RotParams {
     int heads[3], quads[3];      // quads: groups of kHeadsPerThread heads
     int T, d, rot, units;        // units per head
     int t_first;                 // first token of this launch
-    unsigned n_threads;
+    unsigned n_items;            // (token, quad) pairs, times units where lanes are not grouped
+    int lanes;                   // kShuffle: items of one warp
     const float2* table;         // [table_len, rot / 2]
     int table_len;
     const void* positions;       // int32 or int64 [T], or null
@@ -70,20 +71,39 @@ struct alignas(VW * sizeof(E)) Vec {
     E e[VW];
 };
 
-// E: element type; VW: elements of one access; INTER: pairs (2i, 2i + 1);
-// PAGED: k and v go to the cache's pages.
-template <typename E, int VW, bool INTER, bool PAGED>
+// Where the two halves of a pair are: in one access (kInter: pairs (2i, 2i + 1)),
+// in two accesses of the thread (kTwo), or in the accesses of two lanes of a
+// warp, which exchange them (kShuffle: half layout, a head's row in one warp).
+enum Layout { kInter, kTwo, kShuffle };
+
+// E: element type; VW: elements of one access; PAGED: k and v go to the
+// cache's pages.
+template <typename E, int VW, Layout L, bool PAGED>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_constant__ RotParams p) {
     pdl_begin();
-    const unsigned idx = blockIdx.x * kRotThreads + threadIdx.x;
-    if (idx >= p.n_threads) return;
+    constexpr bool INTER = L == kInter;
     using V = Vec<E, VW>;
     const unsigned U = p.units;
-    const unsigned per_token = (unsigned)(p.quads[0] + p.quads[1] + p.quads[2]) * U;
-    const unsigned tok_i = idx / per_token, rem = idx - tok_i * per_token;
+    const unsigned quads = p.quads[0] + p.quads[1] + p.quads[2];
+    unsigned item;  // token * quads + quad
+    int u;
+    bool idle = false;
+    if (L == kShuffle) {  // whole heads to a warp; the lanes left over follow item 0
+        const unsigned lane = threadIdx.x & 31, warp = (blockIdx.x * kRotThreads + threadIdx.x) >> 5;
+        const unsigned g = lane / U;
+        item = warp * p.lanes + g;
+        u = (int)(lane - g * U);
+        idle = g >= (unsigned)p.lanes || item >= p.n_items;
+        if (idle) item = 0;
+    } else {
+        const unsigned idx = blockIdx.x * kRotThreads + threadIdx.x;
+        if (idx >= p.n_items) return;
+        item = idx / U;
+        u = (int)(idx - item * U);
+    }
+    const unsigned tok_i = item / quads;
     const int tok = p.t_first + (int)tok_i;
-    int quad = (int)(rem / U);
-    const int u = (int)(rem - (unsigned)quad * U);
+    int quad = (int)(item - tok_i * quads);
     int seg = 0;
     if (quad >= p.quads[0]) {
         quad -= p.quads[0];
@@ -94,7 +114,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         }
     }
     const int h0 = quad * kHeadsPerThread;
-    const int nh = min(kHeadsPerThread, p.heads[seg] - h0);
+    const int nh = idle ? 0 : min(kHeadsPerThread, p.heads[seg] - h0);
 
     // Columns of this unit: one access (c0) or, for the pairs of the half
     // layout, two (c0 and c1).  first_pair < 0: nothing turns here.
@@ -109,6 +129,9 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             c0 = u * VW;
             if (c0 < p.rot) first_pair = c0 >> 1;
         }
+    } else if (L == kShuffle) {
+        c0 = u * VW;
+        if (c0 < p.rot) first_pair = c0 < half ? c0 : c0 - half;
     } else {
         const int pair_units = half / VW;
         if (u < pair_units) { c0 = u * VW; c1 = c0 + half; first_pair = c0; }
@@ -141,23 +164,24 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             if (r.n < 0) bad = kCacheBadLength;
             else if (slot < 0 || slot >= p.cache.slots) bad = kCacheBadSlot;
             else {
-                const long long at = (long long)p.cache.lengths[slot] - r.n + (tok - r.t0);
-                const long long col = at >= 0 ? at / p.cache.page_size : -1;
-                if (col < 0 || col >= p.cache.max_pages) bad = kCacheBadLength;
+                // (a length is at most 2^30, and out-of-range ones wrap to no column)
+                const int at = p.cache.lengths[slot] - r.n + (tok - r.t0);
+                const unsigned col = (unsigned)at / (unsigned)p.cache.page_size;
+                if (at < 0 || col >= (unsigned)p.cache.max_pages) bad = kCacheBadLength;
                 else {
-                    place = (int)at;
+                    place = at;
                     if (seg != 0) {  // (q stays out of the cache)
                         const int page = p.cache.table[(long long)slot * p.cache.max_pages + col];
                         if (page < 0 || page >= p.cache.pages) bad = kCacheBadSlot;
                         else
                             place_off = ((((long long)p.layer * p.cache.pages + page) *
                                               p.cache.heads + h0) * p.cache.page_size +
-                                         place % p.cache.page_size) * p.d;
+                                         (place & (p.cache.page_size - 1))) * p.d;
                     }
                 }
             }
             if (bad) {
-                atomicOr(p.cache.scratch, bad);
+                if (!idle) atomicOr(p.cache.scratch, bad);
                 writable = false;
             }
         }
@@ -171,13 +195,17 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         pos = p.pos64 ? static_cast<const long long*>(p.positions)[tok]
                       : (long long)static_cast<const int*>(p.positions)[tok];
 
-    if (seg != 2 && first_pair >= 0) {
+    const bool turns = seg != 2 && first_pair >= 0;
+    if (turns || L == kShuffle) {
         // A position outside the table reads nothing and makes the columns NaN.
         const bool known = pos >= 0 && pos < p.table_len;
         constexpr int NP = INTER && VW > 1 ? VW / 2 : VW;  // pairs of this unit
         float cs[NP], sn[NP];
         const float2* row = p.table + (known ? pos : 0) * half + first_pair;
-        if (NP == 1) {
+        if (!turns) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) { cs[i] = 1.f; sn[i] = 0.f; }
+        } else if (NP == 1) {
             const float2 t = *row;
             cs[0] = t.x;
             sn[0] = t.y;
@@ -194,11 +222,28 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
         }
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
-            if (!known) cs[i] = sn[i] = NAN;
+            if (!known && turns) cs[i] = sn[i] = NAN;
             if (p.backward) sn[i] = -sn[i];
+            if (L == kShuffle && c0 < half) sn[i] = -sn[i];
         }
 #pragma unroll
         for (int h = 0; h < kHeadsPerThread; ++h) {
+            if (L == kShuffle) {
+                // own * cos -+ partner * sin, the partner's columns from its lane
+                const int step = turns ? (c0 < half ? half : -half) / VW : 0;
+                V other;
+                const unsigned* mine = reinterpret_cast<const unsigned*>(&x0[h]);
+                unsigned* theirs = reinterpret_cast<unsigned*>(&other);
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(V) / 4; ++i)
+                    theirs[i] = __shfl_sync(0xffffffffu, mine[i], (int)(threadIdx.x & 31) + step);
+                if (turns) {
+#pragma unroll
+                    for (int i = 0; i < VW; ++i)
+                        x0[h].e[i] = from_f<E>(to_f(x0[h].e[i]) * cs[i % NP] + to_f(other.e[i]) * sn[i % NP]);
+                }
+                continue;
+            }
             if (h >= nh) break;
             if (INTER && VW > 1) {
 #pragma unroll
@@ -244,24 +289,30 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     }
 }
 
-template <typename E, int VW, bool PAGED>
-cudaError_t launch_t(RotParams p, int interleaved, cudaStream_t stream) {
+template <typename E, int VW, Layout L, bool PAGED>
+cudaError_t launch_t(RotParams p, cudaStream_t stream) {
     const int half = p.rot / 2;
     p.units = VW == 1 ? half + (p.d - p.rot)
-                      : (interleaved ? p.d / VW : half / VW + (p.d - p.rot) / VW);
+                      : (L != kTwo ? p.d / VW : half / VW + (p.d - p.rot) / VW);
     for (int s = 0; s < 3; ++s) p.quads[s] = cdiv(p.heads[s], kHeadsPerThread);
     const long long per_token = (long long)(p.quads[0] + p.quads[1] + p.quads[2]) * p.units;
     if (per_token == 0) return cudaSuccess;
-    // thread indexes are 32 bits: more tokens than that go in several launches
-    const long long most = 0x7FFFFF00LL / per_token;
+    p.lanes = 32 / p.units;
+    // item and thread indexes are 32 bits: more tokens than that go in several launches
+    const long long most = 0x3FFFFF00LL / per_token;
     for (long long t = 0; t < p.T; t += most) {
         const long long n = p.T - t < most ? p.T - t : most;
         p.t_first = (int)t;
-        p.n_threads = (unsigned)(n * per_token);
-        const dim3 grid((p.n_threads + kRotThreads - 1) / kRotThreads);
-        cudaError_t e = interleaved
-            ? launch_pdl(rotary_kernel<E, VW, true, PAGED>, grid, dim3(kRotThreads), 0, stream, p)
-            : launch_pdl(rotary_kernel<E, VW, false, PAGED>, grid, dim3(kRotThreads), 0, stream, p);
+        long long threads = n * per_token;
+        if (L == kShuffle) {
+            p.n_items = (unsigned)(threads / p.units);
+            threads = ((long long)p.n_items + p.lanes - 1) / p.lanes * 32;
+        } else {
+            p.n_items = (unsigned)threads;
+        }
+        const dim3 grid((unsigned)((threads + kRotThreads - 1) / kRotThreads));
+        const cudaError_t e = launch_pdl(rotary_kernel<E, VW, L, PAGED>, grid, dim3(kRotThreads), 0,
+                                         stream, p);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -287,9 +338,13 @@ bool vector_ok(const RotParams& p, int interleaved, bool paged) {
 
 template <typename E, bool PAGED>
 cudaError_t launch_any(const RotParams& p, int interleaved, cudaStream_t stream) {
-    return vector_ok<E>(p, interleaved, PAGED)
-               ? launch_t<E, 16 / (int)sizeof(E), PAGED>(p, interleaved, stream)
-               : launch_t<E, 1, PAGED>(p, interleaved, stream);
+    constexpr int VW = 16 / (int)sizeof(E);
+    if (!vector_ok<E>(p, interleaved, PAGED))
+        return interleaved ? launch_t<E, 1, kInter, PAGED>(p, stream)
+                           : launch_t<E, 1, kTwo, PAGED>(p, stream);
+    if (interleaved) return launch_t<E, VW, kInter, PAGED>(p, stream);
+    return p.d <= 32 * VW ? launch_t<E, VW, kShuffle, PAGED>(p, stream)
+                          : launch_t<E, VW, kTwo, PAGED>(p, stream);
 }
 
 // Table row of one position: angle p * freq in 64 bits, so that far positions

@@ -94,7 +94,7 @@ def _here(device, stream):
 
 
 def _raw_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _ptr(t):
@@ -220,26 +220,32 @@ def _last_contiguous(g):
 
 
 class _Rotary(torch.autograd.Function):
+    """how: (pos_bytes, B, N, interleaved, backward); positions and cu_seqlens travel in `where`."""
+
     @staticmethod
-    def forward(ctx, q, k, table, positions, pos_bytes, B, N, cu_seqlens, interleaved, backward):
+    def forward(ctx, q, k, table, where, how):
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(table, positions, cu_seqlens)
-        ctx.args = (pos_bytes, B, N, interleaved, backward)
-        return tuple(_rotate(q, k, table, positions, pos_bytes, B, N, cu_seqlens, interleaved,
-                             backward))
+        ctx.save_for_backward(table, *where)
+        ctx.how = how
+        pos_bytes, B, N, interleaved, backward = how
+        return tuple(_rotate(q, k, table, where[0], pos_bytes, B, N, where[1], interleaved, backward))
 
     @staticmethod
     def backward(ctx, gq, gk):
-        table, positions, cu_seqlens = ctx.saved_tensors
-        pos_bytes, B, N, interleaved, back = ctx.args
         if gq is None and gk is None:
-            return (None,) * 10
+            return None, None, None, None, None
+        table, positions, cu_seqlens = ctx.saved_tensors
+        pos_bytes, B, N, interleaved, back = ctx.how
         gq, gk = _last_contiguous(gq), _last_contiguous(gk)
-        # the transposed rotation, itself differentiable
-        with torch.cuda.device((gq if gq is not None else gk).device):
-            dq, dk = _Rotary.apply(gq, gk, table, positions, pos_bytes, B, N, cu_seqlens,
-                                   interleaved, 1 - back)
-        return (dq, dk) + (None,) * 8
+        dev = (gq if gq is not None else gk).device
+        with contextlib.nullcontext() if _here(dev, None) else torch.cuda.device(dev):
+            if torch.is_grad_enabled():  # the transposed rotation, itself differentiable
+                dq, dk = _Rotary.apply(gq, gk, table, (positions, cu_seqlens),
+                                       (pos_bytes, B, N, interleaved, 1 - back))
+            else:
+                dq, dk = _rotate(gq, gk, table, positions, pos_bytes, B, N, cu_seqlens, interleaved,
+                                 1 - back)
+        return dq, dk, None, None, None
 
 
 def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved=False,
@@ -274,10 +280,17 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
     _cuda("q" if q is not None else "k", first)
     grad = torch.is_grad_enabled() and ((q is not None and q.requires_grad) or
                                         (k is not None and k.requires_grad))
-    fn = _Rotary.apply if grad else _rotate
-    with contextlib.nullcontext() if _here(dev, stream) else _on(dev, stream, (q, k, table, positions)):
-        out = fn(q, k, table, positions, pos_bytes, B, N, cu_seqlens, bool(interleaved), 0)
-    return out[0], out[1]
+
+    def call():
+        if grad:
+            return _Rotary.apply(q, k, table, (positions, cu_seqlens),
+                                 (pos_bytes, B, N, interleaved, 0))
+        return tuple(_rotate(q, k, table, positions, pos_bytes, B, N, cu_seqlens, interleaved, 0))
+
+    if _here(dev, stream):
+        return call()
+    with _on(dev, stream, (q, k, table, positions, cu_seqlens)):
+        return call()
 
 
 # -------------------------------------------------------------------------------- cache
