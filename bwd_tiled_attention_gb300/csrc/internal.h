@@ -99,12 +99,15 @@ struct TreeParams {
     const void* mask;              // int64 [T, words], or null: causal
     void* o;                       // bf16 [T, Hq, d]
     float* lse;                    // [Hq, T]
-    int4* meta;                    // per CTA: the item that its first piece ends
+    int4* meta;                    // per CTA: the item that its first piece ends (not fused)
+    unsigned long long* arrived;   // fused: per CTA, partials of the item that ends there
+    unsigned long long call;       // fused: this call's number (56 bits)
+    int fused;                     // the last CTA of an item joins its partials
     float* part_stats;             // [2 * CTAs, part_rows, 2]: m and l
     float* part_o;                 // [2 * CTAs, part_rows, d], not normalised
     int part_rows;
     int layer, B, N, T, Hq, group;
-    int words;
+    int words, page_shift;         // page_size = 1 << page_shift
     int tile_tokens;               // tokens of one 128-row tile
     int min_tiles;                 // least key tiles of a CTA
     int zero_rest;                 // write zeros for tokens that no sequence owns

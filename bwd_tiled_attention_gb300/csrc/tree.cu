@@ -20,7 +20,8 @@
 //   - linear split: all (sequence, kv head, row tile) items' key tiles stand in
 //     one line and CTA c takes [c * per, (c + 1) * per).  Every SM streams the
 //     same number of tiles for any mix of lengths; an item that spans CTAs
-//     leaves partials, joined by a second small kernel in a fixed order.
+//     leaves partials, joined in a fixed order: with few rows by the CTA that
+//     finishes last, otherwise by a second kernel.
 //   - the K and V tiles of a CTA run through one ring of stages in the order
 //     the tensor core consumes them, filled by TMA boxes of one page each.
 //   - up to d = 128 two streams (softmax warpgroups, S/P and O in TMEM) work on
@@ -38,6 +39,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 
@@ -77,6 +79,7 @@ struct Piece {
     int slot, ctx, len;
     int k0, n;           // key tiles [k0, k0 + n)
     int part;            // partial slot, or -1: the whole item
+    int first_cta, last_cta;  // the CTAs that share the item
 };
 
 template <int D, bool PAIR>
@@ -87,9 +90,12 @@ struct Smem {
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
     uint64_t q_full, q_empty, piece_full[2], piece_empty[2];
     uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain;
+    uint64_t join_full, join_go;
     Piece piece[2];
     int start[4];        // this CTA's first item: sequence, kv head, row tile, key tile
+    long long line[3];   // tiles of a CTA, and this CTA's stretch
     long long sums[kThreads / 32];
+    int join_last;
     uint32_t tmem_base;
     int abort_flag, zero;
     int poison;          // a drafted V that is not finite has been met (never cleared)
@@ -153,6 +159,30 @@ __device__ __forceinline__ long long head_tiles(const TreeParams& p, const SeqIn
     return sum;
 }
 
+// a / b without a 64-bit division where both fit 32 bits (nearly always).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+    if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
+// Finds tile `at` (counted from the sequence's first) of sequence s.
+__device__ __forceinline__ void locate(const TreeParams& p, const SeqInfo& s, long long at,
+                                       long long head, int tokens, int bn, int& h, int& q, int& k) {
+    h = (int)divide(at, head);
+    k = (int)(at - h * head);
+    if (p.mask || s.len == 0) {
+        const int t = item_tiles(p, s, 0, tokens, bn);
+        q = k / t;
+        k -= q * t;
+        return;
+    }
+    for (q = 0;; ++q) {
+        const int t = item_tiles(p, s, q, tokens, bn);
+        if (k < t) return;
+        k -= t;
+    }
+}
+
 __device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* flag,
                                              int* status) {
     if (mbar_wait(bar, parity, flag)) return true;
@@ -212,6 +242,67 @@ __device__ __forceinline__ int fifo_v(int j, int n) {
     return PAIR ? 2 * j + 1 : (j < n - 1 ? 2 * j + 2 : 2 * n - 1);
 }
 
+// One row of an item that CTAs c0 .. c0 + n - 1 shared, by one warp: partials
+// stand in slot 2c + 1 of the first CTA and slot 2c of the others, and are
+// added in that order.
+template <int DR>
+__device__ __forceinline__ void join_row(const TreeParams& p, int slot_row, int c0, int n, size_t tok,
+                                         int head) {
+    const int lane = lane_id();
+    constexpr int V = DR / 32;                       // columns of a lane, contiguous
+    constexpr int W = V % 4 == 0 ? 4 : (V % 2 == 0 ? 2 : 1);
+    struct alignas(4 * W) Wide { float x[W]; };
+    auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + slot_row; };
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(p.part_stats + slot(i) * 2));
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    float acc[V], l = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        float w = 0.f, lw = 0.f;                     // of this lane's partial
+        if (i0 + lane < n) {
+            const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + slot(i0 + lane));
+            w = ex2_approx(st.x - base);
+            lw = st.y * w;
+        }
+        const int here = min(32, n - i0);
+#pragma unroll 4
+        for (int i = 0; i < here; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            l += __shfl_sync(0xffffffffu, lw, i);
+            const float* at = p.part_o + slot(i0 + i) * DR + lane * V;
+#pragma unroll
+            for (int v = 0; v < V; v += W) {
+                Wide x;
+                if (W == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(at + v));
+                    x.x[0] = y.x; x.x[1 % W] = y.y; x.x[2 % W] = y.z; x.x[3 % W] = y.w;
+                } else if (W == 2) {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(at + v));
+                    x.x[0] = y.x; x.x[1 % W] = y.y;
+                } else {
+                    x.x[0] = __ldcg(at + v);
+                }
+#pragma unroll
+                for (int e = 0; e < W; ++e) acc[v + e] = fmaf(x.x[e], wi, acc[v + e]);
+            }
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    struct alignas(2 * W) Half { __nv_bfloat16 x[W]; };
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR + lane * V;
+#pragma unroll
+    for (int v = 0; v < V; v += W) {
+        Half y;
+#pragma unroll
+        for (int e = 0; e < W; ++e) y.x[e] = __float2bfloat16_rn(acc[v + e] * inv);
+        *reinterpret_cast<Half*>(o + v) = y;
+    }
+    if (lane == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
+}
+
 // D: tile columns; DR: head dimension in memory (96 runs on 128 columns whose
 // last 32 the TMA fills with zeros).
 template <int D, int DR, bool PAIR>
@@ -245,6 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         mbar_init(smem_u32(&sm.stat_full), 8);
         mbar_init(smem_u32(&sm.drain), 1);
+        mbar_init(smem_u32(&sm.join_full), 8);
+        mbar_init(smem_u32(&sm.join_go), 1);
         sm.abort_flag = sm.zero = sm.poison = 0;
         sm.start[0] = -1;
         fence_barrier_init();
@@ -260,11 +353,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int tokens = p.tile_tokens * C::kQTiles;  // tokens of an item
     pdl_wait();
 
-    // ---- the line of all key tiles, and where this CTA's stretch begins
-    long long per, begin, end;
-    {
-        const int chunk = (p.B + kThreads - 1) / kThreads;
-        const int i0 = threadIdx.x * chunk, i1 = min(p.B, i0 + chunk);
+    // ---- the line of all key tiles, and where this CTA's stretch begins: the
+    // producer warp's own business for small batches, all threads' for large ones
+    if (p.B <= 128 ? warp == 0 : true) {
+        const bool all_threads = p.B > 128;
+        const int chunk = all_threads ? (p.B + kThreads - 1) / kThreads : (p.B + 31) / 32;
+        const int i0 = (all_threads ? (int)threadIdx.x : lane) * chunk, i1 = min(p.B, i0 + chunk);
         long long mine = 0;
         int bad = 0;
         for (int i = i0; i < i1; ++i) {
@@ -278,16 +372,23 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const long long x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
         }
-        if (lane == 31) sm.sums[warp] = incl;
-        __syncthreads();
-        long long before = 0, total = 0;
-        for (int w = 0; w < kThreads / 32; ++w) {
-            if (w < warp) before += sm.sums[w];
-            total += sm.sums[w];
+        long long before = 0, total = __shfl_sync(0xffffffffu, incl, 31);
+        if (all_threads) {
+            if (lane == 31) sm.sums[warp] = incl;
+            __syncthreads();
+            total = 0;
+            for (int w = 0; w < kThreads / 32; ++w) {
+                if (w < warp) before += sm.sums[w];
+                total += sm.sums[w];
+            }
         }
-        per = max((total + gridDim.x - 1) / gridDim.x, (long long)p.min_tiles);
-        begin = min(total, per * blockIdx.x);
-        end = min(total, begin + per);
+        const long long per = max(divide(total + gridDim.x - 1, gridDim.x), (long long)p.min_tiles);
+        const long long begin = min(total, per * blockIdx.x), end = min(total, begin + per);
+        if (threadIdx.x == 0) {
+            sm.line[0] = per;
+            sm.line[1] = begin;
+            sm.line[2] = end;
+        }
         long long at = before + incl - mine;  // first tile of this thread's sequences
         if (begin < end && begin >= at && begin < at + mine) {
             for (int i = i0; i < i1; ++i) {
@@ -297,46 +398,43 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     at += all;
                     continue;
                 }
-                const int h = (int)((begin - at) / ht);
-                int k = (int)((begin - at) - h * ht), q = 0;
-                for (;; ++q) {
-                    const int t = item_tiles(p, s, q, tokens, BN);
-                    if (k < t) break;
-                    k -= t;
-                }
                 sm.start[0] = i;
-                sm.start[1] = h;
-                sm.start[2] = q;
-                sm.start[3] = k;
+                locate(p, s, begin - at, ht, tokens, BN, sm.start[1], sm.start[2], sm.start[3]);
                 break;
             }
         }
-        __syncthreads();
+        if (all_threads) __syncthreads(); else __syncwarp();
     }
     static_assert(128 * 72 + 256 * 216 == 384 * 168, "register split must match the launch");
 
     if (warp == 0) {
         // ------------------------------------------------------------ producer
         setmaxnreg_dec<72>();
-        int it = 0, f = 0, nq = 0;  // pieces, stages and query loads so far
+        int it = 0, f = 0, nq = 0;  // pieces, tile loads and query loads so far
+        int st = 0, phase = 0;      // the next load's stage, and the ring's turn
         bool ok = true;
         int own_first = -1, own_tok0 = 0, own_ntok = 0, own_h = 0;  // an item that ends here
         int b = sm.start[0], h = sm.start[1], q = sm.start[2], k0 = sm.start[3];
-        long long left = end - begin;
+        const long long per = sm.line[0], end = sm.line[2];
+        long long at = sm.line[1];             // place in the line
         SeqInfo s;
         s.n = 0;
-        if (left > 0) s = seq_info(p, b);
-        const int ps = p.cache.page_size;
+        if (at < end) s = seq_info(p, b);
+        const int ps = p.cache.page_size, ps_shift = p.page_shift;
         const int rows = min(ps, BN);          // keys of one box
-        const int boxes = BN / rows;
+        const int rows_shift = rows == ps ? ps_shift : 6;
+        const int boxes = BN >> rows_shift;
         const int my_box = lane / C::kCols, my_col = lane % C::kCols;
         const bool has_box = my_box < boxes;
+        const int my_key = my_box << rows_shift;
+        const uint32_t my_dst = my_col * (BN * 128) + my_key * 128;
+        const int box_bytes = rows * 128 * C::kCols;
         while (ok) {
             const int slot = it & 1;
             if (!(ok = warp_wait(smem_u32(&sm.piece_empty[slot]), ((it >> 1) & 1) ^ 1, stop, status)))
                 break;
             Piece x;
-            if (left <= 0) {
+            if (at >= end) {
                 if (lane == 0) {
                     sm.piece[slot].b = -1;
                     mbar_arrive(smem_u32(&sm.piece_full[slot]));
@@ -353,11 +451,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             x.ctx = s.ctx;
             x.len = s.len;
             x.k0 = k0;
-            x.n = (int)min((long long)(tiles - k0), left);
+            x.n = (int)min((long long)(tiles - k0), end - at);
             const bool whole_end = k0 + x.n == tiles;
             x.part = k0 == 0 ? (whole_end ? -1 : 2 * (int)blockIdx.x + 1) : 2 * (int)blockIdx.x;
+            x.first_cta = x.last_cta = blockIdx.x;
+            if (k0 > 0) x.first_cta = (int)divide(at - k0, per);
+            if (!whole_end) x.last_cta = (int)divide(at - k0 + tiles - 1, per);
             if (k0 > 0 && whole_end) {  // this CTA's first piece ends an item begun elsewhere
-                own_first = (int)((begin - k0) / per);
+                own_first = x.first_cta;
                 own_tok0 = x.tok0;
                 own_ntok = x.ntok;
                 own_h = h;
@@ -369,44 +470,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             __syncwarp();
 
             // -- loads of this piece
-            const int* table = p.cache.table + (long long)x.slot * p.cache.max_pages;
-            const int used = (x.len + ps - 1) / ps;
-            auto table_at = [&](int i) { return i < used ? table[i] : -1; };
-            // page ids of a window of 32 pages, and of the next one
-            int win = (int)((long long)x.k0 * BN / ps);
-            int ids = table_at(win + lane), nxt = table_at(win + 32 + lane);
-            int page_prev = -1;
-            // the page of this lane's box in tile j
-            auto page_of = [&](int j) {
-                const int first = (int)((long long)(x.k0 + j) * BN / ps);
-                if (first >= win + 32) {
-                    win += 32;
-                    ids = nxt;
-                    nxt = table_at(win + 32 + lane);
-                }
-                return __shfl_sync(0xffffffffu, ids, (first - win + my_box) & 31);
-            };
-            auto load_tile = [&](int j, int page, const CUtensorMap* map) {
-                const int st = f % S;
-                if (!(ok = warp_wait(smem_u32(&sm.empty[st]), ((f / S) & 1) ^ 1, stop, status)))
-                    return;
-                const int key0 = (x.k0 + j) * BN, key = key0 + my_box * rows;
-                const int have = max(0, min(boxes, (x.len - key0 + rows - 1) / rows));
-                const uint32_t bar = smem_u32(&sm.full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, have * rows * 128 * C::kCols);
-                __syncwarp();
-                if (has_box && my_box < have) {
-                    // a page id out of range reads the fill value (zeros) and is reported
-                    int plane = -1;
-                    if (page >= 0 && page < p.cache.pages)
-                        plane = (p.layer * p.cache.pages + page) * p.cache.heads + x.h;
-                    else
-                        atomicOr(status, kCacheBadSlot);
-                    tma_load_3d(smem_u32(sm.kv[st]) + my_col * (BN * 128) + my_box * rows * 128, map,
-                                bar, my_col * 64, key % ps, plane);
-                }
-                ++f;
-            };
             auto load_q = [&] {
                 if (!(ok = warp_wait(smem_u32(&sm.q_empty), (it & 1) ^ 1, stop, status))) return;
                 if (lane == 0) {
@@ -421,30 +484,71 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 __syncwarp();
                 ++nq;
             };
+            if (it == 0) load_q();  // (later pieces: behind the first key tile)
+            const int* table = p.cache.table + (long long)x.slot * p.cache.max_pages;
+            const int used = (x.len + ps - 1) >> ps_shift;
+            auto table_at = [&](int i) { return i < used ? table[i] : -1; };
+            // page ids of a window of 32 pages, and of the next one
+            int win = (x.k0 * BN) >> ps_shift;
+            int ids = table_at(win + lane), nxt = table_at(win + 32 + lane);
+            int page_prev = -1;
+            // the page of this lane's box in the tile at key0
+            auto page_of = [&](int key0) {
+                const int first = key0 >> ps_shift;
+                if (first >= win + 32) {
+                    win += 32;
+                    ids = nxt;
+                    nxt = table_at(win + 32 + lane);
+                }
+                return __shfl_sync(0xffffffffu, ids, (first - win + my_box) & 31);
+            };
+            auto load_tile = [&](int key0, int page, const CUtensorMap* map) {
+                if (!(ok = warp_wait(smem_u32(&sm.empty[st]), phase ^ 1, stop, status))) return;
+                const int have = max(0, min(boxes, (x.len - key0 + rows - 1) >> rows_shift));
+                const uint32_t bar = smem_u32(&sm.full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, have * box_bytes);
+                __syncwarp();
+                if (has_box && my_box < have) {
+                    // a page id out of range reads the fill value (zeros) and is reported
+                    int plane = -1;
+                    if (page >= 0 && page < p.cache.pages)
+                        plane = (p.layer * p.cache.pages + page) * p.cache.heads + x.h;
+                    else
+                        atomicOr(status, kCacheBadSlot);
+                    tma_load_3d(smem_u32(sm.kv[st]) + my_dst, map, bar, my_col * 64,
+                                (key0 + my_key) & (ps - 1), plane);
+                }
+                ++f;
+                if (++st == S) {
+                    st = 0;
+                    phase ^= 1;
+                }
+            };
+            int key0 = x.k0 * BN;
             if constexpr (PAIR) {
-                for (int j = 0; j < x.n && ok; ++j) {
-                    const int pg = page_of(j);
-                    load_tile(j, pg, &p.tm_k);
-                    if (ok && j == 0) load_q();
-                    if (ok) load_tile(j, pg, &p.tm_v);
+                for (int j = 0; j < x.n && ok; ++j, key0 += BN) {
+                    const int pg = page_of(key0);
+                    load_tile(key0, pg, &p.tm_k);
+                    if (ok && j == 0 && it > 0) load_q();
+                    if (ok) load_tile(key0, pg, &p.tm_v);
                 }
             } else {
-                for (int j = 0; j <= x.n && ok; ++j) {
+                for (int j = 0; j <= x.n && ok; ++j, key0 += BN) {
                     int pg = -1;
                     if (j < x.n) {
-                        pg = page_of(j);
-                        load_tile(j, pg, &p.tm_k);
-                        if (ok && j == 0) load_q();
+                        pg = page_of(key0);
+                        load_tile(key0, pg, &p.tm_k);
+                        if (ok && j == 0 && it > 0) load_q();
                     }
-                    if (ok && j >= 1) load_tile(j - 1, page_prev, &p.tm_v);
+                    if (ok && j >= 1) load_tile(key0 - BN, page_prev, &p.tm_v);
                     page_prev = pg;
                 }
             }
             ++it;
             // -- the next item
-            left -= x.n;
+            at += x.n;
             k0 = 0;
-            if (left > 0) {
+            if (at < end) {
                 ++q;
                 if (q * tokens >= s.n) {
                     q = 0;
@@ -452,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         h = 0;
                         do {
                             ++b;
-                            if (b >= p.B) {  // (cannot be: left counts real tiles)
-                                left = 0;
+                            if (b >= p.B) {  // (cannot be: the line counts real tiles)
+                                at = end;
                                 break;
                             }
                             s = seq_info(p, b);
@@ -463,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
         }
         if (lane == 0) {
-            p.meta[blockIdx.x] = make_int4(own_first, own_tok0, own_ntok, own_h);
+            if (!p.fused) p.meta[blockIdx.x] = make_int4(own_first, own_tok0, own_ntok, own_h);
             // Never leave a TMA write in flight.
             const volatile int* z = &sm.zero;
             for (int i = 0; i < S && i < f; ++i) {
@@ -590,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const bool row_used = row_tok < p.tile_tokens;
-        int it = 0, f = 0, cnt[2] = {0, 0};
+        int it = 0, f = 0, cnt[2] = {0, 0}, joins = 0;
         bool ok = true;
         while (ok) {
             const int slot = it & 1;
@@ -881,11 +985,65 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[PAIR ? w : 0]));
             }
+            if constexpr (!PAIR) {
+                if (p.fused && x.part >= 0) {
+                    // Whoever brings the item's last partial joins them.  The item's word
+                    // counts those brought under this call's number; anything else that it
+                    // holds counts as none, and the last one clears it.
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.join_full));
+                    if (warp == 4) {
+                        if (!(ok = warp_wait(smem_u32(&sm.join_full), joins & 1, stop, status))) break;
+                        if (lane == 0) {
+                            __threadfence();
+                            unsigned long long* word = p.arrived + x.last_cta;
+                            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
+                            unsigned long long now;
+                            for (;;) {
+                                now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
+                                const unsigned long long seen = atomicCAS(word, old, now);
+                                if (seen == old) break;
+                                old = seen;
+                            }
+                            const int parts = x.last_cta - x.first_cta + 1;
+                            sm.join_last = (int)(now & 255) == parts;
+                            if (sm.join_last) *word = 0;
+                            __threadfence();
+                            mbar_arrive(smem_u32(&sm.join_go));
+                        }
+                        __syncwarp();
+                    }
+                    if (!(ok = warp_wait(smem_u32(&sm.join_go), joins & 1, stop, status))) break;
+                    ++joins;
+                    if (sm.join_last) {
+                        __threadfence();
+                        for (int r = warp - 4; r < p.part_rows; r += 8) {
+                            const int rt = r / p.group;
+                            if (rt >= x.ntok) break;
+                            join_row<DR>(p, r, x.first_cta, x.last_cta - x.first_cta + 1,
+                                         (size_t)x.tok0 + rt, x.h * p.group + r - rt * p.group);
+                        }
+                    }
+                }
+            }
             f += 2 * x.n;
             ++it;
         }
     } else {
-        setmaxnreg_dec<72>();  // warps 2 and 3: TMEM allocation only
+        // ------------------------------------------------------------ warps 2, 3
+        setmaxnreg_dec<72>();
+        if (p.zero_rest && p.cu) {  // tokens that no sequence owns
+            const int used = min(max(p.cu[p.B], 0), p.T);
+            const long long step = (long long)gridDim.x * 64;
+            const long long at = (long long)blockIdx.x * 64 + threadIdx.x - 64;
+            const long long rows = (long long)(p.T - used) * p.Hq;
+            uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
+                                                (long long)used * p.Hq * DR);
+            for (long long i = at; i < rows * (DR / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (long long i = at; i < rows; i += step)
+                p.lse[(i / (p.T - used)) * p.T + used + i % (p.T - used)] = -INFINITY;
+        }
     }
 
     tc_fence_before();
@@ -898,56 +1056,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
 // Joins the partials of every item that more than one CTA worked on: the CTA
 // whose first piece ends the item left (first CTA, token, tokens, head) in
-// meta; its partials stand in slot 2c + 1 of that first CTA and slot 2c of
-// the others, and are added in that order.  One warp a row.  Tokens that no
-// sequence owns are zeroed when asked to.
+// meta.  One warp a row.
 template <int DR>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
     pdl_begin();
     const int4 own = p.meta[blockIdx.x];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slot_row = blockIdx.y * 8 + warp;
+    const int slot_row = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int stream = slot_row >> 7, row = slot_row & 127;
     const int row_tok = row / p.group;
     const int t = stream * p.tile_tokens + row_tok;
-    if (own.x >= 0 && slot_row < p.part_rows && row_tok < p.tile_tokens && t < own.z) {
-        const int c0 = own.x, n = (int)blockIdx.x - c0 + 1;
-        auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + slot_row; };
-        float m = -INFINITY;
-        for (int i = lane; i < n; i += 32) m = fmaxf(m, p.part_stats[slot(i) * 2]);
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float base = m == -INFINITY ? 0.f : m;
-        constexpr int V = DR / 32;  // columns of a lane: lane, lane + 32, ...
-        float acc[V], l = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = 0.f;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const size_t s = slot(i);
-            const float w = ex2_approx(p.part_stats[s * 2] - base);
-            l += p.part_stats[s * 2 + 1] * w;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(p.part_o[s * DR + v * 32 + lane], w, acc[v]);
-        }
-        const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
-        const size_t tok = (size_t)own.y + t;
-        const int head = own.w * p.group + row - row_tok * p.group;
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v * 32 + lane] = __float2bfloat16_rn(acc[v] * inv);
-        if (lane == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
-    }
-    if (p.zero_rest && p.cu) {
-        const int used = min(max(p.cu[p.B], 0), p.T);
-        const long long step = (long long)gridDim.x * gridDim.y * 256;
-        const long long at = ((long long)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
-        const long long rows = (long long)(p.T - used) * p.Hq;
-        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
-                                            (long long)used * p.Hq * DR);
-        for (long long i = at; i < rows * (DR / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
-        for (long long i = at; i < rows; i += step)
-            p.lse[(i / (p.T - used)) * p.T + used + i % (p.T - used)] = -INFINITY;
-    }
+    if (own.x >= 0 && slot_row < p.part_rows && row_tok < p.tile_tokens && t < own.z)
+        join_row<DR>(p, slot_row, own.x, (int)blockIdx.x - own.x + 1, (size_t)own.y + t,
+                     own.w * p.group + row - row_tok * p.group);
 }
 
 // Ancestor bits of drafted trees: token t of a sequence sees itself, its
@@ -979,7 +1099,7 @@ cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.fused) return e;
     return launch_pdl(tree_join_kernel<DR>, dim3(ctas, cdiv(p.part_rows, 8)), dim3(256), 0, stream, p);
 }
 
@@ -997,15 +1117,30 @@ Tiles row_tiles(int group, int N, int d) {
     return t;
 }
 
+// Items of up to this many rows are joined by the CTA that finishes last:
+// one launch less (attention of one token over 501 keys, 16 heads: 18.6 -> XX us),
+// while more rows would leave one CTA too much to read.
+constexpr int kFusedRows = 32;
+
 struct TreeWs {
-    size_t stats, o, bytes;
+    size_t arrived, stats, o, bytes;
 };
 TreeWs tree_ws(int rows, int d) {
     TreeWs w;
-    w.stats = align_up(kTreeMaxCtas * sizeof(int4), kAlign);
+    w.arrived = align_up(kTreeMaxCtas * sizeof(int4), kAlign);
+    w.stats = align_up(w.arrived + kTreeMaxCtas * sizeof(long long), kAlign);
     w.o = align_up(w.stats + (size_t)kTreeMaxCtas * 2 * rows * 2 * sizeof(float), kAlign);
     w.bytes = align_up(w.o + (size_t)kTreeMaxCtas * 2 * rows * d * sizeof(float), kAlign);
     return w;
+}
+
+// A number that no other call of this process has, and whose 56 bits what a
+// workspace happens to hold does not repeat.
+unsigned long long next_call() {
+    static std::atomic<unsigned long long> last{0};
+    unsigned long long x = last.fetch_add(1, std::memory_order_relaxed) + 1;
+    x *= 0x9E3779B97F4A7C15ull;  // (odd: different calls stay different)
+    return x & 0x00FFFFFFFFFFFFFFull;
 }
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -1078,6 +1213,7 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     p.lse = lse;
     char* base = static_cast<char*>(workspace);
     p.meta = reinterpret_cast<int4*>(base);
+    p.arrived = reinterpret_cast<unsigned long long*>(base + ws.arrived);
     p.part_stats = reinterpret_cast<float*>(base + ws.stats);
     p.part_o = reinterpret_cast<float*>(base + ws.o);
     p.part_rows = tiles.rows;
@@ -1085,6 +1221,9 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     p.B = B; p.N = N; p.T = T; p.Hq = Hq;
     p.tile_tokens = tiles.tokens;
     p.min_tiles = 1;
+    p.page_shift = __builtin_ctz(cache->page_size);
+    p.fused = !tiles.pair && tiles.rows <= kFusedRows;
+    p.call = next_call();
     p.zero_rest = zero_rest ? 1 : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     const int nsm = device_sms();
