@@ -90,12 +90,12 @@ struct Smem {
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
     uint64_t q_full, q_empty, piece_full[2], piece_empty[2];
     uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain;
-    uint64_t join_full, join_go;
     Piece piece[2];
     int start[4];        // this CTA's first item: sequence, kv head, row tile, key tile
     long long line[3];   // tiles of a CTA, and this CTA's stretch
     long long sums[kThreads / 32];
-    int join_last;
+    Piece shared[2];     // fused: this CTA's pieces of items that it shares
+    int n_shared, join_last[2];
     uint32_t tmem_base;
     int abort_flag, zero;
     int poison;          // a drafted V that is not finite has been met (never cleared)
@@ -336,10 +336,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         mbar_init(smem_u32(&sm.stat_full), 8);
         mbar_init(smem_u32(&sm.drain), 1);
-        mbar_init(smem_u32(&sm.join_full), 8);
-        mbar_init(smem_u32(&sm.join_go), 1);
         sm.abort_flag = sm.zero = sm.poison = 0;
         sm.start[0] = -1;
+        sm.n_shared = 0;
         fence_barrier_init();
     }
     if (warp == 2) {
@@ -465,6 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             if (lane == 0) {
                 sm.piece[slot] = x;
+                if (x.part >= 0) sm.shared[sm.n_shared++] = x;  // the first and the last at most
                 mbar_arrive(smem_u32(&sm.piece_full[slot]));
             }
             __syncwarp();
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         setmaxnreg_dec<72>();
-        if (lane == 0) {
+        {
             constexpr uint32_t idS = make_idesc_bf16(128, BN, false, false);
             constexpr uint32_t idPV = make_idesc_bf16(128, D, false, true);
             int it = 0, f = 0;
@@ -587,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             int done[2] = {0, 0}; // PAIR: pieces of each stream
             bool ok = true;
             auto wait = [&](uint64_t& bar, int n) {
-                return ok = ok && wait_or_stop(smem_u32(&bar), n & 1, stop, status);
+                return ok = ok && warp_wait(smem_u32(&bar), n & 1, stop, status);
             };
             auto issue_s = [&](int stage_no, int buf, int qt) {
                 const uint64_t da = make_sdesc_here(smem_u32(sm.q[qt]), 16, 1024);
@@ -595,7 +595,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    mma_ss(tmem + buf * 128, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
+                    warp_mma_ss(tmem + buf * 128, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
                            sdesc_add(db, (kk >> 2) * (BN * 128) + (kk & 3) * 32), idS, kk > 0);
             };
             auto issue_pv = [&](int stage_no, int buf, int o, int c, bool first) {
@@ -608,15 +608,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         if (!wait(sm.p_hi[buf], c)) return;
                         tc_fence_after();
                     }
-                    mma_ts(tmem + 256 + o * 128, tmem + buf * 128 + kk * 8, sdesc_add(db, kk * 2048),
+                    warp_mma_ts(tmem + 256 + o * 128, tmem + buf * 128 + kk * 8, sdesc_add(db, kk * 2048),
                            idPV, (first && kk == 0) ? 0u : 1u);
                 }
             };
             while (ok) {
                 const int slot = it & 1;
                 if (!wait(sm.piece_full[slot], it >> 1)) break;
-                const int pb = sm.piece[slot].b, n = sm.piece[slot].n, nt = sm.piece[slot].ntok;
-                mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+                const int pb = __shfl_sync(0xffffffffu, sm.piece[slot].b, 0);
+                const int n = __shfl_sync(0xffffffffu, sm.piece[slot].n, 0);
+                const int nt = __shfl_sync(0xffffffffu, sm.piece[slot].ntok, 0);
+                if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+                __syncwarp();
                 if (pb < 0) break;
                 if (!wait(sm.q_full, it)) break;
                 if constexpr (PAIR) {
@@ -628,11 +631,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             // S_s is free once the P written over it has been read
                             if (cnt[s] > 0 && !wait(sm.o_done[s], cnt[s] - 1)) break;
                             issue_s(fk, s, s);
-                            mma_commit(smem_u32(&sm.s_full[s]));
+                            warp_mma_commit(smem_u32(&sm.s_full[s]));
                         }
                         if (!ok) break;
-                        mma_commit(smem_u32(&sm.empty[fk % S]));
-                        if (j == n - 1) mma_commit(smem_u32(&sm.q_empty));
+                        warp_mma_commit(smem_u32(&sm.empty[fk % S]));
+                        if (j == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
                         for (int s = 0; s < ns && ok; ++s) {
                             // (stream 0 mends V before its P is ready, so both may follow it)
                             if (!wait(sm.p_full[s], cnt[s])) break;
@@ -640,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             if (j == 0 && done[s] > 0 && !wait(sm.o_free[s], done[s] - 1)) break;
                             issue_pv(fv, s, s, cnt[s], j == 0);
                             if (!ok) break;
-                            mma_commit(smem_u32(&sm.o_done[s]));
+                            warp_mma_commit(smem_u32(&sm.o_done[s]));
                             ++cnt[s];
                         }
                         if (!ok) break;
-                        mma_commit(smem_u32(&sm.empty[fv % S]));
+                        warp_mma_commit(smem_u32(&sm.empty[fv % S]));
                     }
                     for (int s = 0; s < ns; ++s) ++done[s];
                 } else {
@@ -656,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         const int c = cnt[bf] + (j >> 1);
                         if (c > 0 && !wait(sm.o_done[bf], c - 1)) return;
                         issue_s(fk, bf, 0);
-                        mma_commit(smem_u32(&sm.empty[fk % S]));
-                        mma_commit(smem_u32(&sm.s_full[bf]));
-                        if (j == n - 1) mma_commit(smem_u32(&sm.q_empty));
+                        warp_mma_commit(smem_u32(&sm.empty[fk % S]));
+                        warp_mma_commit(smem_u32(&sm.s_full[bf]));
+                        if (j == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
                     };
                     do_s(0);
                     if (ok && n > 1) do_s(1);
@@ -671,8 +674,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         issue_pv(fv, bf, C::kStreams == 2 ? bf : 0, c,
                                  C::kStreams == 2 ? j < 2 : j == 0);
                         if (!ok) break;
-                        mma_commit(smem_u32(&sm.empty[fv % S]));
-                        mma_commit(smem_u32(&sm.o_done[bf]));
+                        warp_mma_commit(smem_u32(&sm.empty[fv % S]));
+                        warp_mma_commit(smem_u32(&sm.o_done[bf]));
                         if (j + 2 < n) do_s(j + 2);
                     }
                     cnt[0] += (n + 1) / 2;
@@ -682,7 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 f += 2 * n;
                 ++it;
             }
-            mma_commit(smem_u32(&sm.drain));
+            warp_mma_commit(smem_u32(&sm.drain));
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         }
     } else if (warp >= 4) {
@@ -694,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const bool row_used = row_tok < p.tile_tokens;
-        int it = 0, f = 0, cnt[2] = {0, 0}, joins = 0;
+        int it = 0, f = 0, cnt[2] = {0, 0};
         bool ok = true;
         while (ok) {
             const int slot = it & 1;
@@ -727,6 +730,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_off + buf * 128;
                     const bool ragged = key0 + BN > x.ctx;
+                    // V rows past the length are whatever the page held, and a drafted V
+                    // may be anything: both are mended before P is handed over (before the
+                    // scores take up the registers; only once S(j) is there, so that the stage's
+                    // barrier is at most one phase behind).
+                    if (ragged && (!PAIR || w == 0)) {
+                        const int fv = f + fifo_v<PAIR>(j, x.n);
+                        if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
+                            break;
+                        if (row < BN && key0 + row >= x.ctx) {
+                            const bool past = key0 + row >= x.len;
+#pragma unroll 1
+                            for (int cb = 0; cb < C::kCols; ++cb) {
+                                uint4* at = reinterpret_cast<uint4*>(sm.kv[fv % S] + cb * (BN * 128) +
+                                                                     row * 128);
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const int ch = (e + row) & 7;  // (spreads the banks)
+                                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                    if (!past) {
+                                        v = at[ch];
+                                        bool bad = false;
+                                        auto mend = [&](uint32_t& u) {
+                                            if (!finite_bf16(u)) { u &= 0xffff0000u; bad = true; }
+                                            if (!finite_bf16(u >> 16)) { u &= 0xffffu; bad = true; }
+                                        };
+                                        mend(v.x);
+                                        mend(v.y);
+                                        mend(v.z);
+                                        mend(v.w);
+                                        if (!bad) continue;
+                                        *reinterpret_cast<volatile int*>(&sm.poison) = 1;
+                                    }
+                                    at[ch] = v;
+                                }
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        __syncwarp();
+                    }
                     float s[BN];
                     float alpha = 1.f;
                     bool need = false;
@@ -799,43 +841,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             tmem_st16(o_at + cc * 32, lo);
                             tmem_st16(o_at + cc * 32 + 16, hi);
                         }
-                    }
-                    // V rows past the length are whatever the page held, and a drafted V
-                    // may be anything: both are mended before P is handed over.
-                    if (ragged && (!PAIR || w == 0)) {
-                        const int fv = f + fifo_v<PAIR>(j, x.n);
-                        if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
-                            break;
-                        if (row < BN && key0 + row >= x.ctx) {
-                            const bool past = key0 + row >= x.len;
-#pragma unroll 1
-                            for (int cb = 0; cb < C::kCols; ++cb) {
-                                uint4* at = reinterpret_cast<uint4*>(sm.kv[fv % S] + cb * (BN * 128) +
-                                                                     row * 128);
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int ch = (e + row) & 7;  // (spreads the banks)
-                                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                    if (!past) {
-                                        v = at[ch];
-                                        bool bad = false;
-                                        auto mend = [&](uint32_t& u) {
-                                            if (!finite_bf16(u)) { u &= 0xffff0000u; bad = true; }
-                                            if (!finite_bf16(u >> 16)) { u &= 0xffffu; bad = true; }
-                                        };
-                                        mend(v.x);
-                                        mend(v.y);
-                                        mend(v.z);
-                                        mend(v.w);
-                                        if (!bad) continue;
-                                        *reinterpret_cast<volatile int*>(&sm.poison) = 1;
-                                    }
-                                    at[ch] = v;
-                                }
-                            }
-                            fence_proxy_async_smem();
-                        }
-                        __syncwarp();
                     }
                     uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
@@ -985,48 +990,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[PAIR ? w : 0]));
             }
-            if constexpr (!PAIR) {
-                if (p.fused && x.part >= 0) {
-                    // Whoever brings the item's last partial joins them.  The item's word
-                    // counts those brought under this call's number; anything else that it
-                    // holds counts as none, and the last one clears it.
-                    __threadfence();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.join_full));
-                    if (warp == 4) {
-                        if (!(ok = warp_wait(smem_u32(&sm.join_full), joins & 1, stop, status))) break;
-                        if (lane == 0) {
-                            __threadfence();
-                            unsigned long long* word = p.arrived + x.last_cta;
-                            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word);
-                            unsigned long long now;
-                            for (;;) {
-                                now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
-                                const unsigned long long seen = atomicCAS(word, old, now);
-                                if (seen == old) break;
-                                old = seen;
-                            }
-                            const int parts = x.last_cta - x.first_cta + 1;
-                            sm.join_last = (int)(now & 255) == parts;
-                            if (sm.join_last) *word = 0;
-                            __threadfence();
-                            mbar_arrive(smem_u32(&sm.join_go));
-                        }
-                        __syncwarp();
-                    }
-                    if (!(ok = warp_wait(smem_u32(&sm.join_go), joins & 1, stop, status))) break;
-                    ++joins;
-                    if (sm.join_last) {
-                        __threadfence();
-                        for (int r = warp - 4; r < p.part_rows; r += 8) {
-                            const int rt = r / p.group;
-                            if (rt >= x.ntok) break;
-                            join_row<DR>(p, r, x.first_cta, x.last_cta - x.first_cta + 1,
-                                         (size_t)x.tok0 + rt, x.h * p.group + r - rt * p.group);
-                        }
-                    }
-                }
-            }
             f += 2 * x.n;
             ++it;
         }
@@ -1047,10 +1010,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
 
     tc_fence_before();
+    __threadfence();  // partials, before this CTA says that they are there
     __syncthreads();
     if (warp == 2) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
+    }
+    if constexpr (!PAIR) {
+        // Whoever brings an item's last partial joins them.  The item's word counts
+        // those brought under this call's number; anything else that it holds counts
+        // as none, and the last one clears it.
+        const int n = p.fused && !sm.abort_flag ? sm.n_shared : 0;
+        if (n == 0) return;
+        if (threadIdx.x < n) {
+            const Piece& x = sm.shared[threadIdx.x];
+            __threadfence();
+            unsigned long long* word = p.arrived + x.last_cta;
+            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word), now;
+            for (;;) {
+                now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
+                const unsigned long long seen = atomicCAS(word, old, now);
+                if (seen == old) break;
+                old = seen;
+            }
+            const bool last = (int)(now & 255) == x.last_cta - x.first_cta + 1;
+            sm.join_last[threadIdx.x] = last;
+            if (last) *word = 0;
+            __threadfence();
+        }
+        __syncthreads();
+        for (int i = 0; i < n; ++i) {
+            if (!sm.join_last[i]) continue;
+            const Piece& x = sm.shared[i];
+            for (int r = warp; r < p.part_rows; r += kThreads / 32) {
+                const int rt = r / p.group;
+                if (rt >= x.ntok) break;
+                join_row<DR>(p, r, x.first_cta, x.last_cta - x.first_cta + 1, (size_t)x.tok0 + rt,
+                             x.h * p.group + r - rt * p.group);
+            }
+        }
     }
 }
 

@@ -211,6 +211,16 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 c = cnt[w] + j if pair else cnt[b] + (j >> 1)
                 while not sim.ready(f"s_full{b}", c & 1, c + 1):
                     yield
+                if j >= ragged and (not pair or w == 0) and mistake != "no_mend":
+                    fv = f + fifo_v(pair, j, n)
+                    if mistake != "no_mend_wait":
+                        while not sim.ready(f"full{fv % stages}", (fv // stages) & 1,
+                                            fv // stages + 1):
+                            yield
+                    if smem.get(f"kv{fv % stages}") != ("v", uid, j):
+                        raise Hazard(f"mending ({uid},{j}) found {smem.get(f'kv{fv % stages}')}")
+                    yield
+                    st["mended"][fv % stages].add(q)
                 if st["S"].get(b) != (uid, j):
                     raise Hazard(f"softmax {w}.{q} ({uid},{j}) read S = {st['S'].get(b)}")
                 yield
@@ -225,16 +235,6 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                             yield
                     if st["O"][o] != [(uid, x, h) for x in seen for h in (0, 1)]:
                         raise Hazard(f"rescale of ({uid},{j}) saw O = {st['O'][o]}")
-                if j >= ragged and (not pair or w == 0) and mistake != "no_mend":
-                    fv = f + fifo_v(pair, j, n)
-                    if mistake != "no_mend_wait":
-                        while not sim.ready(f"full{fv % stages}", (fv // stages) & 1,
-                                            fv // stages + 1):
-                            yield
-                    if smem.get(f"kv{fv % stages}") != ("v", uid, j):
-                        raise Hazard(f"mending ({uid},{j}) found {smem.get(f'kv{fv % stages}')}")
-                    yield
-                    st["mended"][fv % stages].add(q)
                 for hf, bar in ((0, "p_full"), (1, "p_hi")):
                     yield
                     st["P"].setdefault((b, hf), {})[q] = (uid, j)
