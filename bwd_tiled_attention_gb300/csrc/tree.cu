@@ -23,7 +23,8 @@
 //     leaves partials, joined in a fixed order: with few rows by the CTA that
 //     finishes last, otherwise by a second kernel.
 //   - the K and V tiles of a CTA run through one ring of stages in the order
-//     the tensor core consumes them, filled by TMA boxes of one page each.
+//     the tensor core consumes them, filled by TMA boxes of one page each, K
+//     and V by a warp each.
 //   - up to d = 128 two streams (softmax warpgroups, S/P and O in TMEM) work on
 //     alternate key tiles of one row tile; with more than 128 rows they take
 //     two row tiles and share each key tile (PAIR), since then the tensor core
@@ -204,6 +205,8 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
         : "memory");
 }
 
+__device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
+
 __device__ __forceinline__ bool finite_bf16(uint32_t lo16) { return (lo16 & 0x7F80u) != 0x7F80u; }
 
 // Bits of the 32 keys from `j0` (an index among the sequence's own tokens;
@@ -214,6 +217,93 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t* words, int nwords,
     const uint32_t hi = w + 1 < 0 ? 0xffffffffu : (w + 1 < nwords ? words[w + 1] : 0u);
     return __funnelshift_r(lo, hi, j0 & 31);
 }
+
+// One warp's loads of K or V tiles into the ring: a box is one page's keys (or
+// 64 of them) by 64 columns, and each box of a tile is a lane's.  K and V have a
+// warp each: a lane's TMA takes ~95 cycles to issue, and a tile of 16-token
+// pages at d = 128 has 16 boxes.
+//
+// The wait for a stage looks at a phase's parity only.  That is enough: tile
+// loads are consumed in ring order, and this warp's previous load has waited
+// for the consumer to pass the place S before it, so the stage is at most one
+// phase behind.
+template <int BN, int S, int COLS>
+struct Loader {
+    const TreeParams& p;
+    const CUtensorMap* map;
+    uint8_t* ring;
+    uint64_t *full, *empty;
+    volatile int* stop;
+    int ps, shift, rows, rows_shift, boxes, box, col, box_key;
+    uint32_t dst;
+    // of the piece: page ids of a window of 32 pages, and of the next one
+    const int* table;
+    int used, win, ids, nxt, key0, len, head;
+    int place = -1;  // ring place of this lane's turn among the last 32 loads
+    int count = 0;
+
+    __device__ __forceinline__ Loader(const TreeParams& p_, const CUtensorMap* map_, uint8_t* ring_,
+                                      uint64_t* full_, uint64_t* empty_, volatile int* stop_)
+        : p(p_), map(map_), ring(ring_), full(full_), empty(empty_), stop(stop_) {
+        ps = p.cache.page_size;
+        shift = p.page_shift;
+        rows = min(ps, BN);
+        rows_shift = rows == ps ? shift : 6;  // (pages of 128 tokens, tiles of 64)
+        boxes = BN >> rows_shift;
+        box = lane_id() / COLS;
+        col = lane_id() % COLS;
+        box_key = box << rows_shift;
+        dst = col * (BN * 128) + box_key * 128;
+    }
+    __device__ __forceinline__ int table_at(int i) const { return i < used ? table[i] : -1; }
+    __device__ __forceinline__ void begin(const Piece& x) {
+        table = p.cache.table + (long long)x.slot * p.cache.max_pages;
+        len = x.len;
+        head = x.h;
+        used = (len + ps - 1) >> shift;
+        key0 = x.k0 * BN;
+        win = key0 >> shift;
+        ids = table_at(win + lane_id());
+        nxt = table_at(win + 32 + lane_id());
+    }
+    // The piece's next tile into place f of the ring.
+    __device__ __forceinline__ bool tile(int f, int* status) {
+        const int first = key0 >> shift;
+        if (first >= win + 32) {
+            win += 32;
+            ids = nxt;
+            nxt = table_at(win + 32 + lane_id());
+        }
+        const int page = __shfl_sync(0xffffffffu, ids, (first - win + box) & 31);
+        const int st = f % S;
+        if (!warp_wait(smem_u32(&empty[st]), ((f / S) & 1) ^ 1, stop, status)) return false;
+        const int have = max(0, min(boxes, (len - key0 + rows - 1) >> rows_shift));
+        const uint32_t bar = smem_u32(&full[st]);
+        if (lane_id() == 0) mbar_arrive_expect_tx(bar, have * rows * 128 * COLS);
+        __syncwarp();
+        if (box < have) {
+            // a page id out of range reads the fill value (zeros) and is reported
+            int plane = -1;
+            if (page >= 0 && page < p.cache.pages)
+                plane = (p.layer * p.cache.pages + page) * p.cache.heads + head;
+            else
+                atomicOr(status, kCacheBadSlot);
+            tma_load_3d(smem_u32(ring) + st * (BN * COLS * 128) + dst, map, bar, col * 64,
+                        (key0 + box_key) & (ps - 1), plane);
+        }
+        if ((count & 31) == (int)lane_id()) place = f;
+        ++count;
+        key0 += BN;
+        return true;
+    }
+    // After an abort: waits (bounded) for the loads that may still fly.
+    __device__ __forceinline__ void drain(const volatile int* never) {
+        int last = place;
+        for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+        if (place >= 0 && place > last - S) mbar_wait(smem_u32(&full[place % S]), (place / S) & 1, never);
+        __syncwarp();
+    }
+};
 
 // P = 2^(s c - m) of 32 columns as bf16 pairs (each rounded once: P enters the
 // tensor core in the type of V), and their fp32 sum before that rounding.
@@ -327,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         mbar_init(smem_u32(&sm.q_empty), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.piece_full[i]), 1);
-            mbar_init(smem_u32(&sm.piece_empty[i]), 1 + 8);
+            mbar_init(smem_u32(&sm.piece_empty[i]), 1 + 8 + 1);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.p_full[i]), 4);
             mbar_init(smem_u32(&sm.p_hi[i]), 4);
@@ -354,6 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
     // ---- the line of all key tiles, and where this CTA's stretch begins: the
     // producer warp's own business for small batches, all threads' for large ones
+    SeqInfo mine_info = {0, 0, 0, 0, 0, 0};  // (one sequence a lane: B <= 32)
     if (p.B <= 128 ? warp == 0 : true) {
         const bool all_threads = p.B > 128;
         const int chunk = all_threads ? (p.B + kThreads - 1) / kThreads : (p.B + 31) / 32;
@@ -363,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int i = i0; i < i1; ++i) {
             const SeqInfo s = seq_info(p, i);
             bad |= s.bad;
+            mine_info = s;
             mine += head_tiles(p, s, tokens, BN) * p.cache.heads;
         }
         if (bad && blockIdx.x == 0) atomicOr(status, bad);
@@ -391,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         long long at = before + incl - mine;  // first tile of this thread's sequences
         if (begin < end && begin >= at && begin < at + mine) {
             for (int i = i0; i < i1; ++i) {
-                const SeqInfo s = seq_info(p, i);
+                const SeqInfo s = chunk == 1 ? mine_info : seq_info(p, i);
                 const long long ht = head_tiles(p, s, tokens, BN), all = ht * p.cache.heads;
                 if (begin >= at + all) {
                     at += all;
@@ -404,30 +496,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         if (all_threads) __syncthreads(); else __syncwarp();
     }
-    static_assert(128 * 72 + 256 * 216 == 384 * 168, "register split must match the launch");
+    // Registers: the launch gives every thread 168.  Two row tiles hold whole rows
+    // of scores; one row tile's loops hold half, and the producer wants the rest.
+    constexpr int kFewRegs = PAIR ? 72 : 104, kManyRegs = PAIR ? 216 : 200;
+    static_assert(128 * kFewRegs + 256 * kManyRegs == 384 * 168, "register split must match the launch");
 
     if (warp == 0) {
-        // ------------------------------------------------------------ producer
-        setmaxnreg_dec<72>();
-        int it = 0, f = 0, nq = 0;  // pieces, tile loads and query loads so far
-        int st = 0, phase = 0;      // the next load's stage, and the ring's turn
+        // ------------------------------------------------------------ pieces, Q and K
+        setmaxnreg_dec<kFewRegs>();
+        int it = 0, f = 0, nq = 0;  // pieces, ring places before this piece, query loads
         bool ok = true;
         int own_first = -1, own_tok0 = 0, own_ntok = 0, own_h = 0;  // an item that ends here
         int b = sm.start[0], h = sm.start[1], q = sm.start[2], k0 = sm.start[3];
         const long long per = sm.line[0], end = sm.line[2];
         long long at = sm.line[1];             // place in the line
+        // sequence i's geometry: a small batch stays in the lanes that looked it up
+        auto sequence = [&](int i) {
+            if (p.B > 32) return seq_info(p, i);
+            SeqInfo y;
+            y.t0 = __shfl_sync(0xffffffffu, mine_info.t0, i);
+            y.n = __shfl_sync(0xffffffffu, mine_info.n, i);
+            y.slot = __shfl_sync(0xffffffffu, mine_info.slot, i);
+            y.len = __shfl_sync(0xffffffffu, mine_info.len, i);
+            y.ctx = __shfl_sync(0xffffffffu, mine_info.ctx, i);
+            return y;
+        };
         SeqInfo s;
         s.n = 0;
-        if (at < end) s = seq_info(p, b);
-        const int ps = p.cache.page_size, ps_shift = p.page_shift;
-        const int rows = min(ps, BN);          // keys of one box
-        const int rows_shift = rows == ps ? ps_shift : 6;
-        const int boxes = BN >> rows_shift;
-        const int my_box = lane / C::kCols, my_col = lane % C::kCols;
-        const bool has_box = my_box < boxes;
-        const int my_key = my_box << rows_shift;
-        const uint32_t my_dst = my_col * (BN * 128) + my_key * 128;
-        const int box_bytes = rows * 128 * C::kCols;
+        if (at < end) s = sequence(b);
+        Loader<BN, S, C::kCols> load(p, &p.tm_k, sm.kv[0], sm.full, sm.empty, stop);
         while (ok) {
             const int slot = it & 1;
             if (!(ok = warp_wait(smem_u32(&sm.piece_empty[slot]), ((it >> 1) & 1) ^ 1, stop, status)))
@@ -469,7 +566,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             __syncwarp();
 
-            // -- loads of this piece
             auto load_q = [&] {
                 if (!(ok = warp_wait(smem_u32(&sm.q_empty), (it & 1) ^ 1, stop, status))) return;
                 if (lane == 0) {
@@ -485,65 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 ++nq;
             };
             if (it == 0) load_q();  // (later pieces: behind the first key tile)
-            const int* table = p.cache.table + (long long)x.slot * p.cache.max_pages;
-            const int used = (x.len + ps - 1) >> ps_shift;
-            auto table_at = [&](int i) { return i < used ? table[i] : -1; };
-            // page ids of a window of 32 pages, and of the next one
-            int win = (x.k0 * BN) >> ps_shift;
-            int ids = table_at(win + lane), nxt = table_at(win + 32 + lane);
-            int page_prev = -1;
-            // the page of this lane's box in the tile at key0
-            auto page_of = [&](int key0) {
-                const int first = key0 >> ps_shift;
-                if (first >= win + 32) {
-                    win += 32;
-                    ids = nxt;
-                    nxt = table_at(win + 32 + lane);
-                }
-                return __shfl_sync(0xffffffffu, ids, (first - win + my_box) & 31);
-            };
-            auto load_tile = [&](int key0, int page, const CUtensorMap* map) {
-                if (!(ok = warp_wait(smem_u32(&sm.empty[st]), phase ^ 1, stop, status))) return;
-                const int have = max(0, min(boxes, (x.len - key0 + rows - 1) >> rows_shift));
-                const uint32_t bar = smem_u32(&sm.full[st]);
-                if (lane == 0) mbar_arrive_expect_tx(bar, have * box_bytes);
-                __syncwarp();
-                if (has_box && my_box < have) {
-                    // a page id out of range reads the fill value (zeros) and is reported
-                    int plane = -1;
-                    if (page >= 0 && page < p.cache.pages)
-                        plane = (p.layer * p.cache.pages + page) * p.cache.heads + x.h;
-                    else
-                        atomicOr(status, kCacheBadSlot);
-                    tma_load_3d(smem_u32(sm.kv[st]) + my_dst, map, bar, my_col * 64,
-                                (key0 + my_key) & (ps - 1), plane);
-                }
-                ++f;
-                if (++st == S) {
-                    st = 0;
-                    phase ^= 1;
-                }
-            };
-            int key0 = x.k0 * BN;
-            if constexpr (PAIR) {
-                for (int j = 0; j < x.n && ok; ++j, key0 += BN) {
-                    const int pg = page_of(key0);
-                    load_tile(key0, pg, &p.tm_k);
-                    if (ok && j == 0 && it > 0) load_q();
-                    if (ok) load_tile(key0, pg, &p.tm_v);
-                }
-            } else {
-                for (int j = 0; j <= x.n && ok; ++j, key0 += BN) {
-                    int pg = -1;
-                    if (j < x.n) {
-                        pg = page_of(key0);
-                        load_tile(key0, pg, &p.tm_k);
-                        if (ok && j == 0 && it > 0) load_q();
-                    }
-                    if (ok && j >= 1) load_tile(key0 - BN, page_prev, &p.tm_v);
-                    page_prev = pg;
-                }
+            load.begin(x);
+            for (int j = 0; j < x.n && ok; ++j) {
+                ok = load.tile(f + fifo_k<PAIR>(j), status);
+                if (ok && j == 0 && it > 0) load_q();
             }
+            f += 2 * x.n;
             ++it;
             // -- the next item
             at += x.n;
@@ -560,25 +603,39 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                                 at = end;
                                 break;
                             }
-                            s = seq_info(p, b);
+                            s = sequence(b);
                         } while (s.n == 0);
                     }
                 }
             }
         }
-        if (lane == 0) {
-            if (!p.fused) p.meta[blockIdx.x] = make_int4(own_first, own_tok0, own_ntok, own_h);
-            // Never leave a TMA write in flight.
-            const volatile int* z = &sm.zero;
-            for (int i = 0; i < S && i < f; ++i) {
-                const int g = f - 1 - i;
-                mbar_wait(smem_u32(&sm.full[g % S]), (g / S) & 1, z);
-            }
-            if (nq > 0) mbar_wait(smem_u32(&sm.q_full), (nq - 1) & 1, z);
+        if (lane == 0 && !p.fused) p.meta[blockIdx.x] = make_int4(own_first, own_tok0, own_ntok, own_h);
+        if (!ok) {  // never leave a TMA write in flight
+            load.drain(&sm.zero);
+            if (lane == 0 && nq > 0) mbar_wait(smem_u32(&sm.q_full), (nq - 1) & 1, &sm.zero);
         }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ V
+        setmaxnreg_dec<kFewRegs>();
+        int it = 0, f = 0;
+        bool ok = true;
+        Loader<BN, S, C::kCols> load(p, &p.tm_v, sm.kv[0], sm.full, sm.empty, stop);
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_full[slot]), (it >> 1) & 1, stop, status))) break;
+            const Piece x = sm.piece[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+            if (x.b < 0) break;
+            load.begin(x);
+            for (int j = 0; j < x.n && ok; ++j) ok = load.tile(f + fifo_v<PAIR>(j, x.n), status);
+            f += 2 * x.n;
+            ++it;
+        }
+        if (!ok) load.drain(&sm.zero);
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        setmaxnreg_dec<72>();
+        setmaxnreg_dec<kFewRegs>();
         {
             constexpr uint32_t idS = make_idesc_bf16(128, BN, false, false);
             constexpr uint32_t idPV = make_idesc_bf16(128, D, false, true);
@@ -663,19 +720,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         warp_mma_commit(smem_u32(&sm.s_full[bf]));
                         if (j == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
                     };
-                    do_s(0);
-                    if (ok && n > 1) do_s(1);
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int fv = f + fifo_v<false>(j, n), bf = j & 1;
-                        const int c = cnt[bf] + (j >> 1);
-                        if (!wait(sm.p_full[bf], c)) break;
-                        if (!wait(sm.full[fv % S], fv / S)) break;
-                        if (j == 0 && it > 0 && !wait(sm.o_free[0], it - 1)) break;
-                        issue_pv(fv, bf, C::kStreams == 2 ? bf : 0, c,
-                                 C::kStreams == 2 ? j < 2 : j == 0);
-                        if (!ok) break;
-                        warp_mma_commit(smem_u32(&sm.empty[fv % S]));
-                        warp_mma_commit(smem_u32(&sm.o_done[bf]));
+                    for (int j = -2; j < n && ok; ++j) {
+                        if (j >= 0) {
+                            const int fv = f + fifo_v<false>(j, n), bf = j & 1;
+                            const int c = cnt[bf] + (j >> 1);
+                            if (!wait(sm.p_full[bf], c)) break;
+                            if (!wait(sm.full[fv % S], fv / S)) break;
+                            if (j == 0 && it > 0 && !wait(sm.o_free[0], it - 1)) break;
+                            issue_pv(fv, bf, C::kStreams == 2 ? bf : 0, c,
+                                     C::kStreams == 2 ? j < 2 : j == 0);
+                            if (!ok) break;
+                            warp_mma_commit(smem_u32(&sm.empty[fv % S]));
+                            warp_mma_commit(smem_u32(&sm.o_done[bf]));
+                        }
                         if (j + 2 < n) do_s(j + 2);
                     }
                     cnt[0] += (n + 1) / 2;
@@ -690,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
     } else if (warp >= 4) {
         // ------------------------------------------------------------ softmax and epilogue
-        setmaxnreg_inc<216>();
+        setmaxnreg_inc<kManyRegs>();
         const int w = (warp - 4) >> 2;          // stream
         const int q4 = warp & 3;                // TMEM lane quarter
         const int row = q4 * 32 + lane;
@@ -769,41 +826,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         }
                         __syncwarp();
                     }
-                    float s[BN];
-                    float alpha = 1.f;
+                    float alpha = 1.f, neg = 0.f;
                     bool need = false;
-                    float neg = 0.f;
-                    if (warp_valid) {
-                        uint32_t r[BN / 32][32];
-#pragma unroll
-                        for (int i = 0; i < BN / 32; ++i) tmem_ld32(s_at + i * 32, r[i]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < BN; ++i) s[i] = __uint_as_float(r[i / 32][i % 32]);
-                        if (ragged) {
-#pragma unroll
-                            for (int i = 0; i < BN / 32; ++i) {
-                                const int kb = key0 + i * 32;
-                                uint32_t bits = p.mask ? mask_bits(words, 2 * p.words, kb - x.ctx)
-                                                       : 0xffffffffu;
-                                const int room = limit - kb;
-                                if (room <= 0) bits = 0;
-                                else if (room < 32) bits &= (1u << room) - 1u;
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (!((bits >> e) & 1u)) s[i * 32 + e] = -INFINITY;
-                            }
-                        }
-                        float m8[8];
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            float m = fmax3(s[k], s[8 + k], s[16 + k]);
-#pragma unroll
-                            for (int i = 24; i + 8 < BN; i += 16) m = fmax3(m, s[i + k], s[i + 8 + k]);
-                            m8[k] = fmaxf(m, s[BN - 8 + k]);
-                        }
-                        const float mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
-                                               fmaxf(m8[6], m8[7])) * p.scale_log2;
+                    // the reference moves when the row maximum outgrows it
+                    auto take_max = [&](float mx) {
                         if (first) {
                             m_ref = mx;
                         } else if (mx > m_ref + kRescale) {
@@ -813,6 +839,84 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             l *= alpha;
                         }
                         neg = m_ref == -INFINITY ? 0.f : -m_ref;
+                    };
+                    auto key_bits = [&](int kb) {
+                        uint32_t bits = p.mask ? mask_bits(words, 2 * p.words, kb - x.ctx) : 0xffffffffu;
+                        const int room = limit - kb;
+                        if (room <= 0) bits = 0;
+                        else if (room < 32) bits &= (1u << room) - 1u;
+                        return bits;
+                    };
+                    float s[PAIR ? BN : 1];
+                    if constexpr (PAIR) {
+                        // tensor-bound: the whole row in registers, all loads in flight
+                        if (warp_valid) {
+                            uint32_t r[BN / 32][32];
+#pragma unroll
+                            for (int i = 0; i < BN / 32; ++i) tmem_ld32(s_at + i * 32, r[i]);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < BN; ++i) s[i] = __uint_as_float(r[i / 32][i % 32]);
+                            if (ragged) {
+#pragma unroll
+                                for (int i = 0; i < BN / 32; ++i) {
+                                    const uint32_t bits = key_bits(key0 + i * 32);
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (!((bits >> e) & 1u)) s[i * 32 + e] = -INFINITY;
+                                }
+                            }
+                            float m8[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                float m = fmax3(s[k], s[8 + k], s[16 + k]);
+#pragma unroll
+                                for (int i = 24; i + 8 < BN; i += 16) m = fmax3(m, s[i + k], s[i + 8 + k]);
+                                m8[k] = fmaxf(m, s[BN - 8 + k]);
+                            }
+                            take_max(fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                                           fmaxf(m8[6], m8[7])) * p.scale_log2);
+                        }
+                    } else if (warp_valid) {
+                        // memory-bound, and often only a few tiles in a CTA: S is read twice in
+                        // loops of 64 columns, whose code is a quarter of the unrolled form's (a
+                        // CTA's first pass through it waits for every instruction line)
+                        if (ragged) {
+#pragma unroll 1
+                            for (int i = 0; i < BN / 32; ++i) {
+                                const uint32_t bits = key_bits(key0 + i * 32);
+                                uint32_t r[32], lo[16], hi[16];
+                                tmem_ld32(s_at + i * 32, r);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    lo[e] = (bits >> e) & 1u ? r[e] : 0xff800000u;
+                                    hi[e] = (bits >> (16 + e)) & 1u ? r[16 + e] : 0xff800000u;
+                                }
+                                tmem_st16(s_at + i * 32, lo);
+                                tmem_st16(s_at + i * 32 + 16, hi);
+                            }
+                            tmem_st_wait();
+                        }
+                        float mx = -INFINITY;
+#pragma unroll 1
+                        for (int i = 0; i < BN; i += 64) {
+                            uint32_t r0[32], r1[32];
+                            tmem_ld32(s_at + i, r0);
+                            tmem_ld32(s_at + i + 32, r1);
+                            tmem_ld_wait();
+                            float m4[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float m = fmaxf(__uint_as_float(r0[k]), __uint_as_float(r1[k]));
+#pragma unroll
+                                for (int e = 4; e < 32; e += 4)
+                                    m = fmax3(m, __uint_as_float(r0[e + k]), __uint_as_float(r1[e + k]));
+                                m4[k] = m;
+                            }
+                            mx = fmax3(mx, fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                        }
+                        take_max(mx * p.scale_log2);
                     }
                     first = false;
                     // O~ is stable when its last PV is done: with two streams S(j) was
@@ -843,20 +947,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         }
                     }
                     uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                    if constexpr (PAIR) {
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        if (warp_valid) {
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (warp_valid) {
 #pragma unroll
-                            for (int cc = hf * (BN / 64); cc < (hf + 1) * (BN / 64); ++cc) {
-                                uint32_t pk[16];
-                                exp_chunk(s + cc * 32, p.scale_log2, neg, acc, pk);
-                                tmem_st16(s_at + cc * 16, pk);
+                                for (int cc = hf * (BN / 64); cc < (hf + 1) * (BN / 64); ++cc) {
+                                    uint32_t pk[16];
+                                    exp_chunk(s + cc * 32, p.scale_log2, neg, acc, pk);
+                                    tmem_st16(s_at + cc * 16, pk);
+                                }
+                                tmem_st_wait();
                             }
-                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(hf == 0 ? &sm.p_full[buf] : &sm.p_hi[buf]));
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(hf == 0 ? &sm.p_full[buf] : &sm.p_hi[buf]));
+                    } else {
+                        // (a chunk's P lies over scores that have been read)
+#pragma unroll 1
+                        for (int hf = 0; hf < 2; ++hf) {
+                            if (warp_valid) {
+                                constexpr int W = BN / 64;  // chunks of a half
+                                uint32_t r[W][32];
+#pragma unroll
+                                for (int c2 = 0; c2 < W; ++c2) tmem_ld32(s_at + (hf * W + c2) * 32, r[c2]);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int c2 = 0; c2 < W; ++c2) {
+                                    uint32_t pk[16];
+                                    exp_chunk(reinterpret_cast<const float*>(r[c2]), p.scale_log2, neg,
+                                              acc, pk);
+                                    tmem_st16(s_at + (hf * W + c2) * 16, pk);
+                                }
+                                tmem_st_wait();
+                            }
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(hf == 0 ? &sm.p_full[buf] : &sm.p_hi[buf]));
+                        }
                     }
                     if (warp_valid) {
                         float a0, a1, b0, b1;
@@ -994,12 +1123,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             ++it;
         }
     } else {
-        // ------------------------------------------------------------ warps 2, 3
-        setmaxnreg_dec<72>();
+        // ------------------------------------------------------------ warp 2
+        setmaxnreg_dec<kFewRegs>();
         if (p.zero_rest && p.cu) {  // tokens that no sequence owns
             const int used = min(max(p.cu[p.B], 0), p.T);
-            const long long step = (long long)gridDim.x * 64;
-            const long long at = (long long)blockIdx.x * 64 + threadIdx.x - 64;
+            const long long step = (long long)gridDim.x * 32;
+            const long long at = (long long)blockIdx.x * 32 + lane;
             const long long rows = (long long)(p.T - used) * p.Hq;
             uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
                                                 (long long)used * p.Hq * DR);
@@ -1010,7 +1139,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     }
 
     tc_fence_before();
-    __threadfence();  // partials, before this CTA says that they are there
     __syncthreads();
     if (warp == 2) {
         tc_fence_after();
@@ -1024,9 +1152,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (n == 0) return;
         if (threadIdx.x < n) {
             const Piece& x = sm.shared[threadIdx.x];
-            __threadfence();
+            fence_gpu();  // all partials of the CTA, before it says that they are there
             unsigned long long* word = p.arrived + x.last_cta;
-            unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(word), now;
+            unsigned long long old = 0, now;  // (what the last call left, most often)
             for (;;) {
                 now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
                 const unsigned long long seen = atomicCAS(word, old, now);
@@ -1035,8 +1163,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
             const bool last = (int)(now & 255) == x.last_cta - x.first_cta + 1;
             sm.join_last[threadIdx.x] = last;
-            if (last) *word = 0;
-            __threadfence();
+            if (last) {
+                *word = 0;
+                fence_gpu();
+            }
         }
         __syncthreads();
         for (int i = 0; i < n; ++i) {

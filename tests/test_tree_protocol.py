@@ -1,8 +1,8 @@
 """Model of the barrier protocol of the attention over the paged cache
 (csrc/tree.cu), run on random pieces and random timings, with the machinery and
-the mbarrier semantics of tests/test_fwd_protocol.py: the producer warp (one
-ring of stages for K and V tiles in the order the tensor core reads them, Q
-after the first K tile), the MMA issuer, and two warpgroups of softmax and
+the mbarrier semantics of tests/test_fwd_protocol.py: the two loading warps (one
+for the pieces, Q and K, one for V, into one ring of stages in the order the
+tensor core reads them), the MMA issuer, and two warpgroups of softmax and
 epilogue warps.
 
 Layouts modelled:
@@ -37,7 +37,7 @@ def fifo_v(pair, j, n):
 def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
     """pieces: list of (n key tiles, row tiles, first ragged tile)."""
     pair, streams = layout == "pair", 1 if layout == "one" else 2
-    sim = Sim(pieces, seed, consumers=1 + 2 * warps)
+    sim = Sim(pieces, seed, consumers=2 + 2 * warps)
     for b in (0, 1):
         for name in ("s_full", "o_done"):
             sim.bar(f"{name}{b}")
@@ -54,27 +54,25 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
     st = {"S": {}, "P": {}, "O": {0: [], 1: []}, "read": {}, "q_read": True, "mended": {},
           "stat": {}}
 
-    def producer():
+    def load(tag, f):
+        s = f % stages
+        if mistake != "no_empty_wait":
+            while not sim.ready(f"empty{s}", ((f // stages) & 1) ^ 1, f // stages):
+                yield
+        if st["read"].get(s) is False:
+            raise Hazard(f"stage {s} reloaded before it was read")
+        st["read"][s] = False
+        st["mended"][s] = set()
+        sim.load(f"full{s}", f"kv{s}", tag)
+        yield
+
+    def keys():
         it = f = 0
         while True:
             piece = yield from sim.grab(it)
             if piece is None:
                 return
             uid, n, _, _ = piece
-
-            def load(tag):
-                nonlocal f
-                s = f % stages
-                if mistake != "no_empty_wait":
-                    while not sim.ready(f"empty{s}", ((f // stages) & 1) ^ 1, f // stages):
-                        yield
-                if st["read"].get(s) is False:
-                    raise Hazard(f"stage {s} reloaded before it was read")
-                st["read"][s] = False
-                st["mended"][s] = set()
-                sim.load(f"full{s}", f"kv{s}", tag)
-                f += 1
-                yield
 
             def load_q():
                 if mistake != "no_q_empty_wait":
@@ -86,15 +84,25 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 sim.load("q_full", "q", uid)
                 yield
 
-            for j in range(n if pair else n + 1):
-                if j < n:
-                    yield from load(("k", uid, j))
-                    if j == 0:
-                        yield from load_q()
-                if pair:
-                    yield from load(("v", uid, j))
-                elif j >= 1:
-                    yield from load(("v", uid, j - 1))
+            if it == 0:
+                yield from load_q()
+            for j in range(n):
+                yield from load(("k", uid, j), f + fifo_k(pair, j))
+                if j == 0 and it > 0:
+                    yield from load_q()
+            f += 2 * n
+            it += 1
+
+    def values():
+        it = f = 0
+        while True:
+            piece = yield from sim.take(it)
+            if piece is None:
+                return
+            uid, n, _, _ = piece
+            for j in range(n):
+                yield from load(("v", uid, j), f + fifo_v(pair, j, n))
+            f += 2 * n
             it += 1
 
     def mma():
@@ -311,7 +319,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
             st["O"][o].append((uid, j, hf))
             st["P"][(b, hf)] = {x: "read" for x in quarters}
 
-    roles = [producer(), mma()] + [softmax(w, q) for w in (0, 1) for q in range(warps)]
+    roles = [keys(), values(), mma()] + [softmax(w, q) for w in (0, 1) for q in range(warps)]
     sim.run(roles, execute, smem)
     want = [(u, w) for u, (n, ns, _) in enumerate(pieces) for w in (0, 1)
             if not pair or w < ns]
