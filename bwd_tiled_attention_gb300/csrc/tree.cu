@@ -184,8 +184,8 @@ __device__ __forceinline__ void locate(const TreeParams& p, const SeqInfo& s, lo
     }
 }
 
-__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* flag,
-                                             int* status) {
+// Bounded wait; on giving up the CTA stops and the status word says so.
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* flag, int* status) {
     if (mbar_wait(bar, parity, flag)) return true;
     *flag = 1;
     atomicOr(status, kCacheTimeout);
@@ -193,7 +193,7 @@ __device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, vola
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
                                           int* status) {
-    return __all_sync(0xffffffffu, wait_or_stop(bar, parity, flag, status));
+    return __all_sync(0xffffffffu, poll(bar, parity, flag, status));
 }
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
@@ -341,43 +341,58 @@ __device__ __forceinline__ void join_row(const TreeParams& p, int slot_row, int 
     const int lane = lane_id();
     constexpr int V = DR / 32;                       // columns of a lane, contiguous
     constexpr int W = V % 4 == 0 ? 4 : (V % 2 == 0 ? 2 : 1);
-    struct alignas(4 * W) Wide { float x[W]; };
     auto slot = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * p.part_rows + slot_row; };
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, __ldcg(p.part_stats + slot(i) * 2));
+    const float2* stats = reinterpret_cast<const float2*>(p.part_stats);
+    // This lane's partial's statistics, and the first partials' columns: one trip
+    // to memory where there are few.
+    constexpr int R = DR > 128 ? 2 : 4;              // partials in flight
+    float x[R][V];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if (i0 + u >= n) continue;
+            const float* at = p.part_o + slot(i0 + u) * DR + lane * V;
+#pragma unroll
+            for (int v = 0; v < V; v += W) {
+                if (W == 4) {
+                    const float4 y = __ldcg(reinterpret_cast<const float4*>(at + v));
+                    x[u][v] = y.x; x[u][v + 1 % W] = y.y; x[u][v + 2 % W] = y.z; x[u][v + 3 % W] = y.w;
+                } else if (W == 2) {
+                    const float2 y = __ldcg(reinterpret_cast<const float2*>(at + v));
+                    x[u][v] = y.x; x[u][v + 1 % W] = y.y;
+                } else {
+                    x[u][v] = __ldcg(at + v);
+                }
+            }
+        }
+    };
+    float2 st = make_float2(-INFINITY, 0.f);
+    if (lane < n) st = __ldcg(stats + slot(lane));
+    fetch(0);
+    float m = st.x;
+    for (int i = lane + 32; i < n; i += 32) m = fmaxf(m, __ldcg(stats + slot(i)).x);
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float base = m == -INFINITY ? 0.f : m;
     float acc[V], l = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) acc[v] = 0.f;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        float w = 0.f, lw = 0.f;                     // of this lane's partial
-        if (i0 + lane < n) {
-            const float2 st = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + slot(i0 + lane));
+    float w = 0.f, lw = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += R) {
+        if (i0 > 0) fetch(i0);
+        if ((i0 & 31) == 0) {                        // weights of the next 32 partials
+            if (i0 > 0)
+                st = i0 + lane < n ? __ldcg(stats + slot(i0 + lane)) : make_float2(-INFINITY, 0.f);
             w = ex2_approx(st.x - base);
             lw = st.y * w;
         }
-        const int here = min(32, n - i0);
-#pragma unroll 4
-        for (int i = 0; i < here; ++i) {
-            const float wi = __shfl_sync(0xffffffffu, w, i);
-            l += __shfl_sync(0xffffffffu, lw, i);
-            const float* at = p.part_o + slot(i0 + i) * DR + lane * V;
 #pragma unroll
-            for (int v = 0; v < V; v += W) {
-                Wide x;
-                if (W == 4) {
-                    const float4 y = __ldcg(reinterpret_cast<const float4*>(at + v));
-                    x.x[0] = y.x; x.x[1 % W] = y.y; x.x[2 % W] = y.z; x.x[3 % W] = y.w;
-                } else if (W == 2) {
-                    const float2 y = __ldcg(reinterpret_cast<const float2*>(at + v));
-                    x.x[0] = y.x; x.x[1 % W] = y.y;
-                } else {
-                    x.x[0] = __ldcg(at + v);
-                }
+        for (int u = 0; u < R; ++u) {
+            if (i0 + u >= n) break;
+            const float wi = __shfl_sync(0xffffffffu, w, (i0 + u) & 31);
+            l += __shfl_sync(0xffffffffu, lw, (i0 + u) & 31);
 #pragma unroll
-                for (int e = 0; e < W; ++e) acc[v + e] = fmaf(x.x[e], wi, acc[v + e]);
-            }
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(x[u][v], wi, acc[v]);
         }
     }
     const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
@@ -440,6 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const int tokens = p.tile_tokens * C::kQTiles;  // tokens of an item
+    if (warp == 1 && lane == 0) {
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+        tma_prefetch_desc(&p.tm_v);
+    }
     pdl_wait();
 
     // ---- the line of all key tiles, and where this CTA's stretch begins: the
@@ -1169,15 +1189,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             }
         }
         __syncthreads();
-        for (int i = 0; i < n; ++i) {
-            if (!sm.join_last[i]) continue;
+        for (int r = warp; r < n * p.part_rows; r += kThreads / 32) {
+            const int i = r >= p.part_rows, row = r - i * p.part_rows;
             const Piece& x = sm.shared[i];
-            for (int r = warp; r < p.part_rows; r += kThreads / 32) {
-                const int rt = r / p.group;
-                if (rt >= x.ntok) break;
-                join_row<DR>(p, r, x.first_cta, x.last_cta - x.first_cta + 1, (size_t)x.tok0 + rt,
-                             x.h * p.group + r - rt * p.group);
-            }
+            const int rt = row / p.group;
+            if (sm.join_last[i] && rt < x.ntok)
+                join_row<DR>(p, row, x.first_cta, x.last_cta - x.first_cta + 1, (size_t)x.tok0 + rt,
+                             x.h * p.group + row - rt * p.group);
         }
     }
 }
