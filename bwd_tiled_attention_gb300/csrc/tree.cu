@@ -207,6 +207,11 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint
 
 __device__ __forceinline__ void fence_gpu() { asm volatile("fence.acq_rel.gpu;" ::: "memory"); }
 
+// Bits 15 and 31: the low or high bf16 of a pair is an infinity or NaN (its
+// exponent, all ones, carries).
+__device__ __forceinline__ uint32_t not_finite(uint32_t pair) {
+    return ((pair & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+}
 __device__ __forceinline__ bool finite_bf16(uint32_t lo16) { return (lo16 & 0x7F80u) != 0x7F80u; }
 
 // Bits of the 32 keys from `j0` (an index among the sequence's own tokens;
@@ -700,32 +705,37 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 if (pb < 0) break;
                 if (!wait(sm.q_full, it)) break;
                 if constexpr (PAIR) {
+                    // Each stream's next scores right behind its PV, so that it does not wait
+                    // for the other's softmax: S0 S1 | PV0 S0 PV1 S1 | PV0 S0 ...
                     const int ns = nt > p.tile_tokens ? 2 : 1;
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int fk = f + 2 * j, fv = fk + 1;
-                        if (!wait(sm.full[fk % S], fk / S)) break;
+                    for (int j = -1; j < n && ok; ++j) {
+                        const int fv = f + 2 * j + 1, fk = fv + 1;  // V(j), K(j + 1)
                         for (int s = 0; s < ns && ok; ++s) {
-                            // S_s is free once the P written over it has been read
-                            if (cnt[s] > 0 && !wait(sm.o_done[s], cnt[s] - 1)) break;
-                            issue_s(fk, s, s);
-                            warp_mma_commit(smem_u32(&sm.s_full[s]));
+                            if (j >= 0) {
+                                // (stream 0 mends V before its P is ready, so both may follow it)
+                                if (!wait(sm.p_full[s], cnt[s])) break;
+                                if (s == 0 && !wait(sm.full[fv % S], fv / S)) break;
+                                if (j == 0 && done[s] > 0 && !wait(sm.o_free[s], done[s] - 1)) break;
+                                issue_pv(fv, s, s, cnt[s], j == 0);
+                                if (!ok) break;
+                                if (s == ns - 1) warp_mma_commit(smem_u32(&sm.empty[fv % S]));
+                                warp_mma_commit(smem_u32(&sm.o_done[s]));
+                                ++cnt[s];
+                            }
+                            if (j + 1 < n) {
+                                if (s == 0 && !wait(sm.full[fk % S], fk / S)) break;
+                                // S_s is free once the P written over it has been read
+                                if (cnt[s] > 0 && !wait(sm.o_done[s], cnt[s] - 1)) break;
+                                issue_s(fk, s, s);
+                                warp_mma_commit(smem_u32(&sm.s_full[s]));
+                                if (s == ns - 1) {
+                                    warp_mma_commit(smem_u32(&sm.empty[fk % S]));
+                                    if (j + 1 == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
+                                }
+                            }
                         }
-                        if (!ok) break;
-                        warp_mma_commit(smem_u32(&sm.empty[fk % S]));
-                        if (j == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
-                        for (int s = 0; s < ns && ok; ++s) {
-                            // (stream 0 mends V before its P is ready, so both may follow it)
-                            if (!wait(sm.p_full[s], cnt[s])) break;
-                            if (s == 0 && !wait(sm.full[fv % S], fv / S)) break;
-                            if (j == 0 && done[s] > 0 && !wait(sm.o_free[s], done[s] - 1)) break;
-                            issue_pv(fv, s, s, cnt[s], j == 0);
-                            if (!ok) break;
-                            warp_mma_commit(smem_u32(&sm.o_done[s]));
-                            ++cnt[s];
-                        }
-                        if (!ok) break;
-                        warp_mma_commit(smem_u32(&sm.empty[fv % S]));
                     }
+                    if (!ok) break;
                     for (int s = 0; s < ns; ++s) ++done[s];
                 } else {
                     // S runs one tile ahead: S(0), S(1), PV(0), S(2), PV(1), ...
@@ -791,6 +801,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const size_t tok = (size_t)x.tok0 + tok_first + row_tok;
             // no key from `limit` on is visible; without a mask all before it are
             const int limit = p.mask ? x.len : min(x.len, x.ctx + trow + 1);
+            // every row of the piece sees all keys before `open`
+            const int open = p.mask ? x.ctx : min(x.len, x.ctx + x.trow0 + 1);
             const uint32_t* words = p.mask
                 ? reinterpret_cast<const uint32_t*>(p.mask) + (valid ? tok : 0) * (2 * (size_t)p.words)
                 : nullptr;
@@ -806,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     if (!(ok = warp_wait(smem_u32(&sm.s_full[buf]), c & 1, stop, status))) break;
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_off + buf * 128;
-                    const bool ragged = key0 + BN > x.ctx;
+                    const bool ragged = key0 + BN > open;
                     // V rows past the length are whatever the page held, and a drafted V
                     // may be anything: both are mended before P is handed over (before the
                     // scores take up the registers; only once S(j) is there, so that the stage's
@@ -815,31 +827,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         const int fv = f + fifo_v<PAIR>(j, x.n);
                         if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
                             break;
-                        if (row < BN && key0 + row >= x.ctx) {
+                        if (row < BN && key0 + row >= open) {
+                            uint8_t* at = sm.kv[fv % S] + row * 128;
                             const bool past = key0 + row >= x.len;
 #pragma unroll 1
-                            for (int cb = 0; cb < C::kCols; ++cb) {
-                                uint4* at = reinterpret_cast<uint4*>(sm.kv[fv % S] + cb * (BN * 128) +
-                                                                     row * 128);
+                            for (int cb = 0; cb < C::kCols; ++cb, at += BN * 128) {
+                                // (chunks in an order of the row's own, which spreads the banks)
+                                uint4* line = reinterpret_cast<uint4*>(at);
+                                uint4 v[8];
+                                uint32_t bad = 0;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const int ch = (e + row) & 7;  // (spreads the banks)
-                                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                    if (!past) {
-                                        v = at[ch];
-                                        bool bad = false;
-                                        auto mend = [&](uint32_t& u) {
-                                            if (!finite_bf16(u)) { u &= 0xffff0000u; bad = true; }
-                                            if (!finite_bf16(u >> 16)) { u &= 0xffffu; bad = true; }
-                                        };
-                                        mend(v.x);
-                                        mend(v.y);
-                                        mend(v.z);
-                                        mend(v.w);
-                                        if (!bad) continue;
-                                        *reinterpret_cast<volatile int*>(&sm.poison) = 1;
-                                    }
-                                    at[ch] = v;
+                                for (int e = 0; e < 8; ++e) v[e] = line[(e + row) & 7];
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    bad |= not_finite(v[e].x) | not_finite(v[e].y) | not_finite(v[e].z) |
+                                           not_finite(v[e].w);
+                                if (past) {
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) line[(e + row) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                                } else if (bad) {
+                                    *reinterpret_cast<volatile int*>(&sm.poison) = 1;
+                                    uint16_t* value = reinterpret_cast<uint16_t*>(at);
+                                    for (int e = 0; e < 64; ++e)
+                                        if (!finite_bf16(value[e])) value[e] = 0;
                                 }
                             }
                             fence_proxy_async_smem();
@@ -1097,7 +1107,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             // a visible drafted V that is not finite: its weight is
                             // positive, so it adds itself
                             const int ps = p.cache.page_size;
-                            const int ka = max(x.ctx, x.k0 * BN);
+                            const int ka = max(open, x.k0 * BN);
                             const int kz = min(limit, (x.k0 + x.n) * BN);
                             for (int key = ka; key < kz; ++key) {
                                 if (p.mask && !(mask_bits(words, 2 * p.words, key - x.ctx) & 1u))

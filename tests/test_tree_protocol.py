@@ -128,34 +128,38 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 sim.pipe.append(("PV", (uid, buf, o, j, no % stages, 1, False)))
 
             if pair:
-                for j in range(n):
-                    fk, fv = f + 2 * j, f + 2 * j + 1
-                    yield from stage(fk)
-                    for s in range(ns):
-                        if cnt[s] > 0:
-                            while not sim.ready(f"o_done{s}", (cnt[s] - 1) & 1, cnt[s]):
-                                yield
-                        sim.pipe.append(("S", (uid, s, j, fk % stages)))
-                        sim.pipe.append(("commit", f"s_full{s}"))
-                    sim.pipe.append(("read", fk % stages))
-                    sim.pipe.append(("commit", f"empty{fk % stages}"))
-                    if j == n - 1:
-                        sim.pipe.append(("commit", "q_empty"))
-                    order = range(ns) if mistake != "pair_order" else reversed(range(ns))
+                for j in range(-1, n):
+                    fv, fk = f + 2 * j + 1, f + 2 * j + 2
+                    order = list(range(ns)) if mistake != "pair_order" else list(reversed(range(ns)))
                     for s in order:
-                        while not sim.ready(f"p_full{s}", cnt[s] & 1, cnt[s] + 1):
-                            yield
-                        if s == 0 or mistake == "pair_order":
-                            yield from stage(fv)
-                        if j == 0 and done[s] > 0:
-                            while not sim.ready(f"o_free{s}", (done[s] - 1) & 1, done[s]):
+                        if j >= 0:
+                            while not sim.ready(f"p_full{s}", cnt[s] & 1, cnt[s] + 1):
                                 yield
-                        yield from pv(fv, s, s, cnt[s], j, j == 0)
-                        sim.pipe.append(("commit", f"o_done{s}"))
-                        cnt[s] += 1
-                    sim.pipe.append(("read", fv % stages))
-                    sim.pipe.append(("commit", f"empty{fv % stages}"))
-                    yield
+                            if s == order[0]:
+                                yield from stage(fv)
+                            if j == 0 and done[s] > 0:
+                                while not sim.ready(f"o_free{s}", (done[s] - 1) & 1, done[s]):
+                                    yield
+                            yield from pv(fv, s, s, cnt[s], j, j == 0)
+                            if s == order[-1]:
+                                sim.pipe.append(("read", fv % stages))
+                                sim.pipe.append(("commit", f"empty{fv % stages}"))
+                            sim.pipe.append(("commit", f"o_done{s}"))
+                            cnt[s] += 1
+                        if j + 1 < n:
+                            if s == order[0]:
+                                yield from stage(fk)
+                            if cnt[s] > 0:
+                                while not sim.ready(f"o_done{s}", (cnt[s] - 1) & 1, cnt[s]):
+                                    yield
+                            sim.pipe.append(("S", (uid, s, j + 1, fk % stages)))
+                            sim.pipe.append(("commit", f"s_full{s}"))
+                            if s == order[-1]:
+                                sim.pipe.append(("read", fk % stages))
+                                sim.pipe.append(("commit", f"empty{fk % stages}"))
+                                if j + 1 == n - 1:
+                                    sim.pipe.append(("commit", "q_empty"))
+                        yield
                 for s in range(ns):
                     done[s] += 1
             else:
