@@ -56,21 +56,25 @@ __device__ __forceinline__ Scratch scratch_of(const fa_cache& c) {
 // Sum over the CTA's threads before this one, and the total.
 __device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    long long incl = x;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
+    auto warp_scan = [&](long long v) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    };
+    const long long incl = warp_scan(x);
     __syncthreads();  // (the last call's sums have been read)
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    long long before = 0;
-    total = 0;
-    for (int w = 0; w < kPlan / 32; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
+    if (warp == 0) {
+        const long long all = warp_scan(sums[lane]);
+        sums[lane] = all - sums[lane];
+        if (lane == 31) sums[32] = all;
     }
-    return before + incl - x;
+    __syncthreads();
+    total = sums[32];
+    return sums[warp] + incl - x;
 }
 
 // entry[i].z = first place in `taken` of entry i, for needs entry[i].x; returns
@@ -88,23 +92,28 @@ __device__ __forceinline__ long long place_needs(int4* entry, int n, long long* 
     return all;
 }
 
+// Free pages, four to a thread from page p0 on: a mask.  The first stretch is
+// looked up before the call knows how many it wants.
+__device__ __forceinline__ int free_pages(const fa_cache& c, long long p0) {
+    const long long p = p0 + threadIdx.x * 4;
+    int mask = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (p + e < c.pages && c.refs[p + e] == 0) mask |= 1 << e;
+    return mask;
+}
+
 // The `want` lowest free pages into taken[]; false when there are fewer.
-__device__ __forceinline__ bool take_pages(const fa_cache& c, int* taken, long long want,
+__device__ __forceinline__ bool take_pages(const fa_cache& c, int* taken, long long want, int mask,
                                            long long* sums) {
     long long have = 0;
     for (long long p0 = 0; p0 < c.pages && have < want; p0 += kPlan * 4) {
-        const long long p = p0 + threadIdx.x * 4;
-        int is_free[4], mine = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            is_free[e] = p + e < c.pages && c.refs[p + e] == 0;
-            mine += is_free[e];
-        }
-        long long total, at = have + block_scan(mine, sums, total);
+        if (p0 > 0) mask = free_pages(c, p0);
+        long long total, at = have + block_scan(__popc(mask), sums, total);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (is_free[e]) {
-                if (at < want) taken[at] = (int)(p + e);
+            if ((mask >> e) & 1) {
+                if (at < want) taken[at] = (int)(p0 + threadIdx.x * 4 + e);
                 ++at;
             }
         have += total;
@@ -124,12 +133,13 @@ __device__ __forceinline__ int length_of(const fa_cache& c, int slot) {
 __global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const int* slots,
                                                         const int* counts, int count, int n) {
     pdl_begin();
-    __shared__ long long sums[kPlan / 32];
+    __shared__ long long sums[kPlan / 32 + 1];
     __shared__ int error;
     const Scratch s = scratch_of(c);
     if (threadIdx.x == 0) error = 0;
     for (int i = threadIdx.x; i < n; i += kPlan)
         if (slot_ok(c, slots[i])) s.mark[slots[i]] = -1;
+    const int free_mask = free_pages(c, 0);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlan) {
         const int slot = slots[i], m = counts ? counts[i] : count;
@@ -155,7 +165,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const 
     }
     __syncthreads();
     const long long want = place_needs(s.entry, n, sums);
-    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, sums)))
+    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, free_mask, sums)))
         if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
     __syncthreads();
     if (error) {
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const 
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, const int* parents,
                                                           const int* children, int n) {
     pdl_begin();
-    __shared__ long long sums[kPlan / 32];
+    __shared__ long long sums[kPlan / 32 + 1];
     __shared__ int error;
     const Scratch s = scratch_of(c);
     if (threadIdx.x == 0) error = 0;
@@ -187,6 +197,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
         if (slot_ok(c, children[i])) s.mark[children[i]] = -1;
         if (slot_ok(c, parents[i])) s.mark[parents[i]] = -1;
     }
+    const int free_mask = free_pages(c, 0);
     __syncthreads();
     // a warp an entry
     for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
@@ -217,7 +228,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
         if (slot_ok(c, parents[i]) && s.mark[parents[i]] != -1) atomicOr(&error, kCacheBadSlot);
     __syncthreads();
     const long long want = place_needs(s.entry, n, sums);
-    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, sums)))
+    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, free_mask, sums)))
         if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -250,7 +261,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
 
 // Copies the first rows of a page to another page: entry (source page,
 // destination page, rows).
-__global__ void __launch_bounds__(256) fork_copy_kernel(const fa_cache c) {
+__global__ void __launch_bounds__(256, 4) fork_copy_kernel(const fa_cache c) {
     pdl_begin();
     const Scratch s = scratch_of(c);
     if (!*s.go) return;
@@ -333,11 +344,12 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
     __syncthreads();
     for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp an entry
         const int slot = slots[i], lane = threadIdx.x & 31;
-        int bad = 0, len = -1, used = 0, fresh = 0;
+        int bad = 0, len = -1, used = 0;
+        bool fresh = false;
         if (slot_ok(c, slot)) {
-            if (lane == 0) fresh = atomicCAS(&s.mark[slot], -1, i) == -1;
-            fresh = __shfl_sync(0xffffffffu, fresh, 0);
             len = length_of(c, slot);
+            if (lane == 0) fresh = atomicCAS(&s.mark[slot], -1, i) == -1;
+            fresh = __any_sync(0xffffffffu, fresh);
         }
         const int b = base[i], m = accepted[i];
         if (!fresh) bad = kCacheBadSlot;
@@ -384,37 +396,50 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
 // V.  path ascends strictly, so path[j] >= j: a thread owns its 16 bytes of a
 // row and walks j upward in runs, reading a run's rows before it writes them;
 // what it has written lies below every row still to be read.
-constexpr int kRun = 8;
-__global__ void __launch_bounds__(128) accept_move_kernel(const fa_cache c, const int* slots,
-                                                          const int* base, const int* path,
-                                                          int width, const int* accepted) {
+// The rows' places are the same in all layers: a CTA takes kMoveLayers of them.
+constexpr int kRun = 8, kMoveLayers = 4, kMoveThreads = 128;
+__global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const fa_cache c, const int* slots,
+                                                                   const int* base, const int* path,
+                                                                   int width, const int* accepted) {
     pdl_begin();
     const Scratch s = scratch_of(c);
+    const int i = blockIdx.x;
     if (!*s.go) return;
-    const int i = blockIdx.x, m = accepted[i], b = base[i];
+    const int m = accepted[i], b = base[i];
     const int* pages = s.shadow + (long long)slots[i] * c.max_pages;
     const int* at = path + (long long)i * width;
-    const int layer = blockIdx.y >> 1;
+    const int first = (blockIdx.y >> 1) * kMoveLayers, last = min(first + kMoveLayers, c.layers);
     uint4* data = static_cast<uint4*>(blockIdx.y & 1 ? c.v : c.k);
-    const int row16 = c.d / 8;
-    const long long plane = (long long)c.page_size * row16;
-    auto row_of = [&](int tok, int head) {
-        return data + (((long long)layer * c.pages + pages[tok / c.page_size]) * c.heads + head) * plane +
-               (long long)(tok % c.page_size) * row16;
-    };
-    for (int x = threadIdx.x; x < c.heads * row16; x += blockDim.x) {
+    const int row16 = c.d / 8;                                     // 16-byte units of a row
+    const unsigned plane = (unsigned)c.page_size * row16;          // of a head in a page
+    const long long layer_units = (long long)c.pages * c.heads * plane;
+    for (int x = threadIdx.x; x < c.heads * row16; x += kMoveThreads) {
         const int head = x / row16, col = x - head * row16;
+        auto place = [&](int tok) {
+            return ((long long)pages[tok / c.page_size] * c.heads + head) * plane +
+                   (unsigned)(tok % c.page_size) * row16 + col;
+        };
         for (int j0 = 0; j0 < m; j0 += kRun) {
-            uint4 v[kRun];
-            int src[kRun];
+            long long from[kRun], to[kRun];                        // from < 0: stays
 #pragma unroll
             for (int u = 0; u < kRun; ++u) {
-                src[u] = j0 + u < m ? at[j0 + u] : j0 + u;
-                if (src[u] != j0 + u) v[u] = row_of(b + src[u], head)[col];
+                const int j = j0 + u, t = j < m ? at[j] : j;
+                from[u] = -1;
+                if (t != j) {
+                    from[u] = place(b + t);
+                    to[u] = place(b + j);
+                }
             }
+            for (int layer = first; layer < last; ++layer) {
+                uint4* rows = data + layer * layer_units;
+                uint4 v[kRun];
 #pragma unroll
-            for (int u = 0; u < kRun; ++u)
-                if (src[u] != j0 + u) row_of(b + j0 + u, head)[col] = v[u];
+                for (int u = 0; u < kRun; ++u)
+                    if (from[u] >= 0) v[u] = rows[from[u]];
+#pragma unroll
+                for (int u = 0; u < kRun; ++u)
+                    if (from[u] >= 0) rows[to[u]] = v[u];
+            }
         }
     }
 }
@@ -505,7 +530,8 @@ fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* ba
                                      base, path, path_width, accepted, n);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     if (path_width == 0) return FA_OK;
-    return launched(launch_pdl(accept_move_kernel, dim3(n, cache->layers * 2), dim3(128), 0, strm,
+    return launched(launch_pdl(accept_move_kernel, dim3(n, cdiv(cache->layers, kMoveLayers) * 2),
+                               dim3(kMoveThreads), 0, strm,
                                *cache, slots, base, path, path_width, accepted));
 }
 
