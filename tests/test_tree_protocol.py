@@ -12,6 +12,9 @@ Layouts modelled:
   store half of the columns each, over both O (d <= 128).
 - one: one row tile, one stream over two S buffers and one O; the second
   warpgroup only stores (d > 128).
+- sep (alternate-sep, pair-sep; d = 64): P in TMEM columns of its own, so that a
+  stream's next scores are issued without waiting for its last PV; the softmax
+  waits for that PV before it writes the next P.
 - pair: two row tiles that share every key tile, one stream each (d <= 128,
   more than 128 rows); the second may have no rows.
 
@@ -36,6 +39,8 @@ def fifo_v(pair, j, n):
 
 def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
     """pieces: list of (n key tiles, row tiles, first ragged tile)."""
+    sep = layout.endswith("-sep")
+    layout = layout.replace("-sep", "")
     pair, streams = layout == "pair", 1 if layout == "one" else 2
     sim = Sim(pieces, seed, consumers=2 + 2 * warps)
     for b in (0, 1):
@@ -149,7 +154,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                         if j + 1 < n:
                             if s == order[0]:
                                 yield from stage(fk)
-                            if cnt[s] > 0:
+                            if cnt[s] > 0 and not sep:
                                 while not sim.ready(f"o_done{s}", (cnt[s] - 1) & 1, cnt[s]):
                                     yield
                             sim.pipe.append(("S", (uid, s, j + 1, fk % stages)))
@@ -167,7 +172,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                     fk, b = f + fifo_k(False, j), j & 1
                     yield from stage(fk)
                     c = cnt[b] + (j >> 1)
-                    if c > 0 and mistake != "no_s_wait":
+                    if c > 0 and not sep and mistake != "no_s_wait":
                         while not sim.ready(f"o_done{b}", (c - 1) & 1, c):
                             yield
                     sim.pipe.append(("S", (uid, b, j, fk % stages)))
@@ -238,6 +243,9 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 yield
                 if st["S"].get(b) != (uid, j):
                     raise Hazard("S overwritten while the softmax read it")
+                if sep and c > 0 and mistake != "no_p_free_wait":
+                    while not sim.ready(f"o_done{b}", (c - 1) & 1, c):
+                        yield
                 if seen and sim.rnd.random() < 0.3:  # rescale O
                     o = w if pair else (b if streams == 2 else 0)
                     if streams == 1 and mistake != "no_rescale_wait":
@@ -249,6 +257,10 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                         raise Hazard(f"rescale of ({uid},{j}) saw O = {st['O'][o]}")
                 for hf, bar in ((0, "p_full"), (1, "p_hi")):
                     yield
+                    if st["S"].get(b) != (uid, j):
+                        raise Hazard("S overwritten while the softmax read it")
+                    if sep and st["P"].get((b, hf), {}).get(q, "read") != "read":
+                        raise Hazard(f"P of ({uid},{j}) written over one not yet read")
                     st["P"].setdefault((b, hf), {})[q] = (uid, j)
                     sim.bars[f"{bar}{b}"].arrive((uid, j))
                 seen.append(j)
@@ -306,6 +318,8 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
             if smem.get("q") != uid or smem.get(f"kv{s}") != ("k", uid, j):
                 raise Hazard(f"S ({uid},{j}) read Q {smem.get('q')}, K {smem.get(f'kv{s}')}")
             for hf in (0, 1):
+                if sep:
+                    continue
                 if any(v != "read" for v in st["P"].get((b, hf), {}).values()):
                     raise Hazard(f"S ({uid},{j}) overwrote P before PV read it")
                 st["P"][(b, hf)] = {}
@@ -335,12 +349,13 @@ def random_pieces(rnd, layout):
     pieces = []
     for _ in range(rnd.randint(0, 7)):
         n = rnd.choice([1, 1, 2, 2, 3, 4, 5, 8])
-        pieces.append((n, rnd.choice([1, 2, 2]) if layout == "pair" else 1,
+        pieces.append((n, rnd.choice([1, 2, 2]) if layout.startswith("pair") else 1,
                        rnd.choice([0, n - 1, n, max(0, n - 2)])))
     return pieces
 
 
-LAYOUTS = [("alternate", 5), ("alternate", 8), ("one", 4), ("one", 7), ("pair", 4), ("pair", 8)]
+LAYOUTS = [("alternate", 5), ("alternate", 8), ("one", 4), ("one", 7), ("pair", 4), ("pair", 8),
+           ("alternate-sep", 8), ("pair-sep", 8)]
 
 
 @pytest.mark.parametrize("warps", [1, 4])
@@ -351,15 +366,18 @@ def test_protocol_is_hazard_and_deadlock_free(layout, stages, warps):
                    warps=warps)
 
 
-# True: the model must catch it; False: another wait implies it (an in-order
-# tensor pipe runs S after the PV that read the P it overwrites, which the
-# kernel does not rely on).
+# True: the model must catch it; False: another wait implies it (in an in-order
+# tensor pipe S runs after the PVs issued before it, so that the P it overwrites,
+# or the P before the one it leads to, has been read; the kernel does not rely on
+# that order).
 MISTAKES = [
     ("alternate", 5, "no_empty_wait", True), ("alternate", 5, "no_q_empty_wait", True),
     ("alternate", 5, "no_p_hi_wait", True), ("alternate", 5, "no_o_free_wait", True),
     ("alternate", 5, "no_s_wait", False), ("alternate", 5, "no_mend", True),
     ("alternate", 5, "no_mend_wait", True), ("alternate", 5, "one_stat_buffer", True),
     ("one", 4, "no_rescale_wait", True), ("one", 4, "no_o_free_wait", True),
+    ("alternate-sep", 8, "no_p_free_wait", False), ("pair-sep", 8, "no_p_free_wait", False),
+    ("alternate-sep", 8, "no_p_hi_wait", True),
     ("pair", 4, "pair_order", True), ("pair", 4, "no_empty_wait", True),
 ]
 
