@@ -305,7 +305,8 @@ class PagedCache:
     an empty cache.  Lists of slots are int32 tensors on the device; nothing synchronises.
     What is wrong in them (a slot out of range or named twice, too long a sequence, no free
     pages, a shared page that would be written) is found on the device: the call then changes
-    nothing, and `check` raises.  Calls on one cache must be ordered on one stream.
+    nothing, and `check` raises.  Page operations on one cache must be ordered on one stream,
+    and appends and attention ordered behind those whose rows they touch.
     """
 
     def __init__(self, k, v, table, lengths, refs):

@@ -328,8 +328,10 @@ fa_status fa_rotary(const void* q, void* q_out, int Hq, long long q_token_stride
  * only partly filled belongs to one sequence.  The caller owns every array;
  * the calls below keep them consistent.
  *
- * All calls on one cache belong to one stream order (a graph replay included):
- * they share the scratch words.  Lists of slots are device arrays.  What is
+ * Page operations (reserve, fork, free, accept) on one cache belong to one
+ * stream order, a graph replay included: they share the scratch words.  Appends
+ * and attention belong behind the operations whose rows they touch, and may
+ * run at the same time as one another.  Lists of slots are device arrays.  What is
  * wrong in them is found on the device: a call on pages then changes nothing
  * at all, and the status word in scratch keeps the reason until fa_cache_check
  * reads it:

@@ -528,3 +528,85 @@ def test_a_drafted_step():
     cache.free(ints([0, 1, 2, 3, 4]))
     cache.check()
     assert not cache.refs.any() and cache.table.eq(-1).all()
+
+
+@pytest.mark.gpu
+def test_far_pages():
+    """Pages whose offsets pass 2^31 elements, written, attended to, copied and moved."""
+    heads, d, ps, pages = 8, 256, 128, 8200       # 2^18 elements a page
+    cache = fa.PagedCache.allocate(1, pages, heads, ps, d, 3, 4)
+    far = [pages - 1, pages - 2, pages - 3]
+    cache.refs[:pages - 3] = 1                    # (so that new pages are far ones)
+    g = torch.Generator().manual_seed(1)
+    n = 150
+    cache.reserve(ints([0]), n)
+    assert cache.table[0, :2].tolist() == [pages - 3, pages - 2]
+    k, v = (torch.randn(n, heads, d, generator=g).bfloat16().cuda() for _ in range(2))
+    fa.cache_append(cache, 0, ints([0]), k, v)
+    q = queries(n, heads, d)
+    o, lse = fa.tree_attention(q, cache, 0, ints([0]))
+    pick = [0, 1, 128, 149]
+    ro, rl, bo, bl = attend(f64(q)[pick], f64(k), f64(v), visible(n, n)[pick], d ** -0.5)
+    within("o", f64(o)[pick], ro, bo)
+    within("lse", f64(lse)[:, pick], rl, bl)
+    cache.fork(ints([0]), ints([2]))
+    assert cache.table[2, :2].tolist() == [pages - 3, far[0]]
+    assert torch.equal(cache.k[0, far[0], :, :n - 128], cache.k[0, far[1], :, :n - 128])
+    cache.accept(ints([2]), ints([129]), ints([[0, 20]]), ints([2]))
+    assert torch.equal(cache.v[0, far[0], :, 2], v[149])
+    cache.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [5, 64, 5000])
+def test_a_bound_far_above_the_tokens(N):
+    """max_seqlen may be any bound: row tiles larger than the whole batch, masks with spare words."""
+    h = Held([40, 133], 2, 64, 16, seed=5)
+    q = queries(7, 2, 64)
+    check(h, [2, 5], q, run(h, q, [2, 5], N=N))
+    rows = [[0], [1], [0], [0, 1], [2], [1, 3], [4]]
+    mask = words_of(rows, -(-N // 64))
+    got = fa.tree_attention(q, h.cache, h.layer, ints(h.slots), mask=mask, cu_seqlens=ints([0, 2, 7]),
+                            max_seqlen=N)
+    check(h, [2, 5], q, got, rows)
+
+
+@pytest.mark.gpu
+def test_calls_back_to_back():
+    """Calls of different shapes on one workspace, one after the other without waiting: what one
+    leaves in it does not reach the next."""
+    a = Held([3000, 900], 2, 128, 64, seed=1, layers=1, layer=0)
+    b = Held([70, 5, 4100, 260], 1, 64, 16, seed=2, layers=1, layer=0)
+    qa, qb = queries(2, 16, 128), queries(120, 4, 64)
+    ws = torch.full((64 << 20,), 255, dtype=torch.uint8).cuda()
+    ra = run(a, qa, [1, 1], dense=True)
+    rb = fa.tree_attention(qb, b.cache, 0, ints(b.slots))
+    outs = []
+    for _ in range(20):
+        outs.append((fa.tree_attention(qa, a.cache, 0, ints(a.slots), workspace=ws), ra))
+        outs.append((fa.tree_attention(qb, b.cache, 0, ints(b.slots), workspace=ws), rb))
+    for got, ref in outs:
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    a.cache.check()
+    # sequence 1 of b holds fewer tokens than the call's 30: reported, and its rows see nothing
+    with pytest.raises(fa.FAError, match="does not fit"):
+        b.cache.check()
+    assert not rb[0][30:60].any()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Two streams read one cache at the same time."""
+    h = Held([5000, 77, 3000, 900], 2, 128, 16, seed=3, layers=1, layer=0)
+    q = queries(4, 8, 128)
+    s = ints(h.slots)
+    ref = fa.tree_attention(q, h.cache, 0, s)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for x in streams:
+        x.wait_stream(torch.cuda.current_stream())
+    outs = [fa.tree_attention(q, h.cache, 0, s, stream=x) for _ in range(10) for x in streams]
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
+    check(h, [1] * 4, q, ref)
+    h.cache.check()
