@@ -68,12 +68,16 @@ struct Cfg {
     static constexpr int kMaxStages = kRoom / kStageBytes;
     static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
     static constexpr int kStreams = D > 128 ? 1 : 2;     // O accumulators
-    // d = 64 leaves TMEM for P in columns of its own, so that the next scores of a
-    // stream need not wait until PV has read the P of the last ones (decoding 64
-    // sequences of 4-8k tokens, 8 kv heads of 64: 154 -> 146 us).
-    static constexpr bool kSepP = D == 64;
-    static constexpr int kOStep = kSepP ? 64 : 128;      // columns from O_0 to O_1
-    static constexpr int kPCol = kSepP ? 384 : 0, kPStep = kSepP ? 64 : 128;
+    // d = 64 and d > 128 leave TMEM for P in columns of its own (behind two O of 64
+    // columns, or between the S buffers of 64), so that the next scores need not
+    // wait until PV has read the P of those two tiles before (decoding 64 sequences
+    // of 4-8k tokens, 8 kv heads of 64: 154 -> 146 us; 2048-token chunks over 4-6k
+    // keys, d = 256: 392 -> 367 us).
+    static constexpr bool kSepP = D != 128;
+    // scores of a row held in registers: 64 of them, or where the tensor core is the bound
+    static constexpr bool kWhole = PAIR || kBN == 64;
+    static constexpr int kOStep = D == 64 ? 64 : 128;    // columns from O_0 to O_1
+    static constexpr int kPCol = D == 64 ? 384 : (kSepP ? 64 : 0), kPStep = D == 64 ? 64 : 128;
     static_assert(kStages >= 4, "the ring holds two K and two V tiles");
     static_assert(!PAIR || D <= 128, "two row tiles need two O accumulators");
 };
@@ -884,9 +888,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         else if (room < 32) bits &= (1u << room) - 1u;
                         return bits;
                     };
-                    float s[PAIR ? BN : 1];
-                    if constexpr (PAIR) {
-                        // tensor-bound: the whole row in registers, all loads in flight
+                    float s[C::kWhole ? BN : 1];
+                    if constexpr (C::kWhole) {
+                        // the whole row in registers, all loads in flight
                         if (warp_valid) {
                             uint32_t r[BN / 32][32];
 #pragma unroll
@@ -989,7 +993,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         }
                     }
                     uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                    if constexpr (PAIR) {
+                    if constexpr (C::kWhole) {
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             if (warp_valid) {

@@ -12,7 +12,7 @@ Layouts modelled:
   store half of the columns each, over both O (d <= 128).
 - one: one row tile, one stream over two S buffers and one O; the second
   warpgroup only stores (d > 128).
-- sep (alternate-sep, pair-sep; d = 64): P in TMEM columns of its own, so that a
+- sep (alternate-sep and pair-sep, d = 64; one-sep, d > 128): P in TMEM columns of its own, so that a
   stream's next scores are issued without waiting for its last PV; the softmax
   waits for that PV before it writes the next P.
 - pair: two row tiles that share every key tile, one stream each (d <= 128,
@@ -355,7 +355,7 @@ def random_pieces(rnd, layout):
 
 
 LAYOUTS = [("alternate", 5), ("alternate", 8), ("one", 4), ("one", 7), ("pair", 4), ("pair", 8),
-           ("alternate-sep", 8), ("pair-sep", 8)]
+           ("alternate-sep", 8), ("pair-sep", 8), ("one-sep", 4), ("one-sep", 7)]
 
 
 @pytest.mark.parametrize("warps", [1, 4])
@@ -377,6 +377,7 @@ MISTAKES = [
     ("alternate", 5, "no_mend_wait", True), ("alternate", 5, "one_stat_buffer", True),
     ("one", 4, "no_rescale_wait", True), ("one", 4, "no_o_free_wait", True),
     ("alternate-sep", 8, "no_p_free_wait", False), ("pair-sep", 8, "no_p_free_wait", False),
+    ("one-sep", 4, "no_p_free_wait", False), ("one-sep", 4, "no_rescale_wait", True),
     ("alternate-sep", 8, "no_p_hi_wait", True),
     ("pair", 4, "pair_order", True), ("pair", 4, "no_empty_wait", True),
 ]
