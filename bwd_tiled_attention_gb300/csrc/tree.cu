@@ -675,24 +675,31 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             constexpr uint32_t idS = make_idesc_bf16(128, BN, false, false);
             constexpr uint32_t idPV = make_idesc_bf16(128, D, false, true);
             int it = 0, f = 0;
+            const uint32_t lead = elect_lead();
             int cnt[2] = {0, 0};  // tiles through each S buffer
             int done[2] = {0, 0}; // PAIR: pieces of each stream
             bool ok = true;
+            // A tile that is nearly always there is looked up beside an earlier wait (a wait
+            // costs ~140 cycles even when nothing is missing).  The place S before it has been
+            // consumed by then, so that the parity tells.
+            auto there = [&](int place) {
+                return mbar_test_wait(smem_u32(&sm.full[place % S]), (place / S) & 1);
+            };
             auto wait = [&](uint64_t& bar, int n) {
                 return ok = ok && warp_wait(smem_u32(&bar), n & 1, stop, status);
             };
             auto issue_s = [&](int stage_no, int buf, int qt) {
-                const uint64_t da = make_sdesc_here(smem_u32(sm.q[qt]), 16, 1024);
-                const uint64_t db = make_sdesc_here(smem_u32(sm.kv[stage_no % S]), 16, 1024);
+                const uint64_t da = make_sdesc(smem_u32(sm.q[qt]), 16, 1024);
+                const uint64_t db = make_sdesc(smem_u32(sm.kv[stage_no % S]), 16, 1024);
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk)
-                    warp_mma_ss(tmem + buf * 128, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
+                    warp_mma_ss(lead, tmem + buf * 128, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
                            sdesc_add(db, (kk >> 2) * (BN * 128) + (kk & 3) * 32), idS, kk > 0);
             };
             auto issue_pv = [&](int stage_no, int buf, int o, int c, bool first) {
                 // keys [0, BN/2) of P, then the others once the softmax has them
-                const uint64_t db = make_sdesc_here(smem_u32(sm.kv[stage_no % S]), BN * 128, 1024);
+                const uint64_t db = make_sdesc(smem_u32(sm.kv[stage_no % S]), BN * 128, 1024);
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk) {
@@ -700,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         if (!wait(sm.p_hi[buf], c)) return;
                         tc_fence_after();
                     }
-                    warp_mma_ts(tmem + 256 + o * C::kOStep, tmem + C::kPCol + buf * C::kPStep + kk * 8,
+                    warp_mma_ts(lead, tmem + 256 + o * C::kOStep, tmem + C::kPCol + buf * C::kPStep + kk * 8,
                                 sdesc_add(db, kk * 2048), idPV, (first && kk == 0) ? 0u : 1u);
                 }
             };
@@ -720,27 +727,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     const int ns = nt > p.tile_tokens ? 2 : 1;
                     for (int j = -1; j < n && ok; ++j) {
                         const int fv = f + 2 * j + 1, fk = fv + 1;  // V(j), K(j + 1)
+                        const bool v_in = j >= 0 && there(fv), k_in = j + 1 < n && there(fk);
                         for (int s = 0; s < ns && ok; ++s) {
                             if (j >= 0) {
                                 // (stream 0 mends V before its P is ready, so both may follow it)
                                 if (!wait(sm.p_full[s], cnt[s])) break;
-                                if (s == 0 && !wait(sm.full[fv % S], fv / S)) break;
+                                if (s == 0 && !v_in && !wait(sm.full[fv % S], fv / S)) break;
                                 if (j == 0 && done[s] > 0 && !wait(sm.o_free[s], done[s] - 1)) break;
                                 issue_pv(fv, s, s, cnt[s], j == 0);
                                 if (!ok) break;
-                                if (s == ns - 1) warp_mma_commit(smem_u32(&sm.empty[fv % S]));
-                                warp_mma_commit(smem_u32(&sm.o_done[s]));
+                                if (s == ns - 1) warp_mma_commit(lead, smem_u32(&sm.empty[fv % S]));
+                                warp_mma_commit(lead, smem_u32(&sm.o_done[s]));
                                 ++cnt[s];
                             }
                             if (j + 1 < n) {
-                                if (s == 0 && !wait(sm.full[fk % S], fk / S)) break;
+                                if (s == 0 && !k_in && !wait(sm.full[fk % S], fk / S)) break;
                                 // S_s is free once the P written over it has been read
                                 if (!C::kSepP && cnt[s] > 0 && !wait(sm.o_done[s], cnt[s] - 1)) break;
                                 issue_s(fk, s, s);
-                                warp_mma_commit(smem_u32(&sm.s_full[s]));
+                                warp_mma_commit(lead, smem_u32(&sm.s_full[s]));
                                 if (s == ns - 1) {
-                                    warp_mma_commit(smem_u32(&sm.empty[fk % S]));
-                                    if (j + 1 == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
+                                    warp_mma_commit(lead, smem_u32(&sm.empty[fk % S]));
+                                    if (j + 1 == n - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty));
                                 }
                             }
                         }
@@ -749,29 +757,33 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                     for (int s = 0; s < ns; ++s) ++done[s];
                 } else {
                     // S runs one tile ahead: S(0), S(1), PV(0), S(2), PV(1), ...
+                    bool k_in = false;
                     auto do_s = [&](int j) {
                         const int fk = f + fifo_k<false>(j), bf = j & 1;
-                        if (!wait(sm.full[fk % S], fk / S)) return;
+                        if (!k_in && !wait(sm.full[fk % S], fk / S)) return;
+                        k_in = false;
                         // the buffer's P of two tiles ago has been read
                         const int c = cnt[bf] + (j >> 1);
                         if (!C::kSepP && c > 0 && !wait(sm.o_done[bf], c - 1)) return;
                         issue_s(fk, bf, 0);
-                        warp_mma_commit(smem_u32(&sm.empty[fk % S]));
-                        warp_mma_commit(smem_u32(&sm.s_full[bf]));
-                        if (j == n - 1) warp_mma_commit(smem_u32(&sm.q_empty));
+                        warp_mma_commit(lead, smem_u32(&sm.empty[fk % S]));
+                        warp_mma_commit(lead, smem_u32(&sm.s_full[bf]));
+                        if (j == n - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty));
                     };
                     for (int j = -2; j < n && ok; ++j) {
                         if (j >= 0) {
                             const int fv = f + fifo_v<false>(j, n), bf = j & 1;
                             const int c = cnt[bf] + (j >> 1);
+                            const bool v_in = there(fv);
+                            k_in = j + 2 < n && there(f + fifo_k<false>(j + 2));
                             if (!wait(sm.p_full[bf], c)) break;
-                            if (!wait(sm.full[fv % S], fv / S)) break;
+                            if (!v_in && !wait(sm.full[fv % S], fv / S)) break;
                             if (j == 0 && it > 0 && !wait(sm.o_free[0], it - 1)) break;
                             issue_pv(fv, bf, C::kStreams == 2 ? bf : 0, c,
                                      C::kStreams == 2 ? j < 2 : j == 0);
                             if (!ok) break;
-                            warp_mma_commit(smem_u32(&sm.empty[fv % S]));
-                            warp_mma_commit(smem_u32(&sm.o_done[bf]));
+                            warp_mma_commit(lead, smem_u32(&sm.empty[fv % S]));
+                            warp_mma_commit(lead, smem_u32(&sm.o_done[bf]));
                         }
                         if (j + 2 < n) do_s(j + 2);
                     }
@@ -782,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 f += 2 * n;
                 ++it;
             }
-            warp_mma_commit(smem_u32(&sm.drain));
+            warp_mma_commit(lead, smem_u32(&sm.drain));
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         }
     } else if (warp >= 4) {

@@ -125,6 +125,9 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 while not sim.ready(f"full{no % stages}", (no // stages) & 1, no // stages + 1):
                     yield
 
+            def there(no):  # a look, without waiting
+                return sim.ready(f"full{no % stages}", (no // stages) & 1, no // stages + 1)
+
             def pv(no, buf, o, c, j, first):
                 sim.pipe.append(("PV", (uid, buf, o, j, no % stages, 0, first)))
                 if mistake != "no_p_hi_wait":
@@ -135,12 +138,13 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
             if pair:
                 for j in range(-1, n):
                     fv, fk = f + 2 * j + 1, f + 2 * j + 2
+                    v_in, k_in = j >= 0 and there(fv), j + 1 < n and there(fk)
                     order = list(range(ns)) if mistake != "pair_order" else list(reversed(range(ns)))
                     for s in order:
                         if j >= 0:
                             while not sim.ready(f"p_full{s}", cnt[s] & 1, cnt[s] + 1):
                                 yield
-                            if s == order[0]:
+                            if s == order[0] and not v_in:
                                 yield from stage(fv)
                             if j == 0 and done[s] > 0:
                                 while not sim.ready(f"o_free{s}", (done[s] - 1) & 1, done[s]):
@@ -152,7 +156,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                             sim.pipe.append(("commit", f"o_done{s}"))
                             cnt[s] += 1
                         if j + 1 < n:
-                            if s == order[0]:
+                            if s == order[0] and not k_in:
                                 yield from stage(fk)
                             if cnt[s] > 0 and not sep:
                                 while not sim.ready(f"o_done{s}", (cnt[s] - 1) & 1, cnt[s]):
@@ -168,9 +172,10 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 for s in range(ns):
                     done[s] += 1
             else:
-                def do_s(j):
+                def do_s(j, k_in=False):
                     fk, b = f + fifo_k(False, j), j & 1
-                    yield from stage(fk)
+                    if not k_in:
+                        yield from stage(fk)
                     c = cnt[b] + (j >> 1)
                     if c > 0 and not sep and mistake != "no_s_wait":
                         while not sim.ready(f"o_done{b}", (c - 1) & 1, c):
@@ -188,9 +193,13 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 for j in range(n):
                     fv, b = f + fifo_v(False, j, n), j & 1
                     c = cnt[b] + (j >> 1)
+                    ahead = j + 3 if mistake == "early_look" else j + 2
+                    v_in = there(fv)
+                    k_in = j + 2 < n and there(f + fifo_k(False, ahead))
                     while not sim.ready(f"p_full{b}", c & 1, c + 1):
                         yield
-                    yield from stage(fv)
+                    if not v_in:
+                        yield from stage(fv)
                     if j == 0 and it > 0 and mistake != "no_o_free_wait":
                         while not sim.ready("o_free0", (it - 1) & 1, it):
                             yield
@@ -200,7 +209,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                     sim.pipe.append(("commit", f"empty{fv % stages}"))
                     sim.pipe.append(("commit", f"o_done{b}"))
                     if j + 2 < n:
-                        yield from do_s(j + 2)
+                        yield from do_s(j + 2, k_in)
                 cnt[0] += (n + 1) // 2
                 cnt[1] += n // 2
             f += 2 * n
@@ -375,6 +384,7 @@ MISTAKES = [
     ("alternate", 5, "no_p_hi_wait", True), ("alternate", 5, "no_o_free_wait", True),
     ("alternate", 5, "no_s_wait", False), ("alternate", 5, "no_mend", True),
     ("alternate", 5, "no_mend_wait", True), ("alternate", 5, "one_stat_buffer", True),
+    ("alternate", 5, "early_look", True),
     ("one", 4, "no_rescale_wait", True), ("one", 4, "no_o_free_wait", True),
     ("alternate-sep", 8, "no_p_free_wait", False), ("pair-sep", 8, "no_p_free_wait", False),
     ("one-sep", 4, "no_p_free_wait", False), ("one-sep", 4, "no_rescale_wait", True),
