@@ -193,9 +193,8 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 for j in range(n):
                     fv, b = f + fifo_v(False, j, n), j & 1
                     c = cnt[b] + (j >> 1)
-                    ahead = j + 3 if mistake == "early_look" else j + 2
                     v_in = there(fv)
-                    k_in = j + 2 < n and there(f + fifo_k(False, ahead))
+                    k_in = j + 2 < n and (mistake == "no_k_wait" or there(f + fifo_k(False, j + 2)))
                     while not sim.ready(f"p_full{b}", c & 1, c + 1):
                         yield
                     if not v_in:
@@ -384,7 +383,7 @@ MISTAKES = [
     ("alternate", 5, "no_p_hi_wait", True), ("alternate", 5, "no_o_free_wait", True),
     ("alternate", 5, "no_s_wait", False), ("alternate", 5, "no_mend", True),
     ("alternate", 5, "no_mend_wait", True), ("alternate", 5, "one_stat_buffer", True),
-    ("alternate", 5, "early_look", True),
+    ("alternate", 5, "no_k_wait", True),
     ("one", 4, "no_rescale_wait", True), ("one", 4, "no_o_free_wait", True),
     ("alternate-sep", 8, "no_p_free_wait", False), ("pair-sep", 8, "no_p_free_wait", False),
     ("one-sep", 4, "no_p_free_wait", False), ("one-sep", 4, "no_rescale_wait", True),
