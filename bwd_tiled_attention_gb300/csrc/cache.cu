@@ -130,25 +130,52 @@ __device__ __forceinline__ int length_of(const fa_cache& c, int slot) {
     return n < 0 || n > (long long)c.max_pages * c.page_size ? -1 : n;
 }
 
+// The planning CTA's threads by entry: groups of g lanes, as many as put all
+// entries to work at once (32 lanes for up to 32 entries, 4 for 256 and more).
+struct Groups {
+    int g, sub, entry, stride;
+    unsigned mask;
+    __device__ __forceinline__ explicit Groups(int n) {
+        g = 32;
+        while (g > 4 && n * g > kPlan) g >>= 1;
+        sub = threadIdx.x & (g - 1);
+        entry = threadIdx.x / g;
+        stride = kPlan / g;
+        mask = g == 32 ? 0xffffffffu : ((1u << g) - 1u) << (threadIdx.x & 31 & ~(g - 1));
+    }
+    __device__ __forceinline__ bool any(bool x) const { return __ballot_sync(mask, x) != 0; }
+    __device__ __forceinline__ int first(int x) const { return __shfl_sync(mask, x, 0, g); }
+};
+
+// Lists of up to kPlan entries and kFew pages stay in shared memory.
+constexpr int kFew = 2048;
+struct PlanSmem {
+    long long sums[kPlan / 32 + 1];
+    int4 entry[kPlan];
+    int taken[kFew];
+    int error;
+};
+
 __global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const int* slots,
                                                         const int* counts, int count, int n) {
     pdl_begin();
-    __shared__ long long sums[kPlan / 32 + 1];
-    __shared__ int error;
+    __shared__ PlanSmem sm;
     const Scratch s = scratch_of(c);
-    if (threadIdx.x == 0) error = 0;
+    int4* entry = n <= kPlan ? sm.entry : s.entry;
+    if (threadIdx.x == 0) sm.error = 0;
+    const int free_mask = free_pages(c, 0);
     for (int i = threadIdx.x; i < n; i += kPlan)
         if (slot_ok(c, slots[i])) s.mark[slots[i]] = -1;
-    const int free_mask = free_pages(c, 0);
     __syncthreads();
     for (int i = threadIdx.x; i < n; i += kPlan) {
         const int slot = slots[i], m = counts ? counts[i] : count;
-        int4 e = make_int4(0, 0, 0, 0);  // pages wanted, pages held, place in the list
+        int4 e = make_int4(0, 0, 0, slot);  // pages wanted, pages held, place in the list, slot
         int bad = 0;
-        if (!slot_ok(c, slot) || atomicCAS(&s.mark[slot], -1, i) != -1) bad = kCacheBadSlot;
+        if (!slot_ok(c, slot)) bad = kCacheBadSlot;
         else {
             const int len = length_of(c, slot);
-            if (len < 0 || m < 0 || (long long)len + m > (long long)c.max_pages * c.page_size)
+            if (atomicCAS(&s.mark[slot], -1, i) != -1) bad = kCacheBadSlot;
+            else if (len < 0 || m < 0 || (long long)len + m > (long long)c.max_pages * c.page_size)
                 bad = kCacheBadLength;
             else {
                 e.y = (len + c.page_size - 1) / c.page_size;
@@ -160,101 +187,106 @@ __global__ void __launch_bounds__(kPlan) reserve_kernel(const fa_cache c, const 
                 }
             }
         }
-        if (bad) atomicOr(&error, bad);
-        s.entry[i] = e;
+        if (bad) atomicOr(&sm.error, bad);
+        entry[i] = e;
     }
     __syncthreads();
-    const long long want = place_needs(s.entry, n, sums);
-    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, free_mask, sums)))
-        if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
+    const long long want = place_needs(entry, n, sm.sums);
+    int* taken = want <= kFew ? sm.taken : s.taken;
+    if (!sm.error && want > 0 && !(want <= c.pages && take_pages(c, taken, want, free_mask, sm.sums)))
+        if (threadIdx.x == 0) atomicOr(&sm.error, kCacheNoPages);
     __syncthreads();
-    if (error) {
-        if (threadIdx.x == 0) atomicOr(s.status, error);
+    if (sm.error) {
+        if (threadIdx.x == 0) atomicOr(s.status, sm.error);
         return;
     }
     for (int r = threadIdx.x; r < want; r += kPlan) {
         int lo = 0, hi = n - 1;  // the last entry whose place is <= r
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (s.entry[mid].z <= r) lo = mid; else hi = mid - 1;
+            if (entry[mid].z <= r) lo = mid; else hi = mid - 1;
         }
-        const int4 e = s.entry[lo];
-        const int page = s.taken[r];
-        c.table[(long long)slots[lo] * c.max_pages + e.y + (r - e.z)] = page;
+        const int4 e = entry[lo];
+        const int page = taken[r];
+        c.table[(long long)e.w * c.max_pages + e.y + (r - e.z)] = page;
         c.refs[page] = 1;
     }
-    for (int i = threadIdx.x; i < n; i += kPlan) c.lengths[slots[i]] += counts ? counts[i] : count;
+    for (int i = threadIdx.x; i < n; i += kPlan) c.lengths[entry[i].w] += counts ? counts[i] : count;
 }
 
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, const int* parents,
                                                           const int* children, int n) {
     pdl_begin();
-    __shared__ long long sums[kPlan / 32 + 1];
-    __shared__ int error;
+    __shared__ PlanSmem sm;
     const Scratch s = scratch_of(c);
-    if (threadIdx.x == 0) error = 0;
-    for (int i = threadIdx.x; i < n; i += kPlan) {
-        if (slot_ok(c, children[i])) s.mark[children[i]] = -1;
-        if (slot_ok(c, parents[i])) s.mark[parents[i]] = -1;
-    }
+    const Groups grp(n);
+    int4* entry = n <= kPlan ? sm.entry : s.entry;
+    if (threadIdx.x == 0) sm.error = 0;
     const int free_mask = free_pages(c, 0);
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int from = parents[i], to = children[i];
+        if (slot_ok(c, to)) s.mark[to] = -1;
+        if (slot_ok(c, from)) s.mark[from] = -1;
+    }
     __syncthreads();
-    // a warp an entry
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
-        const int from = parents[i], to = children[i], lane = threadIdx.x & 31;
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int from = parents[i], to = children[i];
         int4 e = make_int4(0, 0, 0, 0);  // pages wanted (0 or 1), whole pages, place, rows copied
         int bad = 0;
         if (!slot_ok(c, from) || !slot_ok(c, to)) bad = kCacheBadSlot;
         else {
-            const int len = length_of(c, from);
-            if (len < 0 || c.lengths[to] != 0) bad = kCacheBadLength;
+            const int len = length_of(c, from), old = c.lengths[to];
+            if (grp.sub == 0 && atomicCAS(&s.mark[to], -1, i) != -1) bad = kCacheBadSlot;
+            if (len < 0 || old != 0) bad |= kCacheBadLength;
             else {
                 e.y = len / c.page_size;
                 e.w = len % c.page_size;
                 e.x = e.w > 0;
-                for (int k = lane; k < e.y + e.x; k += 32) {
+                for (int k = grp.sub; k < e.y + e.x; k += grp.g) {
                     const int p = c.table[(long long)from * c.max_pages + k];
-                    if (p < 0 || p >= c.pages) bad = kCacheBadSlot;
+                    if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
                 }
             }
-            if (lane == 0 && atomicCAS(&s.mark[to], -1, i) != -1) bad = kCacheBadSlot;
         }
-        if (bad) atomicOr(&error, bad);
-        if (lane == 0) s.entry[i] = e;
+        if (bad) atomicOr(&sm.error, bad);
+        if (grp.sub == 0) entry[i] = e;
     }
     __syncthreads();
     // a slot cannot be read and made in one call
-    for (int i = threadIdx.x; i < n; i += kPlan)
-        if (slot_ok(c, parents[i]) && s.mark[parents[i]] != -1) atomicOr(&error, kCacheBadSlot);
-    __syncthreads();
-    const long long want = place_needs(s.entry, n, sums);
-    if (!error && want > 0 && !(want <= c.pages && take_pages(c, s.taken, want, free_mask, sums)))
-        if (threadIdx.x == 0) atomicOr(&error, kCacheNoPages);
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int from = parents[i];
+        if (slot_ok(c, from) && s.mark[from] != -1) atomicOr(&sm.error, kCacheBadSlot);
+    }
+    const long long want = place_needs(entry, n, sm.sums);  // (begins and ends with a barrier)
+    int* taken = want <= kFew ? sm.taken : s.taken;
+    if (!sm.error && want > 0 && !(want <= c.pages && take_pages(c, taken, want, free_mask, sm.sums)))
+        if (threadIdx.x == 0) atomicOr(&sm.error, kCacheNoPages);
     __syncthreads();
     if (threadIdx.x == 0) {
-        *s.go = error == 0;
-        if (error) atomicOr(s.status, error);
+        *s.go = sm.error == 0;
+        if (sm.error) atomicOr(s.status, sm.error);
     }
-    if (error) return;
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
-        const int4 e = s.entry[i];
-        const int* from = c.table + (long long)parents[i] * c.max_pages;
-        int* to = c.table + (long long)children[i] * c.max_pages;
-        __syncwarp();
-        for (int k = threadIdx.x & 31; k < e.y; k += 32) {
-            to[k] = from[k];
-            atomicAdd(&c.refs[from[k]], 1);
+    if (sm.error) return;
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int4 e = entry[i];
+        const int from_slot = parents[i], to_slot = children[i];
+        const int* from = c.table + (long long)from_slot * c.max_pages;
+        int* to = c.table + (long long)to_slot * c.max_pages;
+        for (int k = grp.sub; k < e.y; k += grp.g) {
+            const int p = from[k];
+            to[k] = p;
+            atomicAdd(&c.refs[p], 1);
         }
-        if ((threadIdx.x & 31) == 0) {
+        if (grp.sub == 0) {
             int src = 0, dst = 0;
             if (e.x) {
                 src = from[e.y];
-                dst = s.taken[e.z];
+                dst = taken[e.z];
                 to[e.y] = dst;
                 c.refs[dst] = 1;
             }
-            c.lengths[children[i]] = c.lengths[parents[i]];
-            s.entry[i] = make_int4(src, dst, e.w, 0);
+            c.lengths[to_slot] = e.y * c.page_size + e.w;
+            s.entry[i] = make_int4(src, dst, e.w, 0);  // for the copying kernel
         }
     }
 }
@@ -293,10 +325,11 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const fa_cache c, const int
     pdl_begin();
     __shared__ int error;
     const Scratch s = scratch_of(c);
+    const Groups grp(n);
     if (threadIdx.x == 0) error = 0;
     __syncthreads();
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp an entry
-        const int slot = slots[i], lane = threadIdx.x & 31;
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int slot = slots[i];
         int bad = 0;
         if (!slot_ok(c, slot)) bad = kCacheBadSlot;
         else {
@@ -304,7 +337,7 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const fa_cache c, const int
             if (len < 0) bad = kCacheBadLength;
             else {
                 const int used = (len + c.page_size - 1) / c.page_size;
-                for (int k = lane; k < used; k += 32) {
+                for (int k = grp.sub; k < used; k += grp.g) {
                     const int p = c.table[(long long)slot * c.max_pages + k];
                     if (p < 0 || p >= c.pages) bad = kCacheBadSlot;
                 }
@@ -317,14 +350,14 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const fa_cache c, const int
         if (threadIdx.x == 0) atomicOr(s.status, error);
         return;
     }
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
-        const int slot = slots[i], lane = threadIdx.x & 31;
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int slot = slots[i];
         int len = 0;
         // whoever takes the length frees the pages: a slot named twice is freed once
-        if (lane == 0) len = atomicExch(&c.lengths[slot], 0);
-        len = __shfl_sync(0xffffffffu, len, 0);
+        if (grp.sub == 0) len = atomicExch(&c.lengths[slot], 0);
+        len = grp.first(len);
         const int used = (len + c.page_size - 1) / c.page_size;
-        for (int k = lane; k < used; k += 32) {
+        for (int k = grp.sub; k < used; k += grp.g) {
             int* at = c.table + (long long)slot * c.max_pages + k;
             atomicSub(&c.refs[*at], 1);
             *at = -1;
@@ -338,36 +371,37 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
     pdl_begin();
     __shared__ int error;
     const Scratch s = scratch_of(c);
+    const Groups grp(n);
     if (threadIdx.x == 0) error = 0;
-    for (int i = threadIdx.x; i < n; i += kPlan)
-        if (slot_ok(c, slots[i])) s.mark[slots[i]] = -1;
+    for (int i = threadIdx.x; i < n; i += kPlan) {
+        const int slot = slots[i];
+        if (slot_ok(c, slot)) s.mark[slot] = -1;
+    }
     __syncthreads();
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {  // a warp an entry
-        const int slot = slots[i], lane = threadIdx.x & 31;
-        int bad = 0, len = -1, used = 0;
-        bool fresh = false;
-        if (slot_ok(c, slot)) {
-            len = length_of(c, slot);
-            if (lane == 0) fresh = atomicCAS(&s.mark[slot], -1, i) == -1;
-            fresh = __any_sync(0xffffffffu, fresh);
-        }
-        const int b = base[i], m = accepted[i];
-        if (!fresh) bad = kCacheBadSlot;
-        else if (len < 0 || b < 0 || b > len || m < 0 || m > width || m > len - b) bad = kCacheBadLength;
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int slot = slots[i], b = base[i], m = accepted[i];
+        const int* at = path + (long long)i * width;
+        int bad = 0;
+        if (!slot_ok(c, slot)) bad = kCacheBadSlot;
         else {
-            used = (len + c.page_size - 1) / c.page_size;
-            const int* row = c.table + (long long)slot * c.max_pages;
-            const int kept = (b + m + c.page_size - 1) / c.page_size;
-            for (int k = b / c.page_size + lane; k < used; k += 32) {
-                const int p = row[k];
-                if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
-                else if (k < kept && c.refs[p] != 1) bad |= kCacheShared;
-                s.shadow[(long long)slot * c.max_pages + k] = p;
-            }
-            const int* at = path + (long long)i * width;
-            for (int j = lane; j < m; j += 32) {  // strictly ascending, within the draft
-                const int t = at[j];
-                if (t < 0 || t >= len - b || (j > 0 && at[j - 1] >= t)) bad |= kCacheBadLength;
+            const int len = length_of(c, slot);
+            const bool again = grp.sub == 0 && atomicCAS(&s.mark[slot], -1, i) != -1;
+            if (grp.any(again)) bad = kCacheBadSlot;
+            else if (len < 0 || b < 0 || b > len || m < 0 || m > width || m > len - b) bad = kCacheBadLength;
+            else {
+                const int used = (len + c.page_size - 1) / c.page_size;
+                const int* row = c.table + (long long)slot * c.max_pages;
+                const int kept = (b + m + c.page_size - 1) / c.page_size;
+                for (int j = grp.sub; j < m; j += grp.g) {  // strictly ascending, within the draft
+                    const int t = at[j];
+                    if (t < 0 || t >= len - b || (j > 0 && at[j - 1] >= t)) bad |= kCacheBadLength;
+                }
+                for (int k = b / c.page_size + grp.sub; k < used; k += grp.g) {
+                    const int p = row[k];
+                    if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
+                    else if (k < kept && c.refs[p] != 1) bad |= kCacheShared;
+                    s.shadow[(long long)slot * c.max_pages + k] = p;
+                }
             }
         }
         if (bad) atomicOr(&error, bad);
@@ -378,17 +412,16 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
         if (error) atomicOr(s.status, error);
     }
     if (error) return;
-    for (int i = threadIdx.x >> 5; i < n; i += kPlan / 32) {
-        const int slot = slots[i], lane = threadIdx.x & 31;
-        const int len = c.lengths[slot], now = base[i] + accepted[i];
-        __syncwarp();
+    for (int i = grp.entry; i < n; i += grp.stride) {
+        const int slot = slots[i], now = base[i] + accepted[i], len = c.lengths[slot];
+        __syncwarp(grp.mask);  // (all have read the length)
         const int used = (len + c.page_size - 1) / c.page_size;
-        for (int k = (now + c.page_size - 1) / c.page_size + lane; k < used; k += 32) {
-            int* at = c.table + (long long)slot * c.max_pages + k;
-            atomicSub(&c.refs[*at], 1);
-            *at = -1;
+        for (int k = (now + c.page_size - 1) / c.page_size + grp.sub; k < used; k += grp.g) {
+            const long long at = (long long)slot * c.max_pages + k;
+            atomicSub(&c.refs[s.shadow[at]], 1);
+            c.table[at] = -1;
         }
-        if (lane == 0) c.lengths[slot] = now;
+        if (grp.sub == 0) c.lengths[slot] = now;
     }
 }
 

@@ -1302,8 +1302,8 @@ Tiles row_tiles(int group, int N, int d) {
 }
 
 // Items of up to this many rows are joined by the CTA that finishes last:
-// one launch less (attention of one token over 501 keys, 16 heads: 18.6 -> XX us),
-// while more rows would leave one CTA too much to read.
+// one launch less (~5 us of the caller's time, and as much on the GPU), while
+// more rows would leave one CTA too much to read.
 constexpr int kFusedRows = 32;
 
 struct TreeWs {
@@ -1404,7 +1404,9 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     p.layer = layer;
     p.B = B; p.N = N; p.T = T; p.Hq = Hq;
     p.tile_tokens = tiles.tokens;
-    p.min_tiles = 1;
+    // Two tiles a CTA at least: the streams alternate, and a join costs about as much
+    // as a tile (one token over 501 keys, 16 heads: 15.8 -> 15.1 us).
+    p.min_tiles = 2;
     p.page_shift = __builtin_ctz(cache->page_size);
     p.fused = !tiles.pair && tiles.rows <= kFusedRows;
     p.call = next_call();
