@@ -105,6 +105,8 @@ def lib_path() -> str:
 def lib():
     """The loaded CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB

@@ -305,18 +305,20 @@ __global__ void __launch_bounds__(256, 4) fork_copy_kernel(const fa_cache c) {
     const int head16 = c.page_size * row16, run = e.z * row16;
     const uint4* src = base + ((long long)layer * c.pages + e.x) * c.heads * head16;
     uint4* dst = base + ((long long)layer * c.pages + e.y) * c.heads * head16;
-    const int all = c.heads * run;
-    for (int i0 = threadIdx.x; i0 < all; i0 += 4 * 256) {
-        uint4 x[4];
+    // (heads in fours, so that no index has to be divided: the copy is close to
+    // bound by instructions otherwise)
+    for (int h = 0; h < c.heads; h += 4) {
+        const uint4* from = src + (long long)h * head16;
+        uint4* to = dst + (long long)h * head16;
+        const int heads = min(4, c.heads - h);
+        for (int i = threadIdx.x; i < run; i += 256) {
+            uint4 x[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * 256;
-            if (i < all) x[u] = src[(long long)(i / run) * head16 + i % run];
-        }
+            for (int u = 0; u < 4; ++u)
+                if (u < heads) x[u] = from[u * head16 + i];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * 256;
-            if (i < all) dst[(long long)(i / run) * head16 + i % run] = x[u];
+            for (int u = 0; u < 4; ++u)
+                if (u < heads) to[u * head16 + i] = x[u];
         }
     }
 }

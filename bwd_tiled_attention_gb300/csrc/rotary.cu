@@ -11,11 +11,19 @@
 //
 // Bound: memory.  Each value is read and written once, and nothing is reused
 // but the token's table row.  So a thread takes one 16-byte unit of a head's
-// columns (half layout: the two units that hold its pairs) in kHeadsPerThread
-// heads of one token: the cos and sin it loads serve all of them, and all its
-// loads are in flight before the first use.  Head dimensions, strides or
-// alignments that do not allow 16-byte accesses run the same code one element
-// at a time (VW = 1).
+// columns in kHeadsPerThread heads of one token: the cos and sin it loads serve
+// all of them, and all its loads are in flight before the first use.  In the
+// half layout the two halves of a pair lie in two lanes, which exchange them:
+// a thread that loads both halves needs 91 registers instead of 56 and has too
+// few warps beside it (bf16, 2 x 8192 tokens, 32 + 8 heads of 128: 91 us, 61 us
+// now; interleaved 67 -> 58 us; fp32 with 16 + 16 heads of 192, 62 us; at the
+// copy rate 50, 50 and 59 us).  bf16 is near the instruction limit too (60% of
+// issue slots), which is why indexes are divided by multiplication.  Blocks of
+// 64 threads, 4 heads a thread: 128 or 256 threads 3-15% slower, 2 heads 15-25%
+// slower, 8 heads 2% faster in the half layout and 30% slower interleaved.
+// Head dimensions, strides or alignments that do not allow 16-byte accesses
+// run the same code one element at a time (VW = 1), and fp32 heads wider than
+// a warp's lanes take both halves in a thread.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,6 +42,21 @@ namespace {
 constexpr int kRotThreads = 64;
 constexpr int kHeadsPerThread = 4;
 
+// Division by a number known at the launch: a high product and a shift
+// (x < 2^31; the multiplier is 2^(32 + s) / d rounded up, 2^s >= d).
+struct Divider {
+    unsigned d, mul, shift;
+    void set(unsigned by) {
+        d = by;
+        shift = 0;
+        while ((1u << shift) < by) ++shift;
+        mul = (unsigned)(((1ull << 32) * ((1ull << shift) - by)) / by + 1);
+    }
+    __device__ __forceinline__ unsigned operator()(unsigned x) const {
+        return (unsigned)(((unsigned long long)__umulhi(x, mul) + x) >> shift);
+    }
+};
+
 struct RotParams {
     // segment 0: q, 1: k, 2: v (copied); heads 0 when absent
     const void* in[3];
@@ -41,6 +64,7 @@ struct RotParams {
     long long ts[3], hs[3];      // input strides in elements
     int heads[3], quads[3];      // quads: groups of kHeadsPerThread heads
     int T, d, rot, units;        // units per head
+    Divider by_units, by_quads;  // quads: of a token, all segments
     int t_first;                 // first token of this launch
     unsigned n_items;            // (token, quad) pairs, times units where lanes are not grouped
     int lanes;                   // kShuffle: items of one warp
@@ -54,7 +78,7 @@ struct RotParams {
     // paged call
     fa_cache cache;
     const int* slots;
-    int layer;
+    int layer, page_shift;
 };
 
 template <typename E>
@@ -90,7 +114,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     bool idle = false;
     if (L == kShuffle) {  // whole heads to a warp; the lanes left over follow item 0
         const unsigned lane = threadIdx.x & 31, warp = (blockIdx.x * kRotThreads + threadIdx.x) >> 5;
-        const unsigned g = lane / U;
+        const unsigned g = p.by_units(lane);
         item = warp * p.lanes + g;
         u = (int)(lane - g * U);
         idle = g >= (unsigned)p.lanes || item >= p.n_items;
@@ -98,10 +122,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     } else {
         const unsigned idx = blockIdx.x * kRotThreads + threadIdx.x;
         if (idx >= p.n_items) return;
-        item = idx / U;
+        item = p.by_units(idx);
         u = (int)(idx - item * U);
     }
-    const unsigned tok_i = item / quads;
+    const unsigned tok_i = p.by_quads(item);
     const int tok = p.t_first + (int)tok_i;
     int quad = (int)(item - tok_i * quads);
     int seg = 0;
@@ -166,7 +190,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
             else {
                 // (a length is at most 2^30, and out-of-range ones wrap to no column)
                 const int at = p.cache.lengths[slot] - r.n + (tok - r.t0);
-                const unsigned col = (unsigned)at / (unsigned)p.cache.page_size;
+                const unsigned col = (unsigned)at >> p.page_shift;
                 if (at < 0 || col >= (unsigned)p.cache.max_pages) bad = kCacheBadLength;
                 else {
                     place = at;
@@ -220,12 +244,14 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
                 sn[2 * i + 1] = t.w;
             }
         }
+        if (turns && !known) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
-            if (!known && turns) cs[i] = sn[i] = NAN;
-            if (p.backward) sn[i] = -sn[i];
-            if (L == kShuffle && c0 < half) sn[i] = -sn[i];
+            for (int i = 0; i < NP; ++i) cs[i] = sn[i] = NAN;
         }
+        // backward turns the other way; own * cos +- partner * sin for the lanes of a pair
+        const float sign = (p.backward != 0) != (L == kShuffle && c0 < half) ? -1.f : 1.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) sn[i] *= sign;
 #pragma unroll
         for (int h = 0; h < kHeadsPerThread; ++h) {
             if (L == kShuffle) {
@@ -298,6 +324,8 @@ cudaError_t launch_t(RotParams p, cudaStream_t stream) {
     const long long per_token = (long long)(p.quads[0] + p.quads[1] + p.quads[2]) * p.units;
     if (per_token == 0) return cudaSuccess;
     p.lanes = 32 / p.units;
+    p.by_units.set(p.units);
+    p.by_quads.set(p.quads[0] + p.quads[1] + p.quads[2]);
     // item and thread indexes are 32 bits: more tokens than that go in several launches
     const long long most = 0x3FFFFF00LL / per_token;
     for (long long t = 0; t < p.T; t += most) {
@@ -462,6 +490,7 @@ fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, in
     p.cache = *cache;
     p.slots = slots;
     p.layer = layer;
+    p.page_shift = __builtin_ctz(cache->page_size);
     const fa_status st = check_rotary(p, table, pos_bytes);
     if (st != FA_OK) return st;
     if (T == 0) return FA_OK;

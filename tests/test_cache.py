@@ -414,3 +414,32 @@ def test_captured_page_operations():
         m.fork([1, 2], [7, 8])
     assert status(c) == 0
     agree(c, m)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("as_int", [False, True])
+def test_on_another_stream(as_int):
+    """Every call on a side stream, given as a stream or as its handle."""
+    side = torch.cuda.Stream()
+    c, m = make(layers=2, d=64)
+    x = torch.randn(6, 2, 64).bfloat16().cuda()
+    lists = [ints(v) for v in ([3, 4], [2, 4], [5, 6], [0, 0], [1, 1])]
+    slots, counts, kids, base, got = lists
+    path = ints([[1], [2]])
+    side.wait_stream(torch.cuda.current_stream())
+    kw = dict(stream=side.cuda_stream if as_int else side)
+    c.reserve(slots, counts, **kw)
+    fa.cache_append(c, 0, slots, x, x, cu_seqlens=ints([0, 2, 6]), **kw)
+    c.fork(slots, kids, **kw)
+    c.accept(slots, base, path, got, **kw)
+    c.free(kids, **kw)
+    c.check(**kw)
+    m.reserve([3, 4], [2, 4])
+    for s, t0, n in ((3, 0, 2), (4, 2, 4)):
+        for j in range(n):
+            page, row = m.place(s, j)
+            m.k[0, page, :, row] = m.v[0, page, :, row] = f64(x[t0 + j])
+    m.fork([3, 4], [5, 6])
+    m.accept([3, 4], [0, 0], [[1], [2]], [1, 1])
+    m.free([5, 6])
+    agree(c, m)

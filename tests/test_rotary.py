@@ -280,3 +280,32 @@ def test_captured_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+@pytest.mark.gpu
+def test_captured_gradients():
+    """Forward and backward in one graph, replayed on other values."""
+    t = fa.rotary_table(64, 100)
+    q = torch.randn(60, 4, 64).cuda().requires_grad_()
+    k = torch.randn(60, 2, 64).cuda().requires_grad_()
+    gq, gk = torch.randn(60, 4, 64).cuda(), torch.randn(60, 2, 64).cuda()
+
+    def step():
+        out = fa.rotary(q, k, t, batch=3)
+        return out + torch.autograd.grad(out, (q, k), (gq, gk))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        got = step()
+    with torch.no_grad():
+        q.copy_(torch.randn_like(q))
+        gk.copy_(torch.randn_like(gk))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, step()):
+        assert torch.equal(a, b)
