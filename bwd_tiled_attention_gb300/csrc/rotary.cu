@@ -41,6 +41,7 @@ namespace {
 
 constexpr int kRotThreads = 64;
 constexpr int kHeadsPerThread = 4;
+constexpr long long kMostThreads = 0x3FFFFF00LL;  // of a launch (idle lanes come on top)
 
 // Division by a number known at the launch: a high product and a shift
 // (x < 2^31; the multiplier is 2^(32 + s) / d rounded up, 2^s >= d).
@@ -327,7 +328,7 @@ cudaError_t launch_t(RotParams p, cudaStream_t stream) {
     p.by_units.set(p.units);
     p.by_quads.set(p.quads[0] + p.quads[1] + p.quads[2]);
     // item and thread indexes are 32 bits: more tokens than that go in several launches
-    const long long most = 0x3FFFFF00LL / per_token;
+    const long long most = kMostThreads / per_token;
     for (long long t = 0; t < p.T; t += most) {
         const long long n = p.T - t < most ? p.T - t : most;
         p.t_first = (int)t;
@@ -404,7 +405,7 @@ fa_status check_rotary(const RotParams& p, const float* table, int pos_bytes) {
         return FA_ERR_INVALID_ARG;
     if (!p.cu && (long long)p.B * p.N != p.T) return FA_ERR_INVALID_ARG;
     // the most threads that one token takes must leave room for 32-bit indexes
-    if (((long long)p.heads[0] + p.heads[1] + p.heads[2] + 12) / kHeadsPerThread * p.d > 0x7FFFFF00LL)
+    if (((long long)p.heads[0] + p.heads[1] + p.heads[2] + 12) / kHeadsPerThread * p.d > kMostThreads)
         return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
@@ -494,7 +495,7 @@ fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, in
     const fa_status st = check_rotary(p, table, pos_bytes);
     if (st != FA_OK) return st;
     if (T == 0) return FA_OK;
-    if (!slots || !k || !v || (Hq > 0 && (!q || !q_out)) || (rot > 0 && (!table || !table_len)))
+    if ((B > 0 && !slots) || !k || !v || (Hq > 0 && (!q || !q_out)) || (rot > 0 && (!table || !table_len)))
         return FA_ERR_INVALID_ARG;
     if (!aligned(slots, 4) || !aligned(q, 2) || !aligned(q_out, 2) || !aligned(k, 2) || !aligned(v, 2))
         return FA_ERR_INVALID_ARG;

@@ -32,6 +32,7 @@ __all__ = ["PagedCache", "rotary", "rotary_table", "cache_append", "tree_attenti
 _INT = (torch.int32,)
 _HEAD_DIMS = (64, 96, 128, 192, 256)
 _PAGE_SIZES = (16, 32, 64, 128)
+_MOST = 2 ** 31 - 1  # counts are 32 bits
 
 
 class _CacheDesc(ctypes.Structure):
@@ -103,6 +104,8 @@ def _ptr(t):
 
 def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
     """(B, N) of the call: N is the dense length, or the bound of a packed batch."""
+    if T > _MOST:
+        raise ValueError(f"{T} tokens: a call takes at most {_MOST}")
     if cu_seqlens is None:
         if batch is None:
             raise ValueError("dense inputs need batch (B); T = B * N")
@@ -119,6 +122,8 @@ def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
         if need_max:
             raise ValueError("variable-length inputs need max_seqlen")
         return B, 0
+    if not 0 <= max_seqlen <= _MOST:
+        raise ValueError(f"max_seqlen must be from 0 to {_MOST}, got {max_seqlen}")
     return B, int(max_seqlen)
 
 
@@ -274,6 +279,7 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
     if 2 * table.shape[1] > first.shape[2]:
         raise ValueError("the table turns more columns than a head has")
     if positions is not None:
+        _sequences(T, 1, None, None, dev)
         B, N, cu_seqlens = 1, T, None
     else:
         B, N = _sequences(T, batch, cu_seqlens, None, dev, need_max=False)
@@ -374,8 +380,8 @@ class PagedCache:
         many = counts if isinstance(counts, torch.Tensor) else None
         if many is not None:
             self._list("counts", many, n)
-        elif counts < 0:
-            raise ValueError("counts must not be negative")
+        elif not 0 <= counts <= _MOST:
+            raise ValueError(f"counts must be from 0 to {_MOST}, got {counts}")
         self._call("fa_cache_reserve", stream, (slots, many), slots.data_ptr(), _ptr(many),
                    0 if many is not None else int(counts), n)
 
@@ -485,8 +491,6 @@ def tree_mask(parents, cu_seqlens=None, max_seqlen=None, batch=None, stream=None
     _want("parents", parents, _INT, 1)
     T = parents.shape[0]
     B, N = _sequences(T, batch, cu_seqlens, max_seqlen, parents.device)
-    if N < 0:
-        raise ValueError("max_seqlen must not be negative")
     _cuda("parents", parents)
     words = max(1, -(-N // 64))
     with _on(parents.device, stream, (parents, cu_seqlens)):

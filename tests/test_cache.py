@@ -246,8 +246,9 @@ def test_refused_on_the_device():
     agree(c, m)
     with pytest.raises(ValueError, match="named twice"):
         c.reserve(ints(list(range(10))), 1)
-    with pytest.raises(ValueError, match="negative"):
-        c.reserve(ints([0]), -1)
+    for counts in (-1, 2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="counts must"):
+            c.reserve(ints([0]), counts)
     with pytest.raises(ValueError, match="entries"):
         c.fork(ints([0]), ints([5, 6]))
     with pytest.raises(ValueError, match="int32"):
@@ -332,6 +333,19 @@ def test_append_positions_and_tokens_of_no_sequence():
     agree(c, m)
     assert not out[7:].any() and out[:7].any()
     assert status(c) == 0
+
+
+@pytest.mark.gpu
+def test_append_to_no_sequence():
+    """A packed batch without sequences: nothing is written, q comes out as zeros."""
+    c, m = make(d=64)
+    x = torch.randn(3, 2, 64).bfloat16().cuda()
+    q = fa.cache_append(c, 0, ints([]), x, x, q=x, cu_seqlens=ints([0]))
+    assert not q.any()
+    o, lse = fa.tree_attention(x, c, 0, ints([]), cu_seqlens=ints([0]), max_seqlen=4)
+    assert not o.any() and lse.eq(-float("inf")).all()
+    assert status(c) == 0
+    agree(c, m)
 
 
 @pytest.mark.gpu

@@ -44,6 +44,10 @@ def test_bad_arguments_are_refused(kw):
     assert call(**kw) == fa.FA_ERR_INVALID_ARG
 
 
+def test_tokens_too_wide_for_the_indexes_are_refused():
+    assert call(Hq=65535, Hkv=60000, d=65536) == fa.FA_ERR_UNSUPPORTED
+
+
 def test_nothing_to_do_is_no_error():
     assert call(T=0, N=0) == fa.FA_OK
     assert call(Hq=0, Hkv=0, q=None, k=None) == fa.FA_OK
@@ -309,3 +313,39 @@ def test_captured_gradients():
     torch.cuda.synchronize()
     for a, b in zip(got, step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_attention_with_rotary_and_different_lengths():
+    """Queries at the end of longer keys: positions for each side."""
+    t = fa.rotary_table(64, 200)
+    g = torch.Generator().manual_seed(8)
+    q = torch.randn(40, 4, 64, generator=g).bfloat16().cuda().requires_grad_()
+    k = torch.randn(130, 2, 64, generator=g).bfloat16().cuda().requires_grad_()
+    v = torch.randn(130, 2, 64, generator=g).bfloat16().cuda().requires_grad_()
+    kw = dict(causal=True, batch=1, deterministic=True)
+    pos = dict(positions=torch.arange(90, 130).cuda(), positions_k=torch.arange(130).cuda())
+    o = fa.attention(q, k, v, rotary=t, interleaved=True, **pos, **kw)
+    qr, _ = fa.rotary(q, None, t, positions=pos["positions"], interleaved=True)
+    _, kr = fa.rotary(None, k, t, positions=pos["positions_k"], interleaved=True)
+    o2 = fa.attention(qr, kr, v, **kw)
+    assert torch.equal(o, o2)
+    w = torch.randn(o.shape, generator=g).bfloat16().cuda()
+    for a, b in zip(torch.autograd.grad(o, (q, k, v), w), torch.autograd.grad(o2, (q, k, v), w)):
+        assert torch.equal(a, b)
+    with pytest.raises(ValueError, match="positions and positions_k"):
+        fa.attention(q, k, v, rotary=t, **kw)
+
+
+@pytest.mark.gpu
+def test_more_tokens_than_one_launch_takes():
+    """Past 2^27 tokens of one head the call runs as several launches."""
+    T, d = (1 << 27) + 1000, 64
+    t = torch.from_numpy(table64(d, 97)).cuda()
+    q = torch.empty(T, 1, d, dtype=torch.bfloat16, device="cuda")
+    q.view(torch.int16).random_(0x3C00, 0x4000)         # finite values
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") % 97
+    got, _ = fa.rotary(q, None, t, positions=pos)
+    for a in (0, (1 << 27) - 300, T - 500):
+        ref, mag = rotate(f64(q[a:a + 500]), table64(d, 97).astype(np.float64), pos[a:a + 500].cpu().numpy(), False)
+        within("q", f64(got[a:a + 500]), ref, rotary_bound(ref, mag, torch.bfloat16))

@@ -387,6 +387,9 @@ def test_tensor_api_refuses():
         go(q=q.float())
     with pytest.raises(ValueError, match="max_seqlen"):
         go(cu_seqlens=ints([0, 3, 6]))
+    for bound in (-1, 2 ** 31, 2 ** 33):
+        with pytest.raises(ValueError, match="max_seqlen must"):
+            go(cu_seqlens=ints([0, 3, 6]), max_seqlen=bound)
     with pytest.raises(ValueError, match="different sizes"):
         go(cu_seqlens=ints([0, 6]), max_seqlen=6)
     with pytest.raises(ValueError, match="B \\* N"):
