@@ -437,7 +437,7 @@ def _of_cache(cache, layer, slots):
 def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
                  interleaved=False, cu_seqlens=None, stream=None):
     """Writes new keys and values ``[T, heads, d]`` to one layer of the cache, as the last tokens of
-    ``slots`` (reserve them first).
+    ``slots``, which must differ (reserve them first: that checks it).
 
     With ``rotary`` (a `rotary_table`) k, and q if given, are turned to ``positions``, by
     default the tokens' places in their sequences.  Returns the turned q (contiguous), or

@@ -400,7 +400,9 @@ fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream);
  * them (and q) on the way.
  *   The call's T tokens are those of B sequences (dense: N each; packed:
  *   cu_seqlens), sequence i being slots[i].  They are the LAST tokens of the
- *   slot: reserve them first.  Slots must differ.
+ *   slot: reserve them first.  Slots must differ; fa_cache_reserve checks that,
+ *   this call does not (with a slot named twice it is not defined whose rows
+ *   stay).
  *   k, v: bf16 [T, heads, d] with token and head strides, q [T,Hq,d] likewise
  *   (Hq = 0: none), q_out contiguous.  rot, table, positions, interleaved as
  *   in fa_rotary (rot = 0: nothing turns); without positions a token's position
