@@ -31,6 +31,14 @@
 //     is the bound.  Above d = 128 TMEM holds one O: one stream with two S
 //     buffers, on tiles of 64 keys.
 //
+// Measured (GPU time): 64 sequences of 4-8k tokens, 32 + 8 heads of 128, one
+// token each, 241 us = 6.66 TB/s, 98% of the copy rate (d = 64 140 us at 5.5
+// TB/s, bound by the streams' chain of ~1500 cycles a tile; d = 256, 32
+// sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 350 us = 1130 TF/s
+// (32 + 8 heads of 128), 345 us = 1150 TF/s (16 + 4 of 256); 4 trees of 64 over
+// 30k keys 135 us.  One token over 501 keys 14.4 us: ~3.5 us until the first
+// load, then one tile's chain, the join, and a CTA's first pass through its code.
+//
 // Pages hold whatever was there before: keys past the length never reach a
 // sum (their scores are replaced, their V rows zeroed in shared memory), and
 // a drafted token's V that is not finite is kept from the rows that do not
