@@ -1191,16 +1191,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else {
         // ------------------------------------------------------------ warp 2
         setmaxnreg_dec<kFewRegs>();
-        if (p.zero_rest && p.cu) {  // tokens that no sequence owns
-            const int used = min(max(p.cu[p.B], 0), p.T);
+        if (p.zero_rest && p.cu) {  // tokens that no sequence owns: before the first one's and
+                                    // behind the last one's
+            const int skip = min(max(p.cu[0], 0), p.T), used = min(max(p.cu[p.B], skip), p.T);
             const long long step = (long long)gridDim.x * 32;
             const long long at = (long long)blockIdx.x * 32 + lane;
-            const long long rows = (long long)(p.T - used) * p.Hq;
-            uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
-                                                (long long)used * p.Hq * DR);
-            for (long long i = at; i < rows * (DR / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
-            for (long long i = at; i < rows; i += step)
-                p.lse[(i / (p.T - used)) * p.T + used + i % (p.T - used)] = -INFINITY;
+            auto clear = [&](int t0, int n) {
+                const long long rows = (long long)n * p.Hq;
+                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
+                                                    (long long)t0 * p.Hq * DR);
+                for (long long i = at; i < rows * (DR / 8); i += step) o[i] = make_uint4(0u, 0u, 0u, 0u);
+                for (long long i = at; i < rows; i += step)
+                    p.lse[(i / n) * p.T + t0 + i % n] = -INFINITY;
+            };
+            clear(0, skip);
+            clear(used, p.T - used);
         }
     }
 

@@ -329,6 +329,28 @@ def test_rows_of_no_sequence():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,heads,N", [(4, 2, 9), (2, 1, 150)])
+def test_rows_before_the_first_sequence(Hq, heads, N):
+    """A packed batch that begins behind other tokens: those rows, and the ones behind the last
+    sequence, come out empty, or stay as they are in `out`."""
+    h = Held([30, 40], heads, 64, 16, seed=8)
+    q = queries(25, Hq, 64)
+    cu = ints([7, 10, 19])
+    part = fa.tree_attention(q[7:19], h.cache, h.layer, ints(h.slots), cu_seqlens=ints([0, 3, 12]),
+                             max_seqlen=N)
+    junk = [torch.full((25, Hq, 64), NAN, dtype=torch.bfloat16).cuda(), torch.full((Hq, 25), NAN).cuda()]
+    del junk  # (what an output's memory is likely to hold)
+    o, lse = fa.tree_attention(q, h.cache, h.layer, ints(h.slots), cu_seqlens=cu, max_seqlen=N)
+    assert torch.equal(o[7:19], part[0]) and torch.equal(lse[:, 7:19], part[1])
+    rest = list(range(7)) + list(range(19, 25))
+    assert (o[rest] == 0).all() and (lse[:, rest] == -INF).all()
+    out = torch.full_like(o, 3.0), torch.full_like(lse, 5.0)
+    fa.tree_attention(q, h.cache, h.layer, ints(h.slots), cu_seqlens=cu, max_seqlen=N, out=out)
+    assert torch.equal(out[0][7:19], part[0]) and (out[0][rest] == 3).all() and (out[1][:, rest] == 5).all()
+    h.cache.check()
+
+
+@pytest.mark.gpu
 def test_a_slot_read_by_several_sequences():
     h = Held([300], 1, 128, 16)
     q = queries(6, 2, 128)
