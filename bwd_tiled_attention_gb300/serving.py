@@ -344,6 +344,7 @@ class PagedCache:
                                 refs.data_ptr(), self.scratch.data_ptr(), layers, pages, heads,
                                 page_size, d, slots, max_pages)
         self._at = ctypes.addressof(self._desc)
+        self._tensors = (k, v, table, lengths, refs, self.scratch)
 
     @classmethod
     def allocate(cls, layers, pages, heads, page_size, d, slots, max_pages, device="cuda"):
@@ -369,7 +370,7 @@ class PagedCache:
         fn = getattr(lib(), name)
         if _here(self.device, stream):
             return _check(fn(self._at, *args, _raw_stream(self.device)), name)
-        with _on(self.device, stream, tensors):
+        with _on(self.device, stream, self._tensors + tensors):
             _check(fn(self._at, *args, _raw_stream(self.device)), name)
 
     def reserve(self, slots, counts, stream=None):
@@ -414,7 +415,7 @@ class PagedCache:
         """Synchronises, and raises if a call on this cache has been refused on the device or
         failed there since the last check."""
         bits = ctypes.c_int(0)
-        with _on(self.device, stream, ()):
+        with _on(self.device, stream, self._tensors):
             st = lib().fa_cache_check(self._at, ctypes.addressof(bits), _raw_stream(self.device))
         if st != FA_OK:
             told = [w for b, w in ((1, "a slot or page index out of range, or a slot named twice"),
@@ -476,7 +477,8 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
 
     if _here(cache.device, stream):
         return call()
-    with _on(cache.device, stream, (slots, k, v, q, rotary, positions, cu_seqlens)):
+    with _on(cache.device, stream,
+             cache._tensors + (slots, k, v, q, rotary, positions, cu_seqlens)):
         return call()
 
 
@@ -561,6 +563,6 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
 
     if _here(dev, stream):
         return call()
-    with _on(dev, stream, (q, slots, mask, cu_seqlens, workspace) +
+    with _on(dev, stream, cache._tensors + (q, slots, mask, cu_seqlens, workspace) +
              (tuple(out) if out is not None else ())):
         return call()

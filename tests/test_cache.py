@@ -457,3 +457,28 @@ def test_on_another_stream(as_int):
     m.accept([3, 4], [0, 0], [[1], [2]], [1, 1])
     m.free([5, 6])
     agree(c, m)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["reserve", "append", "attention"])
+def test_memory_is_kept_for_another_stream(call):
+    """A cache dropped while a call on another stream is still to run keeps its memory until then."""
+    side = torch.cuda.Stream()
+    c = fa.PagedCache.allocate(1, 4096, 2, 16, 64, 4, 8)
+    slots, x = ints([2]), torch.randn(1, 2, 64).bfloat16().cuda()
+    c.reserve(slots, 1)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    if call == "reserve":
+        c.reserve(slots, 1, stream=side)
+    elif call == "append":
+        fa.cache_append(c, 0, slots, x, x, stream=side)
+    else:
+        fa.tree_attention(x, c, 0, slots, stream=side)
+    at, shape = {c.k.data_ptr(), c.v.data_ptr()}, c.k.shape
+    del c
+    new = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    assert not side.query()
+    assert not at & {t.data_ptr() for t in new}
+    side.synchronize()
