@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
                     if (seg != 0) {  // (q stays out of the cache)
                         const int page = p.cache.table[(long long)slot * p.cache.max_pages + col];
                         if (page < 0 || page >= p.cache.pages) bad = kCacheBadSlot;
+                        else if (p.cache.refs[page] > 1) bad = kCacheShared;  // (costs < 1%)
                         else
                             place_off = ((((long long)p.layer * p.cache.pages + page) *
                                               p.cache.heads + h0) * p.cache.page_size +

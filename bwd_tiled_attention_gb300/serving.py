@@ -438,7 +438,8 @@ def _of_cache(cache, layer, slots):
 def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
                  interleaved=False, cu_seqlens=None, stream=None):
     """Writes new keys and values ``[T, heads, d]`` to one layer of the cache, as the last tokens of
-    ``slots``, which must differ (reserve them first: that checks it).
+    ``slots``, which must differ (reserve them first: that checks it).  A token whose place is in
+    a page that several slots share is not written, and `PagedCache.check` raises.
 
     With ``rotary`` (a `rotary_table`) k, and q if given, are turned to ``positions``, by
     default the tokens' places in their sequences.  Returns the turned q (contiguous), or
@@ -515,6 +516,7 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     Each sees all earlier tokens of its sequence, and of the call's own ones those that its
     row of ``mask`` names (`tree_mask`, or any int64 ``[T, words]``), or without a mask
     itself and those before it.  A row that sees nothing gives o = 0 and lse = -inf.
+    Calls that may run at the same time need a ``workspace`` each.
     Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens`` and ``max_seqlen``.
     Tokens no packed sequence owns give o = 0 and lse = -inf, or are left as they are in
     ``out``, a pair (o, lse) to write to.  ``workspace``: uint8, at least

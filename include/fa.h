@@ -384,7 +384,7 @@ fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_strea
  * base[i] + accepted[i], and pages past it are released.  path: device
  * [n, path_width], strictly ascending in its first accepted[i] entries.
  * accepted[i] = 0 drops the whole draft.  Pages that keep tokens behind
- * base[i] must not be shared.
+ * base[i] must not be shared, nor the page that is left partly filled.
  */
 fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* base, const int* path,
                           int path_width, const int* accepted, int n, fa_stream_t stream);
@@ -407,8 +407,9 @@ fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream);
  *   (Hq = 0: none), q_out contiguous.  rot, table, positions, interleaved as
  *   in fa_rotary (rot = 0: nothing turns); without positions a token's position
  *   is its place in the sequence.
- *   A token whose place is not in the cache sets the status word and is not
- *   written; one that no packed sequence owns has zeros in q_out.
+ *   A token whose place is not in the cache, or in a page that several sequences
+ *   share, sets the status word and is not written; one that no packed sequence
+ *   owns has zeros in q_out.
  */
 fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, int B, int N,
                           const int* cu_seqlens, int T, const void* q, void* q_out, int Hq,
@@ -452,6 +453,9 @@ fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, 
  *   or count does not fit sets the status word and its rows see nothing.
  *   Results do not vary from run to run.  A slot may be read by several
  *   sequences of a call.
+ *   Calls that may run at the same time need a workspace each; what it holds
+ *   does not matter, but for a captured call that is replayed after status bit
+ *   16: zero it then.
  *   Keys and values past a sequence's length never matter; those of drafted
  *   tokens matter only to the rows that see them, whatever they hold.
  */

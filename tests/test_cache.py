@@ -395,6 +395,32 @@ def test_append_refused_on_the_device():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 96])
+def test_append_leaves_shared_pages(d):
+    """After a fork the whole pages belong to both: rows of theirs are refused, the page that was
+    copied is not, and once the other sequence is gone they are written again."""
+    c, m = make(d=d)
+    c.reserve(ints([4]), ints([20]))
+    c.fork(ints([4]), ints([7]))
+    m.reserve([4], [20])
+    m.fork([4], [7])
+    k = torch.ones(6, 2, d).bfloat16().cuda()
+    q = fa.cache_append(c, 1, ints([7]), k, k, q=k)
+    page, _ = m.place(7, 16)
+    m.k[1, page, :, :4] = m.v[1, page, :, :4] = 1.0
+    assert status(c) == 8
+    agree(c, m)
+    assert torch.equal(q, k)
+    c.free(ints([4]))
+    m.free([4])
+    fa.cache_append(c, 1, ints([7]), k, k)
+    page, _ = m.place(7, 14)
+    m.k[1, page, :, 14:] = m.v[1, page, :, 14:] = 1.0
+    assert status(c) == 0
+    agree(c, m)
+
+
+@pytest.mark.gpu
 def test_captured_page_operations():
     """reserve, append, fork, accept and free in one graph, replayed, on lengths that change."""
     c, m = make(layers=2, d=64, pages=60)
