@@ -134,6 +134,7 @@ struct SeqInfo {
 
 __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int i) {
     SeqInfo s;
+    const int slot = p.slots[i];  // (in one trip with the boundaries)
     const SeqRange r = seq_range(p.cu, p.N, p.T, i);
     s.t0 = r.t0;
     s.n = r.n;
@@ -144,7 +145,7 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int i) {
         return s;
     }
     if (r.n == 0) return s;
-    s.slot = p.slots[i];
+    s.slot = slot;
     if (s.slot < 0 || s.slot >= p.cache.slots) {
         s.slot = 0;
         s.bad = kCacheBadSlot;
