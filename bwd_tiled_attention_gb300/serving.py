@@ -30,6 +30,7 @@ from . import FA_BF16, FA_FP32, FA_OK, FAError, lib
 __all__ = ["PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask"]
 
 _INT = (torch.int32,)
+_BF16 = (torch.bfloat16,)
 _HEAD_DIMS = (64, 96, 128, 192, 256)
 _PAGE_SIZES = (16, 32, 64, 128)
 _MOST = 2 ** 31 - 1  # counts are 32 bits
@@ -61,6 +62,9 @@ def _want(name, t, dtypes, ndim, device=None, contiguous=True):
 
 def _heads_tensor(name, t, dtypes, device=None):
     """A [T, H, d] tensor with free token and head strides."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 3 and t.stride(2) == 1 and
+            (device is None or t.device == device)):
+        return
     _want(name, t, dtypes, 3, device, contiguous=False)
     if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
         raise ValueError(f"{name} must be contiguous in its last dimension")
@@ -91,7 +95,7 @@ def _on(device, stream, tensors):
 
 def _here(device, stream):
     """Nothing to switch: the usual call."""
-    return stream is None and device.index == torch.cuda.current_device()
+    return stream is None and device.index == torch._C._cuda_getDevice()
 
 
 def _raw_stream(device):
@@ -267,13 +271,14 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
     first = q if q is not None else k
     if first is None:
         raise TypeError("rotary needs q or k")
-    for name, t in (("q", q), ("k", k)):
-        if t is not None:
-            _heads_tensor(name, t, (torch.bfloat16, torch.float32))
-            if t.dtype != first.dtype or t.device != first.device:
-                raise ValueError("q and k must have one type and device")
-            if t.shape[0] != first.shape[0] or t.shape[2] != first.shape[2]:
-                raise ValueError("q and k must have the same tokens and head dimension")
+    both = (torch.bfloat16, torch.float32)
+    _heads_tensor("q" if q is not None else "k", first, both)
+    if q is not None and k is not None:
+        _heads_tensor("k", k, both)
+        if k.dtype != q.dtype or k.device != q.device:
+            raise ValueError("q and k must have one type and device")
+        if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+            raise ValueError("q and k must have the same tokens and head dimension")
     T, dev = first.shape[0], first.device
     pos_bytes = _rotary_args(table, positions, T, dev)
     if 2 * table.shape[1] > first.shape[2]:
@@ -287,16 +292,12 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
     grad = torch.is_grad_enabled() and ((q is not None and q.requires_grad) or
                                         (k is not None and k.requires_grad))
 
-    def call():
-        if grad:
-            return _Rotary.apply(q, k, table, (positions, cu_seqlens),
-                                 (pos_bytes, B, N, interleaved, 0))
-        return tuple(_rotate(q, k, table, positions, pos_bytes, B, N, cu_seqlens, interleaved, 0))
-
-    if _here(dev, stream):
-        return call()
-    with _on(dev, stream, (q, k, table, positions, cu_seqlens)):
-        return call()
+    if not _here(dev, stream):
+        with _on(dev, stream, (q, k, table, positions, cu_seqlens)):
+            return rotary(q, k, table, positions, cu_seqlens, batch, interleaved)
+    if grad:
+        return _Rotary.apply(q, k, table, (positions, cu_seqlens), (pos_bytes, B, N, interleaved, 0))
+    return tuple(_rotate(q, k, table, positions, pos_bytes, B, N, cu_seqlens, interleaved, 0))
 
 
 # -------------------------------------------------------------------------------- cache
@@ -446,41 +447,41 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
     None.  Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens``.
     """
     n = _of_cache(cache, layer, slots)
-    bf16 = (torch.bfloat16,)
-    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() else 0
-    for name, t, heads in (("k", k, cache.heads), ("v", v, cache.heads), ("q", q, None)):
-        if t is None and name == "q":
-            continue
-        _heads_tensor(name, t, bf16, cache.device)
-        if t.shape[2] != cache.d or t.shape[0] != T or (heads and t.shape[1] != heads):
-            raise ValueError(f"{name} {tuple(t.shape)} does not fit the cache or k")
-    B, N = _sequences(T, n, cu_seqlens, None, cache.device, need_max=False)
+    dev = cache.device
+    if not _here(dev, stream):
+        with _on(dev, stream, cache._tensors + (slots, k, v, q, rotary, positions, cu_seqlens)):
+            return cache_append(cache, layer, slots, k, v, q, rotary, positions, interleaved, cu_seqlens)
+    _heads_tensor("k", k, _BF16, dev)
+    _heads_tensor("v", v, _BF16, dev)
+    T = k.shape[0]
+    if k.shape != v.shape or k.shape[1] != cache.heads or k.shape[2] != cache.d:
+        raise ValueError(f"k {tuple(k.shape)} or v {tuple(v.shape)} does not fit the cache")
+    if q is not None:
+        _heads_tensor("q", q, _BF16, dev)
+        if q.shape[0] != T or q.shape[2] != cache.d:
+            raise ValueError(f"q {tuple(q.shape)} does not fit the cache or k")
+    B, N = _sequences(T, n, cu_seqlens, None, dev, need_max=False)
     rot = rows = pos_bytes = 0
     if rotary is not None:
-        pos_bytes = _rotary_args(rotary, positions, T, cache.device)
+        pos_bytes = _rotary_args(rotary, positions, T, dev)
         rows, rot = rotary.shape[0], 2 * rotary.shape[1]
         if rot > cache.d:
             raise ValueError("the table turns more columns than a head has")
     elif positions is not None:
         raise ValueError("positions need a rotary table")
 
-    def call():
-        out = None if q is None else torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        qs = (0, 0, 0) if q is None else q.stride()
-        ks, vs = k.stride(), v.stride()
-        if T:
-            _check(lib().fa_cache_append(
-                cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, _ptr(q), _ptr(out),
-                0 if q is None else q.shape[1], qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
-                v.data_ptr(), vs[0], vs[1], rot, _ptr(rotary), rows, _ptr(positions), pos_bytes,
-                1 if interleaved else 0, _raw_stream(cache.device)), "fa_cache_append")
-        return out
-
-    if _here(cache.device, stream):
-        return call()
-    with _on(cache.device, stream,
-             cache._tensors + (slots, k, v, q, rotary, positions, cu_seqlens)):
-        return call()
+    out, Hq, qt, qh = None, 0, 0, 0
+    if q is not None:
+        out, Hq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev), q.shape[1]
+        qt, qh, _ = q.stride()
+    kt, kh, _ = k.stride()
+    vt, vh, _ = v.stride()
+    if T:
+        _check(lib().fa_cache_append(
+            cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, _ptr(q), _ptr(out), Hq,
+            qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, rot, _ptr(rotary), rows,
+            _ptr(positions), pos_bytes, 1 if interleaved else 0, _raw_stream(dev)), "fa_cache_append")
+    return out
 
 
 # ---------------------------------------------------------------------------- attention
@@ -524,7 +525,12 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     """
     n = _of_cache(cache, layer, slots)
     dev = cache.device
-    _heads_tensor("q", q, (torch.bfloat16,), dev)
+    if not _here(dev, stream):
+        with _on(dev, stream, cache._tensors + (q, slots, mask, cu_seqlens, workspace) +
+                 (tuple(out) if out is not None else ())):
+            return tree_attention(q, cache, layer, slots, mask, scale, cu_seqlens, max_seqlen, out,
+                                  workspace)
+    _heads_tensor("q", q, _BF16, dev)
     T, Hq, d = q.shape
     if d != cache.d:
         raise ValueError("q and the cache differ in head dimension")
@@ -546,25 +552,18 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     if workspace is not None:
         _want("workspace", workspace, (torch.uint8,), 1, dev)
 
-    def call():
-        if out is not None:
-            o, lse = out
-        else:
-            o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-            lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
-        if T == 0:
-            return o, lse
-        ws = workspace if workspace is not None else torch.empty(
-            max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16), dtype=torch.uint8, device=dev)
-        qs = q.stride()
-        _check(lib().fa_tree_fwd(
-            cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qs[0],
-            qs[1], _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, 1 if out is None else 0,
-            ws.data_ptr(), ws.numel(), _raw_stream(dev)), "fa_tree_fwd")
+    if out is not None:
+        o, lse = out
+    else:
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
+    if T == 0:
         return o, lse
-
-    if _here(dev, stream):
-        return call()
-    with _on(dev, stream, cache._tensors + (q, slots, mask, cu_seqlens, workspace) +
-             (tuple(out) if out is not None else ())):
-        return call()
+    ws = workspace if workspace is not None else torch.empty(
+        max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16), dtype=torch.uint8, device=dev)
+    qt, qh, _ = q.stride()
+    _check(lib().fa_tree_fwd(
+        cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
+        _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, 1 if out is None else 0,
+        ws.data_ptr(), ws.numel(), _raw_stream(dev)), "fa_tree_fwd")
+    return o, lse
