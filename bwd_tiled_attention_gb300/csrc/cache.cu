@@ -241,6 +241,8 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
         int bad = 0;
         if (!slot_ok(c, from) || !slot_ok(c, to)) bad = kCacheBadSlot;
         else {
+            const int* row = c.table + (long long)from * c.max_pages;
+            const int page0 = grp.sub < c.max_pages ? row[grp.sub] : -1;  // (in the lengths' trip)
             const int len = length_of(c, from), old = c.lengths[to];
             if (grp.sub == 0 && atomicCAS(&s.mark[to], -1, i) != -1) bad = kCacheBadSlot;
             if (len < 0 || old != 0) bad |= kCacheBadLength;
@@ -249,7 +251,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
                 e.w = len % c.page_size;
                 e.x = e.w > 0;
                 for (int k = grp.sub; k < e.y + e.x; k += grp.g) {
-                    const int p = c.table[(long long)from * c.max_pages + k];
+                    const int p = k == grp.sub ? page0 : row[k];
                     if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
                 }
             }
@@ -341,12 +343,14 @@ __global__ void __launch_bounds__(kPlan) free_kernel(const fa_cache c, const int
         int bad = 0;
         if (!slot_ok(c, slot)) bad = kCacheBadSlot;
         else {
+            const int* row = c.table + (long long)slot * c.max_pages;
+            const int page0 = grp.sub < c.max_pages ? row[grp.sub] : -1;  // (in the length's trip)
             const int len = length_of(c, slot);
             if (len < 0) bad = kCacheBadLength;
             else {
                 const int used = (len + c.page_size - 1) / c.page_size;
                 for (int k = grp.sub; k < used; k += grp.g) {
-                    const int p = c.table[(long long)slot * c.max_pages + k];
+                    const int p = k == grp.sub ? page0 : row[k];
                     if (p < 0 || p >= c.pages) bad = kCacheBadSlot;
                 }
             }
@@ -392,20 +396,30 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
         int bad = 0;
         if (!slot_ok(c, slot)) bad = kCacheBadSlot;
         else {
+            // what the checks look at first comes in one trip with the length: this
+            // lane's entry of the path and its page, wherever the length ends
+            const int* row = c.table + (long long)slot * c.max_pages;
+            const int k0 = b / c.page_size + grp.sub;
+            const int page0 = b >= 0 && k0 < c.max_pages ? row[k0] : -1;
+            int step0 = 0, prev0 = -1;
+            if (grp.sub < m && grp.sub < width) {
+                step0 = at[grp.sub];
+                if (grp.sub > 0) prev0 = at[grp.sub - 1];
+            }
             const int len = length_of(c, slot);
             const bool again = grp.sub == 0 && atomicCAS(&s.mark[slot], -1, i) != -1;
             if (grp.any(again)) bad = kCacheBadSlot;
             else if (len < 0 || b < 0 || b > len || m < 0 || m > width || m > len - b) bad = kCacheBadLength;
             else {
                 const int used = (len + c.page_size - 1) / c.page_size;
-                const int* row = c.table + (long long)slot * c.max_pages;
                 const int kept = (b + m + c.page_size - 1) / c.page_size;
                 for (int j = grp.sub; j < m; j += grp.g) {  // strictly ascending, within the draft
-                    const int t = at[j];
-                    if (t < 0 || t >= len - b || (j > 0 && at[j - 1] >= t)) bad |= kCacheBadLength;
+                    const int t = j == grp.sub ? step0 : at[j];
+                    const int before = j == grp.sub ? prev0 : at[j - 1];  // (-1 before the first)
+                    if (t < 0 || t >= len - b || before >= t) bad |= kCacheBadLength;
                 }
-                for (int k = b / c.page_size + grp.sub; k < used; k += grp.g) {
-                    const int p = row[k];
+                for (int k = k0; k < used; k += grp.g) {
+                    const int p = k == k0 ? page0 : row[k];
                     if (p < 0 || p >= c.pages) bad |= kCacheBadSlot;
                     else if (k < kept && c.refs[p] != 1) bad |= kCacheShared;
                     s.shadow[(long long)slot * c.max_pages + k] = p;
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
         const int used = (len + c.page_size - 1) / c.page_size;
         for (int k = (now + c.page_size - 1) / c.page_size + grp.sub; k < used; k += grp.g) {
             const long long at = (long long)slot * c.max_pages + k;
-            atomicSub(&c.refs[s.shadow[at]], 1);
+            atomicSub(&c.refs[c.table[at]], 1);
             c.table[at] = -1;
         }
         if (grp.sub == 0) c.lengths[slot] = now;
