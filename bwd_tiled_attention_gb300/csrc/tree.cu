@@ -108,13 +108,14 @@ struct Smem {
     alignas(1024) uint8_t kv[C::kStages][C::kStageBytes];
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
     uint64_t q_full, q_empty, piece_full[2], piece_empty[2];
-    uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain;
+    uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain, begun, stored;
     Piece piece[2];
     int start[4];        // this CTA's first item: sequence, kv head, row tile, key tile
     long long line[3];   // tiles of a CTA, and this CTA's stretch
     long long sums[kThreads / 32];
     Piece shared[2];     // fused: this CTA's pieces of items that it shares
     int n_shared, join_last[2];
+    int early;           // the first piece ends an item begun elsewhere: brought as soon as it is stored
     uint32_t tmem_base;
     int abort_flag, zero;
     int poison;          // a drafted V that is not finite has been met (never cleared)
@@ -175,14 +176,16 @@ __device__ __forceinline__ long long head_tiles(const TreeParams& p, const SeqIn
     const int nq = (s.n + tokens - 1) / tokens;
     if (p.mask || s.len == 0) return (long long)nq * item_tiles(p, s, 0, tokens, bn);
     long long sum = 0;
+#pragma unroll 1
     for (int q = 0; q < nq; ++q) sum += item_tiles(p, s, q, tokens, bn);
     return sum;
 }
 
 // a / b without a 64-bit division where both fit 32 bits (nearly always).
+__device__ __noinline__ long long divide_far(long long a, long long b) { return a / b; }
 __device__ __forceinline__ long long divide(long long a, long long b) {
     if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
-    return a / b;
+    return divide_far(a, b);
 }
 
 // Finds tile `at` (counted from the sequence's first) of sequence s.
@@ -196,6 +199,7 @@ __device__ __forceinline__ void locate(const TreeParams& p, const SeqInfo& s, lo
         k -= q * t;
         return;
     }
+#pragma unroll 1
     for (q = 0;; ++q) {
         const int t = item_tiles(p, s, q, tokens, bn);
         if (k < t) return;
@@ -432,6 +436,27 @@ __device__ __forceinline__ void join_row(const TreeParams& p, int slot_row, int 
     if (lane == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
+// One thread says that this CTA's partial of an item is there; true: it was the
+// last one.  The item's word counts those brought under this call's number;
+// anything else that it holds counts as none, and the last one clears it.
+__device__ __forceinline__ bool bring(const TreeParams& p, const Piece& x) {
+    fence_gpu();  // all partials of the CTA, before it says that they are there
+    unsigned long long* word = p.arrived + x.last_cta;
+    unsigned long long old = 0, now;  // (what the last call left, most often)
+    for (;;) {
+        now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
+        const unsigned long long seen = atomicCAS(word, old, now);
+        if (seen == old) break;
+        old = seen;
+    }
+    const bool last = (int)(now & 255) == x.last_cta - x.first_cta + 1;
+    if (last) {
+        *word = 0;
+        fence_gpu();
+    }
+    return last;
+}
+
 // D: tile columns; DR: head dimension in memory (96 runs on 128 columns whose
 // last 32 the TMA fills with zeros).
 template <int D, int DR, bool PAIR>
@@ -465,9 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         mbar_init(smem_u32(&sm.stat_full), 8);
         mbar_init(smem_u32(&sm.drain), 1);
+        mbar_init(smem_u32(&sm.begun), 1);
+        mbar_init(smem_u32(&sm.stored), 8);
         sm.abort_flag = sm.zero = sm.poison = 0;
         sm.start[0] = -1;
-        sm.n_shared = 0;
+        sm.n_shared = sm.early = 0;
         fence_barrier_init();
     }
     if (warp == 2) {
@@ -495,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         const int i0 = (all_threads ? (int)threadIdx.x : lane) * chunk, i1 = min(p.B, i0 + chunk);
         long long mine = 0;
         int bad = 0;
+#pragma unroll 1
         for (int i = i0; i < i1; ++i) {
             const SeqInfo s = seq_info(p, i);
             bad |= s.bad;
@@ -512,6 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             if (lane == 31) sm.sums[warp] = incl;
             __syncthreads();
             total = 0;
+#pragma unroll 1
             for (int w = 0; w < kThreads / 32; ++w) {
                 if (w < warp) before += sm.sums[w];
                 total += sm.sums[w];
@@ -526,6 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         long long at = before + incl - mine;  // first tile of this thread's sequences
         if (begin < end && begin >= at && begin < at + mine) {
+#pragma unroll 1
             for (int i = i0; i < i1; ++i) {
                 const SeqInfo s = chunk == 1 ? mine_info : seq_info(p, i);
                 const long long ht = head_tiles(p, s, tokens, BN), all = ht * p.cache.heads;
@@ -578,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 if (lane == 0) {
                     sm.piece[slot].b = -1;
                     mbar_arrive(smem_u32(&sm.piece_full[slot]));
+                    if (it == 0) mbar_arrive(smem_u32(&sm.begun));
                 }
                 break;
             }
@@ -607,6 +638,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 sm.piece[slot] = x;
                 if (x.part >= 0) sm.shared[sm.n_shared++] = x;  // the first and the last at most
                 mbar_arrive(smem_u32(&sm.piece_full[slot]));
+                if (!PAIR && it == 0) {
+                    sm.early = k0 > 0;
+                    mbar_arrive(smem_u32(&sm.begun));
+                }
             }
             __syncwarp();
 
@@ -1184,7 +1219,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[PAIR ? w : 0]));
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sm.o_free[PAIR ? w : 0]));
+                    if (!PAIR && it == 0) mbar_arrive(smem_u32(&sm.stored));
+                }
             }
             f += 2 * x.n;
             ++it;
@@ -1208,6 +1246,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             clear(0, skip);
             clear(used, p.T - used);
         }
+        if constexpr (!PAIR) {
+            // An item's end is brought while the CTA goes on, so that its beginning, which
+            // a CTA finishes last, is what completes it nearly always: a CTA then joins one
+            // item at its end, not up to two.
+            if (p.fused && warp_wait(smem_u32(&sm.begun), 0, stop, status) && sm.early &&
+                warp_wait(smem_u32(&sm.stored), 0, stop, status) && lane == 0)
+                sm.join_last[0] = bring(p, sm.shared[0]);
+        }
     }
 
     tc_fence_before();
@@ -1217,29 +1263,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         tmem_dealloc(tmem, 512);
     }
     if constexpr (!PAIR) {
-        // Whoever brings an item's last partial joins them.  The item's word counts
-        // those brought under this call's number; anything else that it holds counts
-        // as none, and the last one clears it.
+        // Whoever brings an item's last partial joins them.
         const int n = p.fused && !sm.abort_flag ? sm.n_shared : 0;
         if (n == 0) return;
-        if (threadIdx.x < n) {
-            const Piece& x = sm.shared[threadIdx.x];
-            fence_gpu();  // all partials of the CTA, before it says that they are there
-            unsigned long long* word = p.arrived + x.last_cta;
-            unsigned long long old = 0, now;  // (what the last call left, most often)
-            for (;;) {
-                now = (old >> 8) == p.call ? old + 1 : (p.call << 8) + 1;
-                const unsigned long long seen = atomicCAS(word, old, now);
-                if (seen == old) break;
-                old = seen;
-            }
-            const bool last = (int)(now & 255) == x.last_cta - x.first_cta + 1;
-            sm.join_last[threadIdx.x] = last;
-            if (last) {
-                *word = 0;
-                fence_gpu();
-            }
-        }
+        if (threadIdx.x >= sm.early && threadIdx.x < n)
+            sm.join_last[threadIdx.x] = bring(p, sm.shared[threadIdx.x]);
         __syncthreads();
         for (int r = warp; r < n * p.part_rows; r += kThreads / 32) {
             const int i = r >= p.part_rows, row = r - i * p.part_rows;
