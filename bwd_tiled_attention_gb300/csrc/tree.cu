@@ -30,11 +30,17 @@
 //     two row tiles and share each key tile (PAIR), since then the tensor core
 //     is the bound.  Above d = 128 TMEM holds one O: one stream with two S
 //     buffers, on tiles of 64 keys.
+//   - up to 32 rows at d = 64 (FEW) stand four times in the tile, and each lane
+//     quarter's warp works on a quarter of the keys: its P is 0 elsewhere, and the
+//     quarters' O add up at the end as the streams' do.  A tile's 32 KB take 1400
+//     cycles of memory there, and one warp's chain over 128 keys as many (64
+//     sequences of 4-8k tokens, 8 kv heads, 142 -> 135 us; trees of 5-26 over
+//     0.7-2k, 36.9 -> 35.0).  At d = 128 memory takes twice that, and loading Q four
+//     times and adding up O cost more than they gave (16 x 4 tokens 47 -> 50 us).
 //
 // Measured (GPU time): 64 sequences of 4-8k tokens, 32 + 8 heads of 128, one
-// token each, 241 us = 6.66 TB/s, 98% of the copy rate (d = 64 140 us at 5.5
-// TB/s, bound by the streams' chain of ~1500 cycles a tile; d = 256, 32
-// sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 350 us = 1130 TF/s
+// token each, 241 us = 6.66 TB/s, 98% of the copy rate (d = 64 135 us at 5.8
+// TB/s; d = 256, 32 sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 350 us = 1130 TF/s
 // (32 + 8 heads of 128), 345 us = 1150 TF/s (16 + 4 of 256); 4 trees of 64 over
 // 30k keys 135 us.  One token over 501 keys 14.4 us: ~3.5 us until the first
 // load, then one tile's chain, the join, and a CTA's first pass through its code.
@@ -64,15 +70,19 @@ namespace {
 constexpr int kThreads = 384;
 constexpr float kRescale = 8.0f;  // log2 units: P <= 256 before the reference moves
 
-template <int D, bool PAIR>
+// PAIR: two row tiles.  FEW (d = 64): up to 32 rows, which stand in all four lane
+// quarters of the tile; each quarter's warp takes a quarter of the keys.
+template <int D, bool PAIR, bool FEW>
 struct Cfg {
     static constexpr int kBN = D > 128 ? 64 : 128;       // keys of a tile
     static constexpr int kCols = D / 64;                 // 64-column boxes
     static constexpr int kQTiles = PAIR ? 2 : 1;
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kStageBytes = kBN * D * 2;      // one K or V tile
+    static constexpr int kXStep = 36;                    // FEW: floats of 32 columns of O in shared memory
+    static constexpr int kXBytes = FEW ? 2 * 128 * kXStep * 4 : 0;
     // what 227 KB leave beside Q, the alignment, and the barriers and statistics
-    static constexpr int kRoom = 232448 - 1024 - 5120 - kQTiles * kQBytes;
+    static constexpr int kRoom = 232448 - 1024 - 5120 - kQTiles * kQBytes - kXBytes;
     static constexpr int kMaxStages = kRoom / kStageBytes;
     static constexpr int kStages = kMaxStages > 8 ? 8 : kMaxStages;
     static constexpr int kStreams = D > 128 ? 1 : 2;     // O accumulators
@@ -88,6 +98,7 @@ struct Cfg {
     static constexpr int kPCol = D == 64 ? 384 : (kSepP ? 64 : 0), kPStep = D == 64 ? 64 : 128;
     static_assert(kStages >= 4, "the ring holds two K and two V tiles");
     static_assert(!PAIR || D <= 128, "two row tiles need two O accumulators");
+    static_assert(!FEW || (D == 64 && !PAIR), "a warpgroup adds up half of 64 columns at once");
 };
 
 // A stretch of one item's key tiles, worked on by one CTA.
@@ -101,14 +112,14 @@ struct Piece {
     int first_cta, last_cta;  // the CTAs that share the item
 };
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool FEW>
 struct Smem {
-    using C = Cfg<D, PAIR>;
+    using C = Cfg<D, PAIR, FEW>;
     alignas(1024) uint8_t q[C::kQTiles][C::kQBytes];
     alignas(1024) uint8_t kv[C::kStages][C::kStageBytes];
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
     uint64_t q_full, q_empty, piece_full[2], piece_empty[2];
-    uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain, begun, stored;
+    uint64_t s_full[2], p_full[2], p_hi[2], o_done[2], o_free[2], stat_full, drain, begun, stored, x_full[2];
     Piece piece[2];
     int start[4];        // this CTA's first item: sequence, kv head, row tile, key tile
     long long line[3];   // tiles of a CTA, and this CTA's stretch
@@ -121,12 +132,13 @@ struct Smem {
     int poison;          // a drafted V that is not finite has been met (never cleared)
     // row statistics that the two warpgroups exchange: [piece parity][stream][m, l]
     float stats[2][2][2][128];
+    alignas(16) float x[FEW ? 2 : 1][FEW ? 128 : 1][C::kXStep];  // FEW: O of a warpgroup's lanes
 };
 
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool FEW>
 constexpr size_t smem_bytes() {
-    static_assert(sizeof(Smem<D, PAIR>) + 1024 <= 232448, "shared memory exceeds 227 KB");
-    return sizeof(Smem<D, PAIR>) + 1024;
+    static_assert(sizeof(Smem<D, PAIR, FEW>) + 1024 <= 232448, "shared memory exceeds 227 KB");
+    return sizeof(Smem<D, PAIR, FEW>) + 1024;
 }
 
 struct SeqInfo {
@@ -436,6 +448,70 @@ __device__ __forceinline__ void join_row(const TreeParams& p, int slot_row, int 
     if (lane == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
+// FEW: the sums over lane quarters of columns [32 cc, 32 cc + 32) of a piece's
+// rows, eight of them by each warp: stored, or left as the piece's partial.
+template <int DR, int BN>
+__device__ __forceinline__ void store_few(const TreeParams& p, const Piece& x, const float (*o)[36],
+                                          const float (*stats)[2][128], bool two, int poison, int open,
+                                          int q4, int cc) {
+    const int lane = lane_id(), row = q4 * 8 + (lane >> 2), col = (lane & 3) * 8;
+    const int row_tok = row / p.group, head = x.h * p.group + row - row_tok * p.group;
+    if (row_tok >= x.ntok) return;
+    const size_t tok = (size_t)x.tok0 + row_tok;
+    float y[8];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        float4 a[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = *reinterpret_cast<const float4*>(&o[k * 32 + row][col + i]);
+        y[i] = (a[0].x + a[1].x) + (a[2].x + a[3].x);
+        y[i + 1] = (a[0].y + a[1].y) + (a[2].y + a[3].y);
+        y[i + 2] = (a[0].z + a[1].z) + (a[2].z + a[3].z);
+        y[i + 3] = (a[0].w + a[1].w) + (a[2].w + a[3].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) odd |= !(fabsf(y[i]) < INFINITY);
+    if (odd || poison) {
+        // A visible V that is not finite adds itself, its weight being positive: a
+        // drafted one was zeroed, and one of the context has made NaN of the quarters
+        // whose P is 0 there.  A row whose sum is NaN stays NaN.
+        float sum = 0.f, add[8] = {};
+        for (int i = 0; i < (two ? 2 : 1); ++i)
+            for (int k = 0; k < 4; ++k) sum += stats[i][1][k * 32 + row];
+        const uint32_t* words = p.mask
+            ? reinterpret_cast<const uint32_t*>(p.mask) + tok * (2 * (size_t)p.words) : nullptr;
+        const int limit = p.mask ? x.len : min(x.len, x.ctx + x.trow0 + row_tok + 1);
+        const int end = min(limit, (x.k0 + x.n) * BN), ps = p.cache.page_size;
+        for (int key = odd ? x.k0 * BN : max(open, x.k0 * BN); key < end && sum == sum; ++key) {
+            if (p.mask && !(mask_bits(words, 2 * p.words, key - x.ctx) & 1u)) continue;
+            const int page = p.cache.table[(long long)x.slot * p.cache.max_pages + key / ps];
+            if (page < 0 || page >= p.cache.pages) continue;
+            const uint16_t* v = static_cast<const uint16_t*>(p.cache.v) +
+                                ((((long long)p.layer * p.cache.pages + page) * p.cache.heads + x.h) * ps +
+                                 key % ps) * DR + cc * 32 + col;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t bits = v[i];
+                if (!finite_bf16(bits)) add[i] += __uint_as_float(bits << 16);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (add[i] != 0.f) y[i] = add[i];
+    }
+    if (x.part < 0) {
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR + cc * 32 + col) =
+            make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                       pack_bf16x2(y[6], y[7]));
+    } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + ((size_t)x.part * p.part_rows + row) * DR +
+                                                cc * 32 + col);
+        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
+        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
+}
+
 // One thread says that this CTA's partial of an item is there; true: it was the
 // last one.  The item's word counts those brought under this call's number;
 // anything else that it holds counts as none, and the last one clears it.
@@ -459,11 +535,11 @@ __device__ __forceinline__ bool bring(const TreeParams& p, const Piece& x) {
 
 // D: tile columns; DR: head dimension in memory (96 runs on 128 columns whose
 // last 32 the TMA fills with zeros).
-template <int D, int DR, bool PAIR>
+template <int D, int DR, bool PAIR, bool FEW>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TreeParams p) {
     pdl_trigger();
-    using C = Cfg<D, PAIR>;
-    using SM = Smem<D, PAIR>;
+    using C = Cfg<D, PAIR, FEW>;
+    using SM = Smem<D, PAIR, FEW>;
     constexpr int S = C::kStages, BN = C::kBN;
     extern __shared__ uint8_t smem_raw[];
     SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -487,6 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             mbar_init(smem_u32(&sm.p_hi[i]), 4);
             mbar_init(smem_u32(&sm.o_done[i]), 1);
             mbar_init(smem_u32(&sm.o_free[i]), PAIR ? 4 : 8);
+            mbar_init(smem_u32(&sm.x_full[i]), 4);
         }
         mbar_init(smem_u32(&sm.stat_full), 8);
         mbar_init(smem_u32(&sm.drain), 1);
@@ -650,11 +727,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 if (lane == 0) {
                     const uint32_t bar = smem_u32(&sm.q_full);
                     const int nt = PAIR && x.ntok > p.tile_tokens ? 2 : 1;
-                    mbar_arrive_expect_tx(bar, nt * p.tile_tokens * p.group * 128 * C::kCols);
+                    constexpr int copies = FEW ? 4 : 1;
+                    mbar_arrive_expect_tx(bar, nt * copies * p.tile_tokens * p.group * 128 * C::kCols);
                     for (int t = 0; t < nt; ++t)
                         for (int c = 0; c < C::kCols; ++c)
-                            tma_load_4d(smem_u32(sm.q[t]) + c * 16384, &p.tm_q, bar, c * 64, 0, x.h,
-                                        x.tok0 + t * p.tile_tokens);
+                            for (int y = 0; y < copies; ++y)  // (32 rows of 128 bytes apart)
+                                tma_load_4d(smem_u32(sm.q[t]) + c * 16384 + y * 4096, &p.tm_q, bar,
+                                            c * 64, 0, x.h, x.tok0 + t * p.tile_tokens);
                 }
                 __syncwarp();
                 ++nq;
@@ -747,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk) {
-                    if (kk == BN / 32) {
+                    if (!FEW && kk == BN / 32) {
                         if (!wait(sm.p_hi[buf], c)) return;
                         tc_fence_after();
                     }
@@ -846,12 +925,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         setmaxnreg_inc<kManyRegs>();
         const int w = (warp - 4) >> 2;          // stream
         const int q4 = warp & 3;                // TMEM lane quarter
-        const int row = q4 * 32 + lane;
+        const int at = q4 * 32 + lane;          // lane of TMEM
+        const int row = FEW ? lane : at;
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
         const int row_tok = row / p.group, row_head = row - row_tok * p.group;
         const bool row_used = row_tok < p.tile_tokens;
         int it = 0, f = 0, cnt[2] = {0, 0};
         bool ok = true;
+        if constexpr (FEW) {  // a lane's P of the other quarters' keys: none, for good
+            const uint32_t none[16] = {};
+            for (int i = 0; i < BN / 2; i += 16)
+                tmem_st16(tmem + lane_off + C::kPCol + w * C::kPStep + i, none);
+            tmem_st_wait();
+        }
         while (ok) {
             const int slot = it & 1;
             if (!(ok = warp_wait(smem_u32(&sm.piece_full[slot]), (it >> 1) & 1, stop, status))) break;
@@ -894,27 +980,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         const int fv = f + fifo_v<PAIR>(j, x.n);
                         if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
                             break;
-                        if (row < BN && key0 + row >= open) {
-                            uint8_t* at = sm.kv[fv % S] + row * 128;
-                            const bool past = key0 + row >= x.len;
+                        if (at < BN && key0 + at >= open) {
+                            uint8_t* rest = sm.kv[fv % S] + at * 128;
+                            const bool past = key0 + at >= x.len;
 #pragma unroll 1
-                            for (int cb = 0; cb < C::kCols; ++cb, at += BN * 128) {
+                            for (int cb = 0; cb < C::kCols; ++cb, rest += BN * 128) {
                                 // (chunks in an order of the row's own, which spreads the banks)
-                                uint4* line = reinterpret_cast<uint4*>(at);
+                                uint4* line = reinterpret_cast<uint4*>(rest);
                                 uint4 v[8];
                                 uint32_t bad = 0;
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) v[e] = line[(e + row) & 7];
+                                for (int e = 0; e < 8; ++e) v[e] = line[(e + at) & 7];
 #pragma unroll
                                 for (int e = 0; e < 8; ++e)
                                     bad |= not_finite(v[e].x) | not_finite(v[e].y) | not_finite(v[e].z) |
                                            not_finite(v[e].w);
                                 if (past) {
 #pragma unroll
-                                    for (int e = 0; e < 8; ++e) line[(e + row) & 7] = make_uint4(0u, 0u, 0u, 0u);
+                                    for (int e = 0; e < 8; ++e) line[(e + at) & 7] = make_uint4(0u, 0u, 0u, 0u);
                                 } else if (bad) {
                                     *reinterpret_cast<volatile int*>(&sm.poison) = 1;
-                                    uint16_t* value = reinterpret_cast<uint16_t*>(at);
+                                    uint16_t* value = reinterpret_cast<uint16_t*>(rest);
                                     for (int e = 0; e < 64; ++e)
                                         if (!finite_bf16(value[e])) value[e] = 0;
                                 }
@@ -944,8 +1030,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         else if (room < 32) bits &= (1u << room) - 1u;
                         return bits;
                     };
-                    float s[C::kWhole ? BN : 1];
-                    if constexpr (C::kWhole) {
+                    float s[FEW ? 32 : C::kWhole ? BN : 1];
+                    if constexpr (FEW) {
+                        // this quarter's 32 keys
+                        if (warp_valid) {
+                            uint32_t r[32];
+                            tmem_ld32(s_at + q4 * 32, r);
+                            tmem_ld_wait();
+                            const uint32_t bits = ragged ? key_bits(key0 + q4 * 32) : 0xffffffffu;
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                s[i] = (bits >> i) & 1u ? __uint_as_float(r[i]) : -INFINITY;
+                            float m4[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float m = fmaxf(s[k], s[28 + k]);
+#pragma unroll
+                                for (int i = 4; i < 28; i += 8) m = fmax3(m, s[i + k], s[i + 4 + k]);
+                                m4[k] = m;
+                            }
+                            take_max(fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * p.scale_log2);
+                        }
+                    } else if constexpr (C::kWhole) {
                         // the whole row in registers, all loads in flight
                         if (warp_valid) {
                             uint32_t r[BN / 32][32];
@@ -1049,7 +1155,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         }
                     }
                     uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                    if constexpr (C::kWhole) {
+                    if constexpr (FEW) {
+                        if (warp_valid) {
+                            uint32_t pk[16];
+                            exp_chunk(s, p.scale_log2, neg, acc, pk);
+                            tmem_st16(p_at + q4 * 16, pk);
+                            tmem_st_wait();
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[buf]));
+                    } else if constexpr (C::kWhole) {
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
                             if (warp_valid) {
@@ -1107,16 +1223,28 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 // every other 32 columns
                 auto& st = sm.stats[it & 1];
                 if (w < C::kStreams) {
-                    st[w][0][row] = m_ref;
-                    st[w][1][row] = l;
+                    st[w][0][at] = m_ref;
+                    st[w][1][at] = l;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.stat_full));
                 if (!(ok = warp_wait(smem_u32(&sm.stat_full), it & 1, stop, status))) break;
-                m_ref = st[0][0][row];
-                l = st[0][1][row];
-                if (two) {
-                    const float m1 = st[1][0][row], l1 = st[1][1][row];
+                m_ref = st[0][0][at];
+                l = st[0][1][at];
+                if constexpr (FEW) {
+                    // this lane's weights, and the row's sums over quarters and streams
+                    const float m0 = m_ref, m1 = st[1][0][at];
+                    for (int i = 0; i < (two ? 2 : 1); ++i)
+                        for (int k = 0; k < 4; ++k) m_ref = fmaxf(m_ref, st[i][0][k * 32 + lane]);
+                    const float base = m_ref == -INFINITY ? 0.f : m_ref;
+                    l = 0.f;
+                    for (int i = 0; i < (two ? 2 : 1); ++i)
+                        for (int k = 0; k < 4; ++k)
+                            l += st[i][1][k * 32 + lane] * ex2_approx(st[i][0][k * 32 + lane] - base);
+                    w0 = ex2_approx(m0 - base);
+                    if (two) w1 = ex2_approx(m1 - base);
+                } else if (two) {
+                    const float m1 = st[1][0][at], l1 = st[1][1][at];
                     const float m = fmaxf(m_ref, m1), base = m == -INFINITY ? 0.f : m;
                     w0 = ex2_approx(m_ref - base);
                     w1 = ex2_approx(m1 - base);
@@ -1142,7 +1270,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 const int poison = *reinterpret_cast<volatile int*>(&sm.poison);
                 const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
                 const int head = x.h * p.group + row_head;
-                if (valid && (PAIR || w == 0)) {
+                if (valid && (PAIR || w == 0) && (!FEW || q4 == 0)) {
                     if (x.part < 0) {
                         p.lse[(size_t)head * p.T + tok] = (m_ref + __log2f(l)) * 0.69314718055994531f;
                     } else {
@@ -1174,6 +1302,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         if (x.part < 0) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] *= inv;
+                        }
+                        if constexpr (FEW) {
+                            // The quarters' O add up through shared memory; each warp then
+                            // stores eight of the rows.  (All have read the last piece's: they
+                            // have brought this piece's statistics.)
+                            float4* line = reinterpret_cast<float4*>(sm.x[w][at]);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                line[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(smem_u32(&sm.x_full[w]));
+                            if (!(ok = warp_wait(smem_u32(&sm.x_full[w]), it & 1, stop, status))) break;
+                            store_few<DR, BN>(p, x, sm.x[w], sm.stats[it & 1], two, poison, open, q4, cc);
+                            continue;
                         }
                         if (poison && valid) {
                             // a visible drafted V that is not finite: its weight is
@@ -1217,6 +1359,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         }
                     }
                 }
+                if (FEW && !ok) break;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -1318,10 +1461,10 @@ __global__ void tree_mask_kernel(const int* parents, const int* cu, int B, int N
     }
 }
 
-template <int D, int DR, bool PAIR>
+template <int D, int DR, bool PAIR, bool FEW = false>
 cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
-    auto kern = tree_kernel<D, DR, PAIR>;
-    constexpr size_t smem = smem_bytes<D, PAIR>();
+    auto kern = tree_kernel<D, DR, PAIR, FEW>;
+    constexpr size_t smem = smem_bytes<D, PAIR, FEW>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
@@ -1464,7 +1607,9 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     else if (d == 96)
         e = tiles.pair ? launch_t<128, 96, true>(p, ctas, strm) : launch_t<128, 96, false>(p, ctas, strm);
     else if (d == 64)
-        e = tiles.pair ? launch_t<64, 64, true>(p, ctas, strm) : launch_t<64, 64, false>(p, ctas, strm);
+        e = tiles.pair ? launch_t<64, 64, true>(p, ctas, strm)
+            : p.fused  ? launch_t<64, 64, false, true>(p, ctas, strm)
+                       : launch_t<64, 64, false>(p, ctas, strm);
     else if (d == 192)
         e = launch_t<192, 192, false>(p, ctas, strm);
     else

@@ -275,6 +275,23 @@ def test_values_of_the_context_reach_every_row():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,n", [(64, 2, 1), (64, 3, 4), (64, 32, 1), (64, 40, 1), (128, 2, 4), (256, 2, 3)])
+def test_infinite_values_of_the_context(d, Hq, n):
+    """Single columns of V that are infinite or NaN, in one sequence that several CTAs share and in
+    many that one CTA has to itself: the same columns come out infinite or NaN, in every row."""
+    for lengths in ([700 + n], [130 + n] * 330):
+        h = Held(lengths, 1, d, 16, seed=d + n)
+        for i in range(0, len(lengths), 3):
+            for pos, special in ((9, {3: INF}), (77, {3: INF, 5: -INF, 7: NAN, 33: INF}), (110, {5: INF})):
+                row = torch.randn(d).bfloat16().float()
+                for c, value in special.items():
+                    row[c] = value
+                h.put("v", i, pos, row)
+        q = queries(n * len(lengths), Hq, d)
+        check(h, [n] * len(lengths), q, run(h, q, [n] * len(lengths)))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Hq,heads,d,ps,tree", [(8, 2, 128, 64, True), (4, 4, 64, 16, False),
                                                 (2, 1, 256, 128, True), (32, 8, 128, 128, False)])
 def test_long_contexts(Hq, heads, d, ps, tree):

@@ -15,6 +15,8 @@ Layouts modelled:
 - sep (alternate-sep and pair-sep, d = 64; one-sep, d > 128): P in TMEM columns of its own, so that a
   stream's next scores are issued without waiting for its last PV; the softmax
   waits for that PV before it writes the next P.
+- few (few-sep, d = 64): up to 32 rows in all four lane quarters, whose warps hand over P at once
+  and add up their O in shared memory.
 - pair: two row tiles that share every key tile, one stream each (d <= 128,
   more than 128 rows); the second may have no rows.
 
@@ -41,6 +43,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
     """pieces: list of (n key tiles, row tiles, first ragged tile)."""
     sep = layout.endswith("-sep")
     layout = layout.replace("-sep", "")
+    few = layout == "few"
     pair, streams = layout == "pair", 1 if layout == "one" else 2
     sim = Sim(pieces, seed, consumers=2 + 2 * warps)
     for b in (0, 1):
@@ -50,6 +53,8 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
             sim.bar(f"{name}{b}", warps)
         sim.bar(f"o_free{b}", warps if pair else 2 * warps)
     sim.bar("stat_full", 2 * warps)
+    for w in (0, 1):
+        sim.bar(f"x_full{w}", warps)
     for name in ("q_full", "q_empty"):
         sim.bar(name)
     for s in range(stages):
@@ -57,7 +62,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
         sim.bar(f"empty{s}")
     smem = {}
     st = {"S": {}, "P": {}, "O": {0: [], 1: []}, "read": {}, "q_read": True, "mended": {},
-          "stat": {}}
+          "stat": {}, "x": {}, "x_read": {}}
 
     def load(tag, f):
         s = f % stages
@@ -130,7 +135,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
 
             def pv(no, buf, o, c, j, first):
                 sim.pipe.append(("PV", (uid, buf, o, j, no % stages, 0, first)))
-                if mistake != "no_p_hi_wait":
+                if mistake != "no_p_hi_wait" and not few:
                     while not sim.ready(f"p_hi{buf}", c & 1, c + 1):
                         yield
                 sim.pipe.append(("PV", (uid, buf, o, j, no % stages, 1, False)))
@@ -263,14 +268,15 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                             yield
                     if st["O"][o] != [(uid, x, h) for x in seen for h in (0, 1)]:
                         raise Hazard(f"rescale of ({uid},{j}) saw O = {st['O'][o]}")
-                for hf, bar in ((0, "p_full"), (1, "p_hi")):
+                for hf, bar in ((0, None), (1, "p_full")) if few else ((0, "p_full"), (1, "p_hi")):
                     yield
                     if st["S"].get(b) != (uid, j):
                         raise Hazard("S overwritten while the softmax read it")
                     if sep and st["P"].get((b, hf), {}).get(q, "read") != "read":
                         raise Hazard(f"P of ({uid},{j}) written over one not yet read")
                     st["P"].setdefault((b, hf), {})[q] = (uid, j)
-                    sim.bars[f"{bar}{b}"].arrive((uid, j))
+                    if bar:
+                        sim.bars[f"{bar}{b}"].arrive((uid, j))
                 seen.append(j)
                 yield
             # epilogue
@@ -287,7 +293,7 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                 if w < streams:
                     st["stat"][(slot, w, q)] = uid
                 sim.bars["stat_full"].arrive(uid)
-                while not sim.ready("stat_full", it & 1, it + 1):
+                while mistake != "no_stat_wait" and not sim.ready("stat_full", it & 1, it + 1):
                     yield
                 yield
                 for x in range(streams):
@@ -307,6 +313,20 @@ def run_pieces(layout, pieces, seed, stages, mistake=None, warps=1):
                     if tiles and st["O"][o] != [(uid, x, h) for x in tiles for h in (0, 1)]:
                         raise Hazard(f"epilogue {w}.{q} of {uid} read O_{o} = {st['O'][o]}")
                 yield
+            if few:
+                if len(st["x_read"].get((w, q), range(warps))) != warps:
+                    raise Hazard(f"O of {uid} written over a quarter that is not read")
+                st["x"][(w, q)], st["x_read"][(w, q)] = uid, set()
+                sim.bars[f"x_full{w}"].arrive(uid)
+                if mistake != "no_x_full_wait":
+                    while not sim.ready(f"x_full{w}", it & 1, it + 1):
+                        yield
+                yield
+                for k in range(warps):
+                    if st["x"].get((w, k)) != uid:
+                        raise Hazard(f"{uid} added up {st['x'].get((w, k))}")
+                    yield
+                    st["x_read"][(w, k)].add(q)
             if reads:
                 if q == 0:
                     sim.out.append((uid, w))
@@ -363,7 +383,8 @@ def random_pieces(rnd, layout):
 
 
 LAYOUTS = [("alternate", 5), ("alternate", 8), ("one", 4), ("one", 7), ("pair", 4), ("pair", 8),
-           ("alternate-sep", 8), ("pair-sep", 8), ("one-sep", 4), ("one-sep", 7)]
+           ("alternate-sep", 8), ("pair-sep", 8), ("one-sep", 4), ("one-sep", 7),
+           ("few-sep", 5), ("few-sep", 8)]
 
 
 @pytest.mark.parametrize("warps", [1, 4])
@@ -388,6 +409,9 @@ MISTAKES = [
     ("alternate-sep", 8, "no_p_free_wait", False), ("pair-sep", 8, "no_p_free_wait", False),
     ("one-sep", 4, "no_p_free_wait", False), ("one-sep", 4, "no_rescale_wait", True),
     ("alternate-sep", 8, "no_p_hi_wait", True),
+    ("few-sep", 8, "no_x_full_wait", True), ("few-sep", 8, "no_stat_wait", True),
+    ("few-sep", 5, "no_q_empty_wait", True), ("few-sep", 8, "no_mend_wait", True),
+    ("few-sep", 8, "no_p_free_wait", False),
     ("pair", 4, "pair_order", True), ("pair", 4, "no_empty_wait", True),
 ]
 
