@@ -104,7 +104,8 @@ struct TreeParams {
     unsigned long long call;       // fused: this call's number (56 bits)
     int fused;                     // the last CTA of an item joins its partials
     float* part_stats;             // [2 * CTAs, part_rows, 2]: m and l
-    float* part_o;                 // [2 * CTAs, part_rows, d], not normalised
+    float* part_o;                 // not normalised: [2 * CTAs, part_rows, d] if fused,
+                                   // else [2 * CTAs, d / 4, part_rows, 4]
     int part_rows;
     int layer, B, N, T, Hq, group;
     int words, page_shift;         // page_size = 1 << page_shift

@@ -1350,12 +1350,16 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                                                     pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
                                                     pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
                         } else if (valid) {
-                            float4* dst = reinterpret_cast<float4*>(
-                                p.part_o + ((size_t)x.part * p.part_rows + (PAIR ? w * 128 : 0) + row) *
-                                               DR + cc * 32);
+                            // many rows: columns in fours, rows next to one another, so that a
+                            // warp's stores are contiguous
+                            const int step = p.fused ? 1 : p.part_rows;
+                            const int r = (PAIR ? w * 128 : 0) + row;
+                            float4* dst = reinterpret_cast<float4*>(p.part_o) +
+                                          (size_t)x.part * p.part_rows * (DR / 4) +
+                                          (p.fused ? r * (DR / 4) + cc * 8 : r + cc * 8 * step);
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
-                                dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                                dst[i * step] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                         }
                     }
                 }
@@ -1425,18 +1429,67 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
 // Joins the partials of every item that more than one CTA worked on: the CTA
 // whose first piece ends the item left (first CTA, token, tokens, head) in
-// meta.  One warp a row.
+// meta.  A thread takes eight columns of a row, the rows of a warp are
+// neighbours; partials are added in the CTAs' order, rescaled as the maximum
+// moves.
 template <int DR>
 __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
     pdl_begin();
     const int4 own = p.meta[blockIdx.x];
-    const int slot_row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int e = blockIdx.y * 256 + threadIdx.x;
+    const int c8 = e / p.part_rows, slot_row = e - c8 * p.part_rows;
     const int stream = slot_row >> 7, row = slot_row & 127;
     const int row_tok = row / p.group;
     const int t = stream * p.tile_tokens + row_tok;
-    if (own.x >= 0 && slot_row < p.part_rows && row_tok < p.tile_tokens && t < own.z)
-        join_row<DR>(p, slot_row, own.x, (int)blockIdx.x - own.x + 1, (size_t)own.y + t,
-                     own.w * p.group + row - row_tok * p.group);
+    if (own.x < 0 || c8 >= DR / 8 || row_tok >= p.tile_tokens || t >= own.z) return;
+    constexpr int R = 4;  // partials in flight
+    const int n = (int)blockIdx.x - own.x + 1;
+    float m = -INFINITY, l = 0.f, acc[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += R) {
+        float2 st[R];
+        float4 x[R][2];
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            st[u] = make_float2(-INFINITY, 0.f);
+            x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + u < n) {  // slot 2c + 1 of the first CTA, 2c of the others
+                const size_t slot = 2 * (own.x + i0 + u) + (i0 + u == 0);
+                const float4* at = reinterpret_cast<const float4*>(p.part_o) +
+                                   (slot * (DR / 4) + 2 * c8) * p.part_rows + slot_row;
+                st[u] = __ldcg(reinterpret_cast<const float2*>(p.part_stats) + slot * p.part_rows + slot_row);
+                x[u][0] = __ldcg(at);
+                x[u][1] = __ldcg(at + p.part_rows);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < R; ++u) top = fmaxf(top, st[u].x);
+        const float base = top == -INFINITY ? 0.f : top, keep = ex2_approx(m - base);
+        m = top;
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] *= keep;
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+            if (i0 + u >= n) continue;
+            const float w = ex2_approx(st[u].x - base);
+            l = fmaf(st[u].y, w, l);
+            acc[0] = fmaf(x[u][0].x, w, acc[0]); acc[1] = fmaf(x[u][0].y, w, acc[1]);
+            acc[2] = fmaf(x[u][0].z, w, acc[2]); acc[3] = fmaf(x[u][0].w, w, acc[3]);
+            acc[4] = fmaf(x[u][1].x, w, acc[4]); acc[5] = fmaf(x[u][1].y, w, acc[5]);
+            acc[6] = fmaf(x[u][1].z, w, acc[6]); acc[7] = fmaf(x[u][1].w, w, acc[7]);
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const size_t tok = (size_t)own.y + t;
+    const int head = own.w * p.group + row - row_tok * p.group;
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + (tok * p.Hq + head) * DR + c8 * 8) =
+        make_uint4(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv),
+                   pack_bf16x2(acc[4] * inv, acc[5] * inv), pack_bf16x2(acc[6] * inv, acc[7] * inv));
+    if (c8 == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
 // Ancestor bits of drafted trees: token t of a sequence sees itself, its
@@ -1469,7 +1522,7 @@ cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
     if (e != cudaSuccess || p.fused) return e;
-    return launch_pdl(tree_join_kernel<DR>, dim3(ctas, cdiv(p.part_rows, 8)), dim3(256), 0, stream, p);
+    return launch_pdl(tree_join_kernel<DR>, dim3(ctas, cdiv(p.part_rows * (DR / 8), 256)), dim3(256), 0, stream, p);
 }
 
 // Row tiles: as many whole tokens (of group rows each) as 128 rows hold; more
