@@ -39,11 +39,11 @@
 //     times and adding up O cost more than they gave (16 x 4 tokens 47 -> 50 us).
 //
 // Measured (GPU time): 64 sequences of 4-8k tokens, 32 + 8 heads of 128, one
-// token each, 241 us = 6.66 TB/s, 98% of the copy rate (d = 64 135 us at 5.8
-// TB/s; d = 256, 32 sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 350 us = 1130 TF/s
-// (32 + 8 heads of 128), 345 us = 1150 TF/s (16 + 4 of 256); 4 trees of 64 over
-// 30k keys 135 us.  One token over 501 keys 14.4 us: ~3.5 us until the first
-// load, then one tile's chain, the join, and a CTA's first pass through its code.
+// token each, 243 us = 6.6 TB/s, 97% of the copy rate (d = 64 135 us at 5.8 TB/s;
+// d = 256, 32 sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 340 us =
+// 1165 TF/s (32 + 8 heads of 128), 340 us = 1170 TF/s (16 + 4 of 256); 4 trees of
+// 64 over 30k keys 127 us.  One token over 501 keys 14.4 us: ~2.6 us of lookups and
+// arithmetic, ~2 us until the first tile is there, its chain, the join.
 //
 // Pages hold whatever was there before: keys past the length never reach a
 // sum (their scores are replaced, their V rows zeroed in shared memory), and
