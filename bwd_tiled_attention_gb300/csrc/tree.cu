@@ -1431,9 +1431,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 // whose first piece ends the item left (first CTA, token, tokens, head) in
 // meta.  A thread takes eight columns of a row, the rows of a warp are
 // neighbours; partials are added in the CTAs' order, rescaled as the maximum
-// moves.
+// moves.  Mostly two or three partials, and latency: more blocks to an SM count
+// for as much as more loads in flight (2048-token chunks, 2 / 3 / 4 / 8 in flight:
+// 338.8 / 338.9 / 340.3 / 344 us; 19 partials of 128 rows: 39.4 / 38.8 / 38.4 / 38.8).
 template <int DR>
-__global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ TreeParams p) {
+__global__ void __launch_bounds__(256, 4) tree_join_kernel(const __grid_constant__ TreeParams p) {
     pdl_begin();
     const int4 own = p.meta[blockIdx.x];
     const int e = blockIdx.y * 256 + threadIdx.x;
@@ -1442,7 +1444,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const __grid_constant__ 
     const int row_tok = row / p.group;
     const int t = stream * p.tile_tokens + row_tok;
     if (own.x < 0 || c8 >= DR / 8 || row_tok >= p.tile_tokens || t >= own.z) return;
-    constexpr int R = 4;  // partials in flight
+    constexpr int R = 3;
     const int n = (int)blockIdx.x - own.x + 1;
     float m = -INFINITY, l = 0.f, acc[8];
 #pragma unroll
