@@ -88,7 +88,7 @@ def _on(device, stream, tensors):
             stream = torch.cuda.ExternalStream(int(stream), device=device)
         with torch.cuda.stream(stream):
             for t in tensors:
-                if t is not None:
+                if isinstance(t, torch.Tensor) and t.is_cuda:  # (what else is given is refused later)
                     t.record_stream(stream)
             yield
 

@@ -451,6 +451,30 @@ def test_tensor_api_refuses():
 
 
 @pytest.mark.gpu
+def test_refusals_do_not_depend_on_the_stream():
+    h = Held([20], 2, 64, 16)
+    side, s, x = torch.cuda.Stream(), ints(h.slots), torch.zeros(1, 2, 64).bfloat16()
+    tab = fa.rotary_table(64, 32)
+    for kw in ({}, dict(stream=side)):
+        with pytest.raises(ValueError, match="must be on"):
+            fa.tree_attention(x, h.cache, 0, s, **kw)
+        with pytest.raises(ValueError, match="must be on"):
+            fa.cache_append(h.cache, 0, s, x, x.cuda(), **kw)
+        with pytest.raises(TypeError, match="must be a torch.Tensor"):
+            fa.cache_append(h.cache, 0, s, x.cuda(), [1.0], **kw)
+        with pytest.raises(TypeError, match="must be a PagedCache"):
+            fa.cache_append(None, 0, s, x.cuda(), x.cuda(), **kw)
+        with pytest.raises(ValueError, match="int32"):
+            h.cache.free(s.long(), **kw)
+        with pytest.raises((TypeError, ValueError)):
+            fa.rotary(x.cuda(), [1.0], tab, batch=1, **kw)
+        with pytest.raises(ValueError, match="must be on"):
+            fa.rotary(x.cuda(), None, tab, positions=torch.zeros(1, dtype=torch.int32), **kw)
+    side.synchronize()
+    h.cache.check()
+
+
+@pytest.mark.gpu
 def test_results_do_not_vary():
     counts = [30, 1, 64]
     h = Held([5030, 9000, 700], 2, 128, 64, layers=1, layer=0)
