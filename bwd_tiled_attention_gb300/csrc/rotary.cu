@@ -96,6 +96,24 @@ struct alignas(VW * sizeof(E)) Vec {
     E e[VW];
 };
 
+// Data is read and written once: lines that leave the caches first (2 x 8192
+// tokens 61.6 -> 57.6 us, appended prompts 47.6 -> 46.8; as whole 16-byte values,
+// not as elements, 53.5 -> 47.6).
+template <typename V>
+__device__ __forceinline__ V load_once(const void* p) {
+    if constexpr (sizeof(V) == 16) {
+        const uint4 y = __ldcs(static_cast<const uint4*>(p));
+        return *reinterpret_cast<const V*>(&y);
+    } else {
+        return *static_cast<const V*>(p);
+    }
+}
+template <typename V>
+__device__ __forceinline__ void store_once(void* p, const V& v) {
+    if constexpr (sizeof(V) == 16) __stcs(static_cast<uint4*>(p), *reinterpret_cast<const uint4*>(&v));
+    else *static_cast<V*>(p) = v;
+}
+
 // Where the two halves of a pair are: in one access (kInter: pairs (2i, 2i + 1)),
 // in two accesses of the thread (kTwo), or in the accesses of two lanes of a
 // warp, which exchange them (kShuffle: half layout, a head's row in one warp).
@@ -170,8 +188,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 #pragma unroll
     for (int h = 0; h < kHeadsPerThread; ++h) {
         if (h < nh) {
-            x0[h] = *reinterpret_cast<const V*>(src + h * p.hs[seg] + c0);
-            if (c1 >= 0) x1[h] = *reinterpret_cast<const V*>(src + h * p.hs[seg] + c1);
+            x0[h] = load_once<V>(src + h * p.hs[seg] + c0);
+            if (c1 >= 0) x1[h] = load_once<V>(src + h * p.hs[seg] + c1);
         }
     }
 
@@ -311,8 +329,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
 #pragma unroll
     for (int h = 0; h < kHeadsPerThread; ++h) {
         if (h < nh) {
-            *reinterpret_cast<V*>(dst + h * hs + c0) = x0[h];
-            if (c1 >= 0) *reinterpret_cast<V*>(dst + h * hs + c1) = x1[h];
+            store_once(dst + h * hs + c0, x0[h]);
+            if (c1 >= 0) store_once(dst + h * hs + c1, x1[h]);
         }
     }
 }
