@@ -1377,12 +1377,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else {
         // ------------------------------------------------------------ warp 2
         setmaxnreg_dec<kFewRegs>();
-        if (p.zero_rest && p.cu) {  // tokens that no sequence owns: before the first one's and
-                                    // behind the last one's
-            const int skip = min(max(p.cu[0], 0), p.T), used = min(max(p.cu[p.B], skip), p.T);
-            const long long step = (long long)gridDim.x * 32;
-            const long long at = (long long)blockIdx.x * 32 + lane;
-            auto clear = [&](int t0, int n) {
+        if (p.zero_rest && p.cu) {  // tokens that no sequence owns
+            auto clear = [&](int t0, int n, long long at, long long step) {
                 const long long rows = (long long)n * p.Hq;
                 uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) +
                                                     (long long)t0 * p.Hq * DR);
@@ -1390,8 +1386,25 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 for (long long i = at; i < rows; i += step)
                     p.lse[(i / n) * p.T + t0 + i % n] = -INFINITY;
             };
-            clear(0, skip);
-            clear(used, p.T - used);
+            bool odd = false;
+            for (int i = lane; i < p.B; i += 32) odd |= seq_range(p.cu, p.N, p.T, i).n < 0;
+            if (!__any_sync(0xffffffffu, odd)) {  // before the first one's and behind the last one's
+                const int skip = min(max(p.cu[0], 0), p.T), used = min(max(p.cu[p.B], skip), p.T);
+                const long long at = (long long)blockIdx.x * 32 + lane, step = (long long)gridDim.x * 32;
+                clear(0, skip, at, step);
+                clear(used, p.T - used, at, step);
+            } else {
+                // a sequence with boundaries that are none owns nothing (the status word says
+                // so): each token is looked for in all others
+                for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
+                    bool owned = false;
+                    for (int i = lane; i < p.B && !owned; i += 32) {
+                        const SeqRange r = seq_range(p.cu, p.N, p.T, i);
+                        owned = t >= r.t0 && t < (long long)r.t0 + r.n;
+                    }
+                    if (!__any_sync(0xffffffffu, owned)) clear((int)t, 1, lane, 32);
+                }
+            }
         }
         if constexpr (!PAIR) {
             // An item's end is brought while the CTA goes on, so that its beginning, which

@@ -520,7 +520,8 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     Calls that may run at the same time need a ``workspace`` each.
     Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens`` and ``max_seqlen``.
     Tokens no packed sequence owns give o = 0 and lse = -inf, or are left as they are in
-    ``out``, a pair (o, lse) to write to.  ``workspace``: uint8, at least
+    ``out``, a pair (o, lse) to write to; a sequence whose boundaries decrease or are not
+    within [0, T] owns none, and `PagedCache.check` raises.  ``workspace``: uint8, at least
     ``fa_tree_workspace_size`` bytes.
     """
     n = _of_cache(cache, layer, slots)

@@ -450,7 +450,9 @@ fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, 
  *   o: bf16 [T,Hq,d] contiguous; lse: fp32 [Hq,T], natural log.
  *   Rows of tokens that no packed sequence owns are left as they are, or with
  *   zero_rest = 1 written as O = 0, LSE = -inf.  A sequence whose slot, length
- *   or count does not fit sets the status word and its rows see nothing.
+ *   or count does not fit sets the status word and its rows see nothing; one
+ *   whose boundaries decrease or are not within [0, T] sets it and owns no
+ *   tokens (a token that two others then name holds the row of either).
  *   Results do not vary from run to run.  A slot may be read by several
  *   sequences of a call.
  *   Calls that may run at the same time need a workspace each; what it holds

@@ -414,6 +414,42 @@ def test_refused_on_the_device():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,heads,d", [(4, 2, 64), (32, 1, 64), (80, 1, 128), (6, 2, 192)])
+@pytest.mark.parametrize("cu,N", [([0, 3, 6, 90], 90), ([4, 3, 6, 9], 3), ([-2, 3, 6, 9], 5),
+                                  ([0, 5, 2, 2], 5), ([3, 5, 4, 6], 2), ([0, 0, 2 ** 31 - 1, 9], 9),
+                                  ([1, 3, 3, 10], 7), ([-5, -1, 12, 20], 13)])
+def test_boundaries_that_are_none(cu, N, Hq, heads, d):
+    """A sequence whose boundaries decrease or leave the batch owns no tokens: they come out
+    empty, or stay as they are where the caller asks for that; the other sequences' are right."""
+    T = 9
+    h = Held([50, 300, 20], heads, d, 16, seed=11)
+    q = queries(T, Hq, d)
+    good = [i for i in range(3) if 0 <= cu[i] <= cu[i + 1] <= T]
+    names = [[i for i in good if cu[i] <= t < cu[i + 1]] for t in range(T)]
+    rest = [t for t in range(T) if not names[t]]
+    ws = torch.empty(fa.lib().fa_tree_workspace_size(Hq, heads, N, d), dtype=torch.uint8).cuda()
+    slots, bounds = ints(h.slots), ints(cu)
+    for zero_rest in (1, 0):
+        o = torch.full((T, Hq, d), 7.0, dtype=torch.bfloat16).cuda()
+        lse = torch.full((Hq, T), 7.0).cuda()
+        assert fa.lib().fa_tree_fwd(
+            h.cache._at, h.layer, slots.data_ptr(), 3, N, bounds.data_ptr(), T, q.data_ptr(), Hq, Hq * d,
+            d, None, 0, o.data_ptr(), lse.data_ptr(), d ** -0.5, zero_rest, ws.data_ptr(), ws.numel(),
+            torch.cuda.current_stream().cuda_stream) == fa.FA_OK
+        with pytest.raises(fa.FAError, match="does not fit"):
+            h.cache.check()
+        assert (o[rest] == (0 if zero_rest else 7)).all()
+        assert (lse[:, rest] == (-INF if zero_rest else 7)).all()
+        for i in good:  # (a token that two sequences name holds either's row)
+            once = [t for t in range(cu[i], cu[i + 1]) if names[t] == [i]]
+            if once:
+                see = visible(cu[i + 1] - cu[i], h.lengths[i])[[t - cu[i] for t in once]]
+                ro, rl, bo, bl = attend(f64(q[once]), h.k[i], h.v[i], see, d ** -0.5)
+                within("o", f64(o[once]), ro, bo)
+                within("lse", f64(lse[:, once]), rl, bl)
+
+
+@pytest.mark.gpu
 def test_tensor_api_refuses():
     h = Held([50, 300], 2, 64, 16)
     q, s = queries(6, 4, 64), ints(h.slots)
