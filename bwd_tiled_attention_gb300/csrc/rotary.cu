@@ -81,6 +81,7 @@ struct RotParams {
     fa_cache cache;
     const int* slots;
     int layer, page_shift;
+    unsigned bounds_block;       // one more block, which looks the boundaries over
 };
 
 template <typename E>
@@ -127,6 +128,16 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const __grid_consta
     pdl_begin();
     constexpr bool INTER = L == kInter;
     using V = Vec<E, VW>;
+    if (PAGED && blockIdx.x == p.bounds_block) {
+        // Boundaries that decrease or leave the batch are reported here: the tokens'
+        // search takes them as ascending and may not meet the sequence (as a block of
+        // its own, it delays no token).
+        bool bad = false;
+        for (int i = threadIdx.x; i < p.B; i += kRotThreads)
+            bad |= seq_range(p.cu, p.N, p.T, i).n < 0;
+        if (bad) atomicOr(p.cache.scratch, kCacheBadLength);
+        return;
+    }
     const unsigned U = p.units;
     const unsigned quads = p.quads[0] + p.quads[1] + p.quads[2];
     unsigned item;  // token * quads + quad
@@ -359,7 +370,9 @@ cudaError_t launch_t(RotParams p, cudaStream_t stream) {
         } else {
             p.n_items = (unsigned)threads;
         }
-        const dim3 grid((unsigned)((threads + kRotThreads - 1) / kRotThreads));
+        dim3 grid((unsigned)((threads + kRotThreads - 1) / kRotThreads));
+        p.bounds_block = ~0u;
+        if (PAGED && p.cu && t == 0) p.bounds_block = grid.x++;
         const cudaError_t e = launch_pdl(rotary_kernel<E, VW, L, PAGED>, grid, dim3(kRotThreads), 0,
                                          stream, p);
         if (e != cudaSuccess) return e;

@@ -409,7 +409,9 @@ fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream);
  *   is its place in the sequence.
  *   A token whose place is not in the cache, or in a page that several sequences
  *   share, sets the status word and is not written; one that no packed sequence
- *   owns has zeros in q_out.
+ *   owns has zeros in q_out.  Boundaries that decrease or are not within [0, T]
+ *   set the status word (which tokens are then taken for no sequence's is not
+ *   defined).
  */
 fa_status fa_cache_append(const fa_cache* cache, int layer, const int* slots, int B, int N,
                           const int* cu_seqlens, int T, const void* q, void* q_out, int Hq,

@@ -395,6 +395,34 @@ def test_append_refused_on_the_device():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cu", [[0, 5], [2, 1], [-3, 1], [0, 5, 2], [0, 3, 9], [3, 2, 3], [-4, -2, 0],
+                                [0, 2, 1, 3], [3, 3, 3, 90, 90]])
+@pytest.mark.parametrize("d,interleaved", [(64, False), (64, True), (96, False)])
+def test_append_reports_boundaries_that_are_none(cu, d, interleaved):
+    """Wherever boundaries decrease or leave the batch, whether or not a token lies between them."""
+    c, m = make(d=d)
+    slots = [4, 0, 6, 2][:len(cu) - 1]
+    c.reserve(ints(slots), 40)
+    m.reserve(slots, [40] * len(slots))
+    x = torch.randn(3, 2, d).bfloat16().cuda()
+    tab = fa.rotary_table(32, 64)
+    q = fa.cache_append(c, 1, ints(slots), x, x, q=x, rotary=tab, interleaved=interleaved,
+                        cu_seqlens=ints(cu))
+    assert status(c) == 2
+    assert q.shape == x.shape
+    # nothing but the sequences' own last rows can have been written
+    held = [m.place(s, t) for s in slots for t in range(37, 40)]
+    for mine, theirs in ((f64(c.k), m.k), (f64(c.v), m.v)):
+        other = np.ones(mine.shape, bool)
+        for page, row in held:
+            other[1, page, :, row] = False
+        assert np.array_equal(mine[other], theirs[other])
+    # a batch that is fine reports nothing
+    fa.cache_append(c, 1, ints(slots[:1]), x, x, q=x, rotary=tab, cu_seqlens=ints([0, 3]))
+    assert status(c) == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [64, 96])
 def test_append_leaves_shared_pages(d):
     """After a fork the whole pages belong to both: rows of theirs are refused, the page that was
