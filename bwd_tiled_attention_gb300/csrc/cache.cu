@@ -277,6 +277,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(const fa_cache c, cons
     if (sm.error) return;
     for (int i = grp.entry; i < n; i += grp.stride) {
         const int4 e = entry[i];
+        __syncwarp(grp.mask);  // (all have read it: past kPlan entries the record below lies there)
         const int from_slot = parents[i], to_slot = children[i];
         const int* from = c.table + (long long)from_slot * c.max_pages;
         int* to = c.table + (long long)to_slot * c.max_pages;
