@@ -500,6 +500,13 @@ __global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const fa_cach
     }
 }
 
+// Takes the bits that have been read out of the status word, and no others: calls
+// on other streams may have set some since.
+__global__ void clear_kernel(int* status, int bits) {
+    pdl_begin();
+    atomicAnd(status, ~bits);
+}
+
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
@@ -599,7 +606,9 @@ fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream) {
     if (cudaMemcpyAsync(&word, cache->scratch, sizeof(int), cudaMemcpyDeviceToHost, strm) != cudaSuccess ||
         cudaStreamSynchronize(strm) != cudaSuccess)
         return FA_ERR_CUDA;
-    if (word && cudaMemsetAsync(cache->scratch, 0, sizeof(int), strm) != cudaSuccess) return FA_ERR_CUDA;
+    if (word && (launch_pdl(clear_kernel, dim3(1), dim3(1), 0, strm, cache->scratch, word) != cudaSuccess ||
+                 cudaStreamSynchronize(strm) != cudaSuccess))
+        return FA_ERR_CUDA;
     if (bits) *bits = word;
     if (word & kCacheTimeout) return FA_ERR_TIMEOUT;
     return word ? FA_ERR_INVALID_ARG : FA_OK;

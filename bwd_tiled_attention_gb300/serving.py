@@ -413,8 +413,9 @@ class PagedCache:
                    base.data_ptr(), path.data_ptr(), path.shape[1], accepted.data_ptr(), n)
 
     def check(self, stream=None):
-        """Synchronises, and raises if a call on this cache has been refused on the device or
-        failed there since the last check."""
+        """Synchronises the stream, and raises if a call on this cache has been refused on the
+        device or failed there since the last check.  What a call on another stream finds while
+        this one waits is kept for the next check."""
         bits = ctypes.c_int(0)
         with _on(self.device, stream, self._tensors):
             st = lib().fa_cache_check(self._at, ctypes.addressof(bits), _raw_stream(self.device))

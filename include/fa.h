@@ -390,8 +390,10 @@ fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* ba
                           int path_width, const int* accepted, int n, fa_stream_t stream);
 
 /*
- * Synchronises the stream, reads the status word and clears it: FA_OK,
- * FA_ERR_TIMEOUT (bit 16) or FA_ERR_INVALID_ARG; the bits go to *bits.
+ * Synchronises the stream, reads the status word and clears the bits that it
+ * read: FA_OK, FA_ERR_TIMEOUT (bit 16) or FA_ERR_INVALID_ARG; the bits go to
+ * *bits.  It covers the calls ordered before it on this stream; what calls on
+ * other streams find is there for this check or a later one.
  */
 fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream);
 

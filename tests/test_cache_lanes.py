@@ -160,3 +160,25 @@ def test_many_entries(emulated, n, order, seed):
     code = (f"import sys; sys.path[:0] = [{os.path.dirname(HERE)!r}, {HERE!r}]\n"
             f"import test_cache_lanes as t\nt.many_entries(t.load({emulated!r}), {n}, {order}, {seed})")
     subprocess.run([sys.executable, "-c", code], check=True)
+
+
+@pytest.mark.parametrize("before", [0, 2])
+def test_errors_found_during_a_check_are_kept(emulated, before):
+    """A bit that a call on another stream sets while the check waits, after it has copied the status
+    word, is there for the next check."""
+    L = load(emulated)
+    c = Cache(L, 1, 4, 1, 16, 64, 2, 2)
+    c.scratch[0] = before
+    late = [8]
+
+    def other_stream():
+        if late:
+            c.scratch[0] |= late.pop()
+
+    hook = ctypes.CFUNCTYPE(None)(other_stream)
+    L.at_stream_wait(ctypes.cast(hook, ctypes.c_void_p))
+    try:
+        assert c.status() == before
+    finally:
+        L.at_stream_wait(None)
+    assert c.status() == 8 and c.status() == 0
