@@ -24,6 +24,7 @@ import functools
 import math
 
 import torch
+from torch.autograd import forward_ad
 
 from . import FA_BF16, FA_FP32, FA_OK, FAError, lib
 
@@ -248,7 +249,8 @@ class _Rotary(torch.autograd.Function):
         gq, gk = _last_contiguous(gq), _last_contiguous(gk)
         dev = (gq if gq is not None else gk).device
         with contextlib.nullcontext() if _here(dev, None) else torch.cuda.device(dev):
-            if torch.is_grad_enabled():  # the transposed rotation, itself differentiable
+            # the transposed rotation, itself differentiable (a forward tangent is refused there)
+            if torch.is_grad_enabled() or forward_ad._current_level >= 0:
                 dq, dk = _Rotary.apply(gq, gk, table, (positions, cu_seqlens),
                                        (pos_bytes, B, N, interleaved, 1 - back))
             else:
@@ -259,7 +261,8 @@ class _Rotary(torch.autograd.Function):
 
 def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved=False,
            stream=None):
-    """q and k (or one of them, the other None) turned to their tokens' positions; differentiable.
+    """q and k (or one of them, the other None) turned to their tokens' positions; differentiable
+    in reverse, any number of times (forward tangents are refused, as by `attention`).
 
     ``table`` is that of `rotary_table`; its rot columns of each head turn, the others are
     copied.  Pairs are columns (i, i + rot/2), or (2i, 2i + 1) when interleaved.  Without
@@ -289,8 +292,10 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
     else:
         B, N = _sequences(T, batch, cu_seqlens, None, dev, need_max=False)
     _cuda("q" if q is not None else "k", first)
+    # (inside a dual level an input may have a forward tangent, which the function refuses)
     grad = torch.is_grad_enabled() and ((q is not None and q.requires_grad) or
-                                        (k is not None and k.requires_grad))
+                                        (k is not None and k.requires_grad)) or \
+        forward_ad._current_level >= 0
 
     if not _here(dev, stream):
         with _on(dev, stream, (q, k, table, positions, cu_seqlens)):

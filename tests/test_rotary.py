@@ -5,6 +5,7 @@ import math
 import numpy as np
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import bwd_tiled_attention_gb300 as fa
 from bwd_tiled_attention_gb300 import build as fabuild
@@ -95,6 +96,32 @@ def test_tensor_api_refuses():
         fa.attention(q, q, q, batch=1, rotary=tab, positions_k=torch.zeros(6, dtype=torch.int32))
     with pytest.raises(ValueError, match="rotary table"):
         fa.attention(q, q, q, batch=1, positions=torch.zeros(6, dtype=torch.int32))
+
+
+def refuses_forward_tangents(q, k, table):
+    """A tangent must not be dropped without a word, in the rotation or in its gradient."""
+    with forward_ad.dual_level():
+        dual = forward_ad.make_dual(q, torch.ones_like(q))
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad):
+                for a, b, t in ((dual, k, table), (dual, None, table), (None, dual, table),
+                                (k, None, forward_ad.make_dual(table, table))):
+                    with pytest.raises(NotImplementedError, match="forward"):
+                        fa.rotary(a, b, t, batch=1)
+                assert fa.rotary(k, None, table, batch=1)[0].shape == k.shape  # (no tangent, no error)
+        x = q.clone().requires_grad_()
+        y, _ = fa.rotary(x, None, table, batch=1)
+        with pytest.raises(NotImplementedError, match="forward"):
+            torch.autograd.grad(y, x, forward_ad.make_dual(torch.ones_like(q), torch.ones_like(q)))
+    assert fa.rotary(q, None, table, batch=1)[0].shape == q.shape
+
+
+def test_forward_tangents_are_refused(monkeypatch):
+    monkeypatch.setattr(fa.serving, "_cuda", lambda name, t: None)
+    monkeypatch.setattr(fa.serving, "_here", lambda device, stream: True)
+    monkeypatch.setattr(fa.serving, "_rotate",
+                        lambda q, k, *a: [None if t is None else torch.zeros(t.shape) for t in (q, k)])
+    refuses_forward_tangents(torch.ones(6, 2, 64), torch.ones(6, 2, 64), torch.zeros(9, 32, 2))
 
 
 # ---------------------------------------------------------------------------------- GPU
@@ -243,6 +270,12 @@ def test_tables(kw):
     ref = scale * np.stack([np.cos(a), np.sin(a)], -1)
     # the frequencies may differ in their last places (powers), which a position multiplies
     within("table", got, ref, 2.0 ** -24 * np.abs(ref) + np.maximum(a, 1)[..., None] * 2.0 ** -48 + 2.0 ** -50)
+
+
+@pytest.mark.gpu
+def test_forward_tangents_are_refused_on_the_device():
+    x = torch.randn(6, 2, 64).cuda()
+    refuses_forward_tangents(x, x + 1, fa.rotary_table(64, 9))
 
 
 @pytest.mark.gpu
