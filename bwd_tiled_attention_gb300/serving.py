@@ -71,6 +71,19 @@ def _heads_tensor(name, t, dtypes, device=None):
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+def _not_differentiable(what, *tensors):
+    """A gradient, or a forward tangent, that a call would drop is refused."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{what} is not differentiable: call it under torch.no_grad(), or "
+                                 "detach what requires a gradient")
+    if forward_ad._current_level >= 0:
+        for t in tensors:
+            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+                raise ValueError(f"{what} is not differentiable, and an input has a forward tangent")
+
+
 def _cuda(name, t):
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
@@ -194,6 +207,8 @@ def _rotary_args(table, positions, T, device):
     _want("rotary table", table, (torch.float32,), 3, device)
     if table.shape[2] != 2:
         raise ValueError("the rotary table must be [length, rot / 2, 2]")
+    if table.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the rotary table gets no gradient: detach it")
     if positions is None:
         return 0
     _want("positions", positions, (torch.int32, torch.int64), 1, device)
@@ -450,7 +465,8 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
 
     With ``rotary`` (a `rotary_table`) k, and q if given, are turned to ``positions``, by
     default the tokens' places in their sequences.  Returns the turned q (contiguous), or
-    None.  Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens``.
+    None.  Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens``.  Not differentiable:
+    inputs that require a gradient are refused outside ``torch.no_grad()``.
     """
     n = _of_cache(cache, layer, slots)
     dev = cache.device
@@ -466,6 +482,7 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
         _heads_tensor("q", q, _BF16, dev)
         if q.shape[0] != T or q.shape[2] != cache.d:
             raise ValueError(f"q {tuple(q.shape)} does not fit the cache or k")
+    _not_differentiable("cache_append", k, v, q, rotary, cache.k, cache.v)
     B, N = _sequences(T, n, cu_seqlens, None, dev, need_max=False)
     rot = rows = pos_bytes = 0
     if rotary is not None:
@@ -523,7 +540,8 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     Each sees all earlier tokens of its sequence, and of the call's own ones those that its
     row of ``mask`` names (`tree_mask`, or any int64 ``[T, words]``), or without a mask
     itself and those before it.  A row that sees nothing gives o = 0 and lse = -inf.
-    Calls that may run at the same time need a ``workspace`` each.
+    Calls that may run at the same time need a ``workspace`` each.  Not differentiable:
+    inputs that require a gradient are refused outside ``torch.no_grad()``.
     Sequence i is slots[i]: T = n * N tokens, or ``cu_seqlens`` and ``max_seqlen``.
     Tokens no packed sequence owns give o = 0 and lse = -inf, or are left as they are in
     ``out``, a pair (o, lse) to write to; a sequence whose boundaries decrease or are not
@@ -558,6 +576,7 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
             raise ValueError("out must be ([T, Hq, d], [Hq, T])")
     if workspace is not None:
         _want("workspace", workspace, (torch.uint8,), 1, dev)
+    _not_differentiable("tree_attention", q, cache.k, cache.v, *(out or ()))
 
     if out is not None:
         o, lse = out

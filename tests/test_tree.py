@@ -9,6 +9,7 @@ import random
 import numpy as np
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import bwd_tiled_attention_gb300 as fa
 from bwd_tiled_attention_gb300 import build as fabuild
@@ -52,6 +53,41 @@ def test_workspace_and_mask_arguments():
         assert L.fa_tree_mask(*bad) == fa.FA_ERR_INVALID_ARG
     assert L.fa_tree_mask(FAKE, FAKE, 2, 65, 10, 1, FAKE, None) == fa.FA_ERR_INVALID_ARG
     assert L.fa_tree_mask(None, None, 0, 0, 0, 1, None, None) == fa.FA_OK
+
+
+def refuses_lost_gradients(cache, slots, table):
+    """Whatever requires a gradient, or has a forward tangent, is refused where it would be cut off."""
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device=cache.device)
+    leaf, dual_of = x.clone().requires_grad_(), forward_ad.make_dual
+    o, lse = x.clone(), torch.zeros(2, 2, device=cache.device)
+    append = lambda k=x, v=x, q=x, **kw: fa.cache_append(cache, 0, slots, k, v, q=q, **kw)  # noqa: E731
+    attend = lambda q=x, **kw: fa.tree_attention(q, cache, 0, slots, **kw)  # noqa: E731
+    calls = [lambda t: append(k=t), lambda t: append(v=t), lambda t: append(q=t), lambda t: attend(q=t),
+             lambda t: attend(out=(t, lse))]
+    for call in calls:
+        with pytest.raises(ValueError, match="not differentiable"):
+            call(leaf)
+        with forward_ad.dual_level(), pytest.raises(ValueError, match="forward tangent"):
+            call(dual_of(x, x))
+    with pytest.raises(ValueError, match="not differentiable"):
+        attend(out=(o, lse.clone().requires_grad_()))
+    for c in (lambda t: append(rotary=t), lambda t: fa.rotary(x, None, t, batch=1)):
+        with pytest.raises(ValueError, match="gradient: detach|requires a gradient"):
+            c(table.clone().requires_grad_())
+    for held in (cache.k, cache.v):
+        held.requires_grad_()
+        for call in (append, attend):
+            with pytest.raises(ValueError, match="not differentiable"):
+                call()
+        held.requires_grad_(False)
+    return append, attend, leaf
+
+
+def test_lost_gradients_are_refused(monkeypatch):
+    monkeypatch.setattr(fa.serving, "_cuda", lambda name, t: None)
+    monkeypatch.setattr(fa.serving, "_here", lambda device, stream: True)
+    cache = fa.PagedCache.allocate(1, 3, 2, 16, 64, 2, 2, device="cpu")
+    refuses_lost_gradients(cache, torch.zeros(2, dtype=torch.int32), torch.zeros(9, 32, 2))
 
 
 # ---------------------------------------------------------------------------------- GPU
@@ -484,6 +520,21 @@ def test_tensor_api_refuses():
     with pytest.raises(fa.FAError, match="UNSUPPORTED"):
         go(scale=0.0)
     assert go(q=q[:0])[0].shape == (0, 4, 64)
+
+
+@pytest.mark.gpu
+def test_lost_gradients_are_refused_on_the_device():
+    """And nothing is lost where no gradient is wanted."""
+    cache, slots = fa.PagedCache.allocate(1, 3, 2, 16, 64, 2, 2), ints([0, 1])
+    table = fa.rotary_table(64, 9)
+    append, attend, leaf = refuses_lost_gradients(cache, slots, table)
+    cache.reserve(slots, 1)
+    with torch.no_grad():
+        q = append(k=leaf, v=leaf, q=leaf, rotary=table.clone().requires_grad_())
+        assert attend(q=leaf)[0].shape == q.shape and not q.requires_grad
+    with forward_ad.dual_level():
+        attend(q=leaf.detach())
+    cache.check()
 
 
 @pytest.mark.gpu
