@@ -157,7 +157,7 @@ def rotary_table(rot, length, base=10000.0, scaling=None, factor=1.0, original_l
 
     - ``"linear"``: every frequency divided by factor;
     - ``"ntk"``: the base raised by ``factor ** (rot / (rot - 2))``, so that the slowest
-      pair is divided by factor and the fastest stays;
+      pair is divided by factor and the fastest stays (not with ``frequencies``);
     - ``"by_parts"``: pairs that turn fewer than ``low_turns`` times over
       ``original_length`` are divided by factor, those with more than ``high_turns`` stay,
       those between are mixed; cos and sin are stretched by ``1 + 0.1 ln(factor)``.
@@ -175,6 +175,8 @@ def rotary_table(rot, length, base=10000.0, scaling=None, factor=1.0, original_l
         freq = torch.as_tensor(frequencies, dtype=torch.float64)
         if freq.shape != (rot // 2,):
             raise ValueError("frequencies must have rot / 2 entries")
+        if scaling == "ntk":
+            raise ValueError("ntk scaling raises the base, which frequencies take the place of")
     else:
         if scaling == "ntk":
             if rot < 4:

@@ -98,6 +98,11 @@ def test_tensor_api_refuses():
         fa.attention(q, q, q, batch=1, positions=torch.zeros(6, dtype=torch.int32))
 
 
+def test_a_raised_base_with_frequencies_is_refused():
+    with pytest.raises(ValueError, match="base"):
+        fa.rotary_table(8, 4, scaling="ntk", factor=4.0, frequencies=[1.0, 0.5, 0.2, 0.1])
+
+
 def refuses_forward_tangents(q, k, table):
     """A tangent must not be dropped without a word, in the rotation or in its gradient."""
     with forward_ad.dual_level():
