@@ -173,6 +173,7 @@ def rotary_table(rot, length, base=10000.0, scaling=None, factor=1.0, original_l
     scale = 1.0
     if frequencies is not None:
         freq = torch.as_tensor(frequencies, dtype=torch.float64)
+        _not_differentiable("rotary_table", freq)
         if freq.shape != (rot // 2,):
             raise ValueError("frequencies must have rot / 2 entries")
         if scaling == "ntk":

@@ -103,6 +103,14 @@ def test_a_raised_base_with_frequencies_is_refused():
         fa.rotary_table(8, 4, scaling="ntk", factor=4.0, frequencies=[1.0, 0.5, 0.2, 0.1])
 
 
+def test_frequencies_that_require_a_gradient_are_refused():
+    f = torch.ones(4, requires_grad=True)
+    with pytest.raises(ValueError, match="not differentiable"):
+        fa.rotary_table(8, 4, frequencies=f)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        fa.rotary_table(8, 4, frequencies=f, device="cpu")
+
+
 def refuses_forward_tangents(q, k, table):
     """A tangent must not be dropped without a word, in the rotation or in its gradient."""
     with forward_ad.dual_level():
