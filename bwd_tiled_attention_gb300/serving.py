@@ -59,12 +59,14 @@ def _want(name, t, dtypes, ndim, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.numel() > _MOST and max(t.shape) > _MOST:  # (the library's sizes are 32 bits)
+        raise ValueError(f"{name} has a dimension above {_MOST}: shape {tuple(t.shape)}")
 
 
 def _heads_tensor(name, t, dtypes, device=None):
     """A [T, H, d] tensor with free token and head strides."""
     if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 3 and t.stride(2) == 1 and
-            (device is None or t.device == device)):
+            (device is None or t.device == device) and t.numel() <= _MOST):
         return
     _want(name, t, dtypes, 3, device, contiguous=False)
     if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():

@@ -111,6 +111,37 @@ def test_tensor_api_refuses():
         fa.cache_append(None, 0, n, k, k)
 
 
+def test_sizes_past_32_bits_are_refused(monkeypatch):
+    """Each of them would reach the library cut to its low 32 bits."""
+    monkeypatch.setattr(fa.serving, "_cuda", lambda name, t: None)
+    monkeypatch.setattr(fa.serving, "_here", lambda device, stream: True)
+    far = 2 ** 32 + 64
+
+    def new(*shape, dtype=torch.bfloat16):
+        return torch.empty(shape, dtype=dtype, device="meta")
+
+    i32, f32, q = torch.int32, torch.float32, new(1, 2, 64)
+    cache = fa.PagedCache.allocate(1, 4, 2, 16, 64, 3, 2, device="meta")
+    one, table = new(1, dtype=i32), new(9, 32, 2, dtype=f32)
+    for call in (lambda: fa.rotary(new(1, 1, far), None, table, batch=1),
+                 lambda: fa.rotary(new(1, far, 2), None, table[:, :1].contiguous(), batch=1),
+                 lambda: fa.rotary(q, new(1, far, 64), table, batch=1),
+                 lambda: fa.rotary(q, None, new(far, 1, 2, dtype=f32), batch=1),
+                 lambda: fa.rotary(q, None, table, cu_seqlens=new(far, dtype=i32)),
+                 lambda: fa.tree_attention(q, cache, 0, new(far, dtype=i32)),
+                 lambda: fa.tree_attention(q, cache, 0, one, mask=new(1, far, dtype=torch.int64)),
+                 lambda: fa.cache_append(cache, 0, one, q, q, rotary=new(far, 32, 2, dtype=f32)),
+                 lambda: fa.cache_append(cache, 0, one, q, q, q=new(1, far, 64)),
+                 lambda: fa.tree_mask(new(3, dtype=i32), cu_seqlens=new(far, dtype=i32), max_seqlen=3),
+                 lambda: cache.free(new(far, dtype=i32)),
+                 lambda: cache.accept(one, one, new(1, far, dtype=i32), one),
+                 lambda: fa.PagedCache(cache.k, cache.v, new(far, 2, dtype=i32), new(far, dtype=i32),
+                                       cache.refs),
+                 lambda: fa.PagedCache(cache.k, cache.v, new(3, far, dtype=i32), cache.lengths, cache.refs)):
+        with pytest.raises(ValueError, match="has a dimension above 2147483647"):
+            call()
+
+
 # ---------------------------------------------------------------------------------- GPU
 
 
