@@ -122,6 +122,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _whole(name, x):
+    n = int(x)
+    if n != x:
+        raise ValueError(f"{name} must be a whole number, got {x}")
+    return n
+
+
 def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
     """(B, N) of the call: N is the dense length, or the bound of a packed batch."""
     if T > _MOST:
@@ -129,6 +136,7 @@ def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
     if cu_seqlens is None:
         if batch is None:
             raise ValueError("dense inputs need batch (B); T = B * N")
+        batch = _whole("batch", batch)
         if batch < 0 or (batch == 0 and T) or (batch and T % batch):
             raise ValueError("T must equal B * N for a dense batch")
         return batch, T // batch if batch else 0
@@ -142,9 +150,10 @@ def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
         if need_max:
             raise ValueError("variable-length inputs need max_seqlen")
         return B, 0
+    max_seqlen = _whole("max_seqlen", max_seqlen)
     if not 0 <= max_seqlen <= _MOST:
         raise ValueError(f"max_seqlen must be from 0 to {_MOST}, got {max_seqlen}")
-    return B, int(max_seqlen)
+    return B, max_seqlen
 
 
 # ------------------------------------------------------------------------------- rotary
@@ -407,10 +416,13 @@ class PagedCache:
         many = counts if isinstance(counts, torch.Tensor) else None
         if many is not None:
             self._list("counts", many, n)
-        elif not 0 <= counts <= _MOST:
-            raise ValueError(f"counts must be from 0 to {_MOST}, got {counts}")
+            counts = 0
+        else:
+            counts = _whole("counts", counts)
+            if not 0 <= counts <= _MOST:
+                raise ValueError(f"counts must be from 0 to {_MOST}, got {counts}")
         self._call("fa_cache_reserve", stream, (slots, many), slots.data_ptr(), _ptr(many),
-                   0 if many is not None else int(counts), n)
+                   counts, n)
 
     def fork(self, parents, children, stream=None):
         """children[i], which must be empty, becomes a copy of parents[i]: whole pages are shared,

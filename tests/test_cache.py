@@ -142,6 +142,28 @@ def test_sizes_past_32_bits_are_refused(monkeypatch):
             call()
 
 
+def test_sizes_that_are_not_whole_are_refused(monkeypatch):
+    """A fraction is no count: it must not be cut off."""
+    monkeypatch.setattr(fa.serving, "_cuda", lambda name, t: None)
+    cache = fa.PagedCache.allocate(1, 4, 2, 16, 64, 3, 2, device="cpu")
+    slots, q = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    cu, table = torch.zeros(2, dtype=torch.int32), torch.zeros(9, 32, 2)
+    called = []
+    monkeypatch.setattr(cache, "_call", lambda name, stream, tensors, *a: called.append(a))
+    monkeypatch.setattr(fa.serving, "_here", lambda device, stream: True)
+    for call in (lambda: cache.reserve(slots, 1.5),
+                 lambda: fa.tree_attention(q, cache, 0, slots, cu_seqlens=cu, max_seqlen=1.5),
+                 lambda: fa.tree_mask(slots, cu_seqlens=cu, max_seqlen=1.5),
+                 lambda: fa.rotary(q, None, table, batch=0.5)):
+        with pytest.raises(ValueError, match="whole number"):
+            call()
+    assert not called
+    cache.reserve(slots, np.int64(3))
+    cache.reserve(slots, 2.0)
+    cache.reserve(slots, torch.zeros(1, dtype=torch.int32))
+    assert [a[2] for a in called] == [3, 2, 0]
+
+
 # ---------------------------------------------------------------------------------- GPU
 
 
