@@ -112,6 +112,7 @@ struct TreeParams {
     int tile_tokens;               // tokens of one 128-row tile
     int min_tiles;                 // least key tiles of a CTA
     int zero_rest;                 // write zeros for tokens that no sequence owns
+    int clear_odd;                 // one more slice of the join kernel does so between odd boundaries
     float scale_log2;
 };
 
