@@ -59,31 +59,34 @@ def _want(name, t, dtypes, ndim, device=None, contiguous=True):
         raise ValueError(f"{name} must be contiguous")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.numel() > _MOST and max(t.shape) > _MOST:  # (the library's sizes are 32 bits)
-        raise ValueError(f"{name} has a dimension above {_MOST}: shape {tuple(t.shape)}")
 
 
 def _heads_tensor(name, t, dtypes, device=None):
     """A [T, H, d] tensor with free token and head strides."""
     if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.dim() == 3 and t.stride(2) == 1 and
-            (device is None or t.device == device) and t.numel() <= _MOST):
+            (device is None or t.device == device)):
         return
     _want(name, t, dtypes, 3, device, contiguous=False)
     if t.shape[2] > 1 and t.stride(2) != 1 and t.numel():
         raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
+def _too_far(name, t):
+    """The library's sizes are 32 bits."""
+    raise ValueError(f"{name} has a dimension above {_MOST}: shape {tuple(t.shape)}")
+
+
 def _not_differentiable(what, *tensors):
     """A gradient, or a forward tangent, that a call would drop is refused."""
-    if torch.is_grad_enabled():
-        for t in tensors:
-            if t is not None and t.requires_grad:
-                raise ValueError(f"{what} is not differentiable: call it under torch.no_grad(), or "
-                                 "detach what requires a gradient")
-    if forward_ad._current_level >= 0:
-        for t in tensors:
-            if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-                raise ValueError(f"{what} is not differentiable, and an input has a forward tangent")
+    grad, forward = torch.is_grad_enabled(), forward_ad._current_level >= 0
+    for t in tensors:
+        if t is None:
+            continue
+        if grad and t.requires_grad:
+            raise ValueError(f"{what} is not differentiable: call it under torch.no_grad(), or "
+                             "detach what requires a gradient")
+        if forward and forward_ad.unpack_dual(t).tangent is not None:
+            raise ValueError(f"{what} is not differentiable, and an input has a forward tangent")
 
 
 def _cuda(name, t):
@@ -123,6 +126,8 @@ def _ptr(t):
 
 
 def _whole(name, x):
+    if type(x) is int:
+        return x
     n = int(x)
     if n != x:
         raise ValueError(f"{name} must be a whole number, got {x}")
@@ -142,6 +147,8 @@ def _sequences(T, batch, cu_seqlens, max_seqlen, device, need_max=True):
         return batch, T // batch if batch else 0
     _want("cu_seqlens", cu_seqlens, _INT, 1, device)
     B = cu_seqlens.numel() - 1
+    if B > _MOST:
+        _too_far("cu_seqlens", cu_seqlens)
     if B < 0:
         raise ValueError("cu_seqlens must have B + 1 entries")
     if batch is not None and batch != B:
@@ -219,8 +226,11 @@ def rotary_table(rot, length, base=10000.0, scaling=None, factor=1.0, original_l
 
 def _rotary_args(table, positions, T, device):
     _want("rotary table", table, (torch.float32,), 3, device)
-    if table.shape[2] != 2:
+    length, _, pair = table.shape
+    if pair != 2:
         raise ValueError("the rotary table must be [length, rot / 2, 2]")
+    if length > _MOST:
+        _too_far("rotary table", table)
     if table.requires_grad and torch.is_grad_enabled():
         raise ValueError("the rotary table gets no gradient: detach it")
     if positions is None:
@@ -311,9 +321,13 @@ def rotary(q, k, table, positions=None, cu_seqlens=None, batch=None, interleaved
             raise ValueError("q and k must have one type and device")
         if k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
             raise ValueError("q and k must have the same tokens and head dimension")
-    T, dev = first.shape[0], first.device
+    (T, H, d), dev = first.shape, first.device
+    if H > _MOST or d > _MOST:
+        _too_far("q" if q is not None else "k", first)
+    if k is not None and k.shape[1] > _MOST:
+        _too_far("k", k)
     pos_bytes = _rotary_args(table, positions, T, dev)
-    if 2 * table.shape[1] > first.shape[2]:
+    if 2 * table.shape[1] > d:
         raise ValueError("the table turns more columns than a head has")
     if positions is not None:
         _sequences(T, 1, None, None, dev)
@@ -369,6 +383,9 @@ class PagedCache:
             raise ValueError("lengths must have an entry a slot, refs one a page")
         if not (layers and pages and heads and slots and max_pages):
             raise ValueError("the cache has no room")
+        for name, t in (("k", k), ("table", table)):
+            if max(t.shape) > _MOST:
+                _too_far(name, t)
         _cuda("k", k)
         self.k, self.v, self.table, self.lengths, self.refs = k, v, table, lengths, refs
         self.layers, self.pages, self.heads, self.page_size, self.d = layers, pages, heads, page_size, d
@@ -436,6 +453,8 @@ class PagedCache:
     def free(self, slots, stream=None):
         """Empties slots; pages that no other slot holds are free again."""
         n = self._list("slots", slots).shape[0]
+        if n > _MOST:
+            _too_far("slots", slots)
         self._call("fa_cache_free", stream, (slots,), slots.data_ptr(), n)
 
     def accept(self, slots, base, path, accepted, stream=None):
@@ -445,6 +464,8 @@ class PagedCache:
         self._few(n)
         self._list("base", base, n)
         self._list("path", path, n, 2)
+        if path.shape[1] > _MOST:
+            _too_far("path", path)
         self._list("accepted", accepted, n)
         self._call("fa_cache_accept", stream, (slots, base, path, accepted), slots.data_ptr(),
                    base.data_ptr(), path.data_ptr(), path.shape[1], accepted.data_ptr(), n)
@@ -471,7 +492,10 @@ def _of_cache(cache, layer, slots):
     if not 0 <= layer < cache.layers:
         raise ValueError(f"layer {layer} of {cache.layers}")
     _want("slots", slots, _INT, 1, cache.device)
-    return slots.shape[0]
+    n = slots.shape[0]
+    if n > _MOST:
+        _too_far("slots", slots)
+    return n
 
 
 def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
@@ -497,9 +521,13 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
         raise ValueError(f"k {tuple(k.shape)} or v {tuple(v.shape)} does not fit the cache")
     if q is not None:
         _heads_tensor("q", q, _BF16, dev)
-        if q.shape[0] != T or q.shape[2] != cache.d:
+        Tq, Hq, d = q.shape
+        if Tq != T or d != cache.d:
             raise ValueError(f"q {tuple(q.shape)} does not fit the cache or k")
-    _not_differentiable("cache_append", k, v, q, rotary, cache.k, cache.v)
+        if Hq > _MOST:
+            _too_far("q", q)
+    if torch.is_grad_enabled() or forward_ad._current_level >= 0:
+        _not_differentiable("cache_append", k, v, q, rotary, cache.k, cache.v)
     B, N = _sequences(T, n, cu_seqlens, None, dev, need_max=False)
     rot = rows = pos_bytes = 0
     if rotary is not None:
@@ -510,10 +538,12 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
     elif positions is not None:
         raise ValueError("positions need a rotary table")
 
-    out, Hq, qt, qh = None, 0, 0, 0
+    out = None
     if q is not None:
-        out, Hq = torch.empty(q.shape, dtype=torch.bfloat16, device=dev), q.shape[1]
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         qt, qh, _ = q.stride()
+    else:
+        Hq = qt = qh = 0
     kt, kh, _ = k.stride()
     vt, vh, _ = v.stride()
     if T:
@@ -574,6 +604,8 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
                                   workspace)
     _heads_tensor("q", q, _BF16, dev)
     T, Hq, d = q.shape
+    if Hq > _MOST:
+        _too_far("q", q)
     if d != cache.d:
         raise ValueError("q and the cache differ in head dimension")
     if Hq % cache.heads or Hq == 0:
@@ -582,9 +614,11 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     words = 0
     if mask is not None:
         _want("mask", mask, (torch.int64,), 2, dev)
-        words = mask.shape[1]
-        if mask.shape[0] != T or 64 * words < N:
+        rows, words = mask.shape
+        if rows != T or 64 * words < N:
             raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
+        if words > _MOST:
+            _too_far("mask", mask)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if out is not None:
         _want("out[0]", out[0], (torch.bfloat16,), 3, dev)
@@ -593,7 +627,8 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
             raise ValueError("out must be ([T, Hq, d], [Hq, T])")
     if workspace is not None:
         _want("workspace", workspace, (torch.uint8,), 1, dev)
-    _not_differentiable("tree_attention", q, cache.k, cache.v, *(out or ()))
+    if torch.is_grad_enabled() or forward_ad._current_level >= 0:
+        _not_differentiable("tree_attention", q, cache.k, cache.v, *(out or ()))
 
     if out is not None:
         o, lse = out
