@@ -526,7 +526,8 @@ def cache_append(cache, layer, slots, k, v, q=None, rotary=None, positions=None,
             raise ValueError(f"q {tuple(q.shape)} does not fit the cache or k")
         if Hq > _MOST:
             _too_far("q", q)
-    if torch.is_grad_enabled() or forward_ad._current_level >= 0:
+    if (k.requires_grad or v.requires_grad or (q is not None and q.requires_grad) or
+            cache.k.requires_grad or cache.v.requires_grad or forward_ad._current_level >= 0):
         _not_differentiable("cache_append", k, v, q, rotary, cache.k, cache.v)
     B, N = _sequences(T, n, cu_seqlens, None, dev, need_max=False)
     rot = rows = pos_bytes = 0
@@ -627,7 +628,8 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
             raise ValueError("out must be ([T, Hq, d], [Hq, T])")
     if workspace is not None:
         _want("workspace", workspace, (torch.uint8,), 1, dev)
-    if torch.is_grad_enabled() or forward_ad._current_level >= 0:
+    if (q.requires_grad or cache.k.requires_grad or cache.v.requires_grad or out is not None or
+            forward_ad._current_level >= 0):
         _not_differentiable("tree_attention", q, cache.k, cache.v, *(out or ()))
 
     if out is not None:
@@ -637,11 +639,14 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
         lse = torch.empty((Hq, T), dtype=torch.float32, device=dev)
     if T == 0:
         return o, lse
-    ws = workspace if workspace is not None else torch.empty(
-        max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16), dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        ws, size = workspace, workspace.numel()
+    else:
+        size = max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)
     qt, qh, _ = q.stride()
     _check(lib().fa_tree_fwd(
         cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
         _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, 1 if out is None else 0,
-        ws.data_ptr(), ws.numel(), _raw_stream(dev)), "fa_tree_fwd")
+        ws.data_ptr(), size, _raw_stream(dev)), "fa_tree_fwd")
     return o, lse
