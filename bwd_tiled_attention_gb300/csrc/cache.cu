@@ -11,14 +11,15 @@
 // status word.  Free pages (refs == 0) are handed out lowest index first, in
 // the order of the call's entries: results do not depend on timing.
 //
-// Copying is bound by memory: one CTA a (sequence, layer, K or V), 16-byte
-// accesses, only the rows that a page holds.
+// Copying is bound by memory, in 16-byte accesses of only the rows that a page
+// holds: a CTA a (branch, layer, K or V) in fork, a (sequence, four layers, K or V)
+// in accept.
 //
-// Measured (GPU time): freeing and forking 64 branches of 8 sequences of 400-2000
-// tokens, 8 layers, 8 heads of 128, 33 us, of which the copy is 21 us for 155 MB
-// (reads of a parent's page meet in L2).  Dropping, reserving and accepting drafts
-// of 64 in 64 sequences over 32 layers, four launches, 30 us: each planning CTA is
-// a chain of four or five trips to memory.
+// Measured (GPU time of calls among queued ones): freeing and forking 64 branches of
+// 8 sequences of 400-2000 tokens, 8 layers, 8 heads of 128, 28 us, of which the copy
+// is 21 us for 155 MB (reads of a parent's page meet in L2).  Dropping, reserving and
+// accepting drafts of 64 in 64 sequences over 32 layers, four launches, 28.5 us: each
+// planning CTA is a chain of four or five trips to memory.
 #include <cuda_runtime.h>
 
 #include <cstdint>

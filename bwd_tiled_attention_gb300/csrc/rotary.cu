@@ -15,16 +15,17 @@
 // all of them, and all its loads are in flight before the first use.  In the
 // half layout the two halves of a pair lie in two lanes, which exchange them:
 // a thread that loads both halves needs 91 registers instead of 56 and has too
-// few warps beside it (bf16, 2 x 8192 tokens, 32 + 8 heads of 128: 91 us; now 57
-// us, interleaved 54 us; fp32 with 16 + 16 heads of 192, 62 us; at the copy rate
-// 50, 50 and 59 us).  bf16 is not far from the instruction limit either (60% of
+// few warps beside it (bf16, 2 x 8192 tokens, 32 + 8 heads of 128: 91 us; now 55
+// us, interleaved 50 us; fp32 with 16 + 16 heads of 192, 59 us; at the copy rate
+// 50, 50 and 60 us).  bf16 is not far from the instruction limit either (60% of
 // issue slots), which is why indexes are divided by multiplication.  Blocks of
 // 64 threads, 4 heads a thread: 128 threads up to 3% slower; 32 threads or 2 heads
 // 50% slower, since blocks start no faster than one in a nanosecond; 8 heads 3%
 // faster in the half layout, 2% slower interleaved, 15% slower for few tokens.
 // Head dimensions, strides or alignments that do not allow 16-byte accesses
-// run the same code one element at a time (VW = 1), and fp32 heads wider than
-// a warp's lanes take both halves in a thread.
+// run the same code one element at a time (VW = 1: 2 x 8192 tokens, 32 + 8 heads of
+// 80 with 20 or 40 columns turned in the half layout, 181 and 155 us for 31 us of
+// bytes), and fp32 heads wider than a warp's lanes take both halves in a thread.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

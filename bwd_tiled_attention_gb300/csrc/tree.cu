@@ -38,12 +38,16 @@
 //     0.7-2k, 36.9 -> 35.0).  At d = 128 memory takes twice that, and loading Q four
 //     times and adding up O cost more than they gave (16 x 4 tokens 47 -> 50 us).
 //
-// Measured (GPU time): 64 sequences of 4-8k tokens, 32 + 8 heads of 128, one
-// token each, 243 us = 6.6 TB/s, 97% of the copy rate (d = 64 135 us at 5.8 TB/s;
-// d = 256, 32 sequences, 6.2 TB/s).  2048-token chunks over 4-6k keys: 340 us =
-// 1165 TF/s (32 + 8 heads of 128), 340 us = 1170 TF/s (16 + 4 of 256); 4 trees of
-// 64 over 30k keys 127 us.  One token over 501 keys 14.4 us: ~2.6 us of lookups and
-// arithmetic, ~2 us until the first tile is there, its chain, the join.
+// Measured (GPU time of a call among queued ones; the pairs of figures at single
+// choices are replays of a graph of one call, which take ~3 us more): 64 sequences
+// of 4-8k tokens, 32 + 8 heads of 128, one token each, 240 us = 6.7 TB/s, the rate
+// of a copy (d = 64, 8 heads, 132 us at 6.1 TB/s; d = 96 190 us at 6.3; d = 192 and
+// 256, 32 sequences, 16 + 4 heads, 101 us at 6.0 and 128 us at 6.3).  2048-token
+// chunks over 4000 and 6000 keys, 32 + 8 heads of 128: 367 us = 1168 TF/s (d = 96
+// 342 us; 16 + 4 heads of 192 330 us); 1500- and 2048-token chunks over 4-6k, 16 + 4
+// heads of 256: 340 us = 1167 TF/s; 4 trees of 64 over 30-33k keys 125 us.  One token
+// over 501 keys 11.8 us: ~2.6 us of lookups and arithmetic, ~2 us until the first
+// tile is there, its chain, the join.
 //
 // Pages hold whatever was there before: keys past the length never reach a
 // sum (their scores are replaced, their V rows zeroed in shared memory), and

@@ -4,7 +4,8 @@ The tensor API of the second half of ``include/fa.h``: like the rest of the
 package it marshals arguments and launches the library's kernels on the
 current stream (or ``stream``).  q ``[T, Hq, d]`` and k, v ``[T, Hkv, d]`` may be
 slices of a fused projection: the last dimension must be contiguous, token and
-head strides are free.  Sequences are a dense batch (T = B * N) or a packed one
+head strides are free (for `tree_attention`, positive multiples of 8 elements, and
+the first element on a 16-byte boundary).  Sequences are a dense batch (T = B * N) or a packed one
 (``cu_seqlens`` int32 ``[B+1]``).
 
 A serving step::
@@ -585,6 +586,7 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     """Attention of new tokens over one layer of the cache; returns (o, lse).
 
     The tokens of q ``[T, Hq, d]`` are the last ones of ``slots`` (`cache_append` comes first).
+    ``scale`` is positive, by default 1 / sqrt(d).
     Each sees all earlier tokens of its sequence, and of the call's own ones those that its
     row of ``mask`` names (`tree_mask`, or any int64 ``[T, words]``), or without a mask
     itself and those before it.  A row that sees nothing gives o = 0 and lse = -inf.

@@ -442,7 +442,8 @@ fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, 
                        void* mask, fa_stream_t stream);
 
 /*
- * O = softmax(scale * Q K^T) V of new tokens over one layer of the cache.
+ * O = softmax(scale * Q K^T) V of new tokens over one layer of the cache; scale
+ * is positive and finite.
  *   The T tokens are the LAST tokens of slots[i], as in fa_cache_append, which
  *   comes first.  Every row sees all earlier tokens of its sequence; of the
  *   call's own tokens it sees those with set bits in its row of mask (int64
