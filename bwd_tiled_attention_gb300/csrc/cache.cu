@@ -528,7 +528,7 @@ fa_status check_cache(const fa_cache* c) {
         return FA_ERR_UNSUPPORTED;
     if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128)
         return FA_ERR_UNSUPPORTED;
-    if (c->heads > 65535 || c->layers > 32767 ||
+    if (c->heads > 65535 || c->layers > 32767 || c->slots > kMostSequences ||
         (long long)c->layers * c->pages > 0x7FFFFFFFLL / c->heads ||
         (long long)c->max_pages * c->page_size > 0x40000000LL)
         return FA_ERR_UNSUPPORTED;
@@ -575,6 +575,7 @@ fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_strea
     const fa_status st = check_cache(cache);
     if (st != FA_OK) return st;
     if (n < 0) return FA_ERR_INVALID_ARG;
+    if (n > kMostSequences) return FA_ERR_UNSUPPORTED;
     if (n == 0) return FA_OK;
     if (!list_ok(slots)) return FA_ERR_INVALID_ARG;
     return launched(launch_pdl(free_kernel, dim3(1), dim3(kPlan), 0,

@@ -23,6 +23,10 @@ constexpr int kCacheNoPages = 4;     // not enough free pages
 constexpr int kCacheShared = 8;      // the call would write to a shared page
 constexpr int kCacheTimeout = 16;    // a bounded wait inside a kernel gave up
 
+// Sequences of a call, or slots of a cache, at most: indexes of loops over them,
+// and sums of two, stay within 32 bits.
+constexpr int kMostSequences = 1 << 30;
+
 // The sequences of one call: sequence i is cache slot slots[i] and owns tokens
 // [cu[i], cu[i + 1]) of the packed batch, or [i * N, (i + 1) * N) of a dense
 // one.  Its tokens are the last ones that the slot holds.

@@ -438,6 +438,7 @@ fa_status check_rotary(const RotParams& p, const float* table, int pos_bytes) {
     if (!aligned(p.positions, pos_bytes ? pos_bytes : 1) || !aligned(p.cu, 4) || !aligned(table, 8))
         return FA_ERR_INVALID_ARG;
     if (!p.cu && (long long)p.B * p.N != p.T) return FA_ERR_INVALID_ARG;
+    if (p.B > kMostSequences) return FA_ERR_UNSUPPORTED;
     // the most threads that one token takes must leave room for 32-bit indexes
     if (((long long)p.heads[0] + p.heads[1] + p.heads[2] + 12) / kHeadsPerThread * p.d > kMostThreads)
         return FA_ERR_UNSUPPORTED;

@@ -1634,6 +1634,7 @@ fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, 
                        void* mask, fa_stream_t stream) {
     if (B < 0 || N < 0 || T < 0 || words <= 0 || (long long)words * 64 < N) return FA_ERR_INVALID_ARG;
     if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (B > kMostSequences) return FA_ERR_UNSUPPORTED;
     if (T == 0) return FA_OK;
     if (!parents || !mask || !aligned(parents, 4) || !aligned(cu_seqlens, 4) || !aligned(mask, 8))
         return FA_ERR_INVALID_ARG;
@@ -1653,7 +1654,8 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     const int d = cache->d, Hkv = cache->heads;
     if (layer < 0 || layer >= cache->layers || B < 0 || N < 0 || T < 0 || Hq <= 0 || Hq % Hkv)
         return FA_ERR_INVALID_ARG;
-    if (Hq / Hkv > 128 || Hq > 65535 || (long long)T * Hq * d > (1LL << 40)) return FA_ERR_UNSUPPORTED;
+    if (Hq / Hkv > 128 || Hq > 65535 || (long long)T * Hq * d > (1LL << 40) || B > kMostSequences)
+        return FA_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_UNSUPPORTED;
     if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
     if (mask && (mask_words <= 0 || (long long)mask_words * 64 < N)) return FA_ERR_INVALID_ARG;

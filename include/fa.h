@@ -349,7 +349,8 @@ typedef struct {
     int* refs;      /* device int32 [pages] */
     int* scratch;   /* device, fa_cache_scratch_size bytes, 16-byte aligned, zeroed once */
     int layers, pages, heads, page_size, d, slots, max_pages;
-} fa_cache;         /* d: 64, 96, 128, 192 or 256; page_size: 16, 32, 64 or 128 */
+} fa_cache;         /* d: 64, 96, 128, 192 or 256; page_size: 16, 32, 64 or 128;
+                       slots, like the sequences of any call: at most 2^30 */
 
 /* Bytes of fa_cache.scratch; 0 for invalid sizes. */
 size_t fa_cache_scratch_size(int pages, int slots, int max_pages);

@@ -164,6 +164,22 @@ def test_sizes_that_are_not_whole_are_refused(monkeypatch):
     assert [a[2] for a in called] == [3, 2, 0]
 
 
+def test_more_sequences_than_indexes_hold_are_refused():
+    """Bisection adds two indexes, and loops step past the last one: both must stay within 32 bits."""
+    L, many = fa.lib(), 2 ** 30 + 1
+    c, no = desc(), fa.FA_ERR_UNSUPPORTED
+    at = ctypes.addressof(c)
+    assert set(ops(desc(slots=many))) == {no}
+    assert L.fa_cache_free(at, FAKE, many, None) == no
+    assert L.fa_rotary(FAKE, FAKE, 2, 128, 64, None, None, 0, 0, 0, fa.FA_BF16, 5, 64, 64, FAKE, 9, None, 0,
+                       many, 0, FAKE, 0, 0, None) == no
+    assert L.fa_cache_append(at, 0, FAKE, many, 0, FAKE, 5, None, None, 0, 0, 0, FAKE, 128, 64, FAKE, 128,
+                             64, 0, None, 0, None, 0, 0, None) == no
+    assert L.fa_tree_fwd(at, 0, FAKE, many, 5, FAKE, 5, FAKE, 2, 128, 64, None, 0, FAKE, FAKE, 0.1, 0, FAKE,
+                         1 << 30, None) == no
+    assert L.fa_tree_mask(FAKE, FAKE, many, 5, 5, 1, FAKE, None) == no
+
+
 # ---------------------------------------------------------------------------------- GPU
 
 
