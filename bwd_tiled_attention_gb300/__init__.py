@@ -31,6 +31,7 @@ __all__ = [
     "FAError", "lib", "fa_fwd", "fa_bwd_preprocess", "fa_bwd", "fa_fwd_workspace_size",
     "fa_bwd_workspace_size", "fa_bwd_workspace_semaphore_offset", "fa_check_device_status",
     "fa_bwd_noalloc", "fa_noalloc_check_device_status", "fa_fwd_kv", "fa_bwd_kv_workspace_size", "fa_bwd_kv_preprocess", "fa_bwd_kv",
+    "fa_fwd_window", "fa_bwd_window_workspace_size", "fa_bwd_window_preprocess", "fa_bwd_window",
     "fa_status_string", "forward", "backward", "attention", "FA_OK", "FA_ERR_INVALID_ARG",
     "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT", "FA_BF16", "FA_FP32",
     "PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask",
@@ -72,6 +73,13 @@ _SIGS = {
                                   _i, _vp, _vp, _i, _vp]),
     "fa_bwd_kv": (_i, [_vp] * 9 + [_i, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _vp,
                                    _vp, _i, _vp]),
+    "fa_fwd_window": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
+                           _vp, _vp, _vp, _sz, _vp]),
+    "fa_bwd_window_workspace_size": (_sz, [_i] * 10),
+    "fa_bwd_window_preprocess": (_i, [_vp, _i, _vp, _vp, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _i,
+                                      _i, _i, _vp, _vp, _i, _vp]),
+    "fa_bwd_window": (_i, [_vp] * 9 + [_i, _vp, _sz, _i, _i, _i, _i, _i, _i, _i, _i, _f, _i, _i,
+                                       _vp, _vp, _i, _vp]),
     "fa_rotary_table": (_i, [_vp, _i, _ll, _d, _vp, _vp]),
     "fa_rotary": (_i, [_vp, _vp, _i, _ll, _ll] * 2 + [_i, _i, _i, _i, _vp, _i, _vp, _i, _i, _i,
                                                      _vp, _i, _i, _vp]),
@@ -234,6 +242,39 @@ def fa_bwd_kv(q, k, v, dout, lse, D, dq, dk, dv, grad_dtype, workspace, workspac
                                _ptr(cu_seqlens_k), int(bool(deterministic)), _stream(stream)))
 
 
+def fa_fwd_window(q, k, v, o, o_dtype, lse, B, Hq, Hkv, Nq, total_q, Nk, total_k, d, scale, window,
+                  sinks, cu_seqlens_q, cu_seqlens_k, workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().fa_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _dt(o_dtype), _ptr(lse), B,
+                                   Hq, Hkv, Nq, total_q, Nk, total_k, d, float(scale), window,
+                                   sinks, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                   _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, window, sinks) -> int:
+    return int(lib().fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, window,
+                                                  sinks))
+
+
+def fa_bwd_window_preprocess(o, o_dtype, dout, D, workspace, workspace_bytes, B, Hq, Hkv, Nq,
+                             total_q, Nk, total_k, d, window, sinks, cu_seqlens_q, cu_seqlens_k,
+                             deterministic, stream=None) -> int:
+    return int(lib().fa_bwd_window_preprocess(_ptr(o), _dt(o_dtype), _ptr(dout), _ptr(D),
+                                              _ptr(workspace), int(workspace_bytes), B, Hq, Hkv,
+                                              Nq, total_q, Nk, total_k, d, window, sinks,
+                                              _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                                              int(bool(deterministic)), _stream(stream)))
+
+
+def fa_bwd_window(q, k, v, dout, lse, D, dq, dk, dv, grad_dtype, workspace, workspace_bytes, B, Hq,
+                  Hkv, Nq, total_q, Nk, total_k, d, scale, window, sinks, cu_seqlens_q,
+                  cu_seqlens_k, deterministic, stream=None) -> int:
+    return int(lib().fa_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(dout), _ptr(lse), _ptr(D),
+                                   _ptr(dq), _ptr(dk), _ptr(dv), _dt(grad_dtype), _ptr(workspace),
+                                   int(workspace_bytes), B, Hq, Hkv, Nq, total_q, Nk, total_k, d,
+                                   float(scale), window, sinks, _ptr(cu_seqlens_q),
+                                   _ptr(cu_seqlens_k), int(bool(deterministic)), _stream(stream)))
+
+
 def fa_check_device_status(workspace, stream=None) -> int:
     return int(lib().fa_check_device_status(_ptr(workspace), _stream(stream)))
 
@@ -338,11 +379,33 @@ def _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k, max_seqlen_k, batch
     return B, Hq, Hkv, Nq, Tq, int(max_seqlen_k), Tk, d, True
 
 
+def _count(name, x, least):
+    n = int(x)
+    if n != x or not least <= n <= 2 ** 31 - 1:
+        raise ValueError(f"{name} must be a whole number of at least {least}, got {x}")
+    return n
+
+
+def _check_window(window, sinks, causal):
+    """(window, sinks) as whole numbers, or None without a window."""
+    if window is None:
+        if sinks:
+            raise ValueError("sinks need a window (without one every earlier key is visible)")
+        return None
+    if not causal:
+        raise ValueError("a window needs causal=True")
+    return _count("window", window, 1), _count("sinks", sinks, 0)
+
+
 def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,
             out_dtype=torch.bfloat16, stream=None, workspace=None, cu_seqlens_k=None,
-            max_seqlen_k=None):
-    """Attention forward through the C ABI; returns (o, lse)."""
+            max_seqlen_k=None, window=None, sinks=0):
+    """Attention forward through the C ABI; returns (o, lse).
+
+    With ``window`` (and causal=True) position p sees key j <= p when p - j < window, or when
+    j < sinks: the first ``sinks`` keys of a sequence stay visible to all of it."""
     _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
+    win = _check_window(window, sinks, causal)
     B, Hq, Hkv, Nq, Tq, Nk, Tk, d, kv = _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k,
                                                      max_seqlen_k, batch)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
@@ -351,7 +414,11 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None,
     ws_bytes = fa_fwd_workspace_size(B, Hq, Nq, Tq)
     ws = workspace if workspace is not None else torch.empty(
         max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
-    if kv:
+    if win:
+        _check(fa_fwd_window(q, k, v, o, out_dtype, lse, B, Hq, Hkv, Nq, Tq, Nk, Tk, d, scale, *win,
+                             cu_seqlens, cu_seqlens if cu_seqlens_k is None else cu_seqlens_k, ws,
+                             ws_bytes, stream), "fa_fwd_window")
+    elif kv:
         _check(fa_fwd_kv(q, k, v, o, out_dtype, lse, B, Hq, Hkv, Nq, Tq, Nk, Tk, d, scale, causal,
                          cu_seqlens, cu_seqlens_k, ws, ws_bytes, stream), "fa_fwd_kv")
     else:
@@ -362,9 +429,12 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None,
 
 def backward(q, k, v, o, dout, lse, causal=False, scale=None, cu_seqlens=None, max_seqlen=None,
              batch=None, deterministic=False, grad_dtype=torch.bfloat16, stream=None,
-             workspace=None, check_status=False, cu_seqlens_k=None, max_seqlen_k=None):
-    """Attention backward (preprocess + backward) through the C ABI; returns (dq, dk, dv)."""
+             workspace=None, check_status=False, cu_seqlens_k=None, max_seqlen_k=None, window=None,
+             sinks=0):
+    """Attention backward (preprocess + backward) through the C ABI; returns (dq, dk, dv).
+    causal, window and sinks as in the forward."""
     _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k, dout=dout, o=o, lse=lse)
+    win = _check_window(window, sinks, causal)
     B, Hq, Hkv, Nq, Tq, Nk, Tk, d, kv = _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k,
                                                      max_seqlen_k, batch)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
@@ -372,13 +442,23 @@ def backward(q, k, v, o, dout, lse, causal=False, scale=None, cu_seqlens=None, m
     dk = torch.empty((Tk, Hkv, d), dtype=grad_dtype, device=q.device)
     dv = torch.empty((Tk, Hkv, d), dtype=grad_dtype, device=q.device)
     D = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
-    if kv:
+    if win:
+        ws_bytes = fa_bwd_window_workspace_size(B, Hq, Hkv, Nq, Tq, Nk, Tk, d, *win)
+    elif kv:
         ws_bytes = fa_bwd_kv_workspace_size(B, Hq, Hkv, Nq, Tq, Nk, Tk, d)
     else:
         ws_bytes = fa_bwd_workspace_size(B, Hq, Hkv, Nq, Tq, d)
     ws = workspace if workspace is not None else torch.empty(
         max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
-    if kv:
+    if win:
+        cu_k = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
+        _check(fa_bwd_window_preprocess(o, o.dtype, dout, D, ws, ws_bytes, B, Hq, Hkv, Nq, Tq, Nk,
+                                        Tk, d, *win, cu_seqlens, cu_k, deterministic, stream),
+               "fa_bwd_window_preprocess")
+        _check(fa_bwd_window(q, k, v, dout, lse, D, dq, dk, dv, grad_dtype, ws, ws_bytes, B, Hq,
+                             Hkv, Nq, Tq, Nk, Tk, d, scale, *win, cu_seqlens, cu_k, deterministic,
+                             stream), "fa_bwd_window")
+    elif kv:
         _check(fa_bwd_kv_preprocess(o, o.dtype, dout, D, ws, ws_bytes, B, Hq, Hkv, Nq, Tq, Nk, Tk,
                                     d, causal, cu_seqlens, cu_seqlens_k, deterministic, stream),
                "fa_bwd_kv_preprocess")
@@ -398,27 +478,31 @@ def backward(q, k, v, o, dout, lse, causal=False, scale=None, cu_seqlens=None, m
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, causal, scale, cu_seqlens, max_seqlen, batch, deterministic,
-                cu_seqlens_k, max_seqlen_k):
+                cu_seqlens_k, max_seqlen_k, window, sinks):
         o, lse = forward(q, k, v, causal, scale, cu_seqlens, max_seqlen, batch,
-                         cu_seqlens_k=cu_seqlens_k, max_seqlen_k=max_seqlen_k)
+                         cu_seqlens_k=cu_seqlens_k, max_seqlen_k=max_seqlen_k, window=window,
+                         sinks=sinks)
         ctx.save_for_backward(q, k, v, o, lse, cu_seqlens, cu_seqlens_k)
-        ctx.args = (causal, scale, max_seqlen, batch, deterministic, max_seqlen_k)
+        ctx.args = (causal, scale, max_seqlen, batch, deterministic, max_seqlen_k, window, sinks)
         return o
 
     @staticmethod
     def backward(ctx, dout):
         q, k, v, o, lse, cu_seqlens, cu_seqlens_k = ctx.saved_tensors
-        causal, scale, max_seqlen, batch, deterministic, max_seqlen_k = ctx.args
+        causal, scale, max_seqlen, batch, deterministic, max_seqlen_k, window, sinks = ctx.args
         dq, dk, dv = backward(q, k, v, o, dout.contiguous(), lse, causal, scale, cu_seqlens,
                               max_seqlen, batch, deterministic, cu_seqlens_k=cu_seqlens_k,
-                              max_seqlen_k=max_seqlen_k)
-        return dq, dk, dv, None, None, None, None, None, None, None, None
+                              max_seqlen_k=max_seqlen_k, window=window, sinks=sinks)
+        return dq, dk, dv, None, None, None, None, None, None, None, None, None, None
 
 
 def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,
               deterministic=False, cu_seqlens_k=None, max_seqlen_k=None, rotary=None,
-              positions=None, positions_k=None, interleaved=False):
+              positions=None, positions_k=None, interleaved=False, window=None, sinks=0):
     """Differentiable attention (autograd wrapper around forward/backward).
+
+    window and sinks bound what a position sees, as in `forward`: the last window keys up to
+    its own, and the first sinks ones.
 
     With rotary (a rotary_table) q and k are first turned to their positions: by default
     each sequence counts from 0; positions gives them, for q and k alike unless positions_k
@@ -438,7 +522,7 @@ def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=Non
     elif positions is not None or positions_k is not None:
         raise ValueError("positions need a rotary table")
     return _Attention.apply(q, k, v, causal, scale, cu_seqlens, max_seqlen, batch, deterministic,
-                            cu_seqlens_k, max_seqlen_k)
+                            cu_seqlens_k, max_seqlen_k, window, sinks)
 
 
 from . import serving  # noqa: E402  (uses the binding above)

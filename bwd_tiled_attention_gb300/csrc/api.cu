@@ -174,10 +174,26 @@ bool same_boundaries(const Shape& s, const int* cu_q, const int* cu_k) {
 
 size_t elem_bytes(fa_dtype t) { return t == FA_FP32 ? 4 : 2; }
 
+// A window of W keys and S first ones hides something only where some key is neither;
+// otherwise the call is that without a window (window = 0).
+struct Window {
+    int window, sinks;
+};
+fa_status check_window(int window, int sinks, int Nk, Window& w) {
+    w.window = w.sinks = 0;
+    if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    if (window < Nk && sinks < Nk) {
+        w.window = window;
+        w.sinks = sinks;
+    }
+    return FA_OK;
+}
+
 fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, fa_dtype o_dtype,
                    float* lse, int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k,
                    int d, float scale, int causal, const int* cu_q, const int* cu_k,
-                   void* workspace, size_t workspace_bytes, fa_stream_t stream) {
+                   void* workspace, size_t workspace_bytes, fa_stream_t stream,
+                   Window w = {0, 0}) {
     Shape s;
     fa_status st = check_shape(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, cu_q, cu_k, s);
     if (st != FA_OK) return st;
@@ -211,6 +227,8 @@ fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, fa_dtyp
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal ? 1 : 0;
     p.o_fp32 = o_dtype == FA_FP32;
+    p.window = w.window;
+    p.sinks = w.sinks;
     const int nsm = sm_count();
     if (nsm <= 0) return FA_ERR_CUDA;
     cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
@@ -218,11 +236,11 @@ fa_status fwd_impl(const void* q, const void* k, const void* v, void* o, fa_dtyp
                                  causal ? kOrderLevelDesc : kOrderSeqDesc, lay.max_units,
                                  workspace, lay.units, 0, false, cu_k, Nk, s.Tk, strm);
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    return cuda_status(launch_fwd(p, nsm, strm));
+    return cuda_status(w.window ? launch_fwd_window(p, nsm, strm) : launch_fwd(p, nsm, strm));
 }
 
 size_t bwd_ws_bytes(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k, int d,
-                    bool sems_offset) {
+                    bool sems_offset, Window win = {0, 0}) {
     if (B < 0 || Hq <= 0 || Hkv <= 0 || Nq < 0 || total_q < 0 || Nk < 0 || total_k < 0 ||
         (d != 64 && d != 96 && d != 128 && d != 192 && d != 256))
         return 0;
@@ -230,14 +248,27 @@ size_t bwd_ws_bytes(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int tot
     const long long Tk = total_k > 0 ? total_k : (long long)B * Nk;
     if (Tq > 0x7FFFFFFFLL || Tk > 0x7FFFFFFFLL) return 0;
     const BwdWs lay = bwd_ws_layout(B, Hq, Hkv, (int)Tq, (int)Tk, d);
+    if (win.sinks) return far_ws_layout(lay, B, Hkv, (int)Tq, d, win.sinks).bytes;
     return sems_offset ? lay.sems : lay.bytes;
+}
+
+// Layout of the far units' part (all zero without sinks), and whether the workspace holds
+// everything.
+fa_status far_layout(const Shape& s, const BwdWs& lay, Window win, size_t workspace_bytes, FarWs& far) {
+    if (win.sinks) {
+        far = far_ws_layout(lay, s.B, s.Hkv, s.Tq, s.d, win.sinks);
+        if (s.B >= kFarUnit || (long long)cdiv(cdiv(s.Nq, kTile), far.chunk) * far.tiles > kMaxTiles ||
+            far.max_units + lay.max_units > 0x7FFFFFFFLL)
+            return FA_ERR_UNSUPPORTED;
+    }
+    return workspace_bytes < (win.sinks ? far.bytes : lay.bytes) ? FA_ERR_INVALID_ARG : FA_OK;
 }
 
 fa_status bwd_preprocess_impl(const void* o, fa_dtype o_dtype, const void* dout, float* D,
                               void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
                               int Nq, int total_q, int Nk, int total_k, int d, int causal,
                               const int* cu_q, const int* cu_k, int deterministic,
-                              fa_stream_t stream) {
+                              fa_stream_t stream, Window win = {0, 0}) {
     Shape s;
     fa_status st = check_shape(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, cu_q, cu_k, s);
     if (st != FA_OK) return st;
@@ -248,7 +279,9 @@ fa_status bwd_preprocess_impl(const void* o, fa_dtype o_dtype, const void* dout,
     if (!aligned16(o) || !aligned16(dout) || !aligned4(D) || !aligned16(workspace))
         return FA_ERR_INVALID_ARG;
     const BwdWs lay = bwd_ws_layout(B, Hq, Hkv, s.Tq, s.Tk, d);
-    if (workspace_bytes < lay.bytes) return FA_ERR_INVALID_ARG;
+    FarWs far = {};
+    const fa_status fs = far_layout(s, lay, win, workspace_bytes, far);
+    if (fs != FA_OK) return fs;
     const int nsm = sm_count();
     if (nsm <= 0) return FA_ERR_CUDA;
     cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
@@ -258,8 +291,10 @@ fa_status bwd_preprocess_impl(const void* o, fa_dtype o_dtype, const void* dout,
     char* ws = static_cast<char*>(workspace);
     // units are key/value tiles; dQ semaphores are numbered by query tile
     // units: (key/value tile, run of query heads), runs innermost
-    cudaError_t e = launch_sched(cu_k, B, Nk, s.Tk, Hkv * lay.nruns, kTile, order, lay.max_units,
-                                 workspace, lay.units, lay.tile_off, true, cu_q, Nq, s.Tq, strm);
+    cudaError_t e = launch_sched(cu_k, B, Nk, s.Tk, Hkv * lay.nruns, kTile, order,
+                                 lay.max_units + far.max_units, workspace,
+                                 win.sinks ? far.units : lay.units, lay.tile_off, true, cu_q, Nq,
+                                 s.Tq, strm, far.chunk, far.tiles);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     e = launch_bwd_preprocess(o, o_dtype == FA_FP32, dout, D,
                               reinterpret_cast<float*>(ws + lay.dq_acc),
@@ -273,7 +308,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* dout
                    fa_dtype grad_dtype, void* workspace, size_t workspace_bytes, int B, int Hq,
                    int Hkv, int Nq, int total_q, int Nk, int total_k, int d, float scale,
                    int causal, const int* cu_q, const int* cu_k, int deterministic,
-                   fa_stream_t stream) {
+                   fa_stream_t stream, Window win = {0, 0}) {
     Shape s;
     fa_status st = check_shape(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, cu_q, cu_k, s);
     if (st != FA_OK) return st;
@@ -298,7 +333,9 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* dout
         !aligned16(dk) || !aligned16(dv) || !aligned4(lse) || !aligned4(D) || !aligned16(workspace))
         return FA_ERR_INVALID_ARG;
     const BwdWs lay = bwd_ws_layout(B, Hq, Hkv, s.Tq, s.Tk, d);
-    if (workspace_bytes < lay.bytes) return FA_ERR_INVALID_ARG;
+    FarWs far = {};
+    const fa_status fs = far_layout(s, lay, win, workspace_bytes, far);
+    if (fs != FA_OK) return fs;
     BwdParams p;
     std::memset(&p, 0, sizeof(p));
     if (!make_map(&p.tm_q, q, s.Tq, Hq, d) || !make_map(&p.tm_k, k, s.Tk, Hkv, d) ||
@@ -328,9 +365,15 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* dout
     p.grad_fp32 = grad_dtype == FA_FP32;
     p.hchunk = lay.hchunk;
     p.nchunks = lay.nruns;
+    p.window = win.window;
+    p.sinks = win.sinks;
+    p.far_chunk = far.chunk;
+    p.sink_tiles = far.tiles;
+    p.sink_off = far.sinks;
+    if (win.sinks) p.units_off = far.units;
     const int nsm = sm_count();
     if (nsm <= 0) return FA_ERR_CUDA;
-    cudaError_t e = launch_bwd(p, nsm, strm);
+    cudaError_t e = win.window ? launch_bwd_window(p, nsm, strm) : launch_bwd(p, nsm, strm);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     char* ws = static_cast<char*>(workspace);
     const bool partials = lay.nruns > 1;
@@ -339,6 +382,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* dout
                                partials ? reinterpret_cast<const float*>(ws + lay.dv_acc) : nullptr,
                                dk, dv, s.Tq, s.Tk, Hq, Hkv, lay.nruns, d, scale, p.grad_fp32, nsm,
                                strm);
+    if (e == cudaSuccess && win.sinks) e = launch_fold_sinks(p, nsm, strm);
     return cuda_status(e);
 }
 
@@ -390,6 +434,52 @@ size_t fa_bwd_workspace_size(int B, int Hq, int Hkv, int N, int total_tokens, in
 size_t fa_bwd_kv_workspace_size(int B, int Hq, int Hkv, int Nq, int total_q, int Nk,
                                 int total_k, int d) {
     return bwd_ws_bytes(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, false);
+}
+
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fa_dtype o_dtype,
+                        float* lse, int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k,
+                        int d, float scale, int window, int sinks, const int* cu_seqlens_q,
+                        const int* cu_seqlens_k, void* workspace, size_t workspace_bytes,
+                        fa_stream_t stream) {
+    Window w;
+    const fa_status st = check_window(window, sinks, Nk, w);
+    if (st != FA_OK) return st;
+    return fwd_impl(q, k, v, o, o_dtype, lse, B, Hq, Hkv, Nq, total_q, Nk, total_k, d, scale, 1,
+                    cu_seqlens_q, cu_seqlens_k, workspace, workspace_bytes, stream, w);
+}
+
+size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k,
+                                    int d, int window, int sinks) {
+    Window w;
+    if (check_window(window, sinks, Nk, w) != FA_OK) return 0;
+    return bwd_ws_bytes(B, Hq, Hkv, Nq, total_q, Nk, total_k, d, false, w);
+}
+
+fa_status fa_bwd_window_preprocess(const void* o, fa_dtype o_dtype, const void* dout, float* D,
+                                   void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                                   int Nq, int total_q, int Nk, int total_k, int d, int window,
+                                   int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                   int deterministic, fa_stream_t stream) {
+    Window w;
+    const fa_status st = check_window(window, sinks, Nk, w);
+    if (st != FA_OK) return st;
+    return bwd_preprocess_impl(o, o_dtype, dout, D, workspace, workspace_bytes, B, Hq, Hkv, Nq,
+                               total_q, Nk, total_k, d, 1, cu_seqlens_q, cu_seqlens_k, deterministic,
+                               stream, w);
+}
+
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* dout,
+                        const float* lse, const float* D, void* dq, void* dk, void* dv,
+                        fa_dtype grad_dtype, void* workspace, size_t workspace_bytes, int B, int Hq,
+                        int Hkv, int Nq, int total_q, int Nk, int total_k, int d, float scale,
+                        int window, int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                        int deterministic, fa_stream_t stream) {
+    Window w;
+    const fa_status st = check_window(window, sinks, Nk, w);
+    if (st != FA_OK) return st;
+    return bwd_impl(q, k, v, dout, lse, D, dq, dk, dv, grad_dtype, workspace, workspace_bytes, B, Hq,
+                    Hkv, Nq, total_q, Nk, total_k, d, scale, 1, cu_seqlens_q, cu_seqlens_k,
+                    deterministic, stream, w);
 }
 
 size_t fa_bwd_workspace_semaphore_offset(int B, int Hq, int Hkv, int N, int total_tokens, int d) {

@@ -110,17 +110,79 @@ static_assert(sizeof(BwdSmem<128>) <= 232448, "backward shared memory exceeds 22
 // key of tile j, ni = query tiles the unit visits per head, ns = C * ni steps.
 struct BUnit {
     int b, j, uh, g, h0, t0, L, tk0, Lk, off, nt, ntk, i0, ni, ns;
+    int far;  // with a window: 1 + the chunk of query tiles of a far unit, else 0
 };
+
+// With a window of W keys and S first ones (sinks): a unit of key/value tile j walks
+// the query tiles whose window reaches it (about W / 128 + 1 of them) under the window's
+// mask alone.  The pairs of sinks and rows that lie further on belong to far units, of
+// C = p.far_chunk query tiles each: a tile of sinks would otherwise be one unit that
+// walks every query tile, as long as all the others together where the window is short
+// (N = 32768, W = 1024: 1024 steps of 268 a CTA).  Far units come first in the list.
+// Both leave fp32 partials of the sinks' dK and dV, which fold_sinks_kernel adds up in
+// a fixed order: the near unit in slot 0 of its sequence, chunk q in slot 1 + q.
+
+// Query tiles of unit x of a windowed call: rows r with c - off <= r < c - off + W for a
+// key c of the tile, or for a far unit r >= c - off + W for a sink c of the tile.
+__device__ __forceinline__ void window_span(BUnit& x, const BwdParams& p) {
+    const int c0 = x.j * kTile;
+    int i0, i1;
+    if (x.far == 0) {
+        i0 = max(0, floor_div(c0 - x.off, kTile));
+        i1 = min(x.nt, floor_div(min(c0 + kTile, x.Lk) - 2 + p.window - x.off, kTile) + 1);
+    } else {
+        const int q = x.far - 1;
+        i0 = max(q * p.far_chunk, floor_div(c0 + p.window - x.off, kTile));
+        i1 = min(x.nt, (q + 1) * p.far_chunk);
+        if (c0 >= min(p.sinks, x.Lk) || c0 + p.window >= x.Lk) i1 = i0;
+    }
+    x.i0 = i0;
+    x.ni = max(0, i1 - i0);
+}
+
+// Visible query columns [lo, hi), within query tile i, of key c of unit x.
+__device__ __forceinline__ void window_cols(const BUnit& x, const BwdParams& p, int c, int i, int& lo,
+                                            int& hi) {
+    const int r = c - x.off;  // the key's own row
+    const int from = x.far ? r + p.window : r;
+    const int to = x.far ? (c < min(p.sinks, x.Lk) ? x.L : 0) : (c < x.Lk ? min(x.L, r + p.window) : 0);
+    lo = max(0, from - i * kTile);
+    hi = min(kTile, to - i * kTile);
+}
+
+// Sink tiles with far rows in query tile i: tiles [0, that).
+__device__ __forceinline__ int far_tiles(const BUnit& x, const BwdParams& p, int i) {
+    const int last = min((i + 1) * kTile, x.L) - 1 + x.off;  // the tile's last position
+    return max(0, min(cdiv(min(p.sinks, x.Lk), kTile), floor_div(last - p.window, kTile) + 1));
+}
+
+// Place of the fp32 partials of dK (which = 0) or dV (1) of sink row c of unit x.
+template <int DR>
+__device__ __forceinline__ float* sink_row(const BUnit& x, const BwdParams& p, const int* tile_off,
+                                           int which, int c) {
+    const int slot = tile_off[x.b] / p.far_chunk + 2 * x.b + x.far;
+    float* base = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + p.sink_off);
+    return base + ((((size_t)slot * 2 + which) * (p.Hkv * p.nchunks) + x.uh) * p.sinks + c) * DR;
+}
 
 // KV = false: keys and queries share their boundaries (Lk = L, off = 0), and
 // the geometry is the plain square one.  RUNS = false: one query head per
 // unit (the unit-list head field is that head); true: runs of p.hchunk > 1.
-template <bool KV, bool RUNS>
+template <bool KV, bool RUNS, bool WIN>
 __device__ __forceinline__ BUnit decode_bunit(int2 u, const BwdParams& p) {
+    static_assert(KV || !WIN, "the window has the geometry of separate lengths");
     BUnit x;
     x.b = u.x;
     x.j = unit_tile(u.y);
     x.uh = unit_head(u.y);
+    if constexpr (WIN) {
+        x.far = 0;
+        if (u.x & kFarUnit) {
+            x.b = u.x & ~kFarUnit;
+            x.far = 1 + x.j / p.sink_tiles;
+            x.j -= (x.far - 1) * p.sink_tiles;
+        }
+    }
     if constexpr (RUNS) {
         x.g = x.uh / p.nchunks;
         x.h0 = x.g * (p.Hq / p.Hkv) + (x.uh - x.g * p.nchunks) * p.hchunk;
@@ -134,8 +196,12 @@ __device__ __forceinline__ BUnit decode_bunit(int2 u, const BwdParams& p) {
         seq_bounds(p.cu_seqlens_k, p.Nk, x.b, x.tk0, x.Lk);
         x.off = x.Lk - x.L;
         x.ntk = cdiv(x.Lk, kTile);
-        x.i0 = p.causal ? max(0, floor_div(x.j * kTile - x.off, kTile)) : 0;
-        x.ni = max(0, x.nt - x.i0);  // 0 only when the sequence has no queries
+        if constexpr (WIN) {
+            window_span(x, p);
+        } else {
+            x.i0 = p.causal ? max(0, floor_div(x.j * kTile - x.off, kTile)) : 0;
+            x.ni = max(0, x.nt - x.i0);  // 0 only when the sequence has no queries
+        }
     } else {
         x.tk0 = x.t0;
         x.Lk = x.L;
@@ -156,8 +222,9 @@ __device__ __forceinline__ BUnit decode_bunit(int2 u, const BwdParams& p) {
 // In atomic mode every unit of a (sequence, head) walks the tiles in the same
 // order, so units running side by side load the same Q/dO tile and reduce into
 // the same dQ tile while it is resident in L2.
-template <bool KV>
+template <bool KV, bool WIN>
 __device__ __forceinline__ int walk_tile(const BUnit& x, int s, int deterministic, int causal) {
+    if constexpr (WIN) return deterministic ? x.i0 + s : x.i0 + x.ni - 1 - s;
     if (!causal) return s;
     return deterministic ? (KV ? x.i0 : x.j) + s : x.nt - 1 - s;
 }
@@ -176,15 +243,15 @@ struct StepPos {
 
 // Query head h and query tile i of step s of unit x (w: the walk position of
 // step s, used when the unit walks a run of heads).
-template <bool KV, bool RUNS>
+template <bool KV, bool RUNS, bool WIN>
 __device__ __forceinline__ void unit_step(const BUnit& x, int s, const StepPos& w,
                                           const BwdParams& p, int& h, int& i) {
     if constexpr (RUNS) {
         h = x.h0 + w.hh;
-        i = walk_tile<KV>(x, w.si, p.deterministic, p.causal);
+        i = walk_tile<KV, WIN>(x, w.si, p.deterministic, p.causal);
     } else {
         h = x.h0;
-        i = walk_tile<KV>(x, s, p.deterministic, p.causal);
+        i = walk_tile<KV, WIN>(x, s, p.deterministic, p.causal);
     }
 }
 
@@ -192,12 +259,15 @@ __device__ __forceinline__ void unit_step(const BUnit& x, int s, const StepPos& 
 // Contributions arrive in descending key/value tile: from jmax(i), ..., 0,
 // where jmax(i) is the last key/value tile a row of query tile i sees (i for
 // equal lengths under the causal mask; ntk - 1 without it).
-template <bool KV>
-__device__ __forceinline__ int dq_rank(const BUnit& x, int i, int causal) {
+// With a window the far units' come first, in descending tile too.
+template <bool KV, bool WIN>
+__device__ __forceinline__ int dq_rank(const BUnit& x, const BwdParams& p, int i, int causal) {
     if constexpr (!KV) return causal ? i - x.j : x.nt - 1 - x.j;
+    const int before = WIN ? far_tiles(x, p, i) : 0;
+    if (WIN && x.far) return before - 1 - x.j;
     const int jmax = causal ? min(x.ntk - 1, floor_div((i + 1) * kTile + x.off - 1, kTile))
                             : x.ntk - 1;
-    return jmax - x.j;
+    return before + jmax - x.j;
 }
 
 __device__ __forceinline__ void raise_abort(volatile int* flag, WsHeader* hdr, int code) {
@@ -296,7 +366,7 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&sv)[32], const float* n
 // S and dP contract over the first 96 columns only (6 MMAs of K = 16).  dV, dK
 // and dQ keep N = 128 (their B operands are read MN-major in 64-column swizzle
 // atoms); their last 32 columns are zero and neither stored nor merged.
-template <int D, int DR, bool KV, bool RUNS>
+template <int D, int DR, bool KV, bool RUNS, bool WIN>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     pdl_trigger();
@@ -389,7 +459,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             unit.y = __shfl_sync(0xffffffffu, unit.y, 0);
             ++sched_it;
             if (unit.x < 0) break;
-            const BUnit x = decode_bunit<KV, RUNS>(unit, p);
+            const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
             if (!(ok = lane0_wait(smem_u32(&sm.kv_empty), (unit_it & 1) ^ 1, abort_flag, hdr)))
                 break;
             if (lane == 0) {
@@ -406,7 +476,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             StepPos w;
             for (int s = 0; s < x.ns && ok; ++s, ++c, w.next(x.ni)) {
                 int h, i;
-                unit_step<KV, RUNS>(x, s, w, p, h, i);
+                unit_step<KV, RUNS, WIN>(x, s, w, p, h, i);
                 const int st = c & 1;
                 // Q_i (with its LSE and D rows) into the 2-stage ring
                 if (!(ok = lane0_wait(smem_u32(&sm.q_empty[st]), ((c >> 1) & 1) ^ 1, abort_flag,
@@ -462,11 +532,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_empty[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const BUnit x = decode_bunit<KV, RUNS>(unit, p);
+                const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
                 StepPos w;
                 for (int s = 0; s < x.ns; ++s, ++c, w.next(x.ni)) {
                     int h, i;
-                    unit_step<KV, RUNS>(x, s, w, p, h, i);
+                    unit_step<KV, RUNS, WIN>(x, s, w, p, h, i);
                     if (!(ok = wait_or_abort(smem_u32(&sm.do_empty), (c & 1) ^ 1, abort_flag, hdr)))
                         break;
                     const uint32_t dbar = smem_u32(&sm.do_full);
@@ -517,7 +587,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_empty[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const BUnit x = decode_bunit<KV, RUNS>(unit, p);
+                const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
                 if (!(ok = wait_or_abort(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
                 if ((!KV || x.ns > 0) && !(ok = issue_s(cnt))) break;
                 for (int s = 0; s < x.ns; ++s, ++cnt) {
@@ -687,7 +757,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
             ++sched_it;
             if (unit.x < 0) break;
-            const BUnit x = decode_bunit<KV, RUNS>(unit, p);
+            const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
             // key position c within its sequence: query column r sees it iff
             // r >= c - off (causal) and r < L; a key past the end sees nothing
             const int c = x.j * kTile + rk;
@@ -696,12 +766,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             StepPos w;
             for (int s = 0; s < x.ns; ++s, ++cnt, w.next(x.ni)) {
                 int h, i;
-                unit_step<KV, RUNS>(x, s, w, p, h, i);
+                unit_step<KV, RUNS, WIN>(x, s, w, p, h, i);
                 const int st = cnt & 1;
                 // visible query columns of this key row: [lo, hi); the warp skips the
                 // mask when every row sees every column
                 int lo, hi;
-                if constexpr (KV) {
+                if constexpr (WIN) {
+                    window_cols(x, p, c, i, lo, hi);
+                } else if constexpr (KV) {
                     lo = p.causal ? max(0, c_off - i * kTile) : 0;
                     hi = min(kTile, L_vis - i * kTile);
                 } else {
@@ -806,11 +878,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
             ++sched_it;
             if (unit.x < 0) break;
-            const BUnit x = decode_bunit<KV, RUNS>(unit, p);
+            const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
             StepPos w;
             for (int s = 0; s < x.ns; ++s, w.next(x.ni)) {
                 int h, i;
-                unit_step<KV, RUNS>(x, s, w, p, h, i);
+                unit_step<KV, RUNS, WIN>(x, s, w, p, h, i);
                 if (!(ok = wg_wait(smem_u32(&sm.dq_full), cnt & 1, abort_flag, hdr))) break;
                 tc_fence_after();
                 int* sem = nullptr;
@@ -818,7 +890,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (p.deterministic) {
                     sem = sems + (size_t)h * n_qtiles + tile_off[x.b] + i;
                     if (leader) {
-                        sem_ok = sem_wait(sem, dq_rank<KV>(x, i, p.causal), hdr);
+                        sem_ok = sem_wait(sem, dq_rank<KV, WIN>(x, p, i, p.causal), hdr);
                         if (!sem_ok) raise_abort(abort_flag, hdr, kErrTimeout);
                     }
                     sem_ok = named_bar_and(1, 128, sem_ok);
@@ -911,6 +983,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     if (none) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = 0u;
+                    }
+                    if constexpr (WIN) {
+                        if (kr < p.sinks) {
+                            float4* s4 = reinterpret_cast<float4*>(
+                                sink_row<DR>(x, p, tile_off, which, kr) + cc * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                s4[e] = make_float4(__uint_as_float(v[4 * e]) * mul,
+                                                    __uint_as_float(v[4 * e + 1]) * mul,
+                                                    __uint_as_float(v[4 * e + 2]) * mul,
+                                                    __uint_as_float(v[4 * e + 3]) * mul);
+                        }
+                        if (x.far) continue;
                     }
                     if (partial) {
                         float* acc = (which == 0 ? dk_acc : dv_acc) +
@@ -1042,7 +1127,7 @@ struct Pending {
     bool set = false;
 };
 
-template <int D, bool KV>
+template <int D, bool KV, bool WIN>
 __global__ void __launch_bounds__(kWideThreads, 1)
     fa_bwd_wide_kernel(const __grid_constant__ BwdParams p) {
     pdl_trigger();
@@ -1140,7 +1225,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_full[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const BUnit x = decode_bunit<KV, false>(unit, p);
+                const BUnit x = decode_bunit<KV, false, WIN>(unit, p);
                 const int h = x.h0;
                 if (unit_it > 0 &&
                     !(ok = wait_or_abort(smem_u32(&sm.kv_empty), (unit_it - 1) & 1, abort_flag, hdr)))
@@ -1153,7 +1238,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 }
                 ++unit_it;
                 auto row0 = [&](int s) {
-                    return x.t0 + walk_tile<KV>(x, s, p.deterministic, p.causal) * kTile;
+                    return x.t0 + walk_tile<KV, WIN>(x, s, p.deterministic, p.causal) * kTile;
                 };
                 // pass 1: Q(0), then Q(s), dO(s - 1) for s >= 1, then dO(n - 1)
                 for (int s = 0; s <= x.ns && ok; ++s) {
@@ -1256,7 +1341,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_empty[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const BUnit x = decode_bunit<KV, false>(unit, p);
+                const BUnit x = decode_bunit<KV, false, WIN>(unit, p);
                 if (!(ok = wait_or_abort(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
                 tc_fence_after();
                 ++unit_it;
@@ -1360,13 +1445,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
             ++sched_it;
             if (unit.x < 0) break;
-            const BUnit x = decode_bunit<KV, false>(unit, p);
+            const BUnit x = decode_bunit<KV, false, WIN>(unit, p);
             const int h = x.h0;
             const int c = x.j * kTile + ct;  // this thread's key row within its sequence
             const int c_off = c - x.off;
             const int L_vis = c < x.Lk ? x.L : 0;
             auto visible = [&](int i, int& lo, int& hi) {
-                if constexpr (KV) {
+                if constexpr (WIN) {
+                    window_cols(x, p, c, i, lo, hi);
+                } else if constexpr (KV) {
                     lo = p.causal ? max(0, c_off - i * kTile) : 0;
                     hi = min(kTile, L_vis - i * kTile);
                 } else {
@@ -1403,6 +1490,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         tmem_ld_wait();
                     }
                     if (!valid) continue;
+                    if constexpr (WIN) {
+                        if (c < p.sinks) {
+                            float4* s4 = reinterpret_cast<float4*>(
+                                sink_row<D>(x, p, tile_off, 1 - pass, c) + cc * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                s4[e] = make_float4(__uint_as_float(v[4 * e]) * mul,
+                                                    __uint_as_float(v[4 * e + 1]) * mul,
+                                                    __uint_as_float(v[4 * e + 2]) * mul,
+                                                    __uint_as_float(v[4 * e + 3]) * mul);
+                        }
+                        if (x.far) continue;
+                    }
                     if (partial) {
                         float* acc = (pass == 0 ? dv_acc : dk_acc) +
                                      (tok * (size_t)(p.Hkv * p.nchunks) + x.uh) * D + cc * 32;
@@ -1445,9 +1545,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const uint64_t cc2 = f2_pack(p.scale_log2, p.scale_log2);
             for (int pass = 0; pass < 2 && ok; ++pass) {
                 float nl2 = 0.f, ndd = 0.f;
-                if (x.ns > 0) fetch_rows(walk_tile<KV>(x, 0, p.deterministic, p.causal), nl2, ndd);
+                if (x.ns > 0) fetch_rows(walk_tile<KV, WIN>(x, 0, p.deterministic, p.causal), nl2, ndd);
                 for (int s = 0; s < x.ns; ++s) {
-                    const int i = walk_tile<KV>(x, s, p.deterministic, p.causal);
+                    const int i = walk_tile<KV, WIN>(x, s, p.deterministic, p.causal);
                     const int rb = rs++ & 1;  // row buffer: its readers of two steps ago are past
                     sm.lse2[rb][ct] = -nl2;   // the named barrier of the previous step
                     sm.dd[rb][ct] = -ndd;
@@ -1458,7 +1558,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (!(ok = wg_wait(full_bar, full_par, abort_flag, hdr))) break;
                     tc_fence_after();
                     if (s + 1 < x.ns)
-                        fetch_rows(walk_tile<KV>(x, s + 1, p.deterministic, p.causal), nl2, ndd);
+                        fetch_rows(walk_tile<KV, WIN>(x, s + 1, p.deterministic, p.causal), nl2, ndd);
                     int lo, hi;
                     visible(i, lo, hi);
                     const bool full = lo == 0 && hi == kTile;
@@ -1533,7 +1633,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     bool sem_ok = true;
                     if (p.deterministic) {
                         sem = sems + (size_t)h * n_qtiles + tile_off[x.b] + i;
-                        if (leader && !sem_wait(sem, dq_rank<KV>(x, i, p.causal), hdr)) {
+                        if (leader && !sem_wait(sem, dq_rank<KV, WIN>(x, p, i, p.causal), hdr)) {
                             raise_abort(abort_flag, hdr, kErrTimeout);
                             sem_ok = false;
                         }
@@ -1634,6 +1734,118 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         tmem_dealloc(tmem, 512);
     }
 }
+
+// Units are (key/value tile, run of query heads), and with a window (chunk of query
+// tiles, tile of sinks, run of query heads).
+template <bool WIN>
+int bwd_grid(const BwdParams& p, int num_sms) {
+    long long tiles = max_tiles(p.B, p.Tk, kTile);
+    if (WIN && p.sink_tiles) tiles += far_chunks(p.B, p.T, p.far_chunk) * p.sink_tiles;
+    const long long bound = tiles * p.Hkv * p.nchunks;
+    return (int)(bound < num_sms ? bound : num_sms);
+}
+
+template <int D, bool WIN>
+cudaError_t launch_bwd_wide_t(const BwdParams& p, int num_sms, cudaStream_t stream) {
+    void (*kern)(const BwdParams);
+    if constexpr (WIN)
+        kern = fa_bwd_wide_kernel<D, true, true>;
+    else
+        kern = p.kv ? fa_bwd_wide_kernel<D, true, false> : fa_bwd_wide_kernel<D, false, false>;
+    const size_t smem = sizeof(WideSmem<D>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = bwd_grid<WIN>(p, num_sms);
+    if (grid <= 0) return cudaSuccess;
+    return launch_pdl(kern, dim3(grid), dim3(kWideThreads), smem, stream, p);
+}
+
+template <int D, int DR, bool WIN>
+cudaError_t launch_bwd_t(const BwdParams& p, int num_sms, cudaStream_t stream) {
+    void (*kern)(const BwdParams);
+    if constexpr (WIN)
+        kern = p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, true>
+                            : fa_bwd_kernel<D, DR, true, false, true>;
+    else
+        kern = p.kv ? (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, false>
+                                    : fa_bwd_kernel<D, DR, true, false, false>)
+                    : (p.hchunk > 1 ? fa_bwd_kernel<D, DR, false, true, false>
+                                    : fa_bwd_kernel<D, DR, false, false, false>);
+    const size_t smem = sizeof(BwdSmem<D>);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = bwd_grid<WIN>(p, num_sms);
+    if (grid <= 0) return cudaSuccess;
+    return launch_pdl(kern, dim3(grid), dim3(kBwdThreads), smem, stream, p);
+}
+
+template <bool WIN>
+cudaError_t launch_bwd_d(const BwdParams& p, int num_sms, cudaStream_t stream) {
+    if (p.d == 256) return launch_bwd_wide_t<256, WIN>(p, num_sms, stream);
+    if (p.d == 192) return launch_bwd_wide_t<192, WIN>(p, num_sms, stream);
+    if (p.d == 128) return launch_bwd_t<128, 128, WIN>(p, num_sms, stream);
+    if (p.d == 96) return launch_bwd_t<128, 96, WIN>(p, num_sms, stream);
+    return launch_bwd_t<64, 64, WIN>(p, num_sms, stream);
+}
+
+#ifdef FA_WINDOW
+
+// dK and dV of the sinks: the near unit's partial and the far chunks', summed over the
+// runs of heads, in that order.  A warp a (sequence, key/value head, sink), its lanes the
+// columns; a few thousand rows at most, behind the kernels that leave the partials.
+template <bool F32>
+__global__ void __launch_bounds__(256) fold_sinks_kernel(const __grid_constant__ BwdParams p) {
+    pdl_begin();
+    const WsHeader* hdr = static_cast<const WsHeader*>(p.workspace);
+    if (hdr->error) return;  // (the schedule was refused: nothing has been written)
+    const int* tile_off = reinterpret_cast<const int*>(static_cast<const char*>(p.workspace) + p.tile_off_off);
+    const float* acc = reinterpret_cast<const float*>(static_cast<const char*>(p.workspace) + p.sink_off);
+    const int heads = p.Hkv * p.nchunks, lane = lane_id();
+    const long long rows = (long long)p.B * p.Hkv * p.sinks;
+    for (long long row = (long long)blockIdx.x * 8 + warp_id(); row < rows; row += (long long)gridDim.x * 8) {
+        const int c = (int)(row % p.sinks);
+        const int g = (int)(row / p.sinks % p.Hkv), b = (int)(row / p.sinks / p.Hkv);
+        int t0, L, tk0, Lk;
+        seq_bounds(p.cu_seqlens, p.N, b, t0, L);
+        seq_bounds(p.cu_seqlens_k, p.Nk, b, tk0, Lk);
+        if (c >= Lk) continue;
+        const int slot0 = tile_off[b] / p.far_chunk + 2 * b;
+        const int slots = 1 + cdiv(cdiv(L, kTile), p.far_chunk);
+        for (int col = lane * 4; col < p.d; col += 128)
+            for (int which = 0; which < 2; ++which) {
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int run = 0; run < p.nchunks; ++run)
+                    for (int s = 0; s < slots; ++s) {
+                        const size_t at = ((((size_t)(slot0 + s) * 2 + which) * heads + g * p.nchunks + run) *
+                                               p.sinks + c) * p.d + col;
+                        const float4 x = *reinterpret_cast<const float4*>(acc + at);
+                        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+                    }
+                const size_t out = (((size_t)tk0 + c) * p.Hkv + g) * p.d + col;
+                void* base = which == 0 ? p.dk : p.dv;
+                if (F32)
+                    *reinterpret_cast<float4*>(static_cast<float*>(base) + out) = sum;
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + out) =
+                        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_bwd_window(const BwdParams& p, int num_sms, cudaStream_t stream) {
+    return launch_bwd_d<true>(p, num_sms, stream);
+}
+
+cudaError_t launch_fold_sinks(const BwdParams& p, int num_sms, cudaStream_t stream) {
+    const long long rows = (long long)p.B * p.Hkv * p.sinks, want = (rows + 7) / 8;
+    const int grid = (int)(want < 8LL * num_sms ? want : 8LL * num_sms);
+    return launch_pdl(p.grad_fp32 ? fold_sinks_kernel<true> : fold_sinks_kernel<false>, dim3(grid),
+                      dim3(256), 0, stream, p);
+}
+
+#else
 
 // D = rowsum(dO * O) per (token, head); zero the dQ accumulator row and the
 // semaphores.  Each lane takes 8 elements (16-byte loads), D/8 lanes per row,
@@ -1784,34 +1996,6 @@ int grid_for(long long work, int threads, int num_sms) {
     return (int)(g < 1 ? 1 : g);
 }
 
-template <int D>
-cudaError_t launch_bwd_wide_t(const BwdParams& p, int num_sms, cudaStream_t stream) {
-    auto kern = p.kv ? fa_bwd_wide_kernel<D, true> : fa_bwd_wide_kernel<D, false>;
-    const size_t smem = sizeof(WideSmem<D>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const long long bound = max_tiles(p.B, p.Tk, kTile) * (long long)p.Hkv * p.nchunks;
-    const int grid = (int)(bound < num_sms ? bound : num_sms);
-    if (grid <= 0) return cudaSuccess;
-    return launch_pdl(kern, dim3(grid), dim3(kWideThreads), smem, stream, p);
-}
-
-template <int D, int DR>
-cudaError_t launch_bwd_t(const BwdParams& p, int num_sms, cudaStream_t stream) {
-    auto kern = p.kv ? (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true>
-                                     : fa_bwd_kernel<D, DR, true, false>)
-                     : (p.hchunk > 1 ? fa_bwd_kernel<D, DR, false, true>
-                                     : fa_bwd_kernel<D, DR, false, false>);
-    const size_t smem = sizeof(BwdSmem<D>);
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    // units are (key/value tile, run of query heads)
-    const long long bound = max_tiles(p.B, p.Tk, kTile) * (long long)p.Hkv * p.nchunks;
-    const int grid = (int)(bound < num_sms ? bound : num_sms);
-    if (grid <= 0) return cudaSuccess;
-    return launch_pdl(kern, dim3(grid), dim3(kBwdThreads), smem, stream, p);
-}
-
 }  // namespace
 
 cudaError_t launch_bwd_preprocess(const void* o, int o_fp32, const void* dout, float* D,
@@ -1841,11 +2025,7 @@ cudaError_t launch_bwd_preprocess(const void* o, int o_fp32, const void* dout, f
 }
 
 cudaError_t launch_bwd(const BwdParams& p, int num_sms, cudaStream_t stream) {
-    if (p.d == 256) return launch_bwd_wide_t<256>(p, num_sms, stream);
-    if (p.d == 192) return launch_bwd_wide_t<192>(p, num_sms, stream);
-    if (p.d == 128) return launch_bwd_t<128, 128>(p, num_sms, stream);
-    if (p.d == 96) return launch_bwd_t<128, 96>(p, num_sms, stream);
-    return launch_bwd_t<64, 64>(p, num_sms, stream);
+    return launch_bwd_d<false>(p, num_sms, stream);
 }
 
 cudaError_t launch_bwd_postprocess(const float* dq_acc, void* dq, const float* dk_acc,
@@ -1872,5 +2052,7 @@ cudaError_t launch_bwd_postprocess(const float* dq_acc, void* dq, const float* d
 #undef FA_POST
     return e;
 }
+
+#endif
 
 }  // namespace fa

@@ -11,6 +11,12 @@
 // key c iff c <= r + Lk - Lq under the causal mask), and a row that sees no
 // key gets O = 0 and LSE = -inf.
 //
+// With a window of W keys and S first ones (sinks; fwd_window.cu compiles these
+// kernels), row r at position p = r + Lk - Lq sees keys c <= p with p - c < W or
+// c < S.  The tiles of a query tile are then those of the sinks and a stretch of
+// about W / 128 + 1; a unit walks the union of its two query tiles' stretches, and
+// a tile that one of them does not visit feeds the other's MMAs alone.
+//
 // Blackwell design ("FlashAttention-4 wird offiziell veröffentlicht", section
 // "Neue Hardwaremerkmale von Blackwell": single-thread tcgen05.mma accumulating
 // in tensor memory, A operand readable from tensor memory, warp specialisation):
@@ -123,12 +129,34 @@ static_assert(sizeof(FwdSmem<256>) + 1024 <= 232448, "forward shared memory exce
 // tile t visits (0 when the tile is past the end, or sees no key at all).
 struct UnitGeom {
     int b, m, h, g, t0, L, tk0, Lk, n[2], nkv;  // nkv >= 1 (see decode_unit)
+    // With a window: query tile t visits the sink tiles [0, min(st, lo[t])) and [lo[t],
+    // hi[t]); the unit walks [0, min(st, lo of both)) and the union of the stretches.
+    int st, lo[2], hi[2], first, nsink;
+    // Key/value tile of step j of the unit, and of step j of query tile t.
+    template <bool WIN>
+    __device__ __forceinline__ int tile(int j) const {
+        return !WIN || j < nsink ? j : first + (j - nsink);
+    }
+    template <bool WIN>
+    __device__ __forceinline__ int tile_of(int t, int j) const {
+        if constexpr (!WIN) return j;
+        const int l = t == 0 ? lo[0] : lo[1], s = min(st, l);
+        return j < s ? j : l + (j - s);
+    }
+    // Does query tile t take part in step j of the unit?
+    template <bool WIN>
+    __device__ __forceinline__ bool active(int t, int j) const {
+        if constexpr (!WIN) return j < n[t];
+        const int k = tile<true>(j);
+        return k < hi[t] && (k >= lo[t] || k < st);
+    }
 };
 
 // KV = false: keys and queries share their boundaries (Lk = L, tk0 = t0), and
 // the geometry is the plain square one.
-template <int D, bool KV>
+template <int D, bool KV, bool WIN>
 __device__ __forceinline__ UnitGeom decode_unit(int2 u, const FwdParams& p) {
+    static_assert(KV || !WIN, "the window has the geometry of separate lengths");
     UnitGeom x;
     x.b = u.x;
     x.m = unit_tile(u.y);
@@ -142,23 +170,44 @@ __device__ __forceinline__ UnitGeom decode_unit(int2 u, const FwdParams& p) {
         x.Lk = x.L;
     }
     const int r0 = x.m * FwdCfg<D>::kUnitRows;
+    if constexpr (WIN) {
+        x.st = cdiv(p.sinks, kTile);
+        x.first = 0x7FFFFFFF;
+        int end = 0;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int rs = r0 + t * kTile;  // first row of tile t
-        if (t >= FwdCfg<D>::kQTiles || rs >= x.L) {
-            x.n[t] = 0;
-        } else if (p.causal) {
-            const int re = min(rs + kTile, x.L);  // one past last valid row
-            x.n[t] = KV ? cdiv(max(re + x.Lk - x.L, 0), kTile) : cdiv(re, kTile);
-        } else {
-            x.n[t] = cdiv(x.Lk, kTile);
+        for (int t = 0; t < 2; ++t) {
+            const int rs = r0 + t * kTile, off = x.Lk - x.L;
+            x.n[t] = x.lo[t] = x.hi[t] = 0;
+            if (t < FwdCfg<D>::kQTiles && rs < x.L)
+                x.hi[t] = cdiv(max(min(rs + kTile, x.L) + off, 0), kTile);
+            if (x.hi[t] == 0) continue;
+            x.lo[t] = max(rs + off - p.window + 1, 0) / kTile;  // the first row reaches furthest back
+            x.n[t] = x.hi[t] - x.lo[t] + min(x.st, x.lo[t]);
+            x.first = min(x.first, x.lo[t]);
+            end = max(end, x.hi[t]);
         }
+        x.first = min(x.first, end);
+        x.nsink = min(x.st, x.first);
+        x.nkv = max(end - x.first + x.nsink, 1);
+    } else {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int rs = r0 + t * kTile;  // first row of tile t
+            if (t >= FwdCfg<D>::kQTiles || rs >= x.L) {
+                x.n[t] = 0;
+            } else if (p.causal) {
+                const int re = min(rs + kTile, x.L);  // one past last valid row
+                x.n[t] = KV ? cdiv(max(re + x.Lk - x.L, 0), kTile) : cdiv(re, kTile);
+            } else {
+                x.n[t] = cdiv(x.Lk, kTile);
+            }
+        }
+        // A unit whose rows see no key (KV only) still takes one key/value step
+        // with both query tiles masked off (no MMA issued): the producer and MMA
+        // thread then keep their usual barrier sequence, and the softmax warps
+        // write O = 0.
+        x.nkv = KV ? max(max(x.n[0], x.n[1]), 1) : max(x.n[0], x.n[1]);
     }
-    // A unit whose rows see no key (KV only) still takes one key/value step
-    // with both query tiles masked off (no MMA issued): the producer and MMA
-    // thread then keep their usual barrier sequence, and the softmax warps
-    // write O = 0.
-    x.nkv = KV ? max(max(x.n[0], x.n[1]), 1) : max(x.n[0], x.n[1]);
     return x;
 }
 
@@ -260,7 +309,7 @@ __device__ __forceinline__ void store_row(const FwdParams& p, uint32_t o_addr, i
 // S contracts over the first 96 columns only (6 MMAs of K = 16); PV keeps
 // N = 128 (V is read MN-major in 64-column swizzle atoms), and O's last 32
 // columns (all zero) are not stored.
-template <int D, int DR, bool OUT_FP32, bool KV>
+template <int D, int DR, bool OUT_FP32, bool KV, bool WIN>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     fa_fwd_kernel(const __grid_constant__ FwdParams p) {
     pdl_trigger();
@@ -339,7 +388,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_full[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const UnitGeom x = decode_unit<D, KV>(unit, p);
+                const UnitGeom x = decode_unit<D, KV, WIN>(unit, p);
                 const int row0 = x.t0 + x.m * Cfg::kUnitRows;
                 if (!(ok = wait_or_abort(smem_u32(&sm.q_empty), (unit_it & 1) ^ 1, abort_flag, hdr)))
                     break;
@@ -377,7 +426,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                 // its phase of k_full is complete
                                 if (c == 0) mbar_arrive_expect_tx(kb, Cfg::kTileBytes);
                                 tma_load_3d(smem_u32(sm.k[0]) + c * 16384, &p.tm_k, kb, c * 64,
-                                            x.g, x.tk0 + j * kTile);
+                                            x.g, x.tk0 + x.template tile<WIN>(j) * kTile);
                             }
                             if (!ok) break;
                             ++k_it;
@@ -392,7 +441,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             mbar_arrive_expect_tx(vb, Cfg::kVSlotBytes);
                             for (int c = 0; c < Cfg::kVChunk / 64; ++c)
                                 tma_load_3d(smem_u32(sm.v[slot]) + c * 16384, &p.tm_v, vb,
-                                            h * Cfg::kVChunk + c * 64, x.g, x.tk0 + (j - 1) * kTile);
+                                            h * Cfg::kVChunk + c * 64, x.g,
+                                            x.tk0 + x.template tile<WIN>(j - 1) * kTile);
                             ++v_it;
                         }
                     }
@@ -403,14 +453,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                                  abort_flag, hdr)))
                             break;
                         const uint32_t kb = smem_u32(&sm.k_full[st]), vb = smem_u32(&sm.v_full[st]);
+                        const int tok = x.tk0 + x.template tile<WIN>(j) * kTile;
                         mbar_arrive_expect_tx(kb, Cfg::kTileBytes);
                         for (int c = 0; c < Cfg::kBoxes; ++c)
-                            tma_load_3d(smem_u32(sm.k[st]) + c * 16384, &p.tm_k, kb, c * 64, x.g,
-                                        x.tk0 + j * kTile);
+                            tma_load_3d(smem_u32(sm.k[st]) + c * 16384, &p.tm_k, kb, c * 64, x.g, tok);
                         mbar_arrive_expect_tx(vb, Cfg::kTileBytes);
                         for (int c = 0; c < Cfg::kBoxes; ++c)
-                            tma_load_3d(smem_u32(sm.v[st]) + c * 16384, &p.tm_v, vb, c * 64, x.g,
-                                        x.tk0 + j * kTile);
+                            tma_load_3d(smem_u32(sm.v[st]) + c * 16384, &p.tm_v, vb, c * 64, x.g, tok);
                         ++kv_it;
                     }
                 }
@@ -452,7 +501,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 mbar_arrive(smem_u32(&sm.sched_empty[slot]));
                 ++sched_it;
                 if (unit.x < 0) break;
-                const UnitGeom x = decode_unit<D, KV>(unit, p);
+                const UnitGeom x = decode_unit<D, KV, WIN>(unit, p);
                 if (!(ok = wait_or_abort(smem_u32(&sm.q_full), unit_it & 1, abort_flag, hdr)))
                     break;
                 if constexpr (D > 128) {
@@ -546,13 +595,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ++unit_it;
                     ep[0] += n > 0;
                 } else {
+                    int seen[2] = {0, 0};  // steps that tile t has taken part in
                     for (int j = 0; j < x.nkv && ok; ++j) {
                         const int st = kv_it % S, par = (kv_it / S) & 1;
                         if (!(ok = wait_or_abort(smem_u32(&sm.k_full[st]), par, abort_flag, hdr))) break;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (!ok) break;
-                            if (t >= Cfg::kQTiles || j >= x.n[t]) continue;
+                            if (t >= Cfg::kQTiles || !x.template active<WIN>(t, j)) continue;
                             // S_t / P_t region is free once the previous O_t += P_t V is done
                             if (it[t] > 0 &&
                                 !(ok = wait_or_abort(smem_u32(&sm.o_done[t]), (it[t] - 1) & 1,
@@ -575,11 +625,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (!ok) break;
-                            if (t >= Cfg::kQTiles || j >= x.n[t]) continue;
+                            if (t >= Cfg::kQTiles || !x.template active<WIN>(t, j)) continue;
                             if (!(ok = wait_or_abort(smem_u32(&sm.p_full[t]), it[t] & 1, abort_flag,
                                                      hdr)))
                                 break;
-                            if (j == 0 && ep[t] > 0 &&
+                            const bool first = WIN ? seen[t] == 0 : j == 0;
+                            if (first && ep[t] > 0 &&
                                 !(ok = wait_or_abort(smem_u32(&sm.o_free[t]), (ep[t] - 1) & 1,
                                                      abort_flag, hdr)))
                                 break;
@@ -597,11 +648,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                 }
                                 mma_ts(tmem + o_col, tmem + p_col + kk * 8,
                                        make_sdesc(vb + kk * 2048, 16384, 1024), idPV,
-                                       (j > 0 || kk > 0) ? 1u : 0u);
+                                       (!first || kk > 0) ? 1u : 0u);
                             }
                             if (!ok) break;
                             mma_commit(smem_u32(&sm.o_done[t]));
                             ++it[t];
+                            ++seen[t];
                         }
                         mma_commit(smem_u32(&sm.kv_empty[st]));
                         ++kv_it;
@@ -639,7 +691,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
             ++sched_it;
             if (unit.x < 0) break;
-            const UnitGeom x = decode_unit<D, KV>(unit, p);
+            const UnitGeom x = decode_unit<D, KV, WIN>(unit, p);
             if constexpr (D > 128) {
                 if (t == 1) {
                     // Epilogue warps: store the unit the softmax warps have finished
@@ -680,6 +732,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // visible keys: col < limit (end-aligned causal mask)
             const int limit = KV ? (p.causal ? min(r + 1 + x.Lk - x.L, x.Lk) : x.Lk)
                                  : (p.causal ? min(r + 1, x.L) : x.L);
+            // with a window: and col >= from, or col < p.sinks
+            const int from = WIN ? r + x.Lk - x.L - p.window + 1 : 0;
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < nt; ++j) {
                 // D > 128: S alternates between two buffers, step by step
@@ -706,11 +760,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         s[96 + i] = __uint_as_float(r3[i]);
                     }
                 }
-                const int thr = limit - j * kTile;
+                const int key0 = x.template tile_of<WIN>(t, j) * kTile;
+                const int thr = limit - key0;
                 if (thr < kTile) {
 #pragma unroll
                     for (int i = 0; i < 128; ++i)
                         if (i >= thr) s[i] = -INFINITY;
+                }
+                if constexpr (WIN) {
+                    const int low = from - key0, sink = p.sinks - key0;
+                    if (low > 0) {
+#pragma unroll
+                        for (int i = 0; i < 128; ++i)
+                            if (i < low && i >= sink) s[i] = -INFINITY;
+                    }
                 }
                 // row max: 8 independent chains of 3-input maxima
                 float m8[8];
@@ -878,9 +941,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
 }
 
-template <int D, int DR, bool F32, bool KV>
+template <int D, int DR, bool F32, bool KV, bool WIN>
 cudaError_t launch_fwd_t(const FwdParams& p, int num_sms, cudaStream_t stream) {
-    auto kern = fa_fwd_kernel<D, DR, F32, KV>;
+    auto kern = fa_fwd_kernel<D, DR, F32, KV, WIN>;
     const size_t smem = sizeof(FwdSmem<D>) + 1024;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -890,29 +953,35 @@ cudaError_t launch_fwd_t(const FwdParams& p, int num_sms, cudaStream_t stream) {
     return launch_pdl(kern, dim3(grid), dim3(kFwdThreads), smem, stream, p);
 }
 
-}  // namespace
-
-template <bool KV>
+template <bool KV, bool WIN>
 cudaError_t launch_fwd_kv(const FwdParams& p, int num_sms, cudaStream_t stream) {
     if (p.d == 128)
-        return p.o_fp32 ? launch_fwd_t<128, 128, true, KV>(p, num_sms, stream)
-                        : launch_fwd_t<128, 128, false, KV>(p, num_sms, stream);
+        return p.o_fp32 ? launch_fwd_t<128, 128, true, KV, WIN>(p, num_sms, stream)
+                        : launch_fwd_t<128, 128, false, KV, WIN>(p, num_sms, stream);
     if (p.d == 96)
-        return p.o_fp32 ? launch_fwd_t<128, 96, true, KV>(p, num_sms, stream)
-                        : launch_fwd_t<128, 96, false, KV>(p, num_sms, stream);
+        return p.o_fp32 ? launch_fwd_t<128, 96, true, KV, WIN>(p, num_sms, stream)
+                        : launch_fwd_t<128, 96, false, KV, WIN>(p, num_sms, stream);
     if (p.d == 256)
-        return p.o_fp32 ? launch_fwd_t<256, 256, true, KV>(p, num_sms, stream)
-                        : launch_fwd_t<256, 256, false, KV>(p, num_sms, stream);
+        return p.o_fp32 ? launch_fwd_t<256, 256, true, KV, WIN>(p, num_sms, stream)
+                        : launch_fwd_t<256, 256, false, KV, WIN>(p, num_sms, stream);
     if (p.d == 192)
-        return p.o_fp32 ? launch_fwd_t<192, 192, true, KV>(p, num_sms, stream)
-                        : launch_fwd_t<192, 192, false, KV>(p, num_sms, stream);
-    return p.o_fp32 ? launch_fwd_t<64, 64, true, KV>(p, num_sms, stream)
-                    : launch_fwd_t<64, 64, false, KV>(p, num_sms, stream);
+        return p.o_fp32 ? launch_fwd_t<192, 192, true, KV, WIN>(p, num_sms, stream)
+                        : launch_fwd_t<192, 192, false, KV, WIN>(p, num_sms, stream);
+    return p.o_fp32 ? launch_fwd_t<64, 64, true, KV, WIN>(p, num_sms, stream)
+                    : launch_fwd_t<64, 64, false, KV, WIN>(p, num_sms, stream);
 }
 
-cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
-    return p.kv ? launch_fwd_kv<true>(p, num_sms, stream)
-                : launch_fwd_kv<false>(p, num_sms, stream);
+}  // namespace
+
+#ifdef FA_WINDOW
+cudaError_t launch_fwd_window(const FwdParams& p, int num_sms, cudaStream_t stream) {
+    return launch_fwd_kv<true, true>(p, num_sms, stream);
 }
+#else
+cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream) {
+    return p.kv ? launch_fwd_kv<true, false>(p, num_sms, stream)
+                : launch_fwd_kv<false, false>(p, num_sms, stream);
+}
+#endif
 
 }  // namespace fa

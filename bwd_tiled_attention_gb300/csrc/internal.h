@@ -25,6 +25,7 @@ struct FwdParams {
     const int* cu_seqlens_k;       // key/value sequences; null for dense
     int Nk, Tk;                    // key/value length bound and tokens
     int kv;                        // key boundaries differ from the query ones
+    int window, sinks;             // window > 0: p sees c <= p with p - c < window or c < sinks
 };
 
 struct BwdParams {
@@ -48,6 +49,9 @@ struct BwdParams {
     const int* cu_seqlens_k;       // key/value sequences; null for dense
     int Nk, Tk;                    // key/value length bound and tokens
     int kv;                        // key boundaries differ from the query ones
+    int window, sinks;             // window > 0: p sees c <= p with p - c < window or c < sinks
+    int far_chunk, sink_tiles;     // query tiles of a far unit, tiles that hold sinks (0: none)
+    size_t sink_off;               // fp32 partials of the sinks' dK and dV
 };
 
 // Writes the unit list over the tiles of `cu_seqlens` / N (T tokens) and,
@@ -55,23 +59,30 @@ struct BwdParams {
 // cu_tiles_seqlens / N_tiles (T_tiles tokens) define (the backward's units
 // are key/value tiles, its semaphores query tiles).  Every length is checked
 // against its bound and both boundary arrays against their token counts; on a
-// mismatch no unit is written and the error word is set.
+// mismatch no unit is written and the error word is set.  With sink_tiles > 0
+// the far units of a windowed backward come before the others.
 cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int rows, int order,
                          long long max_units, void* workspace, size_t units_off,
                          size_t tile_off_off, bool want_tile_off, const int* cu_tiles_seqlens,
-                         int N_tiles, int T_tiles, cudaStream_t stream);
+                         int N_tiles, int T_tiles, cudaStream_t stream, int far_chunk = 0,
+                         int sink_tiles = 0);
 
 // Dynamic shared memory the scheduler needs for a packed batch of B sequences
 // whose longest spans at most maxnt_bound tiles (one CTA ranks them all).
 size_t sched_smem_bytes(int B, int maxnt_bound);
 
 cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_fwd_window(const FwdParams& p, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const void* o, int o_fp32, const void* dout, float* D,
                                   float* dq_acc, int* sems, long long n_sems, int T, int Hq,
                                   int d, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_bwd(const BwdParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_bwd_window(const BwdParams& p, int num_sms, cudaStream_t stream);
+
+// dK and dV of the sinks from their partials, behind launch_bwd_postprocess.
+cudaError_t launch_fold_sinks(const BwdParams& p, int num_sms, cudaStream_t stream);
 
 // dk_acc/dv_acc: fp32 partials [Tk, Hkv * nruns, d] to sum per key/value head,
 // or null when each unit wrote final dK/dV.

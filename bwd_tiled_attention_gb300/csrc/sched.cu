@@ -37,7 +37,24 @@ struct SchedArgs {
     WsHeader* header;
     int2* units;
     int* tile_off;          // int[B+1] offsets of the other side's tiles (may be null)
+    int far_chunk, sink_tiles;  // far units of a windowed backward (sink_tiles = 0: none)
 };
+
+// Far unit u of a windowed backward whose sequences have `chunks` chunks of query tiles
+// together: in descending tile of sinks (a deterministic dQ tile takes them in that
+// order), then by chunk (counted over all sequences), heads innermost.
+struct FarEntry {
+    long long chunk;
+    int sink, head;
+};
+__device__ __forceinline__ FarEntry far_entry(const SchedArgs& a, long long chunks, long long u) {
+    FarEntry f;
+    const long long per = chunks * a.H, r = u % per;
+    f.sink = a.sink_tiles - 1 - (int)(u / per);
+    f.chunk = r / a.H;
+    f.head = (int)(r % a.H);
+    return f;
+}
 
 // Number of sequences whose tile count exceeds m, given counts sorted descending.
 __device__ __forceinline__ int count_above(const int* nt_sorted, int B, int m) {
@@ -72,7 +89,9 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         const int nt = cdiv(a.N, a.rows);
         const int nt_aux = cdiv(a.N_aux, a.rows);
         const long long per_level = (long long)B * H;
-        const long long total = per_level * nt;
+        const int chunks = a.sink_tiles ? cdiv(nt_aux, a.far_chunk) : 0;  // of one sequence
+        const long long far = (long long)B * chunks * a.sink_tiles * H;
+        const long long total = far + per_level * nt;
         if (tid == 0) {
             a.header->n_units = (int)(total <= a.max_units ? total : 0);
             a.header->counter = 0;
@@ -80,7 +99,12 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
             a.header->n_qtiles = B * nt_aux;
         }
         if (total > a.max_units) return;
-        for (long long u = tid; u < total; u += kSchedThreads) {
+        for (long long u = tid; u < far; u += kSchedThreads) {
+            const FarEntry f = far_entry(a, (long long)B * chunks, u);
+            const int b = (int)(f.chunk / chunks), q = (int)(f.chunk % chunks);
+            a.units[u] = make_int2(b | kFarUnit, make_unit_y(q * a.sink_tiles + f.sink, f.head));
+        }
+        for (long long u = tid; u < total - far; u += kSchedThreads) {
             int b, tile, h;
             if (a.order == kOrderSeqDesc) {
                 b = (int)(u / ((long long)nt * H));
@@ -94,7 +118,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
                 h = (int)(r % H);
                 tile = (a.order == kOrderLevelDesc) ? nt - 1 - lvl : lvl;
             }
-            a.units[u] = make_int2(b, make_unit_y(tile, h));
+            a.units[far + u] = make_int2(b, make_unit_y(tile, h));
         }
         if (a.tile_off)
             for (int b = tid; b <= B; b += kSchedThreads) a.tile_off[b] = b * nt_aux;
@@ -148,6 +172,28 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     }
     __syncthreads();
     const int maxnt = s_maxnt;
+    long long far = 0, all_chunks = 0;  // far units, chunks of all sequences
+    if (a.sink_tiles) {
+        if (tid == 0) {
+            long long acc = 0;
+            for (int b = 0; b < B; ++b) {
+                prefix[b] = acc;
+                acc += cdiv(cdiv(a.cu_aux[b + 1] - a.cu_aux[b], a.rows), a.far_chunk);
+            }
+            s_total = acc;
+        }
+        __syncthreads();
+        all_chunks = s_total;
+        far = all_chunks * a.sink_tiles * H;
+        if (far <= a.max_units)
+            for (long long u = tid; u < far; u += kSchedThreads) {
+                const FarEntry f = far_entry(a, all_chunks, u);
+                const int b = find_slot(prefix, B, f.chunk);
+                a.units[u] = make_int2(b | kFarUnit, make_unit_y((int)(f.chunk - prefix[b]) * a.sink_tiles +
+                                                                     f.sink, f.head));
+            }
+        __syncthreads();
+    }
     int nslots;
     if (a.order == kOrderSeqDesc) {
         nslots = B;
@@ -170,7 +216,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         }
     }
     __syncthreads();
-    const long long total = s_total;
+    const long long total = far + s_total;
     if (tid == 0) {
         a.header->n_units = (int)(total <= a.max_units ? total : 0);
         a.header->counter = 0;
@@ -188,7 +234,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         a.header->n_qtiles = 0;
     }
     if (total > a.max_units || nslots == 0) return;
-    for (long long u = tid; u < total; u += kSchedThreads) {
+    for (long long u = tid; u < total - far; u += kSchedThreads) {
         const int slot = find_slot(prefix, nslots, u);
         const long long r = u - prefix[slot];
         int b, tile;
@@ -202,7 +248,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
             const int m = maxnt - 1 - slot;   // sequences of this level have nt > m
             tile = (a.order == kOrderLevelDesc) ? m : nt_of[b] - 1 - m;
         }
-        a.units[u] = make_int2(b, make_unit_y(tile, h));
+        a.units[far + u] = make_int2(b, make_unit_y(tile, h));
     }
 }
 
@@ -214,8 +260,11 @@ size_t sched_smem_bytes(int B, int maxnt_bound) {
 cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int rows, int order,
                          long long max_units, void* workspace, size_t units_off,
                          size_t tile_off_off, bool want_tile_off, const int* cu_tiles_seqlens,
-                         int N_tiles, int T_tiles, cudaStream_t stream) {
+                         int N_tiles, int T_tiles, cudaStream_t stream, int far_chunk,
+                         int sink_tiles) {
     SchedArgs a;
+    a.far_chunk = far_chunk;
+    a.sink_tiles = sink_tiles;
     a.cu_seqlens = cu_seqlens;
     a.cu_aux = cu_tiles_seqlens;
     a.T = T;

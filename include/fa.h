@@ -226,6 +226,49 @@ fa_status fa_bwd_kv(const void* q, const void* k, const void* v, const void* dou
                     int deterministic, fa_stream_t stream);
 
 /*
+ * Causal attention within a sliding window, and its gradient: with queries and
+ * keys as in fa_fwd_kv, the query at position p (query i of a sequence stands at
+ * i + Lk - Lq) sees key j <= p when p - j < window, or when j < sinks -- the
+ * first keys of a sequence stay visible to all of it.  window >= 1, sinks >= 0;
+ * where window or sinks reaches Nk the call is the causal one.  Work and traffic
+ * go with the visible pairs, in tiles of 128.
+ *   Boundaries, errors, ownership and limits as in fa_fwd_kv and fa_bwd_kv (queries
+ *   and keys of one packed batch pass the same boundaries twice), and beyond those:
+ *   with sinks > 0 the chunks of ceil(sinks / 128) (at least 16) query tiles of the
+ *   longest sequence times ceil(sinks / 128) stay within 65535, and B < 2^30
+ *   (FA_ERR_UNSUPPORTED).
+ *   fa_fwd_window: workspace as fa_fwd_workspace_size(B, Hq, Nq, total_q).
+ *   fa_bwd_window_preprocess and fa_bwd_window take the same window and sinks, and a
+ *   workspace of fa_bwd_window_workspace_size bytes: that of fa_bwd_kv and, with
+ *   sinks, fp32 partials of their dK and dV and a longer list of units.  It is larger
+ *   the more sinks there are, by less than six times the bytes of fp32 dK and dV.
+ *   deterministic = 1 gives bit-identical dq, dk and dv from run to run.
+ *   Values of keys that a row does not see must be finite, as in the other calls:
+ *   they enter the tensor core with a weight of 0.
+ */
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fa_dtype o_dtype,
+                        float* lse, int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k,
+                        int d, float scale, int window, int sinks, const int* cu_seqlens_q,
+                        const int* cu_seqlens_k, void* workspace, size_t workspace_bytes,
+                        fa_stream_t stream);
+
+size_t fa_bwd_window_workspace_size(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int total_k,
+                                    int d, int window, int sinks);
+
+fa_status fa_bwd_window_preprocess(const void* o, fa_dtype o_dtype, const void* dout, float* D,
+                                   void* workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                                   int Nq, int total_q, int Nk, int total_k, int d, int window,
+                                   int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                   int deterministic, fa_stream_t stream);
+
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* dout,
+                        const float* lse, const float* D, void* dq, void* dk, void* dv,
+                        fa_dtype grad_dtype, void* workspace, size_t workspace_bytes, int B, int Hq,
+                        int Hkv, int Nq, int total_q, int Nk, int total_k, int d, float scale,
+                        int window, int sinks, const int* cu_seqlens_q, const int* cu_seqlens_k,
+                        int deterministic, fa_stream_t stream);
+
+/*
  * Backward pass for callers that cannot allocate device memory: same inputs,
  * outputs and results as fa_bwd_preprocess followed by fa_bwd, but D and the
  * backward workspace live in a 64 MiB scratch array owned by the library, so
