@@ -93,6 +93,8 @@ _SIGS = {
                              _vp, _ll, _ll, _i, _vp, _i, _vp, _i, _i, _vp]),
     "fa_tree_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_tree_mask": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp]),
+    "fa_tree_fwd_window": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp,
+                                _f, _i, _i, _i, _vp, _sz, _vp]),
     "fa_tree_fwd": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _f,
                          _i, _vp, _sz, _vp]),
 }

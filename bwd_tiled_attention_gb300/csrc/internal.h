@@ -125,7 +125,11 @@ struct TreeParams {
     int zero_rest;                 // write zeros for tokens that no sequence owns
     int clear_odd;                 // one more slice of the join kernel does so between odd boundaries
     float scale_log2;
+    int window, sinks;             // window > 0: p sees key j when p - j < window or j < sinks
 };
+
+// The attention over the cache with a window (tree_window.cu).
+cudaError_t launch_tree_window(const TreeParams& p, bool pair, int ctas, cudaStream_t stream);
 
 // The tensor maps of p (api.cu); bn: keys of a tile.
 bool make_tree_maps(TreeParams& p, const fa_cache& c, const void* q, int T, int Hq,

@@ -49,6 +49,14 @@
 // over 501 keys 11.8 us: ~2.6 us of lookups and arithmetic, ~2 us until the first
 // tile is there, its chain, the join.
 //
+// With a window of W keys and S first ones (sinks; tree_window.cu compiles these kernels),
+// a row at position p sees of the keys j before `limit` those with p - j < W or j < S.
+// An item's tiles are then those of the sinks and a stretch that begins where its first
+// row's window does; everything else -- the line, the split, the join -- counts tiles as
+// before, and a tile of the count is turned into one of the sequence where keys are
+// named.  A drafted token stands as many places behind the context as its row names
+// others of the call's own tokens, and the window hides keys of the context alone.
+//
 // Pages hold whatever was there before: keys past the length never reach a
 // sum (their scores are replaced, their V rows zeroed in shared memory), and
 // a drafted token's V that is not finite is kept from the rows that do not
@@ -70,6 +78,12 @@
 
 namespace fa {
 namespace {
+
+#ifdef FA_WINDOW
+constexpr bool kWin = true;
+#else
+constexpr bool kWin = false;
+#endif
 
 constexpr int kThreads = 384;
 constexpr float kRescale = 8.0f;  // log2 units: P <= 256 before the reference moves
@@ -112,9 +126,79 @@ struct Piece {
     int trow0;           // the first token's index in the sequence
     int slot, ctx, len;
     int k0, n;           // key tiles [k0, k0 + n)
+#ifdef FA_WINDOW
+    int nsk, lo;         // of the item's tiles the first nsk hold sinks, the others begin at lo
+#endif
     int part;            // partial slot, or -1: the whole item
     int first_cta, last_cta;  // the CTAs that share the item
+    // First key of the piece's tile j.
+    __device__ __forceinline__ int tile_key(int j, int bn) const {
+#ifdef FA_WINDOW
+        return (k0 + j < nsk ? k0 + j : lo + (k0 + j - nsk)) * bn;
+#else
+        return (k0 + j) * bn;
+#endif
+    }
 };
+
+// What the window leaves of a piece (everything, without one).  A row sees key j when
+// j >= from or j < sinks, apart from what `limit` and the mask say.
+struct Sight {
+    int open;            // every row of the piece sees all keys before that ...
+    int open_lo;         // ... from here on, and the sinks
+    int all_lo;          // no row sees keys before that but the sinks
+    int sinks;
+    __device__ __forceinline__ Sight(const TreeParams& p, const Piece& x) {
+        open = p.mask ? x.ctx : min(x.len, x.ctx + x.trow0 + 1);
+        open_lo = all_lo = sinks = 0;
+        if constexpr (kWin) {
+            sinks = p.sinks;
+            if (p.mask) {
+                open_lo = min(x.ctx, x.len - p.window);
+                all_lo = x.ctx - p.window + 1;
+            } else {
+                open_lo = x.ctx + x.trow0 + x.ntok - p.window;
+                all_lo = x.ctx + x.trow0 - p.window + 1;
+            }
+        }
+    }
+    // Is some key of [key, key + n) hidden from some row?
+    __device__ __forceinline__ bool ragged(int key, int n) const {
+        return key + n > open || (kWin && key < open_lo && key + n > sinks);
+    }
+    __device__ __forceinline__ bool hidden_from_some(int key) const {
+        return key >= open || (kWin && key < open_lo && key >= sinks);
+    }
+    __device__ __forceinline__ bool hidden_from_all(int key, int len) const {
+        return key >= len || (kWin && key < all_lo && key >= sinks);
+    }
+};
+
+// First key of the window of token `trow` of its sequence (0: no window); words: its row
+// of the mask, or null.
+__device__ __forceinline__ int window_from(const TreeParams& p, const Piece& x, const uint32_t* words,
+                                           int trow) {
+    if constexpr (!kWin) return 0;
+    if (!p.mask) return x.ctx + trow - p.window + 1;
+    int others = 0;
+    const int n = x.len - x.ctx;
+#pragma unroll 1
+    for (int w = 0; w * 32 < n && w < 2 * p.words; ++w) {
+        uint32_t bits = words[w];
+        if (n - w * 32 < 32) bits &= (1u << (n - w * 32)) - 1u;
+        if (trow >> 5 == w) bits &= ~(1u << (trow & 31));
+        others += __popc(bits);
+    }
+    return min(x.ctx, x.ctx + others - p.window + 1);
+}
+
+// Bits of the keys of [kb, kb + 32) that a window from `from` with its sinks leaves.
+__device__ __forceinline__ uint32_t window_bits(int kb, int from, int sinks) {
+    const int low = from - kb, few = sinks - kb;
+    uint32_t hidden = low <= 0 ? 0u : (low >= 32 ? 0xffffffffu : (1u << low) - 1u);
+    if (few > 0) hidden &= few >= 32 ? 0u : ~((1u << few) - 1u);
+    return ~hidden;
+}
 
 template <int D, bool PAIR, bool FEW>
 struct Smem {
@@ -205,13 +289,28 @@ __device__ __forceinline__ SeqInfo seq_info(const TreeParams& p, int i) {
     return s;
 }
 
+// With a window: the first tile behind the sinks' that row tile q visits, and the sinks'.
+__device__ __forceinline__ int window_tiles(const TreeParams& p, const SeqInfo& s, int q, int tokens,
+                                            int bn, int& sink_tiles) {
+    const int pos = p.mask ? s.ctx : s.ctx + q * tokens;  // of its first row (at least)
+    const int lo = s.len > 0 ? max(0, pos - p.window + 1) / bn : 0;
+    sink_tiles = min((p.sinks + bn - 1) / bn, lo);
+    return lo;
+}
+
 // Key tiles that row tile q of a sequence visits (one even when it sees no
 // key, so that its rows are written).
 __device__ __forceinline__ int item_tiles(const TreeParams& p, const SeqInfo& s, int q, int tokens,
                                           int bn) {
     int keys = s.len;
     if (!p.mask && s.len > 0) keys = min(s.len, s.ctx + min(s.n, (q + 1) * tokens));
-    return max(1, (keys + bn - 1) / bn);
+    int tiles = (keys + bn - 1) / bn;
+    if constexpr (kWin) {
+        int few;
+        tiles -= window_tiles(p, s, q, tokens, bn, few);
+        tiles += few;
+    }
+    return max(1, tiles);
 }
 
 __device__ __forceinline__ long long head_tiles(const TreeParams& p, const SeqInfo& s, int tokens,
@@ -310,6 +409,9 @@ struct Loader {
     // of the piece: page ids of a window of 32 pages, and of the next one
     const int* table;
     int used, win, ids, nxt, key0, len, head;
+#ifdef FA_WINDOW
+    int left, jump_key, jump_ids, jump_nxt;  // tiles before the window's stretch, and where it begins
+#endif
     int place = -1;  // ring place of this lane's turn among the last 32 loads
     int count = 0;
 
@@ -332,10 +434,18 @@ struct Loader {
         len = x.len;
         head = x.h;
         used = (len + ps - 1) >> shift;
-        key0 = x.k0 * BN;
+        key0 = x.tile_key(0, BN);
         win = key0 >> shift;
         ids = table_at(win + lane_id());
         nxt = table_at(win + 32 + lane_id());
+#ifdef FA_WINDOW
+        left = x.nsk - x.k0;
+        jump_key = x.lo * BN;
+        if (left > 0) {
+            jump_ids = table_at((jump_key >> shift) + lane_id());
+            jump_nxt = table_at((jump_key >> shift) + 32 + lane_id());
+        }
+#endif
     }
     // The piece's next tile into place f of the ring.
     __device__ __forceinline__ bool tile(int f, int* status) {
@@ -365,6 +475,14 @@ struct Loader {
         if ((count & 31) == (int)lane_id()) place = f;
         ++count;
         key0 += BN;
+#ifdef FA_WINDOW
+        if (--left == 0) {
+            key0 = jump_key;
+            win = key0 >> shift;
+            ids = jump_ids;
+            nxt = jump_nxt;
+        }
+#endif
         return true;
     }
     // After an abort: waits (bounded) for the loads that may still fly.
@@ -483,8 +601,8 @@ __device__ __forceinline__ void join_row(const TreeParams& p, int slot_row, int 
 // rows, eight of them by each warp: stored, or left as the piece's partial.
 template <int DR, int BN>
 __device__ __forceinline__ void store_few(const TreeParams& p, const Piece& x, const float (*o)[36],
-                                          const float (*stats)[2][128], bool two, int poison, int open,
-                                          int q4, int cc) {
+                                          const float (*stats)[2][128], bool two, int poison,
+                                          const Sight& sight, int q4, int cc) {
     const int lane = lane_id(), row = q4 * 8 + (lane >> 2), col = (lane & 3) * 8;
     const int row_tok = row / p.group, head = x.h * p.group + row - row_tok * p.group;
     if (row_tok >= x.ntok) return;
@@ -513,8 +631,14 @@ __device__ __forceinline__ void store_few(const TreeParams& p, const Piece& x, c
         const uint32_t* words = p.mask
             ? reinterpret_cast<const uint32_t*>(p.mask) + tok * (2 * (size_t)p.words) : nullptr;
         const int limit = p.mask ? x.len : min(x.len, x.ctx + x.trow0 + row_tok + 1);
-        const int end = min(limit, (x.k0 + x.n) * BN), ps = p.cache.page_size;
-        for (int key = odd ? x.k0 * BN : max(open, x.k0 * BN); key < end && sum == sum; ++key) {
+        const int ps = p.cache.page_size;
+        const int from = window_from(p, x, words, x.trow0 + row_tok);
+        const int skip = kWin || odd ? 0 : max(0, sight.open - x.tile_key(0, BN));  // (tiles in a row)
+        for (int i = skip; i < x.n * BN && sum == sum; ++i) {
+            const int key = x.tile_key(i / BN, BN) + i % BN;
+            if (key >= limit) break;
+            if (kWin && ((!odd && !sight.hidden_from_some(key)) || (key < from && key >= sight.sinks)))
+                continue;
             if (p.mask && !(mask_bits(words, 2 * p.words, key - x.ctx) & 1u)) continue;
             const int page = p.cache.table[(long long)x.slot * p.cache.max_pages + key / ps];
             if (page < 0 || page >= p.cache.pages) continue;
@@ -730,6 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             x.ctx = s.ctx;
             x.len = s.len;
             x.k0 = k0;
+#ifdef FA_WINDOW
+            x.lo = window_tiles(p, s, q, tokens, BN, x.nsk);
+#endif
             x.n = (int)min((long long)(tiles - k0), end - at);
             const bool whole_end = k0 + x.n == tiles;
             x.part = k0 == 0 ? (whole_end ? -1 : 2 * (int)blockIdx.x + 1) : 2 * (int)blockIdx.x;
@@ -984,11 +1111,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const size_t tok = (size_t)x.tok0 + tok_first + row_tok;
             // no key from `limit` on is visible; without a mask all before it are
             const int limit = p.mask ? x.len : min(x.len, x.ctx + trow + 1);
-            // every row of the piece sees all keys before `open`
-            const int open = p.mask ? x.ctx : min(x.len, x.ctx + x.trow0 + 1);
+            const Sight sight(p, x);
             const uint32_t* words = p.mask
                 ? reinterpret_cast<const uint32_t*>(p.mask) + (valid ? tok : 0) * (2 * (size_t)p.words)
                 : nullptr;
+            const int from = window_from(p, x, words, trow);
             const bool active = PAIR ? ntok > 0 : (C::kStreams == 2 || w == 0);
             const int step = PAIR || C::kStreams == 1 ? 1 : 2;
             float m_ref = -INFINITY, l = 0.f;
@@ -997,12 +1124,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                 for (int j = PAIR || C::kStreams == 1 ? 0 : w; j < x.n; j += step) {
                     const int buf = PAIR ? w : j & 1;
                     const int c = PAIR ? cnt[w] + j : cnt[buf] + (j >> 1);
-                    const int key0 = (x.k0 + j) * BN;
+                    const int key0 = x.tile_key(j, BN);
                     if (!(ok = warp_wait(smem_u32(&sm.s_full[buf]), c & 1, stop, status))) break;
                     tc_fence_after();
                     const uint32_t s_at = tmem + lane_off + buf * 128;
                     const uint32_t p_at = tmem + lane_off + C::kPCol + buf * C::kPStep;
-                    const bool ragged = key0 + BN > open;
+                    const bool ragged = sight.ragged(key0, BN);
                     // V rows past the length are whatever the page held, and a drafted V
                     // may be anything: both are mended before P is handed over (before the
                     // scores take up the registers; only once S(j) is there, so that the stage's
@@ -1011,9 +1138,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         const int fv = f + fifo_v<PAIR>(j, x.n);
                         if (!(ok = warp_wait(smem_u32(&sm.full[fv % S]), (fv / S) & 1, stop, status)))
                             break;
-                        if (at < BN && key0 + at >= open) {
+                        if (at < BN && sight.hidden_from_some(key0 + at)) {
                             uint8_t* rest = sm.kv[fv % S] + at * 128;
-                            const bool past = key0 + at >= x.len;
+                            const bool past = sight.hidden_from_all(key0 + at, x.len);
 #pragma unroll 1
                             for (int cb = 0; cb < C::kCols; ++cb, rest += BN * 128) {
                                 // (chunks in an order of the row's own, which spreads the banks)
@@ -1059,6 +1186,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                         const int room = limit - kb;
                         if (room <= 0) bits = 0;
                         else if (room < 32) bits &= (1u << room) - 1u;
+                        if constexpr (kWin) bits &= window_bits(kb, from, sight.sinks);
                         return bits;
                     };
                     float s[FEW ? 32 : C::kWhole ? BN : 1];
@@ -1345,16 +1473,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
                             __syncwarp();
                             if (lane == 0) mbar_arrive(smem_u32(&sm.x_full[w]));
                             if (!(ok = warp_wait(smem_u32(&sm.x_full[w]), it & 1, stop, status))) break;
-                            store_few<DR, BN>(p, x, sm.x[w], sm.stats[it & 1], two, poison, open, q4, cc);
+                            store_few<DR, BN>(p, x, sm.x[w], sm.stats[it & 1], two, poison, sight, q4, cc);
                             continue;
                         }
                         if (poison && valid) {
                             // a visible drafted V that is not finite: its weight is
                             // positive, so it adds itself
                             const int ps = p.cache.page_size;
-                            const int ka = max(open, x.k0 * BN);
-                            const int kz = min(limit, (x.k0 + x.n) * BN);
-                            for (int key = ka; key < kz; ++key) {
+                            const int skip = kWin ? 0 : max(0, sight.open - x.tile_key(0, BN));
+                            for (int i = skip; i < x.n * BN; ++i) {
+                                const int key = x.tile_key(i / BN, BN) + i % BN;
+                                if (key >= limit) break;
+                                if (kWin && (!sight.hidden_from_some(key) ||
+                                             (key < from && key >= sight.sinks)))
+                                    continue;
                                 if (p.mask && !(mask_bits(words, 2 * p.words, key - x.ctx) & 1u))
                                     continue;
                                 const int page = p.cache.table[(long long)x.slot * p.cache.max_pages +
@@ -1542,6 +1674,44 @@ __global__ void __launch_bounds__(256, 4) tree_join_kernel(const __grid_constant
     if (c8 == 0) p.lse[(size_t)head * p.T + tok] = (m + __log2f(l)) * 0.69314718055994531f;
 }
 
+template <int D, int DR, bool PAIR, bool FEW = false>
+cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
+    auto kern = tree_kernel<D, DR, PAIR, FEW>;
+    constexpr size_t smem = smem_bytes<D, PAIR, FEW>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
+    if (e != cudaSuccess || p.fused) return e;
+    const int slices = cdiv(p.part_rows * (DR / 8), 256) + p.clear_odd;
+    return launch_pdl(tree_join_kernel<DR>, dim3(ctas, slices), dim3(256), 0, stream, p);
+}
+
+cudaError_t launch_d(const TreeParams& p, bool pair, int ctas, cudaStream_t strm) {
+    const int d = p.cache.d;
+    if (d == 128)
+        return pair ? launch_t<128, 128, true>(p, ctas, strm) : launch_t<128, 128, false>(p, ctas, strm);
+    if (d == 96)
+        return pair ? launch_t<128, 96, true>(p, ctas, strm) : launch_t<128, 96, false>(p, ctas, strm);
+    if (d == 64)
+        return pair      ? launch_t<64, 64, true>(p, ctas, strm)
+               : p.fused ? launch_t<64, 64, false, true>(p, ctas, strm)
+                         : launch_t<64, 64, false>(p, ctas, strm);
+    if (d == 192) return launch_t<192, 192, false>(p, ctas, strm);
+    return launch_t<256, 256, false>(p, ctas, strm);
+}
+
+#ifdef FA_WINDOW
+
+}  // namespace
+
+cudaError_t launch_tree_window(const TreeParams& p, bool pair, int ctas, cudaStream_t stream) {
+    return launch_d(p, pair, ctas, stream);
+}
+
+}  // namespace fa
+
+#else
+
 // Ancestor bits of drafted trees: token t of a sequence sees itself, its
 // parent, its parent's parent, ... up to a token whose parent is -1 (or is not
 // an earlier token of the sequence).  A thread a row.
@@ -1562,18 +1732,6 @@ __global__ void tree_mask_kernel(const int* parents, const int* cu, int B, int N
         if (up >= j) break;
         j = up;
     }
-}
-
-template <int D, int DR, bool PAIR, bool FEW = false>
-cudaError_t launch_t(const TreeParams& p, int ctas, cudaStream_t stream) {
-    auto kern = tree_kernel<D, DR, PAIR, FEW>;
-    constexpr size_t smem = smem_bytes<D, PAIR, FEW>();
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
-    if (e != cudaSuccess || p.fused) return e;
-    const int slices = cdiv(p.part_rows * (DR / 8), 256) + p.clear_odd;
-    return launch_pdl(tree_join_kernel<DR>, dim3(ctas, slices), dim3(256), 0, stream, p);
 }
 
 // Row tiles: as many whole tokens (of group rows each) as 128 rows hold; more
@@ -1618,37 +1776,12 @@ unsigned long long next_call() {
 
 bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-}  // namespace
-}  // namespace fa
-
-using namespace fa;
-
-extern "C" {
-
-size_t fa_tree_workspace_size(int Hq, int Hkv, int N, int d) {
-    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || N <= 0 || d <= 0) return 0;
-    return tree_ws(row_tiles(Hq / Hkv, N, d).rows, d).bytes;
-}
-
-fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, int T, int words,
-                       void* mask, fa_stream_t stream) {
-    if (B < 0 || N < 0 || T < 0 || words <= 0 || (long long)words * 64 < N) return FA_ERR_INVALID_ARG;
-    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
-    if (B > kMostSequences) return FA_ERR_UNSUPPORTED;
-    if (T == 0) return FA_OK;
-    if (!parents || !mask || !aligned(parents, 4) || !aligned(cu_seqlens, 4) || !aligned(mask, 8))
-        return FA_ERR_INVALID_ARG;
-    const cudaError_t e = launch_pdl(tree_mask_kernel, dim3(cdiv(T, 128)), dim3(128), 0,
-                                     reinterpret_cast<cudaStream_t>(stream), parents, cu_seqlens, B,
-                                     N, T, words, static_cast<unsigned long long*>(mask));
-    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
-}
-
-fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B, int N,
-                      const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
-                      long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
-                      float scale, int zero_rest, void* workspace, size_t workspace_bytes,
-                      fa_stream_t stream) {
+// window = 0: none.
+fa_status tree_impl(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                    const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
+                    long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
+                    float scale, int window, int sinks, int zero_rest, void* workspace,
+                    size_t workspace_bytes, fa_stream_t stream) {
     const fa_status cs = check_cache(cache);
     if (cs != FA_OK) return cs;
     const int d = cache->d, Hkv = cache->heads;
@@ -1703,25 +1836,70 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
     p.call = next_call();
     p.zero_rest = zero_rest ? 1 : 0;
     p.clear_odd = !p.fused && p.zero_rest && p.cu;
+    // a window or sinks as long as any sequence hide nothing
+    const long long room = (long long)cache->max_pages * cache->page_size;
+    if (window > 0 && window < room && sinks < room) {
+        p.window = window;
+        p.sinks = sinks;
+    }
     p.scale_log2 = scale * 1.4426950408889634f;
     const int nsm = device_sms();
     if (nsm <= 0) return FA_ERR_CUDA;
     const int ctas = nsm < kTreeMaxCtas ? nsm : kTreeMaxCtas;
     cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (d == 128)
-        e = tiles.pair ? launch_t<128, 128, true>(p, ctas, strm) : launch_t<128, 128, false>(p, ctas, strm);
-    else if (d == 96)
-        e = tiles.pair ? launch_t<128, 96, true>(p, ctas, strm) : launch_t<128, 96, false>(p, ctas, strm);
-    else if (d == 64)
-        e = tiles.pair ? launch_t<64, 64, true>(p, ctas, strm)
-            : p.fused  ? launch_t<64, 64, false, true>(p, ctas, strm)
-                       : launch_t<64, 64, false>(p, ctas, strm);
-    else if (d == 192)
-        e = launch_t<192, 192, false>(p, ctas, strm);
-    else
-        e = launch_t<256, 256, false>(p, ctas, strm);
+    const cudaError_t e = p.window ? launch_tree_window(p, tiles.pair, ctas, strm)
+                                   : launch_d(p, tiles.pair, ctas, strm);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_tree_workspace_size(int Hq, int Hkv, int N, int d) {
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || Hq / Hkv > 128 || N <= 0 || d <= 0) return 0;
+    return tree_ws(row_tiles(Hq / Hkv, N, d).rows, d).bytes;
+}
+
+fa_status fa_tree_mask(const int* parents, const int* cu_seqlens, int B, int N, int T, int words,
+                       void* mask, fa_stream_t stream) {
+    if (B < 0 || N < 0 || T < 0 || words <= 0 || (long long)words * 64 < N) return FA_ERR_INVALID_ARG;
+    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (B > kMostSequences) return FA_ERR_UNSUPPORTED;
+    if (T == 0) return FA_OK;
+    if (!parents || !mask || !aligned(parents, 4) || !aligned(cu_seqlens, 4) || !aligned(mask, 8))
+        return FA_ERR_INVALID_ARG;
+    const cudaError_t e = launch_pdl(tree_mask_kernel, dim3(cdiv(T, 128)), dim3(128), 0,
+                                     reinterpret_cast<cudaStream_t>(stream), parents, cu_seqlens, B,
+                                     N, T, words, static_cast<unsigned long long*>(mask));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                      const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
+                      long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
+                      float scale, int zero_rest, void* workspace, size_t workspace_bytes,
+                      fa_stream_t stream) {
+    return tree_impl(cache, layer, slots, B, N, cu_seqlens, T, q, Hq, q_token_stride, q_head_stride,
+                     mask, mask_words, o, lse, scale, 0, 0, zero_rest, workspace, workspace_bytes,
+                     stream);
+}
+
+fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                             const int* cu_seqlens, int T, const void* q, int Hq,
+                             long long q_token_stride, long long q_head_stride, const void* mask,
+                             int mask_words, void* o, float* lse, float scale, int window, int sinks,
+                             int zero_rest, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream) {
+    if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+    return tree_impl(cache, layer, slots, B, N, cu_seqlens, T, q, Hq, q_token_stride, q_head_stride,
+                     mask, mask_words, o, lse, scale, window, sinks, zero_rest, workspace,
+                     workspace_bytes, stream);
+}
+
 }  // extern "C"
+
+#endif  // FA_WINDOW

@@ -582,7 +582,7 @@ def _workspace_bytes(Hq, Hkv, N, d):
 
 
 def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=None, max_seqlen=None,
-                   out=None, workspace=None, stream=None):
+                   out=None, workspace=None, stream=None, window=None, sinks=0):
     """Attention of new tokens over one layer of the cache; returns (o, lse).
 
     The tokens of q ``[T, Hq, d]`` are the last ones of ``slots`` (`cache_append` comes first).
@@ -597,6 +597,11 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     ``out``, a pair (o, lse) to write to; a sequence whose boundaries decrease or are not
     within [0, T] owns none, and `PagedCache.check` raises.  ``workspace``: uint8, at least
     ``fa_tree_workspace_size`` bytes.
+
+    With ``window`` a row at position p sees only keys at places j with p - j < window, and
+    the first ``sinks`` ones.  A token's position is its place in the sequence; with a mask
+    it is the context's length plus the number of other own tokens that its row names, and
+    the window hides only what was cached before.
     """
     n = _of_cache(cache, layer, slots)
     dev = cache.device
@@ -604,7 +609,7 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
         with _on(dev, stream, cache._tensors + (q, slots, mask, cu_seqlens, workspace) +
                  (tuple(out) if out is not None else ())):
             return tree_attention(q, cache, layer, slots, mask, scale, cu_seqlens, max_seqlen, out,
-                                  workspace)
+                                  workspace, None, window, sinks)
     _heads_tensor("q", q, _BF16, dev)
     T, Hq, d = q.shape
     if Hq > _MOST:
@@ -622,6 +627,13 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
             raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
         if words > _MOST:
             _too_far("mask", mask)
+    if window is not None:
+        window = _whole("window", window)
+        sinks = _whole("sinks", sinks)
+        if not (1 <= window <= _MOST and 0 <= sinks <= _MOST):
+            raise ValueError(f"window must be from 1 to {_MOST}, sinks from 0, got {window} and {sinks}")
+    elif sinks:
+        raise ValueError("sinks need a window (without one every earlier key is visible)")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if out is not None:
         _want("out[0]", out[0], (torch.bfloat16,), 3, dev)
@@ -647,6 +659,12 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
         size = max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     qt, qh, _ = q.stride()
+    if window is not None:
+        _check(lib().fa_tree_fwd_window(
+            cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
+            _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, window, sinks,
+            1 if out is None else 0, ws.data_ptr(), size, _raw_stream(dev)), "fa_tree_fwd_window")
+        return o, lse
     _check(lib().fa_tree_fwd(
         cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
         _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, 1 if out is None else 0,

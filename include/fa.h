@@ -516,6 +516,23 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
                       float scale, int zero_rest, void* workspace, size_t workspace_bytes,
                       fa_stream_t stream);
 
+/*
+ * fa_tree_fwd within a sliding window: the row at position p sees, of the keys that
+ * it sees there, those at places j with p - j < window, and those with j < sinks.
+ * window >= 1, sinks >= 0.  Without a mask a token's position is its place in the
+ * sequence.  With one it is the context's length plus the number of other tokens of
+ * the call that its row names (its depth in a drafted tree), and the window hides
+ * keys of the context alone: of the call's own tokens a row sees those that it
+ * names.  Key tiles that no row of an item sees are not read; keys and values that a
+ * row does not see never matter to it, whatever they hold.
+ */
+fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                             const int* cu_seqlens, int T, const void* q, int Hq,
+                             long long q_token_stride, long long q_head_stride, const void* mask,
+                             int mask_words, void* o, float* lse, float scale, int window, int sinks,
+                             int zero_rest, void* workspace, size_t workspace_bytes,
+                             fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
