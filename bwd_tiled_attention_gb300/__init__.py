@@ -35,6 +35,7 @@ __all__ = [
     "fa_status_string", "forward", "backward", "attention", "FA_OK", "FA_ERR_INVALID_ARG",
     "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT", "FA_BF16", "FA_FP32",
     "PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask",
+    "cache_weights",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -91,6 +92,9 @@ _SIGS = {
     "fa_cache_check": (_i, [_vp, _vp, _vp]),
     "fa_cache_append": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _ll, _ll, _vp, _ll, _ll,
                              _vp, _ll, _ll, _i, _vp, _i, _vp, _i, _i, _vp]),
+    "fa_cache_weights": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _vp, _i, _vp, _f,
+                              _vp]),
+    "fa_cache_evict": (_i, [_vp, _vp, _vp, _i, _i, _i, _vp, _i, _vp]),
     "fa_tree_workspace_size": (_sz, [_i, _i, _i, _i]),
     "fa_tree_mask": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp]),
     "fa_tree_fwd_window": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp,
@@ -528,5 +532,5 @@ def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=Non
 
 
 from . import serving  # noqa: E402  (uses the binding above)
-from .serving import (PagedCache, cache_append, rotary, rotary_table, tree_attention,  # noqa: E402
-                      tree_mask)
+from .serving import (PagedCache, cache_append, cache_weights, rotary, rotary_table,  # noqa: E402
+                      tree_attention, tree_mask)

@@ -1,0 +1,607 @@
+// weights.cu -- the attention weight that each cached key receives from a call's
+// queries, added up: for every slot, key/value head and key j
+//   w_j += sum over the rows t and heads a of the group that see j of 2^(s_tj c - l_ta),
+// with s = q.k, c = scale log2 e and l = LSE log2 e, which the attention over the cache
+// has left.  It is what an eviction goes by.
+//
+// Bound: reading the keys once (decoding), or one exponential a pair of query row and key
+// (the last tokens of a prompt: 128 x 128 of them take 1024 cycles of an SM's SFU, the
+// scores of d = 128 about 130 of its tensor core).
+//
+// The scores are computed transposed, S^T = K Q^T: a key is a lane of TMEM and a thread,
+// which walks the query columns and adds up in registers.  Nothing is exchanged between
+// threads, a key's sum is complete in one place, and no maximum is needed.  The line of
+// all sequences' and heads' key tiles is split into equal stretches of it, one a CTA, as
+// by the attention; nothing has to be joined.
+//   warp 0       K tiles through a ring of stages, a TMA box a page (or 128 keys of one)
+//   warp 3       Q tiles and the LSE of their rows: once an item where one tile holds all
+//                rows, otherwise again for every pair of key tiles (from L2)
+//   warp 1       MMA issuer: for every Q tile the scores of both key tiles of a pair
+//   warps 4..7, 8..11  the pair's first and second key tile: exponentials and sums
+// Each of the two has two buffers of scores in TMEM, so that the tensor core works on the
+// next Q tile (or pair) meanwhile.
+//
+// A key's sum goes to memory as one addition of the whole call, so that results do not
+// vary from run to run; a slot that a call names twice gets both sums, in either order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "../../include/fa.h"
+#include "cache.cuh"
+#include "common.cuh"
+#include "internal.h"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kBN = 128;  // keys of a tile
+
+struct Params {
+    CUtensorMap tm_q, tm_k;
+    fa_cache cache;
+    const int* slots;
+    const int* cu;
+    const void* mask;
+    const float* lse;
+    float* weights;
+    int layer, B, N, T, Hq, group, words, tile_tokens, page_shift;
+    float scale_log2;
+};
+
+// D: tile columns (96 runs on 128).  NQ: query rows of a tile; 64 above d = 128, where
+// two tiles of 128 beside a pair of key tiles do not fit, unless a group is larger.
+template <int D, int NQ>
+struct Cfg {
+    static constexpr int kCols = D / 64;
+    static constexpr int kQBytes = NQ * D * 2, kStageBytes = kBN * D * 2;
+    static constexpr int kQBufs = NQ * D <= 128 * 192 ? 2 : 1;
+    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBufs * kQBytes;
+    static constexpr int kMost = kRoom / kStageBytes;
+    static constexpr int kStages = kMost > 8 ? 8 : kMost;
+    static_assert(kStages >= 2, "the ring holds a pair of key tiles");
+};
+
+// A stretch of one (sequence, head)'s key tiles.
+struct Piece {
+    int h;               // < 0: none left
+    int tok0, n;         // tokens in the packed batch
+    int slot, ctx, len;
+    int k0, tiles;       // key tiles [k0, k0 + tiles)
+};
+
+template <int D, int NQ>
+struct Smem {
+    using C = Cfg<D, NQ>;
+    alignas(1024) uint8_t q[C::kQBufs][C::kQBytes];
+    alignas(1024) uint8_t k[C::kStages][C::kStageBytes];
+    alignas(16) float nl[C::kQBufs][NQ];  // -LSE log2 e of the Q tile's rows
+    alignas(8) uint64_t full[C::kStages], empty[C::kStages];
+    uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
+    uint64_t piece_full[2], piece_empty[2];
+    uint64_t s_full[2][2], s_free[2][2];  // [key tile of the pair][buffer]
+    uint64_t drain;
+    Piece piece[2];
+    long long sums[kThreads / 32];
+    int start[3];        // this CTA's first item: sequence, head, key tile
+    uint32_t tmem_base;
+    int abort_flag, zero;
+};
+
+__device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int* flag, int* status) {
+    if (mbar_wait(bar, parity, flag)) return true;
+    *flag = 1;
+    atomicOr(status, kCacheTimeout);
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
+                                          int* status) {
+    return __all_sync(0xffffffffu, poll(bar, parity, flag, status));
+}
+
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, uint32_t bar, int c0,
+                                            int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+struct SeqInfo {
+    int t0, n, slot, len, bad;
+};
+
+// Sequence i; one that does not fit, or has no tokens, has len = 0: no keys, no tiles.
+__device__ __forceinline__ SeqInfo seq_info(const Params& p, int i) {
+    SeqInfo s;
+    const int slot = p.slots[i];  // (in one trip with the boundaries)
+    const SeqRange r = seq_range(p.cu, p.N, p.T, i);
+    s.t0 = r.t0;
+    s.n = r.n;
+    s.slot = s.len = s.bad = 0;
+    if (r.n < 0) s.bad = kCacheBadLength;
+    if (r.n <= 0) return s;
+    if (slot < 0 || slot >= p.cache.slots) {
+        s.bad = kCacheBadSlot;
+        return s;
+    }
+    const int len = p.cache.lengths[slot];
+    if (len < s.n || s.n > p.N || len > (long long)p.cache.max_pages * p.cache.page_size) {
+        s.bad = kCacheBadLength;
+        return s;
+    }
+    s.slot = slot;
+    s.len = len;
+    return s;
+}
+
+// The sum over columns [0, ncols) of 2^(s c + nl), s from TMEM.  MASK: column
+// `col` counts only where see(col).
+template <bool MASK, typename See>
+__device__ __forceinline__ float weigh(uint32_t s_at, const float* nl, float c, int ncols, See&& see) {
+    float sum = 0.f;
+    const uint64_t cc = f2_pack(c, c);
+#pragma unroll 1
+    for (int c0 = 0; c0 < ncols; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(s_at + c0, r);
+        tmem_ld_wait();
+        if (!MASK && c0 + 32 <= ncols) {
+            uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const ulonglong2 l = reinterpret_cast<const ulonglong2*>(nl + c0)[e];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[4 * e + 2 * h]),
+                                                      __uint_as_float(r[4 * e + 2 * h + 1])),
+                                              cc, h ? l.y : l.x);
+                    float x0, x1;
+                    f2_unpack(x, x0, x1);
+                    acc[h] = f2_add(acc[h], f2_pack(ex2_approx(x0), ex2_approx(x1)));
+                }
+            }
+            float a, b;
+            f2_unpack(f2_add(acc[0], acc[1]), a, b);
+            sum += a + b;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int col = c0 + i;
+                const float e = ex2_approx(fmaf(__uint_as_float(r[i]), c, nl[min(col, ncols - 1)]));
+                if (col < ncols && (!MASK || see(col))) sum += e;
+            }
+        }
+    }
+    return sum;
+}
+
+template <int D, int DR, int NQ>
+__global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ Params p) {
+    pdl_trigger();
+    using C = Cfg<D, NQ>;
+    using SM = Smem<D, NQ>;
+    constexpr int S = C::kStages, QB = C::kQBufs;
+    static_assert(sizeof(SM) + 1024 <= 232448, "shared memory exceeds 227 KB");
+    extern __shared__ uint8_t smem_raw[];
+    SM& sm = *reinterpret_cast<SM*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = warp_id(), lane = lane_id();
+    volatile int* stop = &sm.abort_flag;
+    int* status = p.cache.scratch;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), 1);
+        }
+        for (int i = 0; i < QB; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 1);
+            mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.piece_full[i]), 1);
+            mbar_init(smem_u32(&sm.piece_empty[i]), 1 + 1 + 8);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sm.s_full[i][b]), 1);
+                mbar_init(smem_u32(&sm.s_free[i][b]), 4);
+            }
+        }
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort_flag = sm.zero = 0;
+        sm.start[0] = -1;
+        fence_barrier_init();
+        tma_prefetch_desc(&p.tm_q);
+        tma_prefetch_desc(&p.tm_k);
+    }
+    if (warp == 2) {
+        tmem_alloc(smem_u32(&sm.tmem_base), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    pdl_wait();
+
+    // ---- the line of all key tiles, and where this CTA's stretch begins
+    long long at, end;
+    {
+        const int chunk = (p.B + kThreads - 1) / kThreads;
+        const int i0 = min((long long)p.B, (long long)threadIdx.x * chunk), i1 = min(p.B, i0 + chunk);
+        long long mine = 0;
+        int bad = 0;
+        for (int i = i0; i < i1; ++i) {
+            const SeqInfo s = seq_info(p, i);
+            bad |= s.bad;
+            mine += (long long)cdiv(s.len, kBN) * p.cache.heads;
+        }
+        if (bad && blockIdx.x == 0) atomicOr(status, bad);
+        long long incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) sm.sums[warp] = incl;
+        __syncthreads();
+        long long before = 0, total = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sm.sums[w];
+            total += sm.sums[w];
+        }
+        const long long per = (total + gridDim.x - 1) / gridDim.x;
+        at = min(total, per * blockIdx.x);
+        end = min(total, at + per);
+        long long first = before + incl - mine;  // first tile of this thread's sequences
+        if (at < end && at >= first && at < first + mine) {
+            for (int i = i0; i < i1; ++i) {
+                const SeqInfo s = seq_info(p, i);
+                const int tiles = cdiv(s.len, kBN);
+                const long long all = (long long)tiles * p.cache.heads;
+                if (at >= first + all) {
+                    first += all;
+                    continue;
+                }
+                sm.start[0] = i;
+                sm.start[1] = (int)((at - first) / tiles);
+                sm.start[2] = (int)((at - first) % tiles);
+                break;
+            }
+        }
+        __syncthreads();
+    }
+    // Q tiles of a piece; where there is one it is loaded once
+    auto q_tiles = [&](int n) { return (n + p.tile_tokens - 1) / p.tile_tokens; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ pieces and K
+        int it = 0, f = 0, b = sm.start[0], h = sm.start[1], k0 = sm.start[2];
+        const int ps = p.cache.page_size, shift = p.page_shift, boxes = kBN >> shift;
+        const int box = lane / C::kCols, col = lane % C::kCols;
+        bool ok = true;
+        int place = -1, count = 0;  // ring place of this lane's turn among the last 32 loads
+        SeqInfo s = {};
+        if (at < end) s = seq_info(p, b);
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_empty[slot]), ((it >> 1) & 1) ^ 1, stop, status)))
+                break;
+            Piece x = {};
+            x.h = -1;
+            if (at < end) {
+                x.h = h;
+                x.tok0 = s.t0;
+                x.n = s.n;
+                x.slot = s.slot;
+                x.len = s.len;
+                x.ctx = s.len - s.n;
+                x.k0 = k0;
+                x.tiles = (int)min((long long)(cdiv(s.len, kBN) - k0), end - at);
+            }
+            if (lane == 0) {
+                sm.piece[slot] = x;
+                mbar_arrive(smem_u32(&sm.piece_full[slot]));
+            }
+            __syncwarp();
+            ++it;
+            if (x.h < 0) break;
+            const int* table = p.cache.table + (long long)x.slot * p.cache.max_pages;
+            const int used = (x.len + ps - 1) >> shift;
+            int win = (x.k0 * kBN) >> shift;  // page ids of a window of 32 pages
+            int ids = win + lane < used ? table[win + lane] : -1;
+            int nxt = win + 32 + lane < used ? table[win + 32 + lane] : -1;
+            for (int j = 0; j < x.tiles && ok; ++j) {
+                const int key0 = (x.k0 + j) * kBN, first = key0 >> shift;
+                if (first >= win + 32) {
+                    win += 32;
+                    ids = nxt;
+                    nxt = win + 32 + lane < used ? table[win + 32 + lane] : -1;
+                }
+                const int page = __shfl_sync(0xffffffffu, ids, (first - win + box) & 31);
+                const int st = f % S;
+                if (!(ok = warp_wait(smem_u32(&sm.empty[st]), ((f / S) & 1) ^ 1, stop, status))) break;
+                const int have = min(boxes, used - first);  // (pages that hold no key are not loaded)
+                const uint32_t bar = smem_u32(&sm.full[st]);
+                if (lane == 0) mbar_arrive_expect_tx(bar, have * ps * 128 * C::kCols);
+                __syncwarp();
+                if (box < have) {  // (8 boxes of 4 columns at most: a lane each)
+                    int plane = -1;  // a page id out of range reads zeros and is reported
+                    if (page >= 0 && page < p.cache.pages)
+                        plane = (p.layer * p.cache.pages + page) * p.cache.heads + x.h;
+                    else
+                        atomicOr(status, kCacheBadSlot);
+                    tma_load_3d(smem_u32(sm.k[st]) + col * (kBN * 128) + (box << shift) * 128, &p.tm_k,
+                                bar, col * 64, 0, plane);
+                }
+                if ((count++ & 31) == lane) place = f;
+                ++f;
+            }
+            at += x.tiles;
+            k0 = 0;
+            if (at < end && ++h == p.cache.heads) {
+                h = 0;
+                do {
+                    ++b;
+                    if (b >= p.B) {  // (cannot be: the line counts real tiles)
+                        at = end;
+                        break;
+                    }
+                    s = seq_info(p, b);
+                } while (s.len == 0);
+            }
+        }
+        if (!ok) {  // never leave a TMA write in flight
+            int last = place;
+            for (int o = 16; o; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
+            if (place >= 0 && place > last - S)
+                mbar_wait(smem_u32(&sm.full[place % S]), (place / S) & 1, &sm.zero);
+            __syncwarp();
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------ Q and LSE
+        int it = 0, g = 0;
+        bool ok = true;
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_full[slot]), (it >> 1) & 1, stop, status))) break;
+            const Piece x = sm.piece[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+            ++it;
+            if (x.h < 0) break;
+            const int nq = q_tiles(x.n), times = nq == 1 ? 1 : (x.tiles + 1) / 2;
+            for (int pr = 0; pr < times && ok; ++pr)
+                for (int qt = 0; qt < nq && ok; ++qt, ++g) {
+                    const int qs = g % QB;
+                    if (!(ok = warp_wait(smem_u32(&sm.q_empty[qs]), ((g / QB) & 1) ^ 1, stop, status)))
+                        break;
+                    const uint32_t bar = smem_u32(&sm.q_full[qs]);
+                    const int tok = x.tok0 + qt * p.tile_tokens;
+                    const int rows = min(p.tile_tokens, x.n - qt * p.tile_tokens) * p.group;
+                    for (int r = lane; r < rows; r += 32) {
+                        const int t = r / p.group;
+                        const float l = p.lse[(size_t)(x.h * p.group + r - t * p.group) * p.T + tok + t];
+                        // (a row that sees nothing gives nothing)
+                        sm.nl[qs][r] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(bar, p.tile_tokens * p.group * 128 * C::kCols);
+                        for (int c = 0; c < C::kCols; ++c)
+                            tma_load_4d(smem_u32(sm.q[qs]) + c * (NQ * 128), &p.tm_q, bar, c * 64, 0, x.h,
+                                        tok);
+                    }
+                    __syncwarp();
+                }
+        }
+        if (!ok && lane == 0)
+            for (int i = 0; i < QB && i < g; ++i)
+                mbar_wait(smem_u32(&sm.q_full[(g - 1 - i) % QB]), ((g - 1 - i) / QB) & 1, &sm.zero);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t id = make_idesc_bf16(128, NQ, false, false);
+        const uint32_t lead = elect_lead();
+        int it = 0, f = 0, g = 0, cnt[2] = {0, 0};
+        bool ok = true;
+        auto wait = [&](uint64_t& bar, int parity) {
+            return ok = ok && warp_wait(smem_u32(&bar), parity & 1, stop, status);
+        };
+        while (ok) {
+            const int slot = it & 1;
+            if (!wait(sm.piece_full[slot], it >> 1)) break;
+            const int h = __shfl_sync(0xffffffffu, sm.piece[slot].h, 0);
+            const int n = __shfl_sync(0xffffffffu, sm.piece[slot].n, 0);
+            const int tiles = __shfl_sync(0xffffffffu, sm.piece[slot].tiles, 0);
+            if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+            __syncwarp();
+            ++it;
+            if (h < 0) break;
+            const int nq = q_tiles(n), pairs = (tiles + 1) / 2;
+            for (int pr = 0; pr < pairs && ok; ++pr) {
+                const int both = min(2, tiles - 2 * pr);
+                for (int qt = 0; qt < nq && ok; ++qt) {
+                    if ((nq > 1 || pr == 0) && !wait(sm.q_full[g % QB], g / QB)) break;
+                    for (int w = 0; w < both; ++w) {
+                        const int fk = f + w, bf = cnt[w] & 1;
+                        if (qt == 0 && !wait(sm.full[fk % S], fk / S)) break;
+                        if (cnt[w] >= 2 && !wait(sm.s_free[w][bf], (cnt[w] - 2) >> 1)) break;
+                        tc_fence_after();
+                        const uint64_t da = make_sdesc(smem_u32(sm.k[fk % S]), 16, 1024);
+                        const uint64_t db = make_sdesc(smem_u32(sm.q[g % QB]), 16, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < DR / 16; ++kk)
+                            warp_mma_ss(lead, tmem + (w * 2 + bf) * 128,
+                                        sdesc_add(da, (kk >> 2) * (kBN * 128) + (kk & 3) * 32),
+                                        sdesc_add(db, (kk >> 2) * (NQ * 128) + (kk & 3) * 32), id, kk > 0);
+                        warp_mma_commit(lead, smem_u32(&sm.s_full[w][bf]));
+                        if (qt == nq - 1) warp_mma_commit(lead, smem_u32(&sm.empty[fk % S]));
+                        ++cnt[w];
+                    }
+                    if (!ok) break;
+                    if (nq > 1 || pr == pairs - 1) {
+                        warp_mma_commit(lead, smem_u32(&sm.q_empty[g % QB]));
+                        ++g;
+                    }
+                }
+                f += both;
+            }
+        }
+        warp_mma_commit(lead, smem_u32(&sm.drain));
+        mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------ exponentials and sums
+        const int w = (warp - 4) >> 2, q4 = warp & 3;
+        const int row = q4 * 32 + lane;  // key of the tile
+        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        int it = 0, g = 0, cnt = 0;
+        bool ok = true;
+        while (ok) {
+            const int slot = it & 1;
+            if (!(ok = warp_wait(smem_u32(&sm.piece_full[slot]), (it >> 1) & 1, stop, status))) break;
+            const Piece x = sm.piece[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
+            ++it;
+            if (x.h < 0) break;
+            const int nq = q_tiles(x.n), pairs = (x.tiles + 1) / 2;
+            float* out = p.weights + ((long long)x.slot * p.cache.heads + x.h) *
+                                         ((long long)p.cache.max_pages * p.cache.page_size);
+            for (int pr = 0; pr < pairs && ok; ++pr) {
+                const bool mine = 2 * pr + w < x.tiles;
+                const int key0 = (x.k0 + 2 * pr + w) * kBN, key = key0 + row;
+                const bool own = key0 + kBN > x.ctx;  // some keys are the call's own tokens
+                float sum = 0.f;
+                for (int qt = 0; qt < nq && ok; ++qt) {
+                    const int qs = g % QB;
+                    if (mine) {
+                        if (!(ok = warp_wait(smem_u32(&sm.s_full[w][cnt & 1]), (cnt >> 1) & 1, stop, status)))
+                            break;
+                        tc_fence_after();
+                        // (the scores are there, so the tile's LSE are; the barrier publishes them)
+                        if (!(ok = warp_wait(smem_u32(&sm.q_full[qs]), (g / QB) & 1, stop, status))) break;
+                        const uint32_t s_at = tmem + lane_off + (w * 2 + (cnt & 1)) * 128;
+                        const int tok0 = qt * p.tile_tokens;
+                        const int ncols = min(p.tile_tokens, x.n - tok0) * p.group;
+                        if (!own) {
+                            sum += weigh<false>(s_at, sm.nl[qs], p.scale_log2, ncols, [](int) { return true; });
+                        } else {
+                            const int j = key - x.ctx;  // among the call's own tokens; < 0: the context
+                            sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols, [&](int col) {
+                                const int t = tok0 + col / p.group;
+                                if (j < 0) return true;
+                                if (!p.mask) return j <= t;
+                                const unsigned long long* words =
+                                    static_cast<const unsigned long long*>(p.mask) +
+                                    (size_t)(x.tok0 + t) * p.words;
+                                return j < 64 * p.words && ((words[j >> 6] >> (j & 63)) & 1) != 0;
+                            });
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[w][cnt & 1]));
+                        ++cnt;
+                    }
+                    if (nq > 1 || pr == pairs - 1) {
+                        // (a phase of q_full may not pass unseen: the parity tells only the last)
+                        if (!mine && !(ok = warp_wait(smem_u32(&sm.q_full[qs]), (g / QB) & 1, stop, status)))
+                            break;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[qs]));
+                        ++g;
+                    }
+                }
+                if (ok && mine && key < x.len) atomicAdd(out + key, sum);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int DR, int NQ>
+cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
+    auto kern = weights_kernel<D, DR, NQ>;
+    constexpr size_t smem = sizeof(Smem<D, NQ>) + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
+}
+
+bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" fa_status fa_cache_weights(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                                      const int* cu_seqlens, int T, const void* q, int Hq,
+                                      long long q_token_stride, long long q_head_stride,
+                                      const float* lse, const void* mask, int mask_words,
+                                      float* weights, float scale, fa_stream_t stream) {
+    const fa_status cs = check_cache(cache);
+    if (cs != FA_OK) return cs;
+    const int d = cache->d, Hkv = cache->heads;
+    if (layer < 0 || layer >= cache->layers || B < 0 || N < 0 || T < 0 || Hq <= 0 || Hq % Hkv)
+        return FA_ERR_INVALID_ARG;
+    if (Hq / Hkv > 128 || Hq > 65535 || (long long)T * Hq * d > (1LL << 40) || B > kMostSequences)
+        return FA_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_UNSUPPORTED;
+    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (mask && (mask_words <= 0 || (long long)mask_words * 64 < N)) return FA_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return FA_OK;
+    if (!slots || !q || !lse || !weights) return FA_ERR_INVALID_ARG;
+    if (N == 0) N = 1;  // (a packed batch of empty sequences)
+    if (!aligned(slots, 4) || !aligned(cu_seqlens, 4) || !aligned(q, 16) || !aligned(lse, 4) ||
+        !aligned(mask, 8) || !aligned(weights, 4))
+        return FA_ERR_INVALID_ARG;
+    if (T == 1) q_token_stride = (long long)Hq * d;  // (a stride that is never taken)
+    if (Hq == 1) q_head_stride = d;
+    if (q_token_stride <= 0 || q_head_stride <= 0 || q_token_stride % 8 || q_head_stride % 8 ||
+        q_token_stride >= (1LL << 38) || q_head_stride >= (1LL << 31))
+        return FA_ERR_INVALID_ARG;
+    const int group = Hq / Hkv, nq = d > 128 && group <= 64 ? 64 : 128;
+    const int tokens = nq / group < N ? nq / group : N;
+    TreeParams maps;
+    std::memset(&maps, 0, sizeof(maps));
+    if (!make_tree_maps(maps, *cache, q, T, Hq, q_token_stride, q_head_stride, tokens, kBN))
+        return FA_ERR_CUDA;
+    Params p;
+    std::memset(&p, 0, sizeof(p));
+    p.tm_q = maps.tm_q;
+    p.tm_k = maps.tm_k;
+    p.cache = *cache;
+    p.slots = slots;
+    p.cu = cu_seqlens;
+    p.mask = mask;
+    p.words = mask_words;
+    p.lse = lse;
+    p.weights = weights;
+    p.layer = layer;
+    p.B = B; p.N = N; p.T = T; p.Hq = Hq;
+    p.group = group;
+    p.tile_tokens = tokens;
+    p.page_shift = __builtin_ctz(cache->page_size);
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const int ctas = device_sms();
+    if (ctas <= 0) return FA_ERR_CUDA;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (d == 64) e = launch<64, 64, 128>(p, ctas, strm);
+    else if (d == 96) e = launch<128, 96, 128>(p, ctas, strm);
+    else if (d == 128) e = launch<128, 128, 128>(p, ctas, strm);
+    else if (d == 192) e = nq == 64 ? launch<192, 192, 64>(p, ctas, strm) : launch<192, 192, 128>(p, ctas, strm);
+    else e = nq == 64 ? launch<256, 256, 64>(p, ctas, strm) : launch<256, 256, 128>(p, ctas, strm);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}

@@ -16,6 +16,12 @@ A serving step::
         o, lse = fa.tree_attention(q, cache, layer, slots, mask=mask)
     cache.accept(slots, base, path, accepted)        # after verifying a drafted tree
     cache.check()                                    # now and then: errors found on the device
+
+A cache that stays within a budget adds up what each key receives, and drops those that received
+least (`weights`: fp32 ``[layers, cache.slots, heads, max_pages * page_size]``, zeros at first)::
+
+    fa.cache_weights(q, lse, cache, layer, slots, weights[layer])     # behind tree_attention
+    cache.evict(slots, weights, keep, recent, sinks=4)                # every so many tokens
 """
 from __future__ import annotations
 
@@ -29,7 +35,8 @@ from torch.autograd import forward_ad
 
 from . import FA_BF16, FA_FP32, FA_OK, FAError, lib
 
-__all__ = ["PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask"]
+__all__ = ["PagedCache", "rotary", "rotary_table", "cache_append", "cache_weights", "tree_attention",
+           "tree_mask"]
 
 _INT = (torch.int32,)
 _BF16 = (torch.bfloat16,)
@@ -471,6 +478,40 @@ class PagedCache:
         self._call("fa_cache_accept", stream, (slots, base, path, accepted), slots.data_ptr(),
                    base.data_ptr(), path.data_ptr(), path.shape[1], accepted.data_ptr(), n)
 
+    def evict(self, slots, weights, keep, recent, sinks=0, stream=None):
+        """Cuts each slot longer than ``keep`` (an int, or int32 ``[n]``) down to that many tokens, in
+        every layer and head on its own: the first ``sinks`` and the last ``recent`` stay, and of
+        the others those with the highest ``weights`` (fp32 ``[layers, slots, heads, max_pages *
+        page_size]``, of all slots of the cache; ties keep the lowest place, NaN counts as
+        highest).  The recent ones become the last ``recent`` rows, in order.  A kept one stays
+        in its place where that lies before them; the others fill the places of dropped ones, in
+        ascending order both.  Weights move with their rows, and those of places behind the new
+        length become 0.  Pages behind it are free again.  Slots must differ; a page that several
+        slots share may not lie where rows are written (from ``sinks`` to ``keep``).
+
+        Places are no longer positions then: give `cache_append` its ``positions``.
+        """
+        n = self._list("slots", slots).shape[0]
+        self._few(n)
+        _want("weights", weights, (torch.float32,), 4, self.device)
+        shape = (self.layers, self.slots, self.heads, self.max_pages * self.page_size)
+        if tuple(weights.shape) != shape:
+            raise ValueError(f"weights must be {shape}, got {tuple(weights.shape)}")
+        _not_differentiable("evict", weights, self.k, self.v)
+        recent, sinks = _whole("recent", recent), _whole("sinks", sinks)
+        if recent < 0 or sinks < 0 or recent + sinks > _MOST:
+            raise ValueError(f"recent and sinks must not be negative, nor above {_MOST} together")
+        many = keep if isinstance(keep, torch.Tensor) else None
+        if many is not None:
+            self._list("keep", many, n)
+            keep = 0
+        else:
+            keep = _whole("keep", keep)
+            if not recent + sinks <= keep <= _MOST:
+                raise ValueError(f"keep must hold the sinks and the recent tokens, got {keep}")
+        self._call("fa_cache_evict", stream, (slots, many, weights), slots.data_ptr(), _ptr(many),
+                   keep, recent, sinks, weights.data_ptr(), n)
+
     def check(self, stream=None):
         """Synchronises the stream, and raises if a call on this cache has been refused on the
         device or failed there since the last check.  What a call on another stream finds while
@@ -670,3 +711,57 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
         _ptr(mask), words, o.data_ptr(), lse.data_ptr(), scale, 1 if out is None else 0,
         ws.data_ptr(), size, _raw_stream(dev)), "fa_tree_fwd")
     return o, lse
+
+
+def cache_weights(q, lse, cache, layer, slots, weights, mask=None, scale=None, cu_seqlens=None,
+                  max_seqlen=None, stream=None):
+    """Adds up what each cached key receives from a call's queries: to ``weights[slot, head, place]``
+    the sum of exp(scale * q.k - lse) over the new tokens that see the key, and over the query
+    heads of its key/value head.
+
+    ``q``, ``mask``, ``scale`` and the sequences are those of the `tree_attention` call (without a
+    window) that gave ``lse``.  ``weights``: fp32 ``[cache.slots, heads, max_pages * page_size]``, those
+    of one layer; places of other slots and behind a sequence's end are left alone.  Any part of a
+    prompt may be asked, for instance only its last tokens.  A row whose lse is -inf gives
+    nothing.  Not differentiable.
+    """
+    n = _of_cache(cache, layer, slots)
+    dev = cache.device
+    if not _here(dev, stream):
+        with _on(dev, stream, cache._tensors + (q, lse, slots, weights, mask, cu_seqlens)):
+            return cache_weights(q, lse, cache, layer, slots, weights, mask, scale, cu_seqlens, max_seqlen)
+    _heads_tensor("q", q, _BF16, dev)
+    T, Hq, d = q.shape
+    if Hq > _MOST:
+        _too_far("q", q)
+    if d != cache.d:
+        raise ValueError("q and the cache differ in head dimension")
+    if Hq % cache.heads or Hq == 0:
+        raise ValueError("the query heads must be a multiple of the key/value heads")
+    B, N = _sequences(T, n, cu_seqlens, max_seqlen, dev)
+    _want("lse", lse, (torch.float32,), 2, dev)
+    if tuple(lse.shape) != (Hq, T):
+        raise ValueError("lse must be [Hq, T]")
+    _want("weights", weights, (torch.float32,), 3, dev)
+    if tuple(weights.shape) != (cache.slots, cache.heads, cache.max_pages * cache.page_size):
+        raise ValueError("weights must be [cache.slots, heads, max_pages * page_size], got "
+                         f"{tuple(weights.shape)}")
+    words = 0
+    if mask is not None:
+        _want("mask", mask, (torch.int64,), 2, dev)
+        rows, words = mask.shape
+        if rows != T or 64 * words < N:
+            raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
+        if words > _MOST:
+            _too_far("mask", mask)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    if (q.requires_grad or lse.requires_grad or weights.requires_grad or cache.k.requires_grad or
+            forward_ad._current_level >= 0):
+        _not_differentiable("cache_weights", q, lse, weights, cache.k)
+    if T == 0:
+        return
+    qt, qh, _ = q.stride()
+    _check(lib().fa_cache_weights(
+        cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
+        lse.data_ptr(), _ptr(mask), words, weights.data_ptr(), scale, _raw_stream(dev)),
+        "fa_cache_weights")

@@ -533,6 +533,48 @@ fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots,
                              int zero_rest, void* workspace, size_t workspace_bytes,
                              fa_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A cache within a budget
+ * ------------------------------------------------------------------------
+ * weights: device fp32, for each layer [slots, heads, max_pages * page_size]: what the
+ * key in each place has received so far.  The caller zeroes them when a slot begins.
+ */
+
+/*
+ * Adds to weights[slot, head, j] (one layer's) the attention that the key in place j
+ * receives from the call's rows: the sum, over the tokens that see it and the query
+ * heads of its head, of exp(scale * q.k - lse).  Sequences, q and mask as in
+ * fa_tree_fwd, whose lse [Hq,T] this takes; scale positive and finite.
+ *   A row with lse = -inf gives nothing.  Sums are fp32, each key's in one addition, so
+ *   that results do not vary from run to run.  A slot that the call names several
+ *   times receives all sums (in any order).  Places behind a sequence's length are
+ *   left alone.  What is wrong in slots, lengths or boundaries sets the status word, and
+ *   that sequence adds nothing.  No workspace; reads keys and tables, like attention.
+ */
+fa_status fa_cache_weights(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                           const int* cu_seqlens, int T, const void* q, int Hq,
+                           long long q_token_stride, long long q_head_stride, const float* lse,
+                           const void* mask, int mask_words, float* weights, float scale,
+                           fa_stream_t stream);
+
+/*
+ * Cuts slots[i] down to keep[i] tokens (keep_all each, keep NULL), where it is longer,
+ * in every layer and head on its own.  Of len tokens the first `sinks` and the last
+ * `recent` are kept, and of the others the keep - sinks - recent with the highest
+ * weights (ties: the lowest place first; NaN highest; -0 is 0).  The recent ones become
+ * the last rows before keep, in order.  A kept one stays in its place where that lies
+ * before them; those that do not fill the places of dropped ones, both in ascending
+ * order.  K, V and weights (fp32 [layers, slots, heads, max_pages * page_size]) move
+ * alike, weights of [keep, len) become 0, rows from keep on are left as they are, the
+ * length becomes keep and pages behind it are released.
+ *   A page operation: ordered with the others of the cache, all or nothing, with the
+ *   same status bits: 1 (slot or page out of range, slot named twice), 2 (a length
+ *   that does not fit, keep < sinks + recent), 8 (a page with a place in [sinks, keep), or
+ *   the page that is left partly filled, is shared).
+ */
+fa_status fa_cache_evict(const fa_cache* cache, const int* slots, const int* keep, int keep_all,
+                         int recent, int sinks, float* weights, int n, fa_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
