@@ -154,18 +154,19 @@ __global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, floa
     const bool cached = many <= room_keys;
     auto key = [&](int j) { return cached ? keys[j] : key_of(w[sinks + j]); };
 
-    // ---- rows: 16-byte pieces of K and V
+    // ---- rows: a thread has one 16-byte piece of them, of K or of V, and takes every
+    // `rows`-th row, kRun in flight
     const int* pages = s.shadow + (long long)slot * c.max_pages;
-    const int row16 = c.d / 8;
-    const long long plane = (long long)c.page_size * row16;
-    uint4* kbase = static_cast<uint4*>(c.k) + ((long long)layer * c.pages * c.heads + head) * plane;
-    uint4* vbase = static_cast<uint4*>(c.v) + ((long long)layer * c.pages * c.heads + head) * plane;
-    auto at = [&](int piece, int tok) {  // piece: of a row's 2 * row16, K first
-        uint4* base = piece < row16 ? kbase : vbase;
-        return base + pages[tok / c.page_size] * (c.heads * plane) + (tok % c.page_size) * row16 +
-               (piece < row16 ? piece : piece - row16);
+    const int row16 = c.d / 8, row0 = tid / (2 * row16), rows = kEvict / (2 * row16);
+    const int piece = tid - row0 * 2 * row16, col = piece < row16 ? piece : piece - row16;
+    const bool moving = row0 < rows;  // (a few threads are left over where rows do not divide them)
+    const int shift = __ffs(c.page_size) - 1;
+    const long long plane = (long long)c.page_size * row16, page = plane * c.heads;
+    uint4* base = static_cast<uint4*>(piece < row16 ? c.k : c.v) +
+                  ((long long)layer * c.pages * c.heads + head) * plane + col;
+    auto at = [&](int tok) {
+        return base + pages[tok >> shift] * page + (tok & (c.page_size - 1)) * row16;
     };
-    const int row32 = 2 * row16;
 
     if (top > 0) {
         for (int j = tid; j < 48; j += kEvict) sm.counts[j / 3][j % 3] = 0;
@@ -235,19 +236,15 @@ __global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, floa
             visit([&](int j) { if (h >= 0 && h < kPairs) sm.hole[h] = sinks + j; ++h; },
                   [&](int j) { if (f >= 0 && f < kPairs) sm.from[f] = sinks + j; ++f; });
             __syncthreads();
-            const int now = min(kPairs, moves - first), pieces = now * row32;
-            for (int u0 = tid; u0 < pieces; u0 += kRun * kEvict) {
+            const int now = min(kPairs, moves - first);
+            for (int m = row0; moving && m < now; m += kRun * rows) {
                 uint4 v[kRun];
 #pragma unroll
-                for (int r = 0; r < kRun; ++r) {
-                    const int u = u0 + r * kEvict;
-                    if (u < pieces) v[r] = __ldcs(at(u % row32, sm.from[u / row32]));
-                }
+                for (int r = 0; r < kRun; ++r)
+                    if (m + r * rows < now) v[r] = __ldcs(at(sm.from[m + r * rows]));
 #pragma unroll
-                for (int r = 0; r < kRun; ++r) {
-                    const int u = u0 + r * kEvict;
-                    if (u < pieces) __stcs(at(u % row32, sm.hole[u / row32]), v[r]);
-                }
+                for (int r = 0; r < kRun; ++r)
+                    if (m + r * rows < now) __stcs(at(sm.hole[m + r * rows]), v[r]);
             }
             for (int m = tid; m < now; m += kEvict) w[sm.hole[m]] = w[sm.from[m]];
             __syncthreads();
@@ -256,19 +253,16 @@ __global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, floa
 
     // ---- the recent rows close up: a run lies above all that earlier runs have written
     const bool apart = recent <= len - keep;  // (nothing that is written is read)
-    for (long long u0 = 0; u0 < (long long)recent * row32; u0 += kRun * kEvict) {
+    for (int m0 = 0; m0 < recent; m0 += kRun * rows) {
+        const int m = moving ? m0 + row0 : recent;
         uint4 v[kRun];
 #pragma unroll
-        for (int r = 0; r < kRun; ++r) {
-            const long long u = u0 + r * kEvict + tid;
-            if (u < (long long)recent * row32) v[r] = __ldcs(at((int)(u % row32), last + (int)(u / row32)));
-        }
+        for (int r = 0; r < kRun; ++r)
+            if (m + r * rows < recent) v[r] = __ldcs(at(last + m + r * rows));
         if (!apart) __syncthreads();
 #pragma unroll
-        for (int r = 0; r < kRun; ++r) {
-            const long long u = u0 + r * kEvict + tid;
-            if (u < (long long)recent * row32) __stcs(at((int)(u % row32), gap + (int)(u / row32)), v[r]);
-        }
+        for (int r = 0; r < kRun; ++r)
+            if (m + r * rows < recent) __stcs(at(gap + m + r * rows), v[r]);
     }
     for (int m0 = 0; m0 < recent; m0 += kEvict) {
         const int m = m0 + tid;

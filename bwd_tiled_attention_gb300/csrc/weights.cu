@@ -147,34 +147,46 @@ template <bool MASK, typename See>
 __device__ __forceinline__ float weigh(uint32_t s_at, const float* nl, float c, int ncols, See&& see) {
     float sum = 0.f;
     const uint64_t cc = f2_pack(c, c);
-#pragma unroll 1
-    for (int c0 = 0; c0 < ncols; c0 += 32) {
-        uint32_t r[32];
-        tmem_ld32(s_at + c0, r);
-        tmem_ld_wait();
-        if (!MASK && c0 + 32 <= ncols) {
-            uint64_t acc[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+    int c0 = 0;
+    if (!MASK && ncols >= 64) {
+        uint64_t acc[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+        for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
+#pragma unroll 1
+        for (; c0 + 64 <= ncols; c0 += 64) {
+            uint32_t r[2][32];
+            tmem_ld32(s_at + c0, r[0]);
+            tmem_ld32(s_at + c0 + 32, r[1]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
                 const ulonglong2 l = reinterpret_cast<const ulonglong2*>(nl + c0)[e];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint64_t x = f2_fma(f2_pack(__uint_as_float(r[4 * e + 2 * h]),
-                                                      __uint_as_float(r[4 * e + 2 * h + 1])),
-                                              cc, h ? l.y : l.x);
+                    const uint32_t* s = &r[e >> 3][(4 * e + 2 * h) & 31];
                     float x0, x1;
-                    f2_unpack(x, x0, x1);
-                    acc[h] = f2_add(acc[h], f2_pack(ex2_approx(x0), ex2_approx(x1)));
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[0]), __uint_as_float(s[1])), cc, h ? l.y : l.x),
+                              x0, x1);
+                    acc[(e & 1) * 2 + h] = f2_add(acc[(e & 1) * 2 + h], f2_pack(ex2_approx(x0), ex2_approx(x1)));
                 }
             }
-            float a, b;
-            f2_unpack(f2_add(acc[0], acc[1]), a, b);
-            sum += a + b;
-        } else {
+        }
+        float a, b;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+        sum = a + b;
+    }
+#pragma unroll 1
+    for (; c0 < ncols; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld32(s_at + c0, r);
+        tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int col = c0 + i;
-                const float e = ex2_approx(fmaf(__uint_as_float(r[i]), c, nl[min(col, ncols - 1)]));
+        for (int i = 0; i < 32; i += 4) {
+            if (c0 + i >= ncols) break;
+#pragma unroll
+            for (int k = i; k < i + 4; ++k) {
+                const int col = c0 + k;
+                const float e = ex2_approx(fmaf(__uint_as_float(r[k]), c, nl[col]));
                 if (col < ncols && (!MASK || see(col))) sum += e;
             }
         }
@@ -201,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             mbar_init(smem_u32(&sm.empty[s]), 1);
         }
         for (int i = 0; i < QB; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), 1);
+            mbar_init(smem_u32(&sm.q_full[i]), 2);
             mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -383,13 +395,6 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     const uint32_t bar = smem_u32(&sm.q_full[qs]);
                     const int tok = x.tok0 + qt * p.tile_tokens;
                     const int rows = min(p.tile_tokens, x.n - qt * p.tile_tokens) * p.group;
-                    for (int r = lane; r < rows; r += 32) {
-                        const int t = r / p.group;
-                        const float l = p.lse[(size_t)(x.h * p.group + r - t * p.group) * p.T + tok + t];
-                        // (a row that sees nothing gives nothing)
-                        sm.nl[qs][r] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-                    }
-                    __syncwarp();
                     if (lane == 0) {
                         mbar_arrive_expect_tx(bar, p.tile_tokens * p.group * 128 * C::kCols);
                         for (int c = 0; c < C::kCols; ++c)
@@ -397,6 +402,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                                         tok);
                     }
                     __syncwarp();
+                    float l[NQ / 32];
+#pragma unroll
+                    for (int i = 0; i < NQ / 32; ++i) {
+                        const int r = i * 32 + lane, t = r / p.group;
+                        l[i] = 0.f;
+                        if (r < rows) l[i] = p.lse[(size_t)(x.h * p.group + r - t * p.group) * p.T + tok + t];
+                    }
+#pragma unroll
+                    for (int i = 0; i < NQ / 32; ++i)  // (a row that sees nothing gives nothing)
+                        sm.nl[qs][i * 32 + lane] = l[i] == -INFINITY ? -INFINITY : -l[i] * 1.4426950408889634f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar);
                 }
         }
         if (!ok && lane == 0)
@@ -459,6 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const int w = (warp - 4) >> 2, q4 = warp & 3;
         const int row = q4 * 32 + lane;  // key of the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        // col / group is (col * per_group) >> 16: the product is less than 128 / 65536 of a
+        // group too large
+        const unsigned per_group = 65536u / p.group + 1;
         int it = 0, g = 0, cnt = 0;
         bool ok = true;
         while (ok) {
@@ -492,15 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                             sum += weigh<false>(s_at, sm.nl[qs], p.scale_log2, ncols, [](int) { return true; });
                         } else {
                             const int j = key - x.ctx;  // among the call's own tokens; < 0: the context
-                            sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols, [&](int col) {
-                                const int t = tok0 + col / p.group;
-                                if (j < 0) return true;
-                                if (!p.mask) return j <= t;
-                                const unsigned long long* words =
-                                    static_cast<const unsigned long long*>(p.mask) +
-                                    (size_t)(x.tok0 + t) * p.words;
-                                return j < 64 * p.words && ((words[j >> 6] >> (j & 63)) & 1) != 0;
-                            });
+                            if (!p.mask) {
+                                const int first = (j - tok0) * p.group;  // column that sees it
+                                sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols,
+                                                   [&](int col) { return col >= first; });
+                            } else {
+                                const unsigned long long* words = static_cast<const unsigned long long*>(p.mask) +
+                                                                  (size_t)(x.tok0 + tok0) * p.words + max(j, 0) / 64;
+                                const bool some = j < 64 * p.words;
+                                sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols, [&](int col) {
+                                    if (j < 0) return true;
+                                    const int t = (int)(((unsigned)col * per_group) >> 16);
+                                    return some && ((words[(size_t)t * p.words] >> (j & 63)) & 1) != 0;
+                                });
+                            }
                         }
                         tc_fence_before();
                         __syncwarp();

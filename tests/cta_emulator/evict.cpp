@@ -1,6 +1,7 @@
 // The eviction's source as the host runs it, beside the page operations' (cache.cpp).
 #include "cuda_runtime.h"
 
+inline int __ffs(int x) { return __builtin_ffs(x); }
 inline int __reduce_add_sync(unsigned mask, int v) {
     const uint64_t* got = emu::collective(mask, emu::bits_of(&v, sizeof(v)));
     int sum = 0;
