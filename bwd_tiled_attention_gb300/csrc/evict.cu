@@ -15,9 +15,10 @@
 // A planning CTA checks the call, copies the page lists of its slots (the moves need
 // them), and does the bookkeeping; then a CTA a (sequence, layer, head):
 //   - weights become 32-bit keys in their order, in shared memory where they fit;
-//   - the lowest kept key is found by a search over its bits, two at a time: 16 counts of
-//     all keys.  (Counting needs no histogram: most weights share their exponent, so that
-//     most of a radix digit's atomics would meet in a few words.)
+//   - the lowest kept key is found by a search over its bits, two at a time, by counting
+//     keys; those that share its first bits are listed once they are few.  (Counting needs
+//     no histogram: most weights share their exponent, so that most of a radix digit's
+//     atomics would meet in a few words.)
 //   - a second and third look count ties, holes and rows to move along each thread's
 //     stretch; ranks from sums over the CTA pair the r-th hole with the r-th such row;
 //   - 16-byte pieces of K and V move, then the recent rows close up from below, in runs
@@ -40,10 +41,9 @@
 namespace fa {
 namespace {
 
-constexpr int kEvict = 512;       // threads of a (sequence, layer, head)'s CTA
 constexpr int kMostKeys = 32768;  // keys in shared memory
 constexpr int kPairs = 2048;      // moves listed at once
-constexpr int kRun = 4;           // 16-byte pieces in flight a thread
+constexpr int kRun = 8;           // 16-byte pieces in flight a thread
 
 __global__ void __launch_bounds__(kPlan) evict_plan_kernel(const fa_cache c, const int* slots,
                                                            const int* keep, int keep_all, int recent,
@@ -110,12 +110,13 @@ __device__ __forceinline__ unsigned key_of(float w) {
 }
 
 struct EvictSmem {
-    int counts[16][3];
-    long long sums[kEvict / 32 + 1];
-    int hole[kPairs], from[kPairs];
+    int counts[16][3], listed;
+    long long sums[16];
+    int hole[2 * kPairs];   // and where they are filled from: hole[kPairs + i]
 };
 
 // Sum over the CTA's threads before this one, and the total.
+template <int kEvict>
 __device__ __forceinline__ long long cta_scan(long long x, long long* sums, long long& total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     long long incl = x;
@@ -135,7 +136,9 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* sums, long
     return before + incl - x;
 }
 
-__global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, float* weights, int recent,
+// kEvict: threads.
+template <int kEvict>
+__global__ void __launch_bounds__(kEvict, 1024 / kEvict) evict_kernel(const fa_cache c, float* weights, int recent,
                                                           int sinks, int room_keys) {
     pdl_begin();
     FA_DYNAMIC_SHARED(unsigned, keys);
@@ -170,18 +173,30 @@ __global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, floa
 
     if (top > 0) {
         for (int j = tid; j < 48; j += kEvict) sm.counts[j / 3][j % 3] = 0;
+        if (tid == 0) sm.listed = 0;
         if (cached)
             for (int j = tid; j < many; j += kEvict) keys[j] = key_of(w[sinks + j]);
         __syncthreads();
-        // ---- the lowest kept key: its bits from above, two at a time.  `need` of the keys
-        // that begin like it are kept.
+        // ---- the lowest kept key: its bits from above, two at a time.  `need` of the `group`
+        // keys that begin like it are kept.  Once few keys do, they alone are looked at.
         unsigned edge = 0;
-        int need = top;
+        int need = top, group = many;
+        bool listed = false;
+        unsigned* list = reinterpret_cast<unsigned*>(sm.hole);  // (not used yet)
         for (int step = 0; step < 16; ++step) {
             const int shift = 30 - 2 * step;
+            if (!listed && group <= 2 * kPairs && group < many / 2) {
+                for (int j = tid; j < many; j += kEvict) {
+                    const unsigned x = key(j);
+                    if ((x >> shift >> 2) == edge) list[atomicAdd(&sm.listed, 1)] = x;
+                }
+                __syncthreads();
+                listed = true;
+            }
             int more[3] = {0, 0, 0};
-            for (int j = tid; j < many; j += kEvict) {
-                const unsigned x = key(j) >> shift;
+            const int end = listed ? sm.listed : many;
+            for (int j = tid; j < end; j += kEvict) {
+                const unsigned x = (listed ? list[j] : key(j)) >> shift;
                 if ((x >> 2) != edge) continue;
                 const unsigned digit = x & 3u;
                 more[0] += digit >= 1;
@@ -193,60 +208,63 @@ __global__ void __launch_bounds__(kEvict, 2) evict_kernel(const fa_cache c, floa
                 if ((tid & 31) == 0 && all) atomicAdd(&sm.counts[step][d], all);
             }
             __syncthreads();
-            int digit = 0, above = sm.counts[step][0];
+            int digit = 0, from = group, above = sm.counts[step][0];  // keys of this digit on, of the next on
             for (int d = 1; d <= 3; ++d) {
                 if (sm.counts[step][d - 1] < need) break;
                 digit = d;
+                from = sm.counts[step][d - 1];
                 above = d < 3 ? sm.counts[step][d] : 0;
             }
             need -= above;
+            group = from - above;
             edge = edge * 4 + digit;
         }
+        const bool ranked = need < group;  // some ties are dropped: those of the highest places
         // ---- each thread's stretch (an odd number of keys: no two threads in one bank)
         const int stretch = ((many + kEvict - 1) / kEvict) | 1;
         const int j0 = (int)min((long long)many, (long long)tid * stretch), j1 = min(many, j0 + stretch);
         long long total;
         int ties = 0, low_ties = 0;  // of all, and of those before `top`
-        for (int j = j0; j < j1; ++j)
+        for (int j = j0; ranked && j < j1; ++j)
             if (key(j) == edge) {
                 ++ties;
                 low_ties += j < top;
             }
-        const int tie0 = (int)cta_scan(ties, sm.sums, total);
+        const int tie0 = ranked ? (int)cta_scan<kEvict>(ties, sm.sums, total) : 0;
         // visits the holes and the rows that move, in ascending order
         auto visit = [&](auto&& hole, auto&& from) {
             int tie = tie0;
             for (int j = j0; j < j1; ++j) {
                 if (j == top) tie = tie0 + low_ties;  // (a hole that has been filled may be a tie now)
                 const unsigned x = key(j);
-                bool stays = x > edge;
-                if (x == edge) stays = tie++ < need;
+                bool stays = x >= edge;
+                if (ranked && x == edge) stays = tie++ < need;
                 if (stays && j >= top) from(j);
                 if (!stays && j < top) hole(j);
             }
         };
         int holes = 0, froms = 0;
         visit([&](int) { ++holes; }, [&](int) { ++froms; });
-        const long long before = cta_scan(((long long)holes << 32) | froms, sm.sums, total);
+        const long long before = cta_scan<kEvict>(((long long)holes << 32) | froms, sm.sums, total);
         const int hole0 = (int)(before >> 32), from0 = (int)before, moves = (int)total;
         // The last moves first: a moved weight changes the key of a hole, where keys are not in
         // shared memory, and a stretch's holes are counted from below.
         for (int first = (moves - 1) / kPairs * kPairs; first >= 0 && moves > 0; first -= kPairs) {
             int h = hole0 - first, f = from0 - first;
             visit([&](int j) { if (h >= 0 && h < kPairs) sm.hole[h] = sinks + j; ++h; },
-                  [&](int j) { if (f >= 0 && f < kPairs) sm.from[f] = sinks + j; ++f; });
+                  [&](int j) { if (f >= 0 && f < kPairs) sm.hole[kPairs + f] = sinks + j; ++f; });
             __syncthreads();
             const int now = min(kPairs, moves - first);
             for (int m = row0; moving && m < now; m += kRun * rows) {
                 uint4 v[kRun];
 #pragma unroll
                 for (int r = 0; r < kRun; ++r)
-                    if (m + r * rows < now) v[r] = __ldcs(at(sm.from[m + r * rows]));
+                    if (m + r * rows < now) v[r] = __ldcs(at(sm.hole[kPairs + m + r * rows]));
 #pragma unroll
                 for (int r = 0; r < kRun; ++r)
                     if (m + r * rows < now) __stcs(at(sm.hole[m + r * rows]), v[r]);
             }
-            for (int m = tid; m < now; m += kEvict) w[sm.hole[m]] = w[sm.from[m]];
+            for (int m = tid; m < now; m += kEvict) w[sm.hole[m]] = w[sm.hole[kPairs + m]];
             __syncthreads();
         }
     }
@@ -300,10 +318,15 @@ extern "C" fa_status fa_cache_evict(const fa_cache* cache, const int* slots, con
     if (e != cudaSuccess) return FA_ERR_CUDA;
     const long long room = (long long)cache->max_pages * cache->page_size;
     const int keys = (int)(room < kMostKeys ? room : kMostKeys);
-    e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    // The search takes the longer the more places there are, the moves the longer the fewer
+    // CTAs an SM has: 512 threads for tables of more than 8192 places (15-16k of them: 147 us
+    // against 182 with 256 threads), 256 below (5120: 240 against 254; 2304: 264 against 290).
+    const bool many = room > 8192;
+    auto kern = many ? evict_kernel<512> : evict_kernel<256>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMostKeys * (int)sizeof(unsigned));
     if (e != cudaSuccess) return FA_ERR_CUDA;
-    e = launch_pdl(evict_kernel, dim3((unsigned)units), dim3(kEvict), (size_t)keys * sizeof(unsigned), strm,
+    e = launch_pdl(kern, dim3((unsigned)units), dim3(many ? 512 : 256), (size_t)keys * sizeof(unsigned), strm,
                    *cache, weights, recent, sinks, keys);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
