@@ -10,12 +10,12 @@
 //
 // The scores are computed transposed, S^T = K Q^T: a key is a lane of TMEM and a thread,
 // which walks the query columns and adds up in registers.  Nothing is exchanged between
-// threads, a key's sum is complete in one place, and no maximum is needed.  The line of
-// all sequences' and heads' key tiles is split into equal stretches of it, one a CTA, as
-// by the attention; nothing has to be joined.
+// threads, a key's sum is complete in one place, and no maximum is needed.  All sequences'
+// and heads' key tiles stand in one line, each as long as its sequence has Q tiles, and
+// every CTA takes an equal stretch; nothing has to be joined.
 //   warp 0       K tiles through a ring of stages, a TMA box a page (or 128 keys of one)
-//   warp 3       Q tiles and the LSE of their rows: once an item where one tile holds all
-//                rows, otherwise again for every pair of key tiles (from L2)
+//   warp 3       Q tiles and the LSE of their rows: once an item where shared memory holds
+//                them, otherwise again for every pair of key tiles (from L2)
 //   warp 1       MMA issuer: for every Q tile the scores of both key tiles of a pair
 //   warps 4..7, 8..11  the pair's first and second key tile: exponentials and sums
 // Each of the two has two buffers of scores in TMEM, so that the tensor core works on the
@@ -56,15 +56,19 @@ struct Params {
 
 // D: tile columns (96 runs on 128).  NQ: query rows of a tile; 64 above d = 128, where
 // two tiles of 128 beside a pair of key tiles do not fit, unless a group is larger.
-template <int D, int NQ>
+// MANY: some item may have several Q tiles.  Up to kQBufs of them stay in shared memory for
+// the whole item, and the keys run through two stages or more; with one Q tile the keys get
+// all the room, for they are the bound.
+template <int D, int NQ, bool MANY>
 struct Cfg {
     static constexpr int kCols = D / 64;
     static constexpr int kQBytes = NQ * D * 2, kStageBytes = kBN * D * 2;
-    static constexpr int kQBufs = NQ * D <= 128 * 192 ? 2 : 1;
-    static constexpr int kRoom = 232448 - 1024 - 4096 - kQBufs * kQBytes;
-    static constexpr int kMost = kRoom / kStageBytes;
+    static constexpr int kRoom = 232448 - 1024 - 5120;
+    static constexpr int kMostQ = (kRoom - 2 * kStageBytes) / kQBytes;
+    static constexpr int kQBufs = kMostQ > 4 && MANY ? 4 : (kMostQ > 2 && !MANY ? 2 : kMostQ);
+    static constexpr int kMost = (kRoom - kQBufs * kQBytes) / kStageBytes;
     static constexpr int kStages = kMost > 8 ? 8 : kMost;
-    static_assert(kStages >= 2, "the ring holds a pair of key tiles");
+    static_assert(kStages >= 2 && kQBufs >= 1, "a pair of key tiles and a Q tile");
 };
 
 // A stretch of one (sequence, head)'s key tiles.
@@ -75,9 +79,9 @@ struct Piece {
     int k0, tiles;       // key tiles [k0, k0 + tiles)
 };
 
-template <int D, int NQ>
+template <int D, int NQ, bool MANY>
 struct Smem {
-    using C = Cfg<D, NQ>;
+    using C = Cfg<D, NQ, MANY>;
     alignas(1024) uint8_t q[C::kQBufs][C::kQBytes];
     alignas(1024) uint8_t k[C::kStages][C::kStageBytes];
     alignas(16) float nl[C::kQBufs][NQ];  // -LSE log2 e of the Q tile's rows
@@ -89,6 +93,7 @@ struct Smem {
     Piece piece[2];
     long long sums[kThreads / 32];
     int start[3];        // this CTA's first item: sequence, head, key tile
+    long long item;      // its place in the line
     uint32_t tmem_base;
     int abort_flag, zero;
 };
@@ -194,11 +199,11 @@ __device__ __forceinline__ float weigh(uint32_t s_at, const float* nl, float c, 
     return sum;
 }
 
-template <int D, int DR, int NQ>
+template <int D, int DR, int NQ, bool MANY>
 __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_constant__ Params p) {
     pdl_trigger();
-    using C = Cfg<D, NQ>;
-    using SM = Smem<D, NQ>;
+    using C = Cfg<D, NQ, MANY>;
+    using SM = Smem<D, NQ, MANY>;
     constexpr int S = C::kStages, QB = C::kQBufs;
     static_assert(sizeof(SM) + 1024 <= 232448, "shared memory exceeds 227 KB");
     extern __shared__ uint8_t smem_raw[];
@@ -241,7 +246,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const uint32_t tmem = sm.tmem_base;
     pdl_wait();
 
-    // ---- the line of all key tiles, and where this CTA's stretch begins
+    // Q tiles of a sequence; up to QB of them are loaded once an item
+    auto q_tiles = [&](int n) { return (n + p.tile_tokens - 1) / p.tile_tokens; };
+
+    // ---- the line of all key tiles, each as long as its Q tiles are many, and where this
+    // CTA's stretch begins: it takes the tiles that begin within
     long long at, end;
     {
         const int chunk = (p.B + kThreads - 1) / kThreads;
@@ -251,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         for (int i = i0; i < i1; ++i) {
             const SeqInfo s = seq_info(p, i);
             bad |= s.bad;
-            mine += (long long)cdiv(s.len, kBN) * p.cache.heads;
+            mine += (long long)cdiv(s.len, kBN) * q_tiles(s.n) * p.cache.heads;
         }
         if (bad && blockIdx.x == 0) atomicOr(status, bad);
         long long incl = mine;
@@ -273,23 +282,21 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         if (at < end && at >= first && at < first + mine) {
             for (int i = i0; i < i1; ++i) {
                 const SeqInfo s = seq_info(p, i);
-                const int tiles = cdiv(s.len, kBN);
-                const long long all = (long long)tiles * p.cache.heads;
+                const int nq = q_tiles(s.n);
+                const long long item = (long long)cdiv(s.len, kBN) * nq, all = item * p.cache.heads;
                 if (at >= first + all) {
                     first += all;
                     continue;
                 }
                 sm.start[0] = i;
-                sm.start[1] = (int)((at - first) / tiles);
-                sm.start[2] = (int)((at - first) % tiles);
+                sm.start[1] = (int)((at - first) / item);
+                sm.item = first + sm.start[1] * item;
+                sm.start[2] = (int)((at - sm.item + nq - 1) / nq);  // (may be behind the item's last)
                 break;
             }
         }
         __syncthreads();
     }
-    // Q tiles of a piece; where there is one it is loaded once
-    auto q_tiles = [&](int n) { return (n + p.tile_tokens - 1) / p.tile_tokens; };
-
     if (warp == 0) {
         // ------------------------------------------------------------ pieces and K
         int it = 0, f = 0, b = sm.start[0], h = sm.start[1], k0 = sm.start[2];
@@ -297,15 +304,35 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const int box = lane / C::kCols, col = lane % C::kCols;
         bool ok = true;
         int place = -1, count = 0;  // ring place of this lane's turn among the last 32 loads
+        long long item = sm.item;   // the item's place in the line
         SeqInfo s = {};
-        if (at < end) s = seq_info(p, b);
+        bool any = at < end;
+        if (any) s = seq_info(p, b);
+        // the item behind this one
+        auto next_item = [&] {
+            item += (long long)cdiv(s.len, kBN) * q_tiles(s.n);
+            k0 = 0;
+            any = item < end;
+            if (any && ++h == p.cache.heads) {
+                h = 0;
+                do {
+                    if (++b >= p.B) {  // (cannot be: the line counts real tiles)
+                        any = false;
+                        break;
+                    }
+                    s = seq_info(p, b);
+                } while (s.len == 0);
+            }
+        };
+        if (any && k0 >= cdiv(s.len, kBN)) next_item();
         while (ok) {
             const int slot = it & 1;
             if (!(ok = warp_wait(smem_u32(&sm.piece_empty[slot]), ((it >> 1) & 1) ^ 1, stop, status)))
                 break;
             Piece x = {};
             x.h = -1;
-            if (at < end) {
+            const int nq = q_tiles(s.n);
+            if (any && item + (long long)k0 * nq < end) {
                 x.h = h;
                 x.tok0 = s.t0;
                 x.n = s.n;
@@ -313,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 x.len = s.len;
                 x.ctx = s.len - s.n;
                 x.k0 = k0;
-                x.tiles = (int)min((long long)(cdiv(s.len, kBN) - k0), end - at);
+                x.tiles = (int)min((long long)cdiv(s.len, kBN), (end - item + nq - 1) / nq) - k0;
             }
             if (lane == 0) {
                 sm.piece[slot] = x;
@@ -353,19 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 if ((count++ & 31) == lane) place = f;
                 ++f;
             }
-            at += x.tiles;
-            k0 = 0;
-            if (at < end && ++h == p.cache.heads) {
-                h = 0;
-                do {
-                    ++b;
-                    if (b >= p.B) {  // (cannot be: the line counts real tiles)
-                        at = end;
-                        break;
-                    }
-                    s = seq_info(p, b);
-                } while (s.len == 0);
-            }
+            next_item();
         }
         if (!ok) {  // never leave a TMA write in flight
             int last = place;
@@ -386,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
             ++it;
             if (x.h < 0) break;
-            const int nq = q_tiles(x.n), times = nq == 1 ? 1 : (x.tiles + 1) / 2;
+            const int nq = q_tiles(x.n), times = nq <= QB ? 1 : (x.tiles + 1) / 2;
             for (int pr = 0; pr < times && ok; ++pr)
                 for (int qt = 0; qt < nq && ok; ++qt, ++g) {
                     const int qs = g % QB;
@@ -440,17 +455,19 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             ++it;
             if (h < 0) break;
             const int nq = q_tiles(n), pairs = (tiles + 1) / 2;
+            const bool stay = nq <= QB;  // the item's Q tiles are loaded once
             for (int pr = 0; pr < pairs && ok; ++pr) {
                 const int both = min(2, tiles - 2 * pr);
                 for (int qt = 0; qt < nq && ok; ++qt) {
-                    if ((nq > 1 || pr == 0) && !wait(sm.q_full[g % QB], g / QB)) break;
+                    const int gq = stay ? g + qt : g;
+                    if ((!stay || pr == 0) && !wait(sm.q_full[gq % QB], gq / QB)) break;
                     for (int w = 0; w < both; ++w) {
                         const int fk = f + w, bf = cnt[w] & 1;
                         if (qt == 0 && !wait(sm.full[fk % S], fk / S)) break;
                         if (cnt[w] >= 2 && !wait(sm.s_free[w][bf], (cnt[w] - 2) >> 1)) break;
                         tc_fence_after();
                         const uint64_t da = make_sdesc(smem_u32(sm.k[fk % S]), 16, 1024);
-                        const uint64_t db = make_sdesc(smem_u32(sm.q[g % QB]), 16, 1024);
+                        const uint64_t db = make_sdesc(smem_u32(sm.q[gq % QB]), 16, 1024);
 #pragma unroll
                         for (int kk = 0; kk < DR / 16; ++kk)
                             warp_mma_ss(lead, tmem + (w * 2 + bf) * 128,
@@ -461,13 +478,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                         ++cnt[w];
                     }
                     if (!ok) break;
-                    if (nq > 1 || pr == pairs - 1) {
-                        warp_mma_commit(lead, smem_u32(&sm.q_empty[g % QB]));
-                        ++g;
-                    }
+                    if (!stay || pr == pairs - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty[gq % QB]));
+                    if (!stay) ++g;
                 }
                 f += both;
             }
+            if (stay) g += nq;
         }
         warp_mma_commit(lead, smem_u32(&sm.drain));
         mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
@@ -490,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             ++it;
             if (x.h < 0) break;
             const int nq = q_tiles(x.n), pairs = (x.tiles + 1) / 2;
+            const bool stay = nq <= QB;
             float* out = p.weights + ((long long)x.slot * p.cache.heads + x.h) *
                                          ((long long)p.cache.max_pages * p.cache.page_size);
             for (int pr = 0; pr < pairs && ok; ++pr) {
@@ -498,13 +515,13 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 const bool own = key0 + kBN > x.ctx;  // some keys are the call's own tokens
                 float sum = 0.f;
                 for (int qt = 0; qt < nq && ok; ++qt) {
-                    const int qs = g % QB;
+                    const int gq = stay ? g + qt : g, qs = gq % QB;
                     if (mine) {
                         if (!(ok = warp_wait(smem_u32(&sm.s_full[w][cnt & 1]), (cnt >> 1) & 1, stop, status)))
                             break;
                         tc_fence_after();
                         // (the scores are there, so the tile's LSE are; the barrier publishes them)
-                        if (!(ok = warp_wait(smem_u32(&sm.q_full[qs]), (g / QB) & 1, stop, status))) break;
+                        if (!(ok = warp_wait(smem_u32(&sm.q_full[qs]), (gq / QB) & 1, stop, status))) break;
                         const uint32_t s_at = tmem + lane_off + (w * 2 + (cnt & 1)) * 128;
                         const int tok0 = qt * p.tile_tokens;
                         const int ncols = min(p.tile_tokens, x.n - tok0) * p.group;
@@ -532,17 +549,18 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                         if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[w][cnt & 1]));
                         ++cnt;
                     }
-                    if (nq > 1 || pr == pairs - 1) {
+                    if (!stay || pr == pairs - 1) {
                         // (a phase of q_full may not pass unseen: the parity tells only the last)
-                        if (!mine && !(ok = warp_wait(smem_u32(&sm.q_full[qs]), (g / QB) & 1, stop, status)))
+                        if (!mine && !(ok = warp_wait(smem_u32(&sm.q_full[qs]), (gq / QB) & 1, stop, status)))
                             break;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[qs]));
-                        ++g;
                     }
+                    if (!stay) ++g;
                 }
                 if (ok && mine && key < x.len) atomicAdd(out + key, sum);
             }
+            if (stay) g += nq;
         }
     }
 
@@ -556,8 +574,9 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 
 template <int D, int DR, int NQ>
 cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
-    auto kern = weights_kernel<D, DR, NQ>;
-    constexpr size_t smem = sizeof(Smem<D, NQ>) + 1024;
+    const bool many = p.N > p.tile_tokens;
+    auto kern = many ? weights_kernel<D, DR, NQ, true> : weights_kernel<D, DR, NQ, false>;
+    const size_t smem = (many ? sizeof(Smem<D, NQ, true>) : sizeof(Smem<D, NQ, false>)) + 1024;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
