@@ -9,20 +9,23 @@
 // scores of d = 128 about 130 of its tensor core).
 //
 // The scores are computed transposed, S^T = K Q^T: a key is a lane of TMEM and a thread,
-// which walks the query columns and adds up in registers.  Nothing is exchanged between
-// threads, a key's sum is complete in one place, and no maximum is needed.  All sequences'
-// and heads' key tiles stand in one line, each as long as its sequence has Q tiles, and
-// every CTA takes an equal stretch; nothing has to be joined.
+// which walks the query columns and adds up in registers, and no maximum is needed.  All
+// sequences' and heads' key tiles stand in one line, each as long as its sequence has Q
+// tiles, and every CTA takes an equal stretch; nothing has to be joined.
 //   warp 0       K tiles through a ring of stages, a TMA box a page (or 128 keys of one)
-//   warp 3       Q tiles and the LSE of their rows: once an item where shared memory holds
-//                them, otherwise again for every pair of key tiles (from L2)
-//   warp 1       MMA issuer: for every Q tile the scores of both key tiles of a pair
-//   warps 4..7, 8..11  the pair's first and second key tile: exponentials and sums
-// Each of the two has two buffers of scores in TMEM, so that the tensor core works on the
-// next Q tile (or pair) meanwhile.
+//   warp 3       Q tiles and the LSE of their rows, for as long as a stretch of keys lasts
+//   warp 1       MMA issuer
+//   warps 4..7, 8..11  exponentials and sums
+// Where one Q tile of up to 128 rows holds all (decoding), the two warpgroups take alternate
+// key tiles, with two buffers of scores each, and the keys get all the shared memory.
+// Otherwise (MANY) Q tiles have 256 rows (128 above d = 128): a 128 x 128 x 16 MMA reads
+// 8 KB of operands in its 64 cycles, all that shared memory gives, and took 100.  Each
+// warpgroup then adds up half of the columns of every tile, and the halves meet in shared
+// memory.  More Q tiles than fit go through the stretch of keys in turns.
 //
-// A key's sum goes to memory as one addition of the whole call, so that results do not
-// vary from run to run; a slot that a call names twice gets both sums, in either order.
+// A key's sum goes to memory as one addition of the whole call (one a turn, by the same
+// thread), so that results do not vary from run to run; a slot that a call names twice gets
+// both sums, in either order.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,27 +57,30 @@ struct Params {
     float scale_log2;
 };
 
-// D: tile columns (96 runs on 128).  NQ: query rows of a tile; 64 above d = 128, where
-// two tiles of 128 beside a pair of key tiles do not fit, unless a group is larger.
-// MANY: some item may have several Q tiles.  Up to kQBufs of them stay in shared memory for
-// the whole item, and the keys run through two stages or more; with one Q tile the keys get
-// all the room, for they are the bound.
+// D: tile columns (96 runs on 128).  NQ: query rows of a tile.  One Q tile has 64 above
+// d = 128, to leave room for keys, unless a group is larger.
 template <int D, int NQ, bool MANY>
 struct Cfg {
     static constexpr int kCols = D / 64;
     static constexpr int kQBytes = NQ * D * 2, kStageBytes = kBN * D * 2;
-    static constexpr int kRoom = 232448 - 1024 - 5120;
+    static constexpr int kRoom = 232448 - 1024 - 8192;
     static constexpr int kMostQ = (kRoom - 2 * kStageBytes) / kQBytes;
-    static constexpr int kQBufs = kMostQ > 4 && MANY ? 4 : (kMostQ > 2 && !MANY ? 2 : kMostQ);
+    static constexpr int kQBufs = kMostQ > (MANY ? 4 : 2) ? (MANY ? 4 : 2) : kMostQ;
     static constexpr int kMost = (kRoom - kQBufs * kQBytes) / kStageBytes;
     static constexpr int kStages = kMost > 8 ? 8 : kMost;
-    static_assert(kStages >= 2 && kQBufs >= 1, "a pair of key tiles and a Q tile");
+    static constexpr int kBuffers = MANY ? 2 : 4;         // of scores
+    static constexpr int kSCols = MANY ? NQ : 128;        // from one to the next
+    static constexpr int kSpan = MANY ? NQ / 2 : NQ;      // columns of a warpgroup
+    static_assert(kStages >= 2 && kQBufs >= 1, "two key tiles and a Q tile");
+    static_assert(kBuffers * kSCols <= 512 && kSpan <= 128, "TMEM holds the scores");
 };
 
 // A stretch of one (sequence, head)'s key tiles.
 struct Piece {
     int h;               // < 0: none left
-    int tok0, n;         // tokens in the packed batch
+    int tok0, n;         // tokens in the packed batch, of this turn
+    int first;           // the first one's index in its sequence
+    int last;            // the item's last turn
     int slot, ctx, len;
     int k0, tiles;       // key tiles [k0, k0 + tiles)
 };
@@ -88,7 +94,11 @@ struct Smem {
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
     uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
     uint64_t piece_full[2], piece_empty[2];
-    uint64_t s_full[2][2], s_free[2][2];  // [key tile of the pair][buffer]
+    uint64_t s_full[C::kBuffers], s_free[C::kBuffers];
+    // MANY: the second warpgroup's sums, and that they are there.  It is less than four key
+    // tiles ahead: the scores that it takes up wait for both to have read those before.
+    uint64_t x_full[4];
+    float x[MANY ? 4 : 1][kBN];
     uint64_t drain;
     Piece piece[2];
     long long sums[kThreads / 32];
@@ -146,14 +156,14 @@ __device__ __forceinline__ SeqInfo seq_info(const Params& p, int i) {
     return s;
 }
 
-// The sum over columns [0, ncols) of 2^(s c + nl), s from TMEM.  MASK: column
+// The sum over columns [c0, ncols) of 2^(s c + nl), s from TMEM.  MASK: column
 // `col` counts only where see(col).
 template <bool MASK, typename See>
-__device__ __forceinline__ float weigh(uint32_t s_at, const float* nl, float c, int ncols, See&& see) {
+__device__ __forceinline__ float weigh(uint32_t s_at, const float* nl, float c, int c0, int ncols,
+                                       See&& see) {
     float sum = 0.f;
     const uint64_t cc = f2_pack(c, c);
-    int c0 = 0;
-    if (!MASK && ncols >= 64) {
+    if (!MASK && ncols >= c0 + 64) {
         uint64_t acc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = f2_pack(0.f, 0.f);
@@ -224,11 +234,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.piece_full[i]), 1);
             mbar_init(smem_u32(&sm.piece_empty[i]), 1 + 1 + 8);
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&sm.s_full[i][b]), 1);
-                mbar_init(smem_u32(&sm.s_free[i][b]), 4);
-            }
         }
+        for (int i = 0; i < C::kBuffers; ++i) {
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.s_free[i]), MANY ? 8 : 4);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sm.x_full[i]), 4);
         mbar_init(smem_u32(&sm.drain), 1);
         sm.abort_flag = sm.zero = 0;
         sm.start[0] = -1;
@@ -246,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     const uint32_t tmem = sm.tmem_base;
     pdl_wait();
 
-    // Q tiles of a sequence; up to QB of them are loaded once an item
+    // Q tiles of a sequence, or of a turn: QB at most
     auto q_tiles = [&](int n) { return (n + p.tile_tokens - 1) / p.tile_tokens; };
 
     // ---- the line of all key tiles, each as long as its Q tiles are many, and where this
@@ -305,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         bool ok = true;
         int place = -1, count = 0;  // ring place of this lane's turn among the last 32 loads
         long long item = sm.item;   // the item's place in the line
+        int turn = 0;               // token that the item's next turn begins with
         SeqInfo s = {};
         bool any = at < end;
         if (any) s = seq_info(p, b);
@@ -334,8 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             const int nq = q_tiles(s.n);
             if (any && item + (long long)k0 * nq < end) {
                 x.h = h;
-                x.tok0 = s.t0;
-                x.n = s.n;
+                x.first = turn;
+                x.tok0 = s.t0 + turn;
+                x.n = min(s.n - turn, QB * p.tile_tokens);
+                x.last = turn + x.n == s.n;
                 x.slot = s.slot;
                 x.len = s.len;
                 x.ctx = s.len - s.n;
@@ -380,7 +394,11 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 if ((count++ & 31) == lane) place = f;
                 ++f;
             }
-            next_item();
+            turn += x.n;
+            if (x.last) {
+                turn = 0;
+                next_item();
+            }
         }
         if (!ok) {  // never leave a TMA write in flight
             int last = place;
@@ -401,8 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
             ++it;
             if (x.h < 0) break;
-            const int nq = q_tiles(x.n), times = nq <= QB ? 1 : (x.tiles + 1) / 2;
-            for (int pr = 0; pr < times && ok; ++pr)
+            {
+                const int nq = q_tiles(x.n);
                 for (int qt = 0; qt < nq && ok; ++qt, ++g) {
                     const int qs = g % QB;
                     if (!(ok = warp_wait(smem_u32(&sm.q_empty[qs]), ((g / QB) & 1) ^ 1, stop, status)))
@@ -430,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar);
                 }
+            }
         }
         if (!ok && lane == 0)
             for (int i = 0; i < QB && i < g; ++i)
@@ -439,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         // ------------------------------------------------------------ MMA issuer
         constexpr uint32_t id = make_idesc_bf16(128, NQ, false, false);
         const uint32_t lead = elect_lead();
-        int it = 0, f = 0, g = 0, cnt[2] = {0, 0};
+        int it = 0, f = 0, g = 0, cnt[2] = {0, 0};  // (MANY: cnt[0])
         bool ok = true;
         auto wait = [&](uint64_t& bar, int parity) {
             return ok = ok && warp_wait(smem_u32(&bar), parity & 1, stop, status);
@@ -454,36 +473,29 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             __syncwarp();
             ++it;
             if (h < 0) break;
-            const int nq = q_tiles(n), pairs = (tiles + 1) / 2;
-            const bool stay = nq <= QB;  // the item's Q tiles are loaded once
-            for (int pr = 0; pr < pairs && ok; ++pr) {
-                const int both = min(2, tiles - 2 * pr);
+            const int nq = q_tiles(n);
+            for (int j = 0; j < tiles && ok; ++j, ++f) {
                 for (int qt = 0; qt < nq && ok; ++qt) {
-                    const int gq = stay ? g + qt : g;
-                    if ((!stay || pr == 0) && !wait(sm.q_full[gq % QB], gq / QB)) break;
-                    for (int w = 0; w < both; ++w) {
-                        const int fk = f + w, bf = cnt[w] & 1;
-                        if (qt == 0 && !wait(sm.full[fk % S], fk / S)) break;
-                        if (cnt[w] >= 2 && !wait(sm.s_free[w][bf], (cnt[w] - 2) >> 1)) break;
-                        tc_fence_after();
-                        const uint64_t da = make_sdesc(smem_u32(sm.k[fk % S]), 16, 1024);
-                        const uint64_t db = make_sdesc(smem_u32(sm.q[gq % QB]), 16, 1024);
+                    const int gq = g + qt, w = MANY ? 0 : j & 1;
+                    const int bf = (MANY ? 0 : 2 * w) + (cnt[w] & 1);
+                    if (j == 0 && !wait(sm.q_full[gq % QB], gq / QB)) break;
+                    if (qt == 0 && !wait(sm.full[f % S], f / S)) break;
+                    if (cnt[w] >= 2 && !wait(sm.s_free[bf], (cnt[w] - 2) >> 1)) break;
+                    tc_fence_after();
+                    const uint64_t da = make_sdesc(smem_u32(sm.k[f % S]), 16, 1024);
+                    const uint64_t db = make_sdesc(smem_u32(sm.q[gq % QB]), 16, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < DR / 16; ++kk)
-                            warp_mma_ss(lead, tmem + (w * 2 + bf) * 128,
-                                        sdesc_add(da, (kk >> 2) * (kBN * 128) + (kk & 3) * 32),
-                                        sdesc_add(db, (kk >> 2) * (NQ * 128) + (kk & 3) * 32), id, kk > 0);
-                        warp_mma_commit(lead, smem_u32(&sm.s_full[w][bf]));
-                        if (qt == nq - 1) warp_mma_commit(lead, smem_u32(&sm.empty[fk % S]));
-                        ++cnt[w];
-                    }
-                    if (!ok) break;
-                    if (!stay || pr == pairs - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty[gq % QB]));
-                    if (!stay) ++g;
+                    for (int kk = 0; kk < DR / 16; ++kk)
+                        warp_mma_ss(lead, tmem + bf * C::kSCols,
+                                    sdesc_add(da, (kk >> 2) * (kBN * 128) + (kk & 3) * 32),
+                                    sdesc_add(db, (kk >> 2) * (NQ * 128) + (kk & 3) * 32), id, kk > 0);
+                    warp_mma_commit(lead, smem_u32(&sm.s_full[bf]));
+                    if (qt == nq - 1) warp_mma_commit(lead, smem_u32(&sm.empty[f % S]));
+                    if (j == tiles - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty[gq % QB]));
+                    ++cnt[w];
                 }
-                f += both;
             }
-            if (stay) g += nq;
+            g += nq;
         }
         warp_mma_commit(lead, smem_u32(&sm.drain));
         mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
@@ -492,10 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
         const int w = (warp - 4) >> 2, q4 = warp & 3;
         const int row = q4 * 32 + lane;  // key of the tile
         const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
-        // col / group is (col * per_group) >> 16: the product is less than 128 / 65536 of a
+        // col / group is (col * per_group) >> 16: the product is less than 256 / 65536 of a
         // group too large
         const unsigned per_group = 65536u / p.group + 1;
-        int it = 0, g = 0, cnt = 0;
+        int it = 0, g = 0, cnt = 0, x_it = 0;  // x_it: key tiles whose halves have met
         bool ok = true;
         while (ok) {
             const int slot = it & 1;
@@ -505,62 +517,67 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             if (lane == 0) mbar_arrive(smem_u32(&sm.piece_empty[slot]));
             ++it;
             if (x.h < 0) break;
-            const int nq = q_tiles(x.n), pairs = (x.tiles + 1) / 2;
-            const bool stay = nq <= QB;
+            const int nq = q_tiles(x.n);
             float* out = p.weights + ((long long)x.slot * p.cache.heads + x.h) *
                                          ((long long)p.cache.max_pages * p.cache.page_size);
-            for (int pr = 0; pr < pairs && ok; ++pr) {
-                const bool mine = 2 * pr + w < x.tiles;
-                const int key0 = (x.k0 + 2 * pr + w) * kBN, key = key0 + row;
+            const int c0 = MANY ? w * C::kSpan : 0;  // this warpgroup's first column
+            for (int qt = 0; qt < nq && ok; ++qt)    // (the LSE that the scores go with)
+                ok = warp_wait(smem_u32(&sm.q_full[(g + qt) % QB]), ((g + qt) / QB) & 1, stop, status);
+            for (int j = MANY ? 0 : w; j < x.tiles && ok; j += MANY ? 1 : 2) {
+                const int key0 = (x.k0 + j) * kBN, key = key0 + row;
                 const bool own = key0 + kBN > x.ctx;  // some keys are the call's own tokens
                 float sum = 0.f;
-                for (int qt = 0; qt < nq && ok; ++qt) {
-                    const int gq = stay ? g + qt : g, qs = gq % QB;
-                    if (mine) {
-                        if (!(ok = warp_wait(smem_u32(&sm.s_full[w][cnt & 1]), (cnt >> 1) & 1, stop, status)))
-                            break;
-                        tc_fence_after();
-                        // (the scores are there, so the tile's LSE are; the barrier publishes them)
-                        if (!(ok = warp_wait(smem_u32(&sm.q_full[qs]), (gq / QB) & 1, stop, status))) break;
-                        const uint32_t s_at = tmem + lane_off + (w * 2 + (cnt & 1)) * 128;
-                        const int tok0 = qt * p.tile_tokens;
-                        const int ncols = min(p.tile_tokens, x.n - tok0) * p.group;
-                        if (!own) {
-                            sum += weigh<false>(s_at, sm.nl[qs], p.scale_log2, ncols, [](int) { return true; });
+                for (int qt = 0; qt < nq; ++qt, ++cnt) {
+                    const int qs = (g + qt) % QB, bf = (MANY ? 0 : 2 * w) + (cnt & 1);
+                    if (!(ok = warp_wait(smem_u32(&sm.s_full[bf]), (cnt >> 1) & 1, stop, status))) break;
+                    tc_fence_after();
+                    const uint32_t s_at = tmem + lane_off + bf * C::kSCols;
+                    const int tok0 = qt * p.tile_tokens;
+                    const int ncols = min(min(p.tile_tokens, x.n - tok0) * p.group, c0 + C::kSpan);
+                    const float* nl = sm.nl[qs];
+                    if (!own) {
+                        sum += weigh<false>(s_at, nl, p.scale_log2, c0, ncols, [](int) { return true; });
+                    } else {
+                        const int k = key - x.ctx;  // among the sequence's new tokens; < 0: the context
+                        if (!p.mask) {
+                            const int from = (k - x.first - tok0) * p.group;  // column that sees it
+                            sum += weigh<true>(s_at, nl, p.scale_log2, c0, ncols,
+                                               [&](int col) { return col >= from; });
                         } else {
-                            const int j = key - x.ctx;  // among the call's own tokens; < 0: the context
-                            if (!p.mask) {
-                                const int first = (j - tok0) * p.group;  // column that sees it
-                                sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols,
-                                                   [&](int col) { return col >= first; });
-                            } else {
-                                const unsigned long long* words = static_cast<const unsigned long long*>(p.mask) +
-                                                                  (size_t)(x.tok0 + tok0) * p.words + max(j, 0) / 64;
-                                const bool some = j < 64 * p.words;
-                                sum += weigh<true>(s_at, sm.nl[qs], p.scale_log2, ncols, [&](int col) {
-                                    if (j < 0) return true;
-                                    const int t = (int)(((unsigned)col * per_group) >> 16);
-                                    return some && ((words[(size_t)t * p.words] >> (j & 63)) & 1) != 0;
-                                });
-                            }
+                            const unsigned long long* words = static_cast<const unsigned long long*>(p.mask) +
+                                                              (size_t)(x.tok0 + tok0) * p.words + max(k, 0) / 64;
+                            const bool some = k < 64 * p.words;
+                            sum += weigh<true>(s_at, nl, p.scale_log2, c0, ncols, [&](int col) {
+                                if (k < 0) return true;
+                                const int t = (int)(((unsigned)col * per_group) >> 16);
+                                return some && ((words[(size_t)t * p.words] >> (k & 63)) & 1) != 0;
+                            });
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[w][cnt & 1]));
-                        ++cnt;
                     }
-                    if (!stay || pr == pairs - 1) {
-                        // (a phase of q_full may not pass unseen: the parity tells only the last)
-                        if (!mine && !(ok = warp_wait(smem_u32(&sm.q_full[qs]), (gq / QB) & 1, stop, status)))
-                            break;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[qs]));
-                    }
-                    if (!stay) ++g;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[bf]));
                 }
-                if (ok && mine && key < x.len) atomicAdd(out + key, sum);
+                if (!ok) break;
+                if constexpr (MANY) {
+                    const int xs = x_it & 3;
+                    if (w == 1) {
+                        sm.x[xs][row] = sum;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.x_full[xs]));
+                    } else {
+                        if (!(ok = warp_wait(smem_u32(&sm.x_full[xs]), (x_it >> 2) & 1, stop, status))) break;
+                        sum += sm.x[xs][row];
+                    }
+                    ++x_it;
+                    if (w == 1) continue;
+                }
+                if (key < x.len) atomicAdd(out + key, sum);
             }
-            if (stay) g += nq;
+            __syncwarp();
+            if (ok && lane == 0)
+                for (int qt = 0; qt < nq; ++qt) mbar_arrive(smem_u32(&sm.q_empty[(g + qt) % QB]));
+            g += nq;
         }
     }
 
@@ -572,11 +589,10 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
     }
 }
 
-template <int D, int DR, int NQ>
+template <int D, int DR, int NQ, bool MANY>
 cudaError_t launch(const Params& p, int ctas, cudaStream_t stream) {
-    const bool many = p.N > p.tile_tokens;
-    auto kern = many ? weights_kernel<D, DR, NQ, true> : weights_kernel<D, DR, NQ, false>;
-    const size_t smem = (many ? sizeof(Smem<D, NQ, true>) : sizeof(Smem<D, NQ, false>)) + 1024;
+    auto kern = weights_kernel<D, DR, NQ, MANY>;
+    constexpr size_t smem = sizeof(Smem<D, NQ, MANY>) + 1024;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(ctas), dim3(kThreads), smem, stream, p);
@@ -615,7 +631,9 @@ extern "C" fa_status fa_cache_weights(const fa_cache* cache, int layer, const in
     if (q_token_stride <= 0 || q_head_stride <= 0 || q_token_stride % 8 || q_head_stride % 8 ||
         q_token_stride >= (1LL << 38) || q_head_stride >= (1LL << 31))
         return FA_ERR_INVALID_ARG;
-    const int group = Hq / Hkv, nq = d > 128 && group <= 64 ? 64 : 128;
+    const int group = Hq / Hkv, few = d > 128 && group <= 64 ? 64 : 128;  // rows of the only Q tile
+    const bool many = (long long)N * group > few;
+    const int nq = !many ? few : (d > 128 ? 128 : 256);
     const int tokens = nq / group < N ? nq / group : N;
     TreeParams maps;
     std::memset(&maps, 0, sizeof(maps));
@@ -642,10 +660,18 @@ extern "C" fa_status fa_cache_weights(const fa_cache* cache, int layer, const in
     if (ctas <= 0) return FA_ERR_CUDA;
     cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (d == 64) e = launch<64, 64, 128>(p, ctas, strm);
-    else if (d == 96) e = launch<128, 96, 128>(p, ctas, strm);
-    else if (d == 128) e = launch<128, 128, 128>(p, ctas, strm);
-    else if (d == 192) e = nq == 64 ? launch<192, 192, 64>(p, ctas, strm) : launch<192, 192, 128>(p, ctas, strm);
-    else e = nq == 64 ? launch<256, 256, 64>(p, ctas, strm) : launch<256, 256, 128>(p, ctas, strm);
+    if (many) {
+        if (d == 64) e = launch<64, 64, 256, true>(p, ctas, strm);
+        else if (d == 96) e = launch<128, 96, 256, true>(p, ctas, strm);
+        else if (d == 128) e = launch<128, 128, 256, true>(p, ctas, strm);
+        else if (d == 192) e = launch<192, 192, 128, true>(p, ctas, strm);
+        else e = launch<256, 256, 128, true>(p, ctas, strm);
+    } else if (d == 64) e = launch<64, 64, 128, false>(p, ctas, strm);
+    else if (d == 96) e = launch<128, 96, 128, false>(p, ctas, strm);
+    else if (d == 128) e = launch<128, 128, 128, false>(p, ctas, strm);
+    else if (d == 192) e = few == 64 ? launch<192, 192, 64, false>(p, ctas, strm)
+                                     : launch<192, 192, 128, false>(p, ctas, strm);
+    else e = few == 64 ? launch<256, 256, 64, false>(p, ctas, strm)
+                       : launch<256, 256, 128, false>(p, ctas, strm);
     return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }

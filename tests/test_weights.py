@@ -226,3 +226,18 @@ def test_refused_on_the_device(change, bits):
     assert w[h.slots[0], :, :100].all()
     if change != "page":
         assert not w[h.slots[1]].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d,Hq,heads", [(64, 4, 1), (128, 8, 1), (128, 2, 2), (192, 6, 1), (256, 4, 2), (96, 128, 1)])
+def test_more_rows_than_stay_in_shared_memory(d, Hq, heads):
+    """Several turns over a stretch of keys, with and without a mask, beside a short sequence."""
+    counts, ctx = [700, 1], [300, 500]
+    h = Held([a + b for a, b in zip(counts, ctx)], heads, d, 64, seed=d)
+    q = queries(sum(counts), Hq, d)
+    lse, before, w = run(h, q, counts)
+    again = before.clone()
+    fa.cache_weights(q, lse, h.cache, h.layer, ints(h.slots), again, cu_seqlens=ints([0, 700, 701]), max_seqlen=700)
+    assert torch.equal(again, w)
+    rnd = random.Random(d)
+    run(h, q, counts, [sorted(rnd.sample(range(700), rnd.randint(0, 5))) for _ in range(700)] + [[0]])
