@@ -76,6 +76,9 @@ __device__ __forceinline__ int find_slot(const long long* prefix, int n, long lo
     return lo;
 }
 
+// FAR: with far units.  (A kernel of its own: their arithmetic, although not run, made the
+// forward's schedule of 1024 units 6 us longer.)
+template <bool FAR>
 __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     pdl_begin();
     extern __shared__ __align__(16) unsigned char sm[];
@@ -89,8 +92,8 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         const int nt = cdiv(a.N, a.rows);
         const int nt_aux = cdiv(a.N_aux, a.rows);
         const long long per_level = (long long)B * H;
-        const int chunks = a.sink_tiles ? cdiv(nt_aux, a.far_chunk) : 0;  // of one sequence
-        const long long far = (long long)B * chunks * a.sink_tiles * H;
+        const int chunks = FAR ? cdiv(nt_aux, a.far_chunk) : 0;  // of one sequence
+        const long long far = FAR ? (long long)B * chunks * a.sink_tiles * H : 0;
         const long long total = far + per_level * nt;
         if (tid == 0) {
             a.header->n_units = (int)(total <= a.max_units ? total : 0);
@@ -99,11 +102,12 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
             a.header->n_qtiles = B * nt_aux;
         }
         if (total > a.max_units) return;
-        for (long long u = tid; u < far; u += kSchedThreads) {
-            const FarEntry f = far_entry(a, (long long)B * chunks, u);
-            const int b = (int)(f.chunk / chunks), q = (int)(f.chunk % chunks);
-            a.units[u] = make_int2(b | kFarUnit, make_unit_y(q * a.sink_tiles + f.sink, f.head));
-        }
+        if constexpr (FAR)
+            for (long long u = tid; u < far; u += kSchedThreads) {
+                const FarEntry f = far_entry(a, (long long)B * chunks, u);
+                const int b = (int)(f.chunk / chunks), q = (int)(f.chunk % chunks);
+                a.units[u] = make_int2(b | kFarUnit, make_unit_y(q * a.sink_tiles + f.sink, f.head));
+            }
         for (long long u = tid; u < total - far; u += kSchedThreads) {
             int b, tile, h;
             if (a.order == kOrderSeqDesc) {
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     __syncthreads();
     const int maxnt = s_maxnt;
     long long far = 0, all_chunks = 0;  // far units, chunks of all sequences
-    if (a.sink_tiles) {
+    if constexpr (FAR) {
         if (tid == 0) {
             long long acc = 0;
             for (int b = 0; b < B; ++b) {
@@ -281,14 +285,15 @@ cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int 
     a.tile_off = want_tile_off ? reinterpret_cast<int*>(static_cast<char*>(workspace) + tile_off_off)
                                : nullptr;
     size_t smem = 0;
+    auto kern = sink_tiles ? sched_kernel<true> : sched_kernel<false>;
     if (cu_seqlens) {
         smem = sched_smem_bytes(B, cdiv(N, rows));
-        cudaError_t e = cudaFuncSetAttribute(sched_kernel,
+        cudaError_t e = cudaFuncSetAttribute(kern,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(sched_kernel, dim3(1), dim3(kSchedThreads), smem, stream, a);
+    return launch_pdl(kern, dim3(1), dim3(kSchedThreads), smem, stream, a);
 }
 
 }  // namespace fa
