@@ -403,6 +403,15 @@ def _check_window(window, sinks, causal):
     return _count("window", window, 1), _count("sinks", sinks, 0)
 
 
+def _workspace(workspace, size, device):
+    """The caller's workspace, if it holds size bytes, or one of this call's own."""
+    if workspace is None:
+        return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    if isinstance(workspace, torch.Tensor) and workspace.numel() * workspace.element_size() < size:
+        raise ValueError(f"the call needs a workspace of {size} bytes")
+    return workspace
+
+
 def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,
             out_dtype=torch.bfloat16, stream=None, workspace=None, cu_seqlens_k=None,
             max_seqlen_k=None, window=None, sinks=0):
@@ -418,8 +427,7 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None,
     o = torch.empty((Tq, Hq, d), dtype=out_dtype, device=q.device)
     lse = torch.empty((Hq, Tq), dtype=torch.float32, device=q.device)
     ws_bytes = fa_fwd_workspace_size(B, Hq, Nq, Tq)
-    ws = workspace if workspace is not None else torch.empty(
-        max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+    ws = _workspace(workspace, ws_bytes, q.device)
     if win:
         _check(fa_fwd_window(q, k, v, o, out_dtype, lse, B, Hq, Hkv, Nq, Tq, Nk, Tk, d, scale, *win,
                              cu_seqlens, cu_seqlens if cu_seqlens_k is None else cu_seqlens_k, ws,
@@ -454,8 +462,7 @@ def backward(q, k, v, o, dout, lse, causal=False, scale=None, cu_seqlens=None, m
         ws_bytes = fa_bwd_kv_workspace_size(B, Hq, Hkv, Nq, Tq, Nk, Tk, d)
     else:
         ws_bytes = fa_bwd_workspace_size(B, Hq, Hkv, Nq, Tq, d)
-    ws = workspace if workspace is not None else torch.empty(
-        max(ws_bytes, 16), dtype=torch.uint8, device=q.device)
+    ws = _workspace(workspace, ws_bytes, q.device)
     if win:
         cu_k = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
         _check(fa_bwd_window_preprocess(o, o.dtype, dout, D, ws, ws_bytes, B, Hq, Hkv, Nq, Tq, Nk,

@@ -411,6 +411,7 @@ struct Loader {
     int used, win, ids, nxt, key0, len, head;
 #ifdef FA_WINDOW
     int left, jump_key, jump_ids, jump_nxt;  // tiles before the window's stretch, and where it begins
+    int sinks, all_lo;                       // no row sees keys of [sinks, all_lo)
 #endif
     int place = -1;  // ring place of this lane's turn among the last 32 loads
     int count = 0;
@@ -439,6 +440,9 @@ struct Loader {
         ids = table_at(win + lane_id());
         nxt = table_at(win + 32 + lane_id());
 #ifdef FA_WINDOW
+        const Sight sight(p, x);
+        sinks = sight.sinks;
+        all_lo = sight.all_lo;
         left = x.nsk - x.k0;
         jump_key = x.lo * BN;
         if (left > 0) {
@@ -460,9 +464,16 @@ struct Loader {
         if (!warp_wait(smem_u32(&empty[st]), ((f / S) & 1) ^ 1, stop, status)) return false;
         const int have = max(0, min(boxes, (len - key0 + rows - 1) >> rows_shift));
         const uint32_t bar = smem_u32(&full[st]);
-        if (lane_id() == 0) mbar_arrive_expect_tx(bar, have * rows * 128 * COLS);
+        int gone0 = 0, gone1 = 0;
+#ifdef FA_WINDOW
+        // Boxes of keys that no row sees are left out (64 sequences, W = 4096, 16 sinks:
+        // 173.5 -> 170.7 us): their scores are replaced and their V zeroed, as behind the length.
+        gone0 = min(have, max(0, (sinks - key0 + rows - 1) >> rows_shift));
+        gone1 = max(gone0, min(have, (all_lo - key0) >> rows_shift));
+#endif
+        if (lane_id() == 0) mbar_arrive_expect_tx(bar, (have - (gone1 - gone0)) * rows * 128 * COLS);
         __syncwarp();
-        if (box < have) {
+        if (box < have && (box < gone0 || box >= gone1)) {
             // a page id out of range reads the fill value (zeros) and is reported
             int plane = -1;
             if (page >= 0 && page < p.cache.pages)

@@ -361,6 +361,24 @@ def test_boundaries_that_do_not_fit_are_reported():
 
 
 @pytest.mark.gpu
+def test_a_short_workspace_is_refused():
+    """One of the plain call does not hold the sinks' partials."""
+    q, k, v, do = make([300], [300], 2, 2, 64)
+    kw = dict(causal=True, batch=1, window=20, sinks=4)
+    o, lse = fa.forward(q, k, v, **kw)
+    plain = torch.zeros(fa.fa_bwd_workspace_size(1, 2, 2, 300, 300, 64), dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        fa.backward(q, k, v, o, do, lse, workspace=plain, **kw)
+    with pytest.raises(ValueError, match="workspace"):
+        fa.forward(q, k, v, workspace=plain[:100], **kw)
+    size = fa.fa_bwd_window_workspace_size(1, 2, 2, 300, 300, 300, 300, 64, 20, 4)
+    whole = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    a = fa.backward(q, k, v, o, do, lse, workspace=whole[:size], deterministic=True, **kw)
+    b = fa.backward(q, k, v, o, do, lse, deterministic=True, **kw)
+    assert all(torch.equal(x, y) for x, y in zip(a, b)) and whole[size:].eq(77).all()
+
+
+@pytest.mark.gpu
 def test_empty_sides():
     q, k, v, do = make([0], [50], 2, 2, 64)
     kw = dict(causal=True, window=7, sinks=1, cu_seqlens=ints([0, 0]), max_seqlen=0,
