@@ -57,6 +57,7 @@
 // columns [384,448) for d = 64.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -336,10 +337,11 @@ __device__ bool sem_wait(const int* sem, int target, const WsHeader* hdr) {
 // P^T for one 32-column chunk of a key row: exp2(S^T * c - LSE2) as packed
 // bf16 pairs; with MASK, columns outside [lo, hi) are zero.  nl2 holds the
 // chunk's LSE2 values negated and cc is c in both halves of an fp32 pair, so
-// the scaling is one packed FMA per two columns.
-template <bool MASK>
+// the scaling is one packed FMA per two columns.  FINE: ph gets the same as fp16 pairs.
+template <bool MASK, bool FINE = false>
 __device__ __forceinline__ void p_chunk(const uint32_t (&sv)[32], const float* nl2, uint64_t cc,
-                                           int lo, int hi, int xb, uint32_t (&pk)[16]) {
+                                           int lo, int hi, int xb, uint32_t (&pk)[16],
+                                           uint32_t* ph = nullptr) {
 #pragma unroll
     for (int e4 = 0; e4 < 8; ++e4) {
         const ulonglong2 lv = reinterpret_cast<const ulonglong2*>(nl2)[e4];
@@ -357,8 +359,26 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&sv)[32], const float* n
                 p1 = (y1 >= lo && y1 < hi) ? p1 : 0.f;
             }
             pk[e] = pack_bf16x2(p0, p1);
+            if constexpr (FINE) {
+                const __half2 h = __floats2half2_rn(p0, p1);
+                ph[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
         }
     }
+}
+
+// The two probabilities of dS: what the tensor core got of P, or, FINE, P itself to 11
+// bits.  (P <= 1 but for the rounding of LSE, and below 2^-14 an fp16 is off by 2^-25 at
+// most.)  The windowed backward takes the latter: dS and dQ, dK are then off by two roundings
+// to bf16, of dS and of the result, instead of three (in the 2-norm 0.0029 -> 0.0024; the
+// call 0.5-1% longer).
+template <bool FINE>
+__device__ __forceinline__ uint64_t p_pair(uint32_t pp) {
+    if constexpr (FINE) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pp));
+        return f2_pack(f.x, f.y);
+    }
+    return f2_pack(__uint_as_float(pp << 16), __uint_as_float(pp & 0xffff0000u));
 }
 
 // D: the tile layout (64 or 128 columns); DR: the head dimension in memory.
@@ -787,6 +807,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_fence_after();
                 const float* l2 = sm.lse2[st] + hc * 64;
                 uint32_t pk[2][16];
+                uint32_t ph[WIN ? 2 : 1][16];
                 {
                     uint32_t sv[2][32];  // this half's two 32-column loads, one wait
                     tmem_ld32(s_addr + hc * 64, sv[0]);
@@ -796,9 +817,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         const int xb = hc * 64 + h * 32;  // first query column of the chunk
                         if (full)
-                            p_chunk<false>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h]);
+                            p_chunk<false, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h], ph[WIN ? h : 0]);
                         else
-                            p_chunk<true>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h]);
+                            p_chunk<true, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h], ph[WIN ? h : 0]);
                         // into this half's own S^T columns, which this warp has
                         // already read (the other half's are still being read)
                         tmem_st16(s_addr + hc * 64 + h * 16, pk[h]);
@@ -829,9 +850,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                             for (int h2 = 0; h2 < 2; ++h2) {
                                 const int e = e4 * 2 + h2;
-                                const uint32_t pp = pk[h][e];
-                                const uint64_t pf = f2_pack(__uint_as_float(pp << 16),
-                                                            __uint_as_float(pp & 0xffff0000u));
+                                const uint64_t pf = p_pair<WIN>(WIN ? ph[WIN ? h : 0][e] : pk[h][e]);
                                 const uint64_t t = f2_add(f2_pack(__uint_as_float(dv[h][2 * e]),
                                                                   __uint_as_float(dv[h][2 * e + 1])),
                                                           h2 ? nd.y : nd.x);
@@ -1597,17 +1616,16 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         tmem_ld32(tmem + lane_off + qc * 32, sv);
                         tmem_ld32(tmem + lane_off + 128 + qc * 32, dv);
                         tmem_ld_wait();
-                        uint32_t pk[16];
+                        uint32_t pk[16], ph[16];
                         if (full)
-                            p_chunk<false>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk);
+                            p_chunk<false, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk, ph);
                         else
-                            p_chunk<true>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk);
+                            p_chunk<true, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk, ph);
                         uint32_t out[16];
                         const uint64_t* nd = reinterpret_cast<const uint64_t*>(sm.dd[rb] + qc * 32);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const uint64_t pf = f2_pack(__uint_as_float(pk[e] << 16),
-                                                        __uint_as_float(pk[e] & 0xffff0000u));
+                            const uint64_t pf = p_pair<WIN>(WIN ? ph[e] : pk[e]);
                             const uint64_t t = f2_add(
                                 f2_pack(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])), nd[e]);
                             float d0, d1;
