@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kEvict, 1024 / kEvict) evict_kernel(const fa_c
             for (int j = tid; j < many; j += kEvict) keys[j] = key_of(w[sinks + j]);
         __syncthreads();
         // ---- the lowest kept key: its bits from above, two at a time.  `need` of the `group`
-        // keys that begin like it are kept.  Once few keys do, they alone are looked at.
+        // keys that begin like it are kept.  Once few keys do, they alone are looked at, and
+        // once all of them are kept (soon, without ties) the other bits do not matter.
         unsigned edge = 0;
         int need = top, group = many;
         bool listed = false;
@@ -218,6 +219,10 @@ __global__ void __launch_bounds__(kEvict, 1024 / kEvict) evict_kernel(const fa_c
             need -= above;
             group = from - above;
             edge = edge * 4 + digit;
+            if (need == group) {
+                edge <<= shift;
+                break;
+            }
         }
         const bool ranked = need < group;  // some ties are dropped: those of the highest places
         // ---- each thread's stretch (an odd number of keys: no two threads in one bank)
