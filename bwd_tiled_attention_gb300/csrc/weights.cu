@@ -535,12 +535,16 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     const int tok0 = qt * p.tile_tokens;
                     const int ncols = min(min(p.tile_tokens, x.n - tok0) * p.group, c0 + C::kSpan);
                     const float* nl = sm.nl[qs];
-                    if (!own) {
+                    // without a mask most Q tiles see all keys of the tile, or none
+                    const int tok = x.first + tok0, k0 = key0 - x.ctx;  // first token, first key
+                    const bool none = !p.mask && k0 >= tok + min(p.tile_tokens, x.n - tok0);
+                    if (none) {
+                    } else if (!own || (!p.mask && k0 + kBN - 1 <= tok)) {
                         sum += weigh<false>(s_at, nl, p.scale_log2, c0, ncols, [](int) { return true; });
                     } else {
                         const int k = key - x.ctx;  // among the sequence's new tokens; < 0: the context
                         if (!p.mask) {
-                            const int from = (k - x.first - tok0) * p.group;  // column that sees it
+                            const int from = (k - tok) * p.group;  // column that sees it
                             sum += weigh<true>(s_at, nl, p.scale_log2, c0, ncols,
                                                [&](int col) { return col >= from; });
                         } else {
