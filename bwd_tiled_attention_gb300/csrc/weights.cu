@@ -479,8 +479,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     const int gq = g + qt, w = MANY ? 0 : j & 1;
                     const int bf = (MANY ? 0 : 2 * w) + (cnt[w] & 1);
                     if (j == 0 && !wait(sm.q_full[gq % QB], gq / QB)) break;
-                    if (qt == 0 && !wait(sm.full[f % S], f / S)) break;
-                    if (cnt[w] >= 2 && !wait(sm.s_free[bf], (cnt[w] - 2) >> 1)) break;
+                    // (a wait takes ~140 cycles even when nothing is missing: both are looked
+                    // up at once first.  Each is at most a phase behind.)
+                    const bool k_in = qt > 0 || mbar_test_wait(smem_u32(&sm.full[f % S]), (f / S) & 1);
+                    const bool s_in = cnt[w] < 2 || mbar_test_wait(smem_u32(&sm.s_free[bf]), ((cnt[w] - 2) >> 1) & 1);
+                    if (!__all_sync(0xffffffffu, k_in) && !wait(sm.full[f % S], f / S)) break;
+                    if (!__all_sync(0xffffffffu, s_in) && !wait(sm.s_free[bf], (cnt[w] - 2) >> 1)) break;
                     tc_fence_after();
                     const uint64_t da = make_sdesc(smem_u32(sm.k[f % S]), 16, 1024);
                     const uint64_t db = make_sdesc(smem_u32(sm.q[gq % QB]), 16, 1024);
