@@ -329,8 +329,9 @@ extern "C" fa_status fa_cache_evict(const fa_cache* cache, const int* slots, con
     const long long room = (long long)cache->max_pages * cache->page_size;
     const int keys = (int)(room < kMostKeys ? room : kMostKeys);
     // The search takes the longer the more places there are, the moves the longer the fewer
-    // CTAs an SM has: 512 threads for tables of more than 8192 places (15-16k of them: 147 us
-    // against 182 with 256 threads), 256 below (5120: 240 against 254; 2304: 264 against 290).
+    // CTAs an SM has: 512 threads for tables of more than 8192 places (16k: 140 us against
+    // 170 with 256 threads), 256 below (5120 places: 231 against 234; 2304: 253 against 270; 640: 226
+    // against 358).
     const bool many = room > 8192;
     auto kern = many ? evict_kernel<512> : evict_kernel<256>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
