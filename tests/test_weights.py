@@ -241,3 +241,27 @@ def test_more_rows_than_stay_in_shared_memory(d, Hq, heads):
     assert torch.equal(again, w)
     rnd = random.Random(d)
     run(h, q, counts, [sorted(rnd.sample(range(700), rnd.randint(0, 5))) for _ in range(700)] + [[0]])
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    """Layers, or sequences, that two streams work on at the same time: what each leaves alone."""
+    a, b = Held([3000, 900], 2, 128, 64, seed=1), Held([2500, 40], 2, 64, 16, seed=2)
+    work = []
+    for h, hq, n in ((a, 8, 1), (b, 4, 40)):
+        q = queries(2 * n, hq, h.k[0].shape[2])
+        _, lse = fa.tree_attention(q, h.cache, h.layer, ints(h.slots))
+        c = h.cache
+        w = torch.zeros(c.slots, c.heads, c.max_pages * c.page_size, device="cuda")
+        fa.cache_weights(q, lse, c, h.layer, ints(h.slots), w)
+        work.append((h, q, lse, ints(h.slots), w, torch.zeros_like(w), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for h, q, lse, s, _, mine, stream in work:
+            with torch.cuda.stream(stream):
+                mine.zero_()
+                fa.cache_weights(q, lse, h.cache, h.layer, s, mine)
+    torch.cuda.synchronize()
+    for h, _, _, _, want, mine, _ in work:
+        assert torch.equal(want, mine)
+        h.cache.check()

@@ -391,3 +391,39 @@ def test_empty_sides():
     o, lse = fa.forward(q, k, v, **kw)
     assert not o.any() and (lse == -math.inf).all()
     assert not fa.backward(q, k, v, o, do, lse, **kw)[0].any()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    work = []
+    for seed, lens, d, W, S in ((1, [2500, 300], 128, 200, 4), (2, [900] * 3, 64, 40, 130)):
+        q, k, v, do = make(lens, lens, 4, 2, d, seed)
+        kw = dict(causal=True, window=W, sinks=S, cu_seqlens=ends(lens), max_seqlen=max(lens))
+        o, lse = fa.forward(q, k, v, **kw)
+        work.append(((q, k, v, do), kw, (o, lse) + fa.backward(q, k, v, o, do, lse, deterministic=True, **kw),
+                     torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for (q, k, v, do), kw, want, stream in work:
+            with torch.cuda.stream(stream):
+                o, lse = fa.forward(q, k, v, **kw)
+                got.append(((o, lse) + fa.backward(q, k, v, o, do, lse, deterministic=True, **kw), want))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for a, b in got for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
+def test_more_queries_than_one_batch_index():
+    """Many short sequences: far units and partials of each, dense and packed."""
+    for lens in ([130] * 300, [1 + 7 * (i % 40) for i in range(400)]):
+        run(lens[:40], lens[:40], 2, 1, 64, 20, 3, det=True)
+        q, k, v, do = make(lens, lens, 2, 1, 64)
+        kw = dict(causal=True, window=20, sinks=3, **layout(lens, lens))
+        o, lse = fa.forward(q, k, v, **kw)
+        whole = fa.backward(q, k, v, o, do, lse, deterministic=True, check_status=True, **kw)
+        n = sum(lens[:40])
+        part = dict(causal=True, window=20, sinks=3, **layout(lens[:40], lens[:40]))
+        few = fa.backward(*(x[:n].contiguous() for x in (q, k, v, o, do)), lse[:, :n].contiguous(),
+                          deterministic=True, **part)
+        assert all(torch.equal(x[:n], y) for x, y in zip(whole, few))
