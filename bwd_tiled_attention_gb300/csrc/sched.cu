@@ -8,7 +8,7 @@
 // order (shortest processing time first).  Section 5.2: query heads that share
 // a key/value head are walked together.
 //
-// One CTA reads cu_seqlens (or the dense length N), ranks the sequences by
+// A CTA reads cu_seqlens (or the dense length N), ranks the sequences by
 // tile count (descending, ties by index), and writes the ordered list of work
 // units (sequence, tile, head) into the workspace, heads innermost.  The
 // attention kernels take units from that list through an atomic counter that
@@ -84,6 +84,9 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     const int tid = threadIdx.x;
     const int B = a.B, H = a.H;
+    // Every CTA ranks the sequences and writes its share of the list, the first one the rest.
+    const long long at = (long long)blockIdx.x * kSchedThreads + tid;
+    const long long step = (long long)gridDim.x * kSchedThreads;
     __shared__ long long s_total;
     __shared__ int s_maxnt, s_bad;
 
@@ -95,7 +98,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         const int chunks = FAR ? cdiv(nt_aux, a.far_chunk) : 0;  // of one sequence
         const long long far = FAR ? (long long)B * chunks * a.sink_tiles * H : 0;
         const long long total = far + per_level * nt;
-        if (tid == 0) {
+        if (at == 0) {
             a.header->n_units = (int)(total <= a.max_units ? total : 0);
             a.header->counter = 0;
             a.header->error = total <= a.max_units ? 0 : kErrSchedule;
@@ -103,12 +106,12 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         }
         if (total > a.max_units) return;
         if constexpr (FAR)
-            for (long long u = tid; u < far; u += kSchedThreads) {
+            for (long long u = at; u < far; u += step) {
                 const FarEntry f = far_entry(a, (long long)B * chunks, u);
                 const int b = (int)(f.chunk / chunks), q = (int)(f.chunk % chunks);
                 a.units[u] = make_int2(b | kFarUnit, make_unit_y(q * a.sink_tiles + f.sink, f.head));
             }
-        for (long long u = tid; u < total - far; u += kSchedThreads) {
+        for (long long u = at; u < total - far; u += step) {
             int b, tile, h;
             if (a.order == kOrderSeqDesc) {
                 b = (int)(u / ((long long)nt * H));
@@ -125,7 +128,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
             a.units[far + u] = make_int2(b, make_unit_y(tile, h));
         }
         if (a.tile_off)
-            for (int b = tid; b <= B; b += kSchedThreads) a.tile_off[b] = b * nt_aux;
+            for (long long b = at; b <= B; b += step) a.tile_off[b] = (int)b * nt_aux;
         return;
     }
 
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     }
     __syncthreads();
     if (s_bad) {
-        if (tid == 0) {
+        if (at == 0) {
             a.header->n_units = 0;
             a.header->counter = 0;
             a.header->error = kErrSchedule;
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         all_chunks = s_total;
         far = all_chunks * a.sink_tiles * H;
         if (far <= a.max_units)
-            for (long long u = tid; u < far; u += kSchedThreads) {
+            for (long long u = at; u < far; u += step) {
                 const FarEntry f = far_entry(a, all_chunks, u);
                 const int b = find_slot(prefix, B, f.chunk);
                 a.units[u] = make_int2(b | kFarUnit, make_unit_y((int)(f.chunk - prefix[b]) * a.sink_tiles +
@@ -221,12 +224,12 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     }
     __syncthreads();
     const long long total = far + s_total;
-    if (tid == 0) {
+    if (at == 0) {
         a.header->n_units = (int)(total <= a.max_units ? total : 0);
         a.header->counter = 0;
         a.header->error = total <= a.max_units ? 0 : kErrSchedule;
     }
-    if (a.tile_off && tid == 0) {
+    if (a.tile_off && at == 0) {
         int acc = 0;
         for (int b = 0; b < B; ++b) {
             a.tile_off[b] = acc;
@@ -234,11 +237,11 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         }
         a.tile_off[B] = acc;
         a.header->n_qtiles = acc;
-    } else if (tid == 0) {
+    } else if (at == 0) {
         a.header->n_qtiles = 0;
     }
     if (total > a.max_units || nslots == 0) return;
-    for (long long u = tid; u < total - far; u += kSchedThreads) {
+    for (long long u = at; u < total - far; u += step) {
         const int slot = find_slot(prefix, nslots, u);
         const long long r = u - prefix[slot];
         int b, tile;
@@ -293,7 +296,11 @@ cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int 
                                              (int)smem);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(kern, dim3(1), dim3(kSchedThreads), smem, stream, a);
+    // (16 packed sequences of 256-8192 tokens, 16 heads: one CTA -> up to 16, forward 1289.5 ->
+    // 1286.8 us, the backward's preparation 179.3 -> 175.0)
+    const int ctas = max_units <= 2 * kSchedThreads ? 1 : (int)(max_units < 16 * kSchedThreads
+                                                                    ? cdiv((int)max_units, kSchedThreads) : 16);
+    return launch_pdl(kern, dim3(ctas), dim3(kSchedThreads), smem, stream, a);
 }
 
 }  // namespace fa
