@@ -117,6 +117,10 @@ struct FwdSmem {
     // epilogue warps
     float ep_m[D > 128 ? kTile : 1], ep_l[D > 128 ? kTile : 1];
     uint64_t ep_full;
+#ifdef FA_WINDOW
+    // D <= 128: K and V tiles one by one in a ring of 2 kStages places, K(0) V(0) K(1) ...
+    uint64_t w_full[2 * FwdCfg<D>::kStages], w_empty[2 * FwdCfg<D>::kStages];
+#endif
 };
 
 // (the kernel aligns the dynamic shared memory to 1024 bytes itself)
@@ -350,6 +354,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         mbar_init(smem_u32(&sm.drain), 1);
         if constexpr (D > 128) mbar_init(smem_u32(&sm.ep_full), kTile);
+#ifdef FA_WINDOW
+        for (int s = 0; s < 2 * S; ++s) {
+            mbar_init(smem_u32(&sm.w_full[s]), 1);
+            mbar_init(smem_u32(&sm.w_empty[s]), 1);
+        }
+#endif
         sm.abort_flag = 0;
         sm.zero = 0;
         fence_barrier_init();
@@ -379,6 +389,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tma_prefetch_desc(&p.tm_v);
             int sched_it = 0, kv_it = 0, unit_it = 0;
             int k_it = 0, v_it = 0;  // D > 128: K tiles and V chunks loaded
+#ifdef FA_WINDOW
+            int w_it = 0;            // D <= 128: K and V tiles loaded
+#endif
             bool ok = true;
             while (ok) {
                 const int slot = sched_it & 1;
@@ -449,6 +462,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             ++v_it;
                         }
                     }
+                } else if constexpr (WIN) {
+#ifdef FA_WINDOW
+                    constexpr int R = 2 * S;
+                    static_assert(sizeof(sm.k) == S * Cfg::kTileBytes, "V's places follow K's");
+                    for (int i = 0; i < 2 * x.nkv && ok; ++i, ++w_it) {
+                        const int pl = w_it % R;
+                        if (!(ok = wait_or_abort(smem_u32(&sm.w_empty[pl]), ((w_it / R) & 1) ^ 1, abort_flag,
+                                                 hdr)))
+                            break;
+                        const uint32_t bar = smem_u32(&sm.w_full[pl]);
+                        const int tok = x.tk0 + x.template tile<WIN>(i >> 1) * kTile;
+                        mbar_arrive_expect_tx(bar, Cfg::kTileBytes);
+                        for (int c = 0; c < Cfg::kBoxes; ++c)
+                            tma_load_3d(smem_u32(sm.k[0]) + pl * Cfg::kTileBytes + c * 16384,
+                                        i & 1 ? &p.tm_v : &p.tm_k, bar, c * 64, x.g, tok);
+                    }
+#endif
                 } else {
                     for (int j = 0; j < x.nkv && ok; ++j) {
                         const int st = kv_it % S;
@@ -477,6 +507,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     mbar_wait(smem_u32(&sm.v_full[it % Cfg::kVSlots]), (it / Cfg::kVSlots) & 1, z);
                 }
             }
+#ifdef FA_WINDOW
+            for (int i = 0; i < 2 * S && i < w_it; ++i) {
+                const int it = w_it - 1 - i;
+                mbar_wait(smem_u32(&sm.w_full[it % (2 * S)]), (it / (2 * S)) & 1, z);
+            }
+#endif
             for (int i = 0; i < S && i < kv_it; ++i) {
                 const int it = kv_it - 1 - i, st = it % S, par = (it / S) & 1;
                 mbar_wait(smem_u32(&sm.k_full[st]), par, z);
@@ -487,6 +523,103 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         setmaxnreg_dec<72>();
+#ifdef FA_WINDOW
+        if constexpr (WIN && D <= 128) {
+            // A converged warp, of which one lane issues (descriptors and addresses stay in
+            // uniform registers), and each query tile's next scores right behind its own PV:
+            // S0 S1 | PV0 S0 PV1 S1 | PV0 S0 ..., so that one tile's MMAs run beside the
+            // other's softmax.
+            constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
+            constexpr uint32_t idPV = make_idesc_bf16(128, D, false, true);
+            constexpr int R = 2 * S;
+            const uint32_t lead = elect_lead(), ring = smem_u32(sm.k[0]);
+            int sched_it = 0, kv_it = 0, unit_it = 0;
+            int it[2] = {0, 0};  // PV MMAs issued per tile (= softmax iterations)
+            int ep[2] = {0, 0};  // units whose epilogue must finish before O_t is reused
+            bool ok = true;
+            auto wait = [&](uint64_t& bar, int parity) {
+                return ok = ok && warp_wait(smem_u32(&bar), parity & 1, abort_flag, hdr);
+            };
+            while (ok) {
+                const int slot = sched_it & 1;
+                if (!wait(sm.sched_full[slot], sched_it >> 1)) break;
+                const int2 unit = make_int2(__shfl_sync(0xffffffffu, sm.sched[slot].x, 0),
+                                            __shfl_sync(0xffffffffu, sm.sched[slot].y, 0));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                ++sched_it;
+                if (unit.x < 0) break;
+                const UnitGeom x = decode_unit<D, KV, WIN>(unit, p);
+                if (!wait(sm.q_full, unit_it)) break;
+                bool begun[2] = {false, false};  // tile t has had a PV in this unit
+                for (int j = -1; j < x.nkv && ok; ++j) {
+                    const int vp = 2 * (kv_it + j) + 1, kp = vp + 1;  // ring places of V(j), K(j + 1)
+                    bool v_in = false, k_in = false;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (!ok) break;
+                        if (j >= 0 && x.template active<true>(t, j)) {
+                            if (!wait(sm.p_full[t], it[t])) break;
+                            if (!v_in && !wait(sm.w_full[vp % R], vp / R)) break;
+                            v_in = true;
+                            if (!begun[t] && ep[t] > 0 && !wait(sm.o_free[t], ep[t] - 1)) break;
+                            tc_fence_after();
+                            const uint64_t db = make_sdesc(ring + vp % R * Cfg::kTileBytes, 16384, 1024);
+                            // keys [0, 64) of P_t, then [64, 128) once the softmax has them
+#pragma unroll
+                            for (int kk = 0; kk < kTile / 16; ++kk) {
+                                if (kk == kTile / 32) {
+                                    if (!wait(sm.p_hi[t], it[t])) break;
+                                    tc_fence_after();
+                                }
+                                warp_mma_ts(lead, tmem + 256 + t * 128, tmem + t * 128 + kk * 8,
+                                            sdesc_add(db, kk * 2048), idPV, (begun[t] || kk > 0) ? 1u : 0u);
+                            }
+                            if (!ok) break;
+                            warp_mma_commit(lead, smem_u32(&sm.o_done[t]));
+                            ++it[t];
+                            begun[t] = true;
+                        }
+                        if (j >= 0 && t == 1) {
+                            // (no phase passes unseen: a unit that sees no key has not waited)
+                            if (!v_in && !wait(sm.w_full[vp % R], vp / R)) break;
+                            warp_mma_commit(lead, smem_u32(&sm.w_empty[vp % R]));
+                        }
+                        if (j + 1 < x.nkv) {
+                            if (!k_in && !wait(sm.w_full[kp % R], kp / R)) break;
+                            k_in = true;
+                            if (x.template active<true>(t, j + 1)) {
+                                // S_t is free once the P written over it has been read
+                                if (it[t] > 0 && !wait(sm.o_done[t], it[t] - 1)) break;
+                                tc_fence_after();
+                                const uint64_t da = make_sdesc(smem_u32(sm.q[t]), 16, 1024);
+                                const uint64_t db = make_sdesc(ring + kp % R * Cfg::kTileBytes, 16, 1024);
+#pragma unroll
+                                for (int kk = 0; kk < DR / 16; ++kk) {  // (columns past DR are zero)
+                                    const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+                                    warp_mma_ss(lead, tmem + t * 128, sdesc_add(da, off), sdesc_add(db, off),
+                                                idS, kk > 0);
+                                }
+                                warp_mma_commit(lead, smem_u32(&sm.s_full[t]));
+                            }
+                            if (t == 1) {
+                                warp_mma_commit(lead, smem_u32(&sm.w_empty[kp % R]));
+                                // the unit's last S MMAs are issued: Q may be overwritten then
+                                if (j + 1 == x.nkv - 1) warp_mma_commit(lead, smem_u32(&sm.q_empty));
+                            }
+                        }
+                    }
+                }
+                if (!ok) break;
+                kv_it += x.nkv;
+                ++unit_it;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) ep[t] += x.n[t] > 0;
+            }
+            warp_mma_commit(lead, smem_u32(&sm.drain));
+            mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
+        } else
+#endif
         if (lane == 0) {
             constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
             constexpr uint32_t idPV = make_idesc_bf16(128, Cfg::kVChunk, false, true);
