@@ -383,6 +383,40 @@ __device__ __forceinline__ uint64_t p_pair(uint32_t pp) {
     return f2_pack(__uint_as_float(pp << 16), __uint_as_float(pp & 0xffff0000u));
 }
 
+// How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
+// issues, so that descriptors and addresses stay in uniform registers.
+template <bool WARP>
+struct Issuer {
+    uint32_t lead = WARP ? elect_lead() : 1;
+    __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) const {
+        if constexpr (WARP) warp_mma_ss(lead, d, a, b, id, acc);
+        else mma_ss(d, a, b, id, acc);
+    }
+    __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) const {
+        if constexpr (WARP) warp_mma_ts(lead, d, a, b, id, acc);
+        else mma_ts(d, a, b, id, acc);
+    }
+    __device__ __forceinline__ void commit(uint32_t bar) const {
+        if constexpr (WARP) warp_mma_commit(lead, bar);
+        else mma_commit(bar);
+    }
+    __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) const {
+        if constexpr (WARP) return make_sdesc(addr, lbo, sbo);
+        else return make_sdesc_here(addr, lbo, sbo);
+    }
+    __device__ __forceinline__ bool any(bool x) const { return WARP ? __any_sync(0xffffffffu, x) : x; }
+    __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) const {
+        const bool in = mbar_test_wait(bar, parity);
+        return WARP ? __all_sync(0xffffffffu, in) : in;
+    }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* flag, WsHeader* hdr) const {
+        return WARP ? warp_wait(bar, parity, flag, hdr) : wait_or_abort(bar, parity, flag, hdr);
+    }
+    __device__ __forceinline__ int2 uniform(int2 x) const {
+        return WARP ? make_int2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0)) : x;
+    }
+};
+
 // D: the tile layout (64 or 128 columns); DR: the head dimension in memory.
 // DR = 96 runs on 128-column tiles: the TMA boxes past column 96 read zeros.
 // S and dP contract over the first 96 columns only (6 MMAs of K = 16).  dV, dK
@@ -574,7 +608,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         setmaxnreg_dec<80>();
-        if (lane == 0) {
+        if (WIN || lane == 0) {
+            const Issuer<WIN> mx;
             constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
             constexpr uint32_t idKV = make_idesc_bf16(128, D, false, true);
             constexpr uint32_t idDQ = make_idesc_bf16(128, D, true, true);
@@ -585,37 +620,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             // S^T(c) = K_j Q_c^T into the S columns: needs Q_c loaded and dV(c-1),
             // the last reader of the previous P^T in those columns, complete.
             auto issue_s = [&](int c) -> bool {
-                if (!wait_or_abort(smem_u32(&sm.q_full[c & 1]), (c >> 1) & 1, abort_flag, hdr))
+                if (!mx.wait(smem_u32(&sm.q_full[c & 1]), (c >> 1) & 1, abort_flag, hdr))
                     return false;
-                if (c > 0 && !wait_or_abort(smem_u32(&sm.s_free), (c - 1) & 1, abort_flag, hdr))
+                if (c > 0 && !mx.wait(smem_u32(&sm.s_free), (c - 1) & 1, abort_flag, hdr))
                     return false;
                 tc_fence_after();
-                const uint64_t da = make_sdesc_here(kaddr, 16, 1024);
-                const uint64_t db = make_sdesc_here(smem_u32(sm.q[c & 1]), 16, 1024);
+                const uint64_t da = mx.sdesc(kaddr, 16, 1024);
+                const uint64_t db = mx.sdesc(smem_u32(sm.q[c & 1]), 16, 1024);
 #pragma unroll
                 for (int kk = 0; kk < DR / 16; ++kk) {
                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                    mma_ss(tmem + Cfg::kColS, sdesc_add(da, off), sdesc_add(db, off), idS, kk > 0);
+                    mx.ss(tmem + Cfg::kColS, sdesc_add(da, off), sdesc_add(db, off), idS, kk > 0);
                 }
-                mma_commit(smem_u32(&sm.s_full));
+                mx.commit(smem_u32(&sm.s_full));
                 return true;
             };
             while (ok) {
                 const int slot = sched_it & 1;
-                if (!(ok = wait_or_abort(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
+                if (!(ok = mx.wait(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
                                          abort_flag, hdr)))
                     break;
-                const int2 unit = sm.sched[slot];
-                mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                const int2 unit = mx.uniform(sm.sched[slot]);
+                if (!WIN || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                if (WIN) __syncwarp();
                 ++sched_it;
                 if (unit.x < 0) break;
                 const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
-                if (!(ok = wait_or_abort(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
+                if (!(ok = mx.wait(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
                 if ((!KV || x.ns > 0) && !(ok = issue_s(cnt))) break;
                 for (int s = 0; s < x.ns; ++s, ++cnt) {
                     const int st = cnt & 1;
                     const uint32_t qaddr = smem_u32(sm.q[st]);
-                    if (!(ok = wait_or_abort(smem_u32(&sm.do_full), cnt & 1, abort_flag, hdr))) break;
+                    if (!(ok = mx.wait(smem_u32(&sm.do_full), cnt & 1, abort_flag, hdr))) break;
                     // dP^T = V_j dO^T and dV_j += P^T dO in whichever order their inputs
                     // become ready (dP first when both are: it is on the critical path
                     // dQ drain -> dP -> dS -> dK/dQ).  For d = 128, dP reuses the TMEM
@@ -629,38 +665,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         while (!(dp_done && dv_done)) {
                             if (!dp_done &&
                                 (!Cfg::kDqAliasesDp || cnt == 0 ||
-                                 mbar_test_wait(smem_u32(&sm.dq_free), (cnt - 1) & 1))) {
+                                 mx.test(smem_u32(&sm.dq_free), (cnt - 1) & 1))) {
                                 tc_fence_after();
-                                const uint64_t da = make_sdesc_here(vaddr, 16, 1024);
-                                const uint64_t db = make_sdesc_here(doaddr, 16, 1024);
+                                const uint64_t da = mx.sdesc(vaddr, 16, 1024);
+                                const uint64_t db = mx.sdesc(doaddr, 16, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < DR / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                                    mma_ss(tmem + Cfg::kColDP, sdesc_add(da, off), sdesc_add(db, off),
+                                    mx.ss(tmem + Cfg::kColDP, sdesc_add(da, off), sdesc_add(db, off),
                                            idS, kk > 0);
                                 }
-                                mma_commit(smem_u32(&sm.dp_full));
+                                mx.commit(smem_u32(&sm.dp_full));
                                 dp_done = true;
                                 continue;
                             }
-                            if (!dv_done && mbar_test_wait(smem_u32(&sm.p_ready), cnt & 1) &&
+                            if (!dv_done && mx.test(smem_u32(&sm.p_ready), cnt & 1) &&
                                 (s != 0 || unit_it == 0 ||
-                                 mbar_test_wait(smem_u32(&sm.dkv_free), (unit_it - 1) & 1))) {
+                                 mx.test(smem_u32(&sm.dkv_free), (unit_it - 1) & 1))) {
                                 tc_fence_after();
                                 // P^T of query columns [64h, 64h+64) sits in TMEM
                                 // columns [64h, 64h+32)
-                                const uint64_t db = make_sdesc_here(doaddr, 16384, 1024);
+                                const uint64_t db = mx.sdesc(doaddr, 16384, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk)
-                                    mma_ts(tmem + Cfg::kColDV,
+                                    mx.ts(tmem + Cfg::kColDV,
                                            tmem + Cfg::kColS + (kk >> 2) * 64 + (kk & 3) * 8,
                                            sdesc_add(db, kk * 2048), idKV, (s > 0 || kk > 0) ? 1u : 0u);
-                                mma_commit(smem_u32(&sm.s_free));
+                                mx.commit(smem_u32(&sm.s_free));
                                 dv_done = true;
                                 continue;
                             }
                             if ((++spins & 63u) == 0 &&
-                                (*abort_flag || globaltimer() - t_start > kSpinLimitNs)) {
+                                mx.any(*abort_flag || globaltimer() - t_start > kSpinLimitNs)) {
                                 raise_abort(abort_flag, hdr, kErrTimeout);
                                 ok = false;
                                 break;
@@ -668,7 +704,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         }
                         if (!ok) break;
                     }
-                    mma_commit(smem_u32(&sm.do_empty));  // dO read by dP and dV
+                    mx.commit(smem_u32(&sm.do_empty));  // dO read by dP and dV
                     // Then this step's dQ, the next step's S and this step's dK, in
                     // that priority as their inputs arrive.  dQ is on the critical
                     // loop dQ -> drain -> dP(c+1) -> dS(c+1) -> dQ(c+1); S(c+1) needs
@@ -679,56 +715,56 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         const uint64_t t_start = globaltimer();
                         uint32_t spins = 0;  // the timer and abort flag every 64 polls
                         while (!(s_done && q_done && k_done)) {
-                            if (!q_done && mbar_test_wait(smem_u32(&sm.ds_ready), cnt & 1) &&
+                            if (!q_done && mx.test(smem_u32(&sm.ds_ready), cnt & 1) &&
                                 (Cfg::kDqAliasesDp || cnt == 0 ||
-                                 mbar_test_wait(smem_u32(&sm.dq_free), (cnt - 1) & 1))) {
+                                 mx.test(smem_u32(&sm.dq_free), (cnt - 1) & 1))) {
                                 tc_fence_after();
                                 // dQ = dS K_j  (A = dS^T in shared memory read as MN-major)
-                                const uint64_t da = make_sdesc_here(dsaddr, 16384, 1024);
-                                const uint64_t db = make_sdesc_here(kaddr, 16384, 1024);
+                                const uint64_t da = mx.sdesc(dsaddr, 16384, 1024);
+                                const uint64_t db = mx.sdesc(kaddr, 16384, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk)
-                                    mma_ss(tmem + Cfg::kColDQ, sdesc_add(da, kk * 2048),
+                                    mx.ss(tmem + Cfg::kColDQ, sdesc_add(da, kk * 2048),
                                            sdesc_add(db, kk * 2048), idDQ, kk > 0);
                                 // committed at once: a commit tracks every MMA issued before
                                 // it, and the drain must not wait for later ones
-                                mma_commit(smem_u32(&sm.dq_full));
+                                mx.commit(smem_u32(&sm.dq_full));
                                 q_done = true;
                                 continue;
                             }
                             if (!s_done &&
-                                mbar_test_wait(smem_u32(&sm.q_full[(cnt + 1) & 1]),
+                                mx.test(smem_u32(&sm.q_full[(cnt + 1) & 1]),
                                                ((cnt + 1) >> 1) & 1) &&
-                                mbar_test_wait(smem_u32(&sm.s_free), cnt & 1)) {
+                                mx.test(smem_u32(&sm.s_free), cnt & 1)) {
                                 tc_fence_after();
-                                const uint64_t da = make_sdesc_here(kaddr, 16, 1024);
-                                const uint64_t db = make_sdesc_here(smem_u32(sm.q[(cnt + 1) & 1]), 16, 1024);
+                                const uint64_t da = mx.sdesc(kaddr, 16, 1024);
+                                const uint64_t db = mx.sdesc(smem_u32(sm.q[(cnt + 1) & 1]), 16, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < DR / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                                    mma_ss(tmem + Cfg::kColS, sdesc_add(da, off), sdesc_add(db, off),
+                                    mx.ss(tmem + Cfg::kColS, sdesc_add(da, off), sdesc_add(db, off),
                                            idS, kk > 0);
                                 }
-                                mma_commit(smem_u32(&sm.s_full));
+                                mx.commit(smem_u32(&sm.s_full));
                                 s_done = true;
                                 continue;
                             }
                             if (!k_done && q_done) {
                                 // dK_j += dS^T Q  (A = dS^T in shared memory, K-major)
-                                const uint64_t da = make_sdesc_here(dsaddr, 16, 1024);
-                                const uint64_t db = make_sdesc_here(qaddr, 16384, 1024);
+                                const uint64_t da = mx.sdesc(dsaddr, 16, 1024);
+                                const uint64_t db = mx.sdesc(qaddr, 16384, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                                    mma_ss(tmem + Cfg::kColDK, sdesc_add(da, off), sdesc_add(db, kk * 2048),
+                                    mx.ss(tmem + Cfg::kColDK, sdesc_add(da, off), sdesc_add(db, kk * 2048),
                                            idKV, (s > 0 || kk > 0) ? 1u : 0u);
                                 }
-                                mma_commit(smem_u32(&sm.q_empty[st]));   // Q(c) read by S(c), dK
+                                mx.commit(smem_u32(&sm.q_empty[st]));   // Q(c) read by S(c), dK
                                 k_done = true;
                                 continue;
                             }
                             if ((++spins & 63u) == 0 &&
-                                (*abort_flag || globaltimer() - t_start > kSpinLimitNs)) {
+                                mx.any(*abort_flag || globaltimer() - t_start > kSpinLimitNs)) {
                                 raise_abort(abort_flag, hdr, kErrTimeout);
                                 ok = false;
                                 break;
@@ -744,15 +780,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     // two such units in a row could put dkv_full two phases ahead of
                     // the epilogue warps, which parity cannot tell apart.
                     if (x.ns == 0 && unit_it > 0 &&
-                        !(ok = wait_or_abort(smem_u32(&sm.dkv_free), (unit_it - 1) & 1, abort_flag,
+                        !(ok = mx.wait(smem_u32(&sm.dkv_free), (unit_it - 1) & 1, abort_flag,
                                              hdr)))
                         break;
                 }
-                mma_commit(smem_u32(&sm.dkv_full));
-                mma_commit(smem_u32(&sm.kv_empty));
+                mx.commit(smem_u32(&sm.dkv_full));
+                mx.commit(smem_u32(&sm.kv_empty));
                 ++unit_it;
             }
-            mma_commit(smem_u32(&sm.drain));
+            mx.commit(smem_u32(&sm.drain));
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         }
     } else if (warp >= 4 && warp < 12) {
