@@ -64,6 +64,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "issue.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fa {
@@ -273,24 +274,6 @@ __device__ __forceinline__ int dq_rank(const BUnit& x, const BwdParams& p, int i
     return before + jmax - x.j;
 }
 
-__device__ __forceinline__ void raise_abort(volatile int* flag, WsHeader* hdr, int code) {
-    *flag = 1;
-    atomicOr(&hdr->error, code);
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* flag,
-                                              WsHeader* hdr) {
-    if (mbar_wait(bar, parity, flag)) return true;
-    raise_abort(flag, hdr, kErrTimeout);
-    return false;
-}
-
-// Whole-warp wait: every lane leaves with the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
-                                          WsHeader* hdr) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, flag, hdr));
-}
-
 // Wait shared by the four warps of the dQ/epilogue warpgroup: they meet on
 // named barrier 1 (deterministic mode), so all 128 threads must take the same
 // branch after every wait.
@@ -382,40 +365,6 @@ __device__ __forceinline__ uint64_t p_pair(uint32_t pp) {
     }
     return f2_pack(__uint_as_float(pp << 16), __uint_as_float(pp & 0xffff0000u));
 }
-
-// How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
-// issues, so that descriptors and addresses stay in uniform registers.
-template <bool WARP>
-struct Issuer {
-    uint32_t lead = WARP ? elect_lead() : 1;
-    __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) const {
-        if constexpr (WARP) warp_mma_ss(lead, d, a, b, id, acc);
-        else mma_ss(d, a, b, id, acc);
-    }
-    __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) const {
-        if constexpr (WARP) warp_mma_ts(lead, d, a, b, id, acc);
-        else mma_ts(d, a, b, id, acc);
-    }
-    __device__ __forceinline__ void commit(uint32_t bar) const {
-        if constexpr (WARP) warp_mma_commit(lead, bar);
-        else mma_commit(bar);
-    }
-    __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) const {
-        if constexpr (WARP) return make_sdesc(addr, lbo, sbo);
-        else return make_sdesc_here(addr, lbo, sbo);
-    }
-    __device__ __forceinline__ bool any(bool x) const { return WARP ? __any_sync(0xffffffffu, x) : x; }
-    __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) const {
-        const bool in = mbar_test_wait(bar, parity);
-        return WARP ? __all_sync(0xffffffffu, in) : in;
-    }
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* flag, WsHeader* hdr) const {
-        return WARP ? warp_wait(bar, parity, flag, hdr) : wait_or_abort(bar, parity, flag, hdr);
-    }
-    __device__ __forceinline__ int2 uniform(int2 x) const {
-        return WARP ? make_int2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0)) : x;
-    }
-};
 
 // D: the tile layout (64 or 128 columns); DR: the head dimension in memory.
 // DR = 96 runs on 128-column tiles: the TMA boxes past column 96 read zeros.
@@ -638,7 +587,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             while (ok) {
                 const int slot = sched_it & 1;
                 if (!(ok = mx.wait(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
-                                         abort_flag, hdr)))
+                                   abort_flag, hdr)))
                     break;
                 const int2 unit = mx.uniform(sm.sched[slot]);
                 if (!WIN || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
@@ -673,7 +622,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 for (int kk = 0; kk < DR / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                                     mx.ss(tmem + Cfg::kColDP, sdesc_add(da, off), sdesc_add(db, off),
-                                           idS, kk > 0);
+                                          idS, kk > 0);
                                 }
                                 mx.commit(smem_u32(&sm.dp_full));
                                 dp_done = true;
@@ -689,8 +638,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk)
                                     mx.ts(tmem + Cfg::kColDV,
-                                           tmem + Cfg::kColS + (kk >> 2) * 64 + (kk & 3) * 8,
-                                           sdesc_add(db, kk * 2048), idKV, (s > 0 || kk > 0) ? 1u : 0u);
+                                          tmem + Cfg::kColS + (kk >> 2) * 64 + (kk & 3) * 8,
+                                          sdesc_add(db, kk * 2048), idKV, (s > 0 || kk > 0) ? 1u : 0u);
                                 mx.commit(smem_u32(&sm.s_free));
                                 dv_done = true;
                                 continue;
@@ -725,7 +674,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk)
                                     mx.ss(tmem + Cfg::kColDQ, sdesc_add(da, kk * 2048),
-                                           sdesc_add(db, kk * 2048), idDQ, kk > 0);
+                                          sdesc_add(db, kk * 2048), idDQ, kk > 0);
                                 // committed at once: a commit tracks every MMA issued before
                                 // it, and the drain must not wait for later ones
                                 mx.commit(smem_u32(&sm.dq_full));
@@ -734,7 +683,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                             }
                             if (!s_done &&
                                 mx.test(smem_u32(&sm.q_full[(cnt + 1) & 1]),
-                                               ((cnt + 1) >> 1) & 1) &&
+                                        ((cnt + 1) >> 1) & 1) &&
                                 mx.test(smem_u32(&sm.s_free), cnt & 1)) {
                                 tc_fence_after();
                                 const uint64_t da = mx.sdesc(kaddr, 16, 1024);
@@ -743,7 +692,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 for (int kk = 0; kk < DR / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                                     mx.ss(tmem + Cfg::kColS, sdesc_add(da, off), sdesc_add(db, off),
-                                           idS, kk > 0);
+                                          idS, kk > 0);
                                 }
                                 mx.commit(smem_u32(&sm.s_full));
                                 s_done = true;
@@ -757,7 +706,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                 for (int kk = 0; kk < kTile / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
                                     mx.ss(tmem + Cfg::kColDK, sdesc_add(da, off), sdesc_add(db, kk * 2048),
-                                           idKV, (s > 0 || kk > 0) ? 1u : 0u);
+                                          idKV, (s > 0 || kk > 0) ? 1u : 0u);
                                 }
                                 mx.commit(smem_u32(&sm.q_empty[st]));   // Q(c) read by S(c), dK
                                 k_done = true;
@@ -781,7 +730,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     // the epilogue warps, which parity cannot tell apart.
                     if (x.ns == 0 && unit_it > 0 &&
                         !(ok = mx.wait(smem_u32(&sm.dkv_free), (unit_it - 1) & 1, abort_flag,
-                                             hdr)))
+                                       hdr)))
                         break;
                 }
                 mx.commit(smem_u32(&sm.dkv_full));
@@ -1320,7 +1269,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (WIN || lane == 0) {
+            const Issuer<WIN> mx;
             int sched_it = 0, unit_it = 0, g = 0;  // g: chunks consumed, over all units
             int c1 = 0, c2 = 0;                    // pass-1 / pass-2 steps, over all units
             // TMEM [0, 128) and [128, 256).  The dK/dV columns need none: the
@@ -1331,7 +1281,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             auto settle = [&](Pending& pd) -> bool {
                 if (!pd.set) return true;
                 pd.set = false;
-                if (!wait_or_abort(pd.bar, pd.parity, abort_flag, hdr)) return false;
+                if (!mx.wait(pd.bar, pd.parity, abort_flag, hdr)) return false;
                 tc_fence_after();
                 return true;
             };
@@ -1345,12 +1295,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             // next chunk of the ring: its shared-memory address once landed, or 0
             auto acquire = [&](int ahead = 0) -> uint32_t {
                 const int ga = g + ahead, slot = ga % kSlots;
-                if (!wait_or_abort(smem_u32(&sm.slot_full[slot]), (ga / kSlots) & 1, abort_flag, hdr))
+                if (!mx.wait(smem_u32(&sm.slot_full[slot]), (ga / kSlots) & 1, abort_flag, hdr))
                     return 0u;
                 tc_fence_after();
                 return smem_u32(sm.ring[slot]);
             };
-            auto release = [&]() { mma_commit(smem_u32(&sm.slot_free[g++ % kSlots])); };
+            auto release = [&]() { mx.commit(smem_u32(&sm.slot_free[g++ % kSlots])); };
             // dV / dK take the chunks' d columns as N: two chunks at once (N = 128)
             // when they sit in adjacent slots (a group of C chunks starts at a
             // multiple of C in the ring, so only a group's last chunk at d = 192
@@ -1379,27 +1329,28 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 for (int cc = 0; cc < C; ++cc) {
                     const uint32_t a = acquire();
                     if (!a) return false;
-                    const uint64_t da = make_sdesc_here(abase + cc * 16384, 16, 1024);
-                    const uint64_t db = make_sdesc_here(a, 16, 1024);
+                    const uint64_t da = mx.sdesc(abase + cc * 16384, 16, 1024);
+                    const uint64_t db = mx.sdesc(a, 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + col, sdesc_add(da, kk * 32), sdesc_add(db, kk * 32), idS,
-                               (cc | kk) > 0);
+                        mx.ss(tmem + col, sdesc_add(da, kk * 32), sdesc_add(db, kk * 32), idS,
+                              (cc | kk) > 0);
                     release();
                 }
                 return true;
             };
             while (ok) {
                 const int slot = sched_it & 1;
-                if (!(ok = wait_or_abort(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
-                                         abort_flag, hdr)))
+                if (!(ok = mx.wait(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
+                                   abort_flag, hdr)))
                     break;
-                const int2 unit = sm.sched[slot];
-                mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                const int2 unit = mx.uniform(sm.sched[slot]);
+                if (!WIN || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                if (WIN) __syncwarp();
                 ++sched_it;
                 if (unit.x < 0) break;
                 const BUnit x = decode_bunit<KV, false, WIN>(unit, p);
-                if (!(ok = wait_or_abort(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
+                if (!(ok = mx.wait(smem_u32(&sm.kv_full), unit_it & 1, abort_flag, hdr))) break;
                 tc_fence_after();
                 ++unit_it;
                 // ---- pass 1: S(0), then S(s), dV(s - 1), then dV(n - 1)
@@ -1408,27 +1359,27 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         const int c = c1 + s, b = c & 1;
                         if (!(ok = settle(pend_s[b]))) break;
                         if (!(ok = issue_s((uint32_t)b * 128, kaddr))) break;
-                        mma_commit(smem_u32(&sm.s_full[b]));
+                        mx.commit(smem_u32(&sm.s_full[b]));
                     }
                     if (s > 0) {
                         const int c = c1 + s - 1, b = c & 1;
-                        if (!(ok = wait_or_abort(smem_u32(&sm.p_ready[b]), (c >> 1) & 1, abort_flag, hdr)))
+                        if (!(ok = mx.wait(smem_u32(&sm.p_ready[b]), (c >> 1) & 1, abort_flag, hdr)))
                             break;
                         tc_fence_after();
                         for (int cc = 0; cc < C && ok;) {
                             const int n = acc_chunks(cc, [&](uint32_t col, uint32_t a, bool n128) {
-                                const uint64_t db = make_sdesc_here(a, 16384, 1024);
+                                const uint64_t db = mx.sdesc(a, 16384, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < kTile / 16; ++kk)
-                                    mma_ts(tmem + col, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                                           sdesc_add(db, kk * 2048), n128 ? idN2 : idN,
-                                           (s > 1 || kk > 0) ? 1u : 0u);
+                                    mx.ts(tmem + col, tmem + b * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                          sdesc_add(db, kk * 2048), n128 ? idN2 : idN,
+                                          (s > 1 || kk > 0) ? 1u : 0u);
                             });
                             ok = n > 0;
                             cc += n;
                         }
                         if (!ok) break;
-                        mma_commit(smem_u32(&sm.s_free[b]));
+                        mx.commit(smem_u32(&sm.s_free[b]));
                         ok = expect(pend_s[b], smem_u32(&sm.s_free[b]), (c >> 1) & 1);
                     }
                 }
@@ -1437,7 +1388,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                 // only units with query tiles signal their accumulators: each such
                 // commit follows an arrival of the compute warps on the same unit,
                 // so it can never run two phases ahead of their wait
-                if (x.ns > 0) mma_commit(smem_u32(&sm.dv_full));
+                if (x.ns > 0) mx.commit(smem_u32(&sm.dv_full));
                 // ---- pass 2
                 for (int s = 0; s < x.ns && ok; ++s) {
                     const int c = c2 + s;
@@ -1445,19 +1396,19 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (!(ok = issue_s(0, kaddr))) break;
                     if (!(ok = settle(pend_s[1]))) break;
                     if (!(ok = issue_s(128, vaddr))) break;  // dP^T = V dO^T (the dO chunks)
-                    mma_commit(smem_u32(&sm.sdp_full));
-                    if (!(ok = wait_or_abort(smem_u32(&sm.ds_ready), c & 1, abort_flag, hdr))) break;
+                    mx.commit(smem_u32(&sm.sdp_full));
+                    if (!(ok = mx.wait(smem_u32(&sm.ds_ready), c & 1, abort_flag, hdr))) break;
                     tc_fence_after();
                     // dK += dS^T Q_i, 64 columns of Q per chunk (A = dS^T, K-major)
                     for (int cc = 0; cc < C && ok;) {
                         const int n = acc_chunks(cc, [&](uint32_t col, uint32_t a, bool n128) {
-                            const uint64_t da = make_sdesc_here(dsaddr, 16, 1024);
-                            const uint64_t db = make_sdesc_here(a, 16384, 1024);
+                            const uint64_t da = mx.sdesc(dsaddr, 16, 1024);
+                            const uint64_t db = mx.sdesc(a, 16384, 1024);
 #pragma unroll
                             for (int kk = 0; kk < kTile / 16; ++kk)
-                                mma_ss(tmem + col, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
-                                       sdesc_add(db, kk * 2048), n128 ? idN2 : idN,
-                                       (s > 0 || kk > 0) ? 1u : 0u);
+                                mx.ss(tmem + col, sdesc_add(da, (kk >> 2) * 16384 + (kk & 3) * 32),
+                                      sdesc_add(db, kk * 2048), n128 ? idN2 : idN,
+                                      (s > 0 || kk > 0) ? 1u : 0u);
                         });
                         ok = n > 0;
                         cc += n;
@@ -1465,24 +1416,24 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     if (!ok) break;
                     // dQ = dS K_j into [0, D): S^T and dP^T have been read
                     {
-                        const uint64_t da = make_sdesc_here(dsaddr, 16384, 1024);
-                        const uint64_t db = make_sdesc_here(kaddr, 16384, 1024);
+                        const uint64_t da = mx.sdesc(dsaddr, 16384, 1024);
+                        const uint64_t db = mx.sdesc(kaddr, 16384, 1024);
 #pragma unroll
                         for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ss(tmem, sdesc_add(da, kk * 2048), sdesc_add(db, kk * 2048), idDQ,
-                                   kk > 0);
+                            mx.ss(tmem, sdesc_add(da, kk * 2048), sdesc_add(db, kk * 2048), idDQ,
+                                  kk > 0);
                     }
-                    mma_commit(smem_u32(&sm.dq_full));
+                    mx.commit(smem_u32(&sm.dq_full));
                     if (!(ok = expect(pend_s[0], smem_u32(&sm.dq_free[0]), c & 1))) break;
                     ok = expect(pend_s[1], smem_u32(&sm.dq_free[1]), c & 1);
                 }
                 if (!ok) break;
                 c2 += x.ns;
-                if (x.ns > 0) mma_commit(smem_u32(&sm.dk_full));
-                mma_commit(smem_u32(&sm.kv_empty));  // K and V read by every MMA issued
+                if (x.ns > 0) mx.commit(smem_u32(&sm.dk_full));
+                mx.commit(smem_u32(&sm.kv_empty));  // K and V read by every MMA issued
             }
             // never leave an MMA in flight
-            mma_commit(smem_u32(&sm.drain));
+            mx.commit(smem_u32(&sm.drain));
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         }
     } else if (warp >= 4) {

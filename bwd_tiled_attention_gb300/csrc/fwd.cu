@@ -59,6 +59,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "issue.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fa {
@@ -235,24 +236,6 @@ __device__ __forceinline__ void softmax_chunk(const float* sc, float c, float ne
         f2_unpack(e, p0, p1);
         pk[i] = pack_bf16x2(p0, p1);
     }
-}
-
-__device__ __forceinline__ void raise_abort(volatile int* flag, WsHeader* hdr, int code) {
-    *flag = 1;
-    atomicOr(&hdr->error, code);
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* flag,
-                                              WsHeader* hdr) {
-    if (mbar_wait(bar, parity, flag)) return true;
-    raise_abort(flag, hdr, kErrTimeout);
-    return false;
-}
-
-// Whole-warp wait: every lane leaves with the same answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
-                                          WsHeader* hdr) {
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, flag, hdr));
 }
 
 // A query row that sees no key: O = 0, LSE = -inf.
@@ -486,7 +469,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                                  abort_flag, hdr)))
                             break;
                         const uint32_t kb = smem_u32(&sm.k_full[st]), vb = smem_u32(&sm.v_full[st]);
-                        const int tok = x.tk0 + x.template tile<WIN>(j) * kTile;
+                        const int tok = x.tk0 + j * kTile;
                         mbar_arrive_expect_tx(kb, Cfg::kTileBytes);
                         for (int c = 0; c < Cfg::kBoxes; ++c)
                             tma_load_3d(smem_u32(sm.k[st]) + c * 16384, &p.tm_k, kb, c * 64, x.g, tok);
@@ -620,7 +603,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         } else
 #endif
-        if (lane == 0) {
+        if (WIN || lane == 0) {
+            const Issuer<WIN> mx;
             constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
             constexpr uint32_t idPV = make_idesc_bf16(128, Cfg::kVChunk, false, true);
             int sched_it = 0, kv_it = 0, unit_it = 0;
@@ -630,15 +614,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             bool ok = true;
             while (ok) {
                 const int slot = sched_it & 1;
-                if (!(ok = wait_or_abort(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
-                                         abort_flag, hdr)))
+                if (!(ok = mx.wait(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1,
+                                   abort_flag, hdr)))
                     break;
-                const int2 unit = sm.sched[slot];
-                mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                const int2 unit = mx.uniform(sm.sched[slot]);
+                if (!WIN || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                if (WIN) __syncwarp();
                 ++sched_it;
                 if (unit.x < 0) break;
                 const UnitGeom x = decode_unit<D, KV, WIN>(unit, p);
-                if (!(ok = wait_or_abort(smem_u32(&sm.q_full), unit_it & 1, abort_flag, hdr)))
+                if (!(ok = mx.wait(smem_u32(&sm.q_full), unit_it & 1, abort_flag, hdr)))
                     break;
                 if constexpr (D > 128) {
                     // One query tile, S double-buffered: step g (counted over all
@@ -649,8 +634,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const int n = x.n[0];
                     for (int j = 0; j <= x.nkv && ok; ++j) {
                         if (j < x.nkv) {
-                            if (!(ok = wait_or_abort(smem_u32(&sm.k_full[0]), k_it & 1, abort_flag,
-                                                     hdr)))
+                            if (!(ok = mx.wait(smem_u32(&sm.k_full[0]), k_it & 1, abort_flag,
+                                               hdr)))
                                 break;
                             if (j < n) {
                                 const int gj = g + j, b = gj & 1;
@@ -658,27 +643,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                 // softmax before PV(gj - 2) was issued; with P written
                                 // over them it is free once PV(gj - 2) has read P too.
                                 if (!Cfg::kSepP && gj >= 2 &&
-                                    !(ok = wait_or_abort(smem_u32(&sm.o_done[b]), ((gj - 2) >> 1) & 1,
-                                                         abort_flag, hdr)))
+                                    !(ok = mx.wait(smem_u32(&sm.o_done[b]), ((gj - 2) >> 1) & 1,
+                                                   abort_flag, hdr)))
                                     break;
                                 tc_fence_after();
-                                const uint64_t da = make_sdesc_here(smem_u32(sm.q[0]), 16, 1024);
-                                const uint64_t db = make_sdesc_here(smem_u32(sm.k[0]), 16, 1024);
+                                const uint64_t da = mx.sdesc(smem_u32(sm.q[0]), 16, 1024);
+                                const uint64_t db = mx.sdesc(smem_u32(sm.k[0]), 16, 1024);
 #pragma unroll
                                 for (int kk = 0; kk < D / 16; ++kk) {
                                     const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-                                    mma_ss(tmem + b * 128, sdesc_add(da, off), sdesc_add(db, off), idS,
-                                           kk > 0);
+                                    mx.ss(tmem + b * 128, sdesc_add(da, off), sdesc_add(db, off), idS,
+                                          kk > 0);
                                     // K's box kk / 4 is read once its four MMAs are done
-                                    if ((kk & 3) == 3) mma_commit(smem_u32(&sm.k_empty[kk >> 2]));
+                                    if ((kk & 3) == 3) mx.commit(smem_u32(&sm.k_empty[kk >> 2]));
                                 }
-                                mma_commit(smem_u32(&sm.s_full[b]));
+                                mx.commit(smem_u32(&sm.s_full[b]));
                             } else {
 #pragma unroll
                                 for (int c = 0; c < Cfg::kBoxes; ++c)
-                                    mma_commit(smem_u32(&sm.k_empty[c]));
+                                    mx.commit(smem_u32(&sm.k_empty[c]));
                             }
-                            if (j == x.nkv - 1) mma_commit(smem_u32(&sm.q_empty));
+                            if (j == x.nkv - 1) mx.commit(smem_u32(&sm.q_empty));
                             ++k_it;
                         }
                         if (j >= 1) {
@@ -686,44 +671,44 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                             // released once its chunk has been read
                             const int jp = j - 1, gj = g + jp, b = gj & 1;
                             if (jp < n) {
-                                if (!(ok = wait_or_abort(smem_u32(&sm.p_full[b]), (gj >> 1) & 1,
-                                                         abort_flag, hdr)))
+                                if (!(ok = mx.wait(smem_u32(&sm.p_full[b]), (gj >> 1) & 1,
+                                                   abort_flag, hdr)))
                                     break;
                                 if (jp == 0 && ep[0] > 0 &&
-                                    !(ok = wait_or_abort(smem_u32(&sm.o_free[0]), (ep[0] - 1) & 1,
-                                                         abort_flag, hdr)))
+                                    !(ok = mx.wait(smem_u32(&sm.o_free[0]), (ep[0] - 1) & 1,
+                                                   abort_flag, hdr)))
                                     break;
                             }
                             for (int h = 0; h < Cfg::kVChunks; ++h) {
                                 const int slot = v_it % Cfg::kVSlots;
-                                if (!(ok = wait_or_abort(smem_u32(&sm.v_full[slot]),
-                                                         (v_it / Cfg::kVSlots) & 1, abort_flag, hdr)))
+                                if (!(ok = mx.wait(smem_u32(&sm.v_full[slot]),
+                                                   (v_it / Cfg::kVSlots) & 1, abort_flag, hdr)))
                                     break;
                                 if (jp < n) {
                                     tc_fence_after();
-                                    const uint64_t db = make_sdesc_here(smem_u32(sm.v[slot]), 16384, 1024);
+                                    const uint64_t db = mx.sdesc(smem_u32(sm.v[slot]), 16384, 1024);
                                     // the first chunk starts on keys [0, 64) of P and waits
                                     // for [64, 128) halfway
 #pragma unroll
                                     for (int kk = 0; kk < kTile / 16; ++kk) {
                                         if (h == 0 && kk == kTile / 32) {
-                                            if (!(ok = wait_or_abort(smem_u32(&sm.p_hi[b]), (gj >> 1) & 1,
-                                                                     abort_flag, hdr)))
+                                            if (!(ok = mx.wait(smem_u32(&sm.p_hi[b]), (gj >> 1) & 1,
+                                                               abort_flag, hdr)))
                                                 break;
                                             tc_fence_after();
                                         }
-                                        mma_ts(tmem + 256 + h * Cfg::kVChunk,
-                                               tmem + (Cfg::kSepP ? Cfg::kPCol : b * 128) + kk * 8,
-                                               sdesc_add(db, kk * 2048), idPV,
-                                               (jp > 0 || kk > 0) ? 1u : 0u);
+                                        mx.ts(tmem + 256 + h * Cfg::kVChunk,
+                                              tmem + (Cfg::kSepP ? Cfg::kPCol : b * 128) + kk * 8,
+                                              sdesc_add(db, kk * 2048), idPV,
+                                              (jp > 0 || kk > 0) ? 1u : 0u);
                                     }
                                     if (!ok) break;
                                 }
-                                mma_commit(smem_u32(&sm.v_empty[slot]));
+                                mx.commit(smem_u32(&sm.v_empty[slot]));
                                 ++v_it;
                             }
                             if (!ok) break;
-                            if (jp < n) mma_commit(smem_u32(&sm.o_done[b]));
+                            if (jp < n) mx.commit(smem_u32(&sm.o_done[b]));
                         }
                     }
                     if (!ok) break;
@@ -731,14 +716,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     ++unit_it;
                     ep[0] += n > 0;
                 } else {
-                    int seen[2] = {0, 0};  // steps that tile t has taken part in
                     for (int j = 0; j < x.nkv && ok; ++j) {
                         const int st = kv_it % S, par = (kv_it / S) & 1;
                         if (!(ok = wait_or_abort(smem_u32(&sm.k_full[st]), par, abort_flag, hdr))) break;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (!ok) break;
-                            if (t >= Cfg::kQTiles || !x.template active<WIN>(t, j)) continue;
+                            if (t >= Cfg::kQTiles || j >= x.n[t]) continue;
                             // S_t / P_t region is free once the previous O_t += P_t V is done
                             if (it[t] > 0 &&
                                 !(ok = wait_or_abort(smem_u32(&sm.o_done[t]), (it[t] - 1) & 1,
@@ -761,12 +745,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
                             if (!ok) break;
-                            if (t >= Cfg::kQTiles || !x.template active<WIN>(t, j)) continue;
+                            if (t >= Cfg::kQTiles || j >= x.n[t]) continue;
                             if (!(ok = wait_or_abort(smem_u32(&sm.p_full[t]), it[t] & 1, abort_flag,
                                                      hdr)))
                                 break;
-                            const bool first = WIN ? seen[t] == 0 : j == 0;
-                            if (first && ep[t] > 0 &&
+                            if (j == 0 && ep[t] > 0 &&
                                 !(ok = wait_or_abort(smem_u32(&sm.o_free[t]), (ep[t] - 1) & 1,
                                                      abort_flag, hdr)))
                                 break;
@@ -784,12 +767,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                 }
                                 mma_ts(tmem + o_col, tmem + p_col + kk * 8,
                                        make_sdesc(vb + kk * 2048, 16384, 1024), idPV,
-                                       (!first || kk > 0) ? 1u : 0u);
+                                       (j > 0 || kk > 0) ? 1u : 0u);
                             }
                             if (!ok) break;
                             mma_commit(smem_u32(&sm.o_done[t]));
                             ++it[t];
-                            ++seen[t];
                         }
                         mma_commit(smem_u32(&sm.kv_empty[st]));
                         ++kv_it;
@@ -801,7 +783,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             }
             // all issued MMAs complete before TMEM is released
-            mma_commit(smem_u32(&sm.drain));
+            mx.commit(smem_u32(&sm.drain));
             mbar_wait(smem_u32(&sm.drain), 0, &sm.zero);
         }
     } else if (warp >= 4) {

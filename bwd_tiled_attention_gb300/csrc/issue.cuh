@@ -1,0 +1,62 @@
+// issue.cuh -- waits that end a kernel with an error, and the MMA issuer's two forms.
+#pragma once
+#include "common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace fa {
+namespace {
+
+__device__ __forceinline__ void raise_abort(volatile int* flag, WsHeader* hdr, int code) {
+    *flag = 1;
+    atomicOr(&hdr->error, code);
+}
+
+__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* flag,
+                                              WsHeader* hdr) {
+    if (mbar_wait(bar, parity, flag)) return true;
+    raise_abort(flag, hdr, kErrTimeout);
+    return false;
+}
+
+// Whole-warp wait: every lane leaves with the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
+                                          WsHeader* hdr) {
+    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, flag, hdr));
+}
+
+// How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
+// issues, so that descriptors and addresses stay in uniform registers.
+template <bool WARP>
+struct Issuer {
+    uint32_t lead = WARP ? elect_lead() : 1;
+    __device__ __forceinline__ void ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) const {
+        if constexpr (WARP) warp_mma_ss(lead, d, a, b, id, acc);
+        else mma_ss(d, a, b, id, acc);
+    }
+    __device__ __forceinline__ void ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) const {
+        if constexpr (WARP) warp_mma_ts(lead, d, a, b, id, acc);
+        else mma_ts(d, a, b, id, acc);
+    }
+    __device__ __forceinline__ void commit(uint32_t bar) const {
+        if constexpr (WARP) warp_mma_commit(lead, bar);
+        else mma_commit(bar);
+    }
+    __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) const {
+        if constexpr (WARP) return make_sdesc(addr, lbo, sbo);
+        else return make_sdesc_here(addr, lbo, sbo);
+    }
+    __device__ __forceinline__ bool any(bool x) const { return WARP ? __any_sync(0xffffffffu, x) : x; }
+    __device__ __forceinline__ bool test(uint32_t bar, uint32_t parity) const {
+        const bool in = mbar_test_wait(bar, parity);
+        return WARP ? __all_sync(0xffffffffu, in) : in;
+    }
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* flag, WsHeader* hdr) const {
+        return WARP ? warp_wait(bar, parity, flag, hdr) : wait_or_abort(bar, parity, flag, hdr);
+    }
+    __device__ __forceinline__ int2 uniform(int2 x) const {
+        return WARP ? make_int2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0)) : x;
+    }
+};
+
+}  // namespace
+}  // namespace fa
