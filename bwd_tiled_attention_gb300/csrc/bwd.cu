@@ -34,7 +34,8 @@
 //   warp 0       producer: K_j, V_j once per unit, then Q_i with LSE_i, D_i
 //                (2-stage ring) by TMA / plain loads
 //   warp 3       dO producer: dO_i (1 stage) by TMA, as soon as its slot frees
-//   warp 1       MMA issuer (tcgen05, one thread).  Per step: dP and dV in the
+//   warp 1       MMA issuer (tcgen05; one thread, or with a window a converged
+//                warp of which one lane issues).  Per step: dP and dV in the
 //                order their inputs arrive, then dQ once dS is in shared memory,
 //                S of the NEXT step as soon as dV has released the S columns, and
 //                dK last (it only accumulates) -- so the dQ drain starts early and
@@ -122,7 +123,8 @@ struct BUnit {
 // walks every query tile, as long as all the others together where the window is short
 // (N = 32768, W = 1024: 1024 steps of 268 a CTA).  Far units come first in the list.
 // Measured with D, conversion and the sinks' sum, 16 heads on 4 of 128, N = 32768: W = 4096,
-// S = 16 2450 us = 1056 TF/s (S = 0: 2421); W = 1024, S = 4 957 us = 709 TF/s (S = 0: 848).
+// S = 16 2338 us = 1106 TF/s (S = 0: 2307); W = 1024, S = 4 928 us = 731 TF/s (S = 0: 819); 2450
+// and 957 us with MMAs from one thread, as without a window.
 // Both leave fp32 partials of the sinks' dK and dV, which fold_sinks_kernel adds up in
 // a fixed order: the near unit in slot 0 of its sequence, chunk q in slot 1 + q.
 
@@ -1081,7 +1083,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // own, as do the MMAs.  Roles (256 threads):
 //   warp 0       producer: unit fetch, K and V, the Q/dO chunks in the order
 //                the MMAs read them
-//   warp 1       MMA issuer (one thread)
+//   warp 1       MMA issuer (one thread; with a window a converged warp)
 //   warp 2       TMEM allocation
 //   warps 4..7   compute, one thread per key row (P^T, dS^T, the dK/dV
 //                epilogue) or per query row (the dQ merge)

@@ -15,10 +15,14 @@
 // kernels), row r at position p = r + Lk - Lq sees keys c <= p with p - c < W or
 // c < S.  The tiles of a query tile are then those of the sinks and a stretch of
 // about W / 128 + 1; a unit walks the union of its two query tiles' stretches, and
-// a tile that one of them does not visit feeds the other's MMAs alone.  Measured, 16 heads
-// of 128: N = 32768, W = 4096, S = 16 975 us = 1060 TF/s of visible pairs (the causal
-// forward of the same length: 1220); 4 x 8192, W = 1024, S = 4 339 us = 764 TF/s, where 10
-// tiles are walked for 8 tiles' worth of pairs.
+// a tile that one of them does not visit feeds the other's MMAs alone.  Units are short, so
+// that a tile's chain S -> softmax -> PV -> S counts for more than without a window: its
+// MMAs are issued by a converged warp, and up to d = 128 a query tile's next scores come right
+// behind its own PV, with K and V tiles in ring places of their own, K a tile ahead of V.
+// Measured, 16 heads of 128: N = 32768 (4 key heads), W = 4096, S = 16 837 us = 1236 TF/s of
+// visible pairs (975 with scores and PVs of both tiles in turns, from one thread); 4 x 8192, W = 1024,
+// S = 4 291 us = 889 TF/s, where 10 tiles are walked for 8 tiles' worth of pairs (339).
+// Heads of 256: 560 us (573 from one thread).
 //
 // Blackwell design ("FlashAttention-4 wird offiziell veröffentlicht", section
 // "Neue Hardwaremerkmale von Blackwell": single-thread tcgen05.mma accumulating

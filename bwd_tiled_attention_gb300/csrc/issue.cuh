@@ -25,7 +25,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
-// issues, so that descriptors and addresses stay in uniform registers.
+// issues, so that descriptors and addresses stay in uniform registers.  Windowed kernels are
+// compiled with the latter: backward of 32768 tokens, 16 heads of 128, W = 4096, 2338 us against
+// 2450 (deterministic 3804 against 3743), d = 256 forward of 3.5k tokens 131 against 152.
 template <bool WARP>
 struct Issuer {
     uint32_t lead = WARP ? elect_lead() : 1;
