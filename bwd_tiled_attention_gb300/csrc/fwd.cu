@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             int ep[2] = {0, 0};  // units whose epilogue must finish before O_t is reused
             bool ok = true;
             auto wait = [&](uint64_t& bar, int parity) {
-                return ok = ok && warp_wait(smem_u32(&bar), parity & 1, abort_flag, hdr);
+                return ok = ok && warp_pass(smem_u32(&bar), parity & 1, abort_flag, hdr);
             };
             while (ok) {
                 const int slot = sched_it & 1;

@@ -123,6 +123,8 @@ __device__ __forceinline__ bool poll(uint32_t bar, uint32_t parity, volatile int
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
                                           int* status) {
+    // the common case in one branch of the whole warp
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, poll(bar, parity, flag, status));
 }
 
