@@ -19,10 +19,10 @@
 // that a tile's chain S -> softmax -> PV -> S counts for more than without a window: its
 // MMAs are issued by a converged warp, and up to d = 128 a query tile's next scores come right
 // behind its own PV, with K and V tiles in ring places of their own, K a tile ahead of V.
-// Measured, 16 heads of 128: N = 32768 (4 key heads), W = 4096, S = 16 837 us = 1236 TF/s of
+// Measured, 16 heads of 128: N = 32768 (4 key heads), W = 4096, S = 16 786 us = 1315 TF/s of
 // visible pairs (975 with scores and PVs of both tiles in turns, from one thread); 4 x 8192, W = 1024,
-// S = 4 291 us = 889 TF/s, where 10 tiles are walked for 8 tiles' worth of pairs (339).
-// Heads of 256: 560 us (573 from one thread).
+// S = 4 276 us = 937 TF/s, where 10 tiles are walked for 8 tiles' worth of pairs (339).
+// Heads of 256: 550 us (573 from one thread).
 //
 // Blackwell design ("FlashAttention-4 wird offiziell veröffentlicht", section
 // "Neue Hardwaremerkmale von Blackwell": single-thread tcgen05.mma accumulating
@@ -525,7 +525,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             int ep[2] = {0, 0};  // units whose epilogue must finish before O_t is reused
             bool ok = true;
             auto wait = [&](uint64_t& bar, int parity) {
-                return ok = ok && warp_pass(smem_u32(&bar), parity & 1, abort_flag, hdr);
+                return ok = ok && warp_wait<true>(smem_u32(&bar), parity & 1, abort_flag, hdr);
             };
             while (ok) {
                 const int slot = sched_it & 1;
@@ -800,12 +800,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint32_t s_addr = tmem + lane_off + t * 128;
         // (D > 128: one O, stored by warps 8..11)
         const uint32_t o_addr = tmem + lane_off + 256 + (D > 128 ? 0 : t * 128);
+        // (windowed, N = 32768, W = 4096 786 us against 803; but 4 x 8192, W = 1024 at d = 192 417
+        // against 404, d = 256 552 against 549)
+        constexpr bool kPass = WIN && D <= 128;
         int sched_it = 0, it = 0;
         int ue = 0;  // D > 128: units handed from the softmax to the epilogue warps
         bool ok = true;
         while (ok) {
             const int slot = sched_it & 1;
-            if (!(ok = warp_wait(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1, abort_flag,
+            if (!(ok = warp_wait<kPass>(smem_u32(&sm.sched_full[slot]), (sched_it >> 1) & 1, abort_flag,
                                  hdr)))
                 break;
             const int2 unit = sm.sched[slot];
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // D > 128: S alternates between two buffers, step by step
                 const int buf = D > 128 ? (it & 1) : t;
                 const uint32_t s_at = D > 128 ? s_addr + (uint32_t)buf * 128 : s_addr;
-                if (!(ok = warp_wait(smem_u32(&sm.s_full[buf]), D > 128 ? (it >> 1) & 1 : it & 1,
+                if (!(ok = warp_wait<kPass>(smem_u32(&sm.s_full[buf]), D > 128 ? (it >> 1) & 1 : it & 1,
                                      abort_flag, hdr)))
                     break;
                 tc_fence_after();
@@ -971,7 +974,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 // the previous P.
                 bool pv_done = it == 0;
                 if (__any_sync(0xffffffffu, need)) {
-                    if (!(ok = warp_wait(smem_u32(&sm.o_done[(it - 1) & 1]), ((it - 1) >> 1) & 1,
+                    if (!(ok = warp_wait<kPass>(smem_u32(&sm.o_done[(it - 1) & 1]), ((it - 1) >> 1) & 1,
                                          abort_flag, hdr)))
                         break;
                     tc_fence_after();
@@ -999,7 +1002,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         for (int c = 0; c < 2; ++c)
                             softmax_chunk(s + (2 * hf + c) * 32, p.scale_log2, neg, acc, pk[c]);
                         if (!pv_done) {
-                            if (!(ok = warp_wait(smem_u32(&sm.o_done[(it - 1) & 1]),
+                            if (!(ok = warp_wait<kPass>(smem_u32(&sm.o_done[(it - 1) & 1]),
                                                  ((it - 1) >> 1) & 1, abort_flag, hdr)))
                                 break;
                             tc_fence_after();
@@ -1044,7 +1047,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 continue;
             }
             // epilogue: O = O~ / l, LSE = (m + log2 l) * ln 2
-            if (!(ok = warp_wait(smem_u32(&sm.o_done[t]), (it - 1) & 1, abort_flag, hdr))) break;
+            if (!(ok = warp_wait<kPass>(smem_u32(&sm.o_done[t]), (it - 1) & 1, abort_flag, hdr))) break;
             tc_fence_after();
             store_row<DR, OUT_FP32, KV>(p, o_addr, x.h, (size_t)x.t0 + (size_t)r, r < x.L, m_ref, l);
             tc_fence_before();

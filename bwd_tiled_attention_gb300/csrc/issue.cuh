@@ -24,17 +24,19 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xffffffffu, wait_or_abort(bar, parity, flag, hdr));
 }
 
-// The same where the phase is mostly there: the common case is one branch of the whole warp.
-__device__ __forceinline__ bool warp_pass(uint32_t bar, uint32_t parity, volatile int* flag,
+// The same; PASS: the phase is mostly there, and the common case is one branch of the whole
+// warp (the windowed forward's issuer, N = 32768, W = 4096: 803 us against 838).
+template <bool PASS>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* flag,
                                           WsHeader* hdr) {
-    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (PASS && __all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return warp_wait(bar, parity, flag, hdr);
 }
 
 // How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
 // issues, so that descriptors and addresses stay in uniform registers.  Windowed kernels are
 // compiled with the latter: backward of 32768 tokens, 16 heads of 128, W = 4096, 2338 us against
-// 2450 (deterministic 3804 against 3743), d = 256 forward of 3.5k tokens 131 against 152.
+// 2450 (deterministic 3804 against 3743), d = 256 forward of 3.5k tokens 129 against 152.
 template <bool WARP>
 struct Issuer {
     uint32_t lead = WARP ? elect_lead() : 1;
@@ -60,7 +62,7 @@ struct Issuer {
         return WARP ? __all_sync(0xffffffffu, in) : in;
     }
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* flag, WsHeader* hdr) const {
-        return WARP ? warp_pass(bar, parity, flag, hdr) : wait_or_abort(bar, parity, flag, hdr);
+        return WARP ? warp_wait<true>(bar, parity, flag, hdr) : wait_or_abort(bar, parity, flag, hdr);
     }
     __device__ __forceinline__ int2 uniform(int2 x) const {
         return WARP ? make_int2(__shfl_sync(0xffffffffu, x.x, 0), __shfl_sync(0xffffffffu, x.y, 0)) : x;
