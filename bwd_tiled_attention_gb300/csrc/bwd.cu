@@ -58,7 +58,6 @@
 // columns [384,448) for d = 64.
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -324,11 +323,10 @@ __device__ bool sem_wait(const int* sem, int target, const WsHeader* hdr) {
 // P^T for one 32-column chunk of a key row: exp2(S^T * c - LSE2) as packed
 // bf16 pairs; with MASK, columns outside [lo, hi) are zero.  nl2 holds the
 // chunk's LSE2 values negated and cc is c in both halves of an fp32 pair, so
-// the scaling is one packed FMA per two columns.  FINE: ph gets the same as fp16 pairs.
+// the scaling is one packed FMA per two columns.  FINE: P^T itself takes sv's place too.
 template <bool MASK, bool FINE = false>
-__device__ __forceinline__ void p_chunk(const uint32_t (&sv)[32], const float* nl2, uint64_t cc,
-                                           int lo, int hi, int xb, uint32_t (&pk)[16],
-                                           uint32_t* ph = nullptr) {
+__device__ __forceinline__ void p_chunk(uint32_t (&sv)[32], const float* nl2, uint64_t cc, int lo,
+                                        int hi, int xb, uint32_t (&pk)[16]) {
 #pragma unroll
     for (int e4 = 0; e4 < 8; ++e4) {
         const ulonglong2 lv = reinterpret_cast<const ulonglong2*>(nl2)[e4];
@@ -347,25 +345,28 @@ __device__ __forceinline__ void p_chunk(const uint32_t (&sv)[32], const float* n
             }
             pk[e] = pack_bf16x2(p0, p1);
             if constexpr (FINE) {
-                const __half2 h = __floats2half2_rn(p0, p1);
-                ph[e] = *reinterpret_cast<const uint32_t*>(&h);
+                sv[2 * e] = __float_as_uint(p0);
+                sv[2 * e + 1] = __float_as_uint(p1);
             }
         }
     }
 }
 
-// The two probabilities of dS: what the tensor core got of P, or, FINE, P itself to 11
-// bits.  (P <= 1 but for the rounding of LSE, and below 2^-14 an fp16 is off by 2^-25 at
-// most.)  The windowed backward takes the latter: dS and dQ, dK are then off by two roundings
-// to bf16, of dS and of the result, instead of three (in the 2-norm 0.0029 -> 0.0024; the
-// call 0.5-1% longer).
-template <bool FINE>
-__device__ __forceinline__ uint64_t p_pair(uint32_t pp) {
-    if constexpr (FINE) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&pp));
-        return f2_pack(f.x, f.y);
-    }
-    return f2_pack(__uint_as_float(pp << 16), __uint_as_float(pp & 0xffff0000u));
+// Two elements of dS^T = P^T (dP^T - D) as a bf16 pair; nd: -D of the two columns.
+__device__ __forceinline__ uint32_t ds_pair(uint64_t p, uint32_t dp0, uint32_t dp1, uint64_t nd) {
+    float d0, d1;
+    f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(dp0), __uint_as_float(dp1)), nd), p), d0, d1);
+    return pack_bf16x2(d0, d1);
+}
+
+// P of dS is what the tensor core got of it, a bf16 pair; with a window it is P in fp32, so
+// that dS and dQ, dK are off by two roundings to bf16, of dS and of the result, instead of
+// three, however small P is (a sink may leave the others 2^-20 and less).
+__device__ __forceinline__ uint64_t bf16_pair(uint32_t pk) {
+    return f2_pack(__uint_as_float(pk << 16), __uint_as_float(pk & 0xffff0000u));
+}
+__device__ __forceinline__ uint64_t fp32_pair(const uint32_t* p) {
+    return f2_pack(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
 // D: the tile layout (64 or 128 columns); DR: the head dimension in memory.
@@ -795,24 +796,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!(ok = warp_wait(smem_u32(&sm.s_full), cnt & 1, abort_flag, hdr))) break;
                 tc_fence_after();
                 const float* l2 = sm.lse2[st] + hc * 64;
-                uint32_t pk[2][16];
-                uint32_t ph[WIN ? 2 : 1][16];
-                {
-                    uint32_t sv[2][32];  // this half's two 32-column loads, one wait
-                    tmem_ld32(s_addr + hc * 64, sv[0]);
-                    tmem_ld32(s_addr + hc * 64 + 32, sv[1]);
-                    tmem_ld_wait();
+                uint32_t sv[2][32];                // this half's two 32-column loads, one wait
+                uint32_t pk[WIN ? 1 : 2][16];
+                tmem_ld32(s_addr + hc * 64, sv[0]);
+                tmem_ld32(s_addr + hc * 64 + 32, sv[1]);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int xb = hc * 64 + h * 32;  // first query column of the chunk
-                        if (full)
-                            p_chunk<false, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h], ph[WIN ? h : 0]);
-                        else
-                            p_chunk<true, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pk[h], ph[WIN ? h : 0]);
-                        // into this half's own S^T columns, which this warp has
-                        // already read (the other half's are still being read)
-                        tmem_st16(s_addr + hc * 64 + h * 16, pk[h]);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    const int xb = hc * 64 + h * 32;  // first query column of the chunk
+                    uint32_t(&pc)[16] = pk[WIN ? 0 : h];
+                    if (full)
+                        p_chunk<false, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pc);
+                    else
+                        p_chunk<true, WIN>(sv[h], l2 + h * 32, cc2, lo, hi, xb, pc);
+                    // into this half's own S^T columns, which this warp has
+                    // already read (the other half's are still being read)
+                    tmem_st16(s_addr + hc * 64 + h * 16, pc);
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -825,7 +824,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!(ok = warp_wait(smem_u32(&sm.dp_full), cnt & 1, abort_flag, hdr))) break;
                 tc_fence_after();
                 const float* dd = sm.dd[st] + hc * 64;
-                {
+                // 8 query columns are a chunk of 16 bytes of this half's block
+                auto put = [&](int ch, const uint32_t* out) {
+                    *reinterpret_cast<uint4*>(ds_row + ((ch ^ sw) << 4)) =
+                        make_uint4(out[0], out[1], out[2], out[3]);
+                };
+                if constexpr (WIN) {
+                    // P takes 64 registers, and dP^T comes 16 columns at a time, a load ahead
+                    uint32_t dv[2][16];
+                    tmem_ld16(dp_addr + hc * 64, dv[0]);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        tmem_ld_wait();
+                        hold16(dv[g & 1]);
+                        if (g < 3) tmem_ld16(dp_addr + hc * 64 + (g + 1) * 16, dv[(g + 1) & 1]);
+                        uint32_t out[8];
+#pragma unroll
+                        for (int e4 = 0; e4 < 4; ++e4) {
+                            const ulonglong2 nd = reinterpret_cast<const ulonglong2*>(dd + g * 16)[e4];
+#pragma unroll
+                            for (int h2 = 0; h2 < 2; ++h2) {
+                                const int e = e4 * 2 + h2;
+                                out[e] = ds_pair(fp32_pair(&sv[g >> 1][(g & 1) * 16 + 2 * e]),
+                                                 dv[g & 1][2 * e], dv[g & 1][2 * e + 1], h2 ? nd.y : nd.x);
+                            }
+                        }
+                        put(g * 2, out);
+                        put(g * 2 + 1, out + 4);
+                    }
+                } else {
                     uint32_t dv[2][32];
                     tmem_ld32(dp_addr + hc * 64, dv[0]);
                     tmem_ld32(dp_addr + hc * 64 + 32, dv[1]);
@@ -839,23 +866,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
                             for (int h2 = 0; h2 < 2; ++h2) {
                                 const int e = e4 * 2 + h2;
-                                const uint64_t pf = p_pair<WIN>(WIN ? ph[WIN ? h : 0][e] : pk[h][e]);
-                                const uint64_t t = f2_add(f2_pack(__uint_as_float(dv[h][2 * e]),
-                                                                  __uint_as_float(dv[h][2 * e + 1])),
-                                                          h2 ? nd.y : nd.x);
-                                float d0, d1;
-                                f2_unpack(f2_mul(t, pf), d0, d1);
-                                out[e] = pack_bf16x2(d0, d1);
+                                out[e] = ds_pair(bf16_pair(pk[WIN ? 0 : h][e]), dv[h][2 * e],
+                                                 dv[h][2 * e + 1], h2 ? nd.y : nd.x);
                             }
                         }
-                        // 32 query columns = 4 chunks of 16 bytes of this half's block
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int ch = h * 4 + e;
-                            *reinterpret_cast<uint4*>(ds_row + ((ch ^ sw) << 4)) =
-                                make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2],
-                                           out[4 * e + 3]);
-                        }
+                        for (int e = 0; e < 4; ++e) put(h * 4 + e, out + 4 * e);
                     }
                 }
                 fence_proxy_async_smem();
@@ -1607,21 +1623,17 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                         tmem_ld32(tmem + lane_off + qc * 32, sv);
                         tmem_ld32(tmem + lane_off + 128 + qc * 32, dv);
                         tmem_ld_wait();
-                        uint32_t pk[16], ph[16];
+                        uint32_t pk[16];
                         if (full)
-                            p_chunk<false, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk, ph);
+                            p_chunk<false, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk);
                         else
-                            p_chunk<true, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk, ph);
+                            p_chunk<true, WIN>(sv, sm.lse2[rb] + qc * 32, cc2, lo, hi, qc * 32, pk);
                         uint32_t out[16];
                         const uint64_t* nd = reinterpret_cast<const uint64_t*>(sm.dd[rb] + qc * 32);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const uint64_t pf = p_pair<WIN>(WIN ? ph[e] : pk[e]);
-                            const uint64_t t = f2_add(
-                                f2_pack(__uint_as_float(dv[2 * e]), __uint_as_float(dv[2 * e + 1])), nd[e]);
-                            float d0, d1;
-                            f2_unpack(f2_mul(t, pf), d0, d1);
-                            out[e] = pack_bf16x2(d0, d1);
+                            const uint64_t pf = WIN ? fp32_pair(&sv[2 * e]) : bf16_pair(pk[e]);
+                            out[e] = ds_pair(pf, dv[2 * e], dv[2 * e + 1], nd[e]);
                         }
                         // 32 query columns = 4 chunks of 16 bytes of half (qc >> 1)'s block
 #pragma unroll
