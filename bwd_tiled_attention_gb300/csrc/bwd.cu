@@ -34,8 +34,8 @@
 //   warp 0       producer: K_j, V_j once per unit, then Q_i with LSE_i, D_i
 //                (2-stage ring) by TMA / plain loads
 //   warp 3       dO producer: dO_i (1 stage) by TMA, as soon as its slot frees
-//   warp 1       MMA issuer (tcgen05; one thread, or with a window a converged
-//                warp of which one lane issues).  Per step: dP and dV in the
+//   warp 1       MMA issuer (tcgen05; one thread, or WARP: a converged warp of
+//                which one lane issues).  Per step: dP and dV in the
 //                order their inputs arrive, then dQ once dS is in shared memory,
 //                S of the NEXT step as soon as dV has released the S columns, and
 //                dK last (it only accumulates) -- so the dQ drain starts early and
@@ -374,7 +374,7 @@ __device__ __forceinline__ uint64_t fp32_pair(const uint32_t* p) {
 // S and dP contract over the first 96 columns only (6 MMAs of K = 16).  dV, dK
 // and dQ keep N = 128 (their B operands are read MN-major in 64-column swizzle
 // atoms); their last 32 columns are zero and neither stored nor merged.
-template <int D, int DR, bool KV, bool RUNS, bool WIN>
+template <int D, int DR, bool KV, bool RUNS, bool WIN, bool WARP>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ BwdParams p) {
     pdl_trigger();
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         setmaxnreg_dec<80>();
-        if (WIN || lane == 0) {
-            const Issuer<WIN> mx;
+        if (WARP || lane == 0) {
+            const Issuer<WARP> mx;
             constexpr uint32_t idS = make_idesc_bf16(128, 128, false, false);
             constexpr uint32_t idKV = make_idesc_bf16(128, D, false, true);
             constexpr uint32_t idDQ = make_idesc_bf16(128, D, true, true);
@@ -593,8 +593,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                                    abort_flag, hdr)))
                     break;
                 const int2 unit = mx.uniform(sm.sched[slot]);
-                if (!WIN || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
-                if (WIN) __syncwarp();
+                if (!WARP || lane == 0) mbar_arrive(smem_u32(&sm.sched_empty[slot]));
+                if (WARP) __syncwarp();
                 ++sched_it;
                 if (unit.x < 0) break;
                 const BUnit x = decode_bunit<KV, RUNS, WIN>(unit, p);
@@ -1785,13 +1785,15 @@ template <int D, int DR, bool WIN>
 cudaError_t launch_bwd_t(const BwdParams& p, int num_sms, cudaStream_t stream) {
     void (*kern)(const BwdParams);
     if constexpr (WIN)
-        kern = p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, true>
-                            : fa_bwd_kernel<D, DR, true, false, true>;
+        kern = p.deterministic ? (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, true, false>
+                                               : fa_bwd_kernel<D, DR, true, false, true, false>)
+                               : (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, true, true>
+                                               : fa_bwd_kernel<D, DR, true, false, true, true>);
     else
-        kern = p.kv ? (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, false>
-                                    : fa_bwd_kernel<D, DR, true, false, false>)
-                    : (p.hchunk > 1 ? fa_bwd_kernel<D, DR, false, true, false>
-                                    : fa_bwd_kernel<D, DR, false, false, false>);
+        kern = p.kv ? (p.hchunk > 1 ? fa_bwd_kernel<D, DR, true, true, false, false>
+                                    : fa_bwd_kernel<D, DR, true, false, false, false>)
+                    : (p.hchunk > 1 ? fa_bwd_kernel<D, DR, false, true, false, false>
+                                    : fa_bwd_kernel<D, DR, false, false, false, false>);
     const size_t smem = sizeof(BwdSmem<D>);
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

@@ -36,7 +36,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 // How the MMAs are issued: by one thread, or (WARP) by a converged warp of which one lane
 // issues, so that descriptors and addresses stay in uniform registers.  Windowed kernels are
 // compiled with the latter: backward of 32768 tokens, 16 heads of 128, W = 4096, 2338 us against
-// 2450 (deterministic 3804 against 3743), d = 256 forward of 3.5k tokens 129 against 152.
+// 2450, d = 256 forward of 3.5k tokens 129 against 152.  The deterministic backward up to
+// d = 128 is not: 3762 against 3823 (d = 64 846 against 857, d = 96 1137 against 1127).  Above, it is
+// (d = 192 3121 against 3281, d = 256 3830 against 3909).
 template <bool WARP>
 struct Issuer {
     uint32_t lead = WARP ? elect_lead() : 1;
