@@ -20,7 +20,8 @@ LIB = os.path.join(BUILD, "libfa_gb300.so")
 SOURCES = ["api.cu", "sched.cu", "fwd.cu", "fwd_window.cu", "bwd.cu", "bwd_window.cu", "noalloc.cu",
            "rotary.cu", "cache.cu", "tree.cu", "tree_window.cu",
            "weights.cu", "evict.cu"]
-HEADERS = ["cache.cuh", "cache_plan.cuh", "common.cuh", "internal.h", "issue.cuh", "sm100_ptx.cuh"]
+HEADERS = ["cache.cuh", "cache_plan.cuh", "common.cuh", "internal.h", "issue.cuh", "sm100_ptx.cuh",
+           "window.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

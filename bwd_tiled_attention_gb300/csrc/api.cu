@@ -12,6 +12,7 @@
 #include "../../include/fa.h"
 #include "common.cuh"
 #include "internal.h"
+#include "window.cuh"
 
 using namespace fa;
 
@@ -159,7 +160,7 @@ fa_status check_shape(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int t
 
 fa_status cuda_status(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
 
-// A packed batch is ranked by one scheduler CTA, with a prefix entry per tile
+// A packed batch is ranked by every scheduler CTA, with a prefix entry per tile
 // level of the longest sequence: its bound N must fit one CTA's shared memory.
 constexpr size_t kSchedSmemMax = 232448;  // 227 KB, the per-block maximum
 bool sched_fits(const Shape& s, int N, int rows) {
@@ -248,7 +249,8 @@ size_t bwd_ws_bytes(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int tot
     const long long Tk = total_k > 0 ? total_k : (long long)B * Nk;
     if (Tq > 0x7FFFFFFFLL || Tk > 0x7FFFFFFFLL) return 0;
     const BwdWs lay = bwd_ws_layout(B, Hq, Hkv, (int)Tq, (int)Tk, d);
-    if (win.sinks) return far_ws_layout(lay, B, Hkv, (int)Tq, d, win.sinks).bytes;
+    if (win.sinks)
+        return far_ws_layout(lay, B, Hkv, (int)Tq, (int)Tk, d, win.window, win.sinks).bytes;
     return sems_offset ? lay.sems : lay.bytes;
 }
 
@@ -256,7 +258,7 @@ size_t bwd_ws_bytes(int B, int Hq, int Hkv, int Nq, int total_q, int Nk, int tot
 // everything.
 fa_status far_layout(const Shape& s, const BwdWs& lay, Window win, size_t workspace_bytes, FarWs& far) {
     if (win.sinks) {
-        far = far_ws_layout(lay, s.B, s.Hkv, s.Tq, s.d, win.sinks);
+        far = far_ws_layout(lay, s.B, s.Hkv, s.Tq, s.Tk, s.d, win.window, win.sinks);
         if (s.B >= kFarUnit || (long long)cdiv(cdiv(s.Nq, kTile), far.chunk) * far.tiles > kMaxTiles ||
             far.max_units + lay.max_units > 0x7FFFFFFFLL)
             return FA_ERR_UNSUPPORTED;
@@ -294,7 +296,7 @@ fa_status bwd_preprocess_impl(const void* o, fa_dtype o_dtype, const void* dout,
     cudaError_t e = launch_sched(cu_k, B, Nk, s.Tk, Hkv * lay.nruns, kTile, order,
                                  lay.max_units + far.max_units, workspace,
                                  win.sinks ? far.units : lay.units, lay.tile_off, true, cu_q, Nq,
-                                 s.Tq, strm, far.chunk, far.tiles);
+                                 s.Tq, strm, far.chunk, win.window, win.sinks);
     if (e != cudaSuccess) return FA_ERR_CUDA;
     e = launch_bwd_preprocess(o, o_dtype == FA_FP32, dout, D,
                               reinterpret_cast<float*>(ws + lay.dq_acc),
@@ -370,6 +372,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* dout
     p.far_chunk = far.chunk;
     p.sink_tiles = far.tiles;
     p.sink_off = far.sinks;
+    p.near_rows = far.near_rows;
     if (win.sinks) p.units_off = far.units;
     const int nsm = sm_count();
     if (nsm <= 0) return FA_ERR_CUDA;

@@ -66,6 +66,7 @@
 #include "internal.h"
 #include "issue.cuh"
 #include "sm100_ptx.cuh"
+#include "window.cuh"
 
 namespace fa {
 namespace {
@@ -124,50 +125,31 @@ struct BUnit {
 // Measured with D, conversion and the sinks' sum, 16 heads on 4 of 128, N = 32768: W = 4096,
 // S = 16 2338 us = 1106 TF/s (S = 0: 2307); W = 1024, S = 4 928 us = 731 TF/s (S = 0: 819); 2450
 // and 957 us with MMAs from one thread, as without a window.
-// Both leave fp32 partials of the sinks' dK and dV, which fold_sinks_kernel adds up in
-// a fixed order: the near unit in slot 0 of its sequence, chunk q in slot 1 + q.
-
-// Query tiles of unit x of a windowed call: rows r with c - off <= r < c - off + W for a
-// key c of the tile, or for a far unit r >= c - off + W for a sink c of the tile.
-__device__ __forceinline__ void window_span(BUnit& x, const BwdParams& p) {
-    const int c0 = x.j * kTile;
-    int i0, i1;
-    if (x.far == 0) {
-        i0 = max(0, floor_div(c0 - x.off, kTile));
-        i1 = min(x.nt, floor_div(min(c0 + kTile, x.Lk) - 2 + p.window - x.off, kTile) + 1);
-    } else {
-        const int q = x.far - 1;
-        i0 = max(q * p.far_chunk, floor_div(c0 + p.window - x.off, kTile));
-        i1 = min(x.nt, (q + 1) * p.far_chunk);
-        if (c0 >= min(p.sinks, x.Lk) || c0 + p.window >= x.Lk) i1 = i0;
-    }
-    x.i0 = i0;
-    x.ni = max(0, i1 - i0);
-}
+// Both leave fp32 partials of the dK and dV of sinks with far rows, which fold_sinks_kernel adds
+// up in a fixed order.
 
 // Visible query columns [lo, hi), within query tile i, of key c of unit x.
-__device__ __forceinline__ void window_cols(const BUnit& x, const BwdParams& p, int c, int i, int& lo,
-                                            int& hi) {
-    const int r = c - x.off;  // the key's own row
-    const int from = x.far ? r + p.window : r;
-    const int to = x.far ? (c < min(p.sinks, x.Lk) ? x.L : 0) : (c < x.Lk ? min(x.L, r + p.window) : 0);
-    lo = max(0, from - i * kTile);
-    hi = min(kTile, to - i * kTile);
+__device__ __forceinline__ void unit_cols(const BUnit& x, const BwdParams& p, int c, int i, int& lo,
+                                          int& hi) {
+    window_cols(x.far != 0, c, i, x.L, x.Lk, p.window, p.sinks, lo, hi);
 }
 
-// Sink tiles with far rows in query tile i: tiles [0, that).
-__device__ __forceinline__ int far_tiles(const BUnit& x, const BwdParams& p, int i) {
-    const int last = min((i + 1) * kTile, x.L) - 1 + x.off;  // the tile's last position
-    return max(0, min(cdiv(min(p.sinks, x.Lk), kTile), floor_div(last - p.window, kTile) + 1));
-}
-
-// Place of the fp32 partials of dK (which = 0) or dV (1) of sink row c of unit x.
+// The partials of sink 0 of unit x's sequence: [row, dK or dV, head, column].
 template <int DR>
-__device__ __forceinline__ float* sink_row(const BUnit& x, const BwdParams& p, const int* tile_off,
-                                           int which, int c) {
-    const int slot = tile_off[x.b] / p.far_chunk + 2 * x.b + x.far;
+__device__ __forceinline__ float* sink_rows(const BUnit& x, const BwdParams& p) {
+    long long row;
+    if (x.far == 0)
+        row = near_place(x.b, x.tk0, p.window, p.sinks);
+    else
+        row = p.near_rows + far_place(x.b, x.t0, x.tk0, p.far_chunk, p.window, p.sinks) +
+              (long long)(x.far - 1) * far_rows(x.Lk, p.window, p.sinks);
     float* base = reinterpret_cast<float*>(static_cast<char*>(p.workspace) + p.sink_off);
-    return base + ((((size_t)slot * 2 + which) * (p.Hkv * p.nchunks) + x.uh) * p.sinks + c) * DR;
+    return base + (row * 2 * (p.Hkv * p.nchunks) + x.uh) * DR;
+}
+// Row c of them, of dK (which = 0) or dV (1).
+template <int DR>
+__device__ __forceinline__ float* sink_row(float* rows, const BwdParams& p, int which, int c) {
+    return rows + ((size_t)c * 2 + which) * (p.Hkv * p.nchunks) * DR;
 }
 
 // KV = false: keys and queries share their boundaries (Lk = L, off = 0), and
@@ -202,7 +184,10 @@ __device__ __forceinline__ BUnit decode_bunit(int2 u, const BwdParams& p) {
         x.off = x.Lk - x.L;
         x.ntk = cdiv(x.Lk, kTile);
         if constexpr (WIN) {
-            window_span(x, p);
+            const WindowSpan w = x.far == 0 ? near_span(x.j, x.L, x.Lk, p.window)
+                                            : far_span(x.j, x.far - 1, p.far_chunk, x.L, x.Lk, p.window, p.sinks);
+            x.i0 = w.i0;
+            x.ni = w.ni;
         } else {
             x.i0 = p.causal ? max(0, floor_div(x.j * kTile - x.off, kTile)) : 0;
             x.ni = max(0, x.nt - x.i0);  // 0 only when the sequence has no queries
@@ -268,11 +253,10 @@ __device__ __forceinline__ void unit_step(const BUnit& x, int s, const StepPos& 
 template <bool KV, bool WIN>
 __device__ __forceinline__ int dq_rank(const BUnit& x, const BwdParams& p, int i, int causal) {
     if constexpr (!KV) return causal ? i - x.j : x.nt - 1 - x.j;
-    const int before = WIN ? far_tiles(x, p, i) : 0;
-    if (WIN && x.far) return before - 1 - x.j;
+    if constexpr (WIN) return window_rank(x.far != 0, x.j, i, x.L, x.Lk, p.window, p.sinks);
     const int jmax = causal ? min(x.ntk - 1, floor_div((i + 1) * kTile + x.off - 1, kTile))
                             : x.ntk - 1;
-    return before + jmax - x.j;
+    return jmax - x.j;
 }
 
 // Wait shared by the four warps of the dQ/epilogue warpgroup: they meet on
@@ -782,7 +766,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 // mask when every row sees every column
                 int lo, hi;
                 if constexpr (WIN) {
-                    window_cols(x, p, c, i, lo, hi);
+                    unit_cols(x, p, c, i, lo, hi);
                 } else if constexpr (KV) {
                     lo = p.causal ? max(0, c_off - i * kTile) : 0;
                     hi = min(kTile, L_vis - i * kTile);
@@ -994,6 +978,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             const size_t tok = (size_t)x.tk0 + (size_t)kr;
             const bool none = KV && x.ns == 0;  // no query: dK = dV = 0, TMEM not written
             const bool partial = p.nchunks > 1;  // other units cover the group's other heads
+            const int far_n = WIN ? far_rows(x.Lk, p.window, p.sinks) : 0;
+            float* sinks = nullptr;
+            if (WIN && x.j * kTile < far_n) sinks = sink_rows<DR>(x, p);
 #pragma unroll 1
             for (int which = 0; which < 2; ++which) {
                 const uint32_t col = which == 0 ? Cfg::kColDK : Cfg::kColDV;
@@ -1009,9 +996,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         for (int e = 0; e < 32; ++e) v[e] = 0u;
                     }
                     if constexpr (WIN) {
-                        if (kr < p.sinks) {
-                            float4* s4 = reinterpret_cast<float4*>(
-                                sink_row<DR>(x, p, tile_off, which, kr) + cc * 32);
+                        if (kr < far_n) {
+                            float4* s4 = reinterpret_cast<float4*>(sink_row<DR>(sinks, p, which, kr) + cc * 32);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 s4[e] = make_float4(__uint_as_float(v[4 * e]) * mul,
@@ -1478,7 +1464,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int L_vis = c < x.Lk ? x.L : 0;
             auto visible = [&](int i, int& lo, int& hi) {
                 if constexpr (WIN) {
-                    window_cols(x, p, c, i, lo, hi);
+                    unit_cols(x, p, c, i, lo, hi);
                 } else if constexpr (KV) {
                     lo = p.causal ? max(0, c_off - i * kTile) : 0;
                     hi = min(kTile, L_vis - i * kTile);
@@ -1498,6 +1484,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     dv = p.D[at];
                 }
             };
+            const int far_n = WIN ? far_rows(x.Lk, p.window, p.sinks) : 0;
+            float* sinks = nullptr;
+            if (WIN && x.j * kTile < far_n) sinks = sink_rows<D>(x, p);
             // dV (pass 1) or dK times scale (pass 2) of this key row, from TMEM
             auto epilogue = [&](int pass) {
                 const bool valid = c < x.Lk;
@@ -1517,9 +1506,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     }
                     if (!valid) continue;
                     if constexpr (WIN) {
-                        if (c < p.sinks) {
-                            float4* s4 = reinterpret_cast<float4*>(
-                                sink_row<D>(x, p, tile_off, 1 - pass, c) + cc * 32);
+                        if (c < far_n) {
+                            float4* s4 = reinterpret_cast<float4*>(sink_row<D>(sinks, p, 1 - pass, c) + cc * 32);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 s4[e] = make_float4(__uint_as_float(v[4 * e]) * mul,
@@ -1761,7 +1749,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 template <bool WIN>
 int bwd_grid(const BwdParams& p, int num_sms) {
     long long tiles = max_tiles(p.B, p.Tk, kTile);
-    if (WIN && p.sink_tiles) tiles += far_chunks(p.B, p.T, p.far_chunk) * p.sink_tiles;
+    if (WIN && p.sink_tiles)
+        tiles += far_chunks(p.B, p.T, p.Tk, p.far_chunk, p.window) * p.sink_tiles;
     const long long bound = tiles * p.Hkv * p.nchunks;
     return (int)(bound < num_sms ? bound : num_sms);
 }
@@ -1813,45 +1802,51 @@ cudaError_t launch_bwd_d(const BwdParams& p, int num_sms, cudaStream_t stream) {
 
 #ifdef FA_WINDOW
 
-// dK and dV of the sinks: the near unit's partial and the far chunks', summed over the
-// runs of heads, in that order.  A warp a (sequence, key/value head, sink), its lanes the
-// columns; a few thousand rows at most, behind the kernels that leave the partials.
+// dK and dV of the sinks with far rows: the near unit's partial and the far chunks', summed over
+// the runs of heads, in that order.  A CTA takes kFold sinks of a (sequence, key/value head), a
+// warp a sink, its lanes the columns; a few thousand rows at most, behind the kernels that
+// leave the partials.
+constexpr int kFold = 32;
+
 template <bool F32>
 __global__ void __launch_bounds__(256) fold_sinks_kernel(const __grid_constant__ BwdParams p) {
     pdl_begin();
     const WsHeader* hdr = static_cast<const WsHeader*>(p.workspace);
     if (hdr->error) return;  // (the schedule was refused: nothing has been written)
-    const int* tile_off = reinterpret_cast<const int*>(static_cast<const char*>(p.workspace) + p.tile_off_off);
     const float* acc = reinterpret_cast<const float*>(static_cast<const char*>(p.workspace) + p.sink_off);
-    const int heads = p.Hkv * p.nchunks, lane = lane_id();
-    const long long rows = (long long)p.B * p.Hkv * p.sinks;
-    for (long long row = (long long)blockIdx.x * 8 + warp_id(); row < rows; row += (long long)gridDim.x * 8) {
-        const int c = (int)(row % p.sinks);
-        const int g = (int)(row / p.sinks % p.Hkv), b = (int)(row / p.sinks / p.Hkv);
+    const int heads = p.Hkv * p.nchunks, lane = lane_id(), parts = cdiv(p.sinks, kFold);
+    const long long items = (long long)p.B * p.Hkv * parts;
+    for (long long item = blockIdx.x; item < items; item += gridDim.x) {
+        const int part = (int)(item % parts);
+        const int g = (int)(item / parts % p.Hkv), b = (int)(item / parts / p.Hkv);
         int t0, L, tk0, Lk;
         seq_bounds(p.cu_seqlens, p.N, b, t0, L);
         seq_bounds(p.cu_seqlens_k, p.Nk, b, tk0, Lk);
-        if (c >= Lk) continue;
-        const int slot0 = tile_off[b] / p.far_chunk + 2 * b;
-        const int slots = 1 + cdiv(cdiv(L, kTile), p.far_chunk);
-        for (int col = lane * 4; col < p.d; col += 128)
-            for (int which = 0; which < 2; ++which) {
-                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int run = 0; run < p.nchunks; ++run)
-                    for (int s = 0; s < slots; ++s) {
-                        const size_t at = ((((size_t)(slot0 + s) * 2 + which) * heads + g * p.nchunks + run) *
-                                               p.sinks + c) * p.d + col;
-                        const float4 x = *reinterpret_cast<const float4*>(acc + at);
-                        sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
-                    }
-                const size_t out = (((size_t)tk0 + c) * p.Hkv + g) * p.d + col;
-                void* base = which == 0 ? p.dk : p.dv;
-                if (F32)
-                    *reinterpret_cast<float4*>(static_cast<float*>(base) + out) = sum;
-                else
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + out) =
-                        make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
-            }
+        const int R = far_rows(Lk, p.window, p.sinks), all = far_all(p.far_chunk, L);
+        if (part * kFold >= R) continue;
+        const long long near = near_place(b, tk0, p.window, p.sinks);
+        const long long far = p.near_rows + far_place(b, t0, tk0, p.far_chunk, p.window, p.sinks);
+        for (int c = part * kFold + warp_id(); c < min(R, (part + 1) * kFold); c += 8) {
+            const int q0 = far_first(c / kTile, p.far_chunk, L, Lk, p.window, p.sinks);
+            for (int col = lane * 4; col < p.d; col += 128)
+                for (int which = 0; which < 2; ++which) {
+                    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int run = 0; run < p.nchunks; ++run)
+                        for (int q = q0 - 1; q < all; ++q) {
+                            const long long row = (q < q0 ? near : far + (long long)q * R) + c;
+                            const float4 x = *reinterpret_cast<const float4*>(
+                                acc + ((row * 2 + which) * heads + g * p.nchunks + run) * p.d + col);
+                            sum.x += x.x; sum.y += x.y; sum.z += x.z; sum.w += x.w;
+                        }
+                    const size_t out = (((size_t)tk0 + c) * p.Hkv + g) * p.d + col;
+                    void* base = which == 0 ? p.dk : p.dv;
+                    if (F32)
+                        *reinterpret_cast<float4*>(static_cast<float*>(base) + out) = sum;
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(base) + out) =
+                            make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
+                }
+        }
     }
 }
 
@@ -1862,7 +1857,7 @@ cudaError_t launch_bwd_window(const BwdParams& p, int num_sms, cudaStream_t stre
 }
 
 cudaError_t launch_fold_sinks(const BwdParams& p, int num_sms, cudaStream_t stream) {
-    const long long rows = (long long)p.B * p.Hkv * p.sinks, want = (rows + 7) / 8;
+    const long long want = (long long)p.B * p.Hkv * cdiv(p.sinks, kFold);
     const int grid = (int)(want < 8LL * num_sms ? want : 8LL * num_sms);
     return launch_pdl(p.grad_fp32 ? fold_sinks_kernel<true> : fold_sinks_kernel<false>, dim3(grid),
                       dim3(256), 0, stream, p);

@@ -35,30 +35,6 @@ __device__ __forceinline__ Scratch scratch_of(const fa_cache& c) {
     return s;
 }
 
-// Sum over the CTA's threads before this one, and the total.
-__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    auto warp_scan = [&](long long v) {
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += y;
-        }
-        return v;
-    };
-    const long long incl = warp_scan(x);
-    __syncthreads();  // (the last call's sums have been read)
-    if (lane == 31) sums[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-        const long long all = warp_scan(sums[lane]);
-        sums[lane] = all - sums[lane];
-        if (lane == 31) sums[32] = all;
-    }
-    __syncthreads();
-    total = sums[32];
-    return sums[warp] + incl - x;
-}
-
 __device__ __forceinline__ bool slot_ok(const fa_cache& c, int slot) { return slot >= 0 && slot < c.slots; }
 
 // A slot's length, or -1 when it is not one.

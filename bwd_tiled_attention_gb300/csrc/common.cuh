@@ -68,6 +68,30 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Sum over the threads of a CTA of 1024 before this one, and the total.  sums: 33 entries.
+__device__ __forceinline__ long long block_scan(long long x, long long* sums, long long& total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto warp_scan = [&](long long v) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    };
+    const long long incl = warp_scan(x);
+    __syncthreads();  // (the last call's sums have been read)
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        const long long all = warp_scan(sums[lane]);
+        sums[lane] = all - sums[lane];
+        if (lane == 31) sums[32] = all;
+    }
+    __syncthreads();
+    total = sums[32];
+    return sums[warp] + incl - x;
+}
+
 // Upper bound on tiles of `rows` rows over all sequences of a batch:
 // sum_b ceil(L_b / rows) <= ceil(T / rows) + B.
 __host__ __device__ inline long long max_tiles(int B, int T, int rows) {
@@ -140,38 +164,6 @@ __host__ __device__ inline BwdWs bwd_ws_layout(int B, int Hq, int Hkv, int Tq, i
 
 __host__ __device__ inline BwdWs bwd_ws_layout(int B, int Hq, int Hkv, int T, int d) {
     return bwd_ws_layout(B, Hq, Hkv, T, T, d);
-}
-
-// A windowed backward with sinks adds far units -- (chunk of C query tiles, tile of
-// sinks): x carries kFarUnit, the tile field is chunk * sink tiles + sink tile -- and
-// fp32 partials of the sinks' dK and dV, [slots, 2, Hkv * runs, sinks, d] (bwd.cu).
-// Slots of sequence b: tile_off[b] / C + 2 b and on, one more than it has chunks.
-// C is 16 tiles, so that a far unit is about as long as one of a window of 2000 keys,
-// or as many as there are sink tiles: the partials stay within three times dK and dV.
-constexpr int kFarUnit = 1 << 30;
-constexpr int kFarChunk = 16;
-
-// Chunks of C query tiles over all sequences, at most.
-__host__ __device__ inline long long far_chunks(int B, int Tq, int C) {
-    return max_tiles(B, Tq, kTile) / C + B + 1;
-}
-
-struct FarWs {
-    int chunk, tiles;      // query tiles of a far unit, sink tiles
-    long long max_units;   // far units, at most
-    size_t sinks, units, bytes;  // offsets of the partials and of the unit list, workspace in all
-};
-
-__host__ __device__ inline FarWs far_ws_layout(const BwdWs& w, int B, int Hkv, int Tq, int d, int sinks) {
-    FarWs f;
-    f.tiles = cdiv(sinks, kTile);
-    f.chunk = f.tiles > kFarChunk ? f.tiles : kFarChunk;
-    f.max_units = far_chunks(B, Tq, f.chunk) * f.tiles * Hkv * w.nruns;
-    const long long slots = w.max_qtiles / f.chunk + 2 * ((long long)B + 1);
-    f.sinks = w.bytes;
-    f.units = align_up(f.sinks + (size_t)slots * 2 * Hkv * w.nruns * (size_t)sinks * d * 4, kAlign);
-    f.bytes = align_up(f.units + (size_t)(w.max_units + f.max_units) * 8, kAlign);
-    return f;
 }
 
 // Causal mask with Lq queries and Lk keys: the queries are the last Lq

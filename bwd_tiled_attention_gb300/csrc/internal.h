@@ -51,7 +51,8 @@ struct BwdParams {
     int kv;                        // key boundaries differ from the query ones
     int window, sinks;             // window > 0: p sees c <= p with p - c < window or c < sinks
     int far_chunk, sink_tiles;     // query tiles of a far unit, tiles that hold sinks (0: none)
-    size_t sink_off;               // fp32 partials of the sinks' dK and dV
+    size_t sink_off;               // fp32 partials of the sinks' dK and dV (window.cuh)
+    long long near_rows;           // of them, near units' rows
 };
 
 // Writes the unit list over the tiles of `cu_seqlens` / N (T tokens) and,
@@ -60,15 +61,15 @@ struct BwdParams {
 // are key/value tiles, its semaphores query tiles).  Every length is checked
 // against its bound and both boundary arrays against their token counts; on a
 // mismatch no unit is written and the error word is set.  With sink_tiles > 0
-// the far units of a windowed backward come before the others.
+// the far units of a windowed backward come before the others (queries of the other side).
 cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int rows, int order,
                          long long max_units, void* workspace, size_t units_off,
                          size_t tile_off_off, bool want_tile_off, const int* cu_tiles_seqlens,
                          int N_tiles, int T_tiles, cudaStream_t stream, int far_chunk = 0,
-                         int sink_tiles = 0);
+                         int window = 0, int sinks = 0);
 
 // Dynamic shared memory the scheduler needs for a packed batch of B sequences
-// whose longest spans at most maxnt_bound tiles (one CTA ranks them all).
+// whose longest spans at most maxnt_bound tiles (each of its CTAs ranks them all).
 size_t sched_smem_bytes(int B, int maxnt_bound);
 
 cudaError_t launch_fwd(const FwdParams& p, int num_sms, cudaStream_t stream);

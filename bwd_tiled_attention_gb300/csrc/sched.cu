@@ -21,6 +21,11 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "window.cuh"
+
+#ifndef FA_DYNAMIC_SHARED
+#define FA_DYNAMIC_SHARED(type, name) extern __shared__ type name[]
+#endif
 
 namespace fa {
 
@@ -37,24 +42,8 @@ struct SchedArgs {
     WsHeader* header;
     int2* units;
     int* tile_off;          // int[B+1] offsets of the other side's tiles (may be null)
-    int far_chunk, sink_tiles;  // far units of a windowed backward (sink_tiles = 0: none)
+    int far_chunk, window, sinks;  // far units of a windowed backward (sinks = 0: none)
 };
-
-// Far unit u of a windowed backward whose sequences have `chunks` chunks of query tiles
-// together: in descending tile of sinks (a deterministic dQ tile takes them in that
-// order), then by chunk (counted over all sequences), heads innermost.
-struct FarEntry {
-    long long chunk;
-    int sink, head;
-};
-__device__ __forceinline__ FarEntry far_entry(const SchedArgs& a, long long chunks, long long u) {
-    FarEntry f;
-    const long long per = chunks * a.H, r = u % per;
-    f.sink = a.sink_tiles - 1 - (int)(u / per);
-    f.chunk = r / a.H;
-    f.head = (int)(r % a.H);
-    return f;
-}
 
 // Number of sequences whose tile count exceeds m, given counts sorted descending.
 __device__ __forceinline__ int count_above(const int* nt_sorted, int B, int m) {
@@ -81,22 +70,30 @@ __device__ __forceinline__ int find_slot(const long long* prefix, int n, long lo
 template <bool FAR>
 __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     pdl_begin();
-    extern __shared__ __align__(16) unsigned char sm[];
+    FA_DYNAMIC_SHARED(long long, sm64);
+    unsigned char* sm = reinterpret_cast<unsigned char*>(sm64);
     const int tid = threadIdx.x;
     const int B = a.B, H = a.H;
     // Every CTA ranks the sequences and writes its share of the list, the first one the rest.
     const long long at = (long long)blockIdx.x * kSchedThreads + tid;
     const long long step = (long long)gridDim.x * kSchedThreads;
     __shared__ long long s_total;
-    __shared__ int s_maxnt, s_bad;
+    __shared__ int s_maxnt, s_bad, s_maxfar;
+    __shared__ long long s_sums[kSchedThreads / 32 + 1];
+    const int sink_tiles = FAR ? cdiv(a.sinks, kTile) : 0;
+    // (far units come in descending tile of sinks, as a deterministic dQ tile takes them, then by
+    // sequence and chunk, heads innermost; only those that have rows are listed)
 
     if (a.cu_seqlens == nullptr) {
         // Dense batch: every sequence has nt tiles; closed-form order.
         const int nt = cdiv(a.N, a.rows);
         const int nt_aux = cdiv(a.N_aux, a.rows);
         const long long per_level = (long long)B * H;
-        const int chunks = FAR ? cdiv(nt_aux, a.far_chunk) : 0;  // of one sequence
-        const long long far = FAR ? (long long)B * chunks * a.sink_tiles * H : 0;
+        const int all = FAR ? far_all(a.far_chunk, a.N_aux) : 0;  // chunks of one sequence
+        long long far = 0;
+        if constexpr (FAR)
+            for (int j = 0; j < sink_tiles; ++j)
+                far += per_level * (all - far_first(j, a.far_chunk, a.N_aux, a.N, a.window, a.sinks));
         const long long total = far + per_level * nt;
         if (at == 0) {
             a.header->n_units = (int)(total <= a.max_units ? total : 0);
@@ -105,12 +102,18 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
             a.header->n_qtiles = B * nt_aux;
         }
         if (total > a.max_units) return;
-        if constexpr (FAR)
-            for (long long u = at; u < far; u += step) {
-                const FarEntry f = far_entry(a, (long long)B * chunks, u);
-                const int b = (int)(f.chunk / chunks), q = (int)(f.chunk % chunks);
-                a.units[u] = make_int2(b | kFarUnit, make_unit_y(q * a.sink_tiles + f.sink, f.head));
+        if constexpr (FAR) {
+            int2* out = a.units;
+            for (int j = sink_tiles - 1; j >= 0; --j) {
+                const int first = far_first(j, a.far_chunk, a.N_aux, a.N, a.window, a.sinks);
+                const int some = all - first;
+                for (long long u = at; u < per_level * some; u += step) {
+                    const int h = (int)(u % H), b = (int)(u / H / some), q = first + (int)(u / H % some);
+                    out[u] = make_int2(b | kFarUnit, make_unit_y(q * sink_tiles + j, h));
+                }
+                out += per_level * some;
             }
+        }
         for (long long u = at; u < total - far; u += step) {
             int b, tile, h;
             if (a.order == kOrderSeqDesc) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     long long* prefix = reinterpret_cast<long long*>(  // [max(B, maxnt) + 1]
         sm + align_up((size_t)3 * B * sizeof(int), 16));
     if (tid == 0) {
-        s_maxnt = 0;
+        s_maxnt = s_maxfar = 0;
         // the boundaries must span exactly the tokens the buffers hold
         s_bad = a.cu_seqlens[0] != 0 || a.cu_seqlens[B] != a.T ||
                 (a.cu_aux && (a.cu_aux[0] != 0 || a.cu_aux[B] != a.T_aux));
@@ -151,6 +154,7 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
         if (a.cu_aux) {
             const int La = a.cu_aux[b + 1] - a.cu_aux[b];
             if (La < 0 || La > a.N_aux) atomicOr(&s_bad, 1);
+            if (FAR && La > 0) atomicMax(&s_maxfar, far_rows(L, a.window, a.sinks));
         }
         const int nt = L > 0 ? cdiv(L, a.rows) : 0;
         nt_of[b] = nt;
@@ -179,27 +183,36 @@ __global__ void __launch_bounds__(kSchedThreads) sched_kernel(SchedArgs a) {
     }
     __syncthreads();
     const int maxnt = s_maxnt;
-    long long far = 0, all_chunks = 0;  // far units, chunks of all sequences
+    long long far = 0;  // far units
     if constexpr (FAR) {
-        if (tid == 0) {
-            long long acc = 0;
-            for (int b = 0; b < B; ++b) {
-                prefix[b] = acc;
-                acc += cdiv(cdiv(a.cu_aux[b + 1] - a.cu_aux[b], a.rows), a.far_chunk);
+        const int each = cdiv(B, kSchedThreads);
+        const int b0 = min(B, tid * each), b1 = min(B, b0 + each);
+        for (int j = cdiv(s_maxfar, kTile) - 1; j >= 0; --j) {
+            // chunks of sequence b with rows for tile j
+            auto first = [&](int b, int& all) {
+                const int L = a.cu_aux[b + 1] - a.cu_aux[b], Lk = a.cu_seqlens[b + 1] - a.cu_seqlens[b];
+                all = far_all(a.far_chunk, L);
+                return far_first(j, a.far_chunk, L, Lk, a.window, a.sinks);
+            };
+            long long mine = 0, total;
+            int all;
+            for (int b = b0; b < b1; ++b) {
+                prefix[b] = mine;
+                const int q0 = first(b, all);
+                mine += all - q0;
             }
-            s_total = acc;
+            const long long before = block_scan(mine, s_sums, total);
+            for (int b = b0; b < b1; ++b) prefix[b] += before;
+            __syncthreads();
+            if (far + total * H <= a.max_units)
+                for (long long u = at; u < total * H; u += step) {
+                    const int b = find_slot(prefix, B, u / H);
+                    const int q = first(b, all) + (int)(u / H - prefix[b]);
+                    a.units[far + u] = make_int2(b | kFarUnit, make_unit_y(q * sink_tiles + j, (int)(u % H)));
+                }
+            far += total * H;
+            __syncthreads();  // (prefix has been read)
         }
-        __syncthreads();
-        all_chunks = s_total;
-        far = all_chunks * a.sink_tiles * H;
-        if (far <= a.max_units)
-            for (long long u = at; u < far; u += step) {
-                const FarEntry f = far_entry(a, all_chunks, u);
-                const int b = find_slot(prefix, B, f.chunk);
-                a.units[u] = make_int2(b | kFarUnit, make_unit_y((int)(f.chunk - prefix[b]) * a.sink_tiles +
-                                                                     f.sink, f.head));
-            }
-        __syncthreads();
     }
     int nslots;
     if (a.order == kOrderSeqDesc) {
@@ -268,10 +281,11 @@ cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int 
                          long long max_units, void* workspace, size_t units_off,
                          size_t tile_off_off, bool want_tile_off, const int* cu_tiles_seqlens,
                          int N_tiles, int T_tiles, cudaStream_t stream, int far_chunk,
-                         int sink_tiles) {
+                         int window, int sinks) {
     SchedArgs a;
     a.far_chunk = far_chunk;
-    a.sink_tiles = sink_tiles;
+    a.window = window;
+    a.sinks = sinks;
     a.cu_seqlens = cu_seqlens;
     a.cu_aux = cu_tiles_seqlens;
     a.T = T;
@@ -288,7 +302,7 @@ cudaError_t launch_sched(const int* cu_seqlens, int B, int N, int T, int H, int 
     a.tile_off = want_tile_off ? reinterpret_cast<int*>(static_cast<char*>(workspace) + tile_off_off)
                                : nullptr;
     size_t smem = 0;
-    auto kern = sink_tiles ? sched_kernel<true> : sched_kernel<false>;
+    auto kern = sinks ? sched_kernel<true> : sched_kernel<false>;
     if (cu_seqlens) {
         smem = sched_smem_bytes(B, cdiv(N, rows));
         cudaError_t e = cudaFuncSetAttribute(kern,

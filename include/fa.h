@@ -240,8 +240,8 @@ fa_status fa_bwd_kv(const void* q, const void* k, const void* v, const void* dou
  *   fa_fwd_window: workspace as fa_fwd_workspace_size(B, Hq, Nq, total_q).
  *   fa_bwd_window_preprocess and fa_bwd_window take the same window and sinks, and a
  *   workspace of fa_bwd_window_workspace_size bytes: that of fa_bwd_kv and, with
- *   sinks, fp32 partials of their dK and dV (a set for every 16 query tiles, or as many
- *   as there are tiles of sinks) and a longer list of units.
+ *   sinks, fp32 partials of their dK and dV (rows of at most total_q + 2 total_k tokens
+ *   over all sequences, few where few are sinks) and a longer list of units.
  *   deterministic = 1 gives bit-identical dq, dk and dv from run to run.
  *   Values of keys that a row does not see must be finite, as in the other calls:
  *   they enter the tensor core with a weight of 0.
