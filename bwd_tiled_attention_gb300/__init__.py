@@ -89,6 +89,8 @@ _SIGS = {
     "fa_cache_fork": (_i, [_vp, _vp, _vp, _i, _vp]),
     "fa_cache_free": (_i, [_vp, _vp, _i, _vp]),
     "fa_cache_accept": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _i, _vp]),
+    "fa_cache_fork_weights": (_i, [_vp, _vp, _vp, _vp, _i, _vp]),
+    "fa_cache_accept_weights": (_i, [_vp, _vp, _vp, _vp, _i, _vp, _vp, _i, _vp]),
     "fa_cache_check": (_i, [_vp, _vp, _vp]),
     "fa_cache_append": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _ll, _ll, _vp, _ll, _ll,
                              _vp, _ll, _ll, _i, _vp, _i, _vp, _i, _i, _vp]),

@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kPlan) accept_plan_kernel(const fa_cache c, co
                     s.shadow[(long long)slot * c.max_pages + k] = p;
                 }
             }
+            if (grp.sub == 0) s.entry[i] = make_int4(slot, len, b, m);  // for the weights' kernel
         }
         if (bad) atomicOr(&error, bad);
     }
@@ -426,6 +427,45 @@ __global__ void __launch_bounds__(kMoveThreads) accept_move_kernel(const fa_cach
     }
 }
 
+// The weights that keys have received (weights.cu) go with their rows: an accepted token's move
+// to its place, those of the dropped ones become 0.  A warp a (sequence, layer, head), which reads
+// 32 before it writes them; path ascends strictly, as above.
+__global__ void __launch_bounds__(kMoveThreads) accept_weights_kernel(const fa_cache c, const int* path,
+                                                                      int width, float* weights, int units) {
+    pdl_begin();
+    const Scratch s = scratch_of(c);
+    if (!*s.go) return;
+    const int unit = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (unit >= units) return;
+    const int planes = c.layers * c.heads, i = unit / planes;
+    const int layer = unit % planes / c.heads, head = unit % c.heads;
+    const int4 e = s.entry[i];  // slot, length before, base, accepted
+    float* w = weights + (((long long)layer * c.slots + e.x) * c.heads + head) * c.max_pages * c.page_size + e.z;
+    const int* at = path + (long long)i * width;
+    for (int j0 = 0; j0 < e.w; j0 += 32) {
+        const int j = j0 + lane;
+        const float x = j < e.w ? w[at[j]] : 0.f;
+        __syncwarp();
+        if (j < e.w) w[j] = x;
+    }
+    for (int j = e.w + lane; j < e.y - e.z; j += 32) w[j] = 0.f;
+}
+
+// A child's weights are its parent's, and 0 behind them: a CTA a (child, layer, head).
+__global__ void __launch_bounds__(256) fork_weights_kernel(const fa_cache c, const int* parents,
+                                                           const int* children, float* weights) {
+    pdl_begin();
+    const Scratch s = scratch_of(c);
+    if (!*s.go) return;
+    const int planes = c.layers * c.heads, i = blockIdx.x / planes;
+    const int layer = blockIdx.x % planes / c.heads, head = blockIdx.x % c.heads;
+    const int room = c.max_pages * c.page_size, len = c.lengths[children[i]];
+    auto row = [&](int slot) { return weights + (((long long)layer * c.slots + slot) * c.heads + head) * room; };
+    const float* from = row(parents[i]);
+    float* to = row(children[i]);
+    for (int j = threadIdx.x; j < room; j += 256) to[j] = j < len ? from[j] : 0.f;
+}
+
 // Takes the bits that have been read out of the status word, and no others: calls
 // on other streams may have set some since.
 __global__ void clear_kernel(int* status, int bits) {
@@ -438,6 +478,53 @@ fa_status launched(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUD
 
 // A list of device integers.
 bool list_ok(const int* p) { return p && aligned(p, 4); }
+
+// (sequence, layer, head) triples of a call on weights; < 0: too many.
+long long weight_rows(const fa_cache& c, int n) {
+    const long long units = (long long)n * c.layers * c.heads;
+    return units > 0x7FFFFFFFLL - kMoveThreads ? -1 : units;
+}
+
+// weights = nullptr: none.
+fa_status fork_impl(const fa_cache* cache, const int* parents, const int* children, float* weights, int n,
+                    fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0 || n > cache->slots) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(parents) || !list_ok(children)) return FA_ERR_INVALID_ARG;
+    if (weights && weight_rows(*cache, n) < 0) return FA_ERR_UNSUPPORTED;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, parents, children, n);
+    if (e == cudaSuccess)
+        e = launch_pdl(fork_copy_kernel, dim3(n, cache->layers * 2), dim3(256), 0, strm, *cache);
+    if (e == cudaSuccess && weights)
+        e = launch_pdl(fork_weights_kernel, dim3((unsigned)weight_rows(*cache, n)), dim3(256), 0, strm, *cache,
+                       parents, children, weights);
+    return launched(e);
+}
+
+fa_status accept_impl(const fa_cache* cache, const int* slots, const int* base, const int* path, int width,
+                      const int* accepted, float* weights, int n, fa_stream_t stream) {
+    const fa_status st = check_cache(cache);
+    if (st != FA_OK) return st;
+    if (n < 0 || n > cache->slots || width < 0) return FA_ERR_INVALID_ARG;
+    if (n == 0) return FA_OK;
+    if (!list_ok(slots) || !list_ok(base) || !list_ok(accepted) || (width > 0 && !list_ok(path)))
+        return FA_ERR_INVALID_ARG;
+    const long long units = weight_rows(*cache, n);
+    if (weights && units < 0) return FA_ERR_UNSUPPORTED;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_pdl(accept_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, slots, base, path,
+                               width, accepted, n);
+    if (e == cudaSuccess && width > 0)
+        e = launch_pdl(accept_move_kernel, dim3(n, cdiv(cache->layers, kMoveLayers) * 2), dim3(kMoveThreads),
+                       0, strm, *cache, slots, base, path, width, accepted);
+    if (e == cudaSuccess && weights)
+        e = launch_pdl(accept_weights_kernel, dim3((unsigned)((units + 3) / 4)), dim3(kMoveThreads), 0, strm,
+                       *cache, path, width, weights, (int)units);
+    return launched(e);
+}
 
 }  // namespace
 
@@ -484,16 +571,13 @@ fa_status fa_cache_reserve(const fa_cache* cache, const int* slots, const int* c
 
 fa_status fa_cache_fork(const fa_cache* cache, const int* parents, const int* children, int n,
                         fa_stream_t stream) {
-    const fa_status st = check_cache(cache);
-    if (st != FA_OK) return st;
-    if (n < 0 || n > cache->slots) return FA_ERR_INVALID_ARG;
-    if (n == 0) return FA_OK;
-    if (!list_ok(parents) || !list_ok(children)) return FA_ERR_INVALID_ARG;
-    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_pdl(fork_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, parents,
-                                     children, n);
-    if (e != cudaSuccess) return FA_ERR_CUDA;
-    return launched(launch_pdl(fork_copy_kernel, dim3(n, cache->layers * 2), dim3(256), 0, strm, *cache));
+    return fork_impl(cache, parents, children, nullptr, n, stream);
+}
+
+fa_status fa_cache_fork_weights(const fa_cache* cache, const int* parents, const int* children,
+                                float* weights, int n, fa_stream_t stream) {
+    if (n > 0 && (!weights || !aligned(weights, 4))) return FA_ERR_INVALID_ARG;
+    return fork_impl(cache, parents, children, weights, n, stream);
 }
 
 fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_stream_t stream) {
@@ -509,20 +593,14 @@ fa_status fa_cache_free(const fa_cache* cache, const int* slots, int n, fa_strea
 
 fa_status fa_cache_accept(const fa_cache* cache, const int* slots, const int* base, const int* path,
                           int path_width, const int* accepted, int n, fa_stream_t stream) {
-    const fa_status st = check_cache(cache);
-    if (st != FA_OK) return st;
-    if (n < 0 || n > cache->slots || path_width < 0) return FA_ERR_INVALID_ARG;
-    if (n == 0) return FA_OK;
-    if (!list_ok(slots) || !list_ok(base) || !list_ok(accepted) || (path_width > 0 && !list_ok(path)))
-        return FA_ERR_INVALID_ARG;
-    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_pdl(accept_plan_kernel, dim3(1), dim3(kPlan), 0, strm, *cache, slots,
-                                     base, path, path_width, accepted, n);
-    if (e != cudaSuccess) return FA_ERR_CUDA;
-    if (path_width == 0) return FA_OK;
-    return launched(launch_pdl(accept_move_kernel, dim3(n, cdiv(cache->layers, kMoveLayers) * 2),
-                               dim3(kMoveThreads), 0, strm,
-                               *cache, slots, base, path, path_width, accepted));
+    return accept_impl(cache, slots, base, path, path_width, accepted, nullptr, n, stream);
+}
+
+fa_status fa_cache_accept_weights(const fa_cache* cache, const int* slots, const int* base,
+                                  const int* path, int path_width, const int* accepted, float* weights,
+                                  int n, fa_stream_t stream) {
+    if (n > 0 && (!weights || !aligned(weights, 4))) return FA_ERR_INVALID_ARG;
+    return accept_impl(cache, slots, base, path, path_width, accepted, weights, n, stream);
 }
 
 fa_status fa_cache_check(const fa_cache* cache, int* bits, fa_stream_t stream) {

@@ -21,6 +21,7 @@ A cache that stays within a budget adds up what each key receives, and drops tho
 least (`weights`: fp32 ``[layers, cache.slots, heads, max_pages * page_size]``, zeros at first)::
 
     fa.cache_weights(q, lse, cache, layer, slots, weights[layer])     # behind tree_attention
+    cache.accept(slots, base, path, accepted, weights=weights)        # rows move with their weights
     cache.evict(slots, weights, keep, recent, sinks=4)                # every so many tokens
 """
 from __future__ import annotations
@@ -449,14 +450,27 @@ class PagedCache:
         self._call("fa_cache_reserve", stream, (slots, many), slots.data_ptr(), _ptr(many),
                    counts, n)
 
-    def fork(self, parents, children, stream=None):
+    def _weights(self, weights, what):
+        """Weights of all layers, as `cache_weights` adds them up."""
+        _want("weights", weights, (torch.float32,), 4, self.device)
+        shape = (self.layers, self.slots, self.heads, self.max_pages * self.page_size)
+        if tuple(weights.shape) != shape:
+            raise ValueError(f"weights must be {shape}, got {tuple(weights.shape)}")
+        _not_differentiable(what, weights, self.k, self.v)
+
+    def fork(self, parents, children, stream=None, weights=None):
         """children[i], which must be empty, becomes a copy of parents[i]: whole pages are shared,
-        a partly filled last page is copied."""
+        a partly filled last page is copied.  ``weights`` (those of `evict`): children's become their
+        parents', 0 behind them."""
         n = self._list("parents", parents).shape[0]
         self._list("children", children, n)
         self._few(n)
-        self._call("fa_cache_fork", stream, (parents, children), parents.data_ptr(),
-                   children.data_ptr(), n)
+        if weights is None:
+            return self._call("fa_cache_fork", stream, (parents, children), parents.data_ptr(),
+                              children.data_ptr(), n)
+        self._weights(weights, "fork")
+        self._call("fa_cache_fork_weights", stream, (parents, children, weights), parents.data_ptr(),
+                   children.data_ptr(), weights.data_ptr(), n)
 
     def free(self, slots, stream=None):
         """Empties slots; pages that no other slot holds are free again."""
@@ -465,9 +479,10 @@ class PagedCache:
             _too_far("slots", slots)
         self._call("fa_cache_free", stream, (slots,), slots.data_ptr(), n)
 
-    def accept(self, slots, base, path, accepted, stream=None):
+    def accept(self, slots, base, path, accepted, stream=None, weights=None):
         """Of the tokens behind position base[i], keeps path[i, :accepted[i]] (strictly ascending
-        indices behind base, int32 ``[n, width]``), moved together, and drops the others."""
+        indices behind base, int32 ``[n, width]``), moved together, and drops the others.
+        ``weights`` (those of `evict`) move with the kept tokens, and the dropped ones' become 0."""
         n = self._list("slots", slots).shape[0]
         self._few(n)
         self._list("base", base, n)
@@ -475,6 +490,11 @@ class PagedCache:
         if path.shape[1] > _MOST:
             _too_far("path", path)
         self._list("accepted", accepted, n)
+        if weights is not None:
+            self._weights(weights, "accept")
+            return self._call("fa_cache_accept_weights", stream, (slots, base, path, accepted, weights),
+                              slots.data_ptr(), base.data_ptr(), path.data_ptr(), path.shape[1],
+                              accepted.data_ptr(), weights.data_ptr(), n)
         self._call("fa_cache_accept", stream, (slots, base, path, accepted), slots.data_ptr(),
                    base.data_ptr(), path.data_ptr(), path.shape[1], accepted.data_ptr(), n)
 
@@ -493,11 +513,7 @@ class PagedCache:
         """
         n = self._list("slots", slots).shape[0]
         self._few(n)
-        _want("weights", weights, (torch.float32,), 4, self.device)
-        shape = (self.layers, self.slots, self.heads, self.max_pages * self.page_size)
-        if tuple(weights.shape) != shape:
-            raise ValueError(f"weights must be {shape}, got {tuple(weights.shape)}")
-        _not_differentiable("evict", weights, self.k, self.v)
+        self._weights(weights, "evict")
         recent, sinks = _whole("recent", recent), _whole("sinks", sinks)
         if recent < 0 or sinks < 0 or recent + sinks > _MOST:
             raise ValueError(f"recent and sinks must not be negative, nor above {_MOST} together")
@@ -724,6 +740,11 @@ def cache_weights(q, lse, cache, layer, slots, weights, mask=None, scale=None, c
     of one layer; places of other slots and behind a sequence's end are left alone.  Any part of a
     prompt may be asked, for instance only its last tokens.  A row whose lse is -inf gives
     nothing.  Not differentiable.
+
+    Of a drafted tree every row counts, those that are rejected later too: fill their lse with
+    -inf, or call this behind `PagedCache.accept`, with the accepted tokens' rows of q and lse and
+    no mask.  Weights go with their rows when `accept` and `fork` are given them; a slot that is
+    used again begins with zeros.
     """
     n = _of_cache(cache, layer, slots)
     dev = cache.device

@@ -538,13 +538,32 @@ fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots,
  * ------------------------------------------------------------------------
  * weights: device fp32, for each layer [slots, heads, max_pages * page_size]: what the
  * key in each place has received so far.  The caller zeroes them when a slot begins.
+ * Operations that move rows have forms that take the weights of all layers, [layers, slots,
+ * heads, max_pages * page_size], along; a cache with weights is forked and its drafts are
+ * accepted by those.
  */
+
+/*
+ * fa_cache_fork, and children[i]'s weights become those of parents[i], 0 behind its length.
+ */
+fa_status fa_cache_fork_weights(const fa_cache* cache, const int* parents, const int* children,
+                                float* weights, int n, fa_stream_t stream);
+
+/*
+ * fa_cache_accept, and the weight of token base[i] + path[i][j] moves to base[i] + j; those of
+ * places from base[i] + accepted[i] to the length before become 0.
+ */
+fa_status fa_cache_accept_weights(const fa_cache* cache, const int* slots, const int* base,
+                                  const int* path, int path_width, const int* accepted, float* weights,
+                                  int n, fa_stream_t stream);
 
 /*
  * Adds to weights[slot, head, j] (one layer's) the attention that the key in place j
  * receives from the call's rows: the sum, over the tokens that see it and the query
  * heads of its head, of exp(scale * q.k - lse).  Sequences, q and mask as in
  * fa_tree_fwd, whose lse [Hq,T] this takes; scale positive and finite.
+ *   Of a drafted tree every row counts, rejected ones too, unless its lse is -inf; or call
+ *   this behind fa_cache_accept, with the accepted tokens' rows of q and lse and no mask.
  *   A row with lse = -inf gives nothing.  Sums are fp32, each key's in one addition, so
  *   that results do not vary from run to run.  A slot that the call names several
  *   times receives all sums (in any order).  Places behind a sequence's length are
