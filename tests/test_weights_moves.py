@@ -83,7 +83,8 @@ def test_on_the_host(library, order, layers, heads):
                                        (dict(n=0, w=None), 0)])
 def test_bad_calls_are_refused(kw, status):
     fabuild.build()
-    c = ctypes.addressof(desc())
+    held = desc()
+    c = ctypes.addressof(held)
     x = dict(a=FAKE, b=FAKE, path=FAKE, width=3, acc=FAKE, w=FAKE, n=2)
     x.update(kw)
     assert fa.lib().fa_cache_accept_weights(c, x["a"], x["b"], x["path"], x["width"], x["acc"], x["w"], x["n"], None) == status
