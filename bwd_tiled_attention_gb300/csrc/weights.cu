@@ -27,7 +27,7 @@
 // of 128, one token each, 130 us = 6.4 TB/s, 94% of a copy (32 sequences, 16 heads: d = 64,
 // 8 key heads, 41 us at 5.2 TB/s; d = 192 and 256, 4 key heads, 53 and 68 us at 5.9 and 6.1).
 // 64-128 tokens over 8-16k in 4 sequences, 32 + 8 heads of 128: 60 us, of which ~8 are the
-// start and the first Q tiles; 2048 tokens over 4-6k in 2: 312 us = 685 TF/s.  One token over
+// start and the first Q tiles; 2048 tokens over 4-6k in 2: 315 us = 678 TF/s.  One token over
 // 501 keys 6.1 us.
 //
 // A key's sum goes to memory as one addition of the whole call (one a turn, by the same
@@ -99,7 +99,8 @@ struct Smem {
     alignas(1024) uint8_t k[C::kStages][C::kStageBytes];
     alignas(16) float nl[C::kQBufs][NQ];  // -LSE log2 e of the Q tile's rows
     alignas(8) uint64_t full[C::kStages], empty[C::kStages];
-    uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];
+    uint64_t q_land[C::kQBufs];  // a Q tile's TMA
+    uint64_t q_full[C::kQBufs], q_empty[C::kQBufs];  // its LSE (and rows cleared), its last reader
     uint64_t piece_full[2], piece_empty[2];
     uint64_t s_full[C::kBuffers], s_free[C::kBuffers];
     // MANY: the second warpgroup's sums, and that they are there.  It is less than four key
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
             mbar_init(smem_u32(&sm.empty[s]), 1);
         }
         for (int i = 0; i < QB; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), 2);
+            mbar_init(smem_u32(&sm.q_land[i]), 1);
+            mbar_init(smem_u32(&sm.q_full[i]), 1);
             mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);
         }
         for (int i = 0; i < 2; ++i) {
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                     const int qs = g % QB;
                     if (!(ok = warp_wait(smem_u32(&sm.q_empty[qs]), ((g / QB) & 1) ^ 1, stop, status)))
                         break;
-                    const uint32_t bar = smem_u32(&sm.q_full[qs]);
+                    const uint32_t bar = smem_u32(&sm.q_land[qs]);
                     const int tok = x.tok0 + qt * p.tile_tokens;
                     const int rows = min(p.tile_tokens, x.n - qt * p.tile_tokens) * p.group;
                     if (lane == 0) {
@@ -455,14 +457,32 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
 #pragma unroll
                     for (int i = 0; i < NQ / 32; ++i)  // (a row that sees nothing gives nothing)
                         sm.nl[qs][i * 32 + lane] = l[i] == -INFINITY ? -INFINITY : -l[i] * 1.4426950408889634f;
+                    // ... whatever its q holds: scores that are not finite would not vanish (-inf + inf
+                    // is NaN), so such rows are cleared.  (This 312 -> 315 us; looking at each sum for NaN: 317)
+                    bool gone = false;
+#pragma unroll
+                    for (int i = 0; i < NQ / 32; ++i) gone |= l[i] == -INFINITY;
+                    if (__any_sync(0xffffffffu, gone)) {
+                        if (!(ok = warp_wait(bar, (g / QB) & 1, stop, status))) {
+                            ++g;
+                            break;
+                        }
+#pragma unroll
+                        for (int i = 0; i < NQ / 32; ++i)
+                            if (l[i] == -INFINITY)
+                                for (int c = 0; c < C::kCols * 8; ++c)
+                                    *reinterpret_cast<uint4*>(sm.q[qs] + (c >> 3) * (NQ * 128) + (i * 32 + lane) * 128 +
+                                                              (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar);
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[qs]));
                 }
             }
         }
         if (!ok && lane == 0)
             for (int i = 0; i < QB && i < g; ++i)
-                mbar_wait(smem_u32(&sm.q_full[(g - 1 - i) % QB]), ((g - 1 - i) / QB) & 1, &sm.zero);
+                mbar_wait(smem_u32(&sm.q_land[(g - 1 - i) % QB]), ((g - 1 - i) / QB) & 1, &sm.zero);
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
@@ -488,7 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1) weights_kernel(const __grid_const
                 for (int qt = 0; qt < nq && ok; ++qt) {
                     const int gq = g + qt, w = MANY ? 0 : j & 1;
                     const int bf = (MANY ? 0 : 2 * w) + (cnt[w] & 1);
-                    if (j == 0 && !wait(sm.q_full[gq % QB], gq / QB)) break;
+                    if (j == 0) {
+                        const bool q_in = mbar_test_wait(smem_u32(&sm.q_land[gq % QB]), (gq / QB) & 1);
+                        const bool l_in = mbar_test_wait(smem_u32(&sm.q_full[gq % QB]), (gq / QB) & 1);
+                        if (!__all_sync(0xffffffffu, q_in) && !wait(sm.q_land[gq % QB], gq / QB)) break;
+                        if (!__all_sync(0xffffffffu, l_in) && !wait(sm.q_full[gq % QB], gq / QB)) break;
+                    }
                     // (a wait takes ~140 cycles even when nothing is missing: both are looked
                     // up at once first.  Each is at most a phase behind.)
                     const bool k_in = qt > 0 || mbar_test_wait(smem_u32(&sm.full[f % S]), (f / S) & 1);
