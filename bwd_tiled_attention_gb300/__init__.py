@@ -35,7 +35,7 @@ __all__ = [
     "fa_status_string", "forward", "backward", "attention", "FA_OK", "FA_ERR_INVALID_ARG",
     "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT", "FA_BF16", "FA_FP32",
     "PagedCache", "rotary", "rotary_table", "cache_append", "tree_attention", "tree_mask",
-    "cache_weights",
+    "cache_weights", "window_mask",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -101,6 +101,9 @@ _SIGS = {
     "fa_tree_mask": (_i, [_vp, _vp, _i, _i, _i, _i, _vp, _vp]),
     "fa_tree_fwd_window": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp,
                                 _f, _i, _i, _i, _vp, _sz, _vp]),
+    "fa_tree_window_mask": (_i, [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp]),
+    "fa_tree_fwd_window_depth": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp,
+                                      _vp, _vp, _f, _i, _i, _i, _vp, _sz, _vp]),
     "fa_tree_fwd": (_i, [_vp, _i, _vp, _i, _i, _vp, _i, _vp, _i, _ll, _ll, _vp, _i, _vp, _vp, _f,
                          _i, _vp, _sz, _vp]),
 }
@@ -542,4 +545,4 @@ def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=Non
 
 from . import serving  # noqa: E402  (uses the binding above)
 from .serving import (PagedCache, cache_append, cache_weights, rotary, rotary_table,  # noqa: E402
-                      tree_attention, tree_mask)
+                      tree_attention, tree_mask, window_mask)

@@ -127,6 +127,7 @@ struct TreeParams {
     int clear_odd;                 // one more slice of the join kernel does so between odd boundaries
     float scale_log2;
     int window, sinks;             // window > 0: p sees key j when p - j < window or j < sinks
+    const int* depth;              // tokens' places behind the context, or null: as the mask says
 };
 
 // The attention over the cache with a window (tree_window.cu).

@@ -55,7 +55,9 @@
 // row's window does; everything else -- the line, the split, the join -- counts tiles as
 // before, and a tile of the count is turned into one of the sequence where keys are
 // named.  A drafted token stands as many places behind the context as its row names
-// others of the call's own tokens, and the window hides keys of the context alone.
+// others of the call's own tokens, or as its depth says, and the window hides keys of the
+// context alone: where drafts may be deeper than the window, the mask leaves out what it hides
+// of them (tree_near_kernel, once a step for all layers).
 // Measured, 64 sequences of 8-16k tokens, 32 + 8 heads of 128, one token each, W = 4096, S =
 // 16: 171 us = 6.3 TB/s of visible keys and values; one token over 5001, W = 512, 16 heads
 // 12.5 us; 16 sequences of 16k, 512 tokens each, W = 1024: 249 us = 555 TF/s.
@@ -177,21 +179,28 @@ struct Sight {
     }
 };
 
-// First key of the window of token `trow` of its sequence (0: no window); words: its row
-// of the mask, or null.
-__device__ __forceinline__ int window_from(const TreeParams& p, const Piece& x, const uint32_t* words,
-                                           int trow) {
-    if constexpr (!kWin) return 0;
-    if (!p.mask) return x.ctx + trow - p.window + 1;
+// Tokens of its sequence's n own ones, other than itself, that token `trow` names in its row of
+// the mask.
+__device__ __forceinline__ int named_others(const uint32_t* row, int words, int n, int trow) {
     int others = 0;
-    const int n = x.len - x.ctx;
 #pragma unroll 1
-    for (int w = 0; w * 32 < n && w < 2 * p.words; ++w) {
-        uint32_t bits = words[w];
+    for (int w = 0; w * 32 < n && w < 2 * words; ++w) {
+        uint32_t bits = row[w];
         if (n - w * 32 < 32) bits &= (1u << (n - w * 32)) - 1u;
         if (trow >> 5 == w) bits &= ~(1u << (trow & 31));
         others += __popc(bits);
     }
+    return others;
+}
+
+// First key of the window of token `trow` of its sequence (0: no window); words: its row
+// of the mask, or null; tok: its place in the batch.
+__device__ __forceinline__ int window_from(const TreeParams& p, const Piece& x, const uint32_t* words,
+                                           int trow, size_t tok) {
+    if constexpr (!kWin) return 0;
+    if (!p.mask) return x.ctx + trow - p.window + 1;
+    const int n = x.len - x.ctx;
+    const int others = p.depth ? max(0, min(p.depth[tok], n - 1)) : named_others(words, p.words, n, trow);
     return min(x.ctx, x.ctx + others - p.window + 1);
 }
 
@@ -646,7 +655,7 @@ __device__ __forceinline__ void store_few(const TreeParams& p, const Piece& x, c
             ? reinterpret_cast<const uint32_t*>(p.mask) + tok * (2 * (size_t)p.words) : nullptr;
         const int limit = p.mask ? x.len : min(x.len, x.ctx + x.trow0 + row_tok + 1);
         const int ps = p.cache.page_size;
-        const int from = window_from(p, x, words, x.trow0 + row_tok);
+        const int from = window_from(p, x, words, x.trow0 + row_tok, tok);
         const int skip = kWin || odd ? 0 : max(0, sight.open - x.tile_key(0, BN));  // (tiles in a row)
         for (int i = skip; i < x.n * BN && sum == sum; ++i) {
             const int key = x.tile_key(i / BN, BN) + i % BN;
@@ -1129,7 +1138,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
             const uint32_t* words = p.mask
                 ? reinterpret_cast<const uint32_t*>(p.mask) + (valid ? tok : 0) * (2 * (size_t)p.words)
                 : nullptr;
-            const int from = window_from(p, x, words, trow);
+            const int from = window_from(p, x, words, trow, valid ? tok : 0);
             const bool active = PAIR ? ntok > 0 : (C::kStreams == 2 || w == 0);
             const int step = PAIR || C::kStreams == 1 ? 1 : 2;
             float m_ref = -INFINITY, l = 0.f;
@@ -1748,6 +1757,46 @@ __global__ void tree_mask_kernel(const int* parents, const int* cu, int B, int N
     }
 }
 
+// The window among the call's own tokens: depth[t] is the number of others that token t names,
+// and of these it keeps in `out` those less than `window` above it, and those whose position is
+// one of the first `sinks`.  A thread a row, then a thread a word of one.
+__global__ void tree_depth_kernel(const uint32_t* mask, const int* cu, int B, int N, int T, int words, int* depth) {
+    pdl_begin();
+    const int t = blockIdx.x * blockDim.x + threadIdx.x;
+    if (t >= T) return;
+    const int b = seq_of_token(cu, B, N, t);
+    int d = 0;
+    if (b >= 0) {
+        const SeqRange r = seq_range(cu, N, T, b);
+        if (t - r.t0 < r.n) d = named_others(mask + (size_t)t * 2 * words, words, r.n, t - r.t0);
+    }
+    depth[t] = d;
+}
+__global__ void tree_near_kernel(const fa_cache c, const int* slots, const unsigned long long* mask, const int* cu,
+                                 int B, int N, int T, int words, int window, int sinks, unsigned long long* out,
+                                 const int* depth) {
+    pdl_begin();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= (long long)T * words) return;
+    const int t = (int)(i / words), first = (int)(i - (long long)t * words) * 64;
+    const int b = seq_of_token(cu, B, N, t);
+    unsigned long long left = 0;
+    if (b >= 0) {
+        const SeqRange r = seq_range(cu, N, T, b);
+        const int slot = slots[b];
+        const int ctx = slot >= 0 && slot < c.slots ? c.lengths[slot] - r.n : 0;
+        unsigned long long bits = t - r.t0 < r.n ? mask[i] : 0;
+        if (r.n - first < 64) bits &= r.n > first ? (1ull << (r.n - first)) - 1 : 0;
+        const int mine = depth[t];
+        for (; bits; bits &= bits - 1) {
+            const int a = first + __ffsll((long long)bits) - 1, at = depth[r.t0 + a];
+            if (r.t0 + a == t || (long long)mine - at < window || (long long)ctx + at < sinks)
+                left |= bits & -bits;
+        }
+    }
+    out[i] = left;
+}
+
 // Row tiles: as many whole tokens (of group rows each) as 128 rows hold; more
 // rows than that take them in pairs where TMEM has two accumulators.
 struct Tiles {
@@ -1794,8 +1843,8 @@ bool aligned(const void* p, unsigned a) { return (reinterpret_cast<uintptr_t>(p)
 fa_status tree_impl(const fa_cache* cache, int layer, const int* slots, int B, int N,
                     const int* cu_seqlens, int T, const void* q, int Hq, long long q_token_stride,
                     long long q_head_stride, const void* mask, int mask_words, void* o, float* lse,
-                    float scale, int window, int sinks, int zero_rest, void* workspace,
-                    size_t workspace_bytes, fa_stream_t stream) {
+                    float scale, int window, int sinks, const int* depth, int zero_rest,
+                    void* workspace, size_t workspace_bytes, fa_stream_t stream) {
     const fa_status cs = check_cache(cache);
     if (cs != FA_OK) return cs;
     const int d = cache->d, Hkv = cache->heads;
@@ -1810,7 +1859,7 @@ fa_status tree_impl(const fa_cache* cache, int layer, const int* slots, int B, i
     if ((B > 0 && !slots) || !q || !o || !lse || !workspace) return FA_ERR_INVALID_ARG;
     if (N == 0) N = 1;  // (a packed batch of empty sequences)
     if (!aligned(slots, 4) || !aligned(cu_seqlens, 4) || !aligned(q, 16) || !aligned(o, 16) ||
-        !aligned(lse, 4) || !aligned(mask, 8) || !aligned(workspace, 16))
+        !aligned(lse, 4) || !aligned(mask, 8) || !aligned(depth, 4) || !aligned(workspace, 16))
         return FA_ERR_INVALID_ARG;
     if (T == 1) q_token_stride = (long long)Hq * d;  // (a stride that is never taken)
     if (Hq == 1) q_head_stride = d;
@@ -1855,6 +1904,7 @@ fa_status tree_impl(const fa_cache* cache, int layer, const int* slots, int B, i
     if (window > 0 && window < room && sinks < room) {
         p.window = window;
         p.sinks = sinks;
+        p.depth = mask ? depth : nullptr;
     }
     p.scale_log2 = scale * 1.4426950408889634f;
     const int nsm = device_sms();
@@ -1898,7 +1948,7 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
                       float scale, int zero_rest, void* workspace, size_t workspace_bytes,
                       fa_stream_t stream) {
     return tree_impl(cache, layer, slots, B, N, cu_seqlens, T, q, Hq, q_token_stride, q_head_stride,
-                     mask, mask_words, o, lse, scale, 0, 0, zero_rest, workspace, workspace_bytes,
+                     mask, mask_words, o, lse, scale, 0, 0, nullptr, zero_rest, workspace, workspace_bytes,
                      stream);
 }
 
@@ -1910,8 +1960,43 @@ fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots,
                              fa_stream_t stream) {
     if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
     return tree_impl(cache, layer, slots, B, N, cu_seqlens, T, q, Hq, q_token_stride, q_head_stride,
-                     mask, mask_words, o, lse, scale, window, sinks, zero_rest, workspace,
+                     mask, mask_words, o, lse, scale, window, sinks, nullptr, zero_rest, workspace,
                      workspace_bytes, stream);
+}
+
+fa_status fa_tree_fwd_window_depth(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                                   const int* cu_seqlens, int T, const void* q, int Hq,
+                                   long long q_token_stride, long long q_head_stride, const void* mask,
+                                   int mask_words, const int* depth, void* o, float* lse, float scale,
+                                   int window, int sinks, int zero_rest, void* workspace,
+                                   size_t workspace_bytes, fa_stream_t stream) {
+    if (window < 1 || sinks < 0 || (T > 0 && (!mask || !depth))) return FA_ERR_INVALID_ARG;
+    return tree_impl(cache, layer, slots, B, N, cu_seqlens, T, q, Hq, q_token_stride, q_head_stride,
+                     mask, mask_words, o, lse, scale, window, sinks, depth, zero_rest, workspace,
+                     workspace_bytes, stream);
+}
+
+fa_status fa_tree_window_mask(const fa_cache* cache, const int* slots, int B, int N,
+                              const int* cu_seqlens, int T, const void* mask, int words, int window,
+                              int sinks, void* out, int* depth, fa_stream_t stream) {
+    const fa_status cs = check_cache(cache);
+    if (cs != FA_OK) return cs;
+    if (B < 0 || N < 0 || T < 0 || words <= 0 || (long long)words * 64 < N || window < 1 || sinks < 0)
+        return FA_ERR_INVALID_ARG;
+    if (!cu_seqlens && (long long)B * N != T) return FA_ERR_INVALID_ARG;
+    if (B > kMostSequences || (long long)T * words > (1LL << 38)) return FA_ERR_UNSUPPORTED;
+    if (T == 0) return FA_OK;
+    if ((B > 0 && !slots) || !mask || !out || !depth || !aligned(slots, 4) || !aligned(cu_seqlens, 4) ||
+        !aligned(mask, 8) || !aligned(out, 8) || !aligned(depth, 4))
+        return FA_ERR_INVALID_ARG;
+    cudaStream_t strm = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = launch_pdl(tree_depth_kernel, dim3(cdiv(T, 128)), dim3(128), 0, strm,
+                               static_cast<const uint32_t*>(mask), cu_seqlens, B, N, T, words, depth);
+    if (e == cudaSuccess)
+        e = launch_pdl(tree_near_kernel, dim3((unsigned)(((long long)T * words + 127) / 128)), dim3(128), 0, strm,
+                       *cache, slots, static_cast<const unsigned long long*>(mask), cu_seqlens, B, N, T, words,
+                       window, sinks, static_cast<unsigned long long*>(out), static_cast<const int*>(depth));
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

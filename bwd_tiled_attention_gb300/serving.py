@@ -37,7 +37,7 @@ from torch.autograd import forward_ad
 from . import FA_BF16, FA_FP32, FA_OK, FAError, lib
 
 __all__ = ["PagedCache", "rotary", "rotary_table", "cache_append", "cache_weights", "tree_attention",
-           "tree_mask"]
+           "tree_mask", "window_mask"]
 
 _INT = (torch.int32,)
 _BF16 = (torch.bfloat16,)
@@ -633,13 +633,57 @@ def tree_mask(parents, cu_seqlens=None, max_seqlen=None, batch=None, stream=None
     return mask
 
 
+def _window(window, sinks):
+    window, sinks = _whole("window", window), _whole("sinks", sinks)
+    if not (1 <= window <= _MOST and 0 <= sinks <= _MOST):
+        raise ValueError(f"window must be from 1 to {_MOST}, sinks from 0, got {window} and {sinks}")
+    return window, sinks
+
+
+def _mask_words(mask, T, N, device):
+    _want("mask", mask, (torch.int64,), 2, device)
+    rows, words = mask.shape
+    if rows != T or 64 * words < N:
+        raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
+    if words > _MOST:
+        _too_far("mask", mask)
+    return words
+
+
+def window_mask(mask, cache, slots, window, sinks=0, cu_seqlens=None, max_seqlen=None, stream=None):
+    """The window among a step's own tokens, for drafts that may be deeper than it: (mask, depth) for
+    `tree_attention`, whose window by itself hides only what was cached before.
+
+    Of the tokens that a row of ``mask`` names it keeps those less than ``window`` above it, and those
+    whose position is one of the first ``sinks``; depth (int32 ``[T]``) holds the places behind the
+    context.  Sequences are those of the `tree_attention` calls, reserved before; one mask serves all
+    layers of a step."""
+    n = _of_cache(cache, 0, slots)
+    dev = cache.device
+    if not _here(dev, stream):
+        with _on(dev, stream, cache._tensors + (mask, slots, cu_seqlens)):
+            return window_mask(mask, cache, slots, window, sinks, cu_seqlens, max_seqlen)
+    _want("mask", mask, (torch.int64,), 2, dev)
+    T = mask.shape[0]
+    B, N = _sequences(T, n, cu_seqlens, max_seqlen, dev)
+    words = _mask_words(mask, T, N, dev)
+    window, sinks = _window(window, sinks)
+    out = torch.empty_like(mask)
+    depth = torch.empty(T, dtype=torch.int32, device=dev)
+    if T:
+        _check(lib().fa_tree_window_mask(cache._at, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, mask.data_ptr(),
+                                         words, window, sinks, out.data_ptr(), depth.data_ptr(),
+                                         _raw_stream(dev)), "fa_tree_window_mask")
+    return out, depth
+
+
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(Hq, Hkv, N, d):
     return int(lib().fa_tree_workspace_size(Hq, Hkv, N, d))
 
 
 def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=None, max_seqlen=None,
-                   out=None, workspace=None, stream=None, window=None, sinks=0):
+                   out=None, workspace=None, stream=None, window=None, sinks=0, depth=None):
     """Attention of new tokens over one layer of the cache; returns (o, lse).
 
     The tokens of q ``[T, Hq, d]`` are the last ones of ``slots`` (`cache_append` comes first).
@@ -658,15 +702,17 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     With ``window`` a row at position p sees only keys at places j with p - j < window, and
     the first ``sinks`` ones.  A token's position is its place in the sequence; with a mask
     it is the context's length plus the number of other own tokens that its row names, and
-    the window hides only what was cached before.
+    the window hides only what was cached before: a draft that may be deeper than the window takes
+    its mask and ``depth`` from `window_mask`, or verifying it differs from decoding it.  Pages that a
+    window has passed stay with their sequence.
     """
     n = _of_cache(cache, layer, slots)
     dev = cache.device
     if not _here(dev, stream):
         with _on(dev, stream, cache._tensors + (q, slots, mask, cu_seqlens, workspace) +
-                 (tuple(out) if out is not None else ())):
+                 (depth,) + (tuple(out) if out is not None else ())):
             return tree_attention(q, cache, layer, slots, mask, scale, cu_seqlens, max_seqlen, out,
-                                  workspace, None, window, sinks)
+                                  workspace, None, window, sinks, depth)
     _heads_tensor("q", q, _BF16, dev)
     T, Hq, d = q.shape
     if Hq > _MOST:
@@ -678,19 +724,15 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
     B, N = _sequences(T, n, cu_seqlens, max_seqlen, dev)
     words = 0
     if mask is not None:
-        _want("mask", mask, (torch.int64,), 2, dev)
-        rows, words = mask.shape
-        if rows != T or 64 * words < N:
-            raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
-        if words > _MOST:
-            _too_far("mask", mask)
+        words = _mask_words(mask, T, N, dev)
     if window is not None:
-        window = _whole("window", window)
-        sinks = _whole("sinks", sinks)
-        if not (1 <= window <= _MOST and 0 <= sinks <= _MOST):
-            raise ValueError(f"window must be from 1 to {_MOST}, sinks from 0, got {window} and {sinks}")
+        window, sinks = _window(window, sinks)
     elif sinks:
         raise ValueError("sinks need a window (without one every earlier key is visible)")
+    if depth is not None:
+        _want("depth", depth, _INT, 1, dev)
+        if mask is None or window is None or depth.shape[0] != T:
+            raise ValueError("depth belongs to a mask and a window, one entry a token")
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if out is not None:
         _want("out[0]", out[0], (torch.bfloat16,), 3, dev)
@@ -716,6 +758,12 @@ def tree_attention(q, cache, layer, slots, mask=None, scale=None, cu_seqlens=Non
         size = max(_workspace_bytes(Hq, cache.heads, N or 1, d), 16)
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
     qt, qh, _ = q.stride()
+    if depth is not None:
+        _check(lib().fa_tree_fwd_window_depth(
+            cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
+            mask.data_ptr(), words, depth.data_ptr(), o.data_ptr(), lse.data_ptr(), scale, window, sinks,
+            1 if out is None else 0, ws.data_ptr(), size, _raw_stream(dev)), "fa_tree_fwd_window_depth")
+        return o, lse
     if window is not None:
         _check(lib().fa_tree_fwd_window(
             cache._at, layer, slots.data_ptr(), B, N, _ptr(cu_seqlens), T, q.data_ptr(), Hq, qt, qh,
@@ -769,12 +817,7 @@ def cache_weights(q, lse, cache, layer, slots, weights, mask=None, scale=None, c
                          f"{tuple(weights.shape)}")
     words = 0
     if mask is not None:
-        _want("mask", mask, (torch.int64,), 2, dev)
-        rows, words = mask.shape
-        if rows != T or 64 * words < N:
-            raise ValueError("mask must be [T, words] with 64 bits a word for every new token")
-        if words > _MOST:
-            _too_far("mask", mask)
+        words = _mask_words(mask, T, N, dev)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     if (q.requires_grad or lse.requires_grad or weights.requires_grad or cache.k.requires_grad or
             forward_ad._current_level >= 0):

@@ -523,7 +523,9 @@ fa_status fa_tree_fwd(const fa_cache* cache, int layer, const int* slots, int B,
  * sequence.  With one it is the context's length plus the number of other tokens of
  * the call that its row names (its depth in a drafted tree), and the window hides
  * keys of the context alone: of the call's own tokens a row sees those that it
- * names.  Key tiles that no row of an item sees are not read; keys and values that a
+ * names -- an ancestor more than the window above it too, where a draft is that deep: such a
+ * call takes its mask and depths from fa_tree_window_mask, or verifying differs from decoding.
+ * Key tiles that no row of an item sees are not read; keys and values that a
  * row does not see never matter to it, whatever they hold.
  */
 fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots, int B, int N,
@@ -532,6 +534,28 @@ fa_status fa_tree_fwd_window(const fa_cache* cache, int layer, const int* slots,
                              int mask_words, void* o, float* lse, float scale, int window, int sinks,
                              int zero_rest, void* workspace, size_t workspace_bytes,
                              fa_stream_t stream);
+
+/*
+ * The window among a call's own tokens, for drafts that may be deeper than it.
+ *   depth[t] (int32 [T]) becomes the number of other own tokens that token t names in its row
+ *   of mask (its place behind the context); out (int64 [T, words], may be mask itself) keeps of
+ *   the named ones those with depth[t] - depth[a] < window, those whose position, the context's
+ *   length plus depth[a], is below sinks, and itself.  Sequences as in fa_tree_fwd, behind
+ *   fa_cache_reserve; made once a step, it serves all layers.  Tokens that no sequence owns get
+ *   no bits and depth 0.
+ * fa_tree_fwd_window_depth: fa_tree_fwd_window with such a mask and its depths, each taken as
+ *   within [0, n - 1] of a sequence's n tokens.
+ */
+fa_status fa_tree_window_mask(const fa_cache* cache, const int* slots, int B, int N,
+                              const int* cu_seqlens, int T, const void* mask, int words, int window,
+                              int sinks, void* out, int* depth, fa_stream_t stream);
+
+fa_status fa_tree_fwd_window_depth(const fa_cache* cache, int layer, const int* slots, int B, int N,
+                                   const int* cu_seqlens, int T, const void* q, int Hq,
+                                   long long q_token_stride, long long q_head_stride, const void* mask,
+                                   int mask_words, const int* depth, void* o, float* lse, float scale,
+                                   int window, int sinks, int zero_rest, void* workspace,
+                                   size_t workspace_bytes, fa_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * A cache within a budget
