@@ -365,6 +365,8 @@ def _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k, dout=None, o=None, lse=None
                     ("cu_seqlens_k", cu_seqlens_k), ("dout", dout), ("o", o), ("lse", lse)):
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be on a CUDA device")
+        if t is not None and t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}, got {t.device}")
 
 
 def _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k, max_seqlen_k, batch):
@@ -412,8 +414,11 @@ def _workspace(workspace, size, device):
     """The caller's workspace, if it holds size bytes, or one of this call's own."""
     if workspace is None:
         return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
-    if isinstance(workspace, torch.Tensor) and workspace.numel() * workspace.element_size() < size:
-        raise ValueError(f"the call needs a workspace of {size} bytes")
+    if isinstance(workspace, torch.Tensor):
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"the workspace must be contiguous, on {device}")
+        if workspace.numel() * workspace.element_size() < size:
+            raise ValueError(f"the call needs a workspace of {size} bytes")
     return workspace
 
 
@@ -423,9 +428,14 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None,
     """Attention forward through the C ABI; returns (o, lse).
 
     With ``window`` (and causal=True) position p sees key j <= p when p - j < window, or when
-    j < sinks: the first ``sinks`` keys of a sequence stay visible to all of it."""
+    j < sinks: the first ``sinks`` keys of a sequence stay visible to all of it.
+    With ``stream`` the call runs there, and its outputs belong to that stream."""
     _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k)
     win = _check_window(window, sinks, causal)
+    if not serving._here(q.device, stream):
+        with serving._on(q.device, stream, (q, k, v, cu_seqlens, workspace, cu_seqlens_k)):
+            return forward(q, k, v, causal, scale, cu_seqlens, max_seqlen, batch, out_dtype, None,
+                           workspace, cu_seqlens_k, max_seqlen_k, window, sinks)
     B, Hq, Hkv, Nq, Tq, Nk, Tk, d, kv = _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k,
                                                      max_seqlen_k, batch)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
@@ -451,9 +461,14 @@ def backward(q, k, v, o, dout, lse, causal=False, scale=None, cu_seqlens=None, m
              workspace=None, check_status=False, cu_seqlens_k=None, max_seqlen_k=None, window=None,
              sinks=0):
     """Attention backward (preprocess + backward) through the C ABI; returns (dq, dk, dv).
-    causal, window and sinks as in the forward."""
+    causal, window, sinks and stream as in the forward."""
     _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k, dout=dout, o=o, lse=lse)
     win = _check_window(window, sinks, causal)
+    if not serving._here(q.device, stream):
+        with serving._on(q.device, stream, (q, k, v, o, dout, lse, cu_seqlens, workspace, cu_seqlens_k)):
+            return backward(q, k, v, o, dout, lse, causal, scale, cu_seqlens, max_seqlen, batch,
+                            deterministic, grad_dtype, None, workspace, check_status, cu_seqlens_k,
+                            max_seqlen_k, window, sinks)
     B, Hq, Hkv, Nq, Tq, Nk, Tk, d, kv = _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k,
                                                      max_seqlen_k, batch)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
