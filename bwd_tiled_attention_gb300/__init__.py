@@ -24,6 +24,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -520,6 +521,7 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, cu_seqlens, cu_seqlens_k = ctx.saved_tensors
         causal, scale, max_seqlen, batch, deterministic, max_seqlen_k, window, sinks = ctx.args
@@ -532,7 +534,8 @@ class _Attention(torch.autograd.Function):
 def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,
               deterministic=False, cu_seqlens_k=None, max_seqlen_k=None, rotary=None,
               positions=None, positions_k=None, interleaved=False, window=None, sinks=0):
-    """Differentiable attention (autograd wrapper around forward/backward).
+    """Differentiable attention (autograd wrapper around forward/backward), once: a gradient of
+    its gradients is refused.
 
     window and sinks bound what a position sees, as in `forward`: the last window keys up to
     its own, and the first sinks ones.

@@ -1,5 +1,5 @@
 """The attention's calls on a given stream: what they allocate belongs to it, and other streams' memory
-does not become theirs; workspaces and inputs that lie elsewhere are refused."""
+does not become theirs; workspaces and inputs that lie elsewhere, and a second gradient, are refused."""
 import pytest
 import torch
 
@@ -52,3 +52,16 @@ def test_inputs_elsewhere_are_refused():
         fa.forward(q, q.cpu(), q, batch=1)
     with pytest.raises(ValueError, match="workspace must be contiguous"):
         fa.forward(q, q, q, batch=1, workspace=torch.zeros(1 << 20, dtype=torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(), dict(window=5, sinks=1)])
+def test_a_gradient_of_gradients_is_refused(kw):
+    """The kernels' gradients are cut off from the inputs: what depends on both must not lose a part."""
+    g = torch.Generator().manual_seed(0)
+    q, k, v = (torch.randn(30, 2, 64, generator=g).bfloat16().cuda().requires_grad_() for _ in range(3))
+    o = fa.attention(q, k, v, causal=True, batch=1, **kw)
+    dq, = torch.autograd.grad(o.float().square().sum(), q, create_graph=True)
+    assert torch.isfinite(dq).all()
+    with pytest.raises(RuntimeError, match="differentiate twice|once_differentiable"):
+        (dq.float().sum() + q.float().sum()).backward()
