@@ -123,8 +123,8 @@ struct BUnit {
 // walks every query tile, as long as all the others together where the window is short
 // (N = 32768, W = 1024: 1024 steps of 268 a CTA).  Far units come first in the list.
 // Measured with D, conversion and the sinks' sum, 16 heads on 4 of 128, N = 32768: W = 4096,
-// S = 16 2338 us = 1106 TF/s (S = 0: 2307); W = 1024, S = 4 928 us = 731 TF/s (S = 0: 819); 2450
-// and 957 us with MMAs from one thread, as without a window.
+// S = 16 2290 us = 1130 TF/s; W = 1024, S = 4 908 us = 747 TF/s (S = 0: 801); deterministic 3780 and
+// 1396 us.  4 x 8192, 16 heads, W = 1024, S = 4, d = 64 / 96 / 192 / 256: 638 / 889 / 2524 / 3134 us.
 // Both leave fp32 partials of the dK and dV of sinks with far rows, which fold_sinks_kernel adds
 // up in a fixed order.
 

@@ -27,7 +27,9 @@
 // Measured (GPU time, the call alone): 16 sequences of 2.1-2.3k tokens back to 2048, R = 512, 16
 // layers, 8 heads of 128: 253 us for 1.41 GB, 82% of a copy; 4 prompts of 8-16k down to 1024:
 // 138 us for 0.60 GB (512 CTAs of one long chain: ~22 us of search and lists, ~27 of moves, in
-// two uneven waves).  One sequence, one layer, 8 heads: 34 us.
+// two uneven waves).  One sequence, one layer, 8 heads: 34 us.  Those are tables as wide as what they
+// hold; shared memory and threads go by the table's width, and tables of 32k places take 389 and
+// 199 us, of 8192 the first 314.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -331,7 +333,7 @@ extern "C" fa_status fa_cache_evict(const fa_cache* cache, const int* slots, con
     // The search takes the longer the more places there are, the moves the longer the fewer
     // CTAs an SM has: 512 threads for tables of more than 8192 places (16k: 140 us against
     // 170 with 256 threads), 256 below (5120 places: 231 against 234; 2304: 253 against 270; 640: 226
-    // against 358).
+    // against 358; sequences that fill their tables).
     const bool many = room > 8192;
     auto kern = many ? evict_kernel<512> : evict_kernel<256>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
