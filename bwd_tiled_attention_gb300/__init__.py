@@ -24,7 +24,6 @@ import os
 import threading
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import build as _build
 
@@ -362,12 +361,12 @@ def _check_inputs(q, k, v, cu_seqlens, cu_seqlens_k, dout=None, o=None, lse=None
         _check_tensor("lse", lse, (torch.float32,), 2)
         if tuple(lse.shape) != (q.shape[1], q.shape[0]):
             raise ValueError("lse must be [Hq, Tq]")
+    at = q.get_device()
     for name, t in (("q", q), ("k", k), ("v", v), ("cu_seqlens", cu_seqlens),
                     ("cu_seqlens_k", cu_seqlens_k), ("dout", dout), ("o", o), ("lse", lse)):
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be on a CUDA device")
-        if t is not None and t.device != q.device:
-            raise ValueError(f"{name} must be on {q.device}, got {t.device}")
+        if t is not None and (t.get_device() != at or at < 0):
+            raise ValueError(f"{name} must be on " + (f"{q.device}, got {t.device}" if t.is_cuda and at >= 0
+                                                      else "a CUDA device"))
 
 
 def _geometry_kv(q, k, cu_seqlens, max_seqlen, cu_seqlens_k, max_seqlen_k, batch):
@@ -521,14 +520,29 @@ class _Attention(torch.autograd.Function):
         return o
 
     @staticmethod
-    @once_differentiable
     def backward(ctx, dout):
         q, k, v, o, lse, cu_seqlens, cu_seqlens_k = ctx.saved_tensors
         causal, scale, max_seqlen, batch, deterministic, max_seqlen_k, window, sinks = ctx.args
-        dq, dk, dv = backward(q, k, v, o, dout.contiguous(), lse, causal, scale, cu_seqlens,
-                              max_seqlen, batch, deterministic, cu_seqlens_k=cu_seqlens_k,
-                              max_seqlen_k=max_seqlen_k, window=window, sinks=sinks)
+
+        def run():
+            return backward(q, k, v, o, dout.contiguous(), lse, causal, scale, cu_seqlens, max_seqlen,
+                            batch, deterministic, cu_seqlens_k=cu_seqlens_k, max_seqlen_k=max_seqlen_k,
+                            window=window, sinks=sinks)
+        # (where a graph of the gradients is asked for, they are its ends)
+        dq, dk, dv = _Gradients.apply(run, q, k, v, dout) if torch.is_grad_enabled() else run()
         return dq, dk, dv, None, None, None, None, None, None, None, None, None, None
+
+
+class _Gradients(torch.autograd.Function):
+    """What `run` computes of the inputs, with no gradient of its own."""
+
+    @staticmethod
+    def forward(ctx, run, *inputs):
+        return run()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("attention is differentiable once: its gradients have none")
 
 
 def attention(q, k, v, causal=False, scale=None, cu_seqlens=None, max_seqlen=None, batch=None,

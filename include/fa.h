@@ -47,7 +47,7 @@
  * - Size limits (FA_ERR_UNSUPPORTED, nothing launched): Hq <= 65535; every
  *   sequence bound N (Nq, Nk) within 65535 tiles of 128 tokens; a dense
  *   batch's B*N < 2^31; T * Hq * d <= 2^40 on either side.  A packed batch
- *   has B <= 4096 sequences.  One scheduler CTA ranks a packed batch, keeping
+ *   has B <= 4096 sequences.  Every scheduler CTA ranks a packed batch, keeping
  *   8 bytes per tile level of the longest sequence in its shared memory, so
  *   there N must also satisfy 16 * ceil(3B / 4) + 8 * (max(B, ceil(N / R)) + 1)
  *   <= 227 KB. R is the work unit's height: 256 rows for the forward up to

@@ -63,5 +63,5 @@ def test_a_gradient_of_gradients_is_refused(kw):
     o = fa.attention(q, k, v, causal=True, batch=1, **kw)
     dq, = torch.autograd.grad(o.float().square().sum(), q, create_graph=True)
     assert torch.isfinite(dq).all()
-    with pytest.raises(RuntimeError, match="differentiate twice|once_differentiable"):
+    with pytest.raises(RuntimeError, match="differentiable once"):
         (dq.float().sum() + q.float().sum()).backward()
