@@ -588,9 +588,9 @@ fa_status fa_cache_accept_weights(const fa_cache* cache, const int* slots, const
  * fa_tree_fwd, whose lse [Hq,T] this takes; scale positive and finite.
  *   Of a drafted tree every row counts, rejected ones too, unless its lse is -inf; or call
  *   this behind fa_cache_accept, with the accepted tokens' rows of q and lse and no mask.
- *   A row with lse = -inf gives nothing.  Sums are fp32, each key's in one addition, so
- *   that results do not vary from run to run.  A slot that the call names several
- *   times receives all sums (in any order).  Places behind a sequence's length are
+ *   A row with lse = -inf gives nothing.  Sums are fp32, each key's in an order of
+ *   its own, so that results do not vary from run to run.  A slot that the call names
+ *   several times receives all sums, in any order: their last bits may vary.  Places behind a sequence's length are
  *   left alone.  What is wrong in slots, lengths or boundaries sets the status word, and
  *   that sequence adds nothing.  No workspace; reads keys and tables, like attention.
  */

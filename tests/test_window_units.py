@@ -95,6 +95,8 @@ def batches():
             (([2600, 130, 129], [2600, 900, 129]), 128, 4), (([64, 4300], [64, 4300]), 100, 300),
             (([20] * 30 + [3000], [20] * 30 + [3000]), 64, 500), (([0, 0, 5], [9, 0, 700]), 8, 3),
             (([200] * 3, [2500] * 3), 1000, 200)]
+    # more sequences than the scheduler has threads
+    some += [(([3] * 1500 + [400] + [130] * 40,) * 2, 100, 5), (([1, 200] * 1040 + [900],) * 2, 129, 140)]
     for _ in range(12):
         n = rnd.randint(1, 6)
         lk = [rnd.choice([0, 1, rnd.randint(1, 3000)]) for _ in range(n - 1)] + [rnd.randint(300, 3000)]
